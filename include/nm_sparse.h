@@ -50,8 +50,10 @@ typedef enum {
 
 typedef enum { NM_I8 = 0, NM_F16 = 1, NM_BF16 = 2, NM_I32 = 3, NM_F32 = 4 } nm_dtype;
 
-/* Activation fused into nm_spmm_act's epilogue. */
-typedef enum { NM_ACT_NONE = 0, NM_ACT_GELU = 1 } nm_act;
+/* Activation fused into an epilogue.  NM_ACT_SILU belongs to the gated
+ * feed-forward block (nm_glu, nm_mx_glu); nm_spmm_act and its relatives take
+ * the first two. */
+typedef enum { NM_ACT_NONE = 0, NM_ACT_GELU = 1, NM_ACT_SILU = 2 } nm_act;
 
 /* Operand layouts: X [K][T] and Y [R][T] (tokens contiguous, as nm_spmm
  * takes them), or the PyTorch-linear layout X [T][K] and Y [T][R] (the
@@ -357,6 +359,130 @@ nm_status nm_hybrid_pack(const void* W, int64_t ldw, nm_hybrid* desc);
  */
 nm_status nm_hybrid_spmm(const nm_hybrid* w, const void* X, int64_t ldx, int64_t T, void* Y, int64_t ldy,
                          int32_t y_dtype, const void* bias, int32_t act, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward block on N:M packed fp16 / bf16 weights, in the
+ * PyTorch-linear layout:
+ *
+ *     G = X Wg^T,  U = X Wu^T,  H = act(G) (.) U
+ *
+ * X [T][ldx] (K contiguous), Wg and Wu packed R x K of one N:M and dtype, H
+ * [T][ldh] (R contiguous).  act: NM_ACT_SILU, x / (1 + exp(-x)), or
+ * NM_ACT_GELU, x Phi(x).  Both projections, the activation and the product
+ * are one launch for few tokens; sums and the activation are binary32, H is
+ * rounded once.
+ * ---------------------------------------------------------------------- */
+
+/* Device workspace nm_glu needs for these weights and T tokens (0: none),
+ * for rows of any stride and alignment: dense copies of the weights, and a
+ * padded copy of X, where the call takes them. */
+nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes);
+
+/*
+ * H = act(X Wg^T) (.) (X Wu^T).  G, U: NULL, or both [T][ldp] buffers of the
+ * weight dtype that receive the two products, rounded once, for
+ * nm_glu_backward.  Weights must be finite where X is not: a pruned weight
+ * multiplies as zero.  The workspace (256-byte aligned, at least
+ * nm_glu_workspace_size bytes) is written and read back within the call's
+ * stream order, so calls that share one must be ordered.
+ * NM_EINVAL: null pointers (or only one of G and U), T < 1, ldx < K, ldh < R,
+ * ldp < R, descriptors whose sizes or versions are wrong or whose shape, N:M
+ * or dtype differ, a small workspace.  NM_EUNSUPPORTED: int8 weights, act not
+ * listed, pointers not aligned to their element, a workspace not 256-byte
+ * aligned, rows so long that 256 of them pass 2^31 bytes.
+ */
+nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
+                 int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* Device workspace nm_glu_backward needs. */
+nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes);
+
+/*
+ * The block's gradients for a fixed mask, from dH = dL/dH and the products
+ * nm_glu kept:
+ *     dG = dH (.) U (.) act'(G),  dU = dH (.) act(G)
+ *     dX  = dG Wg + dU Wu                           [T][lddx]
+ *     dWg = keep_g (.) dG^T X, dWu = keep_u (.) dU^T X   [R][lddw] each
+ * The weight gradients are dense rows, exactly zero where the weight is not
+ * kept (also where the product there is not finite).  dX may be NULL, and so
+ * may both weight gradients together (then they are not computed); not all
+ * three.  dG and dU are rounded to the weight dtype before the two products,
+ * as operands of the matrix instruction; sums are binary32 and every output
+ * is rounded once.  The result does not depend on launch order (no atomics).
+ * All buffers have the weight dtype.  Errors as nm_glu; NM_EINVAL also for
+ * no output at all, one weight gradient without the other, lddx < K, lddw < K.
+ */
+nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
+                          const void* G, const void* U, int64_t ldp, const void* dH, int64_t lddh, int32_t act,
+                          void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point: blocks of 32 consecutive elements along
+ * K, each element E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), one
+ * E8M0 scale (a power of two) per block.
+ *   scale = 2^(floor(log2(amax)) - 2), amax the block's largest magnitude,
+ *   the exponent clamped to [-127, 127] (a block of zeros: 2^-127);
+ *   element = x / scale rounded half to even, magnitudes above 6 become 6.
+ * A block that holds a NaN or an infinity gets the NaN scale (0xFF): all of
+ * it reads back as NaN.  The last block of a row may be short.
+ * Layout, Kp = K rounded up to 256: row r's codes at r * Kp / 2 bytes,
+ * element k in bits 4 (k % 2) .. + 3 of byte k / 2 (sign, two exponent bits,
+ * mantissa), zero past K.  Scales in units of 256 bytes for 32 rows x 256
+ * columns, unit (r / 32) * (Kp / 256) + k / 256, the block of row r and
+ * column k at byte 4 (16 (b % 4) + r % 16) + 2 ((r % 32) / 16) + b / 4 of its
+ * unit, b = (k % 256) / 32: a lane of the scaled matrix instruction finds
+ * the four scales it needs in one word.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int64_t rows, K;
+  uint32_t format_version;  /* NM_FORMAT_VERSION, written by nm_mx_quantize */
+  uint32_t reserved;        /* 0 */
+  void* codes;  size_t codes_bytes;    /* device, sizes from nm_mx_size */
+  void* scales; size_t scales_bytes;
+} nm_mx;
+
+/* Sizes of the two buffers.  NM_EINVAL: null outputs, rows < 1, K < 1. */
+nm_status nm_mx_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes);
+
+/*
+ * X [m->rows][ldx] of x_dtype (NM_F16, NM_BF16 or NM_F32) -> m's buffers.
+ * Every byte of both buffers is written.  NM_EINVAL: null pointers, ldx < K,
+ * buffer sizes not those of nm_mx_size; NM_EUNSUPPORTED: other types, X not
+ * aligned to its element, buffers not 16-byte aligned.
+ */
+nm_status nm_mx_quantize(const void* X, int64_t ldx, int32_t x_dtype, nm_mx* m, void* stream);
+
+/* The values m stands for, Y [rows][ldy] of y_dtype (NM_F16, NM_BF16, NM_F32;
+ * rounded to y_dtype where it cannot hold them).  Errors as nm_mx_quantize. */
+nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype, void* stream);
+
+/*
+ * Activations of nm_mx_linear and nm_mx_glu: either X [T][ldx] of x_dtype
+ * (NM_F16, NM_BF16, NM_F32), which the call quantises as nm_mx_quantize does,
+ * or xq with rows = T (then X, ldx and x_dtype are ignored).
+ *
+ * nm_mx_linear: Y[t][r] = act(sum_k x[t][k] w[r][k] + bias[r]) over the
+ * values the formats stand for, binary32 sums, Y [T][ldy] of y_dtype
+ * (NM_F16, NM_BF16, NM_F32) rounded once; bias NULL or device float[R]; act
+ * NM_ACT_NONE or NM_ACT_GELU.
+ * nm_mx_glu: H = act(x Wg^T) (.) (x Wu^T), act NM_ACT_SILU or NM_ACT_GELU.
+ * Workspace: nm_mx_workspace_size bytes (256-byte aligned; rows_n = R of the
+ * weight, glu != 0 for nm_mx_glu): quantised activations and the partial
+ * sums of a split reduction.  NM_EINVAL: null pointers, T < 1, ldx < K,
+ * ldy < R, xq of other K or rows than asked, descriptors with wrong sizes or
+ * versions, gate and up of other shapes, a small workspace;
+ * NM_EUNSUPPORTED: other types, act not listed, misaligned pointers, rows so
+ * long that 256 of them pass 2^31 bytes.
+ */
+nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* bytes);
+nm_status nm_mx_linear(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
+                       void* Yt, int64_t ldy, int32_t y_dtype, const float* bias, int32_t act, void* workspace,
+                       size_t workspace_bytes, void* stream);
+nm_status nm_mx_glu(const nm_mx* gate, const nm_mx* up, const nm_mx* xq, const void* Xt, int64_t ldx,
+                    int32_t x_dtype, int64_t T, void* Ht, int64_t ldh, int32_t h_dtype, int32_t act,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,15 @@ library every call raises.
     p = pack(W, N, M)                      # W: [R, K] int8 / float16 / bfloat16 on the GPU
     Y = spmm(p, X, bias=None, scale=None, out_dtype=None)   # X: [K, T]  ->  Y: [R, T]
 
+    # the gated feed-forward block on two packed weights, and its gradients
+    H = glu(pg, pu, Xt, act="silu", pre=None)               # Xt: [T, K]  ->  H: [T, R]
+    dX, dWg, dWu = glu_backward(pg, pu, Xt, pre, dH, act="silu")
+
+    # microscaled 4-bit weights: their product and gated block
+    m = mx_quantize(W)                                      # W: [R, K] float16 / bfloat16 / float32
+    Y = mx_linear(m, Xt)                                    # Xt: [T, K]  ->  Y: [T, R]
+    H = mx_glu(mg, mu, Xt, act="silu")
+
 Operation: paper "Realizable N:M Sparse Transformer Inference via
 Search-Kernel Co-Design" (arXiv 2607.12505) -- Sec. 2.1 N:M constraint,
 Sec. 4.2 packed windows and micro-dense execution.
@@ -50,6 +59,12 @@ class NmHybrid(ctypes.Structure):
                 ("res_ptr", ctypes.c_void_p), ("res_ptr_bytes", ctypes.c_size_t),
                 ("res_ent", ctypes.c_void_p), ("res_ent_bytes", ctypes.c_size_t),
                 ("n_fill", ctypes.c_int64), ("n_res", ctypes.c_int64)]
+
+
+class NmMx(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("format_version", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("codes", ctypes.c_void_p), ("codes_bytes", ctypes.c_size_t),
+                ("scales", ctypes.c_void_p), ("scales_bytes", ctypes.c_size_t)]
 
 
 HYBRID_BUFFERS = ("values", "meta", "codes", "res_ptr", "res_ent")
@@ -101,8 +116,21 @@ def lib() -> ctypes.CDLL:
         L.nm_hybrid_pack_size.argtypes = [P, I64, I64, I64, I32, HP]
         L.nm_hybrid_pack.argtypes = [P, I64, HP]
         L.nm_hybrid_spmm.argtypes = [HP, P, I64, I64, P, I64, I32, P, I32, P]
+        L.nm_glu_workspace_size.argtypes = [PP, PP, I64, ctypes.POINTER(SZ)]
+        L.nm_glu.argtypes = [PP, PP, P, I64, I64, P, I64, I32, P, P, I64, P, SZ, P]
+        L.nm_glu_backward_workspace_size.argtypes = [PP, PP, I64, ctypes.POINTER(SZ)]
+        L.nm_glu_backward.argtypes = [PP, PP, P, I64, I64, P, P, I64, P, I64, I32, P, I64, P, P, I64, P, SZ, P]
+        MP = ctypes.POINTER(NmMx)
+        L.nm_mx_size.argtypes = [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
+        L.nm_mx_quantize.argtypes = [P, I64, I32, MP, P]
+        L.nm_mx_dequantize.argtypes = [MP, P, I64, I32, P]
+        L.nm_mx_workspace_size.argtypes = [MP, I64, I32, ctypes.POINTER(SZ)]
+        L.nm_mx_linear.argtypes = [MP, MP, P, I64, I32, I64, P, I64, I32, P, I32, P, SZ, P]
+        L.nm_mx_glu.argtypes = [MP, MP, MP, P, I64, I32, I64, P, I64, I32, I32, P, SZ, P]
         for f in ("nm_pack_size", "nm_pack", "nm_spmm_workspace_size", "nm_spmm", "nm_hybrid_pack_size",
-                  "nm_hybrid_pack", "nm_hybrid_spmm"):
+                  "nm_hybrid_pack", "nm_hybrid_spmm", "nm_glu_workspace_size", "nm_glu",
+                  "nm_glu_backward_workspace_size", "nm_glu_backward", "nm_mx_size", "nm_mx_quantize",
+                  "nm_mx_dequantize", "nm_mx_workspace_size", "nm_mx_linear", "nm_mx_glu"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -438,4 +466,306 @@ def spmm_hybrid(h: Hybrid, X: torch.Tensor, bias: torch.Tensor | None = None,
                               _TORCH_TO_NM[out_dtype], None if bias is None else bias.data_ptr(),
                               ACTS[act], _stream(X.device))
     _check(st, "nm_hybrid_spmm")
+    return out
+
+
+# ---------------------------------------------------------------- gated feed-forward block
+GLU_ACTS = {"gelu": 1, "silu": 2}
+
+
+def _device_of(tensors) -> torch.device:
+    """The one GPU all (name, tensor) pairs live on; None tensors are skipped."""
+    dev = tensors[0][1].device
+    if dev.type != "cuda":
+        raise ValueError(f"{tensors[0][0]} is on {dev}, not on a GPU")
+    for name, t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {dev}")
+    return dev
+
+
+def _row_pitch(name: str, t: torch.Tensor, rows: int, cols: int) -> int:
+    """Elements between the rows of a [rows, cols] tensor with unit stride
+    along its columns, as the library takes them (rows may not overlap)."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its second dimension")
+    if rows == 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} has overlapping rows (stride {t.stride(0)} for {cols} columns)")
+    return t.stride(0)
+
+
+def _workspace(workspace: torch.Tensor | None, need: int, dev: torch.device) -> torch.Tensor | None:
+    """The caller's workspace where it is large enough, else a new one."""
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, the operands on {dev}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+def _ws_args(ws: torch.Tensor | None):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _glu_act(act: str) -> int:
+    if act not in GLU_ACTS:
+        raise ValueError(f"act must be one of {sorted(GLU_ACTS)}, got {act!r}")
+    return GLU_ACTS[act]
+
+
+def _check_dtype(name: str, t: torch.Tensor, want: torch.dtype) -> None:
+    if t.dtype != want:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
+
+
+def _call(dev: torch.device, f, what: str, *args) -> None:
+    """One library call with the operands' device current and its current
+    stream as the last argument."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(dev))
+    _check(st, what)
+
+
+def _glu_operands(gate: Packed, up: Packed, Xt: torch.Tensor):
+    if gate.dtype not in (NM_F16, NM_BF16):
+        raise TypeError(f"the gated block takes float16 / bfloat16 weights, not {gate.torch_dtype}")
+    for f in ("rows", "K", "N", "M", "dtype"):
+        if getattr(gate, f) != getattr(up, f):
+            raise ValueError(f"gate and up differ in {f}: {getattr(gate, f)} and {getattr(up, f)}")
+    if Xt.dim() != 2:
+        raise ValueError("Xt must be a 2-D tensor")
+    T = Xt.shape[0]
+    ldx = _row_pitch("Xt", Xt, T, gate.K)
+    _check_dtype("Xt", Xt, gate.torch_dtype)
+    return T, ldx
+
+
+def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
+    if pre.dim() != 3 or tuple(pre.shape) != (2, T, p.rows):
+        raise ValueError(f"pre must be [2, {T}, {p.rows}], got {tuple(pre.shape)}")
+    _check_dtype("pre", pre, p.torch_dtype)
+    if pre.stride(0) < (T - 1) * pre.stride(1) + p.rows:
+        raise ValueError("the two halves of pre overlap")
+    return _row_pitch("pre", pre[0], T, p.rows)
+
+
+def glu_workspace_size(gate: Packed, up: Packed, T: int) -> int:
+    """nm_glu_workspace_size: bytes of workspace glu() may need."""
+    n, dg, du = ctypes.c_size_t(), gate.desc(), up.desc()
+    _check(lib().nm_glu_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)),
+           "nm_glu_workspace_size")
+    return n.value
+
+
+def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torch.Tensor | None = None,
+        pre: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_glu, the gated feed-forward block on two packed weights of one
+    shape, N:M and dtype (float16 / bfloat16): H[T, R] = act(G) * U with
+    G = Xt @ (mask . Wg)^T, U = Xt @ (mask . Wu)^T, Xt [T, K] (K contiguous).
+    act: "silu" or "gelu".  pre: a [2, T, R] tensor that receives G and U,
+    which glu_backward() takes."""
+    T, ldx = _glu_operands(gate, up, Xt)
+    a = _glu_act(act)
+    if out is None:
+        out = torch.empty((T, gate.rows), dtype=Xt.dtype, device=Xt.device)
+    ldh = _row_pitch("out", out, T, gate.rows)
+    _check_dtype("out", out, Xt.dtype)
+    ldp = 0 if pre is None else _check_pre(pre, T, gate)
+    dev = _device_of([("Xt", Xt), ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
+                      ("up meta", up.meta), ("out", out), ("pre", pre)])
+    dg, du, n = gate.desc(), up.desc(), ctypes.c_size_t()
+    L = lib()
+    _check(L.nm_glu_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)), "nm_glu_workspace_size")
+    ws = _workspace(workspace, n.value, dev)
+    g, u = (None, None) if pre is None else (pre.data_ptr(),
+                                             pre.data_ptr() + pre.stride(0) * pre.element_size())
+    _call(dev, L.nm_glu, "nm_glu", ctypes.byref(dg), ctypes.byref(du), Xt.data_ptr(), ldx, T, out.data_ptr(), ldh, a,
+          g, u, ldp, *_ws_args(ws))
+    return out
+
+
+def glu_backward_workspace_size(gate: Packed, up: Packed, T: int) -> int:
+    """nm_glu_backward_workspace_size: bytes of workspace glu_backward() needs."""
+    n, dg, du = ctypes.c_size_t(), gate.desc(), up.desc()
+    _check(lib().nm_glu_backward_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)),
+           "nm_glu_backward_workspace_size")
+    return n.value
+
+
+def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, dH: torch.Tensor, act: str = "silu",
+                 need_dx: bool = True, need_dw: bool = True, workspace: torch.Tensor | None = None):
+    """nm_glu_backward: the gradients of glu() for a fixed mask, from dH
+    [T, R] and the products glu() kept in `pre`.  Returns (dX [T, K],
+    dWg [R, K], dWu [R, K]) in the weights' dtype; the weight gradients are
+    dense and zero where the weight is pruned.  need_dx / need_dw = False
+    leaves that part out (None in its place)."""
+    T, ldx = _glu_operands(gate, up, Xt)
+    a = _glu_act(act)
+    if not need_dx and not need_dw:
+        raise ValueError("glu_backward needs need_dx or need_dw")
+    ldp = _check_pre(pre, T, gate)
+    lddh = _row_pitch("dH", dH, T, gate.rows)
+    _check_dtype("dH", dH, Xt.dtype)
+    dev = _device_of([("Xt", Xt), ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
+                      ("up meta", up.meta), ("pre", pre), ("dH", dH)])
+    dg, du, n = gate.desc(), up.desc(), ctypes.c_size_t()
+    L = lib()
+    _check(L.nm_glu_backward_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)),
+           "nm_glu_backward_workspace_size")
+    ws = _workspace(workspace, n.value, dev)
+    R, K = gate.rows, gate.K
+    dX = torch.empty((T, K), dtype=Xt.dtype, device=dev) if need_dx else None
+    dWg = torch.empty((R, K), dtype=Xt.dtype, device=dev) if need_dw else None
+    dWu = torch.empty((R, K), dtype=Xt.dtype, device=dev) if need_dw else None
+    _call(dev, L.nm_glu_backward, "nm_glu_backward", ctypes.byref(dg), ctypes.byref(du), Xt.data_ptr(), ldx, T,
+          pre.data_ptr(), pre.data_ptr() + pre.stride(0) * pre.element_size(), ldp, dH.data_ptr(), lddh, a,
+          None if dX is None else dX.data_ptr(), K, None if dWg is None else dWg.data_ptr(),
+          None if dWu is None else dWu.data_ptr(), K, *_ws_args(ws))
+    return dX, dWg, dWu
+
+
+# ---------------------------------------------------------------- microscaled 4-bit format
+@dataclass
+class Mx:
+    """rows x K values in the microscaled 4-bit format (E2M1 elements, one
+    E8M0 scale for each block of 32 along K) as two uint8 device buffers."""
+    rows: int
+    K: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    format_version: int = FORMAT_VERSION
+
+    def desc(self) -> NmMx:
+        return NmMx(self.rows, self.K, self.format_version, 0, self.codes.data_ptr(), self.codes.numel(),
+                    self.scales.data_ptr(), self.scales.numel())
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
+
+
+def _check_float(name: str, dt: torch.dtype) -> None:
+    if dt not in _FLOATS:
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {dt}")
+
+
+def mx_size(rows: int, K: int):
+    """nm_mx_size: bytes of an Mx's codes and scales."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().nm_mx_size(rows, K, ctypes.byref(c), ctypes.byref(s)), "nm_mx_size")
+    return c.value, s.value
+
+
+def mx_quantize(X: torch.Tensor) -> Mx:
+    """nm_mx_quantize: X [rows, K] (float16, bfloat16 or float32) in the
+    microscaled 4-bit format: blocks of 32 along K, scale
+    2^(floor(log2(amax)) - 2), elements rounded half to even and saturated."""
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor")
+    _check_float("X", X.dtype)
+    rows, K = X.shape
+    ldx = _row_pitch("X", X, rows, K)
+    dev = _device_of([("X", X)])
+    c, s = mx_size(rows, K)
+    m = Mx(rows, K, torch.empty(c, dtype=torch.uint8, device=dev), torch.empty(s, dtype=torch.uint8, device=dev), 0)
+    d = m.desc()
+    _call(dev, lib().nm_mx_quantize, "nm_mx_quantize", X.data_ptr(), ldx, _TORCH_TO_NM[X.dtype], ctypes.byref(d))
+    m.format_version = d.format_version
+    return m
+
+
+def mx_dequantize(m: Mx, out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_mx_dequantize: the [rows, K] values m stands for."""
+    dev = _device_of([("codes", m.codes), ("scales", m.scales), ("out", out)])
+    if out is None:
+        out = torch.empty((m.rows, m.K), dtype=out_dtype, device=dev)
+    _check_float("out", out.dtype)
+    ld = _row_pitch("out", out, m.rows, m.K)
+    d = m.desc()
+    _call(dev, lib().nm_mx_dequantize, "nm_mx_dequantize", ctypes.byref(d), out.data_ptr(), ld,
+          _TORCH_TO_NM[out.dtype])
+    return out
+
+
+def mx_workspace_size(w: Mx, T: int, glu: bool = False) -> int:
+    """nm_mx_workspace_size: bytes of workspace mx_linear() / mx_glu() may need."""
+    n, d = ctypes.c_size_t(), w.desc()
+    _check(lib().nm_mx_workspace_size(ctypes.byref(d), T, int(glu), ctypes.byref(n)), "nm_mx_workspace_size")
+    return n.value
+
+
+def _mx_operands(w: Mx, X, out_dtype, out, workspace, others, glu: bool):
+    """Checks shared by mx_linear and mx_glu: (device, T, xq, x pointer, ldx,
+    x dtype, out, ldy, workspace)."""
+    if isinstance(X, Mx):
+        if X.K != w.K:
+            raise ValueError(f"X has K={X.K}, the weight has K={w.K}")
+        T, xq, xp, ldx, xdt = X.rows, ctypes.byref(X.desc()), None, 0, 0
+        xs = [("X codes", X.codes), ("X scales", X.scales)]
+        default = torch.bfloat16
+    else:
+        if X.dim() != 2:
+            raise ValueError("X must be a 2-D tensor or an Mx")
+        _check_float("X", X.dtype)
+        T = X.shape[0]
+        ldx = _row_pitch("X", X, T, w.K)
+        xq, xp, xdt = None, X.data_ptr(), _TORCH_TO_NM[X.dtype]
+        xs = [("X", X)]
+        default = X.dtype
+    if out is None:
+        out = torch.empty((T, w.rows), dtype=default if out_dtype is None else out_dtype, device=xs[0][1].device)
+    elif out_dtype is not None:
+        _check_dtype("out", out, out_dtype)
+    _check_float("out", out.dtype)
+    ldy = _row_pitch("out", out, T, w.rows)
+    dev = _device_of(xs + [("weight codes", w.codes), ("weight scales", w.scales), ("out", out)] + others)
+    need = 0 if xq is not None else mx_workspace_size(w, T, glu)
+    return dev, T, xq, xp, ldx, xdt, out, ldy, _workspace(workspace, need, dev)
+
+
+def mx_linear(w: Mx, X, bias: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+              out: torch.Tensor | None = None, act: str = "none",
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_mx_linear: Y[T, R] = act(X @ W^T + bias) with W and X in the
+    microscaled 4-bit format.  X: a [T, K] float16 / bfloat16 / float32 tensor,
+    quantised by the call, or an Mx; Y has X's dtype (an Mx: bfloat16) unless
+    out_dtype says otherwise; act "none" or "gelu"."""
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    if bias is not None:
+        _check_dtype("bias", bias, torch.float32)
+        if bias.dim() != 1 or bias.numel() != w.rows or (bias.numel() > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias must be a contiguous vector of length R={w.rows}, got {tuple(bias.shape)}")
+    dev, T, xq, xp, ldx, xdt, out, ldy, ws = _mx_operands(w, X, out_dtype, out, workspace, [("bias", bias)], False)
+    d = w.desc()
+    _call(dev, lib().nm_mx_linear, "nm_mx_linear", ctypes.byref(d), xq, xp, ldx, xdt, T, out.data_ptr(), ldy,
+          _TORCH_TO_NM[out.dtype], None if bias is None else bias.data_ptr(), ACTS[act], *_ws_args(ws))
+    return out
+
+
+def mx_glu(gate: Mx, up: Mx, X, act: str = "silu", out_dtype: torch.dtype | None = None,
+           out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_mx_glu: the gated feed-forward block with both weights (and the
+    activations, as in mx_linear) in the microscaled 4-bit format:
+    H[T, R] = act(X @ Wg^T) * (X @ Wu^T); act "silu" or "gelu"."""
+    a = _glu_act(act)
+    if (gate.rows, gate.K) != (up.rows, up.K):
+        raise ValueError(f"gate is {gate.rows} x {gate.K}, up is {up.rows} x {up.K}")
+    dev, T, xq, xp, ldx, xdt, out, ldy, ws = _mx_operands(
+        gate, X, out_dtype, out, workspace, [("up codes", up.codes), ("up scales", up.scales)], True)
+    dg, du = gate.desc(), up.desc()
+    _call(dev, lib().nm_mx_glu, "nm_mx_glu", ctypes.byref(dg), ctypes.byref(du), xq, xp, ldx, xdt, T, out.data_ptr(),
+          ldy, _TORCH_TO_NM[out.dtype], a, *_ws_args(ws))
     return out

@@ -1010,3 +1010,7 @@ nm_status nm_hybrid_spmm(const nm_hybrid* w, const void* X, int64_t ldx, int64_t
 }
 
 }  // extern "C"
+
+namespace nm {
+nm_status check_packed(const nm_packed* w, Geometry* g) { return check_desc(w, g); }
+}  // namespace nm

@@ -1,0 +1,195 @@
+// Shared definitions of the feed-forward operators (gated block on N:M packed
+// weights and its backward pass; the microscaled 4-bit format, its product
+// and its gated block).  Internal; the public surface is include/nm_sparse.h.
+#pragma once
+
+#include "nm_common.hpp"
+
+namespace nm {
+
+// a packed weight's descriptor, checked as nm_spmm checks it (nm_api.hip)
+nm_status check_packed(const nm_packed* w, Geometry* g);
+
+// ---------------------------------------------------------------- microscaled 4-bit layout
+// rows x K values in blocks of 32 along K.  codes: row r at r * ldc bytes,
+// ldc = Kp / 2, Kp = K rounded up to 256, element k in bits 4 (k % 2) .. of
+// byte k / 2.  scales: one 256-byte unit for 32 rows x 256 columns, unit
+// (r / 32) * (Kp / 256) + k / 256; inside it the block of row r, column k at
+// byte 4 (16 (b % 4) + r % 16) + 2 ((r % 32) / 16) + b / 4, b = (k % 256) / 32:
+// dword l of a unit holds the four scales that lane l of a wave needs for two
+// 16-row tiles x two matrix instructions of 128 columns.
+constexpr int kMxSlab = 256;                 // elements of K a unit covers
+inline int64_t mx_kp(int64_t K) { return (K + kMxSlab - 1) / kMxSlab * kMxSlab; }
+inline int64_t mx_codes_bytes(int64_t rows, int64_t K) { return rows * (mx_kp(K) / 2); }
+inline int64_t mx_scales_bytes(int64_t rows, int64_t K) { return (rows + 31) / 32 * (mx_kp(K) / kMxSlab) * 256; }
+
+// ---------------------------------------------------------------- tile product
+// C[m][n] = sum_k A[m][k] B[n][k]: A the activations (rows = tokens, or
+// weight rows in the weight gradient), B the weights, both with the reduction
+// contiguous; a "slab" is 128 bytes of the reduction.
+enum TileOp { TILE_LINEAR = 0, TILE_GLU = 1, TILE_MASKED = 2 };
+
+struct TileArgs {
+  const uint8_t* A[2];       // per batch; lda bytes between rows
+  const uint8_t* B[2];       // TILE_GLU: gate and up weights; else per batch
+  const uint8_t* As;         // scales (microscaled operands), unit layout above
+  const uint8_t* Bs[2];
+  int64_t lda, ldb;          // bytes
+  int64_t Mr, Nr;            // rows of A, rows of B (of one of the two weights)
+  int ka, kb;                // valid 16-byte pieces of an A row, of a B row
+  int nslab;                 // slabs of the reduction
+  void* C[2];                // output, ldc elements between rows
+  int64_t ldc;
+  void* P[2];                // TILE_GLU: the two products (nullptr: not kept), ldp elements between rows
+  int64_t ldp;
+  const float* bias;         // [Nr] or nullptr
+  const uint8_t* mask[2];    // TILE_MASKED: bit k % 8 of byte k / 8 of row m says the weight is kept
+  int64_t ldm;               // bytes
+  int act;                   // NM_ACT_NONE / NM_ACT_GELU / NM_ACT_SILU
+  int batch;                 // 1, or 2 products over A[b], B[b] -> C[b]
+  int mt, nt;                // tiles of one product, filled by the launcher
+  // split of the reduction (TILE_LINEAR): slice s covers slabs s * sps ..,
+  // raw sums to C + s * cs elements of binary32
+  int split, sps;
+  int64_t cs;
+};
+
+// Element types of the tile kernel's operands.
+enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2 };
+
+hipError_t launch_tile_f16(TileOp op, int ydt, const TileArgs& a, hipStream_t s);
+hipError_t launch_tile_bf16(TileOp op, int ydt, const TileArgs& a, hipStream_t s);
+hipError_t launch_tile_mx(TileOp op, int ydt, const TileArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- other launches
+struct GluArgs {
+  Geometry g;                // both weights
+  int wdt;
+  const uint8_t* values[2];
+  const uint8_t* meta[2];
+  const void* X;
+  int64_t ldx, T;
+  void* H;
+  int64_t ldh;
+  void* P[2];
+  int64_t ldp;
+  int act;
+};
+
+// few tokens: the packed weights streamed once per token tile
+hipError_t launch_glu_decode(const GluArgs& a, hipStream_t s);
+
+// Packed weight -> dense [R][Kp] (Kp = K rounded up to 64, zero filled) and /
+// or its transpose [K][ldt] at column c0 (rows r >= R of the last 64 zero),
+// and / or the kept bits [R][Kp / 8].
+hipError_t launch_expand_dense(const Geometry& g, const uint8_t* values, const uint8_t* meta, uint16_t* dense,
+                               hipStream_t s);
+hipError_t launch_expand_transposed(const Geometry& g, const uint8_t* values, const uint8_t* meta, uint16_t* dt,
+                                    int64_t ldt, uint8_t* mask, hipStream_t s);
+
+// dG = dH u act'(g), dU = dH act(g) from P = (g, u): rows of [T][ldd] (gate
+// at column 0, up at column Rp, zeros up to Rp) and transposed [2][R][Tp].
+hipError_t launch_glu_dact(const void* dH, int64_t ldh, const void* G, const void* U, int64_t ldp, int64_t T,
+                           int64_t R, int64_t Rp, void* d, int64_t ldd, void* dt, int64_t Tp, int act, int wdt,
+                           hipStream_t s);
+// copy of X [T][ldx] with rows of Kp elements, zeros past K
+hipError_t launch_pad_rows(const void* X, int64_t ldx, int64_t T, int64_t K, void* Y, int64_t Kp, hipStream_t s);
+
+hipError_t launch_mx_quantize(const void* X, int64_t ldx, int xdt, int64_t rows, int64_t K, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* Y,
+                                int64_t ldy, int ydt, hipStream_t s);
+
+struct MxDecodeArgs {
+  const uint8_t* codes[2];   // one weight, or gate and up
+  const uint8_t* scales[2];
+  int64_t R, K;
+  const void* X;             // 16- or 32-bit activations, quantised in registers ...
+  int64_t ldx;
+  int xdt;
+  const uint8_t* xcodes;     // ... or (X null) already quantised
+  const uint8_t* xscales;
+  int64_t T;
+  void* Y;
+  int64_t ldy;
+  int ydt;
+  const float* bias;
+  int act;
+  bool glu;
+};
+hipError_t launch_mx_decode(const MxDecodeArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- device
+// SiLU(x) = x / (1 + exp(-x)), binary32: exp2 and reciprocal of the
+// transcendental unit (1 ulp each); exp's rounded argument adds 2^-24 |x|
+// relative, so the error stays below 2^-22 (1 + |x|) |SiLU(x)|, far below
+// half a 16-bit step.  x -> -inf: exp overflows, its reciprocal is 0.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
+}
+__device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); }
+
+// act(x) and act'(x) of the gated block (NM_ACT_GELU or NM_ACT_SILU)
+__device__ __forceinline__ float glu_act(int act, float x) { return act == NM_ACT_SILU ? silu_f32(x) : gelu_f32(x); }
+__device__ __forceinline__ void glu_act_slope(int act, float x, float& y, float& dy) {
+  if (act == NM_ACT_SILU) {
+    const float s = sigmoid_f32(x);
+    y = x * s;
+    dy = s * (1.0f + x * (1.0f - s));
+  } else {
+    const float cdf = 0.5f * (1.0f + erf_as(x * 0.70710678118654752440f));
+    y = x * cdf;
+    // x phi(x), phi the normal density
+    dy = cdf + x * 0.39894228040143267794f * __builtin_amdgcn_exp2f(-0.5f * 1.44269504088896341f * x * x);
+  }
+}
+
+// two binary32 -> packed 16-bit floats, round to nearest even
+typedef float v2f_ __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h_ __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf_ __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ uint32_t pack_16x2(float lo, float hi) {
+  if constexpr (DT == NM_F16)
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f_{lo, hi}), v2h_));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f_{lo, hi}), v2bf_));
+}
+template <int DT>
+__device__ __forceinline__ float from_16(uint32_t bits) {
+  if constexpr (DT == NM_F16)
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  else
+    return __builtin_bit_cast(float, bits << 16);
+}
+
+// Four consecutive outputs y[0..3] of a row at element offset o; `n` of them
+// (1..4) exist; `vec`: the row starts and pitch allow one wide store.
+template <int DT>
+__device__ __forceinline__ void store4(void* Y, int64_t o, const float* y, int n, bool vec) {
+  if constexpr (DT == NM_F32) {
+    float* p = static_cast<float*>(Y) + o;
+    if (n == 4 && vec) {
+      *reinterpret_cast<v4f*>(p) = v4f{y[0], y[1], y[2], y[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) p[i] = y[i];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(Y) + o;
+    const uint32_t a = pack_16x2<DT>(y[0], y[1]), b = pack_16x2<DT>(y[2], y[3]);
+    if (n == 4 && vec) {
+      *reinterpret_cast<v2i*>(p) = v2i{(int)a, (int)b};
+    } else {
+      p[0] = (uint16_t)a;
+      if (n > 1) p[1] = (uint16_t)(a >> 16);
+      if (n > 2) p[2] = (uint16_t)b;
+      if (n > 3) p[3] = (uint16_t)(b >> 16);
+    }
+  }
+}
+// whether rows of `ld` elements of `eb` bytes from `p` start on 4-element boundaries
+inline bool vec4_ok(const void* p, int64_t ld, int eb) { return (uintptr_t)p % (4 * eb) == 0 && ld % 4 == 0; }
+
+}  // namespace nm

@@ -1,0 +1,418 @@
+// C ABI of the feed-forward operators (include/nm_sparse.h): host-side
+// validation, choice of the path per shape, launches.  Stateless and
+// thread-safe.
+#include "nm_ffn.hpp"
+
+using nm::Geometry;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// rows the tile kernel addresses with 32-bit offsets: 256 of them within 2^31 bytes
+bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
+
+// Up to this many tokens the weights are streamed (bound by their bytes);
+// beyond, the tile product shares them between tokens.
+constexpr int64_t kFewTokens = 64;
+
+// Longest dimension taken: products of two of them stay within 63 bits.
+constexpr int64_t kMaxLen = 1ll << 30;
+
+// ---------------------------------------------------------------- gated block, N:M weights
+nm_status check_pair(const nm_packed* gate, const nm_packed* up, Geometry* g) {
+  Geometry gu;
+  nm_status st = nm::check_packed(gate, g);
+  if (st != NM_OK) return st;
+  st = nm::check_packed(up, &gu);
+  if (st != NM_OK) return st;
+  if (gate->rows != up->rows || gate->K != up->K || gate->N != up->N || gate->M != up->M || gate->dtype != up->dtype)
+    return NM_EINVAL;
+  if (gate->dtype != NM_F16 && gate->dtype != NM_BF16) return NM_EUNSUPPORTED;
+  // dense rows of K within the tile kernel's offsets; grid limits along R
+  if (!row_ok(up64(g->K) * 2) || g->R > 65535ll * 64) return NM_EUNSUPPORTED;
+  return NM_OK;
+}
+
+bool glu_act_ok(int32_t act) { return act == NM_ACT_SILU || act == NM_ACT_GELU; }
+
+// whether the kernels can read X's rows as they are: 16-byte pieces, none of
+// which crosses the end of a row, and 32-bit offsets
+bool rows_direct(const void* X, int64_t ldx, int64_t K) {
+  return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
+}
+
+size_t padded_bytes(const Geometry& g, int64_t T) { return up256((size_t)(T * up64(g.K) * 2)); }
+size_t dense_bytes(const Geometry& g) { return up256((size_t)(g.R * up64(g.K) * 2)); }
+
+struct BackwardPlan {
+  int64_t Rp, Tp, Kp;
+  size_t d, dt, xt, wt, mask, total;   // bytes of each part (mask: of one weight)
+  BackwardPlan(const Geometry& g, int64_t T) {
+    Rp = up64(g.R);
+    Tp = up64(T);
+    Kp = up64(g.K);
+    d = up256((size_t)(T * 2 * Rp * 2));
+    dt = up256((size_t)(2 * g.R * Tp * 2));
+    xt = up256((size_t)(g.K * Tp * 2));
+    wt = up256((size_t)(g.K * 2 * Rp * 2));
+    mask = up256((size_t)(g.R * Kp / 8));
+    total = d + dt + xt + wt + 2 * mask;
+  }
+};
+
+// ---------------------------------------------------------------- microscaled format
+nm_status check_mx(const nm_mx* m) {
+  if (!m || m->rows < 1 || m->K < 1 || !m->codes || !m->scales) return NM_EINVAL;
+  if (m->K > kMaxLen || m->rows > kMaxLen) return NM_EUNSUPPORTED;
+  if ((int64_t)m->codes_bytes != nm::mx_codes_bytes(m->rows, m->K)) return NM_EINVAL;
+  if ((int64_t)m->scales_bytes != nm::mx_scales_bytes(m->rows, m->K)) return NM_EINVAL;
+  if (!aligned(m->codes, 16) || !aligned(m->scales, 16)) return NM_EUNSUPPORTED;
+  if ((m->rows + 31) / 32 * (nm::mx_kp(m->K) / nm::kMxSlab) >= (1ll << 31)) return NM_EUNSUPPORTED;
+  return NM_OK;
+}
+
+bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_F32; }
+
+size_t mx_ws_codes(int64_t T, int64_t K) { return up256((size_t)nm::mx_codes_bytes(T, K)); }
+size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm::mx_scales_bytes(T, K)); }
+
+nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const void* X, int64_t ldx, int32_t xdt,
+                     int64_t T, void* Y, int64_t ldy, int32_t ydt, const float* bias, int32_t act, void* ws,
+                     size_t ws_bytes, void* stream) {
+  const bool glu = w1 != nullptr;
+  nm_status st = check_mx(w0);
+  if (st != NM_OK) return st;
+  if (w0->format_version != NM_FORMAT_VERSION) return NM_EINVAL;
+  const int64_t R = w0->rows, K = w0->K, Kp = nm::mx_kp(K);
+  if (glu) {
+    st = check_mx(w1);
+    if (st != NM_OK) return st;
+    if (w1->format_version != NM_FORMAT_VERSION || w1->rows != R || w1->K != K) return NM_EINVAL;
+  }
+  if (!Y || T < 1 || ldy < R) return NM_EINVAL;
+  if (!float_dtype(ydt) || T > kMaxLen) return NM_EUNSUPPORTED;
+  if (glu ? !glu_act_ok(act) : (act != NM_ACT_NONE && act != NM_ACT_GELU)) return NM_EUNSUPPORTED;
+  if (!aligned(Y, (size_t)nm::dtype_bytes(ydt)) || (bias && !aligned(bias, 4))) return NM_EUNSUPPORTED;
+  if (!row_ok(Kp / 2)) return NM_EUNSUPPORTED;
+  if (xq) {
+    st = check_mx(xq);
+    if (st != NM_OK) return st;
+    if (xq->format_version != NM_FORMAT_VERSION || xq->rows != T || xq->K != K) return NM_EINVAL;
+  } else {
+    if (!X || ldx < K) return NM_EINVAL;
+    if (!float_dtype(xdt) || !aligned(X, (size_t)nm::dtype_bytes(xdt))) return NM_EUNSUPPORTED;
+    if ((T + 31) / 32 * (Kp / nm::kMxSlab) >= (1ll << 31)) return NM_EUNSUPPORTED;
+  }
+  const int xeb = xq ? 2 : nm::dtype_bytes(xdt);
+  // up to 16 tokens in whole 16-byte pieces are quantised inside the product
+  const bool in_registers = !xq && T <= 16 && aligned(X, 16) && ldx * xeb % 16 == 0 && K * xeb % 16 == 0;
+  const size_t need = xq || in_registers ? 0 : mx_ws(T, K);
+  if (need && (!ws || ws_bytes < need)) return NM_EINVAL;
+  if (need && !aligned(ws, 256)) return NM_EUNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+
+  const uint8_t* xcodes = xq ? static_cast<const uint8_t*>(xq->codes) : nullptr;
+  const uint8_t* xscales = xq ? static_cast<const uint8_t*>(xq->scales) : nullptr;
+  if (need) {
+    uint8_t* c = static_cast<uint8_t*>(ws);
+    uint8_t* sc = c + mx_ws_codes(T, K);
+    if (nm::launch_mx_quantize(X, ldx, xdt, T, K, c, sc, s) != hipSuccess) return NM_EHIP;
+    xcodes = c;
+    xscales = sc;
+  }
+  const nm_mx* ws2[2] = {w0, glu ? w1 : w0};
+  if (T <= kFewTokens) {
+    nm::MxDecodeArgs a{};
+    for (int i = 0; i < 2; ++i) {
+      a.codes[i] = static_cast<const uint8_t*>(ws2[i]->codes);
+      a.scales[i] = static_cast<const uint8_t*>(ws2[i]->scales);
+    }
+    a.R = R;
+    a.K = K;
+    a.X = in_registers ? X : nullptr;
+    a.ldx = ldx;
+    a.xdt = xdt;
+    a.xcodes = xcodes;
+    a.xscales = xscales;
+    a.T = T;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.ydt = ydt;
+    a.bias = bias;
+    a.act = act;
+    a.glu = glu;
+    return nm::launch_mx_decode(a, s) == hipSuccess ? NM_OK : NM_EHIP;
+  }
+  nm::TileArgs a{};
+  a.A[0] = a.A[1] = xcodes;
+  a.As = xscales;
+  for (int i = 0; i < 2; ++i) {
+    a.B[i] = static_cast<const uint8_t*>(ws2[i]->codes);
+    a.Bs[i] = static_cast<const uint8_t*>(ws2[i]->scales);
+  }
+  a.lda = a.ldb = Kp / 2;
+  a.Mr = T;
+  a.Nr = R;
+  a.ka = a.kb = (int)(Kp / 32);
+  a.nslab = (int)(Kp / nm::kMxSlab);
+  a.C[0] = a.C[1] = Y;
+  a.ldc = ldy;
+  a.bias = bias;
+  a.act = act;
+  a.batch = 1;
+  a.split = 1;
+  a.sps = a.nslab;
+  return nm::launch_tile_mx(glu ? nm::TILE_GLU : nm::TILE_LINEAR, ydt, a, s) == hipSuccess ? NM_OK : NM_EHIP;
+}
+
+hipError_t launch_tile16(int wdt, nm::TileOp op, const nm::TileArgs& a, hipStream_t s) {
+  return wdt == NM_F16 ? nm::launch_tile_f16(op, wdt, a, s) : nm::launch_tile_bf16(op, wdt, a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes) {
+  if (!bytes || T < 1) return NM_EINVAL;
+  Geometry g;
+  const nm_status st = check_pair(gate, up, &g);
+  if (st != NM_OK) return st;
+  if (T > kMaxLen) return NM_EUNSUPPORTED;
+  *bytes = padded_bytes(g, T) + (T > kFewTokens ? 2 * dense_bytes(g) : 0);
+  return NM_OK;
+}
+
+nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
+                 int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  Geometry g;
+  const nm_status st = check_pair(gate, up, &g);
+  if (st != NM_OK) return st;
+  if (T > kMaxLen) return NM_EUNSUPPORTED;
+  if (gate->format_version != NM_FORMAT_VERSION || up->format_version != NM_FORMAT_VERSION) return NM_EINVAL;
+  if (!Xt || !Ht || T < 1 || ldx < g.K || ldh < g.R) return NM_EINVAL;
+  if ((G == nullptr) != (U == nullptr) || (G && ldp < g.R)) return NM_EINVAL;
+  if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
+  if (!aligned(Xt, 2) || !aligned(Ht, 2) || (G && (!aligned(G, 2) || !aligned(U, 2)))) return NM_EUNSUPPORTED;
+  const bool direct = rows_direct(Xt, ldx, g.K);
+  const bool few = T <= kFewTokens;
+  const size_t pad = direct ? 0 : padded_bytes(g, T);
+  const size_t need = pad + (few ? 0 : 2 * dense_bytes(g));
+  if (need && (!workspace || workspace_bytes < need)) return NM_EINVAL;
+  if (need && !aligned(workspace, 256)) return NM_EUNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+
+  const void* X = Xt;
+  int64_t ld = ldx;
+  if (!direct) {
+    ld = up64(g.K);
+    if (nm::launch_pad_rows(Xt, ldx, T, g.K, ws, ld, s) != hipSuccess) return NM_EHIP;
+    X = ws;
+  }
+  const nm_packed* w[2] = {gate, up};
+  if (few) {
+    nm::GluArgs a{};
+    a.g = g;
+    a.wdt = gate->dtype;
+    for (int i = 0; i < 2; ++i) {
+      a.values[i] = static_cast<const uint8_t*>(w[i]->values);
+      a.meta[i] = g.w ? static_cast<const uint8_t*>(w[i]->meta) : nullptr;
+    }
+    a.X = X;
+    a.ldx = ld;
+    a.T = T;
+    a.H = Ht;
+    a.ldh = ldh;
+    a.P[0] = G;
+    a.P[1] = U;
+    a.ldp = ldp;
+    a.act = act;
+    // a padded row is all 16-byte pieces: its zeros may be read
+    if (!direct) a.g.K = ld;
+    return nm::launch_glu_decode(a, s) == hipSuccess ? NM_OK : NM_EHIP;
+  }
+  nm::TileArgs a{};
+  const int64_t Kp = up64(g.K);
+  for (int i = 0; i < 2; ++i) {
+    uint8_t* d = ws + pad + i * dense_bytes(g);
+    if (nm::launch_expand_dense(g, static_cast<const uint8_t*>(w[i]->values), static_cast<const uint8_t*>(w[i]->meta),
+                                reinterpret_cast<uint16_t*>(d), s) != hipSuccess)
+      return NM_EHIP;
+    a.A[i] = static_cast<const uint8_t*>(X);
+    a.B[i] = d;
+  }
+  a.lda = ld * 2;
+  a.ldb = Kp * 2;
+  a.Mr = T;
+  a.Nr = g.R;
+  a.ka = (int)((direct ? g.K : Kp) / 8);
+  a.kb = (int)(Kp / 8);
+  a.nslab = (int)(Kp / 64);
+  a.C[0] = Ht;
+  a.ldc = ldh;
+  a.P[0] = G;
+  a.P[1] = U;
+  a.ldp = ldp;
+  a.act = act;
+  a.batch = 1;
+  a.split = 1;
+  a.sps = a.nslab;
+  return launch_tile16(gate->dtype, nm::TILE_GLU, a, s) == hipSuccess ? NM_OK : NM_EHIP;
+}
+
+nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes) {
+  if (!bytes || T < 1) return NM_EINVAL;
+  Geometry g;
+  const nm_status st = check_pair(gate, up, &g);
+  if (st != NM_OK) return st;
+  if (T > kMaxLen) return NM_EUNSUPPORTED;
+  if (!row_ok(up64(T) * 2) || !row_ok(up64(g.R) * 4)) return NM_EUNSUPPORTED;
+  *bytes = BackwardPlan(g, T).total;
+  return NM_OK;
+}
+
+nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
+                          const void* G, const void* U, int64_t ldp, const void* dH, int64_t lddh, int32_t act,
+                          void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  Geometry g;
+  const nm_status st = check_pair(gate, up, &g);
+  if (st != NM_OK) return st;
+  if (T > kMaxLen) return NM_EUNSUPPORTED;
+  if (gate->format_version != NM_FORMAT_VERSION || up->format_version != NM_FORMAT_VERSION) return NM_EINVAL;
+  if (!Xt || !G || !U || !dH || T < 1 || ldx < g.K || ldp < g.R || lddh < g.R) return NM_EINVAL;
+  if ((dWg == nullptr) != (dWu == nullptr) || (!dX && !dWg)) return NM_EINVAL;
+  if ((dX && lddx < g.K) || (dWg && lddw < g.K)) return NM_EINVAL;
+  if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
+  if (!aligned(Xt, 2) || !aligned(G, 2) || !aligned(U, 2) || !aligned(dH, 2) || !aligned(dX, 2) || !aligned(dWg, 2) ||
+      !aligned(dWu, 2))
+    return NM_EUNSUPPORTED;
+  // transposed rows of T, and rows of both dG and dU, within the tile kernel's offsets
+  if (!row_ok(up64(T) * 2) || !row_ok(up64(g.R) * 4)) return NM_EUNSUPPORTED;
+  const BackwardPlan p(g, T);
+  if (!workspace || workspace_bytes < p.total) return NM_EINVAL;
+  if (!aligned(workspace, 256)) return NM_EUNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* d = static_cast<uint8_t*>(workspace);
+  uint8_t* dt = d + p.d;
+  uint8_t* xt = dt + p.dt;
+  uint8_t* wt = xt + p.xt;
+  uint8_t* mask = wt + p.wt;
+  const nm_packed* w[2] = {gate, up};
+
+  if (nm::launch_glu_dact(dH, lddh, G, U, ldp, T, g.R, p.Rp, dX ? d : nullptr, 2 * p.Rp, dWg ? dt : nullptr, p.Tp, act,
+                          gate->dtype, s) != hipSuccess)
+    return NM_EHIP;
+  for (int i = 0; i < 2; ++i)
+    if (nm::launch_expand_transposed(g, static_cast<const uint8_t*>(w[i]->values),
+                                     static_cast<const uint8_t*>(w[i]->meta),
+                                     reinterpret_cast<uint16_t*>(wt) + i * p.Rp, 2 * p.Rp,
+                                     dWg ? mask + i * p.mask : nullptr, s) != hipSuccess)
+      return NM_EHIP;
+  if (dX) {
+    // dX[t][k] = sum over both weights' rows of d[t][r] W[r][k]
+    nm::TileArgs a{};
+    a.A[0] = d;
+    a.B[0] = wt;
+    a.lda = a.ldb = 4 * p.Rp;
+    a.Mr = T;
+    a.Nr = g.K;
+    a.ka = a.kb = (int)(2 * p.Rp / 8);
+    a.nslab = (int)(2 * p.Rp / 64);
+    a.C[0] = dX;
+    a.ldc = lddx;
+    a.batch = 1;
+    a.split = 1;
+    a.sps = a.nslab;
+    if (launch_tile16(gate->dtype, nm::TILE_LINEAR, a, s) != hipSuccess) return NM_EHIP;
+  }
+  if (dWg) {
+    // dW[r][k] = sum over t of d[t][r] X[t][k], both transposed
+    if (nm::launch_transpose(Xt, T, g.K, ldx, xt, p.Tp, p.Tp, 2, s) != hipSuccess) return NM_EHIP;
+    nm::TileArgs a{};
+    for (int i = 0; i < 2; ++i) {
+      a.A[i] = dt + (size_t)i * g.R * p.Tp * 2;
+      a.B[i] = xt;
+      a.mask[i] = mask + i * p.mask;
+    }
+    a.C[0] = dWg;
+    a.C[1] = dWu;
+    a.lda = a.ldb = 2 * p.Tp;
+    a.Mr = g.R;
+    a.Nr = g.K;
+    a.ka = a.kb = (int)(p.Tp / 8);
+    a.nslab = (int)(p.Tp / 64);
+    a.ldc = lddw;
+    a.ldm = p.Kp / 8;
+    a.batch = 2;
+    a.split = 1;
+    a.sps = a.nslab;
+    if (launch_tile16(gate->dtype, nm::TILE_MASKED, a, s) != hipSuccess) return NM_EHIP;
+  }
+  return NM_OK;
+}
+
+nm_status nm_mx_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes) {
+  if (!codes_bytes || !scales_bytes || rows < 1 || K < 1) return NM_EINVAL;
+  if (K > kMaxLen || rows > kMaxLen) return NM_EUNSUPPORTED;
+  *codes_bytes = (size_t)nm::mx_codes_bytes(rows, K);
+  *scales_bytes = (size_t)nm::mx_scales_bytes(rows, K);
+  return NM_OK;
+}
+
+nm_status nm_mx_quantize(const void* X, int64_t ldx, int32_t x_dtype, nm_mx* m, void* stream) {
+  const nm_status st = check_mx(m);
+  if (st != NM_OK) return st;
+  if (!X || ldx < m->K) return NM_EINVAL;
+  if (!float_dtype(x_dtype) || !aligned(X, (size_t)nm::dtype_bytes(x_dtype))) return NM_EUNSUPPORTED;
+  if (nm::launch_mx_quantize(X, ldx, x_dtype, m->rows, m->K, static_cast<uint8_t*>(m->codes),
+                             static_cast<uint8_t*>(m->scales), static_cast<hipStream_t>(stream)) != hipSuccess)
+    return NM_EHIP;
+  m->format_version = NM_FORMAT_VERSION;
+  m->reserved = 0;
+  return NM_OK;
+}
+
+nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype, void* stream) {
+  const nm_status st = check_mx(m);
+  if (st != NM_OK) return st;
+  if (m->format_version != NM_FORMAT_VERSION || !Y || ldy < m->K) return NM_EINVAL;
+  if (!float_dtype(y_dtype) || !aligned(Y, (size_t)nm::dtype_bytes(y_dtype))) return NM_EUNSUPPORTED;
+  if ((m->rows * ((m->K + 7) / 8) + 255) / 256 >= (1ll << 31)) return NM_EUNSUPPORTED;
+  return nm::launch_mx_dequantize(static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales),
+                                  m->rows, m->K, Y, ldy, y_dtype, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? NM_OK
+             : NM_EHIP;
+}
+
+nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* bytes) {
+  (void)glu;
+  if (!bytes || T < 1) return NM_EINVAL;
+  const nm_status st = check_mx(w);
+  if (st != NM_OK) return st;
+  if (!row_ok(nm::mx_kp(w->K) / 2) || T > kMaxLen) return NM_EUNSUPPORTED;
+  *bytes = mx_ws(T, w->K);
+  return NM_OK;
+}
+
+nm_status nm_mx_linear(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
+                       void* Yt, int64_t ldy, int32_t y_dtype, const float* bias, int32_t act, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return mx_product(w, nullptr, xq, Xt, ldx, x_dtype, T, Yt, ldy, y_dtype, bias, act, workspace, workspace_bytes,
+                    stream);
+}
+
+nm_status nm_mx_glu(const nm_mx* gate, const nm_mx* up, const nm_mx* xq, const void* Xt, int64_t ldx,
+                    int32_t x_dtype, int64_t T, void* Ht, int64_t ldh, int32_t h_dtype, int32_t act, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!up) return NM_EINVAL;
+  return mx_product(gate, up, xq, Xt, ldx, x_dtype, T, Ht, ldh, h_dtype, nullptr, act, workspace, workspace_bytes,
+                    stream);
+}
+
+}  // extern "C"

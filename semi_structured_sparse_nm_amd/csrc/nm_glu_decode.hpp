@@ -1,0 +1,209 @@
+// Gated block for few tokens: H = act(X Wg^T) (.) (X Wu^T), both packed
+// weights streamed once from HBM for every tile of 16 NT tokens.
+//
+// With so few tokens the bound is the packed weights' bytes.  A workgroup
+// owns one 16-row block of both weights; its NW waves take every NW-th
+// 64-column block, so they read neighbouring blocks at a time, straight to
+// registers (a fragment of a packed block is one contiguous run), U blocks
+// of both weights in flight per wave; the activations come from the caches
+// (every workgroup reads the same rows).  2:4 windows go to the sparse matrix
+// instruction as they are; other patterns are expanded in registers for the
+// dense one.  The waves' sums meet in LDS, added in wave order.
+#pragma once
+
+#include "nm_expand.hpp"
+#include "nm_ffn.hpp"
+
+namespace nm {
+
+namespace {
+
+typedef _Float16 v16h_ __attribute__((ext_vector_type(16)));
+typedef __bf16 v16bf_ __attribute__((ext_vector_type(16)));
+
+template <int WT>
+__device__ __forceinline__ v4f smfmac24(v4i a, v8i b, v4f c, int idx) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (WT == NM_F16)
+    return __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v16h_, b), c, idx,
+                                                    0, 0);
+  else
+    return __builtin_amdgcn_smfmac_f32_16x16x64_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v16bf_, b), c,
+                                                     idx, 0, 0);
+#else
+  return c;
+#endif
+}
+
+constexpr int kGluWaves = 8;
+
+// One lane's part of one packed block (64 dense columns).
+template <int WT, int N, int M>
+struct GluFrag {
+  typedef Run<WT, N, M> RunT;
+  static constexpr bool SPARSE = N == 2 && M == 4;
+  uint32_t vd[RunT::VD];
+  uint64_t mb;
+  __device__ __forceinline__ void load(const uint8_t* values, const uint8_t* meta, int64_t blk, int li, int lg) {
+    const uint8_t* v = values + blk * (16 * RunT::C_B) + li * RunT::C_B + lg * RunT::VB;
+#pragma unroll
+    for (int i = 0; i < RunT::VD; ++i) vd[i] = reinterpret_cast<const uint32_t*>(v)[i];
+    mb = 0;
+    if constexpr (N != M) {
+      const uint8_t* m = meta + blk * (16 * RunT::MRB) + li * RunT::MRB;
+      if constexpr (SPARSE) {
+        mb = *reinterpret_cast<const uint16_t*>(m + 2 * lg);
+      } else {
+        int dw, sh;
+        RunT::meta_window(lg, dw, sh);
+        const uint32_t* mw = reinterpret_cast<const uint32_t*>(m);
+        mb = mw[dw];
+        if (RunT::MRB >= 8) mb |= (uint64_t)mw[dw + 1] << 32;
+        mb >>= sh;
+        // 7:8 (42 bits a lane): lane group 3 starts at bit 30 of its dword
+        // and needs a third one (every group's third dword is in the row)
+        if constexpr (RunT::MBL > 36) {
+          static_assert(RunT::MRB >= 24, "three dwords from every window's first");
+          if (sh) mb |= (uint64_t)mw[dw + 2] << (64 - sh);
+        }
+      }
+    }
+  }
+  // x: the lane's 16 activations, as the two 16-byte pieces the product wants
+  __device__ __forceinline__ v4f mul(v4i x0, v4i x1, v4f c) const {
+    if constexpr (SPARSE) {
+      const v4i a = {(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
+      return smfmac24<WT>(a, v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]}, c, (int)mb);
+    } else {
+#if defined(__HIP_DEVICE_COMPILE__)
+      c = mfma_dense<WT>(expand_step<WT, N, M, 0>(vd, mb), x0, c);
+      return mfma_dense<WT>(expand_step<WT, N, M, 1>(vd, mb), x1, c);
+#else
+      return c;
+#endif
+    }
+  }
+  // first column of each piece within the block: the sparse instruction's
+  // second operand holds k = 8 lg .. and 32 + 8 lg .., the dense steps the
+  // halves of the lane's run of 16
+  __device__ static int kpiece(int p, int lg) { return SPARSE ? 32 * p + 8 * lg : 16 * lg + 8 * p; }
+};
+
+template <int WT, int N, int M, int NT>
+__global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = kGluWaves;
+  constexpr int U = NT == 1 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) v4f red[NW][2 * NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int li = lane & 15, lg = lane >> 4;
+  const int64_t rb = blockIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+  const int nKB = (int)a.g.nKB;
+  const int K = (int)a.g.K;
+  typedef GluFrag<WT, N, M> Frag;
+
+  const uint16_t* xr[NT];
+  bool xv[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t t = t0 + 16 * j + li;
+    xv[j] = t < a.T;
+    xr[j] = static_cast<const uint16_t*>(a.X) + (xv[j] ? t : 0) * a.ldx;
+  }
+  v4f ag[NT], au[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) ag[j] = au[j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  for (int b0 = wave; b0 < nKB; b0 += NW * U) {
+    Frag fg[U], fu[U];
+    v4i x[U][NT][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int kb = min(b0 + NW * i, nKB - 1);        // past the end: a block read again, not used
+      fg[i].load(a.values[0], a.meta[0], rb * nKB + kb, li, lg);
+      fu[i].load(a.values[1], a.meta[1], rb * nKB + kb, li, lg);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int k = kb * 64 + Frag::kpiece(p, lg);
+          x[i][j][p] = v4i{0, 0, 0, 0};
+          if (xv[j] && k < K) x[i][j][p] = *reinterpret_cast<const v4i*>(xr[j] + k);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (b0 + NW * i < nKB) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          ag[j] = fg[i].mul(x[i][j][0], x[i][j][1], ag[j]);
+          au[j] = fu[i].mul(x[i][j][0], x[i][j][1], au[j]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    red[wave][2 * j][lane] = ag[j];
+    red[wave][2 * j + 1][lane] = au[j];
+  }
+  __syncthreads();
+  for (int q = threadIdx.x; q < 256 * NT; q += NW * 64) {
+    const int row = q & 15, tok = q >> 4;              // token tok % 16 of tile tok / 16
+    const int ln = 16 * (row >> 2) + (tok & 15), v = row & 3, j = tok >> 4;
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      g += reinterpret_cast<const float*>(&red[w][2 * j][ln])[v];
+      u += reinterpret_cast<const float*>(&red[w][2 * j + 1][ln])[v];
+    }
+    const int64_t r = rb * 16 + row, t = t0 + tok;
+    if (r < a.g.R && t < a.T) {
+      const float h = glu_act(a.act, g) * u;
+      static_cast<uint16_t*>(a.H)[t * a.ldh + r] = (uint16_t)pack_16x2<WT>(h, 0.f);
+      if (a.P[0]) {
+        static_cast<uint16_t*>(a.P[0])[t * a.ldp + r] = (uint16_t)pack_16x2<WT>(g, 0.f);
+        static_cast<uint16_t*>(a.P[1])[t * a.ldp + r] = (uint16_t)pack_16x2<WT>(u, 0.f);
+      }
+    }
+  }
+#endif
+}
+
+template <int WT, int N, int M>
+hipError_t launch_glu_decode_nm(const GluArgs& a, hipStream_t s) {
+  const unsigned nrb = (unsigned)a.g.nRB;
+  const dim3 block(kGluWaves * 64);
+  if (a.T <= 16)
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 1>), dim3(nrb, 1), block, 0, s, a);
+  else if (a.T <= 32)
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 2>), dim3(nrb, 1), block, 0, s, a);
+  else
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 4>), dim3(nrb, (unsigned)((a.T + 63) / 64)), block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <int WT>
+hipError_t launch_glu_decode_wt(const GluArgs& a, hipStream_t s) {
+  switch (a.g.M * 16 + a.g.N) {
+    case 4 * 16 + 1: return launch_glu_decode_nm<WT, 1, 4>(a, s);
+    case 4 * 16 + 2: return launch_glu_decode_nm<WT, 2, 4>(a, s);
+    case 4 * 16 + 3: return launch_glu_decode_nm<WT, 3, 4>(a, s);
+    case 4 * 16 + 4: return launch_glu_decode_nm<WT, 4, 4>(a, s);
+    case 8 * 16 + 1: return launch_glu_decode_nm<WT, 1, 8>(a, s);
+    case 8 * 16 + 2: return launch_glu_decode_nm<WT, 2, 8>(a, s);
+    case 8 * 16 + 3: return launch_glu_decode_nm<WT, 3, 8>(a, s);
+    case 8 * 16 + 4: return launch_glu_decode_nm<WT, 4, 8>(a, s);
+    case 8 * 16 + 5: return launch_glu_decode_nm<WT, 5, 8>(a, s);
+    case 8 * 16 + 6: return launch_glu_decode_nm<WT, 6, 8>(a, s);
+    case 8 * 16 + 7: return launch_glu_decode_nm<WT, 7, 8>(a, s);
+    case 8 * 16 + 8: return launch_glu_decode_nm<WT, 8, 8>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+}  // namespace nm

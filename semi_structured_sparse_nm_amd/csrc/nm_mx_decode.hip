@@ -1,0 +1,207 @@
+// Microscaled 4-bit product and gated block for few tokens: the weights'
+// codes are streamed once from HBM for every tile of 16 NT tokens.
+//
+// A workgroup owns 16 weight rows (of both weights for the gated block); its
+// waves take every NW-th slab of 256 columns, so a wave reads whole 128-byte
+// lines of each row.  A lane of the scaled matrix instruction holds exactly
+// one block of 32 of its row, so for up to 16 tokens the activations are
+// quantised in registers on the way (one launch in all); for more they come
+// quantised.  The waves' sums meet in LDS, added in wave order.
+#include "nm_mx_device.hpp"
+
+namespace nm {
+
+namespace {
+
+constexpr int kMxWaves = 8;
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int OA, int OB>
+__device__ __forceinline__ v4f mx_mul(v4i a, v4i b, v4f c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8i{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
+                                                          v8i{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, c, 4, 4, OA, sa,
+                                                          OB, sb);
+}
+#endif
+
+// XDT: type of the activations quantised here (NT = 1), or -1: xcodes
+template <int XDT, bool GLU, int NT>
+__global__ void __launch_bounds__(kMxWaves * 64) mx_decode_kernel(MxDecodeArgs a, int nslab) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = kMxWaves;
+  constexpr int NWT = GLU ? 2 : 1;                     // weights
+  constexpr bool Q = XDT >= 0;
+  constexpr int EB = XDT == NM_F32 ? 4 : 2;
+  constexpr int ND = 8 * EB;                           // dwords of a block of 32
+  static_assert(!Q || NT == 1, "activations are quantised here for one token tile");
+  __shared__ __attribute__((aligned(16))) v4f red[NW][NWT * NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int64_t rb = blockIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+  const int64_t ldc = (int64_t)nslab * 128;
+
+  const int64_t row = min(rb * 16 + li, a.R - 1);      // rows past R: the last one again, not stored
+  const uint8_t* wc[NWT];
+  const uint8_t* wsc[NWT];
+#pragma unroll
+  for (int w = 0; w < NWT; ++w) {
+    wc[w] = a.codes[w] + row * ldc + 16 * lq;
+    wsc[w] = a.scales[w] + (rb / 2) * (int64_t)nslab * 256 + 4 * lane;
+  }
+  const int wsh = 16 * (int)(rb & 1);                  // this 16-row half's two scales of each word
+
+  const uint8_t* xc[NT];
+  bool xv[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t t = t0 + 16 * j + li;
+    xv[j] = t < a.T;
+    if constexpr (Q)
+      xc[j] = static_cast<const uint8_t*>(a.X) + (xv[j] ? t : 0) * a.ldx * EB;
+    else
+      xc[j] = a.xcodes + (xv[j] ? t : 0) * ldc + 16 * lq;
+  }
+
+  v4f acc[NWT][NT];
+#pragma unroll
+  for (int w = 0; w < NWT; ++w)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[w][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  for (int s = wave; s < nslab; s += NW) {
+    v4i fw[NWT][2];
+    int sw[NWT];
+#pragma unroll
+    for (int w = 0; w < NWT; ++w) {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) fw[w][kk] = *reinterpret_cast<const v4i*>(wc[w] + (int64_t)s * 128 + 64 * kk);
+      sw[w] = (int)(*reinterpret_cast<const uint32_t*>(wsc[w] + (int64_t)s * 256) >> wsh);
+    }
+    v4i fx[NT][2];
+    int sx[NT];
+    if constexpr (Q) {
+      uint32_t x[2][ND];
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const int64_t k = (int64_t)s * 256 + kk * 128 + lq * 32;
+#pragma unroll
+        for (int i = 0; i < ND / 4; ++i) {
+          v4i v = {0, 0, 0, 0};
+          if (xv[0] && k + i * (16 / EB) < a.K) v = *reinterpret_cast<const v4i*>(xc[0] + k * EB + 16 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[kk][4 * i + e] = (uint32_t)v[e];
+        }
+      }
+      sx[0] = 0;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        uint32_t m = 0;
+        if constexpr (XDT == NM_F32) {
+#pragma unroll
+          for (int i = 0; i < ND; ++i) m = max(m, x[kk][i] & 0x7FFFFFFFu);
+        } else {
+#pragma unroll
+          for (int i = 0; i < ND; ++i) m = max_16x2(m, x[kk][i] & 0x7FFF7FFFu);
+          m = amax_bits_16<XDT>(m);
+        }
+        const uint32_t byte = mx_scale_byte(m);
+        const float sc = mx_scale_f32(byte);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t c = mx_codes8<XDT>(&x[kk][i * (ND / 4)], sc);
+          fx[0][kk][i] = byte == 255u ? 0 : (int)c;
+        }
+        sx[0] |= (int)(byte << (8 * kk));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          fx[j][kk] = v4i{0, 0, 0, 0};
+          if (xv[j]) fx[j][kk] = *reinterpret_cast<const v4i*>(xc[j] + (int64_t)s * 128 + 64 * kk);
+        }
+        // token tile t0 / 16 + j: half of the scale unit of its 32 tokens
+        const int64_t tt = t0 / 16 + j;
+        const int64_t unit = min(tt / 2, (a.T - 1) / 32);
+        sx[j] = (int)(*reinterpret_cast<const uint32_t*>(a.xscales + (unit * nslab + s) * 256 + 4 * lane) >>
+                      (16 * (int)(tt & 1)));
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < NWT; ++w)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        acc[w][j] = mx_mul<0, 0>(fw[w][0], fx[j][0], acc[w][j], sw[w], sx[j]);
+        acc[w][j] = mx_mul<1, 1>(fw[w][1], fx[j][1], acc[w][j], sw[w], sx[j]);
+      }
+  }
+#pragma unroll
+  for (int w = 0; w < NWT; ++w)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) red[wave][w * NT + j][lane] = acc[w][j];
+  __syncthreads();
+  for (int q = threadIdx.x; q < 256 * NT; q += NW * 64) {
+    const int rr = q & 15, tok = q >> 4;
+    const int ln = 16 * (rr >> 2) + (tok & 15), v = rr & 3, j = tok >> 4;
+    float y[NWT];
+#pragma unroll
+    for (int w = 0; w < NWT; ++w) {
+      y[w] = 0.f;
+#pragma unroll
+      for (int p = 0; p < NW; ++p) y[w] += reinterpret_cast<const float*>(&red[p][w * NT + j][ln])[v];
+    }
+    const int64_t r = rb * 16 + rr, t = t0 + tok;
+    if (r < a.R && t < a.T) {
+      float o;
+      if constexpr (GLU) {
+        o = glu_act(a.act, y[0]) * y[NWT - 1];
+      } else {
+        o = y[0];
+        if (a.bias) o += a.bias[r];
+        if (a.act == NM_ACT_GELU) o = gelu_f32(o);
+      }
+      const int64_t at = t * a.ldy + r;
+      if (a.ydt == NM_F32)
+        static_cast<float*>(a.Y)[at] = o;
+      else if (a.ydt == NM_F16)
+        static_cast<uint16_t*>(a.Y)[at] = (uint16_t)pack_16x2<NM_F16>(o, 0.f);
+      else
+        static_cast<uint16_t*>(a.Y)[at] = (uint16_t)pack_16x2<NM_BF16>(o, 0.f);
+    }
+  }
+#endif
+}
+
+template <bool GLU>
+hipError_t launch_decode(const MxDecodeArgs& a, hipStream_t s) {
+  const int nslab = (int)(mx_kp(a.K) / kMxSlab);
+  const unsigned nrb = (unsigned)((a.R + 15) / 16);
+  const dim3 block(kMxWaves * 64);
+  if (a.X) {
+    const dim3 grid(nrb, (unsigned)((a.T + 15) / 16));
+    if (a.xdt == NM_F16)
+      hipLaunchKernelGGL((mx_decode_kernel<NM_F16, GLU, 1>), grid, block, 0, s, a, nslab);
+    else if (a.xdt == NM_BF16)
+      hipLaunchKernelGGL((mx_decode_kernel<NM_BF16, GLU, 1>), grid, block, 0, s, a, nslab);
+    else
+      hipLaunchKernelGGL((mx_decode_kernel<NM_F32, GLU, 1>), grid, block, 0, s, a, nslab);
+  } else if (a.T <= 16) {
+    hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 1>), dim3(nrb, 1), block, 0, s, a, nslab);
+  } else if (a.T <= 32) {
+    hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 2>), dim3(nrb, 1), block, 0, s, a, nslab);
+  } else {
+    hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 4>), dim3(nrb, (unsigned)((a.T + 63) / 64)), block, 0, s, a, nslab);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_decode(const MxDecodeArgs& a, hipStream_t s) {
+  return a.glu ? launch_decode<true>(a, s) : launch_decode<false>(a, s);
+}
+
+}  // namespace nm

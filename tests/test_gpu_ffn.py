@@ -1,0 +1,404 @@
+"""The feed-forward operators on the GPU against their plain 64-bit forms
+(tests/_ffn.py, which derives the elementwise bounds): the gated block on N:M
+packed weights, its gradients, the microscaled 4-bit format, its product and
+its gated block."""
+import zlib
+
+import pytest
+import torch
+
+import semi_structured_sparse_nm_amd as nm
+from tests import _ffn
+from tests._ffn import TORCH, check
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(*key):
+    g = torch.Generator()
+    g.manual_seed(zlib.crc32(repr(key).encode()))
+    return g
+
+
+def normal(shape, std, dt, *key):
+    return (torch.randn(*shape, generator=_gen(*key)) * std).to(TORCH[dt]).cuda()
+
+
+def wide(t, pad, fill=0.0):
+    """t as a slice of a buffer with `pad` more columns, filled with `fill`."""
+    b = torch.full((t.shape[0], t.shape[1] + pad), fill, dtype=t.dtype, device=t.device)
+    b[:, :t.shape[1]] = t
+    return b, b[:, :t.shape[1]]
+
+
+def weights(R, K, N, M, dt, *key):
+    """(packed, masked dense, mask) of one seeded weight."""
+    W = normal((R, K), 0.05, dt, "W", R, K, *key)
+    k = _ffn.kept(W, N, M)
+    return nm.pack(W, N, M), torch.where(k, W, torch.zeros_like(W)), k
+
+
+# one token to several tiles; rows and columns inside and past 16, 64, 128
+SHAPES = [(1, 1, 8), (1, 16, 64), (2, 17, 72), (15, 40, 264), (16, 130, 512), (17, 33, 64), (31, 64, 1032),
+          (33, 48, 128), (64, 129, 200), (65, 128, 64), (66, 1, 8), (128, 200, 128), (129, 65, 136), (300, 500, 712)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,R,K", SHAPES)
+def test_glu_shapes(T, R, K, dt):
+    pg, wg, _ = weights(R, K, 2, 4, dt, "g")
+    pu, wu, _ = weights(R, K, 2, 4, dt, "u")
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    for act in ("silu", "gelu"):
+        h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, act)
+        pre = torch.full((2, T, R), 7.0, dtype=X.dtype, device="cuda")
+        H = nm.glu(pg, pu, X, act=act, pre=pre)
+        check(H, h, eh, f"H {act}")
+        check(pre[0], g, eg, "G")
+        check(pre[1], u, eu, "U")
+        assert torch.equal(nm.glu(pg, pu, X, act=act), H), "the call without pre differs"
+
+
+@pytest.mark.parametrize("N,M", [(1, 4), (3, 4), (4, 4), (1, 8), (2, 8), (3, 8), (4, 8), (5, 8), (6, 8), (7, 8),
+                                 (8, 8)])
+@pytest.mark.parametrize("T,R,K", [(1, 33, 72), (20, 48, 328), (50, 17, 64), (90, 70, 136)])
+def test_glu_patterns(T, R, K, N, M):
+    dt = "f16" if N % 2 else "bf16"
+    pg, wg, kg = weights(R, K, N, M, dt, "g", N)
+    pu, wu, ku = weights(R, K, N, M, dt, "u", N)
+    X = normal((T, K), 1.0, dt, "X", T, K, N)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "silu")
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    check(nm.glu(pg, pu, X, pre=pre), h, eh, "H")
+    dH = normal((T, R), 0.1, dt, "dH", T, R, N)
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, X, pre, dH), want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+@pytest.mark.parametrize("T,R,K", [(5, 20, 12), (70, 40, 100), (3, 64, 64), (80, 64, 64)])
+@pytest.mark.parametrize("xpad,ypad", [(0, 3), (5, 0), (8, 4), (1, 1)])
+def test_glu_strides(T, R, K, xpad, ypad):
+    """Rows whose pitch or length is no multiple of 16 bytes, an activation
+    buffer whose other columns hold NaN, outputs inside wider buffers."""
+    pg, wg, kg = weights(R, K, 2, 4, "f16", "g")
+    pu, wu, ku = weights(R, K, 2, 4, "f16", "u")
+    X = normal((T, K), 1.0, "f16", "X", T, K)
+    _, xv = wide(X, xpad, float("nan"))
+    hb, hv = wide(torch.zeros(T, R, dtype=X.dtype, device="cuda"), ypad, 5.0)
+    pb = torch.full((2, T, R + ypad), 5.0, dtype=X.dtype, device="cuda")
+    pre = pb[:, :, :R]
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "silu")
+    assert nm.glu(pg, pu, xv, out=hv, pre=pre) is hv
+    check(hv, h, eh, "H")
+    check(pre[0], g, eg, "G")
+    assert bool((hb[:, R:] == 5.0).all()) and bool((pb[:, :, R:] == 5.0).all())
+    dH = normal((T, R), 0.1, "f16", "dH", T, R)
+    _, dv = wide(dH, ypad, float("nan"))
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, xv, pre, dv), want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+@pytest.mark.parametrize("T,R,K,dt", [(1, 1, 8, "f16"), (3, 17, 72, "bf16"), (64, 64, 64, "f16"), (65, 130, 200, "bf16"),
+                                      (197, 200, 768, "f16"), (300, 520, 264, "bf16")])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_glu_backward_shapes(T, R, K, dt, act):
+    pg, wg, kg = weights(R, K, 2, 4, dt, "g")
+    pu, wu, ku = weights(R, K, 2, 4, dt, "u")
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    dH = normal((T, R), 0.1, dt, "dH", T, R)
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    nm.glu(pg, pu, X, act=act, pre=pre)
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, act)
+    got = nm.glu_backward(pg, pu, X, pre, dH, act=act)
+    for a, b, e, k, what in zip(got, want, bound, (None, kg, ku), ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+        if k is not None:
+            assert bool((a[~k] == 0).all()), f"{what} is not zero where the weight is pruned"
+    dx, none_g, none_u = nm.glu_backward(pg, pu, X, pre, dH, act=act, need_dw=False)
+    assert none_g is None and none_u is None and torch.equal(dx, got[0])
+    no_dx, dwg, dwu = nm.glu_backward(pg, pu, X, pre, dH, act=act, need_dx=False)
+    assert no_dx is None and torch.equal(dwg, got[1]) and torch.equal(dwu, got[2])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_glu_backward_against_differences(act):
+    """<dX, v> and <dWg, V> against central differences of
+    L = sum dH act(G) U, G and U moving linearly from the kept products: the
+    difference quotient's own error is below 1e-7 relative at this step."""
+    T, R, K, dt = 40, 96, 136, "f16"
+    pg, wg, kg = weights(R, K, 2, 4, dt, "g")
+    pu, wu, ku = weights(R, K, 2, 4, dt, "u")
+    X = normal((T, K), 1.0, dt, "X")
+    dH = normal((T, R), 0.1, dt, "dH")
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    nm.glu(pg, pu, X, act=act, pre=pre)
+    g, u, dh = pre[0].double(), pre[1].double(), dH.double()
+    dx, dwg, dwu = nm.glu_backward(pg, pu, X, pre, dH, act=act)
+    _, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, act)
+    v = normal((T, K), 1.0, "f32", "v").double()
+    V = normal((R, K), 1.0, "f32", "V").double()
+
+    def loss(sg, su):
+        return float((dh * _ffn.act64(g + sg, act) * (u + su)).sum())
+
+    e = 1e-4
+    moves = [(v @ wg.double().t(), v @ wu.double().t(), dx, v, bound[0]),
+             (X.double() @ (V * kg).t(), 0.0, dwg, V * kg, bound[1]),
+             (0.0, X.double() @ (V * ku).t(), dwu, V * ku, bound[2])]
+    for mg, mu, grad, d, b in moves:
+        quot = (loss(e * mg, e * mu) - loss(-e * mg, -e * mu)) / (2 * e)
+        lim = (d.abs() * (b + _ffn.half_step(grad.dtype) * grad.double().abs() + _ffn.tiny(grad.dtype))).sum()
+        scale = (d * grad.double()).abs().sum()
+        assert abs(quot - float((grad.double() * d).sum())) <= float(lim) + 1e-6 * float(scale)
+
+
+def test_glu_large_tiles():
+    """Enough tiles for the largest tile shape, ragged on every side."""
+    T, R, K, dt = 1000, 6500, 136, "bf16"
+    pg, wg, kg = weights(R, K, 2, 4, dt, "g")
+    pu, wu, ku = weights(R, K, 2, 4, dt, "u")
+    X = normal((T, K), 1.0, dt, "X")
+    h, _, _, eh, _, _ = _ffn.glu64(X, wg, wu, "silu")
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    check(nm.glu(pg, pu, X, pre=pre), h, eh, "H")
+    dH = normal((T, R), 0.1, dt, "dH")
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, X, pre, dH), want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+def test_glu_backward_keeps_pruned_gradients_zero():
+    """An infinite activation and a NaN in dH reach kept weights' gradients
+    only; a kept weight of value zero gets its gradient."""
+    T, R, K = 70, 32, 64
+    W = normal((R, K), 0.05, "f16", "W")
+    W[3] = 0.0                                            # ties: positions 0 and 1 are kept
+    pg = pu = nm.pack(W, 2, 4)
+    k = _ffn.kept(W, 2, 4)
+    X = normal((T, K), 1.0, "f16", "X")
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    nm.glu(pg, pu, X, pre=pre)
+    dH = normal((T, R), 0.1, "f16", "dH")
+    pre[1, :, 3] = 1.0                                    # dG of row 3 is not zero
+    _, dwg, _ = nm.glu_backward(pg, pu, X, pre, dH)
+    assert bool((dwg[3][k[3]] != 0).all()) and bool((dwg[3][~k[3]] == 0).all())
+    X[5, :] = float("inf")
+    dH[7, 4] = float("nan")
+    _, dwg, dwu = nm.glu_backward(pg, pu, X, pre, dH)
+    for d in (dwg, dwu):
+        assert bool((d[~k] == 0).all()), "a pruned weight got a gradient"
+        assert bool(torch.isnan(d[4][k[4]]).all())
+
+
+# ---------------------------------------------------------------- microscaled 4-bit format
+def _check_mx(x):
+    m = nm.mx_quantize(x)
+    val, code, byte = _ffn.mx64(x.cpu())
+    codes, bytes_ = _ffn.mx_read(m)
+    K = x.shape[1]
+    nb = byte.shape[1]
+    assert torch.equal(bytes_[:, :nb], byte), "scales"
+    fin = (byte != 255).repeat_interleave(32, dim=1)[:, :K]
+    # a negative value that rounds to zero may carry either sign
+    same = (codes[:, :K] == code) | ((codes[:, :K] & 7 == 0) & (code & 7 == 0))
+    assert bool(same[fin].all()), f"codes differ at {(~same & fin).nonzero()[:4].tolist()}"
+    assert bool((codes[:, K:] == 0).all()), "codes past K"
+    for dt in (x.dtype, torch.float32):
+        y = nm.mx_dequantize(m, out_dtype=dt).double().cpu()
+        assert torch.equal(torch.isnan(y), torch.isnan(val))
+        assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(val)), dt
+    return m
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("top", [0.0, 1.0, 1.9921875, 6.5, 2.0 ** -20])
+def test_mx_quantize_every_16_bit_value(dt, top):
+    """Every finite 16-bit pattern, below a block's largest magnitude in the
+    first block of its row, among similar magnitudes in the second."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(TORCH[dt])
+    v = v[torch.isfinite(v)]
+    order = torch.argsort(v.abs().float())
+    v = v[order]
+    v = torch.cat((v, v[:-len(v) % 31])).view(-1, 31)
+    lead = torch.full((v.shape[0], 1), top, dtype=v.dtype)
+    x = torch.cat((lead, v), dim=1)
+    _check_mx(x.cuda())
+
+
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 31), (3, 32), (31, 33), (32, 255), (33, 256), (65, 257), (7, 770),
+                                    (200, 1000)])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_mx_quantize_shapes(rows, K, dt):
+    x = normal((rows, K), 1.0, dt, "x", rows, K)
+    _check_mx(x)
+    _, v = wide(x, 3, float("nan"))
+    _check_mx(v)
+
+
+def test_mx_quantize_float32_range():
+    """binary32 blocks at both ends of the scale's range, subnormals among
+    them, and values that round half way."""
+    x = torch.randn(64, 64, generator=_gen("r"))
+    e = torch.linspace(-149, 127, 64).round()
+    x = torch.ldexp(x, e[:, None].to(torch.int32)).clamp(-3e38, 3e38)
+    x[0] = 0.0
+    x[1, ::2] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0]).repeat(4)
+    x[1, 1::2] = -x[1, ::2]
+    _check_mx(x.cuda())
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_mx_quantize_non_finite_blocks(dt, bad):
+    x = normal((5, 100), 1.0, dt, "x")
+    x[2, 40] = bad
+    x[4, 99] = bad
+    m = _check_mx(x)
+    y = nm.mx_dequantize(m)
+    assert bool(torch.isnan(y[2, 32:64]).all()) and bool(torch.isnan(y[4, 96:]).all())
+    assert int(torch.isnan(y).sum()) == 32 + 4
+    # a block without a value taints every sum it enters, and no other
+    w = nm.mx_quantize(normal((48, 100), 1.0, dt, "w"))
+    for X in (x, m):
+        out = nm.mx_linear(w, X, out_dtype=torch.float32)
+        assert bool(torch.isnan(out[[2, 4]]).all()) and bool(torch.isfinite(out[[0, 1, 3]]).all())
+
+
+MX_SHAPES = [(1, 1, 1), (1, 17, 40), (2, 100, 256), (15, 16, 264), (16, 48, 1000), (17, 40, 33), (33, 65, 512),
+             (64, 33, 770), (65, 40, 32), (70, 129, 256), (129, 300, 520), (300, 257, 1288)]
+
+
+def _mx_w(R, K, dt, *key):
+    W = normal((R, K), 0.05, dt, "mw", R, K, *key)
+    return nm.mx_quantize(W), _ffn.mx64(W)[0]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T,R,K", MX_SHAPES)
+def test_mx_linear_shapes(T, R, K, dt):
+    w, W = _mx_w(R, K, dt)
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    X[:, :: 7] *= 10
+    x = _ffn.mx64(X)[0]
+    b = normal((R,), 1.0, "f32", "b", R)
+    y = x @ W.t()
+    e = _ffn.sum_err(K, x.abs() @ W.abs().t())
+    check(nm.mx_linear(w, X), y, e, "Y")
+    yb = y + b.double()
+    eb = e + 2.0 ** -23 * (yb.abs() + e)
+    check(nm.mx_linear(w, X, bias=b, out_dtype=torch.float32), yb, eb, "Y + b")
+    ya = _ffn.act64(yb, "gelu")
+    check(nm.mx_linear(w, X, bias=b, act="gelu"), ya, 1.13 * eb + _ffn.act_err(yb, "gelu") + 1e-6 * eb, "gelu")
+    # activations that come quantised: the same sums
+    q = nm.mx_quantize(X)
+    out = torch.empty(T, R, dtype=TORCH[dt], device="cuda")
+    assert torch.equal(nm.mx_linear(w, q, out=out), nm.mx_linear(w, X))
+    # a pitch that rules out wide accesses on both sides
+    _, xv = wide(X, 3, float("nan"))
+    ob, ov = wide(torch.zeros(T, R, dtype=TORCH[dt], device="cuda"), 3, 5.0)
+    nm.mx_linear(w, xv, out=ov)
+    check(ov, y, e, "strided")
+    assert bool((ob[:, R:] == 5.0).all())
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,R,K", MX_SHAPES + [(700, 4500, 300)])
+def test_mx_glu_shapes(T, R, K, dt):
+    wg, Wg = _mx_w(R, K, dt, "g")
+    wu, Wu = _mx_w(R, K, dt, "u")
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    x = _ffn.mx64(X)[0]
+    for act in ("silu", "gelu"):
+        h, _, _, eh, _, _ = _ffn.glu64(x, Wg, Wu, act)
+        check(nm.mx_glu(wg, wu, X, act=act), h, eh, act)
+    check(nm.mx_glu(wg, wu, nm.mx_quantize(X), act="gelu", out_dtype=torch.float32), h, eh, "quantised X")
+
+
+def test_mx_linear_large_tiles():
+    T, R, K = 1500, 9000, 300
+    w, W = _mx_w(R, K, "bf16")
+    X = normal((T, K), 1.0, "bf16", "X")
+    x = _ffn.mx64(X)[0]
+    check(nm.mx_linear(w, X), x @ W.t(), _ffn.sum_err(K, x.abs() @ W.abs().t()), "Y")
+
+
+# ---------------------------------------------------------------- in use
+def test_pruned_block_end_to_end():
+    """Gated block and down projection of a pruned model, forward and back
+    down to the weights, on a stream of its own."""
+    T, R, K, dt = 96, 256, 128, "bf16"
+    pg, wg, kg = weights(R, K, 2, 4, dt, "g")
+    pu, wu, ku = weights(R, K, 2, 4, dt, "u")
+    pd, wd, _ = weights(K, R, 2, 4, dt, "d")
+    X = normal((T, K), 1.0, dt, "X")
+    pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        H = nm.glu(pg, pu, X, pre=pre)
+        Y = nm.linear(pd, H)
+        dH = (Y.float() @ wd.float()).to(H.dtype)         # dL/dY = Y
+        grads = nm.glu_backward(pg, pu, X, pre, dH)
+    s.synchronize()
+    h, _, _, eh, _, _ = _ffn.glu64(X, wg, wu, "silu")
+    check(H, h, eh, "H")
+    check(Y, H.double() @ wd.double().t(), _ffn.sum_err(R, H.double().abs() @ wd.double().abs().t()), "Y")
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(grads, want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+@pytest.mark.parametrize("T", [1, 20, 100])
+def test_four_bit_block_in_a_graph(T):
+    """Gated block and down projection at 4 bits, and the pruned block with
+    its gradients, captured into one graph and replayed on new inputs with
+    eager work in between: every replay gives the eager call's bits."""
+    R, K, dt = 320, 264, "bf16"
+    g4, u4 = _mx_w(R, K, dt, "g")[0], _mx_w(R, K, dt, "u")[0]
+    d4 = _mx_w(K, R, dt, "d")[0]
+    pg, pu = weights(R, K, 2, 4, dt, "g")[0], weights(R, K, 2, 4, dt, "u")[0]
+    X = normal((T, K), 1.0, dt, "X")
+    dH = normal((T, R), 0.1, dt, "dH")
+    pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+
+    def step():
+        y4 = nm.mx_linear(d4, nm.mx_glu(g4, u4, X))
+        h = nm.glu(pg, pu, X, pre=pre)
+        return (y4, h, *nm.glu_backward(pg, pu, X, pre, dH))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in range(4):
+        X.copy_(normal((T, K), 1.0, dt, "X", i))
+        dH.copy_(normal((T, R), 0.1, dt, "dH", i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), f"replay {i}"
+
+
+def test_results_do_not_vary():
+    """No result depends on the order in which workgroups finish."""
+    T, R, K = 130, 600, 520
+    pg, pu = weights(R, K, 4, 8, "f16", "g")[0], weights(R, K, 4, 8, "f16", "u")[0]
+    X, dH = normal((T, K), 1.0, "f16", "X"), normal((T, R), 0.1, "f16", "dH")
+    pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+    w = _mx_w(R, K, "f16")[0]
+    first = None
+    for _ in range(3):
+        out = (nm.glu(pg, pu, X, pre=pre), *nm.glu_backward(pg, pu, X, pre, dH), nm.mx_linear(w, X))
+        if first is None:
+            first = out
+        for a, b in zip(first, out):
+            assert torch.equal(a, b)
