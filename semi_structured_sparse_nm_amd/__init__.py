@@ -731,7 +731,7 @@ def _mx_operands(w: Mx, X, out_dtype, out, workspace, others, glu: bool):
     _check_float("out", out.dtype)
     ldy = _row_pitch("out", out, T, w.rows)
     dev = _device_of(xs + [("weight codes", w.codes), ("weight scales", w.scales), ("out", out)] + others)
-    need = 0 if xq is not None else mx_workspace_size(w, T, glu)
+    need = mx_workspace_size(w, T, glu)
     return dev, T, xq, xp, ldx, xdt, out, ldy, _workspace(workspace, need, dev)
 
 

@@ -47,7 +47,7 @@ struct TileArgs {
   int64_t ldm;               // bytes
   int act;                   // NM_ACT_NONE / NM_ACT_GELU / NM_ACT_SILU
   int batch;                 // 1, or 2 products over A[b], B[b] -> C[b]
-  int mt, nt;                // tiles of one product, filled by the launcher
+  int shape;                 // tile shape, from plan_tile
   // split of the reduction (TILE_LINEAR): slice s covers slabs s * sps ..,
   // raw sums to C + s * cs elements of binary32
   int split, sps;
@@ -56,6 +56,17 @@ struct TileArgs {
 
 // Element types of the tile kernel's operands.
 enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2 };
+
+// Tile shape (0: 256 x 256, 1: 128 x 256, 2: 128 x 128) and slices of the
+// reduction for one product, by a model of its time.
+struct TilePlan {
+  int shape, split, sps;
+};
+TilePlan plan_tile(TileOp op, int64_t Mr, int64_t Nr, int nslab, int batch, int ebytes_out, int cus);
+int device_cu_count();
+// C[t][r] = act(sum over the slices + bias[r]), part [split][T][R] binary32
+hipError_t launch_tile_reduce(const float* part, int split, int64_t T, int64_t R, const float* bias, int act, void* C,
+                              int64_t ldc, int ydt, hipStream_t s);
 
 hipError_t launch_tile_f16(TileOp op, int ydt, const TileArgs& a, hipStream_t s);
 hipError_t launch_tile_bf16(TileOp op, int ydt, const TileArgs& a, hipStream_t s);

@@ -21,6 +21,32 @@ constexpr int64_t kFewTokens = 64;
 // Longest dimension taken: products of two of them stay within 63 bits.
 constexpr int64_t kMaxLen = 1ll << 30;
 
+// One tile product of elements `et` (TILE_*), with its plan; a split's slices
+// go to `part` (plan.split * Mr * Nr binary32) and are added afterwards.
+hipError_t run_tile(int et, nm::TileOp op, int ydt, nm::TileArgs a, const nm::TilePlan& plan, float* part,
+                    hipStream_t s) {
+  auto launch = et == nm::TILE_F16 ? nm::launch_tile_f16 : et == nm::TILE_BF16 ? nm::launch_tile_bf16 : nm::launch_tile_mx;
+  a.shape = plan.shape;
+  a.split = plan.split;
+  a.sps = plan.sps;
+  if (plan.split == 1) return launch(op, ydt, a, s);
+  nm::TileArgs p = a;
+  p.C[0] = p.C[1] = part;
+  p.ldc = a.Nr;
+  p.cs = a.Mr * a.Nr;
+  p.bias = nullptr;
+  p.act = NM_ACT_NONE;
+  const hipError_t e = launch(op, NM_F32, p, s);
+  if (e != hipSuccess) return e;
+  return nm::launch_tile_reduce(part, plan.split, a.Mr, a.Nr, a.bias, a.act, a.C[0], a.ldc, ydt, s);
+}
+
+size_t part_bytes(const nm::TilePlan& p, int64_t Mr, int64_t Nr) {
+  return p.split > 1 ? up256((size_t)(p.split * Mr * Nr * 4)) : 0;
+}
+
+int tile_type(int wdt) { return wdt == NM_F16 ? nm::TILE_F16 : nm::TILE_BF16; }
+
 // ---------------------------------------------------------------- gated block, N:M weights
 nm_status check_pair(const nm_packed* gate, const nm_packed* up, Geometry* g) {
   Geometry gu;
@@ -49,7 +75,8 @@ size_t dense_bytes(const Geometry& g) { return up256((size_t)(g.R * up64(g.K) * 
 
 struct BackwardPlan {
   int64_t Rp, Tp, Kp;
-  size_t d, dt, xt, wt, mask, total;   // bytes of each part (mask: of one weight)
+  size_t d, dt, xt, wt, mask, part, total;   // bytes of each part (mask: of one weight)
+  nm::TilePlan dx, dw;
   BackwardPlan(const Geometry& g, int64_t T) {
     Rp = up64(g.R);
     Tp = up64(T);
@@ -59,7 +86,11 @@ struct BackwardPlan {
     xt = up256((size_t)(g.K * Tp * 2));
     wt = up256((size_t)(g.K * 2 * Rp * 2));
     mask = up256((size_t)(g.R * Kp / 8));
-    total = d + dt + xt + wt + 2 * mask;
+    const int cus = nm::device_cu_count();
+    dx = nm::plan_tile(nm::TILE_LINEAR, T, g.K, (int)(2 * Rp / 64), 1, 2, cus);
+    dw = nm::plan_tile(nm::TILE_MASKED, g.R, g.K, (int)(Tp / 64), 2, 2, cus);
+    part = part_bytes(dx, T, g.K);
+    total = d + dt + xt + wt + 2 * mask + part;
   }
 };
 
@@ -78,6 +109,10 @@ bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_
 
 size_t mx_ws_codes(int64_t T, int64_t K) { return up256((size_t)nm::mx_codes_bytes(T, K)); }
 size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm::mx_scales_bytes(T, K)); }
+nm::TilePlan mx_plan(bool glu, int64_t T, int64_t R, int64_t K) {
+  return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), 1, 2,
+                       nm::device_cu_count());
+}
 
 nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const void* X, int64_t ldx, int32_t xdt,
                      int64_t T, void* Y, int64_t ldy, int32_t ydt, const float* bias, int32_t act, void* ws,
@@ -109,14 +144,17 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
   const int xeb = xq ? 2 : nm::dtype_bytes(xdt);
   // up to 16 tokens in whole 16-byte pieces are quantised inside the product
   const bool in_registers = !xq && T <= 16 && aligned(X, 16) && ldx * xeb % 16 == 0 && K * xeb % 16 == 0;
-  const size_t need = xq || in_registers ? 0 : mx_ws(T, K);
+  const bool few = T <= kFewTokens;
+  const nm::TilePlan plan = few ? nm::TilePlan{} : mx_plan(glu, T, R, K);
+  const size_t quant = xq || in_registers ? 0 : mx_ws(T, K);
+  const size_t need = quant + (few ? 0 : part_bytes(plan, T, R));
   if (need && (!ws || ws_bytes < need)) return NM_EINVAL;
   if (need && !aligned(ws, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
 
   const uint8_t* xcodes = xq ? static_cast<const uint8_t*>(xq->codes) : nullptr;
   const uint8_t* xscales = xq ? static_cast<const uint8_t*>(xq->scales) : nullptr;
-  if (need) {
+  if (quant) {
     uint8_t* c = static_cast<uint8_t*>(ws);
     uint8_t* sc = c + mx_ws_codes(T, K);
     if (nm::launch_mx_quantize(X, ldx, xdt, T, K, c, sc, s) != hipSuccess) return NM_EHIP;
@@ -124,7 +162,7 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     xscales = sc;
   }
   const nm_mx* ws2[2] = {w0, glu ? w1 : w0};
-  if (T <= kFewTokens) {
+  if (few) {
     nm::MxDecodeArgs a{};
     for (int i = 0; i < 2; ++i) {
       a.codes[i] = static_cast<const uint8_t*>(ws2[i]->codes);
@@ -163,13 +201,9 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
   a.bias = bias;
   a.act = act;
   a.batch = 1;
-  a.split = 1;
-  a.sps = a.nslab;
-  return nm::launch_tile_mx(glu ? nm::TILE_GLU : nm::TILE_LINEAR, ydt, a, s) == hipSuccess ? NM_OK : NM_EHIP;
-}
-
-hipError_t launch_tile16(int wdt, nm::TileOp op, const nm::TileArgs& a, hipStream_t s) {
-  return wdt == NM_F16 ? nm::launch_tile_f16(op, wdt, a, s) : nm::launch_tile_bf16(op, wdt, a, s);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + quant);
+  return run_tile(nm::TILE_MX, glu ? nm::TILE_GLU : nm::TILE_LINEAR, ydt, a, plan, part, s) == hipSuccess ? NM_OK
+                                                                                                         : NM_EHIP;
 }
 
 }  // namespace
@@ -260,9 +294,9 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   a.ldp = ldp;
   a.act = act;
   a.batch = 1;
-  a.split = 1;
-  a.sps = a.nslab;
-  return launch_tile16(gate->dtype, nm::TILE_GLU, a, s) == hipSuccess ? NM_OK : NM_EHIP;
+  const nm::TilePlan plan = nm::plan_tile(nm::TILE_GLU, T, g.R, a.nslab, 1, 2, nm::device_cu_count());
+  return run_tile(tile_type(gate->dtype), nm::TILE_GLU, gate->dtype, a, plan, nullptr, s) == hipSuccess ? NM_OK
+                                                                                                       : NM_EHIP;
 }
 
 nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes) {
@@ -303,6 +337,7 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   uint8_t* xt = dt + p.dt;
   uint8_t* wt = xt + p.xt;
   uint8_t* mask = wt + p.wt;
+  float* part = reinterpret_cast<float*>(mask + 2 * p.mask);
   const nm_packed* w[2] = {gate, up};
 
   if (nm::launch_glu_dact(dH, lddh, G, U, ldp, T, g.R, p.Rp, dX ? d : nullptr, 2 * p.Rp, dWg ? dt : nullptr, p.Tp, act,
@@ -327,9 +362,7 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
     a.C[0] = dX;
     a.ldc = lddx;
     a.batch = 1;
-    a.split = 1;
-    a.sps = a.nslab;
-    if (launch_tile16(gate->dtype, nm::TILE_LINEAR, a, s) != hipSuccess) return NM_EHIP;
+    if (run_tile(tile_type(gate->dtype), nm::TILE_LINEAR, gate->dtype, a, p.dx, part, s) != hipSuccess) return NM_EHIP;
   }
   if (dWg) {
     // dW[r][k] = sum over t of d[t][r] X[t][k], both transposed
@@ -350,9 +383,8 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
     a.ldc = lddw;
     a.ldm = p.Kp / 8;
     a.batch = 2;
-    a.split = 1;
-    a.sps = a.nslab;
-    if (launch_tile16(gate->dtype, nm::TILE_MASKED, a, s) != hipSuccess) return NM_EHIP;
+    if (run_tile(tile_type(gate->dtype), nm::TILE_MASKED, gate->dtype, a, p.dw, nullptr, s) != hipSuccess)
+      return NM_EHIP;
   }
   return NM_OK;
 }
@@ -391,12 +423,11 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
 }
 
 nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* bytes) {
-  (void)glu;
   if (!bytes || T < 1) return NM_EINVAL;
   const nm_status st = check_mx(w);
   if (st != NM_OK) return st;
   if (!row_ok(nm::mx_kp(w->K) / 2) || T > kMaxLen) return NM_EUNSUPPORTED;
-  *bytes = mx_ws(T, w->K);
+  *bytes = mx_ws(T, w->K) + (T > kFewTokens ? part_bytes(mx_plan(glu != 0, T, w->rows, w->K), T, w->rows) : 0);
   return NM_OK;
 }
 

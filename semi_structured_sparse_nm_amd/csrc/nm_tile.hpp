@@ -8,23 +8,26 @@
 // operand and the same cycles, so one kernel serves them: a slab is 128
 // bytes of the reduction (64 halves or 256 4-bit values), two instructions.
 //
-// A workgroup computes a BM x BN tile; its waves form a WM x WN grid.  Slab s
-// of both operands sits in one of two LDS stages, filled by direct-to-LDS
-// loads while the slab before is multiplied; one wait and one barrier per
-// slab.  A stage row is 128 bytes, its 16-byte piece c at position
-// c ^ (row % 8), so that the 16 rows x 4 pieces a fragment read touches fall
-// on different banks.  B rows are the instruction's first operand (D rows),
-// so a lane ends up with four consecutive n of one m: outputs and the kept
-// bits of a group of four are consecutive in memory.
+// Persistent workgroups walk a list of BM x BN tiles as one stream of slabs:
+// slab s of both operands sits in one of NS LDS stages, filled by
+// direct-to-LDS loads issued NS - 1 slabs ahead, across tile borders too, so
+// a tile's first slabs arrive while the tile before is finished and its
+// outputs leave.  A stage row is 128 bytes, its 16-byte piece c at position
+// c ^ (row % 8) (no bank conflicts, by counter).  B rows are the
+// instruction's first operand (D rows), so a lane ends up with four
+// consecutive n of one m: outputs and the kept bits of a group of four are
+// consecutive in memory.
 //
-// Rows past Mr / Nr re-read the last row (their results are not stored);
-// 16-byte pieces past ka / kb read zeros, so the reduction's tail adds
-// nothing.  TILE_GLU: half of a wave's B rows are gate rows, the other half
-// the up rows of the same outputs, so g and u of one output meet in one
-// lane and the activation and product need no exchange.
+// Rows past Mr / Nr repeat the last row (their results are not stored);
+// 16-byte pieces past ka / kb read as zeros, so the reduction's tail adds
+// nothing.  Every slab has a piece inside ka and one inside kb, so no load has
+// all its lanes outside its operand: such a load would return ahead of older
+// ones, and a count of outstanding loads could pass too early.  TILE_GLU: half of a wave's B rows are gate
+// rows, the other half the up rows of the same outputs, so g and u of one
+// output meet in one lane and the activation and product need no exchange.
 #pragma once
 
-#include "nm_ffn.hpp"
+#include "nm_tile_common.hpp"
 
 namespace nm {
 
@@ -33,9 +36,10 @@ namespace {
 #if defined(__HIP_DEVICE_COMPILE__)
 template <int OA, int OB>
 __device__ __forceinline__ v4f mfma_mx_op(v4i a, v4i b, v4f c, int sa, int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8i{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
-                                                          v8i{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, c, 4, 4, OA, sa,
-                                                          OB, sb);
+  // 4-bit operands take the first four registers; the rest stays undefined
+  const v8i a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const v8i b8 = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, OA, sa, OB, sb);
 }
 // scale byte oa of sa, ob of sb; oa and ob share the step (bit 0) and fold to
 // constants in the unrolled loops
@@ -61,268 +65,255 @@ __device__ __forceinline__ v4f mfma_16(v4i a, v4i b, v4f c) {
 }
 #endif
 
-template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(WM * WN * 64) tile_kernel(TileArgs a, int gm) {
+template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
+__global__ void __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+tile_kernel(TileArgs a, TileList list) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles of a wave
   constexpr bool MX = ET == TILE_MX;
+  constexpr bool GLU = OP == TILE_GLU;
   constexpr int ROWS = BM + BN;
   constexpr int DATA = ROWS * 128;
   constexpr int STAGE = DATA + (MX ? ROWS * 8 : 0);
   constexpr int NL = ROWS / 8 / NW;                     // 1 KB loads of a wave per slab
-  constexpr int NU = ROWS / 32;                         // scale units per slab
-  static_assert(ROWS / 8 % NW == 0 && BM / 8 % NW == 0, "whole loads per wave, each of one operand");
-  static_assert(2 * STAGE <= 160 * 1024, "LDS");
-  static_assert(OP != TILE_GLU || (BN / WN / 2) % 32 == 0, "whole scale units per half");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  constexpr int NLA = BM / 8 / NW;                      // of them A rows
+  constexpr int NU = MX ? ROWS / 32 : 0;                // scale units per slab
+  constexpr int NLT = NL + (NU + NW - 1) / NW;          // loads of a wave per slab
+  constexpr int BNO = GLU ? BN / 2 : BN;                // outputs per tile
+  constexpr int HB = BN / WN / 2;                       // TILE_GLU: rows per half
+  constexpr int RJ = 8 * NW;                            // rows one load of every wave covers
+  static_assert(BM % RJ == 0 && BN % RJ == 0, "every load of one operand");
+  static_assert(!GLU || HB % RJ == 0 || RJ % (2 * HB) == 0, "a wave's load has rows of one weight");
+  static_assert(NS * STAGE <= 160 * 1024, "LDS");
+  static_assert(!MX || !GLU || HB % 32 == 0, "whole scale units per half");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
 
-  // work item: XCD x (blockIdx % 8) takes a contiguous run of the list, in
-  // groups of gm row tiles, row tile fastest inside a group: the workgroups
-  // of an XCD that run together share both operands' slabs through its L2
-  const int ntile = a.mt * a.nt;
-  const int total = ntile * a.split * a.batch;
-  const int per = (total + 7) / 8;
-  int L = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (L >= min(((int)(blockIdx.x & 7) + 1) * per, total)) return;
-  const int z = L / ntile;
-  L -= z * ntile;
-  const int bat = z / a.split, ks = z - bat * a.split;
-  const int grp = L / (gm * a.nt);
-  const int in = L - grp * gm * a.nt;
-  const int rows_g = min(gm, a.mt - grp * gm);
-  const int tn_i = in / rows_g;
-  const int tm_i = grp * gm + in - tn_i * rows_g;
-  constexpr int BNO = OP == TILE_GLU ? BN / 2 : BN;     // outputs per tile
-  const int64_t m0 = (int64_t)tm_i * BM;
-  const int64_t n0 = (int64_t)tn_i * BNO;
-
-  const int s0 = ks * a.sps;
-  const int s1 = min(s0 + a.sps, a.nslab);
+  TileWalk walk(list);
+  if (walk.count <= 0) return;
 
   // ---- operand loads: load d fills LDS rows 8 d .. 8 d + 7, lane l row
-  // 8 d + l / 8, position l % 8 = piece (l % 8) ^ (l / 8)
+  // 8 d + l / 8, position l % 8 = piece (l % 8) ^ (l / 8); wave w issues
+  // d = w + NW j
   const int piece = (lane & 7) ^ (lane >> 3);
-  constexpr int HB = BN / WN / 2;                       // TILE_GLU: rows per half
-  const uint8_t* Ab = (bat ? a.A[1] : a.A[0]) + m0 * a.lda;
-  const v4i ra = make_rsrc(Ab, 0x7fffffff);
-  const v4i rb0 = make_rsrc((OP != TILE_GLU && bat ? a.B[1] : a.B[0]) + n0 * a.ldb, 0x7fffffff);
-  const v4i rb1 = make_rsrc(a.B[1] + (OP == TILE_GLU ? n0 * a.ldb : 0), 0x7fffffff);
-  const int mlast = (int)min(a.Mr - m0, (int64_t)BM) - 1;
-  const int nlast = (int)min(a.Nr - n0, (int64_t)BNO) - 1;
-  int voff[NL];
-#pragma unroll
-  for (int j = 0; j < NL; ++j) {
-    const int d = wave + NW * j;                        // j < BM / 8 / NW: A rows
-    int row = 8 * d + (lane >> 3);
-    if (j < BM / 8 / NW) {
-      row = min(row, mlast);
-      voff[j] = row * (int)a.lda + 16 * piece;
-    } else {
+  // TILE_GLU with the RJ rows of a load spanning both halves: a wave's rows are all gate or all up rows
+  constexpr bool SPAN = GLU && HB % RJ != 0;
+  const bool wave_up = SPAN && (8 * wave / HB & 1);
+  // row of the tile (A: of BM, B: of BNO outputs) that load j brings this lane
+  auto load_row = [&](auto jc) {
+    constexpr int j = decltype(jc)::value;
+    int row = 8 * wave + (lane >> 3) + RJ * j;
+    if constexpr (j >= NLA) {
       row -= BM;
-      if constexpr (OP == TILE_GLU) row = row / (2 * HB) * HB + row % HB;
-      row = min(row, nlast);
-      voff[j] = row * (int)a.ldb + 16 * piece;
+      if constexpr (GLU) row = row / (2 * HB) * HB + row % HB;
     }
-  }
+    return row;
+  };
   // pieces past the end of a row, in the last slab: an offset no resource holds
-  const int nfull_a = a.ka >> 3, nfull_b = a.kb >> 3;
-  const int cut_a = piece >= (a.ka & 7) ? (int)0x80000000 : 0;
-  const int cut_b = piece >= (a.kb & 7) ? (int)0x80000000 : 0;
-  auto issue = [&](int s, int st) {
-    uint8_t* sp = lds + st * STAGE;
-    const int so = __builtin_amdgcn_readfirstlane(s * 128);
-    const int ca = s < nfull_a ? 0 : (s > nfull_a ? (int)0x80000000 : cut_a);
-    const int cb = s < nfull_b ? 0 : (s > nfull_b ? (int)0x80000000 : cut_b);
-#pragma unroll
-    for (int j = 0; j < NL; ++j) {
-      const int d = wave + NW * j;
-      if (j < BM / 8 / NW) {
-        lds_dma16(ra, lds_addr(sp + 1024 * d), voff[j] | ca, so);
-      } else if constexpr (OP == TILE_GLU) {
-        const int half = (8 * d - BM) / HB & 1;
-        if (half)
-          lds_dma16(rb1, lds_addr(sp + 1024 * d), voff[j] | cb, so);
-        else
-          lds_dma16(rb0, lds_addr(sp + 1024 * d), voff[j] | cb, so);
-      } else {
-        lds_dma16(rb0, lds_addr(sp + 1024 * d), voff[j] | cb, so);
-      }
-    }
+  const int cut_a = (a.ka & 7) && piece >= (a.ka & 7) ? (int)0x80000000 : 0;
+  const int cut_b = (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
+
+  // the load cursor: work item, its resources, next slab
+  int ck = 0, cs, ce, voff[NL];
+  v4i ra, rb0, rb1, rsc[MX ? (NU + NW - 1) / NW : 1];
+  // (always inlined: a call would keep the cursor, and what it refers to, in memory)
+  auto cursor_item = [&](int k) __attribute__((always_inline)) {
+    const TileItem it = walk.item(k);
+    const int64_t m0 = (int64_t)it.m * BM, n0 = (int64_t)it.n * BNO;
+    auto tile_rsrc = [&](const uint8_t* p, int64_t row0, int64_t ld) {
+      const v4i r = make_rsrc(p + row0 * ld, 0x7fffffff);
+      return v4i{scalar(r[0]), scalar(r[1]), r[2], r[3]};
+    };
+    const int mlast = (int)min(a.Mr - m0, (int64_t)BM) - 1, nlast = (int)min(a.Nr - n0, (int64_t)BNO) - 1;
+    static_for<0, NL>([&](auto jc) {
+      constexpr int j = decltype(jc)::value;
+      voff[j] = j < NLA ? min(load_row(jc), mlast) * (int)a.lda + 16 * piece
+                        : min(load_row(jc), nlast) * (int)a.ldb + 16 * piece;
+    });
+    ra = tile_rsrc(it.batch ? a.A[1] : a.A[0], m0, a.lda);
+    rb0 = tile_rsrc(!GLU && it.batch ? a.B[1] : (wave_up ? a.B[1] : a.B[0]), n0, a.ldb);
+    if constexpr (GLU && !SPAN) rb1 = tile_rsrc(a.B[1], n0, a.ldb);
     if constexpr (MX) {
-      // unit u of the stage: LDS rows 32 u ..; row groups past the end repeat
-      // the last one
-#pragma unroll
-      for (int j = 0; j < (NU + NW - 1) / NW; ++j) {
-        const int u = wave + NW * j;
-        if (NU % NW == 0 || u < NU) {
-          const uint8_t* base;
-          int64_t grp32;
-          if (u < BM / 32) {
-            base = a.As;
-            grp32 = min(m0 / 32 + u, (a.Mr - 1) / 32);
-          } else {
-            int row = 32 * u - BM;
-            base = a.Bs[0];
-            if constexpr (OP == TILE_GLU) {
-              if (row / HB & 1) base = a.Bs[1];
-              row = row / (2 * HB) * HB + row % HB;
-            }
-            grp32 = min((n0 + row) / 32, (a.Nr - 1) / 32);
+      // unit u of a stage: LDS rows 32 u ..; row groups past the end repeat the last one
+      static_for<0, (NU + NW - 1) / NW>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+        const int u = min(wave + NW * j, NU - 1);
+        const uint8_t* base = a.As;
+        int64_t g32 = min(m0 / 32 + u, (a.Mr - 1) / 32);
+        if (u >= BM / 32) {
+          int row = 32 * u - BM;
+          base = a.Bs[0];
+          if constexpr (GLU) {
+            if (row / HB & 1) base = a.Bs[1];
+            row = row / (2 * HB) * HB + row % HB;
           }
-          const v4i rs = make_rsrc(base + (grp32 * a.nslab + s) * 256, 256);
-          const v4i rsu = v4i{__builtin_amdgcn_readfirstlane(rs[0]), __builtin_amdgcn_readfirstlane(rs[1]), rs[2],
-                              rs[3]};
-          lds_dma4(rsu, lds_addr(sp + DATA + 256 * u), 4 * lane, 0);
+          g32 = min((n0 + row) / 32, (a.Nr - 1) / 32);
         }
-      }
+        const v4i r = make_rsrc(base + g32 * a.nslab * 256, 0);
+        rsc[j] = v4i{scalar(r[0]), scalar(r[1]), scalar(a.nslab * 256), r[3]};
+      });
+    }
+    cs = it.s0;
+    ce = it.s1;
+  };
+  auto issue_one = [&](auto jc, int st, int ca, int cb) {
+    constexpr int j = decltype(jc)::value;
+    uint8_t* sp = lds + st * STAGE;
+    if constexpr (j < NL) {
+      const int so = scalar(cs * 128);
+      const uint32_t dst = lds_addr(sp + 1024 * (wave + NW * j));
+      constexpr bool UP = GLU && !SPAN && ((RJ * j - BM) / HB & 1);
+      lds_dma16(j < NLA ? ra : (UP ? rb1 : rb0), dst, voff[j] | (j < NLA ? ca : cb), so);
+    } else {
+      // (a wave without a unit of its own repeats the last one: no branch among the products)
+      const int u = min(wave + NW * (j - NL), NU - 1);
+      lds_dma4(rsc[j - NL], lds_addr(sp + DATA + 256 * u), 4 * lane, cs * 256);
+    }
+  };
+  // part p of NP of the cursor slab's loads into stage st
+  auto issue_part = [&](auto pc, auto npc, int st) {
+    constexpr int P = decltype(pc)::value, NP = decltype(npc)::value;
+    const int ca = cs + 1 < a.nslab ? 0 : cut_a, cb = cs + 1 < a.nslab ? 0 : cut_b;
+    static_for<NLT * P / NP, NLT * (P + 1) / NP>([&](auto jc) { issue_one(jc, st, ca, cb); });
+  };
+  // past the last work item the cursor stays on its last slab: the loads fill
+  // a stage nobody reads
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (__builtin_expect(cs + 1 < ce, 1)) {
+      ++cs;
+    } else if (ck + 1 < walk.count) {
+      asm volatile("" ::: "memory");                    // a branch, not selects around it
+      cursor_item(++ck);
     }
   };
 
   v4f acc[TN][TM];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < TN; ++i)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
 
   // fragment addresses: row li of a 16-row tile, piece 4 kk + lq
   const int arow = (wm * TM * 16 + li) * 128;
   const int brow = (BM + wn * TN * 16 + li) * 128;
-  const int pos[2] = {16 * (lq ^ (li & 7)), 16 * ((4 + lq) ^ (li & 7))};
-
-  issue(s0, 0);
-  __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
-  barrier_nofence();
-  for (int s = s0; s < s1; ++s) {
-    const int st = (s - s0) & 1;
-    if (s + 1 < s1) issue(s + 1, st ^ 1);
-    const uint8_t* sp = lds + st * STAGE;
-    int sa[MX ? TM / 2 : 1], sb[MX ? TN / 2 : 1];
+  const int pos0 = 16 * (lq ^ (li & 7)), pos1 = 16 * ((4 + lq) ^ (li & 7));
+  struct Frag {
+    v4i a[TM], b[TN];
+  };
+  constexpr int NF = TM + TN;
+  auto read_one = [&](Frag& f, auto xc, int st, int pos) {
+    constexpr int X = decltype(xc)::value;
+    const uint8_t* sp = lds + st * STAGE + pos;
+    if constexpr (X < TM)
+      f.a[X] = *reinterpret_cast<const v4i*>(sp + arow + X * 2048);
+    else
+      f.b[X - TM] = *reinterpret_cast<const v4i*>(sp + brow + (X - TM) * 2048);
+  };
+  struct Scales {
+    int a[MX ? TM / 2 : 1], b[MX ? TN / 2 : 1];
+  };
+  auto read_scales = [&](Scales& f, int st) {
     if constexpr (MX) {
+      const uint8_t* sp = lds + st * STAGE + DATA + 4 * lane;
 #pragma unroll
-      for (int j = 0; j < TM / 2; ++j)
-        sa[j] = *reinterpret_cast<const int*>(sp + DATA + (wm * TM / 2 + j) * 256 + 4 * lane);
+      for (int j = 0; j < TM / 2; ++j) f.a[j] = *reinterpret_cast<const int*>(sp + (wm * TM / 2 + j) * 256);
 #pragma unroll
-      for (int i = 0; i < TN / 2; ++i)
-        sb[i] = *reinterpret_cast<const int*>(sp + DATA + (BM / 32 + wn * TN / 2 + i) * 256 + 4 * lane);
+      for (int i = 0; i < TN / 2; ++i) f.b[i] = *reinterpret_cast<const int*>(sp + (BM / 32 + wn * TN / 2 + i) * 256);
     }
+  };
+  auto mul_row = [&](auto ic_, auto kc, const Frag& f, const Scales& c) {
+    constexpr int i = decltype(ic_)::value, kk = decltype(kc)::value;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      v4i fb[TN], fa[TM];
-#pragma unroll
-      for (int j = 0; j < TM; ++j) fa[j] = *reinterpret_cast<const v4i*>(sp + arow + j * 2048 + pos[kk]);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) fb[i] = *reinterpret_cast<const v4i*>(sp + brow + i * 2048 + pos[kk]);
+    for (int j = 0; j < TM; ++j) {
+      if constexpr (MX)
+        acc[i][j] = mfma_mx(f.b[i], f.a[j], acc[i][j], c.b[i / 2], 2 * (i & 1) + kk, c.a[j / 2], 2 * (j & 1) + kk);
+      else
+        acc[i][j] = mfma_16<ET>(f.b[i], f.a[j], acc[i][j]);
+    }
+  };
+
+  // Slab s: its second half's fragments are read between the products of the
+  // first half; then, with slab s + 1 landed and every wave done reading slab
+  // s, the first fragments of slab s + 1 are read and the loads of slab
+  // s + NS go out into s's stage between the products of the second half.
+  cursor_item(0);
+  static_for<0, NS - 1>([&](auto k) {
+    issue_part(ic<0>(), ic<1>(), decltype(k)::value);
+    advance();
+  });
+  constexpr int AHEAD = NLT * (NS - 2);                 // loads that may be outstanding once the next slab is in
+  static_assert(AHEAD < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt(waitcnt(AHEAD, 15));
+  barrier_nofence();
+  issue_part(ic<0>(), ic<1>(), NS - 1);
+  advance();
+  Frag f0, f1;
+  Scales c0, c1;
+  static_for<0, NF>([&](auto x) { read_one(f0, x, 0, pos0); });
+  read_scales(c0, 0);
+  int st = 0;
+  for (int k = 0; k < walk.count; ++k) {
+    const TileItem it = walk.item(k);
+    for (int s = it.s0; s < it.s1; ++s) {
+      static_for<0, TN>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        static_for<NF * I / TN, NF * (I + 1) / TN>([&](auto x) { read_one(f1, x, st, pos1); });
+        __builtin_amdgcn_sched_barrier(0);
+        mul_row(i, ic<0>(), f0, c0);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      __builtin_amdgcn_s_waitcnt(waitcnt(AHEAD, 0));
+      barrier_nofence();
+      const int nx = st + 1 == NS ? 0 : st + 1;
+      read_scales(c1, nx);
+      static_for<0, TN>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        static_for<NF * I / TN, NF * (I + 1) / TN>([&](auto x) { read_one(f0, x, nx, pos0); });
+        issue_part(i, ic<TN>(), st);
+        __builtin_amdgcn_sched_barrier(0);
+        mul_row(i, ic<1>(), f1, c0);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      // the products stay above the cursor's branch (sunk below it they would
+      // keep every fragment of the slab alive)
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          if constexpr (MX)
-            acc[i][j] = mfma_mx(fb[i], fa[j], acc[i][j], sb[i / 2], 2 * (i & 1) + kk, sa[j / 2], 2 * (j & 1) + kk);
-          else
-            acc[i][j] = mfma_16<ET>(fb[i], fa[j], acc[i][j]);
-        }
+        for (int j = 0; j < TM; ++j) asm volatile("" : "+v"(acc[i][j]));
+      advance();
+      c0 = c1;
+      st = nx;
     }
-    // the next slab has landed, and every wave is done with this one
-    __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
-    barrier_nofence();
+    tile_epilogue<OP, OUT, TM, TN>(a, it, (int64_t)it.m * BM + wm * TM * 16, (int64_t)it.n * BNO + wn * (BNO / WN), acc);
+    clear();
   }
-
-  // ---- epilogue: lane (li, lq) holds n = .. + 16 i + 4 lq + v of row m = .. + 16 j + li
-  const int64_t mrow = m0 + wm * TM * 16 + li;
-  if constexpr (OP == TILE_GLU) {
-    constexpr int H = TN / 2;
-    const int64_t ncol = n0 + wn * H * 16 + 4 * lq;
-    const bool vec = (a.ldc % 4 == 0) && ((uintptr_t)a.C[0] % 8 == 0);
-    const bool vecp = a.P[0] && (a.ldp % 4 == 0) && ((uintptr_t)a.P[0] % 8 == 0) && ((uintptr_t)a.P[1] % 8 == 0);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int64_t m = mrow + 16 * j;
-      if (m >= a.Mr) continue;
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const int64_t n = ncol + 16 * i;
-        const int left = (int)min(a.Nr - n, (int64_t)4);
-        if (left <= 0) continue;
-        float g[4], u[4], h[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          g[v] = acc[i][j][v];
-          u[v] = acc[i + H][j][v];
-          h[v] = glu_act(a.act, g[v]) * u[v];
-        }
-        store4<OUT>(a.C[0], m * a.ldc + n, h, left, vec);
-        if (a.P[0]) {
-          store4<OUT>(a.P[0], m * a.ldp + n, g, left, vecp);
-          store4<OUT>(a.P[1], m * a.ldp + n, u, left, vecp);
-        }
-      }
-    }
-  } else {
-    constexpr int EB = OUT == NM_F32 ? 4 : 2;
-    uint8_t* C = static_cast<uint8_t*>(bat ? a.C[1] : a.C[0]) + (int64_t)ks * a.cs * EB;
-    const bool vec = (a.ldc % 4 == 0) && ((uintptr_t)C % (4 * EB) == 0);
-    const uint8_t* mask = OP == TILE_MASKED ? (bat ? a.mask[1] : a.mask[0]) : nullptr;
-    const int64_t ncol = n0 + wn * TN * 16 + 4 * lq;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int64_t n = ncol + 16 * i;
-      const int left = (int)min(a.Nr - n, (int64_t)4);
-      if (left <= 0) continue;
-      float b[4] = {0.f, 0.f, 0.f, 0.f};
-      if (OP == TILE_LINEAR && a.bias) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (v < left) b[v] = a.bias[n + v];
-      }
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const int64_t m = mrow + 16 * j;
-        if (m >= a.Mr) continue;
-        float y[4];
-        int keep = 15;
-        if constexpr (OP == TILE_MASKED) keep = mask[m * a.ldm + (n >> 3)] >> (n & 4);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          y[v] = acc[i][j][v] + b[v];
-          if constexpr (OP == TILE_LINEAR) y[v] = a.act == NM_ACT_GELU ? gelu_f32(y[v]) : y[v];
-          if constexpr (OP == TILE_MASKED) y[v] = (keep >> v & 1) ? y[v] : 0.f;   // a select: NaN is masked too
-        }
-        store4<OUT>(C, m * a.ldc + n, y, left, vec);
-      }
-    }
-  }
+  __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));           // nothing lands in LDS after this
 #endif
 }
 
-template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN>
-hipError_t launch_tile_cfg(TileArgs a, hipStream_t s) {
-  constexpr int BNO = OP == TILE_GLU ? BN / 2 : BN;
-  a.mt = (int)((a.Mr + BM - 1) / BM);
-  a.nt = (int)((a.Nr + BNO - 1) / BNO);
-  const int64_t total = (int64_t)a.mt * a.nt * a.split * a.batch;
-  const int64_t grid = (total + 7) / 8 * 8;
-  const int gm = a.mt < 8 ? a.mt : 8;
-  hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a,
-                     gm);
+template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
+hipError_t launch_tile_cfg(const TileArgs& a, hipStream_t s) {
+  const TileList list = tile_list(a, BM, OP == TILE_GLU ? BN / 2 : BN);
+  hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3((unsigned)list.grid), dim3(WM * WN * 64), 0,
+                     s, a, list);
   return hipGetLastError();
 }
 
-// Tile choice: 256 x 256 where its tiles fill the chip, 128 x 128 (two
-// workgroups share a CU) for fewer.
 template <int ET, int OP, int OUT>
 hipError_t launch_tile_op(const TileArgs& a, hipStream_t s) {
-  constexpr int BNO = OP == TILE_GLU ? 128 : 256;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) dev = 0;
-  const int64_t big = ((a.Mr + 255) / 256) * ((a.Nr + BNO - 1) / BNO) * a.batch * a.split;
-  if (big >= cu_count(dev) * 3 / 4) return launch_tile_cfg<ET, OP, OUT, 256, 256, 4, 2>(a, s);
-  return launch_tile_cfg<ET, OP, OUT, 128, 128, 2, 2>(a, s);
+  switch (a.shape) {
+    case 0: return launch_tile_cfg<ET, OP, OUT, 256, 256, 4, 2, 2>(a, s);
+    case 1: return launch_tile_cfg<ET, OP, OUT, 128, 256, 2, 4, 3>(a, s);
+    default: return launch_tile_cfg<ET, OP, OUT, 128, 128, 2, 2, 4>(a, s);
+  }
 }
 
 template <int ET>
