@@ -89,6 +89,8 @@ struct GluArgs {
 
 // few tokens: the packed weights streamed once per token tile
 hipError_t launch_glu_decode(const GluArgs& a, hipStream_t s);
+// more tokens, both weights 2:4: the sparse tile product
+hipError_t launch_glu_tile24(const GluArgs& a, hipStream_t s);
 
 // Packed weight -> dense [R][Kp] (Kp = K rounded up to 64, zero filled) and /
 // or its transpose [K][ldt] at column c0 (rows r >= R of the last 64 zero),

@@ -70,6 +70,10 @@ bool rows_direct(const void* X, int64_t ldx, int64_t K) {
   return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
 }
 
+// whether the call multiplies dense copies of the weights: neither streamed
+// for few tokens nor fed to the sparse tile product
+bool glu_dense(const Geometry& g, int64_t T) { return T > kFewTokens && !(g.N == 2 && g.M == 4); }
+
 size_t padded_bytes(const Geometry& g, int64_t T) { return up256((size_t)(T * up64(g.K) * 2)); }
 size_t dense_bytes(const Geometry& g) { return up256((size_t)(g.R * up64(g.K) * 2)); }
 
@@ -216,7 +220,7 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int6
   const nm_status st = check_pair(gate, up, &g);
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
-  *bytes = padded_bytes(g, T) + (T > kFewTokens ? 2 * dense_bytes(g) : 0);
+  *bytes = padded_bytes(g, T) + (glu_dense(g, T) ? 2 * dense_bytes(g) : 0);
   return NM_OK;
 }
 
@@ -233,9 +237,9 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
   if (!aligned(Xt, 2) || !aligned(Ht, 2) || (G && (!aligned(G, 2) || !aligned(U, 2)))) return NM_EUNSUPPORTED;
   const bool direct = rows_direct(Xt, ldx, g.K);
-  const bool few = T <= kFewTokens;
+  const bool few = T <= kFewTokens, dense = glu_dense(g, T);
   const size_t pad = direct ? 0 : padded_bytes(g, T);
-  const size_t need = pad + (few ? 0 : 2 * dense_bytes(g));
+  const size_t need = pad + (dense ? 2 * dense_bytes(g) : 0);
   if (need && (!workspace || workspace_bytes < need)) return NM_EINVAL;
   if (need && !aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -249,7 +253,7 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
     X = ws;
   }
   const nm_packed* w[2] = {gate, up};
-  if (few) {
+  if (!dense) {
     nm::GluArgs a{};
     a.g = g;
     a.wdt = gate->dtype;
@@ -268,7 +272,7 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
     a.act = act;
     // a padded row is all 16-byte pieces: its zeros may be read
     if (!direct) a.g.K = ld;
-    return nm::launch_glu_decode(a, s) == hipSuccess ? NM_OK : NM_EHIP;
+    return (few ? nm::launch_glu_decode(a, s) : nm::launch_glu_tile24(a, s)) == hipSuccess ? NM_OK : NM_EHIP;
   }
   nm::TileArgs a{};
   const int64_t Kp = up64(g.K);
