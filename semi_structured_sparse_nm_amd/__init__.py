@@ -472,52 +472,89 @@ def spmm_hybrid(h: Hybrid, X: torch.Tensor, bias: torch.Tensor | None = None,
 # ---------------------------------------------------------------- gated feed-forward block
 GLU_ACTS = {"gelu": 1, "silu": 2}
 
+# The smallest of the calls below take a few microseconds on the GPU, so their
+# host side is kept short: descriptors and workspace sizes are remembered per
+# weight and shape, devices compared by index, streams taken as raw handles.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+_ws_sizes: dict = {}
 
-def _device_of(tensors) -> torch.device:
-    """The one GPU all (name, tensor) pairs live on; None tensors are skipped."""
-    dev = tensors[0][1].device
-    if dev.type != "cuda":
-        raise ValueError(f"{tensors[0][0]} is on {dev}, not on a GPU")
-    for name, t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {dev}")
-    return dev
+
+def _descriptor(p):
+    """byref of p's C descriptor, built again whenever a field changed."""
+    second = p.meta if type(p) is Packed else p.scales
+    first = p.values if type(p) is Packed else p.codes
+    key = (first.data_ptr(), 0 if second is None else second.data_ptr(), first.numel(), p.rows, p.K,
+           p.format_version, (p.N, p.M, p.dtype) if type(p) is Packed else None)
+    c = p.__dict__.get("_c_desc")
+    if c is None or c[0] != key:
+        d = p.desc()
+        c = (key, d, ctypes.byref(d))
+        p.__dict__["_c_desc"] = c
+    return c[2]
+
+
+def _sized(f, what: str, key: tuple, *args) -> int:
+    """A workspace size of the library, remembered by shape and device."""
+    n = _ws_sizes.get(key)
+    if n is None:
+        b = ctypes.c_size_t()
+        _check(f(*args, ctypes.byref(b)), what)
+        if len(_ws_sizes) > 4096:
+            _ws_sizes.clear()
+        n = _ws_sizes[key] = b.value
+    return n
+
+
+def _one_gpu(first: str, t0: torch.Tensor, *rest) -> int:
+    """The index of the one GPU t0 and the (name, tensor) pairs live on; None
+    tensors are skipped."""
+    i = t0.get_device()
+    if i < 0:
+        raise ValueError(f"{first} is on {t0.device}, not on a GPU")
+    for name, t in rest:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"{name} is on {t.device}, {first} on {t0.device}")
+    return i
 
 
 def _row_pitch(name: str, t: torch.Tensor, rows: int, cols: int) -> int:
     """Elements between the rows of a [rows, cols] tensor with unit stride
     along its columns, as the library takes them (rows may not overlap)."""
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its second dimension")
     if rows == 1:
         return cols
-    if t.stride(0) < cols:
-        raise ValueError(f"{name} has overlapping rows (stride {t.stride(0)} for {cols} columns)")
-    return t.stride(0)
+    if s0 < cols:
+        raise ValueError(f"{name} has overlapping rows (stride {s0} for {cols} columns)")
+    return s0
 
 
-def _workspace(workspace: torch.Tensor | None, need: int, dev: torch.device) -> torch.Tensor | None:
-    """The caller's workspace where it is large enough, else a new one."""
+def _workspace(workspace: torch.Tensor | None, need: int, dev: int):
+    """(tensor, pointer, bytes): the caller's workspace where it is large
+    enough, else a new one; the tensor is held by the caller of the library."""
     if workspace is not None:
-        if workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, the operands on {dev}")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, the operands on cuda:{dev}")
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        if workspace.numel() * workspace.element_size() >= need:
-            return workspace
-    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-
-
-def _ws_args(ws: torch.Tensor | None):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+        n = workspace.numel() * workspace.element_size()
+        if n >= need:
+            return workspace, workspace.data_ptr(), n
+    if not need:
+        return None, None, 0
+    workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+    return workspace, workspace.data_ptr(), need
 
 
 def _glu_act(act: str) -> int:
-    if act not in GLU_ACTS:
+    a = GLU_ACTS.get(act)
+    if a is None:
         raise ValueError(f"act must be one of {sorted(GLU_ACTS)}, got {act!r}")
-    return GLU_ACTS[act]
+    return a
 
 
 def _check_dtype(name: str, t: torch.Tensor, want: torch.dtype) -> None:
@@ -525,15 +562,16 @@ def _check_dtype(name: str, t: torch.Tensor, want: torch.dtype) -> None:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
 
 
-def _call(dev: torch.device, f, what: str, *args) -> None:
+def _call(dev: int, f, what: str, *args) -> None:
     """One library call with the operands' device current and its current
     stream as the last argument."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(dev))
+    if dev == torch.cuda.current_device():
+        st = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(dev))
-    _check(st, what)
+            st = f(*args, _raw_stream(dev))
+    if st != NM_OK:
+        raise NmError(st, what)
 
 
 def _glu_operands(gate: Packed, up: Packed, Xt: torch.Tensor):
@@ -551,7 +589,7 @@ def _glu_operands(gate: Packed, up: Packed, Xt: torch.Tensor):
 
 
 def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
-    if pre.dim() != 3 or tuple(pre.shape) != (2, T, p.rows):
+    if pre.shape != (2, T, p.rows):
         raise ValueError(f"pre must be [2, {T}, {p.rows}], got {tuple(pre.shape)}")
     _check_dtype("pre", pre, p.torch_dtype)
     if pre.stride(0) < (T - 1) * pre.stride(1) + p.rows:
@@ -559,10 +597,14 @@ def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
     return _row_pitch("pre", pre[0], T, p.rows)
 
 
+def _glu_key(what: str, p: Packed, T: int, dev: int) -> tuple:
+    return what, p.rows, p.K, p.N, p.M, p.dtype, T, dev
+
+
 def glu_workspace_size(gate: Packed, up: Packed, T: int) -> int:
     """nm_glu_workspace_size: bytes of workspace glu() may need."""
-    n, dg, du = ctypes.c_size_t(), gate.desc(), up.desc()
-    _check(lib().nm_glu_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)),
+    n = ctypes.c_size_t()
+    _check(lib().nm_glu_workspace_size(_descriptor(gate), _descriptor(up), T, ctypes.byref(n)),
            "nm_glu_workspace_size")
     return n.value
 
@@ -576,28 +618,30 @@ def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torc
     which glu_backward() takes."""
     T, ldx = _glu_operands(gate, up, Xt)
     a = _glu_act(act)
+    R = gate.rows
     if out is None:
-        out = torch.empty((T, gate.rows), dtype=Xt.dtype, device=Xt.device)
-    ldh = _row_pitch("out", out, T, gate.rows)
-    _check_dtype("out", out, Xt.dtype)
-    ldp = 0 if pre is None else _check_pre(pre, T, gate)
-    dev = _device_of([("Xt", Xt), ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
-                      ("up meta", up.meta), ("out", out), ("pre", pre)])
-    dg, du, n = gate.desc(), up.desc(), ctypes.c_size_t()
-    L = lib()
-    _check(L.nm_glu_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)), "nm_glu_workspace_size")
-    ws = _workspace(workspace, n.value, dev)
-    g, u = (None, None) if pre is None else (pre.data_ptr(),
-                                             pre.data_ptr() + pre.stride(0) * pre.element_size())
-    _call(dev, L.nm_glu, "nm_glu", ctypes.byref(dg), ctypes.byref(du), Xt.data_ptr(), ldx, T, out.data_ptr(), ldh, a,
-          g, u, ldp, *_ws_args(ws))
+        out = Xt.new_empty((T, R))
+    else:
+        _check_dtype("out", out, Xt.dtype)
+    ldh = _row_pitch("out", out, T, R)
+    ldp, g, u = 0, None, None
+    if pre is not None:
+        ldp = _check_pre(pre, T, gate)
+        g = pre.data_ptr()
+        u = g + pre.stride(0) * pre.element_size()
+    dev = _one_gpu("Xt", Xt, ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
+                   ("up meta", up.meta), ("out", out), ("pre", pre))
+    L, dg, du = lib(), _descriptor(gate), _descriptor(up)
+    need = _sized(L.nm_glu_workspace_size, "nm_glu_workspace_size", _glu_key("glu", gate, T, dev), dg, du, T)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call(dev, L.nm_glu, "nm_glu", dg, du, Xt.data_ptr(), ldx, T, out.data_ptr(), ldh, a, g, u, ldp, wp, wn)
     return out
 
 
 def glu_backward_workspace_size(gate: Packed, up: Packed, T: int) -> int:
     """nm_glu_backward_workspace_size: bytes of workspace glu_backward() needs."""
-    n, dg, du = ctypes.c_size_t(), gate.desc(), up.desc()
-    _check(lib().nm_glu_backward_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)),
+    n = ctypes.c_size_t()
+    _check(lib().nm_glu_backward_workspace_size(_descriptor(gate), _descriptor(up), T, ctypes.byref(n)),
            "nm_glu_backward_workspace_size")
     return n.value
 
@@ -614,23 +658,23 @@ def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, 
     if not need_dx and not need_dw:
         raise ValueError("glu_backward needs need_dx or need_dw")
     ldp = _check_pre(pre, T, gate)
-    lddh = _row_pitch("dH", dH, T, gate.rows)
-    _check_dtype("dH", dH, Xt.dtype)
-    dev = _device_of([("Xt", Xt), ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
-                      ("up meta", up.meta), ("pre", pre), ("dH", dH)])
-    dg, du, n = gate.desc(), up.desc(), ctypes.c_size_t()
-    L = lib()
-    _check(L.nm_glu_backward_workspace_size(ctypes.byref(dg), ctypes.byref(du), T, ctypes.byref(n)),
-           "nm_glu_backward_workspace_size")
-    ws = _workspace(workspace, n.value, dev)
     R, K = gate.rows, gate.K
-    dX = torch.empty((T, K), dtype=Xt.dtype, device=dev) if need_dx else None
-    dWg = torch.empty((R, K), dtype=Xt.dtype, device=dev) if need_dw else None
-    dWu = torch.empty((R, K), dtype=Xt.dtype, device=dev) if need_dw else None
-    _call(dev, L.nm_glu_backward, "nm_glu_backward", ctypes.byref(dg), ctypes.byref(du), Xt.data_ptr(), ldx, T,
-          pre.data_ptr(), pre.data_ptr() + pre.stride(0) * pre.element_size(), ldp, dH.data_ptr(), lddh, a,
-          None if dX is None else dX.data_ptr(), K, None if dWg is None else dWg.data_ptr(),
-          None if dWu is None else dWu.data_ptr(), K, *_ws_args(ws))
+    lddh = _row_pitch("dH", dH, T, R)
+    _check_dtype("dH", dH, Xt.dtype)
+    dev = _one_gpu("Xt", Xt, ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
+                   ("up meta", up.meta), ("pre", pre), ("dH", dH))
+    L, dg, du = lib(), _descriptor(gate), _descriptor(up)
+    need = _sized(L.nm_glu_backward_workspace_size, "nm_glu_backward_workspace_size",
+                  _glu_key("glu_backward", gate, T, dev), dg, du, T)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    dX = Xt.new_empty((T, K)) if need_dx else None
+    dWg = Xt.new_empty((R, K)) if need_dw else None
+    dWu = Xt.new_empty((R, K)) if need_dw else None
+    g = pre.data_ptr()
+    _call(dev, L.nm_glu_backward, "nm_glu_backward", dg, du, Xt.data_ptr(), ldx, T, g,
+          g + pre.stride(0) * pre.element_size(), ldp, dH.data_ptr(), lddh, a,
+          dX.data_ptr() if need_dx else None, K, dWg.data_ptr() if need_dw else None,
+          dWu.data_ptr() if need_dw else None, K, wp, wn)
     return dX, dWg, dWu
 
 
@@ -653,19 +697,26 @@ class Mx:
         return self.codes.numel() + self.scales.numel()
 
 
-_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
+_FLOATS = {torch.float16: NM_F16, torch.bfloat16: NM_BF16, torch.float32: NM_F32}
 
 
-def _check_float(name: str, dt: torch.dtype) -> None:
-    if dt not in _FLOATS:
+def _float_type(name: str, dt: torch.dtype) -> int:
+    n = _FLOATS.get(dt)
+    if n is None:
         raise TypeError(f"{name} must be float16, bfloat16 or float32, got {dt}")
+    return n
 
 
 def mx_size(rows: int, K: int):
     """nm_mx_size: bytes of an Mx's codes and scales."""
-    c, s = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().nm_mx_size(rows, K, ctypes.byref(c), ctypes.byref(s)), "nm_mx_size")
-    return c.value, s.value
+    n = _ws_sizes.get((rows, K))
+    if n is None:
+        c, s = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib().nm_mx_size(rows, K, ctypes.byref(c), ctypes.byref(s)), "nm_mx_size")
+        if len(_ws_sizes) > 4096:
+            _ws_sizes.clear()
+        n = _ws_sizes[(rows, K)] = (c.value, s.value)
+    return n
 
 
 def mx_quantize(X: torch.Tensor) -> Mx:
@@ -674,65 +725,63 @@ def mx_quantize(X: torch.Tensor) -> Mx:
     2^(floor(log2(amax)) - 2), elements rounded half to even and saturated."""
     if X.dim() != 2:
         raise ValueError("X must be a 2-D tensor")
-    _check_float("X", X.dtype)
+    xdt = _float_type("X", X.dtype)
     rows, K = X.shape
     ldx = _row_pitch("X", X, rows, K)
-    dev = _device_of([("X", X)])
+    dev = _one_gpu("X", X)
     c, s = mx_size(rows, K)
-    m = Mx(rows, K, torch.empty(c, dtype=torch.uint8, device=dev), torch.empty(s, dtype=torch.uint8, device=dev), 0)
-    d = m.desc()
-    _call(dev, lib().nm_mx_quantize, "nm_mx_quantize", X.data_ptr(), ldx, _TORCH_TO_NM[X.dtype], ctypes.byref(d))
-    m.format_version = d.format_version
+    # one allocation for both buffers (the codes' size is a multiple of 128)
+    both = X.new_empty((c + s,), dtype=torch.uint8)
+    m = Mx(rows, K, both[:c], both[c:])
+    _call(dev, lib().nm_mx_quantize, "nm_mx_quantize", X.data_ptr(), ldx, xdt, _descriptor(m))
     return m
 
 
 def mx_dequantize(m: Mx, out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
     """nm_mx_dequantize: the [rows, K] values m stands for."""
-    dev = _device_of([("codes", m.codes), ("scales", m.scales), ("out", out)])
     if out is None:
-        out = torch.empty((m.rows, m.K), dtype=out_dtype, device=dev)
-    _check_float("out", out.dtype)
+        out = m.codes.new_empty((m.rows, m.K), dtype=out_dtype)
+    ydt = _float_type("out", out.dtype)
     ld = _row_pitch("out", out, m.rows, m.K)
-    d = m.desc()
-    _call(dev, lib().nm_mx_dequantize, "nm_mx_dequantize", ctypes.byref(d), out.data_ptr(), ld,
-          _TORCH_TO_NM[out.dtype])
+    dev = _one_gpu("codes", m.codes, ("scales", m.scales), ("out", out))
+    _call(dev, lib().nm_mx_dequantize, "nm_mx_dequantize", _descriptor(m), out.data_ptr(), ld, ydt)
     return out
 
 
 def mx_workspace_size(w: Mx, T: int, glu: bool = False) -> int:
     """nm_mx_workspace_size: bytes of workspace mx_linear() / mx_glu() may need."""
-    n, d = ctypes.c_size_t(), w.desc()
-    _check(lib().nm_mx_workspace_size(ctypes.byref(d), T, int(glu), ctypes.byref(n)), "nm_mx_workspace_size")
+    n = ctypes.c_size_t()
+    _check(lib().nm_mx_workspace_size(_descriptor(w), T, int(glu), ctypes.byref(n)), "nm_mx_workspace_size")
     return n.value
 
 
-def _mx_operands(w: Mx, X, out_dtype, out, workspace, others, glu: bool):
+def _mx_operands(w: Mx, X, out_dtype, out, workspace, glu: bool, *others):
     """Checks shared by mx_linear and mx_glu: (device, T, xq, x pointer, ldx,
-    x dtype, out, ldy, workspace)."""
-    if isinstance(X, Mx):
+    x dtype, out, ldy, y dtype, workspace triple)."""
+    if type(X) is Mx:
         if X.K != w.K:
             raise ValueError(f"X has K={X.K}, the weight has K={w.K}")
-        T, xq, xp, ldx, xdt = X.rows, ctypes.byref(X.desc()), None, 0, 0
-        xs = [("X codes", X.codes), ("X scales", X.scales)]
-        default = torch.bfloat16
+        T, xq, xp, ldx, xdt = X.rows, _descriptor(X), None, 0, 0
+        x0, default = X.codes, torch.bfloat16
+        others = (("X scales", X.scales),) + others
     else:
         if X.dim() != 2:
             raise ValueError("X must be a 2-D tensor or an Mx")
-        _check_float("X", X.dtype)
+        xdt = _float_type("X", X.dtype)
         T = X.shape[0]
         ldx = _row_pitch("X", X, T, w.K)
-        xq, xp, xdt = None, X.data_ptr(), _TORCH_TO_NM[X.dtype]
-        xs = [("X", X)]
-        default = X.dtype
+        xq, xp = None, X.data_ptr()
+        x0, default = X, X.dtype
     if out is None:
-        out = torch.empty((T, w.rows), dtype=default if out_dtype is None else out_dtype, device=xs[0][1].device)
+        out = x0.new_empty((T, w.rows), dtype=default if out_dtype is None else out_dtype)
     elif out_dtype is not None:
         _check_dtype("out", out, out_dtype)
-    _check_float("out", out.dtype)
+    ydt = _float_type("out", out.dtype)
     ldy = _row_pitch("out", out, T, w.rows)
-    dev = _device_of(xs + [("weight codes", w.codes), ("weight scales", w.scales), ("out", out)] + others)
-    need = mx_workspace_size(w, T, glu)
-    return dev, T, xq, xp, ldx, xdt, out, ldy, _workspace(workspace, need, dev)
+    dev = _one_gpu("X", x0, ("weight codes", w.codes), ("weight scales", w.scales), ("out", out), *others)
+    need = _sized(lib().nm_mx_workspace_size, "nm_mx_workspace_size", ("mx", w.rows, w.K, T, glu, dev),
+                  _descriptor(w), T, int(glu))
+    return dev, T, xq, xp, ldx, xdt, out, ldy, ydt, _workspace(workspace, need, dev)
 
 
 def mx_linear(w: Mx, X, bias: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
@@ -744,14 +793,16 @@ def mx_linear(w: Mx, X, bias: torch.Tensor | None = None, out_dtype: torch.dtype
     out_dtype says otherwise; act "none" or "gelu"."""
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    bp = None
     if bias is not None:
         _check_dtype("bias", bias, torch.float32)
-        if bias.dim() != 1 or bias.numel() != w.rows or (bias.numel() > 1 and bias.stride(0) != 1):
+        if bias.shape != (w.rows,) or (w.rows > 1 and bias.stride(0) != 1):
             raise ValueError(f"bias must be a contiguous vector of length R={w.rows}, got {tuple(bias.shape)}")
-    dev, T, xq, xp, ldx, xdt, out, ldy, ws = _mx_operands(w, X, out_dtype, out, workspace, [("bias", bias)], False)
-    d = w.desc()
-    _call(dev, lib().nm_mx_linear, "nm_mx_linear", ctypes.byref(d), xq, xp, ldx, xdt, T, out.data_ptr(), ldy,
-          _TORCH_TO_NM[out.dtype], None if bias is None else bias.data_ptr(), ACTS[act], *_ws_args(ws))
+        bp = bias.data_ptr()
+    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, ws = _mx_operands(w, X, out_dtype, out, workspace, False,
+                                                               ("bias", bias))
+    _call(dev, lib().nm_mx_linear, "nm_mx_linear", _descriptor(w), xq, xp, ldx, xdt, T, out.data_ptr(), ldy, ydt, bp,
+          ACTS[act], ws[1], ws[2])
     return out
 
 
@@ -761,11 +812,10 @@ def mx_glu(gate: Mx, up: Mx, X, act: str = "silu", out_dtype: torch.dtype | None
     activations, as in mx_linear) in the microscaled 4-bit format:
     H[T, R] = act(X @ Wg^T) * (X @ Wu^T); act "silu" or "gelu"."""
     a = _glu_act(act)
-    if (gate.rows, gate.K) != (up.rows, up.K):
+    if gate.rows != up.rows or gate.K != up.K:
         raise ValueError(f"gate is {gate.rows} x {gate.K}, up is {up.rows} x {up.K}")
-    dev, T, xq, xp, ldx, xdt, out, ldy, ws = _mx_operands(
-        gate, X, out_dtype, out, workspace, [("up codes", up.codes), ("up scales", up.scales)], True)
-    dg, du = gate.desc(), up.desc()
-    _call(dev, lib().nm_mx_glu, "nm_mx_glu", ctypes.byref(dg), ctypes.byref(du), xq, xp, ldx, xdt, T, out.data_ptr(),
-          ldy, _TORCH_TO_NM[out.dtype], a, *_ws_args(ws))
+    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, ws = _mx_operands(gate, X, out_dtype, out, workspace, True,
+                                                               ("up codes", up.codes), ("up scales", up.scales))
+    _call(dev, lib().nm_mx_glu, "nm_mx_glu", _descriptor(gate), _descriptor(up), xq, xp, ldx, xdt, T, out.data_ptr(),
+          ldy, ydt, a, ws[1], ws[2])
     return out

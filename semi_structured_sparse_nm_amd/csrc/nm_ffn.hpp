@@ -92,19 +92,40 @@ hipError_t launch_glu_decode(const GluArgs& a, hipStream_t s);
 // more tokens, both weights 2:4: the sparse tile product
 hipError_t launch_glu_tile24(const GluArgs& a, hipStream_t s);
 
-// Packed weight -> dense [R][Kp] (Kp = K rounded up to 64, zero filled) and /
-// or its transpose [K][ldt] at column c0 (rows r >= R of the last 64 zero),
-// and / or the kept bits [R][Kp / 8].
-hipError_t launch_expand_dense(const Geometry& g, const uint8_t* values, const uint8_t* meta, uint16_t* dense,
-                               hipStream_t s);
-hipError_t launch_expand_transposed(const Geometry& g, const uint8_t* values, const uint8_t* meta, uint16_t* dt,
-                                    int64_t ldt, uint8_t* mask, hipStream_t s);
+// Both packed weights -> dense [R][Kp] (Kp = K rounded up to 64, zero filled).
+struct DenseArgs {
+  const uint8_t* values[2];
+  const uint8_t* meta[2];
+  uint16_t* dense[2];
+};
+hipError_t launch_expand_dense(const Geometry& g, const DenseArgs& a, hipStream_t s);
 
-// dG = dH u act'(g), dU = dH act(g) from P = (g, u): rows of [T][ldd] (gate
-// at column 0, up at column Rp, zeros up to Rp) and transposed [2][R][Tp].
-hipError_t launch_glu_dact(const void* dH, int64_t ldh, const void* G, const void* U, int64_t ldp, int64_t T,
-                           int64_t R, int64_t Rp, void* d, int64_t ldd, void* dt, int64_t Tp, int act, int wdt,
-                           hipStream_t s);
+// The backward pass's operands (16-bit): from P = (G, U) and dH, dG = dH u
+// act'(g) and dU = dH act(g) as rows d [T][2 Rp] (gate at column 0, up at Rp,
+// zeros from R to Rp) and transposed dt [2][R][Tp]; both weights transposed,
+// wt [K][2 Rp]; their kept bits, mask[w] [R][Kp / 8]; X transposed, xt [K][Tp].
+// Rp, Tp, Kp: R, T, K rounded up to 64, zero filled.  Null outputs are left out.
+struct PrepareArgs {
+  Geometry g;
+  const uint8_t* values[2];
+  const uint8_t* meta[2];
+  const uint16_t* X;
+  int64_t ldx, T;
+  const uint16_t* G;
+  const uint16_t* U;
+  int64_t ldp;
+  const uint16_t* dH;
+  int64_t lddh;
+  int act;
+  int64_t Rp, Tp;
+  uint16_t* d;
+  uint16_t* dt;
+  uint16_t* wt;
+  uint16_t* xt;
+  uint8_t* mask[2];
+  bool vec_h, vec_x;           // 16-byte loads, filled by the launcher
+};
+hipError_t launch_glu_prepare(PrepareArgs a, int wdt, hipStream_t s);
 // copy of X [T][ldx] with rows of Kp elements, zeros past K
 hipError_t launch_pad_rows(const void* X, int64_t ldx, int64_t T, int64_t K, void* Y, int64_t Kp, hipStream_t s);
 

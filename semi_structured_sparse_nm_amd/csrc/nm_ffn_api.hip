@@ -276,14 +276,16 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   }
   nm::TileArgs a{};
   const int64_t Kp = up64(g.K);
+  nm::DenseArgs e{};
   for (int i = 0; i < 2; ++i) {
     uint8_t* d = ws + pad + i * dense_bytes(g);
-    if (nm::launch_expand_dense(g, static_cast<const uint8_t*>(w[i]->values), static_cast<const uint8_t*>(w[i]->meta),
-                                reinterpret_cast<uint16_t*>(d), s) != hipSuccess)
-      return NM_EHIP;
+    e.values[i] = static_cast<const uint8_t*>(w[i]->values);
+    e.meta[i] = static_cast<const uint8_t*>(w[i]->meta);
+    e.dense[i] = reinterpret_cast<uint16_t*>(d);
     a.A[i] = static_cast<const uint8_t*>(X);
     a.B[i] = d;
   }
+  if (nm::launch_expand_dense(g, e, s) != hipSuccess) return NM_EHIP;
   a.lda = ld * 2;
   a.ldb = Kp * 2;
   a.Mr = T;
@@ -344,15 +346,29 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   float* part = reinterpret_cast<float*>(mask + 2 * p.mask);
   const nm_packed* w[2] = {gate, up};
 
-  if (nm::launch_glu_dact(dH, lddh, G, U, ldp, T, g.R, p.Rp, dX ? d : nullptr, 2 * p.Rp, dWg ? dt : nullptr, p.Tp, act,
-                          gate->dtype, s) != hipSuccess)
-    return NM_EHIP;
-  for (int i = 0; i < 2; ++i)
-    if (nm::launch_expand_transposed(g, static_cast<const uint8_t*>(w[i]->values),
-                                     static_cast<const uint8_t*>(w[i]->meta),
-                                     reinterpret_cast<uint16_t*>(wt) + i * p.Rp, 2 * p.Rp,
-                                     dWg ? mask + i * p.mask : nullptr, s) != hipSuccess)
-      return NM_EHIP;
+  nm::PrepareArgs q{};
+  q.g = g;
+  for (int i = 0; i < 2; ++i) {
+    q.values[i] = static_cast<const uint8_t*>(w[i]->values);
+    q.meta[i] = static_cast<const uint8_t*>(w[i]->meta);
+    q.mask[i] = dWg ? mask + i * p.mask : nullptr;
+  }
+  q.X = static_cast<const uint16_t*>(Xt);
+  q.ldx = ldx;
+  q.T = T;
+  q.G = static_cast<const uint16_t*>(G);
+  q.U = static_cast<const uint16_t*>(U);
+  q.ldp = ldp;
+  q.dH = static_cast<const uint16_t*>(dH);
+  q.lddh = lddh;
+  q.act = act;
+  q.Rp = p.Rp;
+  q.Tp = p.Tp;
+  q.d = dX ? reinterpret_cast<uint16_t*>(d) : nullptr;
+  q.wt = dX ? reinterpret_cast<uint16_t*>(wt) : nullptr;
+  q.dt = dWg ? reinterpret_cast<uint16_t*>(dt) : nullptr;
+  q.xt = dWg ? reinterpret_cast<uint16_t*>(xt) : nullptr;
+  if (nm::launch_glu_prepare(q, gate->dtype, s) != hipSuccess) return NM_EHIP;
   if (dX) {
     // dX[t][k] = sum over both weights' rows of d[t][r] W[r][k]
     nm::TileArgs a{};
@@ -370,7 +386,6 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   }
   if (dWg) {
     // dW[r][k] = sum over t of d[t][r] X[t][k], both transposed
-    if (nm::launch_transpose(Xt, T, g.K, ldx, xt, p.Tp, p.Tp, 2, s) != hipSuccess) return NM_EHIP;
     nm::TileArgs a{};
     for (int i = 0; i < 2; ++i) {
       a.A[i] = dt + (size_t)i * g.R * p.Tp * 2;

@@ -58,41 +58,37 @@ __device__ __forceinline__ uint32_t expand8(const Geometry& g, const uint8_t* va
   return keep;
 }
 
-__global__ void __launch_bounds__(256) expand_dense_kernel(Geometry g, const uint8_t* values, const uint8_t* meta,
-                                                           uint16_t* dense) {
-  const int64_t pr = g.nKB * 8;                        // 8-column pieces per row
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= g.R * pr) return;
-  const int64_t r = i / pr, c = (i - r * pr) * 8;
-  uint32_t o[4];
-  expand8(g, values, meta, r, c, o);
-  *reinterpret_cast<v4i*>(dense + r * pr * 8 + c) = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+// Sixteen dense columns c .. c + 15 (c % 16 == 0): one 16-byte piece of the
+// packed row where four of eight are kept.
+__device__ __forceinline__ uint32_t expand16(const Geometry& g, const uint8_t* values, const uint8_t* meta, int64_t r,
+                                             int64_t c, uint32_t (&o)[8]) {
+  uint32_t h[4];
+  uint32_t keep = expand8(g, values, meta, r, c, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = h[i];
+  keep |= expand8(g, values, meta, r, c + 8, h) << 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[4 + i] = h[i];
+  return keep;
 }
 
-// One workgroup per 64 rows x 64 columns: the pieces land transposed in LDS
-// (row pitch 72 halves: the 16-byte reads stay aligned) and leave as rows of dt.
-__global__ void __launch_bounds__(256) expand_transposed_kernel(Geometry g, const uint8_t* values,
-                                                                const uint8_t* meta, uint16_t* dt, int64_t ldt,
-                                                                uint8_t* mask) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
-  const int64_t c0 = (int64_t)blockIdx.x * 64, r0 = (int64_t)blockIdx.y * 64;
-  for (int q = threadIdx.x; q < 512; q += 256) {
-    const int rl = q & 63, cl = (q >> 6) * 8;
-    const int64_t r = r0 + rl;
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
-    if (r < g.R) {
-      const uint32_t keep = expand8(g, values, meta, r, c0 + cl, o);
-      if (mask) mask[r * (g.nKB * 8) + (c0 + cl) / 8] = (uint8_t)keep;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) tile[cl + e][rl] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
-  }
-  __syncthreads();
-  for (int q = threadIdx.x; q < 512; q += 256) {
-    const int kl = q >> 3, rl = (q & 7) * 8;
-    if (c0 + kl < g.K)
-      *reinterpret_cast<v4i*>(dt + (c0 + kl) * ldt + r0 + rl) = *reinterpret_cast<const v4i*>(&tile[kl][rl]);
-  }
+// blockIdx.y: the weight.  A wave covers one packed block (16 rows x 64
+// columns), lane 4 r + q its columns 16 q .. of row r.
+__global__ void __launch_bounds__(256) expand_dense_kernel(Geometry g, DenseArgs a) {
+  const uint8_t* values = blockIdx.y ? a.values[1] : a.values[0];
+  const uint8_t* meta = blockIdx.y ? a.meta[1] : a.meta[0];
+  uint16_t* dense = blockIdx.y ? a.dense[1] : a.dense[0];
+  const int lane = threadIdx.x & 63;
+  const int64_t blk = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (blk >= g.nRB * g.nKB) return;
+  const int64_t rb = blk / g.nKB, kb = blk - rb * g.nKB;
+  const int64_t r = rb * 16 + (lane >> 2), c = kb * 64 + (lane & 3) * 16;
+  if (r >= g.R) return;
+  uint32_t o[8];
+  expand16(g, values, meta, r, c, o);
+  v4i* d = reinterpret_cast<v4i*>(dense + r * (g.nKB * 64) + c);
+  d[0] = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+  d[1] = v4i{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
 }
 
 template <int WT>
@@ -107,35 +103,43 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, b
   }
 }
 
-// One workgroup per 64 tokens x 64 outputs.  dG and dU are rounded to the
-// weights' 16-bit type here: they are operands of the matrix instruction in
-// both products that follow (half a step each, as any 16-bit operand).
+// What the backward pass's products read, in one launch; workgroups take, by
+// index, one of three kinds of tile:
+//
+//  - 64 tokens x 64 outputs of dG and dU, as rows (d) and transposed (dt).  They
+//    are rounded to the weights' 16-bit type here: operands of the matrix
+//    instruction in both products that follow (half a step each, as any
+//    16-bit operand).
+//  - 128 rows x 64 columns of one weight, expanded and transposed (wt), with
+//    the bits of the kept columns.
+//  - 64 tokens x 64 columns of X, transposed (xt).
+//
+// Tiles pass through LDS; every element is read and written once, in 16-byte
+// pieces of at least 128 contiguous bytes.
 template <int WT>
-__global__ void __launch_bounds__(256) glu_dact_kernel(const uint16_t* dH, int64_t lddh, const uint16_t* G,
-                                                       const uint16_t* U, int64_t ldp, int64_t T, int64_t R,
-                                                       int64_t Rp, uint16_t* d, int64_t ldd, uint16_t* dt, int64_t Tp,
-                                                       int act, bool vec) {
+__device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   // pitch 66 halves: eight pieces of a row (8 rows apart here) and eight
   // tokens fall on different banks
-  __shared__ __attribute__((aligned(16))) uint16_t tile[2][64][66];
-  const int64_t t0 = (int64_t)blockIdx.x * 64, r0 = (int64_t)blockIdx.y * 64;
+  uint16_t(*tile)[64][66] = reinterpret_cast<uint16_t(*)[64][66]>(lds);
+  const int64_t tt = (a.T + 63) / 64;
+  const int64_t t0 = (b % tt) * 64, r0 = (b / tt) * 64;
   for (int q = threadIdx.x; q < 512; q += 256) {
     const int tl = q >> 3, rl = (q & 7) * 8;
     const int64_t t = t0 + tl, r = r0 + rl;
     uint32_t og[4] = {0u, 0u, 0u, 0u}, ou[4] = {0u, 0u, 0u, 0u};
-    if (t < T && r < R) {
+    if (t < a.T && r < a.g.R) {
       float h[8], g[8], u[8];
-      load8<WT>(dH + t * lddh, r, R, vec, h);
-      load8<WT>(G + t * ldp, r, R, vec, g);
-      load8<WT>(U + t * ldp, r, R, vec, u);
+      load8<WT>(a.dH + t * a.lddh, r, a.g.R, a.vec_h, h);
+      load8<WT>(a.G + t * a.ldp, r, a.g.R, a.vec_h, g);
+      load8<WT>(a.U + t * a.ldp, r, a.g.R, a.vec_h, u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float dg[2], du[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y, dy;
-          glu_act_slope(act, g[2 * i + e], y, dy);
-          const bool in = r + 2 * i + e < R;
+          glu_act_slope(a.act, g[2 * i + e], y, dy);
+          const bool in = r + 2 * i + e < a.g.R;
           dg[e] = in ? h[2 * i + e] * u[2 * i + e] * dy : 0.f;
           du[e] = in ? h[2 * i + e] * y : 0.f;
         }
@@ -143,11 +147,12 @@ __global__ void __launch_bounds__(256) glu_dact_kernel(const uint16_t* dH, int64
         ou[i] = pack_16x2<WT>(du[0], du[1]);
       }
     }
-    if (d && t < T) {
-      *reinterpret_cast<v4i*>(d + t * ldd + r) = v4i{(int)og[0], (int)og[1], (int)og[2], (int)og[3]};
-      *reinterpret_cast<v4i*>(d + t * ldd + Rp + r) = v4i{(int)ou[0], (int)ou[1], (int)ou[2], (int)ou[3]};
+    if (a.d && t < a.T) {
+      uint16_t* d = a.d + t * (2 * a.Rp) + r;
+      *reinterpret_cast<v4i*>(d) = v4i{(int)og[0], (int)og[1], (int)og[2], (int)og[3]};
+      *reinterpret_cast<v4i*>(d + a.Rp) = v4i{(int)ou[0], (int)ou[1], (int)ou[2], (int)ou[3]};
     }
-    if (dt) {
+    if (a.dt) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         tile[0][rl + e][tl] = (uint16_t)(og[e >> 1] >> (16 * (e & 1)));
@@ -155,16 +160,98 @@ __global__ void __launch_bounds__(256) glu_dact_kernel(const uint16_t* dH, int64
       }
     }
   }
-  if (!dt) return;
+  if (!a.dt) return;
   __syncthreads();
   for (int q = threadIdx.x; q < 1024; q += 256) {
     const int w = q >> 9, rl = (q >> 3) & 63, tl = (q & 7) * 8;
-    if (r0 + rl < R) {
+    if (r0 + rl < a.g.R) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[w][rl][tl]);
-      *reinterpret_cast<v4i*>(dt + ((int64_t)w * R + r0 + rl) * Tp + t0 + tl) =
+      *reinterpret_cast<v4i*>(a.dt + ((int64_t)w * a.g.R + r0 + rl) * a.Tp + t0 + tl) =
           v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
     }
   }
+}
+
+__device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, uint16_t* lds) {
+  // pitch 130 halves: the four 16-column runs of a packed row and its block's
+  // sixteen rows fall on different banks
+  uint16_t(*tile)[130] = reinterpret_cast<uint16_t(*)[130]>(lds);
+  const Geometry& g = a.g;
+  const int64_t rt = (g.R + 127) / 128;
+  const int w = b >= rt * g.nKB;
+  b -= w * rt * g.nKB;
+  const int64_t kb = b % g.nKB, r0 = (b / g.nKB) * 128;
+  const uint8_t* values = w ? a.values[1] : a.values[0];
+  const uint8_t* meta = w ? a.meta[1] : a.meta[0];
+  uint8_t* mask = w ? a.mask[1] : a.mask[0];
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int rl = 16 * (2 * (threadIdx.x >> 6) + it) + (lane >> 2), cl = (lane & 3) * 16;
+    const int64_t r = r0 + rl;
+    uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (r < g.R) {
+      const uint32_t keep = expand16(g, values, meta, r, kb * 64 + cl, o);
+      if (mask) *reinterpret_cast<uint16_t*>(mask + r * (g.nKB * 8) + kb * 8 + cl / 8) = (uint16_t)keep;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) tile[cl + e][rl] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+  }
+  if (!a.wt) return;
+  __syncthreads();
+  for (int q = threadIdx.x; q < 1024; q += 256) {
+    const int kl = q >> 4, rl = (q & 15) * 8;
+    if (kb * 64 + kl < g.K && r0 + rl < a.Rp) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][rl]);
+      *reinterpret_cast<v4i*>(a.wt + (kb * 64 + kl) * (2 * a.Rp) + w * a.Rp + r0 + rl) =
+          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+    }
+  }
+}
+
+__device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, uint16_t* lds) {
+  uint16_t(*tile)[66] = reinterpret_cast<uint16_t(*)[66]>(lds);
+  const int64_t tt = a.Tp / 64, K = a.g.K;
+  const int64_t t0 = (b % tt) * 64, k0 = (b / tt) * 64;
+  for (int q = threadIdx.x; q < 512; q += 256) {
+    const int tl = q >> 3, kl = (q & 7) * 8;
+    const int64_t t = t0 + tl, k = k0 + kl;
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (t < a.T) {
+      const uint16_t* x = a.X + t * a.ldx + k;
+      if (a.vec_x && k + 8 <= K) {
+        const v4i v = *reinterpret_cast<const v4i*>(x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = (uint32_t)v[i];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k + e < K) o[e >> 1] |= (uint32_t)x[e] << (16 * (e & 1));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[kl + e][tl] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+  }
+  __syncthreads();
+  for (int q = threadIdx.x; q < 512; q += 256) {
+    const int kl = q >> 3, tl = (q & 7) * 8;
+    if (k0 + kl < K) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][tl]);
+      *reinterpret_cast<v4i*>(a.xt + (k0 + kl) * a.Tp + t0 + tl) =
+          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+    }
+  }
+}
+
+template <int WT>
+__global__ void __launch_bounds__(256) glu_prepare_kernel(PrepareArgs a, int64_t n_act, int64_t n_weight) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 64 * 66];
+  static_assert(2 * 64 * 66 >= 64 * 130, "the weight tile fits");
+  int64_t b = blockIdx.x;
+  if (b < n_act) return prepare_dact<WT>(a, b, lds);
+  b -= n_act;
+  if (b < n_weight) return prepare_weight(a, b, lds);
+  prepare_tokens(a, b - n_weight, lds);
 }
 
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_t ldx, int64_t T, int64_t K,
@@ -182,35 +269,24 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_
 
 }  // namespace
 
-hipError_t launch_expand_dense(const Geometry& g, const uint8_t* values, const uint8_t* meta, uint16_t* dense,
-                               hipStream_t s) {
-  const int64_t n = g.R * g.nKB * 8;
-  hipLaunchKernelGGL(expand_dense_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, g, values, meta, dense);
+hipError_t launch_expand_dense(const Geometry& g, const DenseArgs& a, hipStream_t s) {
+  const int64_t n = g.nRB * g.nKB;
+  hipLaunchKernelGGL(expand_dense_kernel, dim3((unsigned)((n + 3) / 4), 2), dim3(256), 0, s, g, a);
   return hipGetLastError();
 }
 
-hipError_t launch_expand_transposed(const Geometry& g, const uint8_t* values, const uint8_t* meta, uint16_t* dt,
-                                    int64_t ldt, uint8_t* mask, hipStream_t s) {
-  hipLaunchKernelGGL(expand_transposed_kernel, dim3((unsigned)g.nKB, (unsigned)((g.R + 63) / 64)), dim3(256), 0, s, g,
-                     values, meta, dt, ldt, mask);
-  return hipGetLastError();
-}
-
-hipError_t launch_glu_dact(const void* dH, int64_t ldh, const void* G, const void* U, int64_t ldp, int64_t T,
-                           int64_t R, int64_t Rp, void* d, int64_t ldd, void* dt, int64_t Tp, int act, int wdt,
-                           hipStream_t s) {
-  const bool vec = ldh % 8 == 0 && ldp % 8 == 0 && (uintptr_t)dH % 16 == 0 && (uintptr_t)G % 16 == 0 &&
-                   (uintptr_t)U % 16 == 0;
-  const dim3 grid((unsigned)((T + 63) / 64), (unsigned)(Rp / 64));
-  auto h = static_cast<const uint16_t*>(dH);
-  auto g = static_cast<const uint16_t*>(G);
-  auto u = static_cast<const uint16_t*>(U);
+hipError_t launch_glu_prepare(PrepareArgs a, int wdt, hipStream_t s) {
+  a.vec_h = a.lddh % 8 == 0 && a.ldp % 8 == 0 && (uintptr_t)a.dH % 16 == 0 && (uintptr_t)a.G % 16 == 0 &&
+            (uintptr_t)a.U % 16 == 0;
+  a.vec_x = a.ldx % 8 == 0 && (uintptr_t)a.X % 16 == 0;
+  const int64_t n_act = (a.T + 63) / 64 * (a.Rp / 64);
+  const int64_t n_weight = 2 * ((a.g.R + 127) / 128) * a.g.nKB;
+  const int64_t n_x = a.xt ? a.Tp / 64 * a.g.nKB : 0;
+  const dim3 grid((unsigned)(n_act + n_weight + n_x));
   if (wdt == NM_F16)
-    hipLaunchKernelGGL((glu_dact_kernel<NM_F16>), grid, dim3(256), 0, s, h, ldh, g, u, ldp, T, R, Rp,
-                       static_cast<uint16_t*>(d), ldd, static_cast<uint16_t*>(dt), Tp, act, vec);
+    hipLaunchKernelGGL((glu_prepare_kernel<NM_F16>), grid, dim3(256), 0, s, a, n_act, n_weight);
   else
-    hipLaunchKernelGGL((glu_dact_kernel<NM_BF16>), grid, dim3(256), 0, s, h, ldh, g, u, ldp, T, R, Rp,
-                       static_cast<uint16_t*>(d), ldd, static_cast<uint16_t*>(dt), Tp, act, vec);
+    hipLaunchKernelGGL((glu_prepare_kernel<NM_BF16>), grid, dim3(256), 0, s, a, n_act, n_weight);
   return hipGetLastError();
 }
 

@@ -24,16 +24,18 @@ def _glu(g=None, u=None, X=P[0], ldx=128, T=5, H=P[1], ldh=48, act=2, G=None, U=
 
 def test_glu_refusals():
     L = nm.lib()
+    # a 4:8 weight and more than a few tokens: dense copies in the workspace
+    dense = dict(T=65, g=_w(N=4, M=8), u=_w(N=4, M=8))
     assert L.nm_glu(None, None, P[0], 128, 5, P[1], 48, 2, None, None, 0, None, 0, None) == EINVAL
     for kw in (dict(X=None), dict(H=None), dict(T=0), dict(T=-3), dict(ldx=127), dict(ldh=47), dict(G=P[3], ldp=48),
                dict(U=P[3], ldp=48), dict(G=P[3], U=P[4], ldp=47), dict(u=_w(R=49)), dict(u=_w(K=132)),
                dict(u=_w(N=1)), dict(u=_w(N=4, M=8)), dict(u=_w(dt=nm.NM_BF16)), dict(g=_w(format_version=0)),
                dict(u=_w(format_version=9)), dict(g=_w(values_bytes=7)), dict(u=_w(meta=None)),
-               dict(T=65, ws=None), dict(T=65, wsb=1000), dict(X=P[0] + 2, ws=None)):
+               dict(**dense, ws=None), dict(**dense, wsb=1000), dict(X=P[0] + 2, ws=None)):
         assert _glu(**kw) == EINVAL, kw
     i8 = dict(dt=nm.NM_I8)
     for kw in (dict(g=_w(**i8), u=_w(**i8)), dict(act=0), dict(act=3), dict(X=P[0] + 1), dict(H=P[1] + 1),
-               dict(G=P[3] + 1, U=P[4], ldp=48), dict(T=65, ws=P[2] + 16), dict(T=(1 << 30) + 1)):
+               dict(G=P[3] + 1, U=P[4], ldp=48), dict(**dense, ws=P[2] + 16), dict(T=(1 << 30) + 1)):
         assert _glu(**kw) == EUNSUP, kw
     big = dict(R=16, K=1 << 22)
     assert _glu(g=_w(**big), u=_w(**big), ldx=1 << 22) == EUNSUP
