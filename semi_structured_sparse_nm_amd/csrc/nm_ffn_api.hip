@@ -147,7 +147,8 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
   }
   const int xeb = xq ? 2 : nm::dtype_bytes(xdt);
   // up to 16 tokens in whole 16-byte pieces are quantised inside the product
-  const bool in_registers = !xq && T <= 16 && aligned(X, 16) && ldx * xeb % 16 == 0 && K * xeb % 16 == 0;
+  const bool in_registers =
+      !xq && T <= 16 && aligned(X, 16) && ldx * xeb % 16 == 0 && K * xeb % 16 == 0 && row_ok(ldx * xeb);
   const bool few = T <= kFewTokens;
   const nm::TilePlan plan = few ? nm::TilePlan{} : mx_plan(glu, T, R, K);
   const size_t quant = xq || in_registers ? 0 : mx_ws(T, K);
