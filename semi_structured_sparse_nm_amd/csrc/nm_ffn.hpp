@@ -91,6 +91,8 @@ struct GluArgs {
 hipError_t launch_glu_decode(const GluArgs& a, hipStream_t s);
 // more tokens, both weights 2:4: the sparse tile product
 hipError_t launch_glu_tile24(const GluArgs& a, hipStream_t s);
+// its time in microseconds by the model its tile shape is chosen with
+double glu_tile24_time(int64_t T, int64_t R, int64_t nslab, int cus, int* shape);
 
 // Both packed weights -> dense [R][Kp] (Kp = K rounded up to 64, zero filled).
 struct DenseArgs {

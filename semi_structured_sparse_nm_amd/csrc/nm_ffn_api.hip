@@ -70,12 +70,42 @@ bool rows_direct(const void* X, int64_t ldx, int64_t K) {
   return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
 }
 
-// whether the call multiplies dense copies of the weights: neither streamed
-// for few tokens nor fed to the sparse tile product
-bool glu_dense(const Geometry& g, int64_t T) { return T > kFewTokens && !(g.N == 2 && g.M == 4); }
+// How a call multiplies.
+enum GluPath {
+  GLU_STREAM,   // few tokens: the packed weights streamed past each 16 to 64 of them
+  GLU_SPARSE,   // 2:4: the sparse tile product
+  GLU_REPACK,   // 1:4, 1:8, 2:8: re-packed to 2:4 in the workspace, then the same
+  GLU_DENSE     // others: dense copies in the workspace, the dense tile product
+};
+
+GluPath glu_path(const Geometry& g, int64_t T) {
+  if (g.N == 2 && g.M == 4) {
+    // Streaming re-reads the tokens for every 16 outputs, out of the caches at
+    // about 9.5 TB/s; the weights come at 5.8.  Measured, streamed and sparse
+    // tiles: 11008 x 4096 19 and 23 us (1 token), 24 and 23 (16), 59 and 26
+    // (64); 4096 x 4096 12 and 21 (16), 21 and 21 (64).
+    if (T > kFewTokens) return GLU_SPARSE;
+    const double stream =
+        2.0 + 2.0 * (double)(g.values_bytes() + g.meta_bytes()) / 5.8e6 + (double)(g.nRB * T * g.K * 2) / 9.5e6;
+    return stream <= nm::glu_tile24_time(T, g.R, g.nKB, nm::device_cu_count(), nullptr) ? GLU_STREAM : GLU_SPARSE;
+  }
+  if (T <= kFewTokens) return GLU_STREAM;
+  return nm::repack24_supported(g) ? GLU_REPACK : GLU_DENSE;
+}
+
+Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g.eb); }
+// a weight re-packed to 2:4: values, then positions
+size_t repacked_bytes(const Geometry& g) {
+  const Geometry d = geometry24(g);
+  return up256(d.values_bytes()) + up256(d.meta_bytes());
+}
 
 size_t padded_bytes(const Geometry& g, int64_t T) { return up256((size_t)(T * up64(g.K) * 2)); }
 size_t dense_bytes(const Geometry& g) { return up256((size_t)(g.R * up64(g.K) * 2)); }
+// workspace for both weights' copies
+size_t weights_bytes(const Geometry& g, GluPath path) {
+  return path == GLU_DENSE ? 2 * dense_bytes(g) : path == GLU_REPACK ? 2 * repacked_bytes(g) : 0;
+}
 
 struct BackwardPlan {
   int64_t Rp, Tp, Kp;
@@ -221,7 +251,7 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int6
   const nm_status st = check_pair(gate, up, &g);
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
-  *bytes = padded_bytes(g, T) + (glu_dense(g, T) ? 2 * dense_bytes(g) : 0);
+  *bytes = padded_bytes(g, T) + weights_bytes(g, glu_path(g, T));
   return NM_OK;
 }
 
@@ -238,9 +268,9 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
   if (!aligned(Xt, 2) || !aligned(Ht, 2) || (G && (!aligned(G, 2) || !aligned(U, 2)))) return NM_EUNSUPPORTED;
   const bool direct = rows_direct(Xt, ldx, g.K);
-  const bool few = T <= kFewTokens, dense = glu_dense(g, T);
+  const GluPath path = glu_path(g, T);
   const size_t pad = direct ? 0 : padded_bytes(g, T);
-  const size_t need = pad + (dense ? 2 * dense_bytes(g) : 0);
+  const size_t need = pad + weights_bytes(g, path);
   if (need && (!workspace || workspace_bytes < need)) return NM_EINVAL;
   if (need && !aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -254,7 +284,7 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
     X = ws;
   }
   const nm_packed* w[2] = {gate, up};
-  if (!dense) {
+  if (path != GLU_DENSE) {
     nm::GluArgs a{};
     a.g = g;
     a.wdt = gate->dtype;
@@ -271,9 +301,21 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
     a.P[1] = U;
     a.ldp = ldp;
     a.act = act;
+    if (path == GLU_REPACK) {
+      const Geometry d = geometry24(g);
+      for (int i = 0; i < 2; ++i) {
+        uint8_t* v = ws + pad + i * repacked_bytes(g);
+        uint8_t* m = v + up256(d.values_bytes());
+        if (nm::launch_repack24(g, a.values[i], a.meta[i], d, v, m, s) != hipSuccess) return NM_EHIP;
+        a.values[i] = v;
+        a.meta[i] = m;
+      }
+      a.g = d;
+    }
     // a padded row is all 16-byte pieces: its zeros may be read
     if (!direct) a.g.K = ld;
-    return (few ? nm::launch_glu_decode(a, s) : nm::launch_glu_tile24(a, s)) == hipSuccess ? NM_OK : NM_EHIP;
+    return (path == GLU_STREAM ? nm::launch_glu_decode(a, s) : nm::launch_glu_tile24(a, s)) == hipSuccess ? NM_OK
+                                                                                                          : NM_EHIP;
   }
   nm::TileArgs a{};
   const int64_t Kp = up64(g.K);

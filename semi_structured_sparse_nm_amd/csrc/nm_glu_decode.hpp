@@ -9,6 +9,13 @@
 // (every workgroup reads the same rows).  2:4 windows go to the sparse matrix
 // instruction as they are; other patterns are expanded in registers for the
 // dense one.  The waves' sums meet in LDS, added in wave order.
+//
+// Expansion of 1 to 4 kept of 8: the kept values of a group are at most two
+// registers, so each of its four dense registers is one byte permute of them.
+// The permutes' selectors depend only on which columns are kept: a table in
+// LDS, 16 bytes for each of the 256 sets of columns, read by the set's bits.
+// (Shifting each value to its place takes about three times the vector
+// instructions, which bound the call: 4:8, 16 tokens, 11008 x 4096 31 us.)
 #pragma once
 
 #include "nm_expand.hpp"
@@ -42,6 +49,7 @@ template <int WT, int N, int M>
 struct GluFrag {
   typedef Run<WT, N, M> RunT;
   static constexpr bool SPARSE = N == 2 && M == 4;
+  static constexpr bool TABLE = M == 8 && N <= 4;
   uint32_t vd[RunT::VD];
   uint64_t mb;
   __device__ __forceinline__ void load(const uint8_t* values, const uint8_t* meta, int64_t blk, int li, int lg) {
@@ -69,9 +77,44 @@ struct GluFrag {
       }
     }
   }
+  // group q (of the lane's two) of eight columns, expanded
+  __device__ __forceinline__ v4i group(int q, const v4i* table) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    uint32_t set = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) set |= 1u << ((uint32_t)(mb >> (3 * (q * N + j))) & 7u);
+    // the group's kept values: halves q N .. + N - 1 of the run
+    uint32_t lo, hi = 0;
+    if constexpr (N == 4) {
+      lo = vd[2 * q];
+      hi = vd[2 * q + 1];
+    } else if constexpr (N == 3) {
+      lo = q ? (uint32_t)__builtin_amdgcn_alignbit(vd[2], vd[1], 16) : vd[0];
+      hi = q ? vd[2] >> 16 : vd[1];
+    } else if constexpr (N == 2) {
+      lo = vd[q];
+    } else {
+      lo = vd[0] >> (16 * q);
+    }
+    const v4i sel = table[set];
+    v4i o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[i]);
+    return o;
+#else
+    return v4i{};
+#endif
+  }
   // x: the lane's 16 activations, as the two 16-byte pieces the product wants
-  __device__ __forceinline__ v4f mul(v4i x0, v4i x1, v4f c) const {
-    if constexpr (SPARSE) {
+  __device__ __forceinline__ v4f mul(v4i x0, v4i x1, v4f c, const v4i* table) const {
+    if constexpr (TABLE) {
+#if defined(__HIP_DEVICE_COMPILE__)
+      c = mfma_dense<WT>(group(0, table), x0, c);
+      return mfma_dense<WT>(group(1, table), x1, c);
+#else
+      return c;
+#endif
+    } else if constexpr (SPARSE) {
       const v4i a = {(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
       return smfmac24<WT>(a, v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]}, c, (int)mb);
     } else {
@@ -94,7 +137,25 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = kGluWaves;
   constexpr int U = NT == 1 ? 4 : 2;
+  typedef GluFrag<WT, N, M> Frag;
   __shared__ __attribute__((aligned(16))) v4f red[NW][2 * NT][64];
+  __shared__ __attribute__((aligned(16))) v4i table[Frag::TABLE ? 256 : 1];
+  if constexpr (Frag::TABLE) {
+    // column c of set s: bytes 2 k, 2 k + 1 of the kept values where it is
+    // the set's k-th (from 0), else zeros (selector 12)
+    for (int q = threadIdx.x; q < 1024; q += NW * 64) {
+      const int s = q >> 2, c = 2 * (q & 3);
+      uint32_t sel = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = __builtin_popcount(s & ((1 << (c + e)) - 1));
+        const uint32_t b = (s >> (c + e) & 1) && k < 4 ? (uint32_t)((2 * k + 1) << 8 | 2 * k) : 0x0C0Cu;
+        sel |= b << (16 * e);
+      }
+      reinterpret_cast<uint32_t*>(table)[q] = sel;
+    }
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lg = lane >> 4;
@@ -102,7 +163,6 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
   const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
   const int nKB = (int)a.g.nKB;
   const int K = (int)a.g.K;
-  typedef GluFrag<WT, N, M> Frag;
 
   const uint16_t* xr[NT];
   bool xv[NT];
@@ -138,8 +198,8 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
       if (b0 + NW * i < nKB) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          ag[j] = fg[i].mul(x[i][j][0], x[i][j][1], ag[j]);
-          au[j] = fu[i].mul(x[i][j][0], x[i][j][1], au[j]);
+          ag[j] = fg[i].mul(x[i][j][0], x[i][j][1], ag[j], table);
+          au[j] = fu[i].mul(x[i][j][0], x[i][j][1], au[j], table);
         }
       }
     }

@@ -3,6 +3,49 @@
 
 namespace nm {
 
+namespace {
+
+// Tile shapes (tokens x outputs), with the microseconds a slab and, besides, a
+// tile takes.  Measured at K = 4096 (64 slabs), one tile on every compute
+// unit, and the least of rounds times (slabs x first + second) picks the
+// fastest or is within 10% of it for 11008 and 4096 outputs and 32 to 2048
+// tokens: e.g. 11008 outputs, 64 tokens 26 us (128 x 128: 39), 128 tokens 33
+// (64 x 64: 44), 256 tokens 44 (256 x 128: 58), 512 tokens 62 (128 x 128: 85).
+struct Shape24 {
+  int tokens, outputs;
+  double slab, tile;
+};
+constexpr Shape24 kShapes24[4] = {{256, 128, 1.0, 5.0}, {128, 128, 0.55, 5.0}, {128, 64, 0.40, 5.0}, {64, 64, 0.31, 5.0}};
+
+double shape24_time(const Shape24& h, int64_t T, int64_t R, int64_t nslab, int cus) {
+  const int64_t tiles = (T + h.tokens - 1) / h.tokens * ((R + h.outputs - 1) / h.outputs);
+  return (double)((tiles + cus - 1) / cus) * (nslab * h.slab + h.tile);
+}
+
+template <int WT>
+hipError_t launch_shape24(int shape, const Tile24Args& p, hipStream_t s) {
+  switch (shape) {
+    case 0: return launch_tile24_cfg<WT, 4, 4, 3>(p, s);
+    case 1: return launch_tile24_cfg<WT, 2, 4, 4>(p, s);
+    case 2: return launch_tile24_cfg<WT, 2, 2, 6>(p, s);
+    default: return launch_tile24_cfg<WT, 1, 2, 8>(p, s);
+  }
+}
+
+}  // namespace
+
+double glu_tile24_time(int64_t T, int64_t R, int64_t nslab, int cus, int* shape) {
+  double best = 0;
+  for (int i = 0; i < 4; ++i) {
+    const double t = shape24_time(kShapes24[i], T, R, nslab, cus);
+    if (i == 0 || t < best) {
+      best = t;
+      if (shape) *shape = i;
+    }
+  }
+  return best;
+}
+
 // tokens in X's own rows (a.X, a.ldx: 16-byte pieces), both weights 2:4
 hipError_t launch_glu_tile24(const GluArgs& g, hipStream_t s) {
   Tile24Args p{};
@@ -26,14 +69,9 @@ hipError_t launch_glu_tile24(const GluArgs& g, hipStream_t s) {
     p.values[i] = g.values[i];
     p.meta[i] = g.meta[i];
   }
-  // fewer tokens a tile where 256 of them would leave compute units idle
-  const int64_t nt = (g.g.R + 127) / 128;
-  const int cus = device_cu_count();
-  auto rounds = [&](int bm) { return ((g.T + bm - 1) / bm * nt + cus - 1) / cus; };
-  const bool wide = rounds(256) * 1.0 <= rounds(128) * 0.62;
-  if (g.wdt == NM_F16)
-    return wide ? launch_tile24_cfg<NM_F16, 4, 3>(p, s) : launch_tile24_cfg<NM_F16, 2, 4>(p, s);
-  return wide ? launch_tile24_cfg<NM_BF16, 4, 3>(p, s) : launch_tile24_cfg<NM_BF16, 2, 4>(p, s);
+  int shape = 0;
+  glu_tile24_time(g.T, g.g.R, a.nslab, device_cu_count(), &shape);
+  return g.wdt == NM_F16 ? launch_shape24<NM_F16>(shape, p, s) : launch_shape24<NM_BF16>(shape, p, s);
 }
 
 }  // namespace nm

@@ -50,16 +50,20 @@ struct Tile24Args {
   const uint8_t* meta[2];
 };
 
-// TM: 16-token tiles of a wave; four waves along the tokens, two along the outputs
-template <int WT, int TM, int NS>
+// TM: 16-token tiles of a wave, H: its 16-output tiles; four waves along the
+// tokens, two along the outputs
+template <int WT, int TM, int H, int NS>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 tile24_kernel(Tile24Args p, TileList list) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int NW = 8, BM = 64 * TM, H = 4, TN = 2 * H, BNO = 128;
-  constexpr int XB = BM * 128, VB = 16 * 1024, MB = 16 * 128;
+  constexpr int NW = 8, BM = 64 * TM, TN = 2 * H, BNO = 32 * H;
+  constexpr int NB = 4 * H;                             // blocks of a stage: per wave column H gate, then H up
+  constexpr int XB = BM * 128, VB = NB * 1024, MB = NB * 128;
   constexpr int STAGE = XB + VB + MB;
   constexpr int NLX = BM / 8 / NW;                      // token loads of a wave per slab
-  constexpr int NLT = NLX + 3;                          // and two value blocks, one pair of position blocks
+  constexpr int NLV = NB / NW;                          // value blocks of a wave
+  constexpr int NLT = NLX + NLV + 1;                    // and a pair of position blocks
+  static_assert(NB % NW == 0 && NB >= 8, "whole blocks per wave");
   constexpr int AHEAD = NLT * (NS - 2);
   static_assert(NS * STAGE <= 160 * 1024 && AHEAD < 64, "LDS, vmcnt");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
@@ -75,15 +79,17 @@ tile24_kernel(Tile24Args p, TileList list) {
   TileWalk walk(list);
   if (walk.count <= 0) return;
 
-  // ---- loads.  Tokens: load d = w + 8 j fills LDS rows 8 d .. + 7.  Blocks:
-  // wave w brings blocks 2 w, 2 w + 1 of the stage: outputs 64 (w / 4) + 32
-  // (w % 2) .. + 31 of the gate (w % 4 < 2) or up weight.
+  // ---- loads.  Tokens: load d = w + 8 j fills LDS rows 8 d .. + 7.  Block b
+  // of a stage: wave column b / (2 H), weight b % (2 H) / H, row block b % H of
+  // that column's H.  Wave w brings value blocks NLV w .. and position blocks
+  // 2 p, 2 p + 1, p = w modulo the pairs there are.
   const int piece = (lane & 7) ^ (lane >> 3);
   const int cut = (a.ka & 7) && piece >= (a.ka & 7) ? (int)0x80000000 : 0;
-  const int up = (wave >> 1) & 1;
-  const int rbl = 4 * (wave >> 2) + 2 * (wave & 1);     // first of the wave's row blocks in the tile
+  const int bv = NLV * wave, bm = 2 * (wave % (NB / 2));
+  auto weight_of = [](int b) { return b % (2 * H) / H; };
+  auto row_of = [](int b) { return b / (2 * H) * H + b % H; };
   const int voff_v = (lane >> 2) * 64 + 16 * ((lane & 3) ^ ((lane >> 3) & 3));
-  int ck = 0, cs, ce, voff[NLX], voff_m, so_v[2];
+  int ck = 0, cs, ce, voff[NLX], voff_m, so_v[NLV];
   v4i ra, rv, rm;
   auto cursor_item = [&](int k) __attribute__((always_inline)) {
     const TileItem it = walk.item(k);
@@ -98,13 +104,14 @@ tile24_kernel(Tile24Args p, TileList list) {
       voff[j] = min(8 * (wave + NW * j) + (lane >> 3), mlast) * (int)a.lda + 16 * piece;
     });
     ra = rsrc(a.A[0], m0 * a.lda);
-    rv = rsrc(up ? p.values[1] : p.values[0], rb0 * nKB * 1024);
-    rm = rsrc(up ? p.meta[1] : p.meta[0], rb0 * nKB * 128);
+    rv = rsrc(weight_of(bv) ? p.values[1] : p.values[0], rb0 * nKB * 1024);
+    rm = rsrc(weight_of(bm) ? p.meta[1] : p.meta[0], rb0 * nKB * 128);
     // row blocks past the weights' end repeat the last one (their results are not stored)
     const int blast = (int)min(nRB - rb0, (int64_t)(BNO / 16)) - 1;
-    so_v[0] = scalar(min(rbl, blast) * nKB * 1024);
-    so_v[1] = scalar(min(rbl + 1, blast) * nKB * 1024);
-    voff_m = min(rbl + (lane >> 5), blast) * nKB * 128 + 4 * (lane & 31);
+    static_for<0, NLV>([&](auto q) {
+      so_v[decltype(q)::value] = scalar(min(row_of(bv + decltype(q)::value), blast) * nKB * 1024);
+    });
+    voff_m = min(row_of(bm + (lane >> 5)), blast) * nKB * 128 + 4 * (lane & 31);
     cs = it.s0;
     ce = it.s1;
   };
@@ -114,10 +121,10 @@ tile24_kernel(Tile24Args p, TileList list) {
     if constexpr (j < NLX) {
       const int c = cs + 1 < a.nslab ? 0 : cut;
       lds_dma16(ra, lds_addr(sp + 1024 * (wave + NW * j)), voff[j] | c, cs * 128);
-    } else if constexpr (j < NLX + 2) {
-      lds_dma16(rv, lds_addr(sp + XB + 1024 * (2 * wave + j - NLX)), voff_v, so_v[j - NLX] + cs * 1024);
+    } else if constexpr (j < NLX + NLV) {
+      lds_dma16(rv, lds_addr(sp + XB + 1024 * (bv + j - NLX)), voff_v, so_v[j - NLX] + cs * 1024);
     } else {
-      lds_dma4(rm, lds_addr(sp + XB + VB + 256 * wave), voff_m, cs * 128);
+      lds_dma4(rm, lds_addr(sp + XB + VB + 128 * bm), voff_m, cs * 128);
     }
   };
   auto advance = [&]() __attribute__((always_inline)) {
@@ -219,10 +226,10 @@ tile24_kernel(Tile24Args p, TileList list) {
 #endif
 }
 
-template <int WT, int TM, int NS>
+template <int WT, int TM, int H, int NS>
 hipError_t launch_tile24_cfg(const Tile24Args& p, hipStream_t s) {
-  const TileList list = tile_list(p.t, 64 * TM, 128);
-  hipLaunchKernelGGL((tile24_kernel<WT, TM, NS>), dim3((unsigned)list.grid), dim3(512), 0, s, p, list);
+  const TileList list = tile_list(p.t, 64 * TM, 32 * H);
+  hipLaunchKernelGGL((tile24_kernel<WT, TM, H, NS>), dim3((unsigned)list.grid), dim3(512), 0, s, p, list);
   return hipGetLastError();
 }
 
