@@ -730,9 +730,7 @@ def mx_quantize(X: torch.Tensor) -> Mx:
     ldx = _row_pitch("X", X, rows, K)
     dev = _one_gpu("X", X)
     c, s = mx_size(rows, K)
-    # one allocation for both buffers (the codes' size is a multiple of 128)
-    both = X.new_empty((c + s,), dtype=torch.uint8)
-    m = Mx(rows, K, both[:c], both[c:])
+    m = Mx(rows, K, X.new_empty((c,), dtype=torch.uint8), X.new_empty((s,), dtype=torch.uint8))
     _call(dev, lib().nm_mx_quantize, "nm_mx_quantize", X.data_ptr(), ldx, xdt, _descriptor(m))
     return m
 

@@ -57,12 +57,12 @@ struct TileArgs {
 // Element types of the tile kernel's operands.
 enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2 };
 
-// Tile shape (0: 256 x 256, 1: 128 x 256, 2: 128 x 128) and slices of the
-// reduction for one product, by a model of its time.
+// Tile shape (0: 256 x 256, 1: 128 x 256, 2: 128 x 128, 3: 64 x 128) and slices
+// of the reduction for one product, by a model of its time.
 struct TilePlan {
   int shape, split, sps;
 };
-TilePlan plan_tile(TileOp op, int64_t Mr, int64_t Nr, int nslab, int batch, int ebytes_out, int cus);
+TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int batch, int cus);
 int device_cu_count();
 // C[t][r] = act(sum over the slices + bias[r]), part [split][T][R] binary32
 hipError_t launch_tile_reduce(const float* part, int split, int64_t T, int64_t R, const float* bias, int act, void* C,

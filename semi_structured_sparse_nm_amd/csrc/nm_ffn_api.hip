@@ -121,8 +121,8 @@ struct BackwardPlan {
     wt = up256((size_t)(g.K * 2 * Rp * 2));
     mask = up256((size_t)(g.R * Kp / 8));
     const int cus = nm::device_cu_count();
-    dx = nm::plan_tile(nm::TILE_LINEAR, T, g.K, (int)(2 * Rp / 64), 1, 2, cus);
-    dw = nm::plan_tile(nm::TILE_MASKED, g.R, g.K, (int)(Tp / 64), 2, 2, cus);
+    dx = nm::plan_tile(nm::TILE_LINEAR, false, T, g.K, (int)(2 * Rp / 64), 1, cus);
+    dw = nm::plan_tile(nm::TILE_MASKED, false, g.R, g.K, (int)(Tp / 64), 2, cus);
     part = part_bytes(dx, T, g.K);
     total = d + dt + xt + wt + 2 * mask + part;
   }
@@ -144,7 +144,7 @@ bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_
 size_t mx_ws_codes(int64_t T, int64_t K) { return up256((size_t)nm::mx_codes_bytes(T, K)); }
 size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm::mx_scales_bytes(T, K)); }
 nm::TilePlan mx_plan(bool glu, int64_t T, int64_t R, int64_t K) {
-  return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), 1, 2,
+  return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), 1,
                        nm::device_cu_count());
 }
 
@@ -343,7 +343,7 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   a.ldp = ldp;
   a.act = act;
   a.batch = 1;
-  const nm::TilePlan plan = nm::plan_tile(nm::TILE_GLU, T, g.R, a.nslab, 1, 2, nm::device_cu_count());
+  const nm::TilePlan plan = nm::plan_tile(nm::TILE_GLU, false, T, g.R, a.nslab, 1, nm::device_cu_count());
   return run_tile(tile_type(gate->dtype), nm::TILE_GLU, gate->dtype, a, plan, nullptr, s) == hipSuccess ? NM_OK
                                                                                                        : NM_EHIP;
 }

@@ -312,7 +312,8 @@ hipError_t launch_tile_op(const TileArgs& a, hipStream_t s) {
   switch (a.shape) {
     case 0: return launch_tile_cfg<ET, OP, OUT, 256, 256, 4, 2, 2>(a, s);
     case 1: return launch_tile_cfg<ET, OP, OUT, 128, 256, 2, 4, 3>(a, s);
-    default: return launch_tile_cfg<ET, OP, OUT, 128, 128, 2, 2, 4>(a, s);
+    case 2: return launch_tile_cfg<ET, OP, OUT, 128, 128, 2, 2, 4>(a, s);
+    default: return launch_tile_cfg<ET, OP, OUT, 64, 128, 2, 2, 6>(a, s);
   }
 }
 

@@ -12,26 +12,40 @@ int device_cu_count() {
   return cu_count(dev);
 }
 
-TilePlan plan_tile(TileOp op, int64_t Mr, int64_t Nr, int nslab, int batch, int ebytes_out, int cus) {
+// Microseconds a slab takes with few workgroups running and with one on every
+// compute unit (their operands' traffic, and the power the matrix cores draw,
+// slow each other down), and a tile besides its slabs.  Fitted to products of
+// 64 to 2048 tokens by 768 to 22016 x 768 to 22016; the choice is within 10%
+// of the fastest shape and split there.  For example 2048 tokens, two 4:8
+// weights of 11008 x 4096, gated: 256 x 256 tiles 282 us, 128 x 256 324,
+// 128 x 128 516; 256 tokens: 99, 69 and 99; the gradient of 197 tokens through
+// 4096 x 4096: 256 x 256 160 us, 64 x 128 79, 64 x 128 in two slices 60.
+TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int batch, int cus) {
   struct Shape {
     int bm, bn;
-    double slab, tile;   // microseconds a slab and, besides, a tile takes
+    double idle[2], busy[2], tile;   // [1]: microscaled operands
   };
-  static const Shape shapes[3] = {{256, 256, 1.45, 6.0}, {128, 256, 0.95, 4.0}, {128, 128, 0.75, 3.0}};
+  static const Shape shapes[4] = {{256, 256, {0.93, 1.10}, {1.60, 1.60}, 6.0},
+                                  {128, 256, {0.47, 0.72}, {0.85, 0.97}, 5.0},
+                                  {128, 128, {0.60, 0.75}, {0.73, 0.86}, 4.0},
+                                  {64, 128, {0.33, 0.44}, {0.43, 0.47}, 3.5}};
   TilePlan best{0, 1, nslab};
   double best_t = 0;
-  for (int i = 0; i < 3; ++i) {
-    const int bn = op == TILE_GLU ? shapes[i].bn / 2 : shapes[i].bn;
-    const int64_t tiles = (Mr + shapes[i].bm - 1) / shapes[i].bm * ((Nr + bn - 1) / bn) * batch;
+  for (int i = 0; i < 4; ++i) {
+    const Shape& h = shapes[i];
+    const int bn = op == TILE_GLU ? h.bn / 2 : h.bn;
+    const int64_t tiles = (Mr + h.bm - 1) / h.bm * ((Nr + bn - 1) / bn) * batch;
     const int smax = op == TILE_LINEAR ? std::min(16, nslab) : 1;
     for (int s = 1; s <= smax; ++s) {
       const int sps = (nslab + s - 1) / s;
       const int split = (nslab + sps - 1) / sps;
       if (split != s) continue;
-      const int64_t rounds = (tiles * split + cus - 1) / cus;
-      double t = rounds * (sps * shapes[i].slab + shapes[i].tile) + 4.0;
-      // the slices' sums written and read back at about 4 TB/s, and a launch
-      if (split > 1) t += (double)Mr * Nr * (8.0 * split + ebytes_out) / 4e6 + 5.0;
+      const int64_t items = tiles * split;
+      const double load = std::min(1.0, (double)items / cus);
+      const double slab = h.idle[mx] + (h.busy[mx] - h.idle[mx]) * load;
+      double t = (double)((items + cus - 1) / cus) * (sps * slab + h.tile);
+      // the slices' sums written and read back, and a launch
+      if (split > 1) t += (double)Mr * Nr * (8.0 * split + 2.0) / 8e6 + 5.0;
       if (best_t == 0 || t < best_t) {
         best_t = t;
         best = TilePlan{i, split, sps};
