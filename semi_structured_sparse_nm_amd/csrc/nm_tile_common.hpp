@@ -154,7 +154,20 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
       }
     }
   } else {
-    const uint8_t* mask = OP == TILE_MASKED ? (it.batch ? a.mask[1] : a.mask[0]) : nullptr;
+    // the kept bits of every row and column pair (32 columns, one word: rows
+    // of the mask are padded to 64), in flight together before the first use
+    uint32_t keep[TN / 2][TM];
+    if constexpr (OP == TILE_MASKED) {
+      const uint8_t* mask = it.batch ? a.mask[1] : a.mask[0];
+#pragma unroll
+      for (int i = 0; i < TN / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          const int64_t m = m0 + 16 * j + li, n = n0 + 32 * i;
+          keep[i][j] = m < a.Mr && n < a.Nr ? *reinterpret_cast<const uint32_t*>(mask + m * a.ldm + n / 8) >> (4 * lq) : 0;
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int i = 0; i < TN; i += 2) {
       float b[2][4];
@@ -165,18 +178,6 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
           const int64_t n = n0 + 16 * (i + e) + 4 * lq + v;
           b[e][v] = OP == TILE_LINEAR && a.bias && n < a.Nr ? a.bias[n] : 0.f;
         }
-      int keep[TM][2];
-      if constexpr (OP == TILE_MASKED) {
-        // all of a column pair's kept bits in flight before the first is used
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int64_t m = m0 + 16 * j + li, n = n0 + 16 * (i + e) + 4 * lq;
-            keep[j][e] = m < a.Mr && n < a.Nr ? mask[m * a.ldm + (n >> 3)] >> (n & 4) : 0;
-          }
-        __builtin_amdgcn_sched_barrier(0);
-      }
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
         const int64_t m = m0 + 16 * j + li;
@@ -187,7 +188,7 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
           for (int v = 0; v < 4; ++v) {
             y[e][v] = acc[i + e][j][v] + b[e][v];
             if constexpr (OP == TILE_LINEAR) y[e][v] = a.act == NM_ACT_GELU ? gelu_f32(y[e][v]) : y[e][v];
-            if constexpr (OP == TILE_MASKED) y[e][v] = keep[j][e] >> v & 1 ? y[e][v] : 0.f;   // a select: NaN is masked too
+            if constexpr (OP == TILE_MASKED) y[e][v] = keep[i / 2][j] >> (16 * e + v) & 1 ? y[e][v] : 0.f;   // a select: NaN is masked too
           }
         }
         __builtin_amdgcn_sched_barrier(0);              // one output's temporaries at a time
