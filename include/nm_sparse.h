@@ -381,8 +381,11 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int6
 /*
  * H = act(X Wg^T) (.) (X Wu^T).  G, U: NULL, or both [T][ldp] buffers of the
  * weight dtype that receive the two products, rounded once, for
- * nm_glu_backward.  Weights must be finite where X is not: a pruned weight
- * multiplies as zero.  The workspace (256-byte aligned, at least
+ * nm_glu_backward.  Activations are finite: whether an infinite or NaN one
+ * reaches an output through a pruned weight depends on the path the call
+ * takes (it never reaches another token).  NM_FFN_TILE=<kind>:<shape>[:<split>]
+ * in the environment ("tile" or "tile24", shapes 0 to 3) forces a tile shape
+ * where the call takes that kind of tile product.  The workspace (256-byte aligned, at least
  * nm_glu_workspace_size bytes) is written and read back within the call's
  * stream order, so calls that share one must be ordered.
  * NM_EINVAL: null pointers (or only one of G and U), T < 1, ldx < K, ldh < R,

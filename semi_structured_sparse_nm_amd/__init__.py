@@ -499,7 +499,8 @@ def _sized(f, what: str, key: tuple, *args) -> int:
     n = _ws_sizes.get(key)
     if n is None:
         b = ctypes.c_size_t()
-        _check(f(*args, ctypes.byref(b)), what)
+        with torch.cuda.device(key[-1]):                  # the plan depends on the device
+            _check(f(*args, ctypes.byref(b)), what)
         if len(_ws_sizes) > 4096:
             _ws_sizes.clear()
         n = _ws_sizes[key] = b.value

@@ -64,6 +64,7 @@ struct TilePlan {
 };
 TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int batch, int cus);
 int device_cu_count();
+bool ffn_tile_override(const char* kind, int* shape, int* split);
 // C[t][r] = act(sum over the slices + bias[r]), part [split][T][R] binary32
 hipError_t launch_tile_reduce(const float* part, int split, int64_t T, int64_t R, const float* bias, int act, void* C,
                               int64_t ldc, int ydt, hipStream_t s);

@@ -36,6 +36,11 @@ hipError_t launch_shape24(int shape, const Tile24Args& p, hipStream_t s) {
 
 double glu_tile24_time(int64_t T, int64_t R, int64_t nslab, int cus, int* shape) {
   double best = 0;
+  int only;
+  if (ffn_tile_override("tile24", &only, nullptr)) {
+    if (shape) *shape = only;
+    return 0;
+  }
   for (int i = 0; i < 4; ++i) {
     const double t = shape24_time(kShapes24[i], T, R, nslab, cus);
     if (i == 0 || t < best) {

@@ -1,5 +1,8 @@
 // Choice of the tile product's shape and split of the reduction, and the sum
 // of a split's slices.
+#include <stdlib.h>
+#include <string.h>
+
 #include <algorithm>
 
 #include "nm_ffn.hpp"
@@ -10,6 +13,22 @@ int device_cu_count() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) dev = 0;
   return cu_count(dev);
+}
+
+// The debug override NM_FFN_TILE=<kind>:<shape>[:<split>], kind "tile" (the dense
+// tile product) or "tile24" (the sparse one): that shape, and for a product
+// that takes one that split where its slabs divide into it.  For tests.
+bool ffn_tile_override(const char* kind, int* shape, int* split) {
+  const char* e = getenv("NM_FFN_TILE");
+  if (!e) return false;
+  const char* c = strchr(e, ':');
+  if (!c || (size_t)(c - e) != strlen(kind) || strncmp(e, kind, c - e)) return false;
+  const int v = atoi(c + 1);
+  if (v < 0 || v > 3) return false;
+  *shape = v;
+  c = strchr(c + 1, ':');
+  if (c && split) *split = std::max(0, std::min(16, atoi(c + 1)));
+  return true;
 }
 
 // Microseconds a slab takes with few workgroups running and with one on every
@@ -29,17 +48,20 @@ TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int ba
                                   {128, 256, {0.47, 0.72}, {0.85, 0.97}, 5.0},
                                   {128, 128, {0.60, 0.75}, {0.73, 0.86}, 4.0},
                                   {64, 128, {0.33, 0.44}, {0.43, 0.47}, 3.5}};
+  int only = -1, only_split = 0;
+  ffn_tile_override("tile", &only, &only_split);
   TilePlan best{0, 1, nslab};
   double best_t = 0;
   for (int i = 0; i < 4; ++i) {
     const Shape& h = shapes[i];
+    if (only >= 0 && i != only) continue;
     const int bn = op == TILE_GLU ? h.bn / 2 : h.bn;
     const int64_t tiles = (Mr + h.bm - 1) / h.bm * ((Nr + bn - 1) / bn) * batch;
     const int smax = op == TILE_LINEAR ? std::min(16, nslab) : 1;
     for (int s = 1; s <= smax; ++s) {
       const int sps = (nslab + s - 1) / s;
       const int split = (nslab + sps - 1) / sps;
-      if (split != s) continue;
+      if (split != s || (only_split && op == TILE_LINEAR && s != std::min(only_split, nslab))) continue;
       const int64_t items = tiles * split;
       const double load = std::min(1.0, (double)items / cus);
       const double slab = h.idle[mx] + (h.busy[mx] - h.idle[mx]) * load;

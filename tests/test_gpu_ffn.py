@@ -154,6 +154,71 @@ def test_glu_backward_against_differences(act):
         assert abs(quot - float((grad.double() * d).sum())) <= float(lim) + 1e-6 * float(scale)
 
 
+@pytest.fixture
+def tile(monkeypatch):
+    """Forces a tile shape (and split) of the feed-forward products."""
+    def force(kind, shape, split=0):
+        monkeypatch.setenv("NM_FFN_TILE", f"{kind}:{shape}" + (f":{split}" if split else ""))
+        nm._ws_sizes.clear()
+    yield force
+    nm._ws_sizes.clear()
+
+
+# tokens, rows, columns: several tiles a workgroup, the last ragged both ways
+TILES = {0: (2100, 4200), 1: (1100, 3900), 2: (1100, 4300), 3: (700, 3700)}
+
+
+@pytest.mark.parametrize("N,M", [(2, 4), (4, 8)])
+@pytest.mark.parametrize("K", [64, 72, 456])
+@pytest.mark.parametrize("shape", [0, 1, 2, 3])
+def test_glu_tile_shapes(tile, shape, K, N, M):
+    """Every shape of the sparse and the dense tile product with more tiles
+    than compute units: one slab, a slab and a piece, several."""
+    dt = "bf16" if K == 72 else "f16"
+    T, R = TILES[shape] if (N, M) == (4, 8) else {0: (2100, 4200), 1: (1100, 4300), 2: (1100, 2300), 3: (700, 1900)}[shape]
+    pg, wg, kg = weights(R, K, N, M, dt, "g")
+    pu, wu, ku = weights(R, K, N, M, dt, "u")
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    tile("tile24" if (N, M) == (2, 4) else "tile", shape)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "silu")
+    pre = torch.full((2, T, R), 7.0, dtype=X.dtype, device="cuda")
+    check(nm.glu(pg, pu, X, pre=pre), h, eh, "H")
+    check(pre[0], g, eg, "G")
+    check(pre[1], u, eu, "U")
+
+
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("shape", [0, 1, 2, 3])
+def test_glu_backward_tile_shapes(tile, shape, split):
+    T, R, K, dt = 1100, 700, 1032, "bf16"
+    if shape == 0:
+        R, K = 2300, 2312
+    pg, wg, kg = weights(R, K, 2, 4, dt, "g")
+    pu, wu, ku = weights(R, K, 2, 4, dt, "u")
+    X, dH = normal((T, K), 1.0, dt, "X"), normal((T, R), 0.1, dt, "dH")
+    pre = normal((2 * T, R), 1.0, dt, "pre").view(2, T, R)
+    tile("tile", shape, split)
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, X, pre, dH), want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+def test_glu_offsets_past_32_bits():
+    """Outputs and activations of more than 2^32 bytes: the last rows."""
+    dt = "bf16"
+    for T, R, K in ((70000, 32768, 64), (140000, 64, 16384)):
+        pg, wg, _ = weights(R, K, 2, 4, dt, "g")
+        pu, wu, _ = weights(R, K, 2, 4, dt, "u")
+        g = torch.Generator(device="cuda")
+        g.manual_seed(T)
+        X = torch.empty(T, K, dtype=TORCH[dt], device="cuda").normal_(generator=g)
+        H = nm.glu(pg, pu, X)
+        for rows in (slice(0, 3), slice(T // 2, T // 2 + 3), slice(T - 3, T)):
+            h, _, _, eh, _, _ = _ffn.glu64(X[rows], wg, wu, "silu")
+            check(H[rows], h, eh, f"H {rows}")
+        del X, H
+
+
 def test_glu_large_tiles():
     """Enough tiles for the largest tile shape, ragged on every side."""
     T, R, K, dt = 1000, 6500, 136, "bf16"
@@ -315,6 +380,45 @@ def test_mx_glu_shapes(T, R, K, dt):
         h, _, _, eh, _, _ = _ffn.glu64(x, Wg, Wu, act)
         check(nm.mx_glu(wg, wu, X, act=act), h, eh, act)
     check(nm.mx_glu(wg, wu, nm.mx_quantize(X), act="gelu", out_dtype=torch.float32), h, eh, "quantised X")
+
+
+@pytest.mark.parametrize("K", [32, 300, 1500])
+@pytest.mark.parametrize("shape", [0, 1, 2, 3])
+def test_mx_tile_shapes(tile, shape, K):
+    """Every shape with more tiles than compute units, split and not."""
+    T, R = {0: (2100, 8300), 1: (1100, 8300), 2: (1100, 4300), 3: (700, 3700)}[shape]
+    w, W = _mx_w(R, K, "bf16")
+    X = normal((T, K), 1.0, "bf16", "X", T, K)
+    x = _ffn.mx64(X)[0]
+    y, e = x @ W.t(), _ffn.sum_err(K, x.abs() @ W.abs().t())
+    b = normal((R,), 1.0, "f32", "b", R)
+    for split in (1, 2, 5):
+        tile("tile", shape, split)
+        check(nm.mx_linear(w, X), y, e, f"Y in {split}")
+        yb = y + b.double()
+        eb = e + 2.0 ** -23 * (yb.abs() + e) * split
+        check(nm.mx_linear(w, X, bias=b, out_dtype=torch.float32), yb, eb, f"Y + b in {split}")
+    u, U = _mx_w(R, K, "bf16", "u")
+    h, _, _, eh, _, _ = _ffn.glu64(x, W, U, "silu")
+    check(nm.mx_glu(w, u, X), h, eh, "H")
+
+
+def test_mx_offsets_past_32_bits():
+    """Outputs, then quantised activations, of more than 2^32 bytes."""
+    for T, R, K in ((70000, 32768, 64), (300000, 64, 32768)):
+        w, W = _mx_w(R, K, "bf16")
+        g = torch.Generator(device="cuda")
+        g.manual_seed(T)
+        X = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+        m = nm.mx_quantize(X)
+        Y = nm.mx_linear(w, m)
+        for a in (0, T // 2, T - 3):
+            x = _ffn.mx64(X[a:a + 3])[0]
+            check(Y[a:a + 3], x @ W.t(), _ffn.sum_err(K, x.abs() @ W.abs().t()), f"Y from {a}")
+        if T == 70000:
+            y = nm.mx_dequantize(m, out_dtype=torch.bfloat16)
+            assert torch.equal(y[-3:].double(), _ffn.mx64(X[-3:])[0])
+        del X, Y, m
 
 
 def test_mx_linear_large_tiles():
