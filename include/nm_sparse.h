@@ -374,8 +374,8 @@ nm_status nm_hybrid_spmm(const nm_hybrid* w, const void* X, int64_t ldx, int64_t
  * ---------------------------------------------------------------------- */
 
 /* Device workspace nm_glu needs for these weights and T tokens (0: none),
- * for rows of any stride and alignment: dense copies of the weights, and a
- * padded copy of X, where the call takes them. */
+ * for rows of any stride and alignment: re-packed or dense copies of the
+ * weights, and a padded copy of X, where the call takes them. */
 nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes);
 
 /*
@@ -385,14 +385,15 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int6
  * reaches an output through a pruned weight depends on the path the call
  * takes (it never reaches another token).  NM_FFN_TILE=<kind>:<shape>[:<split>]
  * in the environment ("tile" or "tile24", shapes 0 to 3) forces a tile shape
- * where the call takes that kind of tile product.  The workspace (256-byte aligned, at least
- * nm_glu_workspace_size bytes) is written and read back within the call's
- * stream order, so calls that share one must be ordered.
+ * where the call takes that kind of tile product.  Outputs and workspace
+ * overlap no other buffer of the call.  The workspace (256-byte aligned, at
+ * least nm_glu_workspace_size bytes) is written and read back within the
+ * call's stream order, so calls that share one must be ordered.
  * NM_EINVAL: null pointers (or only one of G and U), T < 1, ldx < K, ldh < R,
  * ldp < R, descriptors whose sizes or versions are wrong or whose shape, N:M
  * or dtype differ, a small workspace.  NM_EUNSUPPORTED: int8 weights, act not
  * listed, pointers not aligned to their element, a workspace not 256-byte
- * aligned, rows so long that 256 of them pass 2^31 bytes.
+ * aligned, rows of K so long that 256 of them pass 2^31 bytes, T > 2^25.
  */
 nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
                  int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, void* workspace,
@@ -414,7 +415,8 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
  * as operands of the matrix instruction; sums are binary32 and every output
  * is rounded once.  The result does not depend on launch order (no atomics).
  * All buffers have the weight dtype.  Errors as nm_glu; NM_EINVAL also for
- * no output at all, one weight gradient without the other, lddx < K, lddw < K.
+ * no output at all, one weight gradient without the other, lddx < K, lddw < K;
+ * NM_EUNSUPPORTED also for T of 2^22 or R of 2^21 and more.
  */
 nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
                           const void* G, const void* U, int64_t ldp, const void* dH, int64_t lddh, int32_t act,
@@ -446,14 +448,15 @@ typedef struct {
   void* scales; size_t scales_bytes;
 } nm_mx;
 
-/* Sizes of the two buffers.  NM_EINVAL: null outputs, rows < 1, K < 1. */
+/* Sizes of the two buffers.  NM_EINVAL: null outputs, rows < 1, K < 1;
+ * NM_EUNSUPPORTED: rows or K above 2^25. */
 nm_status nm_mx_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes);
 
 /*
  * X [m->rows][ldx] of x_dtype (NM_F16, NM_BF16 or NM_F32) -> m's buffers.
  * Every byte of both buffers is written.  NM_EINVAL: null pointers, ldx < K,
  * buffer sizes not those of nm_mx_size; NM_EUNSUPPORTED: other types, X not
- * aligned to its element, buffers not 16-byte aligned.
+ * aligned to its element, buffers not 16-byte aligned, more than 2^24 units.
  */
 nm_status nm_mx_quantize(const void* X, int64_t ldx, int32_t x_dtype, nm_mx* m, void* stream);
 
@@ -477,7 +480,9 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
  * ldy < R, xq of other K or rows than asked, descriptors with wrong sizes or
  * versions, gate and up of other shapes, a small workspace;
  * NM_EUNSUPPORTED: other types, act not listed, misaligned pointers, rows so
- * long that 256 of them pass 2^31 bytes.
+ * long that 256 of them pass 2^31 bytes, T > 2^25.  Outputs and workspace
+ * overlap no other buffer of the call; calls that share a workspace must be
+ * ordered.
  */
 nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* bytes);
 nm_status nm_mx_linear(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,

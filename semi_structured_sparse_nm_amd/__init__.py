@@ -156,6 +156,11 @@ def pack_size(rows: int, K: int, N: int, M: int, dtype: int):
     return vb.value, mb.value
 
 
+def _fields_of(p) -> dict:
+    """What a copy or a pickle of p holds: not its cached C descriptor."""
+    return {k: v for k, v in p.__dict__.items() if k != "_c_desc"}
+
+
 @dataclass
 class Packed:
     """Packed N:M weights on the GPU (two uint8 device buffers + shape)."""
@@ -178,6 +183,9 @@ class Packed:
         else:
             d.meta, d.meta_bytes = None, 0
         return d
+
+    def __getstate__(self):
+        return _fields_of(self)
 
     @property
     def torch_dtype(self):
@@ -484,8 +492,8 @@ def _descriptor(p):
     """byref of p's C descriptor, built again whenever a field changed."""
     second = p.meta if type(p) is Packed else p.scales
     first = p.values if type(p) is Packed else p.codes
-    key = (first.data_ptr(), 0 if second is None else second.data_ptr(), first.numel(), p.rows, p.K,
-           p.format_version, (p.N, p.M, p.dtype) if type(p) is Packed else None)
+    key = (first.data_ptr(), first.numel(), (0, 0) if second is None else (second.data_ptr(), second.numel()),
+           p.rows, p.K, p.format_version, (p.N, p.M, p.dtype) if type(p) is Packed else None)
     c = p.__dict__.get("_c_desc")
     if c is None or c[0] != key:
         d = p.desc()
@@ -593,9 +601,11 @@ def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
     if pre.shape != (2, T, p.rows):
         raise ValueError(f"pre must be [2, {T}, {p.rows}], got {tuple(pre.shape)}")
     _check_dtype("pre", pre, p.torch_dtype)
-    if pre.stride(0) < (T - 1) * pre.stride(1) + p.rows:
+    ld, half = _row_pitch("pre", pre[0], T, p.rows), pre.stride(0)
+    # one half behind the other, or their rows in turn
+    if half < (T - 1) * ld + p.rows and not p.rows <= half <= ld - p.rows:
         raise ValueError("the two halves of pre overlap")
-    return _row_pitch("pre", pre[0], T, p.rows)
+    return ld
 
 
 def _glu_key(what: str, p: Packed, T: int, dev: int) -> tuple:
@@ -693,6 +703,9 @@ class Mx:
     def desc(self) -> NmMx:
         return NmMx(self.rows, self.K, self.format_version, 0, self.codes.data_ptr(), self.codes.numel(),
                     self.scales.data_ptr(), self.scales.numel())
+
+    def __getstate__(self):
+        return _fields_of(self)
 
     def nbytes(self) -> int:
         return self.codes.numel() + self.scales.numel()

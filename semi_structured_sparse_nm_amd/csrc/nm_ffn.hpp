@@ -64,6 +64,12 @@ struct TilePlan {
 };
 TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int batch, int cus);
 int device_cu_count();
+// Workgroups of `block` threads for n items, at most 2^22 (a launch has fewer
+// than 2^32 threads): kernels launched so loop over the rest.
+inline unsigned grid_1d(int64_t n, int block) {
+  const int64_t b = (n + block - 1) / block;
+  return (unsigned)(b < (1 << 22) ? b : 1 << 22);
+}
 bool ffn_tile_override(const char* kind, int* shape, int* split);
 // C[t][r] = act(sum over the slices + bias[r]), part [split][T][R] binary32
 hipError_t launch_tile_reduce(const float* part, int split, int64_t T, int64_t R, const float* bias, int act, void* C,

@@ -18,8 +18,10 @@ bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
 // beyond, the tile product shares them between tokens.
 constexpr int64_t kFewTokens = 64;
 
-// Longest dimension taken: products of two of them stay within 63 bits.
-constexpr int64_t kMaxLen = 1ll << 30;
+// Longest dimension taken, and most workgroups of 256 threads: a launch has
+// fewer than 2^32 threads.
+constexpr int64_t kMaxLen = 1ll << 25;
+constexpr int64_t kMaxGrid = 1ll << 24;
 
 // One tile product of elements `et` (TILE_*), with its plan; a split's slices
 // go to `part` (plan.split * Mr * Nr binary32) and are added afterwards.
@@ -107,6 +109,13 @@ size_t weights_bytes(const Geometry& g, GluPath path) {
   return path == GLU_DENSE ? 2 * dense_bytes(g) : path == GLU_REPACK ? 2 * repacked_bytes(g) : 0;
 }
 
+// transposed rows of T, and rows of both dG and dU, within the tile kernel's
+// offsets; the operands' tiles within one launch
+bool backward_ok(const Geometry& g, int64_t T) {
+  return row_ok(up64(T) * 2) && row_ok(up64(g.R) * 4) &&
+         up64(T) / 64 * (up64(g.R) / 64 + g.nKB) + 2 * ((g.R + 127) / 128) * g.nKB < kMaxGrid;
+}
+
 struct BackwardPlan {
   int64_t Rp, Tp, Kp;
   size_t d, dt, xt, wt, mask, part, total;   // bytes of each part (mask: of one weight)
@@ -135,7 +144,7 @@ nm_status check_mx(const nm_mx* m) {
   if ((int64_t)m->codes_bytes != nm::mx_codes_bytes(m->rows, m->K)) return NM_EINVAL;
   if ((int64_t)m->scales_bytes != nm::mx_scales_bytes(m->rows, m->K)) return NM_EINVAL;
   if (!aligned(m->codes, 16) || !aligned(m->scales, 16)) return NM_EUNSUPPORTED;
-  if ((m->rows + 31) / 32 * (nm::mx_kp(m->K) / nm::kMxSlab) >= (1ll << 31)) return NM_EUNSUPPORTED;
+  if ((m->rows + 31) / 32 * (nm::mx_kp(m->K) / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
   return NM_OK;
 }
 
@@ -173,7 +182,7 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
   } else {
     if (!X || ldx < K) return NM_EINVAL;
     if (!float_dtype(xdt) || !aligned(X, (size_t)nm::dtype_bytes(xdt))) return NM_EUNSUPPORTED;
-    if ((T + 31) / 32 * (Kp / nm::kMxSlab) >= (1ll << 31)) return NM_EUNSUPPORTED;
+    if ((T + 31) / 32 * (Kp / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
   }
   const int xeb = xq ? 2 : nm::dtype_bytes(xdt);
   // up to 16 tokens in whole 16-byte pieces are quantised inside the product
@@ -354,7 +363,7 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
   const nm_status st = check_pair(gate, up, &g);
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
-  if (!row_ok(up64(T) * 2) || !row_ok(up64(g.R) * 4)) return NM_EUNSUPPORTED;
+  if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
   *bytes = BackwardPlan(g, T).total;
   return NM_OK;
 }
@@ -375,8 +384,7 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   if (!aligned(Xt, 2) || !aligned(G, 2) || !aligned(U, 2) || !aligned(dH, 2) || !aligned(dX, 2) || !aligned(dWg, 2) ||
       !aligned(dWu, 2))
     return NM_EUNSUPPORTED;
-  // transposed rows of T, and rows of both dG and dU, within the tile kernel's offsets
-  if (!row_ok(up64(T) * 2) || !row_ok(up64(g.R) * 4)) return NM_EUNSUPPORTED;
+  if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
   const BackwardPlan p(g, T);
   if (!workspace || workspace_bytes < p.total) return NM_EINVAL;
   if (!aligned(workspace, 256)) return NM_EUNSUPPORTED;
@@ -477,7 +485,6 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
   if (st != NM_OK) return st;
   if (m->format_version != NM_FORMAT_VERSION || !Y || ldy < m->K) return NM_EINVAL;
   if (!float_dtype(y_dtype) || !aligned(Y, (size_t)nm::dtype_bytes(y_dtype))) return NM_EUNSUPPORTED;
-  if ((m->rows * ((m->K + 7) / 8) + 255) / 256 >= (1ll << 31)) return NM_EUNSUPPORTED;
   return nm::launch_mx_dequantize(static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales),
                                   m->rows, m->K, Y, ldy, y_dtype, static_cast<hipStream_t>(stream)) == hipSuccess
              ? NM_OK
@@ -489,6 +496,7 @@ nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* b
   const nm_status st = check_mx(w);
   if (st != NM_OK) return st;
   if (!row_ok(nm::mx_kp(w->K) / 2) || T > kMaxLen) return NM_EUNSUPPORTED;
+  if ((T + 31) / 32 * (nm::mx_kp(w->K) / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
   *bytes = mx_ws(T, w->K) + (T > kFewTokens ? part_bytes(mx_plan(glu != 0, T, w->rows, w->K), T, w->rows) : 0);
   return NM_OK;
 }

@@ -257,14 +257,14 @@ __global__ void __launch_bounds__(256) glu_prepare_kernel(PrepareArgs a, int64_t
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_t ldx, int64_t T, int64_t K,
                                                        uint16_t* Y, int64_t Kp) {
   const int64_t pr = Kp / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= T * pr) return;
-  const int64_t t = i / pr, k = (i - t * pr) * 8;
-  uint32_t o[4] = {0u, 0u, 0u, 0u};
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * pr; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / pr, k = (i - t * pr) * 8;
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (k + e < K) o[e >> 1] |= (uint32_t)X[t * ldx + k + e] << (16 * (e & 1));
-  *reinterpret_cast<v4i*>(Y + t * Kp + k) = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+    for (int e = 0; e < 8; ++e)
+      if (k + e < K) o[e >> 1] |= (uint32_t)X[t * ldx + k + e] << (16 * (e & 1));
+    *reinterpret_cast<v4i*>(Y + t * Kp + k) = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+  }
 }
 
 }  // namespace
@@ -292,7 +292,7 @@ hipError_t launch_glu_prepare(PrepareArgs a, int wdt, hipStream_t s) {
 
 hipError_t launch_pad_rows(const void* X, int64_t ldx, int64_t T, int64_t K, void* Y, int64_t Kp, hipStream_t s) {
   const int64_t n = T * (Kp / 8);
-  hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(grid_1d(n, 256)), dim3(256), 0, s,
                      static_cast<const uint16_t*>(X), ldx, T, K, static_cast<uint16_t*>(Y), Kp);
   return hipGetLastError();
 }

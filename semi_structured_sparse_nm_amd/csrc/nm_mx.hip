@@ -87,29 +87,29 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes
                                                             int64_t K, int64_t nslab, void* Y, int64_t ldy,
                                                             bool vec) {
   const int64_t pr = (K + 7) / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * pr) return;
-  const int64_t r = i / pr, k = (i - r * pr) * 8;
-  const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + r * (nslab * 128) + k / 2);
-  const int b = (int)(k & 255) >> 5, rl = (int)(r & 31);
-  const uint32_t byte =
-      scales[((r >> 5) * nslab + (k >> 8)) * 256 + 4 * (16 * (b & 3) + (rl & 15)) + 2 * (rl >> 4) + (b >> 2)];
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = mx_value(c >> (4 * e) & 15u, byte);
-  const int n = (int)min(K - k, (int64_t)8);
-  if constexpr (DT != NM_F32) {
-    if (vec && n == 8) {
-      uint32_t o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = pack_16x2<DT>(y[2 * e], y[2 * e + 1]);
-      *reinterpret_cast<v4i*>(static_cast<uint16_t*>(Y) + r * ldy + k) =
-          v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
-      return;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pr; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / pr, k = (i - r * pr) * 8;
+    const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + r * (nslab * 128) + k / 2);
+    const int b = (int)(k & 255) >> 5, rl = (int)(r & 31);
+    const uint32_t byte =
+        scales[((r >> 5) * nslab + (k >> 8)) * 256 + 4 * (16 * (b & 3) + (rl & 15)) + 2 * (rl >> 4) + (b >> 2)];
+    float y[8];
+  #pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = mx_value(c >> (4 * e) & 15u, byte);
+    const int n = (int)min(K - k, (int64_t)8);
+    if constexpr (DT != NM_F32) {
+      if (vec && n == 8) {
+        uint32_t o[4];
+  #pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack_16x2<DT>(y[2 * e], y[2 * e + 1]);
+        *reinterpret_cast<v4i*>(static_cast<uint16_t*>(Y) + r * ldy + k) =
+            v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+        continue;
+      }
     }
+    store4<DT>(Y, r * ldy + k, y, min(n, 4), vec);
+    if (n > 4) store4<DT>(Y, r * ldy + k + 4, y + 4, n - 4, vec);
   }
-  store4<DT>(Y, r * ldy + k, y, min(n, 4), vec);
-  if (n > 4) store4<DT>(Y, r * ldy + k + 4, y + 4, n - 4, vec);
 }
 
 }  // namespace
@@ -135,7 +135,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
   const int64_t nslab = mx_kp(K) / kMxSlab;
   const bool vec = ydt == NM_F32 ? vec4_ok(Y, ldy, 4) : (uintptr_t)Y % 16 == 0 && ldy % 8 == 0;
   const int64_t n = rows * ((K + 7) / 8);
-  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+  const dim3 grid(grid_1d(n, 256)), block(256);
   if (ydt == NM_F16)
     hipLaunchKernelGGL((mx_dequantize_kernel<NM_F16>), grid, block, 0, s, codes, scales, rows, K, nslab, Y, ldy, vec);
   else if (ydt == NM_BF16)

@@ -71,6 +71,29 @@ def test_glu_backward_refusals():
     for kw in (dict(act=0), dict(act=7), dict(ws=P[7] + 16), dict(dH=P[3] + 1), dict(dWu=P[6] + 1), dict(dX=P[4] + 1),
                dict(T=1 << 22)):
         assert _bwd(**kw) == EUNSUP, kw
+    long = dict(R=1 << 21, K=8)
+    assert _bwd(g=_w(**long), u=_w(**long), T=1, ldx=8, ldp=1 << 21, lddh=1 << 21, lddx=8, lddw=8) == EUNSUP
+    # operands' tiles past one launch
+    wide = dict(R=1 << 20, K=1 << 12)
+    assert _bwd(g=_w(**wide), u=_w(**wide), T=1 << 21, ldx=1 << 12, ldp=1 << 20, lddh=1 << 20, lddx=1 << 12,
+                lddw=1 << 12, wsb=1 << 62) == EUNSUP
+
+
+def test_lengths_past_one_launch():
+    """Sizes whose launch would pass 2^32 threads are refused."""
+    c = ctypes.c_size_t()
+    assert nm.lib().nm_mx_size(1 << 26, 8, ctypes.byref(c), ctypes.byref(c)) == EUNSUP
+    assert nm.lib().nm_mx_size(8, 1 << 26, ctypes.byref(c), ctypes.byref(c)) == EUNSUP
+    m = _mx(1 << 24, 1 << 13)
+    assert nm.lib().nm_mx_quantize(P[0], 1 << 13, nm.NM_F16, ctypes.byref(m), None) == EUNSUP
+    w = _mx(16, 1 << 13)
+    f = nm.lib().nm_mx_workspace_size
+    assert f(ctypes.byref(w), 1 << 24, 0, ctypes.byref(c)) == EUNSUP
+    assert f(ctypes.byref(w), 1 << 20, 0, ctypes.byref(c)) == nm.NM_OK
+    assert nm.lib().nm_mx_linear(ctypes.byref(w), None, P[0], 1 << 13, nm.NM_F16, 1 << 24, P[1], 16, nm.NM_F16, None,
+                                 0, P[2], 1 << 62, None) == EUNSUP
+    g = _w(R=8, K=8)
+    assert nm.lib().nm_glu_workspace_size(ctypes.byref(g), ctypes.byref(g), (1 << 25) + 1, ctypes.byref(c)) == EUNSUP
 
 
 def _mx(rows=40, K=300, **kw):

@@ -2,6 +2,8 @@
 (tests/_ffn.py, which derives the elementwise bounds): the gated block on N:M
 packed weights, its gradients, the microscaled 4-bit format, its product and
 its gated block."""
+import copy
+import pickle
 import zlib
 
 import pytest
@@ -152,6 +154,131 @@ def test_glu_backward_against_differences(act):
         lim = (d.abs() * (b + _ffn.half_step(grad.dtype) * grad.double().abs() + _ffn.tiny(grad.dtype))).sum()
         scale = (d * grad.double()).abs().sum()
         assert abs(quot - float((grad.double() * d).sum())) <= float(lim) + 1e-6 * float(scale)
+
+
+@pytest.mark.parametrize("N,M", [(2, 4), (4, 8), (1, 4), (8, 8)])
+@pytest.mark.parametrize("T", [3, 40, 90, 300])
+def test_glu_tokens_are_independent(T, N, M):
+    """Infinite and NaN activations change no other token's bits."""
+    R, K = 150, 200
+    pg, pu = weights(R, K, N, M, "bf16", "g")[0], weights(R, K, N, M, "bf16", "u")[0]
+    X = normal((T, K), 1.0, "bf16", "X", T)
+    pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+    clean = nm.glu(pg, pu, X, pre=pre).clone(), pre.clone()
+    rows = torch.ones(T, dtype=torch.bool)
+    for t, v in ((0, float("inf")), (T - 1, float("nan")), (T // 2, float("-inf"))):
+        X[t, (7 * t) % K] = v
+        rows[t] = False
+    H = nm.glu(pg, pu, X, pre=pre)
+    assert torch.equal(H[rows], clean[0][rows]) and torch.equal(pre[:, rows], clean[1][:, rows])
+    assert not bool(torch.isfinite(H[T - 1]).all())
+
+
+@pytest.mark.parametrize("N,M", [(2, 4), (3, 8), (1, 4)])
+@pytest.mark.parametrize("T", [1, 33, 130])
+def test_glu_layouts(T, N, M):
+    """Rows at odd addresses, the two products in turn by token, gradients
+    from strided operands, one token in a wide buffer."""
+    R, K, dt = 77, 130 if M == 4 else 136, "f16"
+    K = K // M * M
+    pg, wg, kg = weights(R, K, N, M, dt, "g")
+    pu, wu, ku = weights(R, K, N, M, dt, "u")
+    X = normal((T, K), 1.0, dt, "X", T, N)
+    flat = torch.full((T * (K + 9) + 1,), float("nan"), dtype=X.dtype, device="cuda")
+    xv = flat[1:].view(T, K + 9)[:, :K]
+    xv.copy_(X)
+    both = torch.empty(T, 2, R, dtype=X.dtype, device="cuda")
+    pre = both.transpose(0, 1)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "silu")
+    check(nm.glu(pg, pu, xv, pre=pre), h, eh, "H")
+    check(both[:, 0], g, eg, "G")
+    check(both[:, 1], u, eu, "U")
+    dH = normal((R, T), 0.1, dt, "dH", T, N).t().contiguous()
+    db = torch.full((T, R + 3), float("nan"), dtype=X.dtype, device="cuda")
+    db[:, 3:] = dH
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, xv, pre, db[:, 3:]), want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+def test_weights_of_zeros_and_saturated_gates():
+    """Products of zero, and gates at the ends of the activation's range."""
+    T, R, K = 70, 32, 64
+    z = nm.pack(torch.zeros(R, K, dtype=torch.bfloat16, device="cuda"), 2, 4)
+    w = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = 1.0
+    p = nm.pack(w, 2, 4)
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = torch.linspace(-3e4, 3e4, T)
+    for act in ("silu", "gelu"):
+        for n in (1, 20, T):
+            assert bool((nm.glu(z, p, X[:n], act=act) == 0).all()) and bool((nm.glu(p, z, X[:n], act=act) == 0).all())
+            h, _, _, eh, _, _ = _ffn.glu64(X[:n], w, w, act)
+            check(nm.glu(p, p, X[:n], act=act), h, eh, act)
+        pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+        nm.glu(p, p, X, act=act, pre=pre)
+        k = torch.zeros_like(w, dtype=torch.bool)
+        k[:, 0:2] = True
+        k[:, 4::4] = k[:, 5::4] = True
+        dH = torch.ones(T, R, dtype=X.dtype, device="cuda")
+        want, bound = _ffn.glu_grad64(X, w, w, k, k, pre, dH, act)
+        for a, b, e, what in zip(nm.glu_backward(p, p, X, pre, dH, act=act), want, bound, ("dX", "dWg", "dWu")):
+            check(a, b, e, what)
+
+
+def test_packed_weights_copy_and_pickle():
+    """A weight that has been used copies and pickles like one that has not."""
+    pg, pu = weights(16, 64, 2, 4, "f16", "g")[0], weights(16, 64, 2, 4, "f16", "u")[0]
+    w = _mx_w(16, 64, "f16")[0]
+    X = normal((3, 64), 1.0, "f16", "X")
+    H, Y = nm.glu(pg, pu, X), nm.mx_linear(w, X)
+    for f in (copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p))):
+        assert torch.equal(nm.glu(f(pg), f(pu), X), H) and torch.equal(nm.mx_linear(f(w), X), Y)
+    other = weights(16, 64, 2, 4, "f16", "other")[0]
+    pg.values, pg.meta = other.values, other.meta             # a field that changes is seen
+    assert torch.equal(nm.glu(pg, pu, X), nm.glu(other, pu, X))
+
+
+def test_workspaces():
+    """A workspace that is larger or smaller than needed, shared by calls in
+    order, and by two graphs replayed in order."""
+    T, R, K, dt = 130, 200, 264, "bf16"
+    pg, pu = weights(R, K, 4, 8, dt, "g")[0], weights(R, K, 4, 8, dt, "u")[0]
+    w = _mx_w(R, K, dt)[0]
+    X, dH = normal((T, K), 1.0, dt, "X"), normal((T, R), 0.1, dt, "dH")
+    pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+
+    def forward(ws=None):
+        return nm.glu(pg, pu, X, pre=pre, workspace=ws), nm.mx_linear(w, X, workspace=ws)
+
+    def backward(ws=None):
+        return nm.glu_backward(pg, pu, X, pre, dH, workspace=ws)
+
+    want = forward(), backward()
+    need = max(nm.glu_workspace_size(pg, pu, T), nm.mx_workspace_size(w, T), nm.glu_backward_workspace_size(pg, pu, T))
+    big = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    for ws in (big, big[:need], torch.empty(64, dtype=torch.uint8, device="cuda")):
+        for got, ref in zip((forward(ws), backward(ws)), want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert bool((big[need:] == 0xAB).all())
+    with pytest.raises(nm.NmError):
+        backward(big[8:])                                     # not 256-byte aligned
+    with pytest.raises(ValueError, match="contiguous"):
+        forward(big[::2])
+    torch.cuda.synchronize()
+    ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(ga):
+        fa = forward(big)
+    with torch.cuda.graph(gb):
+        bb = backward(big)
+    for i in range(3):
+        X.copy_(normal((T, K), 1.0, dt, "X", i))
+        ga.replay()
+        gb.replay()
+        got = [t.clone() for t in (*fa, *bb)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, (*forward(), *backward())):
+            assert torch.equal(a, b), f"replay {i}"
 
 
 @pytest.fixture
@@ -401,6 +528,27 @@ def test_mx_tile_shapes(tile, shape, K):
     u, U = _mx_w(R, K, "bf16", "u")
     h, _, _, eh, _, _ = _ffn.glu64(x, W, U, "silu")
     check(nm.mx_glu(w, u, X), h, eh, "H")
+
+
+@pytest.mark.parametrize("split", [2, 7, 16])
+@pytest.mark.parametrize("R", [1, 333, 642])
+def test_mx_split_reductions(tile, R, split):
+    """Parts of a long reduction added with the bias and the activation;
+    outputs of an odd width, in rows of an odd pitch."""
+    T, K = 70, 8200
+    w, W = _mx_w(R, K, "bf16")
+    X = normal((T, K), 0.05, "bf16", "X", R)
+    b = normal((R,), 1.0, "f32", "b", R)
+    x = _ffn.mx64(X)[0]
+    y, e = x @ W.t() + b.double(), _ffn.sum_err(K, x.abs() @ W.abs().t()) + 2.0 ** -23 * split * b.double().abs()
+    tile("tile", 3, split)
+    ob, ov = wide(torch.zeros(T, R, dtype=torch.float16, device="cuda"), 3, 5.0)
+    check(nm.mx_linear(w, X, bias=b, out=ov), y, e + 2.0 ** -23 * (y.abs() + e), "Y")
+    assert bool((ob[:, R:] == 5.0).all())
+    want = _ffn.act64(y, "gelu")
+    err = 1.13 * (e + 2.0 ** -23 * (y.abs() + e)) + _ffn.act_err(y, "gelu") + 2.0 ** -22 * e
+    check(nm.mx_linear(w, X, bias=b, act="gelu", out=ov), want, err, "gelu(Y)")
+    assert bool((ob[:, R:] == 5.0).all())
 
 
 def test_mx_offsets_past_32_bits():
