@@ -27,31 +27,46 @@ inline int64_t mx_scales_bytes(int64_t rows, int64_t K) { return (rows + 31) / 3
 // C[m][n] = sum_k A[m][k] B[n][k]: A the activations (rows = tokens, or
 // weight rows in the weight gradient), B the weights, both with the reduction
 // contiguous; a "slab" is 128 bytes of the reduction.
-enum TileOp { TILE_LINEAR = 0, TILE_GLU = 1, TILE_MASKED = 2 };
+//   TILE_LINEAR  act(C + bias)
+//   TILE_GLU     act(C0) * C1 over two weights
+//   TILE_BACK    the gradients of the gated block in one launch: A B^T of the
+//                fields below (16-bit, or binary32 slices where split > 1), and
+//                A B^T of `w`, twice, where kept
+enum TileOp { TILE_LINEAR = 0, TILE_GLU = 1, TILE_BACK = 2 };
+
+struct TileGradArgs {
+  const uint8_t* A[2];       // transposed dG, dU: [Mr] rows of ld bytes
+  const uint8_t* B;          // X transposed: [Nr] rows of ld bytes
+  int64_t ld, Mr, Nr;
+  int nslab;
+  void* C[2];                // nullptr: not computed
+  int64_t ldc;
+  const uint8_t* mask[2];    // bit k % 8 of byte k / 8 of row m says the weight is kept
+  int64_t ldm;               // bytes
+  int lead;                  // from plan_back
+};
 
 struct TileArgs {
-  const uint8_t* A[2];       // per batch; lda bytes between rows
-  const uint8_t* B[2];       // TILE_GLU: gate and up weights; else per batch
+  const uint8_t* A;          // lda bytes between rows
+  const uint8_t* B[2];       // TILE_GLU: gate and up weights; else the first
   const uint8_t* As;         // scales (microscaled operands), unit layout above
   const uint8_t* Bs[2];
   int64_t lda, ldb;          // bytes
   int64_t Mr, Nr;            // rows of A, rows of B (of one of the two weights)
   int ka, kb;                // valid 16-byte pieces of an A row, of a B row
   int nslab;                 // slabs of the reduction
-  void* C[2];                // output, ldc elements between rows
+  void* C;                   // output, ldc elements between rows (TILE_BACK: nullptr, not computed)
   int64_t ldc;
   void* P[2];                // TILE_GLU: the two products (nullptr: not kept), ldp elements between rows
   int64_t ldp;
   const float* bias;         // [Nr] or nullptr
-  const uint8_t* mask[2];    // TILE_MASKED: bit k % 8 of byte k / 8 of row m says the weight is kept
-  int64_t ldm;               // bytes
   int act;                   // NM_ACT_NONE / NM_ACT_GELU / NM_ACT_SILU
-  int batch;                 // 1, or 2 products over A[b], B[b] -> C[b]
-  int shape;                 // tile shape, from plan_tile
-  // split of the reduction (TILE_LINEAR): slice s covers slabs s * sps ..,
-  // raw sums to C + s * cs elements of binary32
+  int shape;                 // tile shape, from plan_tile or plan_back
+  // split of the reduction (TILE_LINEAR, TILE_BACK): slice s covers slabs
+  // s * sps .., raw sums to C + s * cs elements of binary32
   int split, sps;
   int64_t cs;
+  TileGradArgs w;            // TILE_BACK
 };
 
 // Element types of the tile kernel's operands.
@@ -60,9 +75,13 @@ enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2 };
 // Tile shape (0: 256 x 256, 1: 128 x 256, 2: 128 x 128, 3: 64 x 128) and slices
 // of the reduction for one product, by a model of its time.
 struct TilePlan {
-  int shape, split, sps;
+  int shape, split, sps, lead;
 };
-TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int batch, int cus);
+TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int cus);
+// The same for TILE_BACK's products of T tokens: T x K over 2 R and, twice, R x
+// K over T, in slabs; lead: products of the second kind that a workgroup with
+// one product less of the first takes ahead of the others.
+TilePlan plan_back(int64_t T, int64_t R, int64_t K, int nslab_x, int nslab_w, bool dx, bool dw, int cus);
 int device_cu_count();
 // Workgroups of `block` threads for n items, at most 2^22 (a launch has fewer
 // than 2^32 threads): kernels launched so loop over the rest.

@@ -1,6 +1,8 @@
 // C ABI of the feed-forward operators (include/nm_sparse.h): host-side
 // validation, choice of the path per shape, launches.  Stateless and
 // thread-safe.
+#include <algorithm>
+
 #include "nm_ffn.hpp"
 
 using nm::Geometry;
@@ -31,16 +33,17 @@ hipError_t run_tile(int et, nm::TileOp op, int ydt, nm::TileArgs a, const nm::Ti
   a.shape = plan.shape;
   a.split = plan.split;
   a.sps = plan.sps;
-  if (plan.split == 1) return launch(op, ydt, a, s);
+  a.w.lead = plan.lead;
+  if (plan.split == 1 || !a.C) return launch(op, ydt, a, s);
   nm::TileArgs p = a;
-  p.C[0] = p.C[1] = part;
+  p.C = part;
   p.ldc = a.Nr;
   p.cs = a.Mr * a.Nr;
   p.bias = nullptr;
   p.act = NM_ACT_NONE;
-  const hipError_t e = launch(op, NM_F32, p, s);
+  const hipError_t e = launch(op, op == nm::TILE_LINEAR ? NM_F32 : ydt, p, s);
   if (e != hipSuccess) return e;
-  return nm::launch_tile_reduce(part, plan.split, a.Mr, a.Nr, a.bias, a.act, a.C[0], a.ldc, ydt, s);
+  return nm::launch_tile_reduce(part, plan.split, a.Mr, a.Nr, a.bias, a.act, a.C, a.ldc, ydt, s);
 }
 
 size_t part_bytes(const nm::TilePlan& p, int64_t Mr, int64_t Nr) {
@@ -119,8 +122,8 @@ bool backward_ok(const Geometry& g, int64_t T) {
 struct BackwardPlan {
   int64_t Rp, Tp, Kp;
   size_t d, dt, xt, wt, mask, part, total;   // bytes of each part (mask: of one weight)
-  nm::TilePlan dx, dw;
-  BackwardPlan(const Geometry& g, int64_t T) {
+  nm::TilePlan plan;
+  BackwardPlan(const Geometry& g, int64_t T, bool dx, bool dw) {
     Rp = up64(g.R);
     Tp = up64(T);
     Kp = up64(g.K);
@@ -129,10 +132,8 @@ struct BackwardPlan {
     xt = up256((size_t)(g.K * Tp * 2));
     wt = up256((size_t)(g.K * 2 * Rp * 2));
     mask = up256((size_t)(g.R * Kp / 8));
-    const int cus = nm::device_cu_count();
-    dx = nm::plan_tile(nm::TILE_LINEAR, false, T, g.K, (int)(2 * Rp / 64), 1, cus);
-    dw = nm::plan_tile(nm::TILE_MASKED, false, g.R, g.K, (int)(Tp / 64), 2, cus);
-    part = part_bytes(dx, T, g.K);
+    plan = nm::plan_back(T, g.R, g.K, (int)(2 * Rp / 64), (int)(Tp / 64), dx, dw, nm::device_cu_count());
+    part = dx ? part_bytes(plan, T, g.K) : 0;
     total = d + dt + xt + wt + 2 * mask + part;
   }
 };
@@ -153,7 +154,7 @@ bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_
 size_t mx_ws_codes(int64_t T, int64_t K) { return up256((size_t)nm::mx_codes_bytes(T, K)); }
 size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm::mx_scales_bytes(T, K)); }
 nm::TilePlan mx_plan(bool glu, int64_t T, int64_t R, int64_t K) {
-  return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), 1,
+  return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab),
                        nm::device_cu_count());
 }
 
@@ -229,7 +230,7 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     return nm::launch_mx_decode(a, s) == hipSuccess ? NM_OK : NM_EHIP;
   }
   nm::TileArgs a{};
-  a.A[0] = a.A[1] = xcodes;
+  a.A = xcodes;
   a.As = xscales;
   for (int i = 0; i < 2; ++i) {
     a.B[i] = static_cast<const uint8_t*>(ws2[i]->codes);
@@ -240,11 +241,10 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
   a.Nr = R;
   a.ka = a.kb = (int)(Kp / 32);
   a.nslab = (int)(Kp / nm::kMxSlab);
-  a.C[0] = a.C[1] = Y;
+  a.C = Y;
   a.ldc = ldy;
   a.bias = bias;
   a.act = act;
-  a.batch = 1;
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + quant);
   return run_tile(nm::TILE_MX, glu ? nm::TILE_GLU : nm::TILE_LINEAR, ydt, a, plan, part, s) == hipSuccess ? NM_OK
                                                                                                          : NM_EHIP;
@@ -334,9 +334,9 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
     e.values[i] = static_cast<const uint8_t*>(w[i]->values);
     e.meta[i] = static_cast<const uint8_t*>(w[i]->meta);
     e.dense[i] = reinterpret_cast<uint16_t*>(d);
-    a.A[i] = static_cast<const uint8_t*>(X);
     a.B[i] = d;
   }
+  a.A = static_cast<const uint8_t*>(X);
   if (nm::launch_expand_dense(g, e, s) != hipSuccess) return NM_EHIP;
   a.lda = ld * 2;
   a.ldb = Kp * 2;
@@ -345,14 +345,13 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   a.ka = (int)((direct ? g.K : Kp) / 8);
   a.kb = (int)(Kp / 8);
   a.nslab = (int)(Kp / 64);
-  a.C[0] = Ht;
+  a.C = Ht;
   a.ldc = ldh;
   a.P[0] = G;
   a.P[1] = U;
   a.ldp = ldp;
   a.act = act;
-  a.batch = 1;
-  const nm::TilePlan plan = nm::plan_tile(nm::TILE_GLU, false, T, g.R, a.nslab, 1, nm::device_cu_count());
+  const nm::TilePlan plan = nm::plan_tile(nm::TILE_GLU, false, T, g.R, a.nslab, nm::device_cu_count());
   return run_tile(tile_type(gate->dtype), nm::TILE_GLU, gate->dtype, a, plan, nullptr, s) == hipSuccess ? NM_OK
                                                                                                        : NM_EHIP;
 }
@@ -364,7 +363,7 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
   if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
-  *bytes = BackwardPlan(g, T).total;
+  *bytes = std::max(BackwardPlan(g, T, true, true).total, BackwardPlan(g, T, true, false).total);
   return NM_OK;
 }
 
@@ -385,7 +384,7 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
       !aligned(dWu, 2))
     return NM_EUNSUPPORTED;
   if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
-  const BackwardPlan p(g, T);
+  const BackwardPlan p(g, T, dX != nullptr, dWg != nullptr);
   if (!workspace || workspace_bytes < p.total) return NM_EINVAL;
   if (!aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -420,43 +419,33 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   q.dt = dWg ? reinterpret_cast<uint16_t*>(dt) : nullptr;
   q.xt = dWg ? reinterpret_cast<uint16_t*>(xt) : nullptr;
   if (nm::launch_glu_prepare(q, gate->dtype, s) != hipSuccess) return NM_EHIP;
-  if (dX) {
-    // dX[t][k] = sum over both weights' rows of d[t][r] W[r][k]
-    nm::TileArgs a{};
-    a.A[0] = d;
-    a.B[0] = wt;
-    a.lda = a.ldb = 4 * p.Rp;
-    a.Mr = T;
-    a.Nr = g.K;
-    a.ka = a.kb = (int)(2 * p.Rp / 8);
-    a.nslab = (int)(2 * p.Rp / 64);
-    a.C[0] = dX;
-    a.ldc = lddx;
-    a.batch = 1;
-    if (run_tile(tile_type(gate->dtype), nm::TILE_LINEAR, gate->dtype, a, p.dx, part, s) != hipSuccess) return NM_EHIP;
+  nm::TileArgs a{};
+  // dX[t][k] = sum over both weights' rows of d[t][r] W[r][k]
+  a.A = d;
+  a.B[0] = wt;
+  a.lda = a.ldb = 4 * p.Rp;
+  a.Mr = T;
+  a.Nr = g.K;
+  a.ka = a.kb = (int)(2 * p.Rp / 8);
+  a.nslab = (int)(2 * p.Rp / 64);
+  a.C = dX;
+  a.ldc = lddx;
+  // dW[r][k] = sum over t of d[t][r] X[t][k], both transposed
+  a.w.B = xt;
+  a.w.ld = 2 * p.Tp;
+  a.w.Mr = g.R;
+  a.w.Nr = g.K;
+  a.w.nslab = (int)(p.Tp / 64);
+  a.w.C[0] = dWg;
+  a.w.C[1] = dWu;
+  a.w.ldc = lddw;
+  a.w.ldm = p.Kp / 8;
+  for (int i = 0; i < 2; ++i) {
+    a.w.A[i] = dt + (size_t)i * g.R * p.Tp * 2;
+    a.w.mask[i] = mask + i * p.mask;
   }
-  if (dWg) {
-    // dW[r][k] = sum over t of d[t][r] X[t][k], both transposed
-    nm::TileArgs a{};
-    for (int i = 0; i < 2; ++i) {
-      a.A[i] = dt + (size_t)i * g.R * p.Tp * 2;
-      a.B[i] = xt;
-      a.mask[i] = mask + i * p.mask;
-    }
-    a.C[0] = dWg;
-    a.C[1] = dWu;
-    a.lda = a.ldb = 2 * p.Tp;
-    a.Mr = g.R;
-    a.Nr = g.K;
-    a.ka = a.kb = (int)(p.Tp / 8);
-    a.nslab = (int)(p.Tp / 64);
-    a.ldc = lddw;
-    a.ldm = p.Kp / 8;
-    a.batch = 2;
-    if (run_tile(tile_type(gate->dtype), nm::TILE_MASKED, gate->dtype, a, p.dw, nullptr, s) != hipSuccess)
-      return NM_EHIP;
-  }
-  return NM_OK;
+  return run_tile(tile_type(gate->dtype), nm::TILE_BACK, gate->dtype, a, p.plan, part, s) == hipSuccess ? NM_OK
+                                                                                                       : NM_EHIP;
 }
 
 nm_status nm_mx_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes) {

@@ -25,6 +25,7 @@
 // ones, and a count of outstanding loads could pass too early.  TILE_GLU: half of a wave's B rows are gate
 // rows, the other half the up rows of the same outputs, so g and u of one
 // output meet in one lane and the activation and product need no exchange.
+// TILE_BACK: the input's and both weights' gradients are items of one launch.
 #pragma once
 
 #include "nm_tile_common.hpp"
@@ -67,12 +68,13 @@ __device__ __forceinline__ v4f mfma_16(v4i a, v4i b, v4f c) {
 
 template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
 __global__ void __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
-tile_kernel(TileArgs a, TileList list) {
+tile_kernel(TileArgs a, TileList list, TileList list2) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles of a wave
   constexpr bool MX = ET == TILE_MX;
   constexpr bool GLU = OP == TILE_GLU;
+  constexpr bool BACK = OP == TILE_BACK;
   constexpr int ROWS = BM + BN;
   constexpr int DATA = ROWS * 128;
   constexpr int STAGE = DATA + (MX ? ROWS * 8 : 0);
@@ -94,7 +96,7 @@ tile_kernel(TileArgs a, TileList list) {
   const int li = lane & 15, lq = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
 
-  TileWalk walk(list);
+  const TileWalk<BACK> walk(list, list2, a.w.lead);
   if (walk.count <= 0) return;
 
   // ---- operand loads: load d fills LDS rows 8 d .. 8 d + 7, lane l row
@@ -115,8 +117,9 @@ tile_kernel(TileArgs a, TileList list) {
     return row;
   };
   // pieces past the end of a row, in the last slab: an offset no resource holds
-  const int cut_a = (a.ka & 7) && piece >= (a.ka & 7) ? (int)0x80000000 : 0;
-  const int cut_b = (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
+  // (TILE_BACK: rows of whole slabs)
+  const int cut_a = !BACK && (a.ka & 7) && piece >= (a.ka & 7) ? (int)0x80000000 : 0;
+  const int cut_b = !BACK && (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
 
   // the load cursor: work item, its resources, next slab
   int ck = 0, cs, ce, voff[NL];
@@ -129,15 +132,18 @@ tile_kernel(TileArgs a, TileList list) {
       const v4i r = make_rsrc(p + row0 * ld, 0x7fffffff);
       return v4i{scalar(r[0]), scalar(r[1]), r[2], r[3]};
     };
-    const int mlast = (int)min(a.Mr - m0, (int64_t)BM) - 1, nlast = (int)min(a.Nr - n0, (int64_t)BNO) - 1;
+    const bool grad = BACK && it.batch;                 // a weight gradient
+    const int64_t Mr = grad ? a.w.Mr : a.Mr, Nr = grad ? a.w.Nr : a.Nr;
+    const int64_t lda = grad ? a.w.ld : a.lda, ldb = grad ? a.w.ld : a.ldb;
+    const int mlast = (int)min(Mr - m0, (int64_t)BM) - 1, nlast = (int)min(Nr - n0, (int64_t)BNO) - 1;
     static_for<0, NL>([&](auto jc) {
       constexpr int j = decltype(jc)::value;
-      voff[j] = j < NLA ? min(load_row(jc), mlast) * (int)a.lda + 16 * piece
-                        : min(load_row(jc), nlast) * (int)a.ldb + 16 * piece;
+      voff[j] = j < NLA ? min(load_row(jc), mlast) * (int)lda + 16 * piece
+                        : min(load_row(jc), nlast) * (int)ldb + 16 * piece;
     });
-    ra = tile_rsrc(it.batch ? a.A[1] : a.A[0], m0, a.lda);
-    rb0 = tile_rsrc(!GLU && it.batch ? a.B[1] : (wave_up ? a.B[1] : a.B[0]), n0, a.ldb);
-    if constexpr (GLU && !SPAN) rb1 = tile_rsrc(a.B[1], n0, a.ldb);
+    ra = tile_rsrc(grad ? (it.batch > 1 ? a.w.A[1] : a.w.A[0]) : a.A, m0, lda);
+    rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], n0, ldb);
+    if constexpr (GLU && !SPAN) rb1 = tile_rsrc(a.B[1], n0, ldb);
     if constexpr (MX) {
       // unit u of a stage: LDS rows 32 u ..; row groups past the end repeat the last one
       static_for<0, (NU + NW - 1) / NW>([&](auto jc) {
@@ -178,7 +184,7 @@ tile_kernel(TileArgs a, TileList list) {
   // part p of NP of the cursor slab's loads into stage st
   auto issue_part = [&](auto pc, auto npc, int st) {
     constexpr int P = decltype(pc)::value, NP = decltype(npc)::value;
-    const int ca = cs + 1 < a.nslab ? 0 : cut_a, cb = cs + 1 < a.nslab ? 0 : cut_b;
+    const int ca = BACK || cs + 1 < a.nslab ? 0 : cut_a, cb = BACK || cs + 1 < a.nslab ? 0 : cut_b;
     static_for<NLT * P / NP, NLT * (P + 1) / NP>([&](auto jc) { issue_one(jc, st, ca, cb); });
   };
   // past the last work item the cursor stays on its last slab: the loads fill
@@ -304,9 +310,13 @@ tile_kernel(TileArgs a, TileList list) {
 
 template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
 hipError_t launch_tile_cfg(const TileArgs& a, hipStream_t s) {
-  const TileList list = tile_list(a, BM, OP == TILE_GLU ? BN / 2 : BN);
-  hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3((unsigned)list.grid), dim3(WM * WN * 64), 0,
-                     s, a, list);
+  constexpr int BNO = OP == TILE_GLU ? BN / 2 : BN;
+  const bool back = OP == TILE_BACK;
+  const TileList list = tile_list(a.Mr, a.Nr, BM, BNO, a.split, a.sps, a.nslab, back && !a.C ? 0 : 1);
+  const TileList list2 = tile_list(a.w.Mr, a.w.Nr, BM, BNO, 1, a.w.nslab, a.w.nslab, back && a.w.C[0] ? 2 : 0);
+  const int grid = 8 * tile_slots(list.per + list2.per);
+  hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s,
+                     a, list, list2);
   return hipGetLastError();
 }
 
@@ -339,13 +349,10 @@ hipError_t launch_tile(TileOp op, int ydt, const TileArgs& a, hipStream_t s) {
     if (ydt == NM_BF16) return launch_tile_op<ET, TILE_LINEAR, NM_BF16>(a, s);
     return launch_tile_op<ET, TILE_LINEAR, NM_F32>(a, s);
   } else {
-    switch (op) {
-      case TILE_GLU: return launch_tile_op<ET, TILE_GLU, W16>(a, s);
-      case TILE_MASKED: return launch_tile_op<ET, TILE_MASKED, W16>(a, s);
-      default:
-        return ydt == NM_F32 ? launch_tile_op<ET, TILE_LINEAR, NM_F32>(a, s)
-                             : launch_tile_op<ET, TILE_LINEAR, W16>(a, s);
-    }
+    if (ydt != W16) return hipErrorInvalidValue;
+    if (op == TILE_GLU) return launch_tile_op<ET, TILE_GLU, W16>(a, s);
+    if (op == TILE_BACK) return launch_tile_op<ET, TILE_BACK, W16>(a, s);
+    return hipErrorInvalidValue;
   }
 }
 

@@ -55,19 +55,18 @@ double glu_tile24_time(int64_t T, int64_t R, int64_t nslab, int cus, int* shape)
 hipError_t launch_glu_tile24(const GluArgs& g, hipStream_t s) {
   Tile24Args p{};
   TileArgs& a = p.t;
-  a.A[0] = a.A[1] = static_cast<const uint8_t*>(g.X);
+  a.A = static_cast<const uint8_t*>(g.X);
   a.lda = g.ldx * 2;
   a.Mr = g.T;
   a.Nr = g.g.R;
   a.ka = (int)(g.g.K / 8);
   a.nslab = (int)g.g.nKB;
-  a.C[0] = g.H;
+  a.C = g.H;
   a.ldc = g.ldh;
   a.P[0] = g.P[0];
   a.P[1] = g.P[1];
   a.ldp = g.ldp;
   a.act = g.act;
-  a.batch = 1;
   a.split = 1;
   a.sps = a.nslab;
   for (int i = 0; i < 2; ++i) {

@@ -76,7 +76,7 @@ tile24_kernel(Tile24Args p, TileList list) {
   const int nKB = a.nslab;
   const int64_t nRB = (a.Nr + 15) / 16;
 
-  TileWalk walk(list);
+  const TileWalk<false> walk(list, list, 0);
   if (walk.count <= 0) return;
 
   // ---- loads.  Tokens: load d = w + 8 j fills LDS rows 8 d .. + 7.  Block b
@@ -103,7 +103,7 @@ tile24_kernel(Tile24Args p, TileList list) {
       constexpr int j = decltype(jc)::value;
       voff[j] = min(8 * (wave + NW * j) + (lane >> 3), mlast) * (int)a.lda + 16 * piece;
     });
-    ra = rsrc(a.A[0], m0 * a.lda);
+    ra = rsrc(a.A, m0 * a.lda);
     rv = rsrc(weight_of(bv) ? p.values[1] : p.values[0], rb0 * nKB * 1024);
     rm = rsrc(weight_of(bm) ? p.meta[1] : p.meta[0], rb0 * nKB * 128);
     // row blocks past the weights' end repeat the last one (their results are not stored)
@@ -228,8 +228,8 @@ tile24_kernel(Tile24Args p, TileList list) {
 
 template <int WT, int TM, int H, int NS>
 hipError_t launch_tile24_cfg(const Tile24Args& p, hipStream_t s) {
-  const TileList list = tile_list(p.t, 64 * TM, 32 * H);
-  hipLaunchKernelGGL((tile24_kernel<WT, TM, H, NS>), dim3((unsigned)list.grid), dim3(512), 0, s, p, list);
+  const TileList list = tile_list(p.t.Mr, p.t.Nr, 64 * TM, 32 * H, 1, p.t.nslab, p.t.nslab, 1);
+  hipLaunchKernelGGL((tile24_kernel<WT, TM, H, NS>), dim3((unsigned)(8 * tile_slots(list.per))), dim3(512), 0, s, p, list);
   return hipGetLastError();
 }
 

@@ -19,28 +19,30 @@ __device__ __forceinline__ void static_for(F&& f) {
 // unit: buffer resources chosen by their results must be in scalar registers)
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Work items: mt x nt tiles, a.split slices of the reduction, a.batch
-// products.  XCD x (blockIdx % 8) takes a contiguous run of the list, in
-// groups of gm row tiles, row tile fastest inside a group: the workgroups of
-// an XCD that run together share both operands' slabs through its L2.
+// Work items: mt x nt tiles, split slices of the reduction, batch products.
+// XCD x (blockIdx % 8) takes a contiguous run of the list, in groups of gm row
+// tiles, row tile fastest inside a group: the workgroups of an XCD that run
+// together share both operands' slabs through its L2.
 struct TileList {
-  int mt, nt, gm, batch, split, sps, nslab, total, per, grid;
+  int mt, nt, gm, split, sps, nslab, total, per;
 };
 
-inline TileList tile_list(const TileArgs& a, int bm, int bno) {
+inline TileList tile_list(int64_t Mr, int64_t Nr, int bm, int bno, int split, int sps, int nslab, int batch) {
   TileList l;
-  l.mt = (int)((a.Mr + bm - 1) / bm);
-  l.nt = (int)((a.Nr + bno - 1) / bno);
+  l.mt = (int)((Mr + bm - 1) / bm);
+  l.nt = (int)((Nr + bno - 1) / bno);
   l.gm = l.mt < 8 ? l.mt : 8;
-  l.batch = a.batch;
-  l.split = a.split;
-  l.sps = a.sps;
-  l.nslab = a.nslab;
-  l.total = l.mt * l.nt * a.split * a.batch;
+  l.split = split;
+  l.sps = sps;
+  l.nslab = nslab;
+  l.total = l.mt * l.nt * split * batch;
   l.per = (l.total + 7) / 8;
-  const int slots = (device_cu_count() + 7) / 8;   // workgroups of an XCD (one a CU)
-  l.grid = 8 * (l.per < slots ? l.per : slots);
   return l;
+}
+// workgroups of an XCD for `per` items: at most one a CU
+inline int tile_slots(int per) {
+  const int slots = (device_cu_count() + 7) / 8;
+  return per < slots ? per : slots;
 }
 
 struct TileItem {
@@ -50,32 +52,54 @@ struct TileItem {
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// the items of one workgroup: every (workgroups of an XCD)-th of its XCD's run
+// The items of one workgroup, of `step` on its XCD: every step-th of the XCD's
+// run.  TWO: of list l, then of l2 (their products count from 1).  Where l
+// leaves q workgroups one item more than the others, those others take `lead`
+// items of l2 each ahead of the rest, which goes to all in turn.
+template <bool TWO>
 struct TileWalk {
   const TileList& l;
-  int first, step, count;
-  __device__ __forceinline__ explicit TileWalk(const TileList& list) : l(list) {
-    const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
-    step = l.grid >> 3;
-    first = x * l.per + j;
-    const int end = min((x + 1) * l.per, l.total);
-    count = first < end ? scalar((end - first + step - 1) / step) : 0;
+  const TileList& l2;
+  int x, j, step, n0, q, lead, ahead, count;
+  static __device__ __forceinline__ int rounds(int n, int step) { return n > 0 ? scalar((n + step - 1) / step) : 0; }
+  __device__ __forceinline__ TileWalk(const TileList& list, const TileList& list2, int lead_) : l(list), l2(list2) {
+    x = blockIdx.x & 7;
+    j = blockIdx.x >> 3;
+    step = gridDim.x >> 3;
+    count = n0 = rounds(min(l.per, l.total - x * l.per) - j, step);
+    if constexpr (TWO) {
+      const int len = min(l2.per, l2.total - x * l2.per);
+      q = l.per - scalar(l.per / step) * step;
+      lead = lead_;
+      ahead = lead * (step - q);
+      if (j >= q) count += min(lead, rounds(len - (j - q), step - q));
+      count += rounds(len - ahead - j, step);
+    }
   }
   __device__ __forceinline__ TileItem item(int k) const {
-    int L = first + k * step;
-    const int ntile = l.mt * l.nt;
-    const int z = scalar(L / ntile);
-    L -= z * ntile;
+    const bool second = TWO && k >= n0;
+    int L = x * l.per + j + k * step;
+    if (second) {
+      k -= n0;
+      if (j < q) k += lead;
+      L = x * l2.per + (k < lead ? k * (step - q) + j - q : ahead + (k - lead) * step + j);
+    }
+    const int mt = second ? l2.mt : l.mt, nt = second ? l2.nt : l.nt, gm = second ? l2.gm : l.gm;
+    const int split = second ? l2.split : l.split, sps = second ? l2.sps : l.sps;
+    const int nslab = second ? l2.nslab : l.nslab;
+    const int z = scalar(L / (mt * nt));
+    L -= z * mt * nt;
     TileItem t;
-    t.batch = scalar(z / l.split);
-    t.ks = z - t.batch * l.split;
-    const int grp = scalar(L / (l.gm * l.nt));
-    const int in = L - grp * l.gm * l.nt;
-    const int rows = min(l.gm, l.mt - grp * l.gm);
+    t.batch = scalar(z / split);
+    t.ks = z - t.batch * split;
+    const int grp = scalar(L / (gm * nt));
+    const int in = L - grp * gm * nt;
+    const int rows = min(gm, mt - grp * gm);
     t.n = scalar(in / rows);
-    t.m = grp * l.gm + in - t.n * rows;
-    t.s0 = t.ks * l.sps;
-    t.s1 = min(t.s0 + l.sps, l.nslab);
+    t.m = grp * gm + in - t.n * rows;
+    t.s0 = t.ks * sps;
+    t.s1 = min(t.s0 + sps, nslab);
+    if (second) ++t.batch;
     return t;
   }
 };
@@ -114,21 +138,77 @@ __device__ __forceinline__ void store_pair(void* C, int64_t row, int64_t n, int6
   }
 }
 
-// Epilogue of one wave's TN x TM tiles of 16 x 16: lane (li, lq) holds n = n0
-// + 16 i + 4 lq + v of row m0 + 16 j + li.  TILE_GLU: tiles i < TN / 2 are
-// gate, the others up columns of the same outputs.
+__device__ __forceinline__ bool rows_vec(const void* p, int64_t ld, int n, int eb) {
+  return ld % n == 0 && (uintptr_t)p % (n * eb) == 0;
+}
+
+// One wave's TN x TM tiles of 16 x 16 as rows of C [Mr][ldc]: lane (li, lq)
+// holds n = n0 + 16 i + 4 lq + v of row m0 + 16 j + li.  MASKED: zero where
+// the mask has no bit; else act(C + bias).
+template <bool MASKED, int OUT, int TM, int TN>
+__device__ __forceinline__ void tile_rows(void* C, int64_t ldc, int64_t Mr, int64_t Nr, const float* bias, int act,
+                                          const uint8_t* mask, int64_t ldm, int64_t m0, int64_t n0,
+                                          const v4f (&acc)[TN][TM]) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+  constexpr int EB = OUT == NM_F32 ? 4 : 2;
+  const bool v8 = rows_vec(C, ldc, 8, EB), v4 = rows_vec(C, ldc, 4, EB);
+  // the kept bits of every row and column pair (32 columns, one word: rows of
+  // the mask are padded to 64), in flight together before the first use
+  uint32_t keep[MASKED ? TN / 2 : 1][TM];
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int i = 0; i < TN / 2; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int64_t m = m0 + 16 * j + li, n = n0 + 32 * i;
+        keep[i][j] = m < Mr && n < Nr ? *reinterpret_cast<const uint32_t*>(mask + m * ldm + n / 8) >> (4 * lq) : 0;
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = 0; i < TN; i += 2) {
+    float b[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t n = n0 + 16 * (i + e) + 4 * lq + v;
+        b[e][v] = !MASKED && bias && n < Nr ? bias[n] : 0.f;
+      }
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t m = m0 + 16 * j + li;
+      float y[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if constexpr (MASKED) {
+            y[e][v] = keep[i / 2][j] >> (16 * e + v) & 1 ? acc[i + e][j][v] : 0.f;   // a select: NaN is masked too
+          } else {
+            y[e][v] = acc[i + e][j][v] + b[e][v];
+            y[e][v] = act == NM_ACT_GELU ? gelu_f32(y[e][v]) : y[e][v];
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);                // one output's temporaries at a time
+      if (m < Mr) store_pair<OUT>(C, m * ldc, n0 + 16 * i, Nr, lq, y[0], y[1], v8, v4);
+    }
+  }
+}
+
+// Epilogue of one wave's tiles.  TILE_GLU: tiles i < TN / 2 are gate, the
+// others up columns of the same outputs.
 template <int OP, int OUT, int TM, int TN>
 __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem& it, int64_t m0, int64_t n0,
                                               const v4f (&acc)[TN][TM]) {
-  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
-  constexpr int EB = OUT == NM_F32 ? 4 : 2;
-  uint8_t* C = static_cast<uint8_t*>(OP == TILE_MASKED && it.batch ? a.C[1] : a.C[0]) + (int64_t)it.ks * a.cs * EB;
-  auto vec = [](const void* p, int64_t ld, int n) { return ld % n == 0 && (uintptr_t)p % (n * EB) == 0; };
-  const bool v8 = vec(C, a.ldc, 8), v4 = vec(C, a.ldc, 4);
   if constexpr (OP == TILE_GLU) {
+    const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+    constexpr int EB = OUT == NM_F32 ? 4 : 2;
     constexpr int H = TN / 2;
-    const bool p8 = a.P[0] && vec(a.P[0], a.ldp, 8) && vec(a.P[1], a.ldp, 8);
-    const bool p4 = a.P[0] && vec(a.P[0], a.ldp, 4) && vec(a.P[1], a.ldp, 4);
+    const bool v8 = rows_vec(a.C, a.ldc, 8, EB), v4 = rows_vec(a.C, a.ldc, 4, EB);
+    const bool p8 = a.P[0] && rows_vec(a.P[0], a.ldp, 8, EB) && rows_vec(a.P[1], a.ldp, 8, EB);
+    const bool p4 = a.P[0] && rows_vec(a.P[0], a.ldp, 4, EB) && rows_vec(a.P[1], a.ldp, 4, EB);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const int64_t m = m0 + 16 * j + li;
@@ -145,7 +225,7 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
           }
         __builtin_amdgcn_sched_barrier(0);              // one output's temporaries at a time
         if (m < a.Mr) {
-          store_pair<OUT>(C, m * a.ldc, n0 + 16 * i, a.Nr, lq, h[0], h[1], v8, v4);
+          store_pair<OUT>(a.C, m * a.ldc, n0 + 16 * i, a.Nr, lq, h[0], h[1], v8, v4);
           if (a.P[0]) {
             store_pair<OUT>(a.P[0], m * a.ldp, n0 + 16 * i, a.Nr, lq, g[0], g[1], p8, p4);
             store_pair<OUT>(a.P[1], m * a.ldp, n0 + 16 * i, a.Nr, lq, u[0], u[1], p8, p4);
@@ -153,48 +233,18 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
         }
       }
     }
+  } else if constexpr (OP == TILE_LINEAR) {
+    void* C = static_cast<uint8_t*>(a.C) + (int64_t)it.ks * a.cs * (OUT == NM_F32 ? 4 : 2);
+    tile_rows<false, OUT, TM, TN>(C, a.ldc, a.Mr, a.Nr, a.bias, a.act, nullptr, 0, m0, n0, acc);
+  } else if (it.batch) {
+    const bool up = it.batch > 1;
+    tile_rows<true, OUT, TM, TN>(up ? a.w.C[1] : a.w.C[0], a.w.ldc, a.w.Mr, a.w.Nr, nullptr, NM_ACT_NONE,
+                                 up ? a.w.mask[1] : a.w.mask[0], a.w.ldm, m0, n0, acc);
+  } else if (a.split > 1) {
+    tile_rows<false, NM_F32, TM, TN>(static_cast<float*>(a.C) + (int64_t)it.ks * a.cs, a.ldc, a.Mr, a.Nr, nullptr,
+                                     NM_ACT_NONE, nullptr, 0, m0, n0, acc);
   } else {
-    // the kept bits of every row and column pair (32 columns, one word: rows
-    // of the mask are padded to 64), in flight together before the first use
-    uint32_t keep[TN / 2][TM];
-    if constexpr (OP == TILE_MASKED) {
-      const uint8_t* mask = it.batch ? a.mask[1] : a.mask[0];
-#pragma unroll
-      for (int i = 0; i < TN / 2; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          const int64_t m = m0 + 16 * j + li, n = n0 + 32 * i;
-          keep[i][j] = m < a.Mr && n < a.Nr ? *reinterpret_cast<const uint32_t*>(mask + m * a.ldm + n / 8) >> (4 * lq) : 0;
-        }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < TN; i += 2) {
-      float b[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t n = n0 + 16 * (i + e) + 4 * lq + v;
-          b[e][v] = OP == TILE_LINEAR && a.bias && n < a.Nr ? a.bias[n] : 0.f;
-        }
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const int64_t m = m0 + 16 * j + li;
-        float y[2][4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            y[e][v] = acc[i + e][j][v] + b[e][v];
-            if constexpr (OP == TILE_LINEAR) y[e][v] = a.act == NM_ACT_GELU ? gelu_f32(y[e][v]) : y[e][v];
-            if constexpr (OP == TILE_MASKED) y[e][v] = keep[i / 2][j] >> (16 * e + v) & 1 ? y[e][v] : 0.f;   // a select: NaN is masked too
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);              // one output's temporaries at a time
-        if (m < a.Mr) store_pair<OUT>(C, m * a.ldc, n0 + 16 * i, a.Nr, lq, y[0], y[1], v8, v4);
-      }
-    }
+    tile_rows<false, OUT, TM, TN>(a.C, a.ldc, a.Mr, a.Nr, nullptr, NM_ACT_NONE, nullptr, 0, m0, n0, acc);
   }
 }
 #endif

@@ -39,42 +39,81 @@ bool ffn_tile_override(const char* kind, int* shape, int* split) {
 // weights of 11008 x 4096, gated: 256 x 256 tiles 282 us, 128 x 256 324,
 // 128 x 128 516; 256 tokens: 99, 69 and 99; the gradient of 197 tokens through
 // 4096 x 4096: 256 x 256 160 us, 64 x 128 79, 64 x 128 in two slices 60.
-TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int batch, int cus) {
-  struct Shape {
-    int bm, bn;
-    double idle[2], busy[2], tile;   // [1]: microscaled operands
-  };
-  static const Shape shapes[4] = {{256, 256, {0.93, 1.10}, {1.60, 1.60}, 6.0},
+namespace {
+
+struct TileShape {
+  int bm, bn;
+  double idle[2], busy[2], tile;   // [1]: microscaled operands
+  double slab(bool mx, int64_t items, int cus) const {
+    return idle[mx] + (busy[mx] - idle[mx]) * std::min(1.0, (double)items / cus);
+  }
+};
+constexpr TileShape kShapes[4] = {{256, 256, {0.93, 1.10}, {1.50, 1.60}, 6.0},
                                   {128, 256, {0.47, 0.72}, {0.85, 0.97}, 5.0},
                                   {128, 128, {0.60, 0.75}, {0.73, 0.86}, 4.0},
                                   {64, 128, {0.33, 0.44}, {0.43, 0.47}, 3.5}};
+
+int64_t tiles(int64_t Mr, int64_t Nr, int bm, int bn) { return (Mr + bm - 1) / bm * ((Nr + bn - 1) / bn); }
+
+// the slices' sums written and read back, and a launch
+double split_time(int64_t Mr, int64_t Nr, int split) {
+  return split > 1 ? (double)Mr * Nr * (8.0 * split + 2.0) / 8e6 + 5.0 : 0.0;
+}
+
+// plan(shape, split, slabs of a slice) -> time, over all of them
+template <class F>
+TilePlan best_plan(int smax, int nslab, F&& time) {
   int only = -1, only_split = 0;
   ffn_tile_override("tile", &only, &only_split);
-  TilePlan best{0, 1, nslab};
+  TilePlan best{0, 1, nslab, 0};
   double best_t = 0;
   for (int i = 0; i < 4; ++i) {
-    const Shape& h = shapes[i];
     if (only >= 0 && i != only) continue;
-    const int bn = op == TILE_GLU ? h.bn / 2 : h.bn;
-    const int64_t tiles = (Mr + h.bm - 1) / h.bm * ((Nr + bn - 1) / bn) * batch;
-    const int smax = op == TILE_LINEAR ? std::min(16, nslab) : 1;
     for (int s = 1; s <= smax; ++s) {
       const int sps = (nslab + s - 1) / s;
       const int split = (nslab + sps - 1) / sps;
-      if (split != s || (only_split && op == TILE_LINEAR && s != std::min(only_split, nslab))) continue;
-      const int64_t items = tiles * split;
-      const double load = std::min(1.0, (double)items / cus);
-      const double slab = h.idle[mx] + (h.busy[mx] - h.idle[mx]) * load;
-      double t = (double)((items + cus - 1) / cus) * (sps * slab + h.tile);
-      // the slices' sums written and read back, and a launch
-      if (split > 1) t += (double)Mr * Nr * (8.0 * split + 2.0) / 8e6 + 5.0;
+      if (split != s || (only_split && smax > 1 && s != std::min(only_split, nslab))) continue;
+      TilePlan p{i, split, sps, 0};
+      const double t = time(kShapes[i], p);
       if (best_t == 0 || t < best_t) {
         best_t = t;
-        best = TilePlan{i, split, sps};
+        best = p;
       }
     }
   }
   return best;
+}
+
+}  // namespace
+
+TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int cus) {
+  return best_plan(op == TILE_LINEAR ? std::min(16, nslab) : 1, nslab, [&](const TileShape& h, TilePlan& p) {
+    const int64_t items = tiles(Mr, Nr, h.bm, op == TILE_GLU ? h.bn / 2 : h.bn) * p.split;
+    return (double)((items + cus - 1) / cus) * (p.sps * h.slab(mx, items, cus) + h.tile) + split_time(Mr, Nr, p.split);
+  });
+}
+
+// The products' items are dealt to an XCD's workgroups as TileWalk does.
+TilePlan plan_back(int64_t T, int64_t R, int64_t K, int nslab_x, int nslab_w, bool dx, bool dw, int cus) {
+  return best_plan(dx ? std::min(16, nslab_x) : 1, nslab_x, [&](const TileShape& h, TilePlan& p) {
+    const int64_t a = dx ? (tiles(T, K, h.bm, h.bn) * p.split + 7) / 8 : 0;
+    const int64_t b = dw ? (2 * tiles(R, K, h.bm, h.bn) + 7) / 8 : 0;
+    const int64_t w = std::min<int64_t>(a + b, (cus + 7) / 8), q = a % w;
+    const double slab = h.slab(false, 8 * (a + b), cus);
+    const double ta = p.sps * slab + h.tile, tb = nslab_w * slab + 1.5 * h.tile;   // (the mask is read too)
+    const int64_t most = (b + w - q - 1) / (w - q), near = (int64_t)(ta / tb);
+    double best = 0;
+    for (const int64_t lead : {int64_t(0), near, near + 1, most}) {
+      if (lead > most || (lead && !q)) continue;
+      const int64_t rest = std::max<int64_t>(0, (b - lead * (w - q) + w - 1) / w);
+      const double t = std::max((double)((a + w - 1) / w) * ta + rest * tb, (double)(a / w) * ta + (lead + rest) * tb);
+      if (best == 0 || t < best) {
+        best = t;
+        p.lead = (int)lead;
+      }
+    }
+    return best + (dx ? split_time(T, K, p.split) : 0.0);
+  });
 }
 
 namespace {
