@@ -373,10 +373,13 @@ nm_status nm_hybrid_spmm(const nm_hybrid* w, const void* X, int64_t ldx, int64_t
  * rounded once.
  * ---------------------------------------------------------------------- */
 
-/* Device workspace nm_glu needs for these weights and T tokens (0: none),
- * for rows of any stride and alignment: re-packed or dense copies of the
- * weights, and a padded copy of X, where the call takes them. */
-nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes);
+/* Device workspace nm_glu needs for these weights and T tokens (0: none): for
+ * the rows Xt and ldx of the call (read are only the pointer's alignment and
+ * the stride), or, Xt NULL, for rows of any stride and alignment.  It holds
+ * re-packed or dense copies of the weights and a padded copy of X, where the
+ * call takes them.  Errors as nm_glu. */
+nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
+                                size_t* bytes);
 
 /*
  * H = act(X Wg^T) (.) (X Wu^T).  G, U: NULL, or both [T][ldp] buffers of the
@@ -474,9 +477,9 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
  * (NM_F16, NM_BF16, NM_F32) rounded once; bias NULL or device float[R]; act
  * NM_ACT_NONE or NM_ACT_GELU.
  * nm_mx_glu: H = act(x Wg^T) (.) (x Wu^T), act NM_ACT_SILU or NM_ACT_GELU.
- * Workspace: nm_mx_workspace_size bytes (256-byte aligned; rows_n = R of the
- * weight, glu != 0 for nm_mx_glu): quantised activations and the partial
- * sums of a split reduction.  NM_EINVAL: null pointers, T < 1, ldx < K,
+ * Workspace: nm_mx_workspace_size bytes (256-byte aligned; glu != 0 for
+ * nm_mx_glu; xq or Xt as the call gets them, both NULL for any): quantised
+ * activations and the partial sums of a split reduction.  NM_EINVAL: null pointers, T < 1, ldx < K,
  * ldy < R, xq of other K or rows than asked, descriptors with wrong sizes or
  * versions, gate and up of other shapes, a small workspace;
  * NM_EUNSUPPORTED: other types, act not listed, misaligned pointers, rows so
@@ -484,7 +487,8 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
  * overlap no other buffer of the call; calls that share a workspace must be
  * ordered.
  */
-nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* bytes);
+nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
+                               int32_t glu, size_t* bytes);
 nm_status nm_mx_linear(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
                        void* Yt, int64_t ldy, int32_t y_dtype, const float* bias, int32_t act, void* workspace,
                        size_t workspace_bytes, void* stream);

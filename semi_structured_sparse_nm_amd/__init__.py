@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
         L.nm_hybrid_pack_size.argtypes = [P, I64, I64, I64, I32, HP]
         L.nm_hybrid_pack.argtypes = [P, I64, HP]
         L.nm_hybrid_spmm.argtypes = [HP, P, I64, I64, P, I64, I32, P, I32, P]
-        L.nm_glu_workspace_size.argtypes = [PP, PP, I64, ctypes.POINTER(SZ)]
+        L.nm_glu_workspace_size.argtypes = [PP, PP, P, I64, I64, ctypes.POINTER(SZ)]
         L.nm_glu.argtypes = [PP, PP, P, I64, I64, P, I64, I32, P, P, I64, P, SZ, P]
         L.nm_glu_backward_workspace_size.argtypes = [PP, PP, I64, ctypes.POINTER(SZ)]
         L.nm_glu_backward.argtypes = [PP, PP, P, I64, I64, P, P, I64, P, I64, I32, P, I64, P, P, I64, P, SZ, P]
@@ -124,7 +124,7 @@ def lib() -> ctypes.CDLL:
         L.nm_mx_size.argtypes = [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
         L.nm_mx_quantize.argtypes = [P, I64, I32, MP, P]
         L.nm_mx_dequantize.argtypes = [MP, P, I64, I32, P]
-        L.nm_mx_workspace_size.argtypes = [MP, I64, I32, ctypes.POINTER(SZ)]
+        L.nm_mx_workspace_size.argtypes = [MP, MP, P, I64, I32, I64, I32, ctypes.POINTER(SZ)]
         L.nm_mx_linear.argtypes = [MP, MP, P, I64, I32, I64, P, I64, I32, P, I32, P, SZ, P]
         L.nm_mx_glu.argtypes = [MP, MP, MP, P, I64, I32, I64, P, I64, I32, I32, P, SZ, P]
         for f in ("nm_pack_size", "nm_pack", "nm_spmm_workspace_size", "nm_spmm", "nm_hybrid_pack_size",
@@ -601,21 +601,28 @@ def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
     if pre.shape != (2, T, p.rows):
         raise ValueError(f"pre must be [2, {T}, {p.rows}], got {tuple(pre.shape)}")
     _check_dtype("pre", pre, p.torch_dtype)
-    ld, half = _row_pitch("pre", pre[0], T, p.rows), pre.stride(0)
+    half, ld, s2 = pre.stride()
+    if s2 != 1 and p.rows > 1:
+        raise ValueError("pre must have unit stride along its last dimension")
+    if T == 1:
+        ld = p.rows
+    elif ld < p.rows:
+        raise ValueError(f"pre has overlapping rows (stride {ld} for {p.rows} columns)")
     # one half behind the other, or their rows in turn
-    if half < (T - 1) * ld + p.rows and not p.rows <= half <= ld - p.rows:
+    if half < (T - 1) * ld + p.rows and not (T > 1 and p.rows <= half <= ld - p.rows):
         raise ValueError("the two halves of pre overlap")
     return ld
 
 
-def _glu_key(what: str, p: Packed, T: int, dev: int) -> tuple:
-    return what, p.rows, p.K, p.N, p.M, p.dtype, T, dev
+def _glu_key(what: str, p: Packed, T: int, rows, dev: int) -> tuple:
+    return what, p.rows, p.K, p.N, p.M, p.dtype, T, rows, dev
 
 
 def glu_workspace_size(gate: Packed, up: Packed, T: int) -> int:
-    """nm_glu_workspace_size: bytes of workspace glu() may need."""
+    """nm_glu_workspace_size: bytes of workspace glu() may need for T rows of
+    any stride and alignment."""
     n = ctypes.c_size_t()
-    _check(lib().nm_glu_workspace_size(_descriptor(gate), _descriptor(up), T, ctypes.byref(n)),
+    _check(lib().nm_glu_workspace_size(_descriptor(gate), _descriptor(up), None, 0, T, ctypes.byref(n)),
            "nm_glu_workspace_size")
     return n.value
 
@@ -643,9 +650,11 @@ def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torc
     dev = _one_gpu("Xt", Xt, ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
                    ("up meta", up.meta), ("out", out), ("pre", pre))
     L, dg, du = lib(), _descriptor(gate), _descriptor(up)
-    need = _sized(L.nm_glu_workspace_size, "nm_glu_workspace_size", _glu_key("glu", gate, T, dev), dg, du, T)
+    x = Xt.data_ptr()
+    need = _sized(L.nm_glu_workspace_size, "nm_glu_workspace_size", _glu_key("glu", gate, T, (x % 16, ldx), dev), dg,
+                  du, x, ldx, T)
     ws, wp, wn = _workspace(workspace, need, dev)
-    _call(dev, L.nm_glu, "nm_glu", dg, du, Xt.data_ptr(), ldx, T, out.data_ptr(), ldh, a, g, u, ldp, wp, wn)
+    _call(dev, L.nm_glu, "nm_glu", dg, du, x, ldx, T, out.data_ptr(), ldh, a, g, u, ldp, wp, wn)
     return out
 
 
@@ -676,7 +685,7 @@ def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, 
                    ("up meta", up.meta), ("pre", pre), ("dH", dH))
     L, dg, du = lib(), _descriptor(gate), _descriptor(up)
     need = _sized(L.nm_glu_backward_workspace_size, "nm_glu_backward_workspace_size",
-                  _glu_key("glu_backward", gate, T, dev), dg, du, T)
+                  _glu_key("glu_backward", gate, T, None, dev), dg, du, T)
     ws, wp, wn = _workspace(workspace, need, dev)
     dX = Xt.new_empty((T, K)) if need_dx else None
     dWg = Xt.new_empty((R, K)) if need_dw else None
@@ -761,9 +770,11 @@ def mx_dequantize(m: Mx, out_dtype: torch.dtype = torch.float32, out: torch.Tens
 
 
 def mx_workspace_size(w: Mx, T: int, glu: bool = False) -> int:
-    """nm_mx_workspace_size: bytes of workspace mx_linear() / mx_glu() may need."""
+    """nm_mx_workspace_size: bytes of workspace mx_linear() / mx_glu() may need
+    for T tokens of any form, stride and alignment."""
     n = ctypes.c_size_t()
-    _check(lib().nm_mx_workspace_size(_descriptor(w), T, int(glu), ctypes.byref(n)), "nm_mx_workspace_size")
+    _check(lib().nm_mx_workspace_size(_descriptor(w), None, None, 0, 0, T, int(glu), ctypes.byref(n)),
+           "nm_mx_workspace_size")
     return n.value
 
 
@@ -791,8 +802,9 @@ def _mx_operands(w: Mx, X, out_dtype, out, workspace, glu: bool, *others):
     ydt = _float_type("out", out.dtype)
     ldy = _row_pitch("out", out, T, w.rows)
     dev = _one_gpu("X", x0, ("weight codes", w.codes), ("weight scales", w.scales), ("out", out), *others)
-    need = _sized(lib().nm_mx_workspace_size, "nm_mx_workspace_size", ("mx", w.rows, w.K, T, glu, dev),
-                  _descriptor(w), T, int(glu))
+    rows = None if xq else (xp % 16, ldx, xdt)
+    need = _sized(lib().nm_mx_workspace_size, "nm_mx_workspace_size", ("mx", w.rows, w.K, T, glu, rows, dev),
+                  _descriptor(w), xq, xp, ldx, xdt, T, int(glu))
     return dev, T, xq, xp, ldx, xdt, out, ldy, ydt, _workspace(workspace, need, dev)
 
 

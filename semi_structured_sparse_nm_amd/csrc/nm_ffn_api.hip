@@ -153,6 +153,11 @@ bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_
 
 size_t mx_ws_codes(int64_t T, int64_t K) { return up256((size_t)nm::mx_codes_bytes(T, K)); }
 size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm::mx_scales_bytes(T, K)); }
+// up to 16 tokens in whole 16-byte pieces are quantised inside the product
+bool mx_in_registers(const void* X, int64_t ldx, int32_t xdt, int64_t T, int64_t K) {
+  const int eb = nm::dtype_bytes(xdt);
+  return T <= 16 && aligned(X, 16) && ldx * eb % 16 == 0 && K * eb % 16 == 0 && row_ok(ldx * eb);
+}
 nm::TilePlan mx_plan(bool glu, int64_t T, int64_t R, int64_t K) {
   return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab),
                        nm::device_cu_count());
@@ -185,10 +190,7 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     if (!float_dtype(xdt) || !aligned(X, (size_t)nm::dtype_bytes(xdt))) return NM_EUNSUPPORTED;
     if ((T + 31) / 32 * (Kp / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
   }
-  const int xeb = xq ? 2 : nm::dtype_bytes(xdt);
-  // up to 16 tokens in whole 16-byte pieces are quantised inside the product
-  const bool in_registers =
-      !xq && T <= 16 && aligned(X, 16) && ldx * xeb % 16 == 0 && K * xeb % 16 == 0 && row_ok(ldx * xeb);
+  const bool in_registers = !xq && mx_in_registers(X, ldx, xdt, T, K);
   const bool few = T <= kFewTokens;
   const nm::TilePlan plan = few ? nm::TilePlan{} : mx_plan(glu, T, R, K);
   const size_t quant = xq || in_registers ? 0 : mx_ws(T, K);
@@ -254,13 +256,15 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
 
 extern "C" {
 
-nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes) {
+nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
+                                size_t* bytes) {
   if (!bytes || T < 1) return NM_EINVAL;
   Geometry g;
   const nm_status st = check_pair(gate, up, &g);
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
-  *bytes = padded_bytes(g, T) + weights_bytes(g, glu_path(g, T));
+  if (Xt && ldx < g.K) return NM_EINVAL;
+  *bytes = (Xt && rows_direct(Xt, ldx, g.K) ? 0 : padded_bytes(g, T)) + weights_bytes(g, glu_path(g, T));
   return NM_OK;
 }
 
@@ -480,13 +484,17 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
              : NM_EHIP;
 }
 
-nm_status nm_mx_workspace_size(const nm_mx* w, int64_t T, int32_t glu, size_t* bytes) {
+nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
+                               int32_t glu, size_t* bytes) {
   if (!bytes || T < 1) return NM_EINVAL;
   const nm_status st = check_mx(w);
   if (st != NM_OK) return st;
   if (!row_ok(nm::mx_kp(w->K) / 2) || T > kMaxLen) return NM_EUNSUPPORTED;
   if ((T + 31) / 32 * (nm::mx_kp(w->K) / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
-  *bytes = mx_ws(T, w->K) + (T > kFewTokens ? part_bytes(mx_plan(glu != 0, T, w->rows, w->K), T, w->rows) : 0);
+  if (Xt && !xq && ldx < w->K) return NM_EINVAL;
+  if (Xt && !xq && !float_dtype(x_dtype)) return NM_EUNSUPPORTED;
+  const bool quant = !xq && !(Xt && mx_in_registers(Xt, ldx, x_dtype, T, w->K));
+  *bytes = (quant ? mx_ws(T, w->K) : 0) + (T > kFewTokens ? part_bytes(mx_plan(glu != 0, T, w->rows, w->K), T, w->rows) : 0);
   return NM_OK;
 }
 

@@ -45,10 +45,15 @@ def test_glu_workspace():
     n = ctypes.c_size_t()
     f = nm.lib().nm_glu_workspace_size
     g, u = _w(R=50, K=100), _w(R=50, K=100)
-    assert f(ctypes.byref(g), ctypes.byref(u), 5, ctypes.byref(n)) == nm.NM_OK and n.value == 5 * 128 * 2
-    assert f(ctypes.byref(g), ctypes.byref(u), 0, ctypes.byref(n)) == EINVAL
-    assert f(ctypes.byref(g), ctypes.byref(u), 5, None) == EINVAL
-    assert f(ctypes.byref(g), ctypes.byref(_w(R=51, K=100)), 5, ctypes.byref(n)) == EINVAL
+    assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 5, ctypes.byref(n)) == nm.NM_OK and n.value == 5 * 128 * 2
+    assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 0, ctypes.byref(n)) == EINVAL
+    assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 5, None) == EINVAL
+    assert f(ctypes.byref(g), ctypes.byref(u), P[0], 99, 5, ctypes.byref(n)) == EINVAL
+    assert f(ctypes.byref(g), ctypes.byref(_w(R=51, K=100)), None, 0, 5, ctypes.byref(n)) == EINVAL
+    # rows the kernels read as they are, and not
+    d = _w(R=50, K=104)
+    for X, ldx, want in ((P[0], 104, 0), (P[0] + 16, 112, 0), (P[0] + 2, 104, 1280), (P[0], 105, 1280)):
+        assert f(ctypes.byref(d), ctypes.byref(d), X, ldx, 5, ctypes.byref(n)) == nm.NM_OK and n.value == want
     b = nm.lib().nm_glu_backward_workspace_size
     assert b(ctypes.byref(g), ctypes.byref(u), 5, ctypes.byref(n)) == nm.NM_OK and n.value > 0
     assert b(ctypes.byref(g), ctypes.byref(u), 1 << 22, ctypes.byref(n)) == EUNSUP
@@ -79,6 +84,21 @@ def test_glu_backward_refusals():
                 lddw=1 << 12, wsb=1 << 62) == EUNSUP
 
 
+def test_mx_workspace():
+    n = ctypes.c_size_t()
+    f = nm.lib().nm_mx_workspace_size
+    w, x = _mx(40, 304), _mx(5, 304)
+    b, nb = ctypes.byref(w), ctypes.byref(n)
+    assert f(b, None, None, 0, 0, 5, 0, nb) == nm.NM_OK and n.value == 5 * 256 + 2 * 256
+    for args, want in (((ctypes.byref(x), None, 0, 0, 5), 0), ((None, P[0], 304, nm.NM_BF16, 16), 0),
+                       ((None, P[0], 305, nm.NM_BF16, 5), 1), ((None, P[0] + 2, 304, nm.NM_BF16, 5), 1),
+                       ((None, P[0], 304, nm.NM_F32, 17), 1)):
+        assert f(b, *args, 1, nb) == nm.NM_OK and (n.value > 0) == bool(want), args
+    assert f(b, None, P[0], 303, nm.NM_F16, 5, 0, nb) == EINVAL
+    assert f(b, None, P[0], 304, nm.NM_I8, 5, 0, nb) == EUNSUP
+    assert f(b, None, None, 0, 0, 0, 0, nb) == EINVAL and f(None, None, None, 0, 0, 5, 0, nb) == EINVAL
+
+
 def test_lengths_past_one_launch():
     """Sizes whose launch would pass 2^32 threads are refused."""
     c = ctypes.c_size_t()
@@ -88,12 +108,12 @@ def test_lengths_past_one_launch():
     assert nm.lib().nm_mx_quantize(P[0], 1 << 13, nm.NM_F16, ctypes.byref(m), None) == EUNSUP
     w = _mx(16, 1 << 13)
     f = nm.lib().nm_mx_workspace_size
-    assert f(ctypes.byref(w), 1 << 24, 0, ctypes.byref(c)) == EUNSUP
-    assert f(ctypes.byref(w), 1 << 20, 0, ctypes.byref(c)) == nm.NM_OK
+    assert f(ctypes.byref(w), None, None, 0, 0, 1 << 24, 0, ctypes.byref(c)) == EUNSUP
+    assert f(ctypes.byref(w), None, None, 0, 0, 1 << 20, 0, ctypes.byref(c)) == nm.NM_OK
     assert nm.lib().nm_mx_linear(ctypes.byref(w), None, P[0], 1 << 13, nm.NM_F16, 1 << 24, P[1], 16, nm.NM_F16, None,
                                  0, P[2], 1 << 62, None) == EUNSUP
     g = _w(R=8, K=8)
-    assert nm.lib().nm_glu_workspace_size(ctypes.byref(g), ctypes.byref(g), (1 << 25) + 1, ctypes.byref(c)) == EUNSUP
+    assert nm.lib().nm_glu_workspace_size(ctypes.byref(g), ctypes.byref(g), None, 0, (1 << 25) + 1, ctypes.byref(c)) == EUNSUP
 
 
 def _mx(rows=40, K=300, **kw):
@@ -195,6 +215,12 @@ def test_binding_refuses_before_the_library():
         nm.glu(p, p, X, pre=torch.zeros(3, 16, dtype=torch.float16))
     with pytest.raises(ValueError, match="halves of pre overlap"):
         nm.glu(p, p, X, pre=torch.zeros(1, 3, 16, dtype=torch.float16).expand(2, 3, 16))
+    with pytest.raises(ValueError, match="halves of pre overlap"):
+        nm.glu(p, p, X, pre=torch.zeros(4, 40, dtype=torch.float16).as_strided((2, 3, 16), (30, 40, 1)))
+    with pytest.raises(ValueError, match="pre has overlapping rows"):
+        nm.glu(p, p, X, pre=torch.zeros(2, 1, 16, dtype=torch.float16).expand(2, 3, 16))
+    with pytest.raises(ValueError, match="pre must have unit stride"):
+        nm.glu(p, p, X, pre=torch.zeros(2, 16, 3, dtype=torch.float16).transpose(1, 2))
     pre, dH = torch.zeros(2, 3, 16, dtype=torch.float16), torch.zeros(3, 16, dtype=torch.float16)
     with pytest.raises(ValueError, match="need_dx or need_dw"):
         nm.glu_backward(p, p, X, pre, dH, need_dx=False, need_dw=False)
