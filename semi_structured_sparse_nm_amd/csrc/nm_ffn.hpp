@@ -76,6 +76,7 @@ enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2 };
 // of the reduction for one product, by a model of its time.
 struct TilePlan {
   int shape, split, sps, lead;
+  double time;               // microseconds, by the model
 };
 TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int cus);
 // The same for TILE_BACK's products of T tokens: T x K over 2 R and, twice, R x

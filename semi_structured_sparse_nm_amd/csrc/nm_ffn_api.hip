@@ -16,9 +16,12 @@ int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 // rows the tile kernel addresses with 32-bit offsets: 256 of them within 2^31 bytes
 bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
 
-// Up to this many tokens the weights are streamed (bound by their bytes);
+// Up to this many tokens 4-bit weights are streamed (bound by their bytes);
 // beyond, the tile product shares them between tokens.
 constexpr int64_t kFewTokens = 64;
+
+// Most tokens the packed weights of the gated block are streamed for.
+constexpr int64_t kStreamTokens = 512;
 
 // Longest dimension taken, and most workgroups of 256 threads: a launch has
 // fewer than 2^32 threads.
@@ -83,22 +86,40 @@ enum GluPath {
   GLU_DENSE     // others: dense copies in the workspace, the dense tile product
 };
 
+Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g.eb); }
+
+// By models of both times (microseconds).  Streaming: the packed weights at
+// 5.8 TB/s for every 64 tokens, and the tokens, re-read for every 16 outputs,
+// at 60 TB/s (up to 32 tokens, two workgroups a compute unit) or 29.  Tiles:
+// their own model, and the copies at 5 TB/s.  Measured, streamed and tiles:
+// 11008 x 4096, 2:4 17 and 23 us (16 tokens), 21 and 22 (32), 30 and 22 (64);
+// 4:8 33 and 93 (64), 98 and 112 (256), 149 and 133 (384); 1000 x 3000, 4:8 11
+// and 33 (64), 20 and 33 (512).
 GluPath glu_path(const Geometry& g, int64_t T) {
-  if (g.N == 2 && g.M == 4) {
-    // Streaming re-reads the tokens for every 16 outputs, out of the caches at
-    // about 9.5 TB/s; the weights come at 5.8.  Measured, streamed and sparse
-    // tiles: 11008 x 4096 19 and 23 us (1 token), 24 and 23 (16), 59 and 26
-    // (64); 4096 x 4096 12 and 21 (16), 21 and 21 (64).
-    if (T > kFewTokens) return GLU_SPARSE;
-    const double stream =
-        2.0 + 2.0 * (double)(g.values_bytes() + g.meta_bytes()) / 5.8e6 + (double)(g.nRB * T * g.K * 2) / 9.5e6;
-    return stream <= nm::glu_tile24_time(T, g.R, g.nKB, nm::device_cu_count(), nullptr) ? GLU_STREAM : GLU_SPARSE;
+  const GluPath tiles = g.N == 2 && g.M == 4 ? GLU_SPARSE : nm::repack24_supported(g) ? GLU_REPACK : GLU_DENSE;
+  if (T > kStreamTokens) return tiles;
+  int forced;
+  if (nm::ffn_tile_override("stream", &forced, nullptr)) return forced ? GLU_STREAM : tiles;
+  const int cus = nm::device_cu_count();
+  const double packed = 2.0 * (double)(g.values_bytes() + g.meta_bytes());
+  const double x = (double)(g.nRB * g.K * 2);          // bytes of a token, once for every 16 outputs
+  const int64_t groups = T <= 32 ? 1 : (T + 63) / 64;
+  const double stream = 2.0 + groups * (packed / 5.8e6 + x * (T <= 16 ? 16 : T <= 32 ? 32 : 64) / (T <= 32 ? 60e6 : 29e6));
+  double other;
+  if (tiles == GLU_DENSE) {
+    const int64_t Kp = up64(g.K);
+    other = 5.0 + (packed + 4.0 * g.R * Kp) / 5e6 +
+            nm::plan_tile(nm::TILE_GLU, false, T, g.R, (int)(Kp / 64), cus).time;
+  } else {
+    other = nm::glu_tile24_time(T, g.R, g.nKB, cus, nullptr);
+    if (tiles == GLU_REPACK) {
+      const Geometry d = geometry24(g);
+      other += 8.0 + (packed + 2.0 * (double)(d.values_bytes() + d.meta_bytes())) / 5e6;
+    }
   }
-  if (T <= kFewTokens) return GLU_STREAM;
-  return nm::repack24_supported(g) ? GLU_REPACK : GLU_DENSE;
+  return stream <= other ? GLU_STREAM : tiles;
 }
 
-Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g.eb); }
 // a weight re-packed to 2:4: values, then positions
 size_t repacked_bytes(const Geometry& g) {
   const Geometry d = geometry24(g);

@@ -5,17 +5,24 @@
 // owns one 16-row block of both weights; its NW waves take every NW-th
 // 64-column block, so they read neighbouring blocks at a time, straight to
 // registers (a fragment of a packed block is one contiguous run), U blocks
-// of both weights in flight per wave; the activations come from the caches
-// (every workgroup reads the same rows).  2:4 windows go to the sparse matrix
+// of both weights in flight per wave.  2:4 windows go to the sparse matrix
 // instruction as they are; other patterns are expanded in registers for the
 // dense one.  The waves' sums meet in LDS, added in wave order.
+//
+// Activations come from the caches, 128 bytes of eight tokens a load, and
+// change to the matrix instruction's order in the wave's own LDS.  (Loaded in
+// that order, 16 bytes of each of 16 tokens for every quarter of a load, they
+// pass the vector cache at a quarter of its rate, which bound the call: two
+// 4:8 weights of 11008 x 4096, 16 tokens 22 us against 19 now, 32 tokens 33
+// and 23, 64 tokens 60 and 33.)  At 64 tokens one block in flight leaves the
+// registers for two workgroups on a compute unit (two: 37 us, one workgroup).
 //
 // Expansion of 1 to 4 kept of 8: the kept values of a group are at most two
 // registers, so each of its four dense registers is one byte permute of them.
 // The permutes' selectors depend only on which columns are kept: a table in
 // LDS, 16 bytes for each of the 256 sets of columns, read by the set's bits.
 // (Shifting each value to its place takes about three times the vector
-// instructions, which bound the call: 4:8, 16 tokens, 11008 x 4096 31 us.)
+// instructions, which would bound the call: 4:8, 16 tokens, 11008 x 4096 31 us.)
 #pragma once
 
 #include "nm_expand.hpp"
@@ -133,11 +140,12 @@ struct GluFrag {
 };
 
 template <int WT, int N, int M, int NT>
-__global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
+__global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, int groups) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = kGluWaves;
-  constexpr int U = NT == 1 ? 4 : 2;
+  constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;
   typedef GluFrag<WT, N, M> Frag;
+  // a wave's activations of one block, then its sums
   __shared__ __attribute__((aligned(16))) v4f red[NW][2 * NT][64];
   __shared__ __attribute__((aligned(16))) v4i table[Frag::TABLE ? 256 : 1];
   if constexpr (Frag::TABLE) {
@@ -159,19 +167,28 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t rb = blockIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
+  // workgroups 8 apart (neighbours on their XCD) take the token groups of one row block
+  const int b = blockIdx.x >> 3, q8 = __builtin_amdgcn_readfirstlane(b / groups);
+  const int64_t rb = q8 * 8 + (blockIdx.x & 7);
+  const int64_t t0 = (b - q8 * groups) * (16 * NT);
+  if (rb >= a.g.nRB) return;
   const int nKB = (int)a.g.nKB;
   const int K = (int)a.g.K;
 
-  const uint16_t* xr[NT];
-  bool xv[NT];
+  // activations: load h of token tile j brings rows 8 h .. 8 h + 7 of it, lane l
+  // piece l % 8 (eight columns) of row 8 h + l / 8; tokens past the last
+  // repeat it (their results are not stored)
+  const int piece = lane & 7;
+  const uint16_t* xr[NT][2];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = t0 + 16 * j + li;
-    xv[j] = t < a.T;
-    xr[j] = static_cast<const uint16_t*>(a.X) + (xv[j] ? t : 0) * a.ldx;
-  }
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xr[j][h] = static_cast<const uint16_t*>(a.X) + min(t0 + 16 * j + 8 * h + (lane >> 3), a.T - 1) * a.ldx + 8 * piece;
+  uint8_t* const xs = reinterpret_cast<uint8_t*>(&red[wave][0][0]);
+  const int put = (lane >> 3) * 128 + 16 * (piece ^ (lane >> 3));
+  const int get0 = li * 128 + 16 * ((Frag::kpiece(0, lg) >> 3) ^ (li & 7));
+  const int get1 = li * 128 + 16 * ((Frag::kpiece(1, lg) >> 3) ^ (li & 7));
   v4f ag[NT], au[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) ag[j] = au[j] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -187,20 +204,27 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int k = kb * 64 + Frag::kpiece(p, lg);
-          x[i][j][p] = v4i{0, 0, 0, 0};
-          if (xv[j] && k < K) x[i][j][p] = *reinterpret_cast<const v4i*>(xr[j] + k);
+        for (int h = 0; h < 2; ++h) {
+          x[i][j][h] = v4i{0, 0, 0, 0};
+          if (kb * 64 + 8 * piece < K) x[i][j][h] = *reinterpret_cast<const v4i*>(xr[j][h] + kb * 64);
         }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (b0 + NW * i < nKB) {
 #pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) *reinterpret_cast<v4i*>(xs + 2048 * j + 1024 * h + put) = x[i][j][h];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
         for (int j = 0; j < NT; ++j) {
-          ag[j] = fg[i].mul(x[i][j][0], x[i][j][1], ag[j], table);
-          au[j] = fu[i].mul(x[i][j][0], x[i][j][1], au[j], table);
+          const v4i x0 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get0);
+          const v4i x1 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get1);
+          ag[j] = fg[i].mul(x0, x1, ag[j], table);
+          au[j] = fu[i].mul(x0, x1, au[j], table);
         }
+        __builtin_amdgcn_wave_barrier();
       }
     }
   }
@@ -234,14 +258,14 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a) {
 
 template <int WT, int N, int M>
 hipError_t launch_glu_decode_nm(const GluArgs& a, hipStream_t s) {
-  const unsigned nrb = (unsigned)a.g.nRB;
-  const dim3 block(kGluWaves * 64);
+  const int groups = a.T <= 32 ? 1 : (int)((a.T + 63) / 64);
+  const dim3 grid((unsigned)((a.g.nRB + 7) / 8 * 8 * groups)), block(kGluWaves * 64);
   if (a.T <= 16)
-    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 1>), dim3(nrb, 1), block, 0, s, a);
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 1>), grid, block, 0, s, a, groups);
   else if (a.T <= 32)
-    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 2>), dim3(nrb, 1), block, 0, s, a);
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 2>), grid, block, 0, s, a, groups);
   else
-    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 4>), dim3(nrb, (unsigned)((a.T + 63) / 64)), block, 0, s, a);
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 4>), grid, block, 0, s, a, groups);
   return hipGetLastError();
 }
 

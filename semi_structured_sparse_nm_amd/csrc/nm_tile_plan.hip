@@ -17,7 +17,8 @@ int device_cu_count() {
 
 // The debug override NM_FFN_TILE=<kind>:<shape>[:<split>], kind "tile" (the dense
 // tile product) or "tile24" (the sparse one): that shape, and for a product
-// that takes one that split where its slabs divide into it.  For tests.
+// that takes one that split where its slabs divide into it; kind "stream", 0 or
+// 1: whether the gated block streams its weights.  For tests.
 bool ffn_tile_override(const char* kind, int* shape, int* split) {
   const char* e = getenv("NM_FFN_TILE");
   if (!e) return false;
@@ -65,20 +66,16 @@ template <class F>
 TilePlan best_plan(int smax, int nslab, F&& time) {
   int only = -1, only_split = 0;
   ffn_tile_override("tile", &only, &only_split);
-  TilePlan best{0, 1, nslab, 0};
-  double best_t = 0;
+  TilePlan best{0, 1, nslab, 0, 0};
   for (int i = 0; i < 4; ++i) {
     if (only >= 0 && i != only) continue;
     for (int s = 1; s <= smax; ++s) {
       const int sps = (nslab + s - 1) / s;
       const int split = (nslab + sps - 1) / sps;
       if (split != s || (only_split && smax > 1 && s != std::min(only_split, nslab))) continue;
-      TilePlan p{i, split, sps, 0};
-      const double t = time(kShapes[i], p);
-      if (best_t == 0 || t < best_t) {
-        best_t = t;
-        best = p;
-      }
+      TilePlan p{i, split, sps, 0, 0};
+      p.time = time(kShapes[i], p);
+      if (best.time == 0 || p.time < best.time) best = p;
     }
   }
   return best;

@@ -24,8 +24,8 @@ def _glu(g=None, u=None, X=P[0], ldx=128, T=5, H=P[1], ldh=48, act=2, G=None, U=
 
 def test_glu_refusals():
     L = nm.lib()
-    # a 4:8 weight and more than a few tokens: dense copies in the workspace
-    dense = dict(T=65, g=_w(N=4, M=8), u=_w(N=4, M=8))
+    # a 4:8 weight and many tokens: dense copies in the workspace
+    dense = dict(T=600, g=_w(N=4, M=8), u=_w(N=4, M=8))
     assert L.nm_glu(None, None, P[0], 128, 5, P[1], 48, 2, None, None, 0, None, 0, None) == EINVAL
     for kw in (dict(X=None), dict(H=None), dict(T=0), dict(T=-3), dict(ldx=127), dict(ldh=47), dict(G=P[3], ldp=48),
                dict(U=P[3], ldp=48), dict(G=P[3], U=P[4], ldp=47), dict(u=_w(R=49)), dict(u=_w(K=132)),

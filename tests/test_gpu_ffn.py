@@ -158,8 +158,10 @@ def test_glu_backward_against_differences(act):
 
 @pytest.mark.parametrize("N,M", [(2, 4), (4, 8), (1, 4), (8, 8)])
 @pytest.mark.parametrize("T", [3, 40, 90, 300])
-def test_glu_tokens_are_independent(T, N, M):
+@pytest.mark.parametrize("stream", [0, 1])
+def test_glu_tokens_are_independent(tile, stream, T, N, M):
     """Infinite and NaN activations change no other token's bits."""
+    tile("stream", stream)
     R, K = 150, 200
     pg, pu = weights(R, K, N, M, "bf16", "g")[0], weights(R, K, N, M, "bf16", "u")[0]
     X = normal((T, K), 1.0, "bf16", "X", T)
@@ -310,6 +312,24 @@ def test_glu_tile_shapes(tile, shape, K, N, M):
     h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "silu")
     pre = torch.full((2, T, R), 7.0, dtype=X.dtype, device="cuda")
     check(nm.glu(pg, pu, X, pre=pre), h, eh, "H")
+    check(pre[0], g, eg, "G")
+    check(pre[1], u, eu, "U")
+
+
+@pytest.mark.parametrize("N,M", [(2, 4), (3, 4), (4, 4), (1, 8), (4, 8), (7, 8)])
+@pytest.mark.parametrize("T,R,K", [(1, 300, 1032), (17, 150, 520), (33, 40, 64), (64, 130, 200), (65, 16, 1096),
+                                   (130, 333, 584), (512, 40, 72)])
+@pytest.mark.parametrize("stream", [0, 1])
+def test_glu_streamed_and_not(tile, stream, T, R, K, N, M):
+    """Both ways of every pattern: one to eight groups of tokens, the last short."""
+    dt = "f16" if T % 2 else "bf16"
+    pg, wg, _ = weights(R, K, N, M, dt, "g", N)
+    pu, wu, _ = weights(R, K, N, M, dt, "u", N)
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    tile("stream", stream)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "gelu")
+    pre = torch.full((2, T, R), 7.0, dtype=X.dtype, device="cuda")
+    check(nm.glu(pg, pu, X, act="gelu", pre=pre), h, eh, "H")
     check(pre[0], g, eg, "G")
     check(pre[1], u, eu, "U")
 
