@@ -51,9 +51,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const uint8_t* X, int6
           }
       }
     }
-    uint32_t m = mx_amax8<DT>(x);
-    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    const uint32_t m = quad_max(mx_amax8<DT>(x));
     const uint32_t byte = mx_scale_byte(m);
     uint32_t c = mx_codes8<DT>(x, mx_scale_f32(byte));
     if (byte == 255u) c = 0;

@@ -117,9 +117,7 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int t = (i0 + 2 * u + hx) & 15;
-          uint32_t m = mx_amax8<XDT>(x[u]);
-          m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-          m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+          const uint32_t m = quad_max(mx_amax8<XDT>(x[u]));
           // (a NaN scale makes every product NaN whatever the codes)
           const uint32_t byte = mx_scale_byte(m);
           *reinterpret_cast<uint32_t*>(qw + t * 128 + 16 * ((px >> 2) ^ (t & 7)) + 4 * (px & 3)) =

@@ -67,6 +67,12 @@ __device__ __forceinline__ uint32_t mx_codes8(const uint32_t* x, float scale) {
   return r;
 }
 
+// largest of the four lanes 4 i .. 4 i + 3 (lane exchanges inside the vector unit)
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+}
+
 // bits of the largest magnitude (as binary32) among eight values
 template <int DT>
 __device__ __forceinline__ uint32_t mx_amax8(const uint32_t* x) {
