@@ -38,10 +38,11 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
   constexpr int EB = XDT == NM_F32 ? 4 : 2;
   constexpr int ND = 2 * EB;                           // dwords of eight values
   static_assert(!Q || NT == 1, "activations are quantised here for one token tile");
-  __shared__ __attribute__((aligned(16))) v4f red[NW][NWT * NT][64];
-  // a wave's quantised slab: 16 tokens of 128 bytes (16-byte piece c of token
-  // t at c ^ (t % 8)), then two scales a token and lane group
-  __shared__ __attribute__((aligned(16))) uint8_t qbuf[Q ? NW : 1][Q ? 16 * 128 + 16 * 8 : 16];
+  // a wave's slab of activations: 128 bytes of every token (16-byte piece c of
+  // token t at c ^ (t % 8)), and where it is quantised here two scales a token
+  // and lane group; then its sums
+  constexpr int XBYTES = NT * 2048 + (Q ? 16 * 8 : 0), RBYTES = NWT * NT * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t buf[NW][XBYTES > RBYTES ? XBYTES : RBYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
@@ -68,15 +69,14 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
       const_cast<uint8_t*>(Q ? static_cast<const uint8_t*>(a.X) + t0 * a.ldx * EB : a.xcodes), 0, 0x7fffffff,
       0x00020000);
   const int kbytes = (int)a.K * EB, pitch = (int)a.ldx * EB;
-  uint8_t* const qw = qbuf[Q ? wave : 0];
-  const uint8_t* xc[NT];
-  bool xv[NT];
+  uint8_t* const qw = buf[wave];
+  // quantised activations: load h brings tokens 8 h .. 8 h + 7, lane l piece
+  // l % 8 of token 8 h + l / 8; tokens past the last repeat it (not stored)
+  const uint8_t* xc[2 * NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = t0 + 16 * j + li;
-    xv[j] = t < a.T;
-    xc[j] = Q ? nullptr : a.xcodes + (xv[j] ? t : 0) * ldc + 16 * lq;
-  }
+  for (int h = 0; h < 2 * NT; ++h)
+    xc[h] = Q ? nullptr : a.xcodes + min(t0 + 8 * h + (lane >> 3), a.T - 1) * ldc + 16 * (lane & 7);
+  const int put = (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));
 
   v4f acc[NWT][NT];
 #pragma unroll
@@ -132,19 +132,26 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
       }
       sx[0] = li < tn ? (int)*reinterpret_cast<const uint16_t*>(qw + 16 * 128 + li * 8 + 2 * lq) : 0;
     } else {
+      v4i x[2 * NT];
+#pragma unroll
+      for (int h = 0; h < 2 * NT; ++h) x[h] = *reinterpret_cast<const v4i*>(xc[h] + (int64_t)s * 128);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          fx[j][kk] = v4i{0, 0, 0, 0};
-          if (xv[j]) fx[j][kk] = *reinterpret_cast<const v4i*>(xc[j] + (int64_t)s * 128 + 64 * kk);
-        }
         // token tile t0 / 16 + j: half of the scale unit of its 32 tokens
         const int64_t tt = t0 / 16 + j;
         const int64_t unit = min(tt / 2, (a.T - 1) / 32);
         sx[j] = (int)(*reinterpret_cast<const uint32_t*>(a.xscales + (unit * nslab + s) * 256 + 4 * lane) >>
                       (16 * (int)(tt & 1)));
       }
+#pragma unroll
+      for (int h = 0; h < 2 * NT; ++h) *reinterpret_cast<v4i*>(qw + 1024 * h + put) = x[h];
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          fx[j][kk] = *reinterpret_cast<const v4i*>(qw + 2048 * j + li * 128 + 16 * ((4 * kk + lq) ^ (li & 7)));
+      __builtin_amdgcn_wave_barrier();
     }
 #pragma unroll
     for (int w = 0; w < NWT; ++w)
@@ -154,10 +161,11 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
         acc[w][j] = mx_mul<1, 1>(fw[w][1], fx[j][1], acc[w][j], sw[w], sx[j]);
       }
   }
+  v4f(*const sum)[64] = reinterpret_cast<v4f(*)[64]>(qw);   // this wave's own reads of it are done
 #pragma unroll
   for (int w = 0; w < NWT; ++w)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) red[wave][w * NT + j][lane] = acc[w][j];
+    for (int j = 0; j < NT; ++j) sum[w * NT + j][lane] = acc[w][j];
   __syncthreads();
   for (int q = threadIdx.x; q < 256 * NT; q += NW * 64) {
     const int rr = q & 15, tok = q >> 4;
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
     for (int w = 0; w < NWT; ++w) {
       y[w] = 0.f;
 #pragma unroll
-      for (int p = 0; p < NW; ++p) y[w] += reinterpret_cast<const float*>(&red[p][w * NT + j][ln])[v];
+      for (int p = 0; p < NW; ++p) y[w] += reinterpret_cast<const float*>(buf[p] + ((w * NT + j) * 64 + ln) * 16)[v];
     }
     const int64_t r = rb * 16 + rr, t = t0 + tok;
     if (r < a.R && t < a.T) {
