@@ -16,12 +16,18 @@ int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 // rows the tile kernel addresses with 32-bit offsets: 256 of them within 2^31 bytes
 bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
 
-// Up to this many tokens 4-bit weights are streamed (bound by their bytes);
-// beyond, the tile product shares them between tokens.
-constexpr int64_t kFewTokens = 64;
+// Up to the first number of tokens weights are streamed always, up to the
+// second where that is faster; beyond, the tile product shares them.
+constexpr int64_t kStreamOnly = 32, kStreamTokens = 512;
 
-// Most tokens the packed weights of the gated block are streamed for.
-constexpr int64_t kStreamTokens = 512;
+// Microseconds of a product whose weights (`weights` bytes) are streamed for
+// every 64 of T tokens: at 5.8 TB/s from HBM first, then out of the caches;
+// `x` bytes of each token, re-read for each of `blocks` of 16 outputs, at `rate`
+// bytes/us; and `each` us a workgroup of a compute unit besides.
+double stream_time(int64_t T, int64_t blocks, double weights, double x, double rate, double each, int cus) {
+  const double groups = (double)((T + 63) / 64), b = (double)blocks;
+  return 2.0 + weights / 5.8e6 * (0.4 + 0.6 * groups) + groups * b * (64 * x / rate + each / cus);
+}
 
 // Longest dimension taken, and most workgroups of 256 threads: a launch has
 // fewer than 2^32 threads.
@@ -88,10 +94,8 @@ enum GluPath {
 
 Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g.eb); }
 
-// By models of both times (microseconds).  Streaming: the packed weights at
-// 5.8 TB/s for every 64 tokens, and the tokens, re-read for every 16 outputs,
-// at 60 TB/s (up to 32 tokens, two workgroups a compute unit) or 29.  Tiles:
-// their own model, and the copies at 5 TB/s.  Measured, streamed and tiles:
+// By models of both times: stream_time; the tile product's own, and the copies
+// at 5 TB/s.  Measured, streamed and tiles:
 // 11008 x 4096, 2:4 17 and 23 us (16 tokens), 21 and 22 (32), 30 and 22 (64);
 // 4:8 33 and 93 (64), 98 and 112 (256), 149 and 133 (384); 1000 x 3000, 4:8 11
 // and 33 (64), 20 and 33 (512).
@@ -100,11 +104,10 @@ GluPath glu_path(const Geometry& g, int64_t T) {
   if (T > kStreamTokens) return tiles;
   int forced;
   if (nm::ffn_tile_override("stream", &forced, nullptr)) return forced ? GLU_STREAM : tiles;
+  if (T <= kStreamOnly) return GLU_STREAM;
   const int cus = nm::device_cu_count();
   const double packed = 2.0 * (double)(g.values_bytes() + g.meta_bytes());
-  const double x = (double)(g.nRB * g.K * 2);          // bytes of a token, once for every 16 outputs
-  const int64_t groups = T <= 32 ? 1 : (T + 63) / 64;
-  const double stream = 2.0 + groups * (packed / 5.8e6 + x * (T <= 16 ? 16 : T <= 32 ? 32 : 64) / (T <= 32 ? 60e6 : 29e6));
+  const double stream = stream_time(T, g.nRB, packed, 2.0 * g.K, 35e6, 0.8, cus);
   double other;
   if (tiles == GLU_DENSE) {
     const int64_t Kp = up64(g.K);
@@ -179,9 +182,28 @@ bool mx_in_registers(const void* X, int64_t ldx, int32_t xdt, int64_t T, int64_t
   const int eb = nm::dtype_bytes(xdt);
   return T <= 16 && aligned(X, 16) && ldx * eb % 16 == 0 && K * eb % 16 == 0 && row_ok(ldx * eb);
 }
-nm::TilePlan mx_plan(bool glu, int64_t T, int64_t R, int64_t K) {
-  return nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab),
-                       nm::device_cu_count());
+// How a product of T tokens is computed: the weights streamed for every 64 of
+// them, or the tile product with its plan.  By models of both times.
+// Measured, streamed and tiles: gated block of 11008 x 4096 14.6 and 14.3 us
+// (64 tokens), 23 and 20 (128); of 4096 x 11008 22 and 26 (128), 37 and 27
+// (256); product of 1000 x 3000 5.5 and 12 (256), 7.2 and 12 (512).
+struct MxPath {
+  bool stream;
+  nm::TilePlan plan;
+};
+MxPath mx_path(bool glu, int64_t T, int64_t R, int64_t K) {
+  MxPath p{};
+  int forced = -1;
+  if (T <= kStreamTokens && nm::ffn_tile_override("stream", &forced, nullptr) ? forced : T <= kStreamOnly) {
+    p.stream = true;
+    return p;
+  }
+  const int cus = nm::device_cu_count();
+  p.plan = nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), cus);
+  if (T > kStreamTokens || !forced) return p;
+  const double w = (glu ? 2.0 : 1.0) * (double)(R * nm::mx_kp(K)) * 17 / 32;
+  p.stream = stream_time(T, (R + 15) / 16, w, 0.5 * nm::mx_kp(K), 30e6, 0.3, cus) <= p.plan.time;
+  return p;
 }
 
 nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const void* X, int64_t ldx, int32_t xdt,
@@ -212,10 +234,9 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     if ((T + 31) / 32 * (Kp / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
   }
   const bool in_registers = !xq && mx_in_registers(X, ldx, xdt, T, K);
-  const bool few = T <= kFewTokens;
-  const nm::TilePlan plan = few ? nm::TilePlan{} : mx_plan(glu, T, R, K);
+  const MxPath path = in_registers ? MxPath{true, {}} : mx_path(glu, T, R, K);
   const size_t quant = xq || in_registers ? 0 : mx_ws(T, K);
-  const size_t need = quant + (few ? 0 : part_bytes(plan, T, R));
+  const size_t need = quant + part_bytes(path.plan, T, R);
   if (need && (!ws || ws_bytes < need)) return NM_EINVAL;
   if (need && !aligned(ws, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -230,7 +251,7 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     xscales = sc;
   }
   const nm_mx* ws2[2] = {w0, glu ? w1 : w0};
-  if (few) {
+  if (path.stream) {
     nm::MxDecodeArgs a{};
     for (int i = 0; i < 2; ++i) {
       a.codes[i] = static_cast<const uint8_t*>(ws2[i]->codes);
@@ -269,8 +290,9 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
   a.bias = bias;
   a.act = act;
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + quant);
-  return run_tile(nm::TILE_MX, glu ? nm::TILE_GLU : nm::TILE_LINEAR, ydt, a, plan, part, s) == hipSuccess ? NM_OK
-                                                                                                         : NM_EHIP;
+  return run_tile(nm::TILE_MX, glu ? nm::TILE_GLU : nm::TILE_LINEAR, ydt, a, path.plan, part, s) == hipSuccess
+             ? NM_OK
+             : NM_EHIP;
 }
 
 }  // namespace
@@ -515,7 +537,8 @@ nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, const void* Xt, 
   if (Xt && !xq && ldx < w->K) return NM_EINVAL;
   if (Xt && !xq && !float_dtype(x_dtype)) return NM_EUNSUPPORTED;
   const bool quant = !xq && !(Xt && mx_in_registers(Xt, ldx, x_dtype, T, w->K));
-  *bytes = (quant ? mx_ws(T, w->K) : 0) + (T > kFewTokens ? part_bytes(mx_plan(glu != 0, T, w->rows, w->K), T, w->rows) : 0);
+  const size_t part = quant || xq ? part_bytes(mx_path(glu != 0, T, w->rows, w->K).plan, T, w->rows) : 0;
+  *bytes = (quant ? mx_ws(T, w->K) : 0) + part;
   return NM_OK;
 }
 
