@@ -35,11 +35,11 @@ bool ffn_tile_override(const char* kind, int* shape, int* split) {
 // Microseconds a slab takes with few workgroups running and with one on every
 // compute unit (their operands' traffic, and the power the matrix cores draw,
 // slow each other down), and a tile besides its slabs.  Fitted to products of
-// 64 to 2048 tokens by 768 to 22016 x 768 to 22016; the choice is within 10%
-// of the fastest shape and split there.  For example 2048 tokens, two 4:8
-// weights of 11008 x 4096, gated: 256 x 256 tiles 282 us, 128 x 256 324,
-// 128 x 128 516; 256 tokens: 99, 69 and 99; the gradient of 197 tokens through
-// 4096 x 4096: 256 x 256 160 us, 64 x 128 79, 64 x 128 in two slices 60.
+// 16 to 2048 tokens by 428 to 22016 x 536 to 22016; the choice is within 10%
+// of the fastest shape and split nearly everywhere there.  For example 2048
+// tokens, two 4:8 weights of 11008 x 4096, gated: 256 x 256 tiles 290 us, 128 x
+// 256 306, 128 x 128 498; 256 tokens: 89, 65 and 90; the gradients of 197 tokens
+// through two weights of 768 x 768: 256 x 256 42 us, 64 x 128 in four slices 20.
 namespace {
 
 struct TileShape {
