@@ -6,15 +6,15 @@
 // two lane exchanges, each lane writes its eight codes as one dword, and the
 // unit's scales are gathered in LDS and leave as one 256-byte piece.  Bound by
 // HBM: 2 (or 4) bytes read and 17 / 32 written per element (11008 x 4096 bf16:
-// 20 us, 5.7 TB/s; back to bf16 28 us, 4.1 TB/s).
+// 20 us, 5.7 TB/s; back to bf16 24 us, 4.8 TB/s).
 #include "nm_mx_device.hpp"
 
 namespace nm {
 
 namespace {
 
-template <int DT>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(const uint8_t* X, int64_t ldx, int64_t rows, int64_t K,
+template <int DT, int TH>
+__global__ void __launch_bounds__(TH) mx_quantize_kernel(const uint8_t* X, int64_t ldx, int64_t rows, int64_t K,
                                                           int64_t nslab, uint8_t* codes, uint8_t* scales, bool vec) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int EB = DT == NM_F32 ? 4 : 2;
@@ -22,11 +22,11 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const uint8_t* X, int6
   __shared__ uint8_t sc[256];
   const int64_t slab = blockIdx.x % nslab, grp = blockIdx.x / nslab;
   const int64_t k0 = slab * kMxSlab;
-  sc[threadIdx.x] = 0;
+  if (threadIdx.x < 256) sc[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int q = it * 256 + threadIdx.x;              // 32 pieces of eight per row
+  for (int it = 0; it < 1024 / TH; ++it) {
+    const int q = it * TH + (int)threadIdx.x;              // 32 pieces of eight per row
     const int rl = q >> 5, pc = q & 31;
     const int64_t r = grp * 32 + rl, k = k0 + 8 * pc;
     uint32_t x[ND];
@@ -81,25 +81,29 @@ __device__ __forceinline__ float mx_value(uint32_t code, uint32_t byte) {
   return code & 8 ? -y : y;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+// the quantiser's units and lanes, the other way
+template <int DT, int TH>
+__global__ void __launch_bounds__(TH) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                                             int64_t K, int64_t nslab, void* Y, int64_t ldy,
                                                             bool vec) {
-  const int64_t pr = (K + 7) / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pr; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / pr, k = (i - r * pr) * 8;
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + r * (nslab * 128) + k / 2);
-    const int b = (int)(k & 255) >> 5, rl = (int)(r & 31);
-    const uint32_t byte =
-        scales[((r >> 5) * nslab + (k >> 8)) * 256 + 4 * (16 * (b & 3) + (rl & 15)) + 2 * (rl >> 4) + (b >> 2)];
+  const int64_t slab = blockIdx.x % nslab, grp = blockIdx.x / nslab;
+  const uint8_t* sc = scales + (grp * nslab + slab) * 256;
+#pragma unroll
+  for (int it = 0; it < 1024 / TH; ++it) {
+    const int q = it * TH + (int)threadIdx.x;
+    const int rl = q >> 5, pc = q & 31, b = pc >> 2;
+    const int64_t r = grp * 32 + rl, k = slab * kMxSlab + 8 * pc;
+    if (r >= rows || k >= K) continue;
+    const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + r * (nslab * 128) + slab * 128 + 4 * pc);
+    const uint32_t byte = sc[4 * (16 * (b & 3) + (rl & 15)) + 2 * (rl >> 4) + (b >> 2)];
     float y[8];
-  #pragma unroll
+#pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = mx_value(c >> (4 * e) & 15u, byte);
     const int n = (int)min(K - k, (int64_t)8);
     if constexpr (DT != NM_F32) {
       if (vec && n == 8) {
         uint32_t o[4];
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = pack_16x2<DT>(y[2 * e], y[2 * e + 1]);
         *reinterpret_cast<v4i*>(static_cast<uint16_t*>(Y) + r * ldy + k) =
             v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
@@ -113,19 +117,46 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes
 
 }  // namespace
 
+namespace {
+
+// Threads of a workgroup: 256, four passes over the unit; 1024, one pass, where
+// there are few units (197 x 770: 4.6 us, both ways, against 5.6 and 6.8).
+bool few_units(int64_t units) { return units < 4 * device_cu_count(); }
+
+template <int DT>
+void quantize(const uint8_t* x, int64_t ldx, int64_t rows, int64_t K, int64_t nslab, uint8_t* codes, uint8_t* scales,
+              bool vec, hipStream_t s) {
+  const unsigned units = (unsigned)((rows + 31) / 32 * nslab);
+  if (few_units(units))
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, 1024>), dim3(units), dim3(1024), 0, s, x, ldx, rows, K, nslab, codes,
+                       scales, vec);
+  else
+    hipLaunchKernelGGL((mx_quantize_kernel<DT, 256>), dim3(units), dim3(256), 0, s, x, ldx, rows, K, nslab, codes,
+                       scales, vec);
+}
+
+template <int DT>
+void dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, int64_t nslab, void* Y,
+                int64_t ldy, bool vec, hipStream_t s) {
+  const unsigned units = (unsigned)((rows + 31) / 32 * nslab);
+  if (few_units(units))
+    hipLaunchKernelGGL((mx_dequantize_kernel<DT, 1024>), dim3(units), dim3(1024), 0, s, codes, scales, rows, K, nslab,
+                       Y, ldy, vec);
+  else
+    hipLaunchKernelGGL((mx_dequantize_kernel<DT, 256>), dim3(units), dim3(256), 0, s, codes, scales, rows, K, nslab, Y,
+                       ldy, vec);
+}
+
+}  // namespace
+
 hipError_t launch_mx_quantize(const void* X, int64_t ldx, int xdt, int64_t rows, int64_t K, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
   const int64_t nslab = mx_kp(K) / kMxSlab;
   const int eb = xdt == NM_F32 ? 4 : 2;
   const bool vec = (uintptr_t)X % 16 == 0 && ldx * eb % 16 == 0;
-  const dim3 grid((unsigned)((rows + 31) / 32 * nslab)), block(256);
   const uint8_t* x = static_cast<const uint8_t*>(X);
-  if (xdt == NM_F16)
-    hipLaunchKernelGGL((mx_quantize_kernel<NM_F16>), grid, block, 0, s, x, ldx, rows, K, nslab, codes, scales, vec);
-  else if (xdt == NM_BF16)
-    hipLaunchKernelGGL((mx_quantize_kernel<NM_BF16>), grid, block, 0, s, x, ldx, rows, K, nslab, codes, scales, vec);
-  else
-    hipLaunchKernelGGL((mx_quantize_kernel<NM_F32>), grid, block, 0, s, x, ldx, rows, K, nslab, codes, scales, vec);
+  auto f = xdt == NM_F16 ? quantize<NM_F16> : xdt == NM_BF16 ? quantize<NM_BF16> : quantize<NM_F32>;
+  f(x, ldx, rows, K, nslab, codes, scales, vec, s);
   return hipGetLastError();
 }
 
@@ -133,14 +164,8 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
                                 int64_t ldy, int ydt, hipStream_t s) {
   const int64_t nslab = mx_kp(K) / kMxSlab;
   const bool vec = ydt == NM_F32 ? vec4_ok(Y, ldy, 4) : (uintptr_t)Y % 16 == 0 && ldy % 8 == 0;
-  const int64_t n = rows * ((K + 7) / 8);
-  const dim3 grid(grid_1d(n, 256)), block(256);
-  if (ydt == NM_F16)
-    hipLaunchKernelGGL((mx_dequantize_kernel<NM_F16>), grid, block, 0, s, codes, scales, rows, K, nslab, Y, ldy, vec);
-  else if (ydt == NM_BF16)
-    hipLaunchKernelGGL((mx_dequantize_kernel<NM_BF16>), grid, block, 0, s, codes, scales, rows, K, nslab, Y, ldy, vec);
-  else
-    hipLaunchKernelGGL((mx_dequantize_kernel<NM_F32>), grid, block, 0, s, codes, scales, rows, K, nslab, Y, ldy, vec);
+  auto f = ydt == NM_F16 ? dequantize<NM_F16> : ydt == NM_BF16 ? dequantize<NM_BF16> : dequantize<NM_F32>;
+  f(codes, scales, rows, K, nslab, Y, ldy, vec, s);
   return hipGetLastError();
 }
 
