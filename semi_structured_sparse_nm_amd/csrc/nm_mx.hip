@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(TH) mx_quantize_kernel(const uint8_t* X, int64
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int EB = DT == NM_F32 ? 4 : 2;
   constexpr int ND = 8 * EB / 4;                       // dwords of eight elements
-  __shared__ uint8_t sc[256];
+  __shared__ __attribute__((aligned(16))) uint8_t sc[256];
   const int64_t slab = blockIdx.x % nslab, grp = blockIdx.x / nslab;
   const int64_t k0 = slab * kMxSlab;
   if (threadIdx.x < 256) sc[threadIdx.x] = 0;
