@@ -397,7 +397,8 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, cons
  * ldp < R, descriptors whose sizes or versions are wrong or whose shape, N:M
  * or dtype differ, a small workspace.  NM_EUNSUPPORTED: int8 weights, act not
  * listed, pointers not aligned to their element, a workspace not 256-byte
- * aligned, rows of K so long that 256 of them pass 2^31 bytes, T > 2^25.
+ * aligned, rows of K so long that 256 of them pass 2^31 bytes, T > 2^25, R >
+ * 2^22.
  */
 nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
                  int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, void* workspace,

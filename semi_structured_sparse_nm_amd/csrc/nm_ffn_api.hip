@@ -71,8 +71,8 @@ nm_status check_pair(const nm_packed* gate, const nm_packed* up, Geometry* g) {
   if (gate->rows != up->rows || gate->K != up->K || gate->N != up->N || gate->M != up->M || gate->dtype != up->dtype)
     return NM_EINVAL;
   if (gate->dtype != NM_F16 && gate->dtype != NM_BF16) return NM_EUNSUPPORTED;
-  // dense rows of K within the tile kernel's offsets; grid limits along R
-  if (!row_ok(up64(g->K) * 2) || g->R > 65535ll * 64) return NM_EUNSUPPORTED;
+  // dense rows of K within the tile kernel's offsets; launches along R
+  if (!row_ok(up64(g->K) * 2) || g->R > (1ll << 22)) return NM_EUNSUPPORTED;
   return NM_OK;
 }
 
@@ -202,7 +202,7 @@ MxPath mx_path(bool glu, int64_t T, int64_t R, int64_t K) {
   p.plan = nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), cus);
   if (T > kStreamTokens || !forced) return p;
   const double w = (glu ? 2.0 : 1.0) * (double)(R * nm::mx_kp(K)) * 17 / 32;
-  p.stream = stream_time(T, (R + 15) / 16, w, 0.5 * nm::mx_kp(K), 30e6, 0.3, cus) <= p.plan.time;
+  if (stream_time(T, (R + 15) / 16, w, 0.5 * nm::mx_kp(K), 30e6, 0.3, cus) <= p.plan.time) p = MxPath{true, {}};
   return p;
 }
 

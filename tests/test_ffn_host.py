@@ -37,6 +37,8 @@ def test_glu_refusals():
     for kw in (dict(g=_w(**i8), u=_w(**i8)), dict(act=0), dict(act=3), dict(X=P[0] + 1), dict(H=P[1] + 1),
                dict(G=P[3] + 1, U=P[4], ldp=48), dict(**dense, ws=P[2] + 16), dict(T=(1 << 30) + 1)):
         assert _glu(**kw) == EUNSUP, kw
+    big = dict(R=(1 << 22) + 16, K=8)
+    assert _glu(g=_w(**big), u=_w(**big), ldx=8, ldh=big["R"]) == EUNSUP
     big = dict(R=16, K=1 << 22)
     assert _glu(g=_w(**big), u=_w(**big), ldx=1 << 22) == EUNSUP
 
