@@ -335,8 +335,13 @@ hipError_t launch_tile_op(const TileArgs& a, hipStream_t s) {
       if constexpr (ET == TILE_MX) return launch_tile_cfg<ET, OP, OUT, 256, 256, 4, 2, 2>(a, s);
       else return launch_tile_cfg<ET, OP, OUT, 256, 256, 2, 4, 2>(a, s);
     case 1: return launch_tile_cfg<ET, OP, OUT, 128, 256, 2, 4, 3>(a, s);
-    case 2: return launch_tile_cfg<ET, OP, OUT, 128, 128, 2, 2, 4>(a, s);
-    default: return launch_tile_cfg<ET, OP, OUT, 64, 128, 2, 2, 6>(a, s);
+    case 2:
+      if constexpr (OP == TILE_GLU) return launch_tile_cfg<ET, OP, OUT, 128, 128, 4, 2, 4>(a, s);
+      else return launch_tile_cfg<ET, OP, OUT, 128, 128, 2, 4, 4>(a, s);
+    default:
+      if constexpr (OP == TILE_GLU && ET == TILE_MX) return launch_tile_cfg<ET, OP, OUT, 64, 128, 2, 2, 6>(a, s);
+      else if constexpr (OP == TILE_GLU) return launch_tile_cfg<ET, OP, OUT, 64, 128, 4, 2, 6>(a, s);
+      else return launch_tile_cfg<ET, OP, OUT, 64, 128, 2, 4, 6>(a, s);
   }
 }
 
