@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(256) expand_dense_kernel(Geometry g, DenseArgs
 }
 
 template <int WT>
-__device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, bool vec, float (&f)[8]) {
-  if (vec && r + 8 <= R) {
-    const v4i x = *reinterpret_cast<const v4i*>(p + r);
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, float (&f)[8]) {
+  if (r + 8 <= R) {
+    const v4i x = load16(p + r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = from_16<WT>(((uint32_t)x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
   } else {
@@ -130,9 +130,9 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
     uint32_t og[4] = {0u, 0u, 0u, 0u}, ou[4] = {0u, 0u, 0u, 0u};
     if (t < a.T && r < a.g.R) {
       float h[8], g[8], u[8];
-      load8<WT>(a.dH + t * a.lddh, r, a.g.R, a.vec_h, h);
-      load8<WT>(a.G + t * a.ldp, r, a.g.R, a.vec_h, g);
-      load8<WT>(a.U + t * a.ldp, r, a.g.R, a.vec_h, u);
+      load8<WT>(a.dH + t * a.lddh, r, a.g.R, h);
+      load8<WT>(a.G + t * a.ldp, r, a.g.R, g);
+      load8<WT>(a.U + t * a.ldp, r, a.g.R, u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float dg[2], du[2];
@@ -220,8 +220,8 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
     uint32_t o[4] = {0u, 0u, 0u, 0u};
     if (t < a.T) {
       const uint16_t* x = a.X + t * a.ldx + k;
-      if (a.vec_x && k + 8 <= K) {
-        const v4i v = *reinterpret_cast<const v4i*>(x);
+      if (k + 8 <= K) {
+        const v4i v = load16(x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = (uint32_t)v[i];
       } else {
@@ -260,11 +260,15 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_
   const int64_t pr = Kp / 8;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * pr; i += (int64_t)gridDim.x * 256) {
     const int64_t t = i / pr, k = (i - t * pr) * 8;
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    v4i o = {0, 0, 0, 0};
+    if (k + 8 <= K) {
+      o = load16(X + t * ldx + k);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k + e < K) o[e >> 1] |= (uint32_t)X[t * ldx + k + e] << (16 * (e & 1));
-    *reinterpret_cast<v4i*>(Y + t * Kp + k) = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) o[e >> 1] |= (int)((uint32_t)X[t * ldx + k + e] << (16 * (e & 1)));
+    }
+    *reinterpret_cast<v4i*>(Y + t * Kp + k) = o;
   }
 }
 
@@ -276,10 +280,7 @@ hipError_t launch_expand_dense(const Geometry& g, const DenseArgs& a, hipStream_
   return hipGetLastError();
 }
 
-hipError_t launch_glu_prepare(PrepareArgs a, int wdt, hipStream_t s) {
-  a.vec_h = a.lddh % 8 == 0 && a.ldp % 8 == 0 && (uintptr_t)a.dH % 16 == 0 && (uintptr_t)a.G % 16 == 0 &&
-            (uintptr_t)a.U % 16 == 0;
-  a.vec_x = a.ldx % 8 == 0 && (uintptr_t)a.X % 16 == 0;
+hipError_t launch_glu_prepare(const PrepareArgs& a, int wdt, hipStream_t s) {
   const int64_t n_act = (a.T + 63) / 64 * (a.Rp / 64);
   const int64_t n_weight = 2 * ((a.g.R + 127) / 128) * a.g.nKB;
   const int64_t n_x = a.xt ? a.Tp / 64 * a.g.nKB : 0;

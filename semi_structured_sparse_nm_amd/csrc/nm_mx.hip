@@ -15,7 +15,7 @@ namespace {
 
 template <int DT, int TH>
 __global__ void __launch_bounds__(TH) mx_quantize_kernel(const uint8_t* X, int64_t ldx, int64_t rows, int64_t K,
-                                                          int64_t nslab, uint8_t* codes, uint8_t* scales, bool vec) {
+                                                          int64_t nslab, uint8_t* codes, uint8_t* scales) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int EB = DT == NM_F32 ? 4 : 2;
   constexpr int ND = 8 * EB / 4;                       // dwords of eight elements
@@ -34,10 +34,10 @@ __global__ void __launch_bounds__(TH) mx_quantize_kernel(const uint8_t* X, int64
     for (int i = 0; i < ND; ++i) x[i] = 0;
     if (r < rows && k < K) {
       const uint8_t* p = X + (r * ldx + k) * EB;
-      if (vec && k + 8 <= K) {
+      if (k + 8 <= K) {
 #pragma unroll
         for (int i = 0; i < ND / 4; ++i) {
-          const v4i v = reinterpret_cast<const v4i*>(p)[i];
+          const v4i v = load16(p + 16 * i);
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[4 * i + e] = (uint32_t)v[e];
         }
@@ -84,8 +84,8 @@ __device__ __forceinline__ float mx_value(uint32_t code, uint32_t byte) {
 // the quantiser's units and lanes, the other way
 template <int DT, int TH>
 __global__ void __launch_bounds__(TH) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
-                                                            int64_t K, int64_t nslab, void* Y, int64_t ldy,
-                                                            bool vec) {
+                                                            int64_t K, int64_t nslab, void* Y,
+                                                            int64_t ldy) {
   const int64_t slab = blockIdx.x % nslab, grp = blockIdx.x / nslab;
   const uint8_t* sc = scales + (grp * nslab + slab) * 256;
 #pragma unroll
@@ -101,17 +101,17 @@ __global__ void __launch_bounds__(TH) mx_dequantize_kernel(const uint8_t* codes,
     for (int e = 0; e < 8; ++e) y[e] = mx_value(c >> (4 * e) & 15u, byte);
     const int n = (int)min(K - k, (int64_t)8);
     if constexpr (DT != NM_F32) {
-      if (vec && n == 8) {
+      if (n == 8) {
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = pack_16x2<DT>(y[2 * e], y[2 * e + 1]);
-        *reinterpret_cast<v4i*>(static_cast<uint16_t*>(Y) + r * ldy + k) =
-            v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+        *reinterpret_cast<v4i_any*>(static_cast<uint16_t*>(Y) + r * ldy + k) =
+            v4i_any{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
         continue;
       }
     }
-    store4<DT>(Y, r * ldy + k, y, min(n, 4), vec);
-    if (n > 4) store4<DT>(Y, r * ldy + k + 4, y + 4, n - 4, vec);
+    store4<DT>(Y, r * ldy + k, y, min(n, 4));
+    if (n > 4) store4<DT>(Y, r * ldy + k + 4, y + 4, n - 4);
   }
 }
 
@@ -125,26 +125,26 @@ bool few_units(int64_t units) { return units < 4 * device_cu_count(); }
 
 template <int DT>
 void quantize(const uint8_t* x, int64_t ldx, int64_t rows, int64_t K, int64_t nslab, uint8_t* codes, uint8_t* scales,
-              bool vec, hipStream_t s) {
+              hipStream_t s) {
   const unsigned units = (unsigned)((rows + 31) / 32 * nslab);
   if (few_units(units))
     hipLaunchKernelGGL((mx_quantize_kernel<DT, 1024>), dim3(units), dim3(1024), 0, s, x, ldx, rows, K, nslab, codes,
-                       scales, vec);
+                       scales);
   else
     hipLaunchKernelGGL((mx_quantize_kernel<DT, 256>), dim3(units), dim3(256), 0, s, x, ldx, rows, K, nslab, codes,
-                       scales, vec);
+                       scales);
 }
 
 template <int DT>
 void dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, int64_t nslab, void* Y,
-                int64_t ldy, bool vec, hipStream_t s) {
+                int64_t ldy, hipStream_t s) {
   const unsigned units = (unsigned)((rows + 31) / 32 * nslab);
   if (few_units(units))
     hipLaunchKernelGGL((mx_dequantize_kernel<DT, 1024>), dim3(units), dim3(1024), 0, s, codes, scales, rows, K, nslab,
-                       Y, ldy, vec);
+                       Y, ldy);
   else
     hipLaunchKernelGGL((mx_dequantize_kernel<DT, 256>), dim3(units), dim3(256), 0, s, codes, scales, rows, K, nslab, Y,
-                       ldy, vec);
+                       ldy);
 }
 
 }  // namespace
@@ -152,20 +152,17 @@ void dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64
 hipError_t launch_mx_quantize(const void* X, int64_t ldx, int xdt, int64_t rows, int64_t K, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
   const int64_t nslab = mx_kp(K) / kMxSlab;
-  const int eb = xdt == NM_F32 ? 4 : 2;
-  const bool vec = (uintptr_t)X % 16 == 0 && ldx * eb % 16 == 0;
   const uint8_t* x = static_cast<const uint8_t*>(X);
   auto f = xdt == NM_F16 ? quantize<NM_F16> : xdt == NM_BF16 ? quantize<NM_BF16> : quantize<NM_F32>;
-  f(x, ldx, rows, K, nslab, codes, scales, vec, s);
+  f(x, ldx, rows, K, nslab, codes, scales, s);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* Y,
                                 int64_t ldy, int ydt, hipStream_t s) {
   const int64_t nslab = mx_kp(K) / kMxSlab;
-  const bool vec = ydt == NM_F32 ? vec4_ok(Y, ldy, 4) : (uintptr_t)Y % 16 == 0 && ldy % 8 == 0;
   auto f = ydt == NM_F16 ? dequantize<NM_F16> : ydt == NM_BF16 ? dequantize<NM_BF16> : dequantize<NM_F32>;
-  f(codes, scales, rows, K, nslab, Y, ldy, vec, s);
+  f(codes, scales, rows, K, nslab, Y, ldy, s);
   return hipGetLastError();
 }
 

@@ -105,15 +105,16 @@ struct TileWalk {
 };
 
 // Outputs of one row m: per pair of 16-column tiles i, i + 1 lane group lq
-// holds columns 4 lq .. + 3 of each.  Where rows allow 16-byte stores, two
-// lane exchanges leave it with columns 8 lq .. + 7 of the pair's 32, so a row
-// leaves in 64-byte pieces.
+// holds columns 4 lq .. + 3 of each.  Two lane exchanges leave it with columns
+// 8 lq .. + 7 of the pair's 32, so a 16-bit row leaves in 64-byte pieces: past
+// the caches where rows are whole pieces, through them where they start
+// anywhere (past them 2048 x 4098 outputs at 4 bits, K 4096, take 39 us against 32).
 // y0, y1: the lane's four values of each tile; n: first column of the pair.
 template <int OUT>
 __device__ __forceinline__ void store_pair(void* C, int64_t row, int64_t n, int64_t N, int lq, const float* y0,
-                                           const float* y1, bool vec8, bool vec4) {
+                                           const float* y1, bool whole) {
   if constexpr (OUT != NM_F32) {
-    if (vec8 && n + 32 <= N) {
+    if (n + 32 <= N) {
       uint32_t a0 = pack_16x2<OUT>(y0[0], y0[1]), a1 = pack_16x2<OUT>(y0[2], y0[3]);
       uint32_t b0 = pack_16x2<OUT>(y1[0], y1[1]), b1 = pack_16x2<OUT>(y1[2], y1[3]);
       // lane groups of a: 0 1 2 3, of b: 4 5 6 7 -> (0 1 | 4 5), (2 3 | 6 7) -> (0 2 4 6), (1 3 5 7)
@@ -126,7 +127,9 @@ __device__ __forceinline__ void store_pair(void* C, int64_t row, int64_t n, int6
       swap(a0, b0);
       swap(a1, b1);
       const v4i v = {(int)a0, (int)a1, (int)b0, (int)b1};
-      __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(static_cast<uint16_t*>(C) + row + n + 8 * lq));
+      uint16_t* p = static_cast<uint16_t*>(C) + row + n + 8 * lq;
+      if (whole) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(p));
+      else *reinterpret_cast<v4i_any*>(p) = v;
       return;
     }
   }
@@ -134,13 +137,12 @@ __device__ __forceinline__ void store_pair(void* C, int64_t row, int64_t n, int6
   for (int h = 0; h < 2; ++h) {
     const int64_t c = n + 16 * h + 4 * lq;
     const int left = (int)min(N - c, (int64_t)4);
-    if (left > 0) store4<OUT>(C, row + c, h ? y1 : y0, left, vec4);
+    if (left > 0) store4<OUT>(C, row + c, h ? y1 : y0, left);
   }
 }
 
-__device__ __forceinline__ bool rows_vec(const void* p, int64_t ld, int n, int eb) {
-  return ld % n == 0 && (uintptr_t)p % (n * eb) == 0;
-}
+// whether rows of ld 16-bit elements from p are whole 16-byte pieces
+__device__ __forceinline__ bool whole_pieces(const void* p, int64_t ld) { return ld % 8 == 0 && (uintptr_t)p % 16 == 0; }
 
 // One wave's TN x TM tiles of 16 x 16 as rows of C [Mr][ldc]: lane (li, lq)
 // holds n = n0 + 16 i + 4 lq + v of row m0 + 16 j + li.  MASKED: zero where
@@ -150,8 +152,7 @@ __device__ __forceinline__ void tile_rows(void* C, int64_t ldc, int64_t Mr, int6
                                           const uint8_t* mask, int64_t ldm, int64_t m0, int64_t n0,
                                           const v4f (&acc)[TN][TM]) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
-  constexpr int EB = OUT == NM_F32 ? 4 : 2;
-  const bool v8 = rows_vec(C, ldc, 8, EB), v4 = rows_vec(C, ldc, 4, EB);
+  const bool whole = whole_pieces(C, ldc);
   // the kept bits of every row and column pair (32 columns, one word: rows of
   // the mask are padded to 64), in flight together before the first use
   uint32_t keep[MASKED ? TN / 2 : 1][TM];
@@ -192,7 +193,7 @@ __device__ __forceinline__ void tile_rows(void* C, int64_t ldc, int64_t Mr, int6
         }
       }
       __builtin_amdgcn_sched_barrier(0);                // one output's temporaries at a time
-      if (m < Mr) store_pair<OUT>(C, m * ldc, n0 + 16 * i, Nr, lq, y[0], y[1], v8, v4);
+      if (m < Mr) store_pair<OUT>(C, m * ldc, n0 + 16 * i, Nr, lq, y[0], y[1], whole);
     }
   }
 }
@@ -204,11 +205,9 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
                                               const v4f (&acc)[TN][TM]) {
   if constexpr (OP == TILE_GLU) {
     const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
-    constexpr int EB = OUT == NM_F32 ? 4 : 2;
     constexpr int H = TN / 2;
-    const bool v8 = rows_vec(a.C, a.ldc, 8, EB), v4 = rows_vec(a.C, a.ldc, 4, EB);
-    const bool p8 = a.P[0] && rows_vec(a.P[0], a.ldp, 8, EB) && rows_vec(a.P[1], a.ldp, 8, EB);
-    const bool p4 = a.P[0] && rows_vec(a.P[0], a.ldp, 4, EB) && rows_vec(a.P[1], a.ldp, 4, EB);
+    const bool whole = whole_pieces(a.C, a.ldc);
+    const bool kept = whole_pieces(a.P[0], a.ldp) && whole_pieces(a.P[1], a.ldp);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const int64_t m = m0 + 16 * j + li;
@@ -225,10 +224,10 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
           }
         __builtin_amdgcn_sched_barrier(0);              // one output's temporaries at a time
         if (m < a.Mr) {
-          store_pair<OUT>(a.C, m * a.ldc, n0 + 16 * i, a.Nr, lq, h[0], h[1], v8, v4);
+          store_pair<OUT>(a.C, m * a.ldc, n0 + 16 * i, a.Nr, lq, h[0], h[1], whole);
           if (a.P[0]) {
-            store_pair<OUT>(a.P[0], m * a.ldp, n0 + 16 * i, a.Nr, lq, g[0], g[1], p8, p4);
-            store_pair<OUT>(a.P[1], m * a.ldp, n0 + 16 * i, a.Nr, lq, u[0], u[1], p8, p4);
+            store_pair<OUT>(a.P[0], m * a.ldp, n0 + 16 * i, a.Nr, lq, g[0], g[1], kept);
+            store_pair<OUT>(a.P[1], m * a.ldp, n0 + 16 * i, a.Nr, lq, u[0], u[1], kept);
           }
         }
       }

@@ -117,8 +117,7 @@ namespace {
 
 template <int OUT>
 __global__ void __launch_bounds__(256) tile_reduce_kernel(const float* part, int split, int64_t T, int64_t R,
-                                                          const float* bias, int act, void* C, int64_t ldc,
-                                                          bool vec) {
+                                                          const float* bias, int act, void* C, int64_t ldc) {
   const int64_t pr = (R + 3) / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= T * pr) return;
@@ -127,8 +126,8 @@ __global__ void __launch_bounds__(256) tile_reduce_kernel(const float* part, int
   float y[4] = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < split; ++s) {
     const float* p = part + ((int64_t)s * T + t) * R + r;
-    if (R % 4 == 0) {
-      const v4f v = *reinterpret_cast<const v4f*>(p);
+    if (n == 4) {
+      const v4f v = *reinterpret_cast<const v4f_any*>(p);
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] += v[e];
     } else {
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(256) tile_reduce_kernel(const float* part, int
     if (bias && e < n) y[e] += bias[r + e];
     if (act == NM_ACT_GELU) y[e] = gelu_f32(y[e]);
   }
-  store4<OUT>(C, t * ldc + r, y, n, vec);
+  store4<OUT>(C, t * ldc + r, y, n);
 }
 
 }  // namespace
@@ -151,13 +150,12 @@ hipError_t launch_tile_reduce(const float* part, int split, int64_t T, int64_t R
                               int64_t ldc, int ydt, hipStream_t s) {
   const int64_t n = T * ((R + 3) / 4);
   const dim3 grid((unsigned)((n + 255) / 256)), block(256);
-  const bool vec = vec4_ok(C, ldc, ydt == NM_F32 ? 4 : 2);
   if (ydt == NM_F16)
-    hipLaunchKernelGGL((tile_reduce_kernel<NM_F16>), grid, block, 0, s, part, split, T, R, bias, act, C, ldc, vec);
+    hipLaunchKernelGGL((tile_reduce_kernel<NM_F16>), grid, block, 0, s, part, split, T, R, bias, act, C, ldc);
   else if (ydt == NM_BF16)
-    hipLaunchKernelGGL((tile_reduce_kernel<NM_BF16>), grid, block, 0, s, part, split, T, R, bias, act, C, ldc, vec);
+    hipLaunchKernelGGL((tile_reduce_kernel<NM_BF16>), grid, block, 0, s, part, split, T, R, bias, act, C, ldc);
   else
-    hipLaunchKernelGGL((tile_reduce_kernel<NM_F32>), grid, block, 0, s, part, split, T, R, bias, act, C, ldc, vec);
+    hipLaunchKernelGGL((tile_reduce_kernel<NM_F32>), grid, block, 0, s, part, split, T, R, bias, act, C, ldc);
   return hipGetLastError();
 }
 
