@@ -78,12 +78,6 @@ nm_status check_pair(const nm_packed* gate, const nm_packed* up, Geometry* g) {
 
 bool glu_act_ok(int32_t act) { return act == NM_ACT_SILU || act == NM_ACT_GELU; }
 
-// whether the kernels can read X's rows as they are: 16-byte pieces, none of
-// which crosses the end of a row, and 32-bit offsets
-bool rows_direct(const void* X, int64_t ldx, int64_t K) {
-  return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
-}
-
 // How a call multiplies.
 enum GluPath {
   GLU_STREAM,   // few tokens: the packed weights streamed past each 16 to 64 of them
@@ -121,6 +115,14 @@ GluPath glu_path(const Geometry& g, int64_t T) {
     }
   }
   return stream <= other ? GLU_STREAM : tiles;
+}
+
+// Whether the path's kernel reads X's rows as they are.  Streamed: any rows of
+// at least one 16-byte piece; tiles: 16-byte pieces, none of which crosses the
+// end of a row, and 32-bit offsets.
+bool rows_direct(GluPath path, const void* X, int64_t ldx, int64_t K) {
+  if (path == GLU_STREAM) return K >= 8;
+  return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
 }
 
 // a weight re-packed to 2:4: values, then positions
@@ -307,7 +309,10 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, cons
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
   if (Xt && ldx < g.K) return NM_EINVAL;
-  *bytes = (Xt && rows_direct(Xt, ldx, g.K) ? 0 : padded_bytes(g, T)) + weights_bytes(g, glu_path(g, T));
+  const GluPath path = glu_path(g, T);
+  // (NULL: the worst rows)
+  *bytes = (rows_direct(path, Xt ? Xt : reinterpret_cast<const void*>(2), ldx, g.K) ? 0 : padded_bytes(g, T)) +
+           weights_bytes(g, path);
   return NM_OK;
 }
 
@@ -323,8 +328,8 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   if ((G == nullptr) != (U == nullptr) || (G && ldp < g.R)) return NM_EINVAL;
   if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
   if (!aligned(Xt, 2) || !aligned(Ht, 2) || (G && (!aligned(G, 2) || !aligned(U, 2)))) return NM_EUNSUPPORTED;
-  const bool direct = rows_direct(Xt, ldx, g.K);
   const GluPath path = glu_path(g, T);
+  const bool direct = rows_direct(path, Xt, ldx, g.K);
   const size_t pad = direct ? 0 : padded_bytes(g, T);
   const size_t need = pad + weights_bytes(g, path);
   if (need && (!workspace || workspace_bytes < need)) return NM_EINVAL;

@@ -139,7 +139,16 @@ struct GluFrag {
   __device__ static int kpiece(int p, int lg) { return SPARSE ? 32 * p + 8 * lg : 16 * lg + 8 * p; }
 };
 
-template <int WT, int N, int M, int NT>
+#if defined(__HIP_DEVICE_COMPILE__)
+// eight 16-bit values without their first n (zeros follow)
+__device__ __forceinline__ v4i shift_out(v4i x, int n) {
+  const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, x);
+  return __builtin_bit_cast(v4i, v >> (16 * n));
+}
+#endif
+
+// SHORT: K is no multiple of eight (groups of four only).
+template <int WT, int N, int M, int NT, bool SHORT>
 __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, int groups) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = kGluWaves;
@@ -178,7 +187,10 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, i
   // activations: load h of token tile j brings rows 8 h .. 8 h + 7 of it, lane l
   // piece l % 8 (eight columns) of row 8 h + l / 8; tokens past the last
   // repeat it (their results are not stored)
+  // A row's last piece may hold fewer than eight columns: it is read as the
+  // row's last eight and shifted, so nothing past the row is read.
   const int piece = lane & 7;
+  const int short_by = SHORT ? 8 - (K & 7) : 0;        // columns its last piece lacks
   const uint16_t* xr[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -205,13 +217,21 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, i
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const int k = kb * 64 + 8 * piece;
           x[i][j][h] = v4i{0, 0, 0, 0};
-          if (kb * 64 + 8 * piece < K) x[i][j][h] = *reinterpret_cast<const v4i*>(xr[j][h] + kb * 64);
+          if (k < K) x[i][j][h] = load16(xr[j][h] + kb * 64 - (SHORT && k + 8 > K ? short_by : 0));
         }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (b0 + NW * i < nKB) {
+        if (SHORT && b0 + NW * i == nKB - 1) {
+          const bool last = (b0 + NW * i) * 64 + 8 * piece + 8 > K;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[i][j][h] = last ? shift_out(x[i][j][h], short_by) : x[i][j][h];
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -256,17 +276,24 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, i
 #endif
 }
 
-template <int WT, int N, int M>
-hipError_t launch_glu_decode_nm(const GluArgs& a, hipStream_t s) {
+template <int WT, int N, int M, bool SHORT>
+hipError_t launch_glu_decode_rows(const GluArgs& a, hipStream_t s) {
   const int groups = a.T <= 32 ? 1 : (int)((a.T + 63) / 64);
   const dim3 grid((unsigned)((a.g.nRB + 7) / 8 * 8 * groups)), block(kGluWaves * 64);
   if (a.T <= 16)
-    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 1>), grid, block, 0, s, a, groups);
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 1, SHORT>), grid, block, 0, s, a, groups);
   else if (a.T <= 32)
-    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 2>), grid, block, 0, s, a, groups);
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 2, SHORT>), grid, block, 0, s, a, groups);
   else
-    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 4>), grid, block, 0, s, a, groups);
+    hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 4, SHORT>), grid, block, 0, s, a, groups);
   return hipGetLastError();
+}
+
+template <int WT, int N, int M>
+hipError_t launch_glu_decode_nm(const GluArgs& a, hipStream_t s) {
+  if constexpr (M == 4)
+    if (a.g.K % 8) return launch_glu_decode_rows<WT, N, M, true>(a, s);
+  return launch_glu_decode_rows<WT, N, M, false>(a, s);
 }
 
 template <int WT>

@@ -334,6 +334,24 @@ def test_glu_streamed_and_not(tile, stream, T, R, K, N, M):
     check(pre[1], u, eu, "U")
 
 
+@pytest.mark.parametrize("N,M", [(2, 4), (3, 4)])
+@pytest.mark.parametrize("T,K,xpad", [(1, 4, 0), (1, 12, 0), (20, 60, 0), (33, 68, 1), (70, 100, 3), (100, 516, 0),
+                                      (7, 1020, 2), (65, 64, 5)])
+def test_glu_streamed_rows_of_any_width(tile, T, K, xpad, N, M):
+    """Rows whose last piece is short, at every alignment; the next row and the
+    columns between rows hold NaN."""
+    R, dt = 50, "bf16"
+    pg, wg, _ = weights(R, K, N, M, dt, "g", N)
+    pu, wu, _ = weights(R, K, N, M, dt, "u", N)
+    X = normal((T, K), 1.0, dt, "X", T, K)
+    flat = torch.full((1 + T * (K + xpad) + 9,), float("nan"), dtype=X.dtype, device="cuda")
+    xv = flat[1:1 + T * (K + xpad)].view(T, K + xpad)[:, :K]
+    xv.copy_(X)
+    tile("stream", 1)
+    h, _, _, eh, _, _ = _ffn.glu64(X, wg, wu, "silu")
+    check(nm.glu(pg, pu, xv), h, eh, "H")
+
+
 @pytest.mark.parametrize("split", [1, 3])
 @pytest.mark.parametrize("shape", [0, 1, 2, 3])
 def test_glu_backward_tile_shapes(tile, shape, split):
