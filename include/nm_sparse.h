@@ -480,8 +480,8 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
  * NM_ACT_NONE or NM_ACT_GELU.
  * nm_mx_glu: H = act(x Wg^T) (.) (x Wu^T), act NM_ACT_SILU or NM_ACT_GELU.
  * Workspace: nm_mx_workspace_size bytes (256-byte aligned; glu != 0 for
- * nm_mx_glu; xq or Xt as the call gets them, both NULL for any): quantised
- * activations and the partial sums of a split reduction.  NM_EINVAL: null pointers, T < 1, ldx < K,
+ * nm_mx_glu; xq as the call gets it): quantised activations and the partial
+ * sums of a split reduction.  NM_EINVAL: null pointers, T < 1, ldx < K,
  * ldy < R, xq of other K or rows than asked, descriptors with wrong sizes or
  * versions, gate and up of other shapes, a small workspace;
  * NM_EUNSUPPORTED: other types, act not listed, misaligned pointers, rows so
@@ -489,8 +489,7 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
  * overlap no other buffer of the call; calls that share a workspace must be
  * ordered.
  */
-nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
-                               int32_t glu, size_t* bytes);
+nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, int64_t T, int32_t glu, size_t* bytes);
 nm_status nm_mx_linear(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
                        void* Yt, int64_t ldy, int32_t y_dtype, const float* bias, int32_t act, void* workspace,
                        size_t workspace_bytes, void* stream);

@@ -124,7 +124,7 @@ def lib() -> ctypes.CDLL:
         L.nm_mx_size.argtypes = [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
         L.nm_mx_quantize.argtypes = [P, I64, I32, MP, P]
         L.nm_mx_dequantize.argtypes = [MP, P, I64, I32, P]
-        L.nm_mx_workspace_size.argtypes = [MP, MP, P, I64, I32, I64, I32, ctypes.POINTER(SZ)]
+        L.nm_mx_workspace_size.argtypes = [MP, MP, I64, I32, ctypes.POINTER(SZ)]
         L.nm_mx_linear.argtypes = [MP, MP, P, I64, I32, I64, P, I64, I32, P, I32, P, SZ, P]
         L.nm_mx_glu.argtypes = [MP, MP, MP, P, I64, I32, I64, P, I64, I32, I32, P, SZ, P]
         for f in ("nm_pack_size", "nm_pack", "nm_spmm_workspace_size", "nm_spmm", "nm_hybrid_pack_size",
@@ -771,10 +771,9 @@ def mx_dequantize(m: Mx, out_dtype: torch.dtype = torch.float32, out: torch.Tens
 
 def mx_workspace_size(w: Mx, T: int, glu: bool = False) -> int:
     """nm_mx_workspace_size: bytes of workspace mx_linear() / mx_glu() may need
-    for T tokens of any form, stride and alignment."""
+    for T tokens."""
     n = ctypes.c_size_t()
-    _check(lib().nm_mx_workspace_size(_descriptor(w), None, None, 0, 0, T, int(glu), ctypes.byref(n)),
-           "nm_mx_workspace_size")
+    _check(lib().nm_mx_workspace_size(_descriptor(w), None, T, int(glu), ctypes.byref(n)), "nm_mx_workspace_size")
     return n.value
 
 
@@ -802,9 +801,8 @@ def _mx_operands(w: Mx, X, out_dtype, out, workspace, glu: bool, *others):
     ydt = _float_type("out", out.dtype)
     ldy = _row_pitch("out", out, T, w.rows)
     dev = _one_gpu("X", x0, ("weight codes", w.codes), ("weight scales", w.scales), ("out", out), *others)
-    rows = None if xq else (xp % 16, ldx, xdt)
-    need = _sized(lib().nm_mx_workspace_size, "nm_mx_workspace_size", ("mx", w.rows, w.K, T, glu, rows, dev),
-                  _descriptor(w), xq, xp, ldx, xdt, T, int(glu))
+    need = _sized(lib().nm_mx_workspace_size, "nm_mx_workspace_size", ("mx", w.rows, w.K, T, glu, xq is None, dev),
+                  _descriptor(w), xq, T, int(glu))
     return dev, T, xq, xp, ldx, xdt, out, ldy, ydt, _workspace(workspace, need, dev)
 
 

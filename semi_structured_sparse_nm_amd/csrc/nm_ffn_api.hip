@@ -179,11 +179,8 @@ bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_
 
 size_t mx_ws_codes(int64_t T, int64_t K) { return up256((size_t)nm::mx_codes_bytes(T, K)); }
 size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm::mx_scales_bytes(T, K)); }
-// up to 16 tokens in whole 16-byte pieces are quantised inside the product
-bool mx_in_registers(const void* X, int64_t ldx, int32_t xdt, int64_t T, int64_t K) {
-  const int eb = nm::dtype_bytes(xdt);
-  return T <= 16 && aligned(X, 16) && ldx * eb % 16 == 0 && K * eb % 16 == 0 && row_ok(ldx * eb);
-}
+// up to 16 tokens are quantised inside the product (in pieces of eight columns)
+bool mx_inside(int64_t T, int64_t K) { return T <= 16 && K >= 8; }
 // How a product of T tokens is computed: the weights streamed for every 64 of
 // them, or the tile product with its plan.  By models of both times.
 // Measured, streamed and tiles: gated block of 11008 x 4096 14.6 and 14.3 us
@@ -235,9 +232,9 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     if (!float_dtype(xdt) || !aligned(X, (size_t)nm::dtype_bytes(xdt))) return NM_EUNSUPPORTED;
     if ((T + 31) / 32 * (Kp / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
   }
-  const bool in_registers = !xq && mx_in_registers(X, ldx, xdt, T, K);
-  const MxPath path = in_registers ? MxPath{true, {}} : mx_path(glu, T, R, K);
-  const size_t quant = xq || in_registers ? 0 : mx_ws(T, K);
+  const bool inside = !xq && mx_inside(T, K);
+  const MxPath path = inside ? MxPath{true, {}} : mx_path(glu, T, R, K);
+  const size_t quant = xq || inside ? 0 : mx_ws(T, K);
   const size_t need = quant + part_bytes(path.plan, T, R);
   if (need && (!ws || ws_bytes < need)) return NM_EINVAL;
   if (need && !aligned(ws, 256)) return NM_EUNSUPPORTED;
@@ -261,7 +258,7 @@ nm_status mx_product(const nm_mx* w0, const nm_mx* w1, const nm_mx* xq, const vo
     }
     a.R = R;
     a.K = K;
-    a.X = in_registers ? X : nullptr;
+    a.X = inside ? X : nullptr;
     a.ldx = ldx;
     a.xdt = xdt;
     a.xcodes = xcodes;
@@ -532,16 +529,13 @@ nm_status nm_mx_dequantize(const nm_mx* m, void* Y, int64_t ldy, int32_t y_dtype
              : NM_EHIP;
 }
 
-nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, const void* Xt, int64_t ldx, int32_t x_dtype, int64_t T,
-                               int32_t glu, size_t* bytes) {
+nm_status nm_mx_workspace_size(const nm_mx* w, const nm_mx* xq, int64_t T, int32_t glu, size_t* bytes) {
   if (!bytes || T < 1) return NM_EINVAL;
   const nm_status st = check_mx(w);
   if (st != NM_OK) return st;
   if (!row_ok(nm::mx_kp(w->K) / 2) || T > kMaxLen) return NM_EUNSUPPORTED;
   if ((T + 31) / 32 * (nm::mx_kp(w->K) / nm::kMxSlab) >= kMaxGrid) return NM_EUNSUPPORTED;
-  if (Xt && !xq && ldx < w->K) return NM_EINVAL;
-  if (Xt && !xq && !float_dtype(x_dtype)) return NM_EUNSUPPORTED;
-  const bool quant = !xq && !(Xt && mx_in_registers(Xt, ldx, x_dtype, T, w->K));
+  const bool quant = !xq && !mx_inside(T, w->K);
   const size_t part = quant || xq ? part_bytes(mx_path(glu != 0, T, w->rows, w->K).plan, T, w->rows) : 0;
   *bytes = (quant ? mx_ws(T, w->K) : 0) + part;
   return NM_OK;

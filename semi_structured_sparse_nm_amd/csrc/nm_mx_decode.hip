@@ -3,12 +3,13 @@
 //
 // A workgroup owns 16 weight rows (of both weights for the gated block); its
 // waves take every NW-th slab of 256 columns, so a wave reads whole 128-byte
-// lines of each row.  Up to 16 tokens that come as 16- or 32-bit values are
-// quantised on the way (one launch in all): a wave reads its slab of a token
-// pair in one 1 KB load, four lanes share a block as in the quantiser, and
-// codes and scales pass through the wave's own LDS to the lanes of the scaled
-// matrix instruction.  (Each lane reading the block it needs itself touches 64
-// pieces of 64 bytes a load: 20 us instead of 14 for 11008 x 4096, 16 tokens.)
+// lines of each row.  Up to 16 tokens that come as 16- or 32-bit values, in
+// rows of any alignment, are quantised on the way (one launch in all): a wave
+// reads its slab of a token pair in one 1 KB load, four lanes share a block as
+// in the quantiser, and codes and scales pass through the wave's own LDS to the
+// lanes of the scaled matrix instruction.  (Each lane reading the block it
+// needs itself touches 64 pieces of 64 bytes a load: 20 us instead of 14 for
+// 11008 x 4096, 16 tokens.)
 // More tokens come quantised, whole lines of eight tokens a load, and change
 // to the instruction's order in the wave's LDS likewise (gated block of 11008 x
 // 4096, 64 tokens: 24.4 us in that order from the caches, 17.6 so).  The waves'
@@ -30,9 +31,30 @@ __device__ __forceinline__ v4f mx_mul(v4i a, v4i b, v4f c, int sa, int sb) {
 }
 #endif
 
-// XDT: type of the activations quantised here (NT = 1), or -1: xcodes.  NW:
-// waves the slabs are dealt to.
-template <int XDT, bool GLU, int NT, int NW>
+#if defined(__HIP_DEVICE_COMPILE__)
+// ND dwords without their first `bytes` (zeros follow; 32: all of them)
+template <int ND>
+__device__ __forceinline__ void drop_front(uint32_t (&x)[ND], int bytes) {
+#pragma unroll
+  for (int w = 16; w >= 4; w /= 2)
+#pragma unroll
+    for (int i = 0; i < ND; ++i) {
+      const uint32_t y = i + w / 4 < ND ? x[i + w / 4] : 0u;
+      x[i] = bytes & w ? y : x[i];
+    }
+#pragma unroll
+  for (int i = 0; i < ND; ++i) {
+    const uint32_t hi = i + 1 < ND ? x[i + 1] : 0u;
+    if (bytes & 2) x[i] = x[i] >> 16 | hi << 16;
+    if (bytes & 32) x[i] = 0;
+  }
+}
+#endif
+
+// XDT: type of the activations quantised here (NT = 1), or -1: xcodes.  ANY:
+// their rows start anywhere or end inside a 16-byte piece.  NW: waves the slabs
+// are dealt to.
+template <int XDT, bool GLU, int NT, int NW, bool ANY = false>
 __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int nslab, int groups) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NWT = GLU ? 2 : 1;                     // weights
@@ -109,6 +131,24 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int t = i0 + 2 * u + hx;
+          if constexpr (ANY) {
+            // a row's short last piece as its last eight values, shifted; all
+            // lanes read inside their row
+            const int64_t k = (int64_t)s * 256 + px * 8;
+            const uint8_t* p =
+                static_cast<const uint8_t*>(a.X) + (min(t0 + t, a.T - 1) * a.ldx + min(k, a.K - 8)) * EB;
+#pragma unroll
+            for (int i = 0; i < ND / 4; ++i) {
+              const v4i v = load16(p + 16 * i);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[u][4 * i + e] = (uint32_t)v[e];
+            }
+            if (s == nslab - 1) drop_front<ND>(x[u], k < a.K ? max((int)(k + 8 - a.K), 0) * EB : 32);
+            if (t >= tn)
+#pragma unroll
+              for (int i = 0; i < ND; ++i) x[u][i] = 0;
+            continue;
+          }
           const int off = t * pitch + px * 8 * EB;
 #pragma unroll
           for (int i = 0; i < ND / 4; ++i) {
@@ -204,17 +244,27 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
 #endif
 }
 
+template <bool GLU, int NW, int XDT>
+void launch_quantising(const MxDecodeArgs& a, int nslab, dim3 grid, hipStream_t s) {
+  constexpr int EB = XDT == NM_F32 ? 4 : 2;
+  // 16-byte pieces within 32-bit offsets
+  if ((uintptr_t)a.X % 16 == 0 && a.ldx * EB % 16 == 0 && a.K * EB % 16 == 0 && a.ldx * EB < (1 << 26))
+    hipLaunchKernelGGL((mx_decode_kernel<XDT, GLU, 1, NW>), grid, dim3(NW * 64), 0, s, a, nslab, 1);
+  else
+    hipLaunchKernelGGL((mx_decode_kernel<XDT, GLU, 1, NW, true>), grid, dim3(NW * 64), 0, s, a, nslab, 1);
+}
+
 template <bool GLU, int NW>
 hipError_t launch_one_tile(const MxDecodeArgs& a, int nslab, unsigned nrb, hipStream_t s) {
-  const dim3 grid((nrb + 7) / 8 * 8), block(NW * 64);
+  const dim3 grid((nrb + 7) / 8 * 8);
   if (!a.X)
-    hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 1, NW>), grid, block, 0, s, a, nslab, 1);
+    hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 1, NW>), grid, dim3(NW * 64), 0, s, a, nslab, 1);
   else if (a.xdt == NM_F16)
-    hipLaunchKernelGGL((mx_decode_kernel<NM_F16, GLU, 1, NW>), grid, block, 0, s, a, nslab, 1);
+    launch_quantising<GLU, NW, NM_F16>(a, nslab, grid, s);
   else if (a.xdt == NM_BF16)
-    hipLaunchKernelGGL((mx_decode_kernel<NM_BF16, GLU, 1, NW>), grid, block, 0, s, a, nslab, 1);
+    launch_quantising<GLU, NW, NM_BF16>(a, nslab, grid, s);
   else
-    hipLaunchKernelGGL((mx_decode_kernel<NM_F32, GLU, 1, NW>), grid, block, 0, s, a, nslab, 1);
+    launch_quantising<GLU, NW, NM_F32>(a, nslab, grid, s);
   return hipGetLastError();
 }
 

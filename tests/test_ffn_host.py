@@ -91,16 +91,13 @@ def test_glu_backward_refusals():
 def test_mx_workspace():
     n = ctypes.c_size_t()
     f = nm.lib().nm_mx_workspace_size
-    w, x = _mx(40, 304), _mx(5, 304)
+    w, x = _mx(40, 304), _mx(17, 304)
     b, nb = ctypes.byref(w), ctypes.byref(n)
-    assert f(b, None, None, 0, 0, 5, 0, nb) == nm.NM_OK and n.value == 5 * 256 + 2 * 256
-    for args, want in (((ctypes.byref(x), None, 0, 0, 5), 0), ((None, P[0], 304, nm.NM_BF16, 16), 0),
-                       ((None, P[0], 305, nm.NM_BF16, 5), 1), ((None, P[0] + 2, 304, nm.NM_BF16, 5), 1),
-                       ((None, P[0], 304, nm.NM_F32, 17), 1)):
-        assert f(b, *args, 1, nb) == nm.NM_OK and (n.value > 0) == bool(want), args
-    assert f(b, None, P[0], 303, nm.NM_F16, 5, 0, nb) == EINVAL
-    assert f(b, None, P[0], 304, nm.NM_I8, 5, 0, nb) == EUNSUP
-    assert f(b, None, None, 0, 0, 0, 0, nb) == EINVAL and f(None, None, None, 0, 0, 5, 0, nb) == EINVAL
+    for xq, T, want in ((None, 16, 0), (None, 17, 17 * 256 + 2 * 256), (ctypes.byref(x), 17, 0)):
+        assert f(b, xq, T, 0, nb) == nm.NM_OK and n.value == want
+    narrow = _mx(40, 7)
+    assert f(ctypes.byref(narrow), None, 1, 0, nb) == nm.NM_OK and n.value == 2 * 256
+    assert f(b, None, 0, 0, nb) == EINVAL and f(None, None, 5, 0, nb) == EINVAL and f(b, None, 5, 0, None) == EINVAL
 
 
 def test_lengths_past_one_launch():
@@ -112,8 +109,8 @@ def test_lengths_past_one_launch():
     assert nm.lib().nm_mx_quantize(P[0], 1 << 13, nm.NM_F16, ctypes.byref(m), None) == EUNSUP
     w = _mx(16, 1 << 13)
     f = nm.lib().nm_mx_workspace_size
-    assert f(ctypes.byref(w), None, None, 0, 0, 1 << 24, 0, ctypes.byref(c)) == EUNSUP
-    assert f(ctypes.byref(w), None, None, 0, 0, 1 << 20, 0, ctypes.byref(c)) == nm.NM_OK
+    assert f(ctypes.byref(w), None, 1 << 24, 0, ctypes.byref(c)) == EUNSUP
+    assert f(ctypes.byref(w), None, 1 << 20, 0, ctypes.byref(c)) == nm.NM_OK
     assert nm.lib().nm_mx_linear(ctypes.byref(w), None, P[0], 1 << 13, nm.NM_F16, 1 << 24, P[1], 16, nm.NM_F16, None,
                                  0, P[2], 1 << 62, None) == EUNSUP
     g = _w(R=8, K=8)

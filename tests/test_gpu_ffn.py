@@ -497,8 +497,9 @@ def test_mx_quantize_non_finite_blocks(dt, bad):
         assert bool(torch.isnan(out[[2, 4]]).all()) and bool(torch.isfinite(out[[0, 1, 3]]).all())
 
 
-MX_SHAPES = [(1, 1, 1), (1, 17, 40), (2, 100, 256), (15, 16, 264), (16, 48, 1000), (17, 40, 33), (33, 65, 512),
-             (64, 33, 770), (65, 40, 32), (70, 129, 256), (129, 300, 520), (300, 257, 1288)]
+MX_SHAPES = [(1, 1, 1), (1, 8, 7), (1, 17, 40), (2, 100, 256), (3, 33, 9), (9, 20, 261), (15, 16, 264),
+             (16, 40, 1027), (16, 48, 1000), (17, 40, 33), (33, 65, 512), (64, 33, 770), (65, 40, 32),
+             (70, 129, 256), (129, 300, 520), (300, 257, 1288)]
 
 
 def _mx_w(R, K, dt, *key):
