@@ -35,11 +35,10 @@ bool ffn_tile_override(const char* kind, int* shape, int* split) {
 // Microseconds a slab takes with few workgroups running and with one on every
 // compute unit (their operands' traffic, and the power the matrix cores draw,
 // slow each other down), and a tile besides its slabs.  Fitted to products of
-// 16 to 2048 tokens by 428 to 22016 x 536 to 22016; the choice is within 10%
-// of the fastest shape and split nearly everywhere there.  For example 2048
-// tokens, two 4:8 weights of 11008 x 4096, gated: 256 x 256 tiles 290 us, 128 x
-// 256 306, 128 x 128 498; 256 tokens: 89, 65 and 90; the gradients of 197 tokens
-// through two weights of 768 x 768: 256 x 256 42 us, 64 x 128 in four slices 20.
+// 64 to 2048 tokens by 411 to 11008 x 182 to 11008; the choice is within 7% of
+// the fastest shape and split there.  For example 2048 tokens, two 4:8 weights
+// of 11008 x 4096, gated: 256 x 256 tiles 290 us, 128 x 256 306; 600 tokens, 1614
+// x 2364: 68, 44, 128 x 128 32 and 64 x 128 41; at 4 bits 26, 17, 12 and 18.
 namespace {
 
 struct TileShape {
@@ -51,8 +50,8 @@ struct TileShape {
 };
 constexpr TileShape kShapes[4] = {{256, 256, {0.93, 1.10}, {1.50, 1.60}, 6.0},
                                   {128, 256, {0.47, 0.72}, {0.85, 0.97}, 5.0},
-                                  {128, 128, {0.60, 0.75}, {0.73, 0.86}, 4.0},
-                                  {64, 128, {0.33, 0.44}, {0.43, 0.47}, 3.5}};
+                                  {128, 128, {0.42, 0.50}, {0.60, 0.65}, 4.0},
+                                  {64, 128, {0.25, 0.35}, {0.34, 0.42}, 3.5}};
 
 int64_t tiles(int64_t Mr, int64_t Nr, int bm, int bn) { return (Mr + bm - 1) / bm * ((Nr + bn - 1) / bn); }
 
@@ -90,14 +89,28 @@ TilePlan plan_tile(TileOp op, bool mx, int64_t Mr, int64_t Nr, int nslab, int cu
   });
 }
 
-// The products' items are dealt to an XCD's workgroups as TileWalk does.
+// The products' items are dealt to an XCD's workgroups as TileWalk does.  Its
+// own constants, fitted to 18 sizes of 3 to 2048 tokens in every shape and
+// split: a slab with few and with all compute units at work, a tile of the
+// input's gradient and of a weight's besides its slabs (its mask is read).  The
+// choice is within 5% of the fastest at 16 of them, within 9% at the others
+// (for example 30 tokens, two weights of 3490 x 3688: 128 x 128 tiles 67 us, 256
+// x 256 81; 1024 tokens, 11008 x 4096: 573 and 477).
 TilePlan plan_back(int64_t T, int64_t R, int64_t K, int nslab_x, int nslab_w, bool dx, bool dw, int cus) {
+  struct Cost {
+    double idle, busy, x, w;
+  };
+  static const Cost costs[4] = {{0.69, 1.30, 6.1, 10.8},
+                                {0.39, 0.67, 5.0, 6.6},
+                                {0.29, 0.375, 2.7, 3.8},
+                                {0.11, 0.25, 1.4, 2.55}};
   return best_plan(dx ? std::min(16, nslab_x) : 1, nslab_x, [&](const TileShape& h, TilePlan& p) {
+    const Cost& c = costs[p.shape];
     const int64_t a = dx ? (tiles(T, K, h.bm, h.bn) * p.split + 7) / 8 : 0;
     const int64_t b = dw ? (2 * tiles(R, K, h.bm, h.bn) + 7) / 8 : 0;
     const int64_t w = std::min<int64_t>(a + b, (cus + 7) / 8), q = a % w;
-    const double slab = h.slab(false, 8 * (a + b), cus);
-    const double ta = p.sps * slab + h.tile, tb = nslab_w * slab + 1.5 * h.tile;   // (the mask is read too)
+    const double slab = c.idle + (c.busy - c.idle) * std::min(1.0, 8.0 * (double)(a + b) / cus);
+    const double ta = p.sps * slab + c.x, tb = nslab_w * slab + c.w;
     const int64_t most = (b + w - q - 1) / (w - q), near = (int64_t)(ta / tb);
     double best = 0;
     for (const int64_t lead : {int64_t(0), near, near + 1, most}) {
@@ -109,7 +122,8 @@ TilePlan plan_back(int64_t T, int64_t R, int64_t K, int nslab_x, int nslab_w, bo
         p.lead = (int)lead;
       }
     }
-    return best + (dx ? split_time(T, K, p.split) : 0.0);
+    if (p.split > 1) best += (double)T * (double)K * (8.0 * p.split + 2.0) / 16.4e6 + 2.0;
+    return best;
   });
 }
 
