@@ -114,6 +114,10 @@ struct GluArgs {
   int act;
 };
 
+// Tiles of 16 tokens (1, 2 or 4) that a workgroup of a streamed product takes:
+// as many as there are, but fewer where the workgroups would leave half the
+// compute units idle.
+int stream_tiles(int64_t blocks, int64_t T);
 // few tokens: the packed weights streamed once per token tile
 hipError_t launch_glu_decode(const GluArgs& a, hipStream_t s);
 // more tokens, both weights 2:4: the sparse tile product

@@ -278,11 +278,12 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, i
 
 template <int WT, int N, int M, bool SHORT>
 hipError_t launch_glu_decode_rows(const GluArgs& a, hipStream_t s) {
-  const int groups = a.T <= 32 ? 1 : (int)((a.T + 63) / 64);
+  const int nt = stream_tiles(a.g.nRB, a.T);
+  const int groups = (int)((a.T + 16 * nt - 1) / (16 * nt));
   const dim3 grid((unsigned)((a.g.nRB + 7) / 8 * 8 * groups)), block(kGluWaves * 64);
-  if (a.T <= 16)
+  if (nt == 1)
     hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 1, SHORT>), grid, block, 0, s, a, groups);
-  else if (a.T <= 32)
+  else if (nt == 2)
     hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 2, SHORT>), grid, block, 0, s, a, groups);
   else
     hipLaunchKernelGGL((glu_decode_kernel<WT, N, M, 4, SHORT>), grid, block, 0, s, a, groups);

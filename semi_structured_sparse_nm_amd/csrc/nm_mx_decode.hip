@@ -279,9 +279,12 @@ hipError_t launch_decode(const MxDecodeArgs& a, hipStream_t s) {
     if (nrb <= (unsigned)device_cu_count() && nslab > NW) return launch_one_tile<GLU, 16>(a, nslab, nrb, s);
     return launch_one_tile<GLU, NW>(a, nslab, nrb, s);
   }
-  const int groups = a.T <= 32 ? 1 : (int)((a.T + 63) / 64);
+  const int nt = stream_tiles(nrb, a.T);
+  const int groups = (int)((a.T + 16 * nt - 1) / (16 * nt));
   const dim3 grid((nrb + 7) / 8 * 8 * groups), block(NW * 64);
-  if (a.T <= 32)
+  if (nt == 1)
+    hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 1, NW>), grid, block, 0, s, a, nslab, groups);
+  else if (nt == 2)
     hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 2, NW>), grid, block, 0, s, a, nslab, groups);
   else
     hipLaunchKernelGGL((mx_decode_kernel<-1, GLU, 4, NW>), grid, block, 0, s, a, nslab, groups);
