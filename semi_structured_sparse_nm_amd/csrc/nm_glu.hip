@@ -29,8 +29,10 @@ __device__ __forceinline__ uint32_t expand8(const Geometry& g, const uint8_t* va
     const v2i x = *reinterpret_cast<const v2i*>(v);
     e[0] = (uint32_t)x[0];
     e[1] = (uint32_t)x[1];
-  } else if (cnt == 2) {
-    e[0] = *reinterpret_cast<const uint32_t*>(v);
+  } else if (cnt % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (2 * i < cnt) e[i] = reinterpret_cast<const uint32_t*>(v)[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -124,7 +126,9 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
   uint16_t(*tile)[64][66] = reinterpret_cast<uint16_t(*)[64][66]>(lds);
   const int64_t tt = (a.T + 63) / 64;
   const int64_t t0 = (b % tt) * 64, r0 = (b / tt) * 64;
-  for (int q = threadIdx.x; q < 512; q += 256) {
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int q = it * 256 + threadIdx.x;
     const int tl = q >> 3, rl = (q & 7) * 8;
     const int64_t t = t0 + tl, r = r0 + rl;
     uint32_t og[4] = {0u, 0u, 0u, 0u}, ou[4] = {0u, 0u, 0u, 0u};
@@ -163,7 +167,9 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
   }
   if (!a.dt) return;
   __syncthreads();
-  for (int q = threadIdx.x; q < 1024; q += 256) {
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int q = it * 256 + threadIdx.x;
     const int w = q >> 9, rl = (q >> 3) & 63, tl = (q & 7) * 8;
     if (r0 + rl < a.g.R) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[w][rl][tl]);
@@ -200,7 +206,9 @@ __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, 
   }
   if (!a.wt) return;
   __syncthreads();
-  for (int q = threadIdx.x; q < 1024; q += 256) {
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int q = it * 256 + threadIdx.x;
     const int kl = q >> 4, rl = (q & 15) * 8;
     if (kb * 64 + kl < g.K && r0 + rl < a.Rp) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][rl]);
@@ -214,7 +222,9 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
   uint16_t(*tile)[66] = reinterpret_cast<uint16_t(*)[66]>(lds);
   const int64_t tt = a.Tp / 64, K = a.g.K;
   const int64_t t0 = (b % tt) * 64, k0 = (b / tt) * 64;
-  for (int q = threadIdx.x; q < 512; q += 256) {
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int q = it * 256 + threadIdx.x;
     const int tl = q >> 3, kl = (q & 7) * 8;
     const int64_t t = t0 + tl, k = k0 + kl;
     uint32_t o[4] = {0u, 0u, 0u, 0u};
@@ -234,7 +244,9 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
     for (int e = 0; e < 8; ++e) tile[kl + e][tl] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
   }
   __syncthreads();
-  for (int q = threadIdx.x; q < 512; q += 256) {
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int q = it * 256 + threadIdx.x;
     const int kl = q >> 3, tl = (q & 7) * 8;
     if (k0 + kl < K) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][tl]);
