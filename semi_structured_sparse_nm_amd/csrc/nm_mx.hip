@@ -6,7 +6,7 @@
 // two lane exchanges, each lane writes its eight codes as one dword, and the
 // unit's scales are gathered in LDS and leave as one 256-byte piece.  Bound by
 // HBM: 2 (or 4) bytes read and 17 / 32 written per element (11008 x 4096 bf16:
-// 20 us, 5.7 TB/s; back to bf16 24 us, 4.8 TB/s).
+// 20 us, 5.7 TB/s; back to bf16 21.5 us, 5.3 TB/s).
 #include "nm_mx_device.hpp"
 
 namespace nm {
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(TH) mx_dequantize_kernel(const uint8_t* codes,
 namespace {
 
 // Threads of a workgroup: 256, four passes over the unit; 1024, one pass, where
-// there are few units (197 x 770: 4.6 us, both ways, against 5.6 and 6.8).
+// there are few units (197 x 768: 4.6 us, both ways, against 5.6 and 6.8).
 bool few_units(int64_t units) { return units < 4 * device_cu_count(); }
 
 template <int DT>
