@@ -119,7 +119,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, f
 // Tiles pass through LDS; every element is read and written once, in 16-byte
 // pieces of at least 128 contiguous bytes: 595 MB in 120 us (5 TB/s, a large
 // copy's rate) for 2048 tokens and two 2:4 weights of 11008 x 4096.
-template <int WT>
+template <int WT, int TH>
 __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   // pitch 66 halves: eight pieces of a row (8 rows apart here) and eight
   // tokens fall on different banks
@@ -127,8 +127,8 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
   const int64_t tt = (a.T + 63) / 64;
   const int64_t t0 = (b % tt) * 64, r0 = (b / tt) * 64;
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int q = it * 256 + threadIdx.x;
+  for (int it = 0; it < 512 / TH; ++it) {
+    const int q = it * TH + threadIdx.x;
     const int tl = q >> 3, rl = (q & 7) * 8;
     const int64_t t = t0 + tl, r = r0 + rl;
     uint32_t og[4] = {0u, 0u, 0u, 0u}, ou[4] = {0u, 0u, 0u, 0u};
@@ -168,8 +168,8 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
   if (!a.dt) return;
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int q = it * 256 + threadIdx.x;
+  for (int it = 0; it < 1024 / TH; ++it) {
+    const int q = it * TH + threadIdx.x;
     const int w = q >> 9, rl = (q >> 3) & 63, tl = (q & 7) * 8;
     if (r0 + rl < a.g.R) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[w][rl][tl]);
@@ -179,6 +179,7 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
   }
 }
 
+template <int TH>
 __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   // pitch 130 halves: the four 16-column runs of a packed row and its block's
   // sixteen rows fall on different banks
@@ -193,8 +194,8 @@ __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, 
   uint8_t* mask = w ? a.mask[1] : a.mask[0];
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int rl = 16 * (2 * (threadIdx.x >> 6) + it) + (lane >> 2), cl = (lane & 3) * 16;
+  for (int it = 0; it < 512 / TH; ++it) {
+    const int rl = 16 * (it * (TH / 64) + (threadIdx.x >> 6)) + (lane >> 2), cl = (lane & 3) * 16;
     const int64_t r = r0 + rl;
     uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
     if (r < g.R) {
@@ -207,8 +208,8 @@ __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, 
   if (!a.wt) return;
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int q = it * 256 + threadIdx.x;
+  for (int it = 0; it < 1024 / TH; ++it) {
+    const int q = it * TH + threadIdx.x;
     const int kl = q >> 4, rl = (q & 15) * 8;
     if (kb * 64 + kl < g.K && r0 + rl < a.Rp) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][rl]);
@@ -218,13 +219,14 @@ __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, 
   }
 }
 
+template <int TH>
 __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   uint16_t(*tile)[66] = reinterpret_cast<uint16_t(*)[66]>(lds);
   const int64_t tt = a.Tp / 64, K = a.g.K;
   const int64_t t0 = (b % tt) * 64, k0 = (b / tt) * 64;
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int q = it * 256 + threadIdx.x;
+  for (int it = 0; it < 512 / TH; ++it) {
+    const int q = it * TH + threadIdx.x;
     const int tl = q >> 3, kl = (q & 7) * 8;
     const int64_t t = t0 + tl, k = k0 + kl;
     uint32_t o[4] = {0u, 0u, 0u, 0u};
@@ -245,8 +247,8 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
   }
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int q = it * 256 + threadIdx.x;
+  for (int it = 0; it < 512 / TH; ++it) {
+    const int q = it * TH + threadIdx.x;
     const int kl = q >> 3, tl = (q & 7) * 8;
     if (k0 + kl < K) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][tl]);
@@ -256,15 +258,15 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
   }
 }
 
-template <int WT>
-__global__ void __launch_bounds__(256) glu_prepare_kernel(PrepareArgs a, int64_t n_act, int64_t n_weight) {
+template <int WT, int TH>
+__global__ void __launch_bounds__(TH) glu_prepare_kernel(PrepareArgs a, int64_t n_act, int64_t n_weight) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 64 * 66];
   static_assert(2 * 64 * 66 >= 64 * 130, "the weight tile fits");
   int64_t b = blockIdx.x;
-  if (b < n_act) return prepare_dact<WT>(a, b, lds);
+  if (b < n_act) return prepare_dact<WT, TH>(a, b, lds);
   b -= n_act;
-  if (b < n_weight) return prepare_weight(a, b, lds);
-  prepare_tokens(a, b - n_weight, lds);
+  if (b < n_weight) return prepare_weight<TH>(a, b, lds);
+  prepare_tokens<TH>(a, b - n_weight, lds);
 }
 
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_t ldx, int64_t T, int64_t K,
@@ -296,11 +298,18 @@ hipError_t launch_glu_prepare(const PrepareArgs& a, int wdt, hipStream_t s) {
   const int64_t n_act = (a.T + 63) / 64 * (a.Rp / 64);
   const int64_t n_weight = 2 * ((a.g.R + 127) / 128) * a.g.nKB;
   const int64_t n_x = a.xt ? a.Tp / 64 * a.g.nKB : 0;
-  const dim3 grid((unsigned)(n_act + n_weight + n_x));
+  const unsigned grid = (unsigned)(n_act + n_weight + n_x);
+  // few workgroups: twice the threads each, half the passes one after another
+  // (1152 tokens, 428 x 1116: 11.6 us against 14.1; 2048, 11008 x 4096: 135
+  // against 120)
+  const bool wide = grid < 8u * device_cu_count();
+  auto launch = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, s, a, n_act, n_weight);
+  };
   if (wdt == NM_F16)
-    hipLaunchKernelGGL((glu_prepare_kernel<NM_F16>), grid, dim3(256), 0, s, a, n_act, n_weight);
+    wide ? launch(glu_prepare_kernel<NM_F16, 512>, 512) : launch(glu_prepare_kernel<NM_F16, 256>, 256);
   else
-    hipLaunchKernelGGL((glu_prepare_kernel<NM_BF16>), grid, dim3(256), 0, s, a, n_act, n_weight);
+    wide ? launch(glu_prepare_kernel<NM_BF16, 512>, 512) : launch(glu_prepare_kernel<NM_BF16, 256>, 256);
   return hipGetLastError();
 }
 
