@@ -483,22 +483,25 @@ GLU_ACTS = {"gelu": 1, "silu": 2}
 # The smallest of the calls below take a few microseconds on the GPU, so their
 # host side is kept short: descriptors and workspace sizes are remembered per
 # weight and shape, devices compared by index, streams taken as raw handles.
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda i: torch.cuda.current_stream(i).cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _ws_sizes: dict = {}
 
 
 def _descriptor(p):
     """byref of p's C descriptor, built again whenever a field changed."""
-    second = p.meta if type(p) is Packed else p.scales
-    first = p.values if type(p) is Packed else p.codes
-    key = (first.data_ptr(), first.numel(), (0, 0) if second is None else (second.data_ptr(), second.numel()),
-           p.rows, p.K, p.format_version, (p.N, p.M, p.dtype) if type(p) is Packed else None)
+    if type(p) is Packed:
+        v, m = p.values, p.meta
+        key = (v.data_ptr(), v.numel(), p.rows, p.K, p.N, p.M, p.dtype, p.format_version)
+    else:
+        v, m = p.codes, p.scales
+        key = (v.data_ptr(), v.numel(), p.rows, p.K, p.format_version)
+    if m is not None:
+        key += (m.data_ptr(), m.numel())
     c = p.__dict__.get("_c_desc")
     if c is None or c[0] != key:
         d = p.desc()
-        c = (key, d, ctypes.byref(d))
-        p.__dict__["_c_desc"] = c
+        c = p.__dict__["_c_desc"] = (key, d, ctypes.byref(d))
     return c[2]
 
 
@@ -515,14 +518,16 @@ def _sized(f, what: str, key: tuple, *args) -> int:
     return n
 
 
-def _one_gpu(first: str, t0: torch.Tensor, *rest) -> int:
-    """The index of the one GPU t0 and the (name, tensor) pairs live on; None
-    tensors are skipped."""
+def _one_gpu(names: str, t0: torch.Tensor, *rest) -> int:
+    """The index of the one GPU t0 and the other tensors live on (None ones are
+    skipped); names: of all of them, for the error."""
     i = t0.get_device()
     if i < 0:
-        raise ValueError(f"{first} is on {t0.device}, not on a GPU")
-    for name, t in rest:
+        raise ValueError(f"{names.split(', ')[0]} is on {t0.device}, not on a GPU")
+    for t in rest:
         if t is not None and t.get_device() != i:
+            first, *others = names.split(", ")
+            name = others[next(k for k, r in enumerate(rest) if r is t)]
             raise ValueError(f"{name} is on {t.device}, {first} on {t0.device}")
     return i
 
@@ -574,7 +579,7 @@ def _check_dtype(name: str, t: torch.Tensor, want: torch.dtype) -> None:
 def _call(dev: int, f, what: str, *args) -> None:
     """One library call with the operands' device current and its current
     stream as the last argument."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         st = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -586,9 +591,9 @@ def _call(dev: int, f, what: str, *args) -> None:
 def _glu_operands(gate: Packed, up: Packed, Xt: torch.Tensor):
     if gate.dtype not in (NM_F16, NM_BF16):
         raise TypeError(f"the gated block takes float16 / bfloat16 weights, not {gate.torch_dtype}")
-    for f in ("rows", "K", "N", "M", "dtype"):
-        if getattr(gate, f) != getattr(up, f):
-            raise ValueError(f"gate and up differ in {f}: {getattr(gate, f)} and {getattr(up, f)}")
+    if (gate.rows, gate.K, gate.N, gate.M, gate.dtype) != (up.rows, up.K, up.N, up.M, up.dtype):
+        f = next(f for f in ("rows", "K", "N", "M", "dtype") if getattr(gate, f) != getattr(up, f))
+        raise ValueError(f"gate and up differ in {f}: {getattr(gate, f)} and {getattr(up, f)}")
     if Xt.dim() != 2:
         raise ValueError("Xt must be a 2-D tensor")
     T = Xt.shape[0]
@@ -647,8 +652,8 @@ def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torc
         ldp = _check_pre(pre, T, gate)
         g = pre.data_ptr()
         u = g + pre.stride(0) * pre.element_size()
-    dev = _one_gpu("Xt", Xt, ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
-                   ("up meta", up.meta), ("out", out), ("pre", pre))
+    dev = _one_gpu("Xt, gate, gate meta, up, up meta, out, pre", Xt, gate.values, gate.meta, up.values, up.meta, out,
+                   pre)
     L, dg, du = lib(), _descriptor(gate), _descriptor(up)
     x = Xt.data_ptr()
     need = _sized(L.nm_glu_workspace_size, "nm_glu_workspace_size", _glu_key("glu", gate, T, (x % 16, ldx), dev), dg,
@@ -681,8 +686,8 @@ def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, 
     R, K = gate.rows, gate.K
     lddh = _row_pitch("dH", dH, T, R)
     _check_dtype("dH", dH, Xt.dtype)
-    dev = _one_gpu("Xt", Xt, ("gate", gate.values), ("gate meta", gate.meta), ("up", up.values),
-                   ("up meta", up.meta), ("pre", pre), ("dH", dH))
+    dev = _one_gpu("Xt, gate, gate meta, up, up meta, pre, dH", Xt, gate.values, gate.meta, up.values, up.meta, pre,
+                   dH)
     L, dg, du = lib(), _descriptor(gate), _descriptor(up)
     need = _sized(L.nm_glu_backward_workspace_size, "nm_glu_backward_workspace_size",
                   _glu_key("glu_backward", gate, T, None, dev), dg, du, T)
@@ -764,7 +769,7 @@ def mx_dequantize(m: Mx, out_dtype: torch.dtype = torch.float32, out: torch.Tens
         out = m.codes.new_empty((m.rows, m.K), dtype=out_dtype)
     ydt = _float_type("out", out.dtype)
     ld = _row_pitch("out", out, m.rows, m.K)
-    dev = _one_gpu("codes", m.codes, ("scales", m.scales), ("out", out))
+    dev = _one_gpu("codes, scales, out", m.codes, m.scales, out)
     _call(dev, lib().nm_mx_dequantize, "nm_mx_dequantize", _descriptor(m), out.data_ptr(), ld, ydt)
     return out
 
@@ -777,15 +782,14 @@ def mx_workspace_size(w: Mx, T: int, glu: bool = False) -> int:
     return n.value
 
 
-def _mx_operands(w: Mx, X, out_dtype, out, workspace, glu: bool, *others):
+def _mx_operands(w: Mx, X, out_dtype, out, workspace, glu: bool, names: str, *others):
     """Checks shared by mx_linear and mx_glu: (device, T, xq, x pointer, ldx,
     x dtype, out, ldy, y dtype, workspace triple)."""
     if type(X) is Mx:
         if X.K != w.K:
             raise ValueError(f"X has K={X.K}, the weight has K={w.K}")
         T, xq, xp, ldx, xdt = X.rows, _descriptor(X), None, 0, 0
-        x0, default = X.codes, torch.bfloat16
-        others = (("X scales", X.scales),) + others
+        x0, xs, default = X.codes, X.scales, torch.bfloat16
     else:
         if X.dim() != 2:
             raise ValueError("X must be a 2-D tensor or an Mx")
@@ -793,14 +797,14 @@ def _mx_operands(w: Mx, X, out_dtype, out, workspace, glu: bool, *others):
         T = X.shape[0]
         ldx = _row_pitch("X", X, T, w.K)
         xq, xp = None, X.data_ptr()
-        x0, default = X, X.dtype
+        x0, xs, default = X, None, X.dtype
     if out is None:
         out = x0.new_empty((T, w.rows), dtype=default if out_dtype is None else out_dtype)
     elif out_dtype is not None:
         _check_dtype("out", out, out_dtype)
     ydt = _float_type("out", out.dtype)
     ldy = _row_pitch("out", out, T, w.rows)
-    dev = _one_gpu("X", x0, ("weight codes", w.codes), ("weight scales", w.scales), ("out", out), *others)
+    dev = _one_gpu(names, x0, xs, w.codes, w.scales, out, *others)
     need = _sized(lib().nm_mx_workspace_size, "nm_mx_workspace_size", ("mx", w.rows, w.K, T, glu, xq is None, dev),
                   _descriptor(w), xq, T, int(glu))
     return dev, T, xq, xp, ldx, xdt, out, ldy, ydt, _workspace(workspace, need, dev)
@@ -821,8 +825,8 @@ def mx_linear(w: Mx, X, bias: torch.Tensor | None = None, out_dtype: torch.dtype
         if bias.shape != (w.rows,) or (w.rows > 1 and bias.stride(0) != 1):
             raise ValueError(f"bias must be a contiguous vector of length R={w.rows}, got {tuple(bias.shape)}")
         bp = bias.data_ptr()
-    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, ws = _mx_operands(w, X, out_dtype, out, workspace, False,
-                                                               ("bias", bias))
+    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, ws = _mx_operands(
+        w, X, out_dtype, out, workspace, False, "X, X scales, weight codes, weight scales, out, bias", bias)
     _call(dev, lib().nm_mx_linear, "nm_mx_linear", _descriptor(w), xq, xp, ldx, xdt, T, out.data_ptr(), ldy, ydt, bp,
           ACTS[act], ws[1], ws[2])
     return out
@@ -836,8 +840,9 @@ def mx_glu(gate: Mx, up: Mx, X, act: str = "silu", out_dtype: torch.dtype | None
     a = _glu_act(act)
     if gate.rows != up.rows or gate.K != up.K:
         raise ValueError(f"gate is {gate.rows} x {gate.K}, up is {up.rows} x {up.K}")
-    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, ws = _mx_operands(gate, X, out_dtype, out, workspace, True,
-                                                               ("up codes", up.codes), ("up scales", up.scales))
+    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, ws = _mx_operands(
+        gate, X, out_dtype, out, workspace, True,
+        "X, X scales, gate codes, gate scales, out, up codes, up scales", up.codes, up.scales)
     _call(dev, lib().nm_mx_glu, "nm_mx_glu", _descriptor(gate), _descriptor(up), xq, xp, ldx, xdt, T, out.data_ptr(),
           ldy, ydt, a, ws[1], ws[2])
     return out

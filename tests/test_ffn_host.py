@@ -260,3 +260,22 @@ def test_binding_refuses_mx_operands():
         nm.mx_glu(w, nm.Mx(17, 64, w.codes, w.scales), X)
     with pytest.raises(ValueError, match="not on a GPU"):
         nm.mx_glu(w, w, X)
+
+
+class _On:
+    """Stands for a tensor on one device."""
+
+    def __init__(self, i):
+        self.i, self.device = i, f"cuda:{i}"
+
+    def get_device(self):
+        return self.i
+
+
+def test_binding_names_the_tensor_on_another_gpu():
+    a, b = _On(0), _On(1)
+    assert nm._one_gpu("X, gate, out", a, a, None) == 0 and nm._one_gpu("X, gate, out", b, None, b) == 1
+    with pytest.raises(ValueError, match="out is on cuda:1, X on cuda:0"):
+        nm._one_gpu("X, gate, out", a, None, b)
+    with pytest.raises(ValueError, match="gate is on cuda:0, X on cuda:1"):
+        nm._one_gpu("X, gate, out", b, a, b)
