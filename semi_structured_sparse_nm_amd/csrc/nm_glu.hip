@@ -95,14 +95,9 @@ __global__ void __launch_bounds__(256) expand_dense_kernel(Geometry g, DenseArgs
 
 template <int WT>
 __device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, float (&f)[8]) {
-  if (r + 8 <= R) {
-    const v4i x = load16(p + r);
+  const v4i x = load_piece(p, r, R);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = from_16<WT>(((uint32_t)x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = r + i < R ? from_16<WT>(p[r + i]) : 0.f;
-  }
+  for (int i = 0; i < 8; ++i) f[i] = from_16<WT>(((uint32_t)x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
 }
 
 // What the backward pass's products read, in one launch; workgroups take, by
@@ -229,21 +224,10 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
     const int q = it * TH + threadIdx.x;
     const int tl = q >> 3, kl = (q & 7) * 8;
     const int64_t t = t0 + tl, k = k0 + kl;
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
-    if (t < a.T) {
-      const uint16_t* x = a.X + t * a.ldx + k;
-      if (k + 8 <= K) {
-        const v4i v = load16(x);
+    v4i o = {0, 0, 0, 0};
+    if (t < a.T && k < K) o = load_piece(a.X + t * a.ldx, k, K);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = (uint32_t)v[i];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (k + e < K) o[e >> 1] |= (uint32_t)x[e] << (16 * (e & 1));
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) tile[kl + e][tl] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+    for (int e = 0; e < 8; ++e) tile[kl + e][tl] = (uint16_t)((uint32_t)o[e >> 1] >> (16 * (e & 1)));
   }
   __syncthreads();
 #pragma unroll
@@ -274,14 +258,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_
   const int64_t pr = Kp / 8;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * pr; i += (int64_t)gridDim.x * 256) {
     const int64_t t = i / pr, k = (i - t * pr) * 8;
-    v4i o = {0, 0, 0, 0};
-    if (k + 8 <= K) {
-      o = load16(X + t * ldx + k);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < K) o[e >> 1] |= (int)((uint32_t)X[t * ldx + k + e] << (16 * (e & 1)));
-    }
+    const v4i o = k < K ? load_piece(X + t * ldx, k, K) : v4i{0, 0, 0, 0};
     *reinterpret_cast<v4i*>(Y + t * Kp + k) = o;
   }
 }

@@ -139,14 +139,6 @@ struct GluFrag {
   __device__ static int kpiece(int p, int lg) { return SPARSE ? 32 * p + 8 * lg : 16 * lg + 8 * p; }
 };
 
-#if defined(__HIP_DEVICE_COMPILE__)
-// eight 16-bit values without their first n (zeros follow)
-__device__ __forceinline__ v4i shift_out(v4i x, int n) {
-  const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, x);
-  return __builtin_bit_cast(v4i, v >> (16 * n));
-}
-#endif
-
 // SHORT: K is no multiple of eight (groups of four only).
 template <int WT, int N, int M, int NT, bool SHORT>
 __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, int groups) {

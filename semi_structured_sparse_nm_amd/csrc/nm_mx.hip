@@ -34,9 +34,13 @@ __global__ void __launch_bounds__(TH) mx_quantize_kernel(const uint8_t* X, int64
     for (int i = 0; i < ND; ++i) x[i] = 0;
     if (r < rows && k < K) {
       const uint8_t* p = X + (r * ldx + k) * EB;
-      if (k + 8 <= K) {
+      if constexpr (EB == 2) {
+        const v4i v = load_piece(reinterpret_cast<const uint16_t*>(X) + r * ldx, k, K);
 #pragma unroll
-        for (int i = 0; i < ND / 4; ++i) {
+        for (int e = 0; e < 4; ++e) x[e] = (uint32_t)v[e];
+      } else if (k + 8 <= K) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           const v4i v = load16(p + 16 * i);
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[4 * i + e] = (uint32_t)v[e];
@@ -44,12 +48,7 @@ __global__ void __launch_bounds__(TH) mx_quantize_kernel(const uint8_t* X, int64
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (k + i < K) {
-            if constexpr (EB == 4)
-              x[i] = reinterpret_cast<const uint32_t*>(p)[i];
-            else
-              x[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-          }
+          if (k + i < K) x[i] = reinterpret_cast<const uint32_t*>(p)[i];
       }
     }
     const uint32_t m = quad_max(mx_amax8<DT>(x));
