@@ -387,9 +387,9 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, cons
  * nm_glu_backward.  Activations are finite: whether an infinite or NaN one
  * reaches an output through a pruned weight depends on the path the call
  * takes (it never reaches another token).  NM_FFN_TILE=<kind>:<shape>[:<split>]
- * in the environment ("tile" or "tile24", shapes 0 to 3) forces a tile shape
- * where the call takes that kind of tile product; stream:1 and stream:0 force
- * and forbid streamed weights (up to 512 tokens).  Outputs and workspace
+ * in the environment ("tile" or "tile24", shapes 0 to 3) forces that kind's
+ * tile products to a shape, and a call to tile products; stream:1 and stream:0
+ * force and forbid streamed weights (up to 1024 tokens).  Outputs and workspace
  * overlap no other buffer of the call.  The workspace (256-byte aligned, at
  * least nm_glu_workspace_size bytes) is written and read back within the
  * call's stream order, so calls that share one must be ordered.

@@ -18,7 +18,14 @@ bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
 
 // Up to the first number of tokens weights are streamed always, up to the
 // second where that is faster; beyond, the tile product shares them.
-constexpr int64_t kStreamOnly = 32, kStreamTokens = 512;
+constexpr int64_t kStreamOnly = 32, kStreamTokens = 1024;
+
+// -1, or what the environment forces: 1 streamed weights, 0 tiles
+int stream_forced() {
+  int v;
+  if (nm::ffn_tile_override("stream", &v, nullptr)) return v != 0;
+  return nm::ffn_tile_override("tile", &v, nullptr) || nm::ffn_tile_override("tile24", &v, nullptr) ? 0 : -1;
+}
 
 // Microseconds of a product whose weights (`weights` bytes) are streamed for
 // every 64 of T tokens: at 5.8 TB/s from HBM first, then out of the caches;
@@ -26,7 +33,8 @@ constexpr int64_t kStreamOnly = 32, kStreamTokens = 512;
 // bytes/us; and `each` us a workgroup of a compute unit besides.
 double stream_time(int64_t T, int64_t blocks, double weights, double x, double rate, double each, int cus) {
   const double groups = (double)((T + 63) / 64), b = (double)blocks;
-  return 2.0 + weights / 5.8e6 * (0.4 + 0.6 * groups) + groups * b * (64 * x / rate + each / cus);
+  const double t = 2.0 + weights / 5.8e6 * (0.4 + 0.6 * groups) + groups * b * (64 * x / rate + each / cus);
+  return T <= 512 ? t : 1.4 * t;                       // (600 x 4096, 2:4: 21 us for 600 tokens, 34 for 1024)
 }
 
 // Longest dimension taken, and most workgroups of 256 threads: a launch has
@@ -96,8 +104,8 @@ Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g
 GluPath glu_path(const Geometry& g, int64_t T) {
   const GluPath tiles = g.N == 2 && g.M == 4 ? GLU_SPARSE : nm::repack24_supported(g) ? GLU_REPACK : GLU_DENSE;
   if (T > kStreamTokens) return tiles;
-  int forced;
-  if (nm::ffn_tile_override("stream", &forced, nullptr)) return forced ? GLU_STREAM : tiles;
+  const int forced = stream_forced();
+  if (forced >= 0) return forced ? GLU_STREAM : tiles;
   if (T <= kStreamOnly) return GLU_STREAM;
   const int cus = nm::device_cu_count();
   const double packed = 2.0 * (double)(g.values_bytes() + g.meta_bytes());
@@ -192,14 +200,14 @@ struct MxPath {
 };
 MxPath mx_path(bool glu, int64_t T, int64_t R, int64_t K) {
   MxPath p{};
-  int forced = -1;
-  if (T <= kStreamTokens && nm::ffn_tile_override("stream", &forced, nullptr) ? forced : T <= kStreamOnly) {
+  const int forced = stream_forced();
+  if (T <= kStreamTokens && (forced >= 0 ? forced : T <= kStreamOnly)) {
     p.stream = true;
     return p;
   }
   const int cus = nm::device_cu_count();
   p.plan = nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), cus);
-  if (T > kStreamTokens || !forced) return p;
+  if (T > kStreamTokens || forced == 0) return p;
   const double w = (glu ? 2.0 : 1.0) * (double)(R * nm::mx_kp(K)) * 17 / 32;
   if (stream_time(T, (R + 15) / 16, w, 0.5 * nm::mx_kp(K), 30e6, 0.3, cus) <= p.plan.time) p = MxPath{true, {}};
   return p;

@@ -25,13 +25,13 @@ def _glu(g=None, u=None, X=P[0], ldx=128, T=5, H=P[1], ldh=48, act=2, G=None, U=
 def test_glu_refusals():
     L = nm.lib()
     # a 4:8 weight and many tokens: dense copies in the workspace
-    dense = dict(T=600, g=_w(N=4, M=8), u=_w(N=4, M=8))
+    dense = dict(T=1100, g=_w(N=4, M=8), u=_w(N=4, M=8))
     assert L.nm_glu(None, None, P[0], 128, 5, P[1], 48, 2, None, None, 0, None, 0, None) == EINVAL
     for kw in (dict(X=None), dict(H=None), dict(T=0), dict(T=-3), dict(ldx=127), dict(ldh=47), dict(G=P[3], ldp=48),
                dict(U=P[3], ldp=48), dict(G=P[3], U=P[4], ldp=47), dict(u=_w(R=49)), dict(u=_w(K=132)),
                dict(u=_w(N=1)), dict(u=_w(N=4, M=8)), dict(u=_w(dt=nm.NM_BF16)), dict(g=_w(format_version=0)),
                dict(u=_w(format_version=9)), dict(g=_w(values_bytes=7)), dict(u=_w(meta=None)),
-               dict(**dense, ws=None), dict(**dense, wsb=1000), dict(T=600, X=P[0] + 2, ws=None)):
+               dict(**dense, ws=None), dict(**dense, wsb=1000), dict(T=1100, X=P[0] + 2, ws=None)):
         assert _glu(**kw) == EINVAL, kw
     i8 = dict(dt=nm.NM_I8)
     for kw in (dict(g=_w(**i8), u=_w(**i8)), dict(act=0), dict(act=3), dict(X=P[0] + 1), dict(H=P[1] + 1),
@@ -47,15 +47,15 @@ def test_glu_workspace():
     n = ctypes.c_size_t()
     f = nm.lib().nm_glu_workspace_size
     g, u = _w(R=50, K=100), _w(R=50, K=100)
-    assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 600, ctypes.byref(n)) == nm.NM_OK and n.value == 600 * 256
+    assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 1100, ctypes.byref(n)) == nm.NM_OK and n.value == 1100 * 256
     assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 0, ctypes.byref(n)) == EINVAL
     assert f(ctypes.byref(g), ctypes.byref(u), None, 0, 5, None) == EINVAL
     assert f(ctypes.byref(g), ctypes.byref(u), P[0], 99, 5, ctypes.byref(n)) == EINVAL
     assert f(ctypes.byref(g), ctypes.byref(_w(R=51, K=100)), None, 0, 5, ctypes.byref(n)) == EINVAL
     # rows the kernels read as they are, and not: tiles, then streamed weights
     d, short = _w(R=50, K=104), _w(R=50, K=4)
-    for X, ldx, want in ((P[0], 104, 0), (P[0] + 16, 112, 0), (P[0] + 2, 104, 600 * 256), (P[0], 105, 600 * 256)):
-        assert f(ctypes.byref(d), ctypes.byref(d), X, ldx, 600, ctypes.byref(n)) == nm.NM_OK and n.value == want
+    for X, ldx, want in ((P[0], 104, 0), (P[0] + 16, 112, 0), (P[0] + 2, 104, 1100 * 256), (P[0], 105, 1100 * 256)):
+        assert f(ctypes.byref(d), ctypes.byref(d), X, ldx, 1100, ctypes.byref(n)) == nm.NM_OK and n.value == want
         assert f(ctypes.byref(d), ctypes.byref(d), X, ldx, 5, ctypes.byref(n)) == nm.NM_OK and n.value == 0
     assert f(ctypes.byref(short), ctypes.byref(short), P[0], 4, 5, ctypes.byref(n)) == nm.NM_OK and n.value == 1280 // 2 + 128
     b = nm.lib().nm_glu_backward_workspace_size

@@ -318,7 +318,7 @@ def test_glu_tile_shapes(tile, shape, K, N, M):
 
 @pytest.mark.parametrize("N,M", [(2, 4), (3, 4), (4, 4), (1, 8), (4, 8), (7, 8)])
 @pytest.mark.parametrize("T,R,K", [(1, 300, 1032), (17, 150, 520), (33, 40, 64), (64, 130, 200), (65, 16, 1096),
-                                   (130, 333, 584), (512, 40, 72)])
+                                   (130, 333, 584), (1024, 40, 72)])
 @pytest.mark.parametrize("stream", [0, 1])
 def test_glu_streamed_and_not(tile, stream, T, R, K, N, M):
     """Both ways of every pattern: one to eight groups of tokens, the last short."""
