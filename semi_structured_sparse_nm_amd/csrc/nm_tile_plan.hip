@@ -130,7 +130,8 @@ TilePlan plan_back(int64_t T, int64_t R, int64_t K, int nslab_x, int nslab_w, bo
         p.lead = (int)lead;
       }
     }
-    if (p.split > 1) best += (double)T * (double)K * (8.0 * p.split + 2.0) / 16.4e6 + 2.0;
+    // (and a launch, of which small calls wait for the host's part)
+    if (p.split > 1) best += (double)T * (double)K * (8.0 * p.split + 2.0) / 16.4e6 + 4.5;
     return best;
   });
 }
