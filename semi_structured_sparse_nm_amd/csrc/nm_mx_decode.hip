@@ -15,6 +15,7 @@
 // 4096, 64 tokens: 24.4 us in that order from the caches, 17.6 so).  The waves'
 // sums meet in LDS, added in wave order.
 #include "nm_mx_device.hpp"
+#include "nm_mx_lanes.hpp"
 
 namespace nm {
 
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
   const int wsh = 16 * (int)(rb & 1);                  // this 16-row half's two scales of each word
 
   // activations to quantise: lane 32 h + p takes values 8 p .. of the slab of
-  // token 2 i + h; tokens past T and columns past K read as zeros (an offset
-  // the resource does not hold)
+  // token 2 i + h.  Tokens past T repeat the last (what they give is not used);
+  // columns past K are zeroed in registers
   const int hx = lane >> 5, px = lane & 31;
   const int tn = Q ? (int)min(a.T - t0, (int64_t)16) : 0;
   const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
@@ -130,8 +131,8 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
         uint32_t x[2][ND];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int t = i0 + 2 * u + hx;
           if constexpr (ANY) {
+            const int t = i0 + 2 * u + hx;
             // a row's short last piece as its last eight values, shifted; all
             // lanes read inside their row
             const int64_t k = (int64_t)s * 256 + px * 8;
@@ -149,15 +150,18 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
               for (int i = 0; i < ND; ++i) x[u][i] = 0;
             continue;
           }
-          const int off = t * pitch + px * 8 * EB;
 #pragma unroll
           for (int i = 0; i < ND / 4; ++i) {
-            const bool in = t < tn && so + px * 8 * EB + 16 * i < kbytes;
-            const v4i v = __builtin_bit_cast(
-                v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? off + 16 * i : (int)0x80000000, so, 0));
+            const int off = mx_lane_offset<EB>(lane, i0 + 2 * u, i, tn, pitch, so, kbytes);
+            const v4i v = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, off, so, 0));
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[u][4 * i + e] = (uint32_t)v[e];
           }
+        }
+        if (!ANY && so + 256 * EB > kbytes) {            // the row's last slab, short
+#pragma unroll
+          for (int i = 0; i < ND; ++i)
+            if (!mx_lane_inside<EB>(lane, i / 4, so, kbytes)) x[0][i] = x[1][i] = 0;
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -170,12 +174,14 @@ __global__ void __launch_bounds__(NW * 64) mx_decode_kernel(MxDecodeArgs a, int 
           if ((px & 3) == 0) qw[16 * 128 + t * 8 + 2 * ((px >> 2) & 3) + (px >> 4)] = (uint8_t)byte;
         }
       }
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         const v4i v = *reinterpret_cast<const v4i*>(qw + li * 128 + 16 * ((4 * kk + lq) ^ (li & 7)));
         fx[0][kk] = li < tn ? v : v4i{0, 0, 0, 0};
       }
       sx[0] = li < tn ? (int)*reinterpret_cast<const uint16_t*>(qw + 16 * 128 + li * 8 + 2 * lq) : 0;
+      __builtin_amdgcn_wave_barrier();
     } else {
       v4i x[2 * NT];
 #pragma unroll

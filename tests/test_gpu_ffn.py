@@ -502,6 +502,21 @@ MX_SHAPES = [(1, 1, 1), (1, 8, 7), (1, 17, 40), (2, 100, 256), (3, 33, 9), (9, 2
              (70, 129, 256), (129, 300, 520), (300, 257, 1288)]
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T", range(1, 17))
+def test_mx_few_tokens_quantised_inside(T, dt):
+    """Activations quantised inside the product and beforehand: the same bits,
+    for every token count a load of token pairs can end at, one to several
+    slabs a wave, the last one whole and short, inputs new to the caches."""
+    for K, R in ((256, 40), (264, 33), (2560, 17), (8712, 100)):
+        w, u = _mx_w(R, K, dt)[0], _mx_w(R, K, dt, "u")[0]
+        for i in range(3):
+            X = normal((T, K), 1.0, dt, "X", T, K, i)
+            q = nm.mx_quantize(X)
+            assert torch.equal(nm.mx_linear(w, X), nm.mx_linear(w, q, out_dtype=X.dtype)), (K, i)
+            assert torch.equal(nm.mx_glu(w, u, X), nm.mx_glu(w, u, q, out_dtype=X.dtype)), (K, i)
+
+
 def _mx_w(R, K, dt, *key):
     W = normal((R, K), 0.05, dt, "mw", R, K, *key)
     return nm.mx_quantize(W), _ffn.mx64(W)[0]
