@@ -25,8 +25,8 @@ int stream_tiles(int64_t blocks, int64_t T) {
 
 // The debug override NM_FFN_TILE=<kind>:<shape>[:<split>], kind "tile" (the dense
 // tile product) or "tile24" (the sparse one): that shape, and for a product
-// that takes one that split where its slabs divide into it; kind "stream", 0 or
-// 1: whether the gated block streams its weights.  For tests.
+// that takes one that split, or the next smaller one its slabs divide into;
+// kind "stream", 0 or 1: whether a product streams its weights.  For tests.
 bool ffn_tile_override(const char* kind, int* shape, int* split) {
   const char* e = getenv("NM_FFN_TILE");
   if (!e) return false;
@@ -73,13 +73,18 @@ template <class F>
 TilePlan best_plan(int smax, int nslab, F&& time) {
   int only = -1, only_split = 0;
   ffn_tile_override("tile", &only, &only_split);
+  if (only_split) {
+    // the most slices up to the forced ones that the slabs divide into
+    const int sps = (nslab + std::min(only_split, smax) - 1) / std::min(only_split, smax);
+    only_split = (nslab + sps - 1) / sps;
+  }
   TilePlan best{0, 1, nslab, 0, 0};
   for (int i = 0; i < 4; ++i) {
     if (only >= 0 && i != only) continue;
     for (int s = 1; s <= smax; ++s) {
       const int sps = (nslab + s - 1) / s;
       const int split = (nslab + sps - 1) / sps;
-      if (split != s || (only_split && smax > 1 && s != std::min(only_split, nslab))) continue;
+      if (split != s || (only_split && s != only_split)) continue;
       TilePlan p{i, split, sps, 0, 0};
       p.time = time(kShapes[i], p);
       if (best.time == 0 || p.time < best.time) best = p;

@@ -100,6 +100,29 @@ def test_mx_workspace():
     assert f(b, None, 0, 0, nb) == EINVAL and f(None, None, 5, 0, nb) == EINVAL and f(b, None, 5, 0, None) == EINVAL
 
 
+@pytest.mark.parametrize("shape", [0, 1, 2, 3])
+@pytest.mark.parametrize("asked,slabs,split", [(1, 33, 1), (2, 33, 2), (7, 33, 7), (16, 33, 11), (16, 32, 16), (5, 6, 3),
+                                               (5, 10, 5), (5, 1, 1), (16, 3, 3)])
+def test_forced_splits(monkeypatch, shape, asked, slabs, split):
+    """A forced split is taken, or the most slices up to it that the reduction
+    divides into: seen by the partial sums' workspace."""
+    monkeypatch.setenv("NM_FFN_TILE", f"tile:{shape}:{asked}")
+    n = ctypes.c_size_t()
+    T, R = 70, 333
+    w, x = _mx(R, 256 * slabs), _mx(T, 256 * slabs)
+    assert nm.lib().nm_mx_workspace_size(ctypes.byref(w), ctypes.byref(x), T, 0, ctypes.byref(n)) == nm.NM_OK
+    assert n.value == (-(-split * T * R * 4 // 256) * 256 if split > 1 else 0)
+    # the input's gradient: a reduction over both weights' rows, 64 a slab
+    if slabs % 2 == 0:
+        g = _w(R=32 * slabs - 5, K=128)
+        f = nm.lib().nm_glu_backward_workspace_size
+        assert f(ctypes.byref(g), ctypes.byref(g), T, ctypes.byref(n)) == nm.NM_OK
+        got = n.value
+        monkeypatch.setenv("NM_FFN_TILE", f"tile:{shape}:1")
+        assert f(ctypes.byref(g), ctypes.byref(g), T, ctypes.byref(n)) == nm.NM_OK
+        assert got - n.value == (-(-split * T * 128 * 4 // 256) * 256 if split > 1 else 0)
+
+
 def test_lengths_past_one_launch():
     """Sizes whose launch would pass 2^32 threads are refused."""
     c = ctypes.c_size_t()

@@ -605,6 +605,26 @@ def test_mx_split_reductions(tile, R, split):
     assert bool((ob[:, R:] == 5.0).all())
 
 
+@pytest.mark.parametrize("shape", [0, 1, 2, 3])
+@pytest.mark.parametrize("split,K", [(5, 2560), (16, 8192), (16, 4096), (11, 8200)])
+def test_mx_splits_that_divide(tile, shape, split, K):
+    """The largest splits in every shape, one slab a slice and more; the
+    workspace holds that many slices."""
+    T, R = 130, 300
+    w, W = _mx_w(R, K, "bf16")
+    X = normal((T, K), 0.05, "bf16", "X", K)
+    q = nm.mx_quantize(X)
+    b = normal((R,), 1.0, "f32", "b", R)
+    tile("tile", shape, split)
+    quant = -(-T * (-(-K // 256) * 128) // 256) * 256 + -(-T // 32) * -(-K // 256) * 256
+    assert nm.mx_workspace_size(w, T) == quant + -(-split * T * R * 4 // 256) * 256
+    x = _ffn.mx64(X)[0]
+    y, e = x @ W.t() + b.double(), _ffn.sum_err(K, x.abs() @ W.abs().t()) + 2.0 ** -23 * split * b.double().abs()
+    Y = nm.mx_linear(w, X, bias=b)
+    check(Y, y, e + 2.0 ** -23 * (y.abs() + e), "Y")
+    assert torch.equal(nm.mx_linear(w, q, bias=b), Y)
+
+
 def test_mx_offsets_past_32_bits():
     """Outputs, then quantised activations, of more than 2^32 bytes."""
     for T, R, K in ((70000, 32768, 64), (300000, 64, 32768)):
