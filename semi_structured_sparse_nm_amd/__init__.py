@@ -25,6 +25,7 @@ Sec. 4.2 packed windows and micro-dense execution.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -486,6 +487,9 @@ GLU_ACTS = {"gelu": 1, "silu": 2}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _ws_sizes: dict = {}
+# NM_FFN_TILE as it is now, or None; from the mapping behind os.environ (50 ns
+# against 550, in calls of 9 us)
+_forced_path = functools.partial(os.environ._data.get, os.environ.encodekey("NM_FFN_TILE"))
 
 
 def _descriptor(p):
@@ -506,15 +510,19 @@ def _descriptor(p):
 
 
 def _sized(f, what: str, key: tuple, *args) -> int:
-    """A workspace size of the library, remembered by shape and device."""
-    n = _ws_sizes.get(key)
+    """A workspace size of the library, remembered by shape and device; asked
+    for again where the environment forces a path, which decides it too."""
+    forced = _forced_path() is not None
+    n = None if forced else _ws_sizes.get(key)
     if n is None:
         b = ctypes.c_size_t()
         with torch.cuda.device(key[-1]):                  # the plan depends on the device
             _check(f(*args, ctypes.byref(b)), what)
-        if len(_ws_sizes) > 4096:
-            _ws_sizes.clear()
-        n = _ws_sizes[key] = b.value
+        n = b.value
+        if not forced:
+            if len(_ws_sizes) > 4096:
+                _ws_sizes.clear()
+            _ws_sizes[key] = n
     return n
 
 

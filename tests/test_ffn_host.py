@@ -1,6 +1,7 @@
 """Refusals of the feed-forward operators, on the host (no GPU needed): every
 documented error comes back before anything is launched, so the fake device
 addresses are never touched; and the binding's own checks."""
+import contextlib
 import ctypes
 
 import pytest
@@ -302,3 +303,26 @@ def test_binding_names_the_tensor_on_another_gpu():
         nm._one_gpu("X, gate, out", a, None, b)
     with pytest.raises(ValueError, match="gate is on cuda:0, X on cuda:1"):
         nm._one_gpu("X, gate, out", b, a, b)
+
+
+def test_workspace_sizes_follow_a_forced_path(monkeypatch):
+    """A size remembered for one path is not given to a call that the
+    environment sends down another."""
+    asked = []
+
+    def size(want, out):
+        asked.append(want)
+        out._obj.value = want
+        return nm.NM_OK
+
+    monkeypatch.setattr(torch.cuda, "device", lambda i: contextlib.nullcontext())
+    monkeypatch.setattr(nm, "_ws_sizes", {})
+    monkeypatch.delenv("NM_FFN_TILE", raising=False)
+    key = ("glu", 8, 8, 0)
+    assert nm._sized(size, "size", key, 5) == 5 and nm._sized(size, "size", key, 6) == 5 and asked == [5]
+    monkeypatch.setenv("NM_FFN_TILE", "stream:0")
+    assert nm._sized(size, "size", key, 7) == 7
+    monkeypatch.setenv("NM_FFN_TILE", "stream:1")
+    assert nm._sized(size, "size", key, 8) == 8
+    monkeypatch.delenv("NM_FFN_TILE")
+    assert nm._sized(size, "size", key, 9) == 5 and asked == [5, 7, 8]

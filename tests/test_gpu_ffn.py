@@ -293,6 +293,27 @@ def tile(monkeypatch):
     nm._ws_sizes.clear()
 
 
+def test_forced_path_after_a_call(monkeypatch):
+    """A path forced between calls gets the workspace it needs: dense copies
+    (4:8 by tiles) after streamed weights, which need none, and back."""
+    T, R, K, dt = 40, 96, 264, "bf16"
+    pg, wg, _ = weights(R, K, 4, 8, dt, "g")
+    pu, wu, _ = weights(R, K, 4, 8, dt, "u")
+    w, W = _mx_w(R, K, dt)
+    X = normal((T, K), 1.0, dt, "X")
+    h, _, _, eh, _, _ = _ffn.glu64(X, wg, wu, "silu")
+    x = _ffn.mx64(X)[0]
+    y, e = x @ W.t(), _ffn.sum_err(K, x.abs() @ W.abs().t())
+    monkeypatch.delenv("NM_FFN_TILE", raising=False)
+    for forced in (None, "stream:0", "stream:1", "tile:3:2", None):
+        if forced is None:
+            monkeypatch.delenv("NM_FFN_TILE", raising=False)
+        else:
+            monkeypatch.setenv("NM_FFN_TILE", forced)
+        check(nm.glu(pg, pu, X), h, eh, f"H {forced}")
+        check(nm.mx_linear(w, X), y, e, f"Y {forced}")
+
+
 # tokens, rows, columns: several tiles a workgroup, the last ragged both ways
 TILES = {0: (2100, 4200), 1: (1100, 3900), 2: (1100, 4300), 3: (700, 3700)}
 
