@@ -418,7 +418,8 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
  * may both weight gradients together (then they are not computed); not all
  * three.  dG and dU are rounded to the weight dtype before the two products,
  * as operands of the matrix instruction; sums are binary32 and every output
- * is rounded once.  The result does not depend on launch order (no atomics).
+ * is rounded once.  An infinite G or U (fp16: a product nm_glu rounded from
+ * beyond 65504) counts as the type's largest value of its sign.  The result does not depend on launch order (no atomics).
  * All buffers have the weight dtype.  Errors as nm_glu; NM_EINVAL also for
  * no output at all, one weight gradient without the other, lddx < K, lddw < K;
  * NM_EUNSUPPORTED also for T of 2^22 or R of 2^21 and more.

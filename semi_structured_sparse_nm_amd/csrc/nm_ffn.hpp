@@ -221,6 +221,12 @@ __device__ __forceinline__ uint32_t pack_16x2(float lo, float hi) {
   else
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f_{lo, hi}), v2bf_));
 }
+// infinities as the 16-bit type's largest value of their sign (NaN stays)
+template <int DT>
+__device__ __forceinline__ float finite_16(float x) {
+  constexpr float top = DT == NM_F16 ? 65504.f : 0x1.FEp127f;
+  return __builtin_fabsf(x) > top ? __builtin_copysignf(top, x) : x;
+}
 template <int DT>
 __device__ __forceinline__ float from_16(uint32_t bits) {
   if constexpr (DT == NM_F16)

@@ -106,7 +106,9 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, f
 //  - 64 tokens x 64 outputs of dG and dU, as rows (d) and transposed (dt).  They
 //    are rounded to the weights' 16-bit type here: operands of the matrix
 //    instruction in both products that follow (half a step each, as any
-//    16-bit operand).
+//    16-bit operand).  A kept product past the type's range (fp16: the forward
+//    pass has it in binary32 and H stays finite) counts as the largest value:
+//    as an infinity it would meet the slope's zero and make whole rows NaN.
 //  - 128 rows x 64 columns of one weight, expanded and transposed (wt), with
 //    the bits of the kept columns.
 //  - 64 tokens x 64 columns of X, transposed (xt).
@@ -138,9 +140,9 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y, dy;
-          glu_act_slope(a.act, g[2 * i + e], y, dy);
+          glu_act_slope(a.act, finite_16<WT>(g[2 * i + e]), y, dy);
           const bool in = r + 2 * i + e < a.g.R;
-          dg[e] = in ? h[2 * i + e] * u[2 * i + e] * dy : 0.f;
+          dg[e] = in ? h[2 * i + e] * finite_16<WT>(u[2 * i + e]) * dy : 0.f;
           du[e] = in ? h[2 * i + e] * y : 0.f;
         }
         og[i] = pack_16x2<WT>(dg[0], dg[1]);

@@ -443,6 +443,46 @@ def test_glu_backward_keeps_pruned_gradients_zero():
         assert bool(torch.isnan(d[4][k[4]]).all())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [3, 70, 200])
+def test_glu_backward_of_products_past_the_type(T, dt, act):
+    """Products that 16 bits hold as infinities: H is finite, and the gradients
+    are those of the type's largest value, finite in every row."""
+    R, K = 48, 64
+    top = torch.finfo(TORCH[dt]).max
+    Wg = normal((R, K), 0.05, dt, "Wg")
+    Wg[:, 0] = 0.0
+    Wg[::3, 0] = 40000.0 if dt == "f16" else 0.0
+    Wu = normal((R, K), 0.05, dt, "Wu")
+    kg, ku = _ffn.kept(Wg, 2, 4), _ffn.kept(Wu, 2, 4)
+    wg, wu = torch.where(kg, Wg, 0.0), torch.where(ku, Wu, 0.0)
+    pg, pu = nm.pack(Wg, 2, 4), nm.pack(Wu, 2, 4)
+    X = normal((T, K), 0.1, dt, "X", T)
+    X[:, 0] = torch.tensor([2.0, -2.0, 0.5], device="cuda").repeat(T)[:T]
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    H = nm.glu(pg, pu, X, act=act, pre=pre)
+    assert bool(torch.isfinite(H).all())
+    if dt == "f16":
+        assert bool((pre[0, 0::3, ::3] == float("inf")).all()) and bool((pre[0, 1::3, ::3] == float("-inf")).all())
+    else:
+        pre[0, 0, ::3], pre[0, 1, ::3] = float("inf"), float("-inf")
+    pre[1, 2, 5::6] = float("inf")
+    dH = normal((T, R), 0.0005, dt, "dH", T)
+    if dt == "bf16":
+        dH *= 2.0 ** -100                                 # outputs within the type
+    else:
+        dH[2, 5::6] = 2.0 ** -14
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre.clamp(-top, top), dH, act)
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, X, pre, dH, act=act), want, bound, ("dX", "dWg", "dWu")):
+        assert bool(torch.isfinite(a).all()), what
+        check(a, b, e, what)
+    pre[0, 1, 1] = float("nan")                           # what is no number stays none
+    dx, dwg, dwu = nm.glu_backward(pg, pu, X, pre, dH, act=act)
+    assert bool(torch.isnan(dx[1]).any()) and bool(torch.isfinite(dx[[0, 2]]).all())
+    assert bool(torch.isnan(dwg[1][kg[1]]).all()) and bool(torch.isnan(dwu[1][ku[1]]).all())
+
+
 # ---------------------------------------------------------------- microscaled 4-bit format
 def _check_mx(x):
     m = nm.mx_quantize(x)
