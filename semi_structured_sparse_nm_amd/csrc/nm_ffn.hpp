@@ -189,18 +189,30 @@ hipError_t launch_mx_decode(const MxDecodeArgs& a, hipStream_t s);
 // SiLU(x) = x / (1 + exp(-x)), binary32: exp2 and reciprocal of the
 // transcendental unit (1 ulp each); exp's rounded argument adds 2^-24 |x|
 // relative, so the error stays below 2^-22 (1 + |x|) |SiLU(x)|, far below
-// half a 16-bit step.  x -> -inf: exp overflows, its reciprocal is 0.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
+// half a 16-bit step.  With q = exp(-|x| / 2), r = 1 / (1 + q^2) and p = q for
+// negative x, else 1, the sigmoid is p^2 r: multiplied in this order nothing
+// leaves binary32's range before the result does (x / (1 + exp(-x)) as it stands
+// is 0 below x = -88.7, where SiLU is a normal number down to -91.8; gated
+// block of 2048 tokens, 11008 x 4096: 212 us, 209 with it as it stands, 211 with
+// a branch for the far values).
+__device__ __forceinline__ void sigmoid_parts(float x, float& p, float& r) {
+  const float q = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * -0.72134752044448170368f);
+  r = __builtin_amdgcn_rcpf(__builtin_fmaf(q, q, 1.0f));
+  p = x < 0.0f ? q : 1.0f;
 }
-__device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); }
-
+__device__ __forceinline__ float silu_f32(float x) {
+  float p, r;
+  sigmoid_parts(x, p, r);
+  return (x * p) * (p * r);
+}
 // act(x) and act'(x) of the gated block (NM_ACT_GELU or NM_ACT_SILU)
 __device__ __forceinline__ float glu_act(int act, float x) { return act == NM_ACT_SILU ? silu_f32(x) : gelu_f32(x); }
 __device__ __forceinline__ void glu_act_slope(int act, float x, float& y, float& dy) {
   if (act == NM_ACT_SILU) {
-    const float s = sigmoid_f32(x);
-    y = x * s;
+    float p, r;
+    sigmoid_parts(x, p, r);
+    y = (x * p) * (p * r);
+    const float s = p * (p * r);
     dy = s * (1.0f + x * (1.0f - s));
   } else {
     const float cdf = 0.5f * (1.0f + erf_as(x * 0.70710678118654752440f));

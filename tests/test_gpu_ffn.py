@@ -228,6 +228,52 @@ def test_weights_of_zeros_and_saturated_gates():
             check(a, b, e, what)
 
 
+@pytest.mark.parametrize("N,M", [(2, 4), (4, 8)])
+@pytest.mark.parametrize("T", [1, 20, 70, 193])
+def test_silu_of_far_negative_gates(tile, T, N, M):
+    """Gates from -80 to -104, where SiLU leaves the normal numbers but not
+    the type, times factors from 1 to 2^40; and their gradients."""
+    R, K = 20, 64
+    wg, wu = torch.zeros(2, R, K, dtype=torch.bfloat16, device="cuda")
+    wg[:, 0] = 1.0
+    wu[:, 33] = torch.exp2(torch.arange(R, device="cuda") * 2.0)
+    kg, ku = _ffn.kept(wg, N, M), _ffn.kept(wu, N, M)
+    pg, pu = nm.pack(wg, N, M), nm.pack(wu, N, M)
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = torch.linspace(-80, -104, 193)[-T:]
+    X[:, 33] = 1.0
+    h, _, _, eh, _, _ = _ffn.glu64(X, wg, wu, "silu")
+    dH = torch.ones(T, R, dtype=X.dtype, device="cuda")
+    for stream in (0, 1):
+        tile("stream", stream)
+        pre = torch.empty(2, T, R, dtype=X.dtype, device="cuda")
+        check(nm.glu(pg, pu, X, pre=pre), h, eh, f"H {stream}")
+        want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+        dx, dwg, dwu = nm.glu_backward(pg, pu, X, pre, dH)
+        for a, b, e, what in zip((dx, dwg, dwu), want, bound, ("dX", "dWg", "dWu")):
+            check(a, b, e, what)
+        # dWu's column 33 sums dU = SiLU(G): 2^-9 of it for dU's rounding, 2^-9 for its own, 2^-14 for the rest
+        want = _ffn.act64(pre[0].double(), "silu").sum(0)
+        assert bool(((dwu[:, 33].double() - want).abs() <= want.abs() * 2.0 ** -7.9 + T * _ffn.tiny(X.dtype)).all())
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 100])
+def test_mx_silu_of_far_negative_gates(tile, T):
+    """The same at 4 bits: gates of -96 and -64, every path."""
+    R, K = 20, 64
+    W = torch.zeros(2, R, K, dtype=torch.bfloat16, device="cuda")
+    W[0, :, 0] = 1.0
+    W[1, :, 33] = torch.exp2(torch.arange(R, device="cuda") * 2.0)
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    X[:, 0] = torch.tensor([-96.0, -64.0], device="cuda").repeat(T)[:T]
+    X[:, 33] = 1.0
+    h, _, _, eh, _, _ = _ffn.glu64(X, W[0], W[1], "silu")
+    wg, wu = nm.mx_quantize(W[0]), nm.mx_quantize(W[1])
+    for stream in (0, 1):
+        tile("stream", stream)
+        check(nm.mx_glu(wg, wu, X), h, eh, f"H {stream}")
+
+
 def test_packed_weights_copy_and_pickle():
     """A weight that has been used copies and pickles like one that has not."""
     pg, pu = weights(16, 64, 2, 4, "f16", "g")[0], weights(16, 64, 2, 4, "f16", "u")[0]
