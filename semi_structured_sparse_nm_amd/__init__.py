@@ -685,7 +685,10 @@ def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, 
     [T, R] and the products glu() kept in `pre`.  Returns (dX [T, K],
     dWg [R, K], dWu [R, K]) in the weights' dtype; the weight gradients are
     dense and zero where the weight is pruned.  need_dx / need_dw = False
-    leaves that part out (None in its place)."""
+    leaves that part out (None in its place).  The gradients of G and U are
+    operands of the weights' type: float16 ones beyond 65504 are infinite and
+    below 2^-25 zero, so losses are scaled as for any float16 gradient.
+    Neither call is part of autograd's graph."""
     T, ldx = _glu_operands(gate, up, Xt)
     a = _glu_act(act)
     if not need_dx and not need_dw:

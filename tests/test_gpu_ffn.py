@@ -491,6 +491,55 @@ def test_glu_backward_keeps_pruned_gradients_zero():
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,R,K,N,M", [(40, 512, 256, 2, 4), (197, 1000, 768, 4, 8), (512, 700, 520, 3, 4)])
+def test_training_step_against_unrounded_gradients(T, R, K, N, M, dt, act):
+    """Forward and backward against gradients in 64 bits from the inputs alone.
+    A rounding is off by at most half a step h of the value, evenly spread: at
+    most h / sqrt(3) as a norm.  dWg and dX's gate part have four (U, dG, the
+    output, and G through the slope's change, whose norm is below the slope's),
+    dWu and dX's up part three (dU, the output, and G, times at most 1.4): less
+    than 2 h / sqrt(3) together.  binary32 sums add nothing to that."""
+    pg, wg, kg = weights(R, K, N, M, dt, "g")
+    pu, wu, ku = weights(R, K, N, M, dt, "u")
+    X, dH = normal((T, K), 1.0, dt, "X", T), normal((T, R), 0.1, dt, "dH", T)
+    pre = torch.empty((2, T, R), dtype=X.dtype, device="cuda")
+    nm.glu(pg, pu, X, act=act, pre=pre)
+    got = nm.glu_backward(pg, pu, X, pre, dH, act=act)
+    x, g, u, dh = X.double(), X.double() @ wg.double().t(), X.double() @ wu.double().t(), dH.double()
+    dg, du = dh * u * _ffn.slope64(g, act), dh * _ffn.act64(g, act)
+    want = (dg @ wg.double() + du @ wu.double(), (dg.t() @ x) * kg, (du.t() @ x) * ku)
+    lim = 2 * _ffn.half_step(X.dtype) / 3 ** 0.5
+    for a, b, what in zip(got, want, ("dX", "dWg", "dWu")):
+        off = float((a.double() - b).norm() / b.norm())
+        assert off <= lim, f"{what}: {off:.6f} of the norm, at most {lim:.6f}"
+
+
+@pytest.mark.parametrize("T", [5, 70, 300])
+def test_glu_backward_past_the_range_of_fp16(T):
+    """dG or dU beyond 65504: the token's dX and the row of the weight gradient
+    are not finite, nothing else changes; below 2^-25: zero."""
+    R, K = 80, 136
+    pg, _, kg = weights(R, K, 2, 4, "f16", "g")
+    pu, _, ku = weights(R, K, 2, 4, "f16", "u")
+    X, dH = normal((T, K), 1.0, "f16", "X", T), normal((T, R), 0.1, "f16", "dH", T)
+    pre = normal((2 * T, R), 1.0, "f16", "pre", T).view(2, T, R)
+    clean = nm.glu_backward(pg, pu, X, pre, dH)
+    pre[:, 2, 7] = torch.tensor([30.0, 40.0], device="cuda")
+    dH[2, 7] = 30000.0                                    # dG = 1.2e6, dU = 9e5
+    dx, dwg, dwu = nm.glu_backward(pg, pu, X, pre, dH)
+    t, r = torch.arange(T, device="cuda") != 2, torch.arange(R, device="cuda") != 7
+    assert torch.equal(dx[t], clean[0][t]) and torch.equal(dwg[r], clean[1][r]) and torch.equal(dwu[r], clean[2][r])
+    assert not bool(torch.isfinite(dx[2]).all())
+    for d, k in ((dwg, kg), (dwu, ku)):
+        assert not bool(torch.isfinite(d[7][k[7]]).any()) and bool((d[7][~k[7]] == 0).all())
+    pre.fill_(0.25)
+    dH.fill_(2.0 ** -24)                                  # dG, dU below 2^-26
+    for d in nm.glu_backward(pg, pu, X, pre, dH):
+        assert bool((d == 0).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("T", [3, 70, 200])
 def test_glu_backward_of_products_past_the_type(T, dt, act):
     """Products that 16 bits hold as infinities: H is finite, and the gradients
