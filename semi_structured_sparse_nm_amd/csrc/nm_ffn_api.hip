@@ -16,9 +16,10 @@ int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 // rows the tile kernel addresses with 32-bit offsets: 256 of them within 2^31 bytes
 bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
 
-// Up to the first number of tokens weights are streamed always, up to the
-// second where that is faster; beyond, the tile product shares them.
-constexpr int64_t kStreamOnly = 32, kStreamTokens = 1024;
+// Up to the first number of tokens (one tile of the matrix instruction) weights
+// are streamed always, up to the second where that is faster; beyond, the tile
+// product shares them.
+constexpr int64_t kStreamOnly = 16, kStreamTokens = 1024;
 
 // -1, or what the environment forces: 1 streamed weights, 0 tiles
 int stream_forced() {
@@ -27,15 +28,27 @@ int stream_forced() {
   return nm::ffn_tile_override("tile", &v, nullptr) || nm::ffn_tile_override("tile24", &v, nullptr) ? 0 : -1;
 }
 
-// Microseconds of a product whose weights (`weights` bytes) are streamed for
-// every 64 of T tokens: at 5.8 TB/s from HBM first, then out of the caches;
-// `x` bytes of each token, re-read for each of `blocks` of 16 outputs, at `rate`
-// bytes/us; and `each` us a workgroup of a compute unit besides.
-double stream_time(int64_t T, int64_t blocks, double weights, double x, double rate, double each, int cus) {
-  const double groups = (double)((T + 63) / 64), b = (double)blocks;
-  const double t = 2.0 + weights / 5.8e6 * (0.4 + 0.6 * groups) + groups * b * (64 * x / rate + each / cus);
-  return T <= 512 ? t : 1.4 * t;                       // (600 x 4096, 2:4: 21 us for 600 tokens, 34 for 1024)
-}
+// A product whose weights are streamed runs in whole rounds of workgroups, one
+// to a compute unit: the row blocks (16 outputs) of an XCD times the groups of
+// tokens, over its compute units.
+struct StreamRounds {
+  int64_t rounds;
+  int nt;                    // 16-token tiles of a workgroup
+  StreamRounds(int64_t blocks, int64_t T, int cus) : nt(nm::stream_tiles(blocks, T)) {
+    const int64_t slots = (cus + 7) / 8;
+    rounds = ((blocks + 7) / 8 * ((T + 16 * nt - 1) / (16 * nt)) + slots - 1) / slots;
+  }
+  // Microseconds.  passes: of the workgroup's eight waves along K; weight: what
+  // a pass costs for its weights, and 0.2 for each token tile; `bytes` of weights
+  // at 5.4 TB/s at least.  Fitted to 960 products of every pattern and of 4 bits,
+  // 17 to 1024 tokens, 160 to 131072 outputs, K 256 to 8192: 7% off as a root mean
+  // square, 30% at most; the choice costs 0.3% against the faster way as a mean
+  // over them.  For example 2:4, 600 x 4096: 384 tokens 12.5 us (one round), 512
+  // 21.1 and 768 22.6 (two), 1024 33.4 (three).
+  double time(double passes, double weight, double bytes) const {
+    return 2.7 + std::max(rounds * (0.3 + 0.25 * nt + passes * (weight + 0.2 * nt)), bytes / 5.4e6);
+  }
+};
 
 // Longest dimension taken, and most workgroups of 256 threads: a launch has
 // fewer than 2^32 threads.
@@ -96,11 +109,13 @@ enum GluPath {
 
 Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g.eb); }
 
-// By models of both times: stream_time; the tile product's own, and the copies
-// at 5 TB/s.  Measured, streamed and tiles:
-// 11008 x 4096, 2:4 17 and 23 us (16 tokens), 21 and 22 (32), 30 and 22 (64);
-// 4:8 33 and 93 (64), 98 and 112 (256), 149 and 133 (384); 1000 x 3000, 4:8 11
-// and 33 (64), 20 and 33 (512).
+// Weights of one round are streamed: measured, streamed and tiles, 2:4 of 600 x
+// 4096 12.5 and 20.7 us (384 tokens), 4:4 of 600 x 8192 28 and 46, 7:8 43 and 54.
+// More rounds by models of both times: StreamRounds; the tile product's own, and
+// the copies at 5 TB/s.  Measured, streamed and tiles: 11008 x 4096, 2:4 21.4 and
+// 21.3 us (32 tokens), 31 and 22 (64); 4:8 33 and 93 (64), 98 and 112 (256), 149
+// and 133 (384); 131072 x 256, 2:4 42 and 27 (32); 600 x 4096, 2:4 22.6 and 20.9
+// (768), 4:8 23.5 and 30.7.
 GluPath glu_path(const Geometry& g, int64_t T) {
   const GluPath tiles = g.N == 2 && g.M == 4 ? GLU_SPARSE : nm::repack24_supported(g) ? GLU_REPACK : GLU_DENSE;
   if (T > kStreamTokens) return tiles;
@@ -108,12 +123,18 @@ GluPath glu_path(const Geometry& g, int64_t T) {
   if (forced >= 0) return forced ? GLU_STREAM : tiles;
   if (T <= kStreamOnly) return GLU_STREAM;
   const int cus = nm::device_cu_count();
+  const StreamRounds r(g.nRB, T, cus);
+  if (r.rounds == 1) return GLU_STREAM;
+  // what 512 columns of both weights' 16 rows cost a wave: sparse as they are or
+  // by the selector table, and expanded by shifts (3:4, 5:8 to 7:8)
+  static const double weight[2][8] = {{0.10, 0.17, 0.43, 0.63}, {0.22, 0.24, 0.27, 0.34, 1.06, 1.2, 1.67, 0.63}};
   const double packed = 2.0 * (double)(g.values_bytes() + g.meta_bytes());
-  const double stream = stream_time(T, g.nRB, packed, 2.0 * g.K, 35e6, 0.8, cus);
+  const double stream = r.time((double)g.K / 512, weight[g.M == 8][g.N - 1], packed);
   double other;
   if (tiles == GLU_DENSE) {
     const int64_t Kp = up64(g.K);
-    other = 5.0 + (packed + 4.0 * g.R * Kp) / 5e6 +
+    // (odd N of 8: kept values read one at a time)
+    other = 5.0 + ((g.M == 8 && g.N % 2 ? 3.0 : 1.0) * packed + 4.0 * g.R * Kp) / 5e6 +
             nm::plan_tile(nm::TILE_GLU, false, T, g.R, (int)(Kp / 64), cus).time;
   } else {
     other = nm::glu_tile24_time(T, g.R, g.nKB, cus, nullptr);
@@ -190,10 +211,11 @@ size_t mx_ws(int64_t T, int64_t K) { return mx_ws_codes(T, K) + up256((size_t)nm
 // up to 16 tokens are quantised inside the product (in pieces of eight columns)
 bool mx_inside(int64_t T, int64_t K) { return T <= 16 && K >= 8; }
 // How a product of T tokens is computed: the weights streamed for every 64 of
-// them, or the tile product with its plan.  By models of both times.
-// Measured, streamed and tiles: gated block of 11008 x 4096 14.6 and 14.3 us
-// (64 tokens), 23 and 20 (128); of 4096 x 11008 22 and 26 (128), 37 and 27
-// (256); product of 1000 x 3000 5.5 and 12 (256), 7.2 and 12 (512).
+// them (always where that is one round), or the tile product with its plan, by
+// models of both times.  Measured, streamed and tiles: gated block of 11008 x
+// 4096 14.6 and 14.3 us (64 tokens), 23 and 20 (128); of 4096 x 11008 22 and 26
+// (128), 37 and 27 (256); product of 1000 x 3000 5.5 and 12 (256), 7.2 and 12
+// (512); of 131072 x 256 22 and 11 (32).
 struct MxPath {
   bool stream;
   nm::TilePlan plan;
@@ -206,10 +228,13 @@ MxPath mx_path(bool glu, int64_t T, int64_t R, int64_t K) {
     return p;
   }
   const int cus = nm::device_cu_count();
+  const StreamRounds r((R + 15) / 16, T, cus);
+  if (T <= kStreamTokens && forced < 0 && r.rounds == 1) return MxPath{true, {}};
   p.plan = nm::plan_tile(glu ? nm::TILE_GLU : nm::TILE_LINEAR, true, T, R, (int)(nm::mx_kp(K) / nm::kMxSlab), cus);
   if (T > kStreamTokens || forced == 0) return p;
   const double w = (glu ? 2.0 : 1.0) * (double)(R * nm::mx_kp(K)) * 17 / 32;
-  if (stream_time(T, (R + 15) / 16, w, 0.5 * nm::mx_kp(K), 30e6, 0.3, cus) <= p.plan.time) p = MxPath{true, {}};
+  // (2.5: the launch, which the 4-bit tiles' model leaves out)
+  if (r.time((double)nm::mx_kp(K) / 2048, glu ? 0.7 : 0.35, w) <= p.plan.time + 2.5) p = MxPath{true, {}};
   return p;
 }
 
