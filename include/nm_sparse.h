@@ -384,25 +384,31 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, cons
 /*
  * H = act(X Wg^T) (.) (X Wu^T).  G, U: NULL, or both [T][ldp] buffers of the
  * weight dtype that receive the two products, rounded once, for
- * nm_glu_backward.  Activations are finite: whether an infinite or NaN one
+ * nm_glu_backward; nm_glu_kept: of p_dtype, the weight dtype or NM_F32 (the
+ * binary32 sums as they are).  Activations are finite: whether an infinite or NaN one
  * reaches an output through a pruned weight depends on the path the call
  * takes (it never reaches another token).  NM_FFN_TILE=<kind>:<shape>[:<split>]
  * in the environment ("tile" or "tile24", shapes 0 to 3) forces that kind's
- * tile products to a shape, and a call to tile products; stream:1 and stream:0
- * force and forbid streamed weights (up to 1024 tokens).  Outputs and workspace
+ * tile products to a shape (and to a split, or the next smaller one that their
+ * reduction divides into), and a call to tile products; stream:1 and stream:0
+ * force and forbid streamed weights (up to 1024 tokens); workspace sizes follow
+ * it, so it stays between asking for one and the call.  Outputs and workspace
  * overlap no other buffer of the call.  The workspace (256-byte aligned, at
  * least nm_glu_workspace_size bytes) is written and read back within the
  * call's stream order, so calls that share one must be ordered.
  * NM_EINVAL: null pointers (or only one of G and U), T < 1, ldx < K, ldh < R,
  * ldp < R, descriptors whose sizes or versions are wrong or whose shape, N:M
- * or dtype differ, a small workspace.  NM_EUNSUPPORTED: int8 weights, act not
- * listed, pointers not aligned to their element, a workspace not 256-byte
+ * or dtype differ, a small workspace.  NM_EUNSUPPORTED: int8 weights, act or
+ * p_dtype not listed, pointers not aligned to their element, a workspace not 256-byte
  * aligned, rows of K so long that 256 of them pass 2^31 bytes, T > 2^25, R >
  * 2^22.
  */
 nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
                  int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, void* workspace,
                  size_t workspace_bytes, void* stream);
+nm_status nm_glu_kept(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
+                      int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, int32_t p_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Device workspace nm_glu_backward needs. */
 nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed* up, int64_t T, size_t* bytes);
@@ -418,14 +424,17 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
  * may both weight gradients together (then they are not computed); not all
  * three.  dG and dU are rounded to the weight dtype before the two products,
  * as operands of the matrix instruction; sums are binary32 and every output
- * is rounded once.  With G and U, which are 16-bit too, the gradients' distance
- * from unrounded ones is at most 1.2 half steps of the type, as a norm (bf16
- * 0.0030 and fp16 0.00038 measured, 0.0017 and 0.00021 for the output rounding
- * alone).  fp16 holds dG and dU like any fp16 gradient: beyond 65504 they are
- * infinite, and the token's dX and that row of dWg or dWu are not finite;
- * below 2^-25 they are 0.  An infinite G or U (fp16: a product nm_glu rounded from
- * beyond 65504) counts as the type's largest value of its sign.  The result does not depend on launch order (no atomics).
- * All buffers have the weight dtype.  Errors as nm_glu; NM_EINVAL also for
+ * is rounded once.  As a norm, the gradients' distance from unrounded ones is
+ * at most 1.2 half steps of the type with G and U in the weight dtype and 0.82
+ * with them in binary32 (nm_glu_kept and nm_glu_backward_kept, p_dtype NM_F32):
+ * bf16 0.0030 and 0.0024, fp16 0.00038 and 0.00029 measured, where the output's
+ * rounding alone is 0.0017 and 0.00021.  fp16 holds dG and dU like any fp16
+ * gradient: beyond 65504 they are infinite, and the token's dX and that row of
+ * dWg or dWu are not finite; below 2^-25 they are 0.  An infinite G or U of the
+ * weight dtype (fp16: a product rounded from beyond 65504) counts as the type's
+ * largest value of its sign.  The result does not depend on launch order (no
+ * atomics).
+ * All other buffers have the weight dtype.  Errors as nm_glu; NM_EINVAL also for
  * no output at all, one weight gradient without the other, lddx < K, lddw < K;
  * NM_EUNSUPPORTED also for T of 2^22 or R of 2^21 and more.
  */
@@ -433,6 +442,10 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
                           const void* G, const void* U, int64_t ldp, const void* dH, int64_t lddh, int32_t act,
                           void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* workspace,
                           size_t workspace_bytes, void* stream);
+nm_status nm_glu_backward_kept(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
+                               const void* G, const void* U, int64_t ldp, int32_t p_dtype, const void* dH,
+                               int64_t lddh, int32_t act, void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Microscaled 4-bit floating point: blocks of 32 consecutive elements along

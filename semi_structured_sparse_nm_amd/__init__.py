@@ -119,8 +119,11 @@ def lib() -> ctypes.CDLL:
         L.nm_hybrid_spmm.argtypes = [HP, P, I64, I64, P, I64, I32, P, I32, P]
         L.nm_glu_workspace_size.argtypes = [PP, PP, P, I64, I64, ctypes.POINTER(SZ)]
         L.nm_glu.argtypes = [PP, PP, P, I64, I64, P, I64, I32, P, P, I64, P, SZ, P]
+        L.nm_glu_kept.argtypes = [PP, PP, P, I64, I64, P, I64, I32, P, P, I64, I32, P, SZ, P]
         L.nm_glu_backward_workspace_size.argtypes = [PP, PP, I64, ctypes.POINTER(SZ)]
         L.nm_glu_backward.argtypes = [PP, PP, P, I64, I64, P, P, I64, P, I64, I32, P, I64, P, P, I64, P, SZ, P]
+        L.nm_glu_backward_kept.argtypes = [PP, PP, P, I64, I64, P, P, I64, I32, P, I64, I32, P, I64, P, P, I64, P, SZ,
+                                           P]
         MP = ctypes.POINTER(NmMx)
         L.nm_mx_size.argtypes = [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
         L.nm_mx_quantize.argtypes = [P, I64, I32, MP, P]
@@ -129,8 +132,8 @@ def lib() -> ctypes.CDLL:
         L.nm_mx_linear.argtypes = [MP, MP, P, I64, I32, I64, P, I64, I32, P, I32, P, SZ, P]
         L.nm_mx_glu.argtypes = [MP, MP, MP, P, I64, I32, I64, P, I64, I32, I32, P, SZ, P]
         for f in ("nm_pack_size", "nm_pack", "nm_spmm_workspace_size", "nm_spmm", "nm_hybrid_pack_size",
-                  "nm_hybrid_pack", "nm_hybrid_spmm", "nm_glu_workspace_size", "nm_glu",
-                  "nm_glu_backward_workspace_size", "nm_glu_backward", "nm_mx_size", "nm_mx_quantize",
+                  "nm_hybrid_pack", "nm_hybrid_spmm", "nm_glu_workspace_size", "nm_glu", "nm_glu_kept",
+                  "nm_glu_backward_workspace_size", "nm_glu_backward", "nm_glu_backward_kept", "nm_mx_size", "nm_mx_quantize",
                   "nm_mx_dequantize", "nm_mx_workspace_size", "nm_mx_linear", "nm_mx_glu"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -610,10 +613,13 @@ def _glu_operands(gate: Packed, up: Packed, Xt: torch.Tensor):
     return T, ldx
 
 
-def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
+def _check_pre(pre: torch.Tensor, T: int, p: Packed):
+    """(elements between pre's rows, its type)"""
     if pre.shape != (2, T, p.rows):
         raise ValueError(f"pre must be [2, {T}, {p.rows}], got {tuple(pre.shape)}")
-    _check_dtype("pre", pre, p.torch_dtype)
+    dt = _TORCH_TO_NM.get(pre.dtype)
+    if dt != p.dtype and dt != NM_F32:
+        raise TypeError(f"pre has dtype {pre.dtype}, expected {p.torch_dtype} or {torch.float32}")
     half, ld, s2 = pre.stride()
     if s2 != 1 and p.rows > 1:
         raise ValueError("pre must have unit stride along its last dimension")
@@ -624,7 +630,7 @@ def _check_pre(pre: torch.Tensor, T: int, p: Packed) -> int:
     # one half behind the other, or their rows in turn
     if half < (T - 1) * ld + p.rows and not (T > 1 and p.rows <= half <= ld - p.rows):
         raise ValueError("the two halves of pre overlap")
-    return ld
+    return ld, dt
 
 
 def _glu_key(what: str, p: Packed, T: int, rows, dev: int) -> tuple:
@@ -646,7 +652,10 @@ def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torc
     shape, N:M and dtype (float16 / bfloat16): H[T, R] = act(G) * U with
     G = Xt @ (mask . Wg)^T, U = Xt @ (mask . Wu)^T, Xt [T, K] (K contiguous).
     act: "silu" or "gelu".  pre: a [2, T, R] tensor that receives G and U,
-    which glu_backward() takes."""
+    which glu_backward() takes, in float32 as they are summed or rounded to
+    the weights' dtype (half the memory; the gradients' distance from unrounded
+    ones grows from 1.4 to 1.8 times that of the output's rounding alone).  Not
+    part of autograd's graph."""
     T, ldx = _glu_operands(gate, up, Xt)
     a = _glu_act(act)
     R = gate.rows
@@ -655,9 +664,9 @@ def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torc
     else:
         _check_dtype("out", out, Xt.dtype)
     ldh = _row_pitch("out", out, T, R)
-    ldp, g, u = 0, None, None
+    ldp, pdt, g, u = 0, 0, None, None
     if pre is not None:
-        ldp = _check_pre(pre, T, gate)
+        ldp, pdt = _check_pre(pre, T, gate)
         g = pre.data_ptr()
         u = g + pre.stride(0) * pre.element_size()
     dev = _one_gpu("Xt, gate, gate meta, up, up meta, out, pre", Xt, gate.values, gate.meta, up.values, up.meta, out,
@@ -667,7 +676,7 @@ def glu(gate: Packed, up: Packed, Xt: torch.Tensor, act: str = "silu", out: torc
     need = _sized(L.nm_glu_workspace_size, "nm_glu_workspace_size", _glu_key("glu", gate, T, (x % 16, ldx), dev), dg,
                   du, x, ldx, T)
     ws, wp, wn = _workspace(workspace, need, dev)
-    _call(dev, L.nm_glu, "nm_glu", dg, du, x, ldx, T, out.data_ptr(), ldh, a, g, u, ldp, wp, wn)
+    _call(dev, L.nm_glu_kept, "nm_glu", dg, du, x, ldx, T, out.data_ptr(), ldh, a, g, u, ldp, pdt, wp, wn)
     return out
 
 
@@ -693,7 +702,7 @@ def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, 
     a = _glu_act(act)
     if not need_dx and not need_dw:
         raise ValueError("glu_backward needs need_dx or need_dw")
-    ldp = _check_pre(pre, T, gate)
+    ldp, pdt = _check_pre(pre, T, gate)
     R, K = gate.rows, gate.K
     lddh = _row_pitch("dH", dH, T, R)
     _check_dtype("dH", dH, Xt.dtype)
@@ -707,8 +716,8 @@ def glu_backward(gate: Packed, up: Packed, Xt: torch.Tensor, pre: torch.Tensor, 
     dWg = Xt.new_empty((R, K)) if need_dw else None
     dWu = Xt.new_empty((R, K)) if need_dw else None
     g = pre.data_ptr()
-    _call(dev, L.nm_glu_backward, "nm_glu_backward", dg, du, Xt.data_ptr(), ldx, T, g,
-          g + pre.stride(0) * pre.element_size(), ldp, dH.data_ptr(), lddh, a,
+    _call(dev, L.nm_glu_backward_kept, "nm_glu_backward", dg, du, Xt.data_ptr(), ldx, T, g,
+          g + pre.stride(0) * pre.element_size(), ldp, pdt, dH.data_ptr(), lddh, a,
           dX.data_ptr() if need_dx else None, K, dWg.data_ptr() if need_dw else None,
           dWu.data_ptr() if need_dw else None, K, wp, wn)
     return dX, dWg, dWu

@@ -59,6 +59,7 @@ struct TileArgs {
   int64_t ldc;
   void* P[2];                // TILE_GLU: the two products (nullptr: not kept), ldp elements between rows
   int64_t ldp;
+  bool p32;                  // in binary32, else the output's type
   const float* bias;         // [Nr] or nullptr
   int act;                   // NM_ACT_NONE / NM_ACT_GELU / NM_ACT_SILU
   int shape;                 // tile shape, from plan_tile or plan_back
@@ -109,8 +110,9 @@ struct GluArgs {
   int64_t ldx, T;
   void* H;
   int64_t ldh;
-  void* P[2];
+  void* P[2];                // the two products, as in TileArgs
   int64_t ldp;
+  bool p32;
   int act;
 };
 
@@ -133,7 +135,8 @@ struct DenseArgs {
 };
 hipError_t launch_expand_dense(const Geometry& g, const DenseArgs& a, hipStream_t s);
 
-// The backward pass's operands (16-bit): from P = (G, U) and dH, dG = dH u
+// The backward pass's operands (16-bit): from P = (G, U), in the weights' type
+// or binary32 (p32), and dH, dG = dH u
 // act'(g) and dU = dH act(g) as rows d [T][2 Rp] (gate at column 0, up at Rp,
 // zeros from R to Rp) and transposed dt [2][R][Tp]; both weights transposed,
 // wt [K][2 Rp]; their kept bits, mask[w] [R][Kp / 8]; X transposed, xt [K][Tp].
@@ -144,9 +147,10 @@ struct PrepareArgs {
   const uint8_t* meta[2];
   const uint16_t* X;
   int64_t ldx, T;
-  const uint16_t* G;
-  const uint16_t* U;
+  const void* G;
+  const void* U;
   int64_t ldp;
+  bool p32;
   const uint16_t* dH;
   int64_t lddh;
   int act;

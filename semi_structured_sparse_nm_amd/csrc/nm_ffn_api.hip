@@ -98,6 +98,7 @@ nm_status check_pair(const nm_packed* gate, const nm_packed* up, Geometry* g) {
 }
 
 bool glu_act_ok(int32_t act) { return act == NM_ACT_SILU || act == NM_ACT_GELU; }
+bool kept_type_ok(int32_t p_dtype, int32_t wdt) { return p_dtype == wdt || p_dtype == NM_F32; }
 
 // How a call multiplies.
 enum GluPath {
@@ -349,6 +350,13 @@ nm_status nm_glu_workspace_size(const nm_packed* gate, const nm_packed* up, cons
 nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
                  int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, void* workspace, size_t workspace_bytes,
                  void* stream) {
+  return nm_glu_kept(gate, up, Xt, ldx, T, Ht, ldh, act, G, U, ldp, gate ? gate->dtype : 0, workspace,
+                     workspace_bytes, stream);
+}
+
+nm_status nm_glu_kept(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T, void* Ht,
+                      int64_t ldh, int32_t act, void* G, void* U, int64_t ldp, int32_t p_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
   Geometry g;
   const nm_status st = check_pair(gate, up, &g);
   if (st != NM_OK) return st;
@@ -356,8 +364,9 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   if (gate->format_version != NM_FORMAT_VERSION || up->format_version != NM_FORMAT_VERSION) return NM_EINVAL;
   if (!Xt || !Ht || T < 1 || ldx < g.K || ldh < g.R) return NM_EINVAL;
   if ((G == nullptr) != (U == nullptr) || (G && ldp < g.R)) return NM_EINVAL;
-  if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
-  if (!aligned(Xt, 2) || !aligned(Ht, 2) || (G && (!aligned(G, 2) || !aligned(U, 2)))) return NM_EUNSUPPORTED;
+  if (!glu_act_ok(act) || (G && !kept_type_ok(p_dtype, gate->dtype))) return NM_EUNSUPPORTED;
+  const size_t pb = p_dtype == NM_F32 ? 4 : 2;
+  if (!aligned(Xt, 2) || !aligned(Ht, 2) || (G && (!aligned(G, pb) || !aligned(U, pb)))) return NM_EUNSUPPORTED;
   const GluPath path = glu_path(g, T);
   const bool direct = rows_direct(path, Xt, ldx, g.K);
   const size_t pad = direct ? 0 : padded_bytes(g, T);
@@ -391,6 +400,7 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
     a.P[0] = G;
     a.P[1] = U;
     a.ldp = ldp;
+    a.p32 = p_dtype == NM_F32;
     a.act = act;
     if (path == GLU_REPACK) {
       const Geometry d = geometry24(g);
@@ -432,6 +442,7 @@ nm_status nm_glu(const nm_packed* gate, const nm_packed* up, const void* Xt, int
   a.P[0] = G;
   a.P[1] = U;
   a.ldp = ldp;
+  a.p32 = p_dtype == NM_F32;
   a.act = act;
   const nm::TilePlan plan = nm::plan_tile(nm::TILE_GLU, false, T, g.R, a.nslab, nm::device_cu_count());
   return run_tile(tile_type(gate->dtype), nm::TILE_GLU, gate->dtype, a, plan, nullptr, s) == hipSuccess ? NM_OK
@@ -453,6 +464,14 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
                           const void* G, const void* U, int64_t ldp, const void* dH, int64_t lddh, int32_t act,
                           void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* workspace,
                           size_t workspace_bytes, void* stream) {
+  return nm_glu_backward_kept(gate, up, Xt, ldx, T, G, U, ldp, gate ? gate->dtype : 0, dH, lddh, act, dX, lddx, dWg,
+                              dWu, lddw, workspace, workspace_bytes, stream);
+}
+
+nm_status nm_glu_backward_kept(const nm_packed* gate, const nm_packed* up, const void* Xt, int64_t ldx, int64_t T,
+                               const void* G, const void* U, int64_t ldp, int32_t p_dtype, const void* dH,
+                               int64_t lddh, int32_t act, void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw,
+                               void* workspace, size_t workspace_bytes, void* stream) {
   Geometry g;
   const nm_status st = check_pair(gate, up, &g);
   if (st != NM_OK) return st;
@@ -461,8 +480,9 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   if (!Xt || !G || !U || !dH || T < 1 || ldx < g.K || ldp < g.R || lddh < g.R) return NM_EINVAL;
   if ((dWg == nullptr) != (dWu == nullptr) || (!dX && !dWg)) return NM_EINVAL;
   if ((dX && lddx < g.K) || (dWg && lddw < g.K)) return NM_EINVAL;
-  if (!glu_act_ok(act)) return NM_EUNSUPPORTED;
-  if (!aligned(Xt, 2) || !aligned(G, 2) || !aligned(U, 2) || !aligned(dH, 2) || !aligned(dX, 2) || !aligned(dWg, 2) ||
+  if (!glu_act_ok(act) || !kept_type_ok(p_dtype, gate->dtype)) return NM_EUNSUPPORTED;
+  const size_t pb = p_dtype == NM_F32 ? 4 : 2;
+  if (!aligned(Xt, 2) || !aligned(G, pb) || !aligned(U, pb) || !aligned(dH, 2) || !aligned(dX, 2) || !aligned(dWg, 2) ||
       !aligned(dWu, 2))
     return NM_EUNSUPPORTED;
   if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
@@ -488,9 +508,10 @@ nm_status nm_glu_backward(const nm_packed* gate, const nm_packed* up, const void
   q.X = static_cast<const uint16_t*>(Xt);
   q.ldx = ldx;
   q.T = T;
-  q.G = static_cast<const uint16_t*>(G);
-  q.U = static_cast<const uint16_t*>(U);
+  q.G = G;
+  q.U = U;
   q.ldp = ldp;
+  q.p32 = p_dtype == NM_F32;
   q.dH = static_cast<const uint16_t*>(dH);
   q.lddh = lddh;
   q.act = act;

@@ -99,6 +99,28 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, f
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = from_16<WT>(((uint32_t)x[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
 }
+// eight kept products from r: binary32, or 16-bit with infinities made finite
+template <int WT, bool P32>
+__device__ __forceinline__ void load_kept(const void* P, int64_t row, int64_t r, int64_t R, float (&f)[8]) {
+  if constexpr (P32) {
+    const float* p = static_cast<const float*>(P) + row + r;
+    if (r + 8 <= R) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const v4f x = *reinterpret_cast<const v4f_any*>(p + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[4 * i + e] = x[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = r + i < R ? p[i] : 0.f;
+    }
+  } else {
+    load8<WT>(static_cast<const uint16_t*>(P) + row, r, R, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = finite_16<WT>(f[i]);
+  }
+}
 
 // What the backward pass's products read, in one launch; workgroups take, by
 // index, one of three kinds of tile:
@@ -116,7 +138,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t r, int64_t R, f
 // Tiles pass through LDS; every element is read and written once, in 16-byte
 // pieces of at least 128 contiguous bytes: 595 MB in 120 us (5 TB/s, a large
 // copy's rate) for 2048 tokens and two 2:4 weights of 11008 x 4096.
-template <int WT, int TH>
+template <int WT, int TH, bool P32>
 __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   // pitch 66 halves: eight pieces of a row (8 rows apart here) and eight
   // tokens fall on different banks
@@ -132,17 +154,17 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
     if (t < a.T && r < a.g.R) {
       float h[8], g[8], u[8];
       load8<WT>(a.dH + t * a.lddh, r, a.g.R, h);
-      load8<WT>(a.G + t * a.ldp, r, a.g.R, g);
-      load8<WT>(a.U + t * a.ldp, r, a.g.R, u);
+      load_kept<WT, P32>(a.G, t * a.ldp, r, a.g.R, g);
+      load_kept<WT, P32>(a.U, t * a.ldp, r, a.g.R, u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float dg[2], du[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y, dy;
-          glu_act_slope(a.act, finite_16<WT>(g[2 * i + e]), y, dy);
+          glu_act_slope(a.act, g[2 * i + e], y, dy);
           const bool in = r + 2 * i + e < a.g.R;
-          dg[e] = in ? h[2 * i + e] * finite_16<WT>(u[2 * i + e]) * dy : 0.f;
+          dg[e] = in ? h[2 * i + e] * u[2 * i + e] * dy : 0.f;
           du[e] = in ? h[2 * i + e] * y : 0.f;
         }
         og[i] = pack_16x2<WT>(dg[0], dg[1]);
@@ -244,12 +266,12 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
   }
 }
 
-template <int WT, int TH>
+template <int WT, int TH, bool P32>
 __global__ void __launch_bounds__(TH) glu_prepare_kernel(PrepareArgs a, int64_t n_act, int64_t n_weight) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 64 * 66];
   static_assert(2 * 64 * 66 >= 64 * 130, "the weight tile fits");
   int64_t b = blockIdx.x;
-  if (b < n_act) return prepare_dact<WT, TH>(a, b, lds);
+  if (b < n_act) return prepare_dact<WT, TH, P32>(a, b, lds);
   b -= n_act;
   if (b < n_weight) return prepare_weight<TH>(a, b, lds);
   prepare_tokens<TH>(a, b - n_weight, lds);
@@ -285,10 +307,15 @@ hipError_t launch_glu_prepare(const PrepareArgs& a, int wdt, hipStream_t s) {
   auto launch = [&](auto kernel, int threads) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, s, a, n_act, n_weight);
   };
+  auto pick = [&](auto wt, auto p32) {
+    constexpr int WT = decltype(wt)::value;
+    constexpr bool P32 = decltype(p32)::value;
+    wide ? launch(glu_prepare_kernel<WT, 512, P32>, 512) : launch(glu_prepare_kernel<WT, 256, P32>, 256);
+  };
   if (wdt == NM_F16)
-    wide ? launch(glu_prepare_kernel<NM_F16, 512>, 512) : launch(glu_prepare_kernel<NM_F16, 256>, 256);
+    a.p32 ? pick(ic<NM_F16>(), ic<1>()) : pick(ic<NM_F16>(), ic<0>());
   else
-    wide ? launch(glu_prepare_kernel<NM_BF16, 512>, 512) : launch(glu_prepare_kernel<NM_BF16, 256>, 256);
+    a.p32 ? pick(ic<NM_BF16>(), ic<1>()) : pick(ic<NM_BF16>(), ic<0>());
   return hipGetLastError();
 }
 

@@ -259,7 +259,10 @@ __global__ void __launch_bounds__(kGluWaves * 64) glu_decode_kernel(GluArgs a, i
     if (r < a.g.R && t < a.T) {
       const float h = glu_act(a.act, g) * u;
       static_cast<uint16_t*>(a.H)[t * a.ldh + r] = (uint16_t)pack_16x2<WT>(h, 0.f);
-      if (a.P[0]) {
+      if (a.P[0] && a.p32) {
+        static_cast<float*>(a.P[0])[t * a.ldp + r] = g;
+        static_cast<float*>(a.P[1])[t * a.ldp + r] = u;
+      } else if (a.P[0]) {
         static_cast<uint16_t*>(a.P[0])[t * a.ldp + r] = (uint16_t)pack_16x2<WT>(g, 0.f);
         static_cast<uint16_t*>(a.P[1])[t * a.ldp + r] = (uint16_t)pack_16x2<WT>(u, 0.f);
       }

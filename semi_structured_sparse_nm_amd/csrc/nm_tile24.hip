@@ -66,6 +66,7 @@ hipError_t launch_glu_tile24(const GluArgs& g, hipStream_t s) {
   a.P[0] = g.P[0];
   a.P[1] = g.P[1];
   a.ldp = g.ldp;
+  a.p32 = g.p32;
   a.act = g.act;
   a.split = 1;
   a.sps = a.nslab;

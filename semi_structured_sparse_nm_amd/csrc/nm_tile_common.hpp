@@ -225,7 +225,10 @@ __device__ __forceinline__ void tile_epilogue(const TileArgs& a, const TileItem&
         __builtin_amdgcn_sched_barrier(0);              // one output's temporaries at a time
         if (m < a.Mr) {
           store_pair<OUT>(a.C, m * a.ldc, n0 + 16 * i, a.Nr, lq, h[0], h[1], whole);
-          if (a.P[0]) {
+          if (a.P[0] && a.p32) {
+            store_pair<NM_F32>(a.P[0], m * a.ldp, n0 + 16 * i, a.Nr, lq, g[0], g[1], false);
+            store_pair<NM_F32>(a.P[1], m * a.ldp, n0 + 16 * i, a.Nr, lq, u[0], u[1], false);
+          } else if (a.P[0]) {
             store_pair<OUT>(a.P[0], m * a.ldp, n0 + 16 * i, a.Nr, lq, g[0], g[1], kept);
             store_pair<OUT>(a.P[1], m * a.ldp, n0 + 16 * i, a.Nr, lq, u[0], u[1], kept);
           }

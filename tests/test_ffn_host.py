@@ -89,6 +89,34 @@ def test_glu_backward_refusals():
                 lddw=1 << 12, wsb=1 << 62) == EUNSUP
 
 
+def test_kept_products_type():
+    """G and U in the weights' type or binary32, aligned to their element."""
+    L = nm.lib()
+
+    def fwd(pdt, G=P[3], U=P[4], ldp=47):
+        g, u = _w(), _w()
+        return L.nm_glu_kept(ctypes.byref(g), ctypes.byref(u), P[0], 128, 5, P[1], 48, 2, G, U, ldp, pdt, P[2], 1 << 30,
+                             None)
+
+    def bwd(pdt, G=P[1], U=P[2], wsb=100):
+        g, u = _w(), _w()
+        return L.nm_glu_backward_kept(ctypes.byref(g), ctypes.byref(u), P[0], 128, 5, G, U, 48, pdt, P[3], 48, 2, P[4],
+                                      128, P[5], P[6], 128, P[7], wsb, None)
+
+    for pdt in (nm.NM_F16, nm.NM_F32):                    # (as far as the row pitch and the workspace, which are refused)
+        assert fwd(pdt) == EINVAL and bwd(pdt) == EINVAL
+    for pdt in (nm.NM_BF16, nm.NM_I8, nm.NM_I32, 9):
+        assert fwd(pdt, ldp=48) == EUNSUP and bwd(pdt) == EUNSUP
+    assert fwd(nm.NM_F32, G=P[3] + 2, ldp=48) == EUNSUP and fwd(nm.NM_F32, U=P[4] + 2, ldp=48) == EUNSUP
+    assert bwd(nm.NM_F32, G=P[1] + 2) == EUNSUP and bwd(nm.NM_F32, U=P[2] + 2) == EUNSUP
+    p = _packed()
+    X = torch.zeros(3, 64, dtype=torch.float16)
+    with pytest.raises(TypeError, match="pre has dtype torch.bfloat16, expected torch.float16 or torch.float32"):
+        nm.glu(p, p, X, pre=torch.zeros(2, 3, 16, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="not on a GPU"):
+        nm.glu(p, p, X, pre=torch.zeros(2, 3, 16))
+
+
 def test_mx_workspace():
     n = ctypes.c_size_t()
     f = nm.lib().nm_mx_workspace_size

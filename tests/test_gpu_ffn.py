@@ -514,6 +514,105 @@ def test_training_step_against_unrounded_gradients(T, R, K, N, M, dt, act):
         assert off <= lim, f"{what}: {off:.6f} of the norm, at most {lim:.6f}"
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,R,K,N,M", [(40, 512, 256, 2, 4), (197, 1000, 768, 4, 8), (512, 700, 520, 3, 4)])
+def test_training_step_with_products_in_float32(T, R, K, N, M, dt, act):
+    """The same with G and U kept in float32: two roundings are left (dG or dU,
+    and the output), at most h sqrt(2 / 3) together."""
+    pg, wg, kg = weights(R, K, N, M, dt, "g")
+    pu, wu, ku = weights(R, K, N, M, dt, "u")
+    X, dH = normal((T, K), 1.0, dt, "X", T), normal((T, R), 0.1, dt, "dH", T)
+    pre = torch.empty((2, T, R), device="cuda")
+    H = nm.glu(pg, pu, X, act=act, pre=pre)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, act)
+    check(H, h, eh, "H")
+    check(pre[0], g, eg, "G")
+    check(pre[1], u, eu, "U")
+    got = nm.glu_backward(pg, pu, X, pre, dH, act=act)
+    dh = dH.double()
+    dg, du = dh * u * _ffn.slope64(g, act), dh * _ffn.act64(g, act)
+    want = (dg @ wg.double() + du @ wu.double(), (dg.t() @ X.double()) * kg, (du.t() @ X.double()) * ku)
+    lim = _ffn.half_step(X.dtype) * (2 / 3) ** 0.5
+    for a, b, what in zip(got, want, ("dX", "dWg", "dWu")):
+        off = float((a.double() - b).norm() / b.norm())
+        assert off <= lim, f"{what}: {off:.6f} of the norm, at most {lim:.6f}"
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, act)
+    for a, b, e, what in zip(got, want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
+@pytest.mark.parametrize("N,M", [(2, 4), (4, 8), (1, 4)])
+@pytest.mark.parametrize("T,R,K", [(1, 1, 8), (1, 77, 136), (16, 130, 512), (33, 77, 136), (70, 1, 64), (130, 333, 584),
+                                   (300, 500, 712)])
+@pytest.mark.parametrize("stream", [0, 1])
+def test_glu_float32_products_everywhere(tile, stream, T, R, K, N, M):
+    """float32 G and U on every path: contiguous, their rows in turn, inside
+    wider buffers at odd elements; H's bits do not change."""
+    dt = "bf16" if T % 2 else "f16"
+    pg, wg, kg = weights(R, K, N, M, dt, "g")
+    pu, wu, ku = weights(R, K, N, M, dt, "u")
+    X, dH = normal((T, K), 1.0, dt, "X", T), normal((T, R), 0.1, dt, "dH", T)
+    tile("stream", stream)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "silu")
+    H = nm.glu(pg, pu, X)
+    first = None
+    for layout in range(3):
+        if layout == 0:
+            buf = pre = torch.full((2, T, R), 7.0, device="cuda")
+        elif layout == 1:
+            buf = torch.full((T, 2, R), 7.0, device="cuda")
+            pre = buf.transpose(0, 1)
+        else:
+            buf = torch.full((2, T, R + 6), 7.0, device="cuda")
+            pre = buf[:, :, 3:R + 3]
+        assert torch.equal(nm.glu(pg, pu, X, pre=pre), H)
+        check(pre[0], g, eg, "G")
+        check(pre[1], u, eu, "U")
+        if layout == 2:
+            assert bool((buf[:, :, :3] == 7.0).all()) and bool((buf[:, :, R + 3:] == 7.0).all())
+        got = nm.glu_backward(pg, pu, X, pre, dH)
+        want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+        for a, b, e, what in zip(got, want, bound, ("dX", "dWg", "dWu")):
+            check(a, b, e, what)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("shape", [0, 1, 2, 3])
+@pytest.mark.parametrize("N,M", [(2, 4), (4, 8)])
+def test_glu_float32_products_in_every_shape(tile, shape, N, M):
+    T, R, K, dt = 700, 1900, 136, "bf16"
+    pg, wg, _ = weights(R, K, N, M, dt, "g")
+    pu, wu, _ = weights(R, K, N, M, dt, "u")
+    X = normal((T, K), 1.0, dt, "X")
+    tile("tile24" if (N, M) == (2, 4) else "tile", shape)
+    h, g, u, eh, eg, eu = _ffn.glu64(X, wg, wu, "gelu")
+    pre = torch.full((2, T, R), 7.0, device="cuda")
+    check(nm.glu(pg, pu, X, act="gelu", pre=pre), h, eh, "H")
+    check(pre[0], g, eg, "G")
+    check(pre[1], u, eu, "U")
+
+
+def test_float32_products_past_the_type():
+    """Products that fp16 cannot hold: float32 ones give their own gradients."""
+    T, R, K = 70, 48, 64
+    Wg, Wu = normal((R, K), 0.05, "f16", "Wg"), normal((R, K), 0.05, "f16", "Wu")
+    Wg[:, 0] = 40000.0
+    kg, ku = _ffn.kept(Wg, 2, 4), _ffn.kept(Wu, 2, 4)
+    wg, wu = torch.where(kg, Wg, 0.0), torch.where(ku, Wu, 0.0)
+    pg, pu = nm.pack(Wg, 2, 4), nm.pack(Wu, 2, 4)
+    X = normal((T, K), 0.1, "f16", "X")
+    X[:, 0] = torch.linspace(-8, 8, T)
+    pre = torch.empty(2, T, R, device="cuda")
+    nm.glu(pg, pu, X, pre=pre)
+    assert bool(torch.isfinite(pre).all()) and float(pre[0].max()) > 3e5
+    dH = normal((T, R), 0.0005, "f16", "dH")
+    want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, "silu")
+    for a, b, e, what in zip(nm.glu_backward(pg, pu, X, pre, dH), want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
 @pytest.mark.parametrize("T", [5, 70, 300])
 def test_glu_backward_past_the_range_of_fp16(T):
     """dG or dU beyond 65504: the token's dX and the row of the weight gradient
