@@ -428,7 +428,9 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
  * at most 1.2 half steps of the type with G and U in the weight dtype and 0.82
  * with them in binary32 (nm_glu_kept and nm_glu_backward_kept, p_dtype NM_F32):
  * bf16 0.0030 and 0.0024, fp16 0.00038 and 0.00029 measured, where the output's
- * rounding alone is 0.0017 and 0.00021.  fp16 holds dG and dU like any fp16
+ * rounding alone is 0.0017 and 0.00021.  With them in binary32 and T R K up to
+ * 2^26, dG and dU enter as the sum of two numbers of the weight dtype, and the
+ * output's rounding alone is left.  fp16 holds dG and dU like any fp16
  * gradient: beyond 65504 they are infinite, and the token's dX and that row of
  * dWg or dWu are not finite; below 2^-25 they are 0.  An infinite G or U of the
  * weight dtype (fp16: a product rounded from beyond 65504) counts as the type's

@@ -175,20 +175,32 @@ bool backward_ok(const Geometry& g, int64_t T) {
          up64(T) / 64 * (up64(g.R) / 64 + g.nKB) + 2 * ((g.R + 127) / 128) * g.nKB < kMaxGrid;
 }
 
+// With kept products in binary32, up to this many multiply-adds a product: dG and
+// dU in two 16-bit parts.  One part's rounding makes the gradients' distance from
+// 64-bit ones 1.41 times the output rounding's, but where few of them meet up to
+// 1.7 times (over 1.5 in 41 of 390 products of random sizes, in 1 of those beyond
+// this limit); two parts leave the output's rounding alone.  They double
+// reductions that are short here: 64 tokens, 256 x 256 10.2 -> 12.6 us, 16, 1000 x
+// 768 15.4 -> 18.8, 128, 512 x 512 13.3 -> 18.1; beyond, 197, 2048 x 2048 34 -> 43.
+constexpr double kTwoPartWork = 1 << 26;
+
 struct BackwardPlan {
   int64_t Rp, Tp, Kp;
+  int parts;
   size_t d, dt, xt, wt, mask, part, total;   // bytes of each part (mask: of one weight)
   nm::TilePlan plan;
-  BackwardPlan(const Geometry& g, int64_t T, bool dx, bool dw) {
+  BackwardPlan(const Geometry& g, int64_t T, bool dx, bool dw, bool p32) {
     Rp = up64(g.R);
     Tp = up64(T);
     Kp = up64(g.K);
-    d = up256((size_t)(T * 2 * Rp * 2));
-    dt = up256((size_t)(2 * g.R * Tp * 2));
-    xt = up256((size_t)(g.K * Tp * 2));
-    wt = up256((size_t)(g.K * 2 * Rp * 2));
+    parts = p32 && (double)T * (double)g.R * (double)g.K <= kTwoPartWork && row_ok(Tp * 4) && row_ok(Rp * 8) ? 2 : 1;
+    d = up256((size_t)(T * 2 * Rp * parts * 2));
+    dt = up256((size_t)(2 * g.R * Tp * parts * 2));
+    xt = up256((size_t)(g.K * Tp * parts * 2));
+    wt = up256((size_t)(g.K * 2 * Rp * parts * 2));
     mask = up256((size_t)(g.R * Kp / 8));
-    plan = nm::plan_back(T, g.R, g.K, (int)(2 * Rp / 64), (int)(Tp / 64), dx, dw, nm::device_cu_count());
+    plan = nm::plan_back(T, g.R, g.K, (int)(parts * 2 * Rp / 64), (int)(parts * Tp / 64), dx, dw,
+                         nm::device_cu_count());
     part = dx ? part_bytes(plan, T, g.K) : 0;
     total = d + dt + xt + wt + 2 * mask + part;
   }
@@ -456,7 +468,8 @@ nm_status nm_glu_backward_workspace_size(const nm_packed* gate, const nm_packed*
   if (st != NM_OK) return st;
   if (T > kMaxLen) return NM_EUNSUPPORTED;
   if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
-  *bytes = std::max(BackwardPlan(g, T, true, true).total, BackwardPlan(g, T, true, false).total);
+  *bytes = 0;
+  for (int i = 0; i < 4; ++i) *bytes = std::max(*bytes, BackwardPlan(g, T, true, i & 1, i & 2).total);
   return NM_OK;
 }
 
@@ -486,7 +499,7 @@ nm_status nm_glu_backward_kept(const nm_packed* gate, const nm_packed* up, const
       !aligned(dWu, 2))
     return NM_EUNSUPPORTED;
   if (!backward_ok(g, T)) return NM_EUNSUPPORTED;
-  const BackwardPlan p(g, T, dX != nullptr, dWg != nullptr);
+  const BackwardPlan p(g, T, dX != nullptr, dWg != nullptr, p_dtype == NM_F32);
   if (!workspace || workspace_bytes < p.total) return NM_EINVAL;
   if (!aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -517,6 +530,7 @@ nm_status nm_glu_backward_kept(const nm_packed* gate, const nm_packed* up, const
   q.act = act;
   q.Rp = p.Rp;
   q.Tp = p.Tp;
+  q.parts = p.parts;
   q.d = dX ? reinterpret_cast<uint16_t*>(d) : nullptr;
   q.wt = dX ? reinterpret_cast<uint16_t*>(wt) : nullptr;
   q.dt = dWg ? reinterpret_cast<uint16_t*>(dt) : nullptr;
@@ -526,25 +540,25 @@ nm_status nm_glu_backward_kept(const nm_packed* gate, const nm_packed* up, const
   // dX[t][k] = sum over both weights' rows of d[t][r] W[r][k]
   a.A = d;
   a.B[0] = wt;
-  a.lda = a.ldb = 4 * p.Rp;
+  a.lda = a.ldb = 4 * p.Rp * p.parts;
   a.Mr = T;
   a.Nr = g.K;
-  a.ka = a.kb = (int)(2 * p.Rp / 8);
-  a.nslab = (int)(2 * p.Rp / 64);
+  a.ka = a.kb = (int)(2 * p.Rp * p.parts / 8);
+  a.nslab = (int)(2 * p.Rp * p.parts / 64);
   a.C = dX;
   a.ldc = lddx;
   // dW[r][k] = sum over t of d[t][r] X[t][k], both transposed
   a.w.B = xt;
-  a.w.ld = 2 * p.Tp;
+  a.w.ld = 2 * p.Tp * p.parts;
   a.w.Mr = g.R;
   a.w.Nr = g.K;
-  a.w.nslab = (int)(p.Tp / 64);
+  a.w.nslab = (int)(p.Tp * p.parts / 64);
   a.w.C[0] = dWg;
   a.w.C[1] = dWu;
   a.w.ldc = lddw;
   a.w.ldm = p.Kp / 8;
   for (int i = 0; i < 2; ++i) {
-    a.w.A[i] = dt + (size_t)i * g.R * p.Tp * 2;
+    a.w.A[i] = dt + (size_t)i * g.R * p.Tp * p.parts * 2;
     a.w.mask[i] = mask + i * p.mask;
   }
   return run_tile(tile_type(gate->dtype), nm::TILE_BACK, gate->dtype, a, p.plan, part, s) == hipSuccess ? NM_OK

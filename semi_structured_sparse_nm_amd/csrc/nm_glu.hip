@@ -122,6 +122,13 @@ __device__ __forceinline__ void load_kept(const void* P, int64_t row, int64_t r,
   }
 }
 
+// what rounding x0, x1 to the pair h left, rounded (0 where it gave an infinity)
+template <int WT>
+__device__ __forceinline__ uint32_t rest_16x2(float x0, float x1, uint32_t h) {
+  const float h0 = from_16<WT>(h & 0xFFFFu), h1 = from_16<WT>(h >> 16);
+  return pack_16x2<WT>(__builtin_isinf(h0) ? 0.f : x0 - h0, __builtin_isinf(h1) ? 0.f : x1 - h1);
+}
+
 // What the backward pass's products read, in one launch; workgroups take, by
 // index, one of three kinds of tile:
 //
@@ -138,7 +145,7 @@ __device__ __forceinline__ void load_kept(const void* P, int64_t row, int64_t r,
 // Tiles pass through LDS; every element is read and written once, in 16-byte
 // pieces of at least 128 contiguous bytes: 595 MB in 120 us (5 TB/s, a large
 // copy's rate) for 2048 tokens and two 2:4 weights of 11008 x 4096.
-template <int WT, int TH, bool P32>
+template <int WT, int TH, bool P32, int PARTS>
 __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   // pitch 66 halves: eight pieces of a row (8 rows apart here) and eight
   // tokens fall on different banks
@@ -150,7 +157,7 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
     const int q = it * TH + threadIdx.x;
     const int tl = q >> 3, rl = (q & 7) * 8;
     const int64_t t = t0 + tl, r = r0 + rl;
-    uint32_t og[4] = {0u, 0u, 0u, 0u}, ou[4] = {0u, 0u, 0u, 0u};
+    uint32_t og[PARTS][4] = {}, ou[PARTS][4] = {};
     if (t < a.T && r < a.g.R) {
       float h[8], g[8], u[8];
       load8<WT>(a.dH + t * a.lddh, r, a.g.R, h);
@@ -167,38 +174,45 @@ __device__ __forceinline__ void prepare_dact(const PrepareArgs& a, int64_t b, ui
           dg[e] = in ? h[2 * i + e] * u[2 * i + e] * dy : 0.f;
           du[e] = in ? h[2 * i + e] * y : 0.f;
         }
-        og[i] = pack_16x2<WT>(dg[0], dg[1]);
-        ou[i] = pack_16x2<WT>(du[0], du[1]);
+        og[0][i] = pack_16x2<WT>(dg[0], dg[1]);
+        ou[0][i] = pack_16x2<WT>(du[0], du[1]);
+        if constexpr (PARTS == 2) {
+          og[1][i] = rest_16x2<WT>(dg[0], dg[1], og[0][i]);
+          ou[1][i] = rest_16x2<WT>(du[0], du[1], ou[0][i]);
+        }
       }
     }
-    if (a.d && t < a.T) {
-      uint16_t* d = a.d + t * (2 * a.Rp) + r;
-      *reinterpret_cast<v4i*>(d) = v4i{(int)og[0], (int)og[1], (int)og[2], (int)og[3]};
-      *reinterpret_cast<v4i*>(d + a.Rp) = v4i{(int)ou[0], (int)ou[1], (int)ou[2], (int)ou[3]};
-    }
-    if (a.dt) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        tile[0][rl + e][tl] = (uint16_t)(og[e >> 1] >> (16 * (e & 1)));
-        tile[1][rl + e][tl] = (uint16_t)(ou[e >> 1] >> (16 * (e & 1)));
+    for (int p = 0; p < PARTS; ++p) {
+      if (a.d && t < a.T) {
+        uint16_t* d = a.d + t * (2 * PARTS * a.Rp) + 2 * p * a.Rp + r;
+        *reinterpret_cast<v4i*>(d) = v4i{(int)og[p][0], (int)og[p][1], (int)og[p][2], (int)og[p][3]};
+        *reinterpret_cast<v4i*>(d + a.Rp) = v4i{(int)ou[p][0], (int)ou[p][1], (int)ou[p][2], (int)ou[p][3]};
+      }
+      if (a.dt) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          tile[2 * p][rl + e][tl] = (uint16_t)(og[p][e >> 1] >> (16 * (e & 1)));
+          tile[2 * p + 1][rl + e][tl] = (uint16_t)(ou[p][e >> 1] >> (16 * (e & 1)));
+        }
       }
     }
   }
   if (!a.dt) return;
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 1024 / TH; ++it) {
+  for (int it = 0; it < PARTS * 1024 / TH; ++it) {
     const int q = it * TH + threadIdx.x;
-    const int w = q >> 9, rl = (q >> 3) & 63, tl = (q & 7) * 8;
+    const int w = (q >> 9) & 1, rl = (q >> 3) & 63, tl = (q & 7) * 8;
     if (r0 + rl < a.g.R) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[w][rl][tl]);
-      *reinterpret_cast<v4i*>(a.dt + ((int64_t)w * a.g.R + r0 + rl) * a.Tp + t0 + tl) =
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[q >> 9][rl][tl]);
+      *reinterpret_cast<v4i*>(a.dt + (((int64_t)w * a.g.R + r0 + rl) * PARTS + (q >> 10)) * a.Tp + t0 + tl) =
           v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
     }
   }
 }
 
-template <int TH>
+template <int TH, int PARTS>
 __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   // pitch 130 halves: the four 16-column runs of a packed row and its block's
   // sixteen rows fall on different banks
@@ -232,13 +246,15 @@ __device__ __forceinline__ void prepare_weight(const PrepareArgs& a, int64_t b, 
     const int kl = q >> 4, rl = (q & 15) * 8;
     if (kb * 64 + kl < g.K && r0 + rl < a.Rp) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][rl]);
-      *reinterpret_cast<v4i*>(a.wt + (kb * 64 + kl) * (2 * a.Rp) + w * a.Rp + r0 + rl) =
-          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h)
+        *reinterpret_cast<v4i*>(a.wt + ((kb * 64 + kl) * PARTS + h) * (2 * a.Rp) + w * a.Rp + r0 + rl) =
+            v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
     }
   }
 }
 
-template <int TH>
+template <int TH, int PARTS>
 __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, uint16_t* lds) {
   uint16_t(*tile)[66] = reinterpret_cast<uint16_t(*)[66]>(lds);
   const int64_t tt = a.Tp / 64, K = a.g.K;
@@ -260,21 +276,23 @@ __device__ __forceinline__ void prepare_tokens(const PrepareArgs& a, int64_t b, 
     const int kl = q >> 3, tl = (q & 7) * 8;
     if (k0 + kl < K) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][tl]);
-      *reinterpret_cast<v4i*>(a.xt + (k0 + kl) * a.Tp + t0 + tl) =
-          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h)
+        *reinterpret_cast<v4i*>(a.xt + ((k0 + kl) * PARTS + h) * a.Tp + t0 + tl) =
+            v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
     }
   }
 }
 
-template <int WT, int TH, bool P32>
+template <int WT, int TH, bool P32, int PARTS>
 __global__ void __launch_bounds__(TH) glu_prepare_kernel(PrepareArgs a, int64_t n_act, int64_t n_weight) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 64 * 66];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * PARTS * 64 * 66];
   static_assert(2 * 64 * 66 >= 64 * 130, "the weight tile fits");
   int64_t b = blockIdx.x;
-  if (b < n_act) return prepare_dact<WT, TH, P32>(a, b, lds);
+  if (b < n_act) return prepare_dact<WT, TH, P32, PARTS>(a, b, lds);
   b -= n_act;
-  if (b < n_weight) return prepare_weight<TH>(a, b, lds);
-  prepare_tokens<TH>(a, b - n_weight, lds);
+  if (b < n_weight) return prepare_weight<TH, PARTS>(a, b, lds);
+  prepare_tokens<TH, PARTS>(a, b - n_weight, lds);
 }
 
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* X, int64_t ldx, int64_t T, int64_t K,
@@ -307,15 +325,18 @@ hipError_t launch_glu_prepare(const PrepareArgs& a, int wdt, hipStream_t s) {
   auto launch = [&](auto kernel, int threads) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, s, a, n_act, n_weight);
   };
-  auto pick = [&](auto wt, auto p32) {
-    constexpr int WT = decltype(wt)::value;
+  auto pick = [&](auto wt, auto p32, auto parts) {
+    constexpr int WT = decltype(wt)::value, PARTS = decltype(parts)::value;
     constexpr bool P32 = decltype(p32)::value;
-    wide ? launch(glu_prepare_kernel<WT, 512, P32>, 512) : launch(glu_prepare_kernel<WT, 256, P32>, 256);
+    wide ? launch(glu_prepare_kernel<WT, 512, P32, PARTS>, 512) : launch(glu_prepare_kernel<WT, 256, P32, PARTS>, 256);
   };
-  if (wdt == NM_F16)
-    a.p32 ? pick(ic<NM_F16>(), ic<1>()) : pick(ic<NM_F16>(), ic<0>());
-  else
-    a.p32 ? pick(ic<NM_BF16>(), ic<1>()) : pick(ic<NM_BF16>(), ic<0>());
+  auto pick_type = [&](auto wt) {
+    if (a.parts == 2)
+      a.p32 ? pick(wt, ic<1>(), ic<2>()) : pick(wt, ic<0>(), ic<2>());
+    else
+      a.p32 ? pick(wt, ic<1>(), ic<1>()) : pick(wt, ic<0>(), ic<1>());
+  };
+  wdt == NM_F16 ? pick_type(ic<NM_F16>()) : pick_type(ic<NM_BF16>());
   return hipGetLastError();
 }
 

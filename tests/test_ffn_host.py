@@ -141,7 +141,10 @@ def test_forced_splits(monkeypatch, shape, asked, slabs, split):
     w, x = _mx(R, 256 * slabs), _mx(T, 256 * slabs)
     assert nm.lib().nm_mx_workspace_size(ctypes.byref(w), ctypes.byref(x), T, 0, ctypes.byref(n)) == nm.NM_OK
     assert n.value == (-(-split * T * R * 4 // 256) * 256 if split > 1 else 0)
-    # the input's gradient: a reduction over both weights' rows, 64 a slab
+    # the input's gradient: a reduction over both weights' rows, 64 a slab, in two
+    # parts at this size (the most a call can need)
+    sps = -(-2 * slabs // min(asked, 2 * slabs, 16))
+    split = -(-2 * slabs // sps)
     if slabs % 2 == 0:
         g = _w(R=32 * slabs - 5, K=128)
         f = nm.lib().nm_glu_backward_workspace_size

@@ -542,6 +542,41 @@ def test_training_step_with_products_in_float32(T, R, K, N, M, dt, act):
         check(a, b, e, what)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,R,K,N,M", [(1, 200, 136, 2, 4), (6, 92, 592, 2, 4), (24, 149, 72, 4, 8), (65, 130, 264, 3, 4),
+                                       (128, 512, 512, 2, 4), (1000, 64, 1048, 1, 8), (1100, 64, 1048, 1, 8)])
+def test_small_steps_leave_the_output_rounding_alone(T, R, K, N, M, dt, act):
+    """Up to 2^26 multiply-adds and float32 products: dG and dU come in two
+    parts, off by h^2 of the value (fp16: h 2^-14 absolutely, where the second
+    is below its normal numbers), so what is left is one rounding of exact
+    gradients: elementwise half a step and the sums' error."""
+    pg, wg, kg = weights(R, K, N, M, dt, "g")
+    pu, wu, ku = weights(R, K, N, M, dt, "u")
+    X, dH = normal((T, K), 1.0, dt, "X", T), normal((T, R), 0.1, dt, "dH", T)
+    pre = torch.empty((2, T, R), device="cuda")
+    nm.glu(pg, pu, X, act=act, pre=pre)
+    got = nm.glu_backward(pg, pu, X, pre, dH, act=act)
+    g, u, dh, x = pre[0].double(), pre[1].double(), dH.double(), X.double()
+    dg, du = dh * u * _ffn.slope64(g, act), dh * _ffn.act64(g, act)
+    want = (dg @ wg.double() + du @ wu.double(), (dg.t() @ x) * kg, (du.t() @ x) * ku)
+    if T * R * K > 2 ** 26:                               # one part: the bound of any other call
+        want, bound = _ffn.glu_grad64(X, wg, wu, kg, ku, pre, dH, act)
+    else:
+        h = _ffn.half_step(X.dtype)
+        eg = (dh * u).abs() * 2.0 ** -19 * (1 + g.abs()) + h * h * dg.abs() + _ffn.tiny(X.dtype)
+        eu = dh.abs() * _ffn.act_err(g, act) + h * h * du.abs() + _ffn.tiny(X.dtype)
+        ex = eg @ wg.double().abs() + eu @ wu.double().abs() + _ffn.sum_err(
+            4 * R, (dg.abs() + eg) @ wg.double().abs() + (du.abs() + eu) @ wu.double().abs())
+        bound = (ex, *((e.t() @ x.abs()) + _ffn.sum_err(2 * T, (d.abs() + e).t() @ x.abs()) for d, e in ((dg, eg), (du, eu))))
+        # as a norm: the output's rounding, evenly spread over half a step, and the slope's own 2^-19
+        for a, b, what in zip(got, want, ("dX", "dWg", "dWu")):
+            off = float((a.double() - b).norm() / b.norm())
+            assert off <= h / 3 ** 0.5 + 2.0 ** -17, f"{what}: {off:.6f} of the norm"
+    for a, b, e, what in zip(got, want, bound, ("dX", "dWg", "dWu")):
+        check(a, b, e, what)
+
+
 @pytest.mark.parametrize("N,M", [(2, 4), (4, 8), (1, 4)])
 @pytest.mark.parametrize("T,R,K", [(1, 1, 8), (1, 77, 136), (16, 130, 512), (33, 77, 136), (70, 1, 64), (130, 333, 584),
                                    (300, 500, 712)])
