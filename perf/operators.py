@@ -211,7 +211,8 @@ def _own(state):
     if op == "glu":
         return nm.glu(W[0], W[1], X, act=act)
     if op == "glu_train":
-        pre = torch.empty(2, X.shape[0], W[0].rows, dtype=X.dtype, device=X.device)
+        # the kept products in 32 bits, as the plain form has them
+        pre = torch.empty(2, X.shape[0], W[0].rows, dtype=torch.float32, device=X.device)
         h = nm.glu(W[0], W[1], X, act=act, pre=pre)
         return (h, *nm.glu_backward(W[0], W[1], X, pre, state["dH"], act=act))
     if op == "mx_quantize":
