@@ -13,8 +13,9 @@
 // change to the matrix instruction's order in the wave's own LDS.  (Loaded in
 // that order, 16 bytes of each of 16 tokens for every quarter of a load, they
 // pass the vector cache at a quarter of its rate, which bound the call: two
-// 4:8 weights of 11008 x 4096, 16 tokens 22 us against 19 now, 32 tokens 33
-// and 23, 64 tokens 60 and 33.)  At 64 tokens one block in flight leaves the
+// 4:8 weights of 11008 x 4096, the same in every call, 16 tokens 22 us against
+// 19 now, 32 tokens 33 and 23, 64 tokens 60 and 33; with weights that change
+// between calls 16 tokens take 24.)  At 64 tokens one block in flight leaves the
 // registers for two workgroups on a compute unit (two: 37 us, one workgroup).
 //
 // Expansion of 1 to 4 kept of 8: the kept values of a group are at most two

@@ -9,7 +9,7 @@
 // in the quantiser, and codes and scales pass through the wave's own LDS to the
 // lanes of the scaled matrix instruction.  (Each lane reading the block it
 // needs itself touches 64 pieces of 64 bytes a load: 20 us instead of 14 for
-// 11008 x 4096, 16 tokens.)
+// 11008 x 4096, 16 tokens, on the same weights in every call; 15 on others.)
 // More tokens come quantised, whole lines of eight tokens a load, and change
 // to the instruction's order in the wave's LDS likewise (gated block of 11008 x
 // 4096, 64 tokens: 24.4 us in that order from the caches, 17.6 so).  The waves'

@@ -27,10 +27,14 @@
 // output meet in one lane and the activation and product need no exchange.
 // TILE_BACK: the input's and both weights' gradients are items of one launch.
 //
-// Bound by the matrix cores at the clock their power allows (a full last round
-// of the gradients' items changed nothing at 2048 tokens): bf16, 2048 tokens,
-// two 11008 x 4096 weights, gated 290 us (1.27 PFLOP/s), both gradients 675
-// (1.09); 4 bits, 1900 tokens, gated 90 (3.8).
+// bf16, 2048 tokens, two 11008 x 4096 weights: gated 285 us (1.3 PFLOP/s), both
+// gradients 675 (1.09); 4 bits, 1900 tokens, gated 96 (3.6).  By counters the
+// matrix cores are busy 59%, 46% and 39% of that (2048 of some 3500 to 5300 cycles
+// a slab of the 256 x 256 shape), and LDS is read for 1536 cycles a slab, without
+// bank conflicts.  Power is a part of it only: on operands of zeros, the same
+// instructions, the gated products take 12% and 18% less (fp16 with its copies
+// 327 -> 289, 4 bits 95 -> 78), the gradients 1%.  (A full last round of the
+// gradients' items changed nothing at 2048 tokens.)
 #pragma once
 
 #include "nm_tile_common.hpp"
@@ -242,8 +246,8 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
   };
   auto mul_row = [&](auto ic_, auto kc, const Frag& f, const Scales& c) {
     constexpr int i = decltype(ic_)::value, kk = decltype(kc)::value;
-    // back and forth: one operand stays at the turn too (the matrix cores are
-    // bound by power here, and what changes at their inputs costs it: 2-4%)
+    // back and forth: one operand stays at the turn too (what changes at the
+    // matrix cores' inputs costs power: 2-4% of the forward products)
 #pragma unroll
     for (int q = 0; q < TM; ++q) {
       const int j = i & 1 ? TM - 1 - q : q;

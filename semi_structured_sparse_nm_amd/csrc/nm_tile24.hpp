@@ -8,9 +8,11 @@
 // reads between the products.  A slab is 64 columns: BM token rows of 128
 // bytes, and for 128 outputs the 16-row blocks of both weights, 1 KB of values
 // and 128 bytes of positions each.  Half the products of the dense form, and
-// 50 KB instead of 64 KB a slab at BM = 256.  Bound by the matrix cores' power:
-// 2048 tokens, 11008 x 4096, 203 us (1.8 PFLOP/s of the dense product, which
-// takes 290 by dense tiles); 256 tokens 36 us.
+// 50 KB instead of 64 KB a slab at BM = 256.  2048 tokens, 11008 x 4096: 198 to 212
+// us (1.8 PFLOP/s of the dense product, which takes 285 by dense tiles); 256
+// tokens 36 us.  By counters the matrix cores are busy 75 us of it (1024 cycles a
+// slab, and LDS is read for as many); a quarter is power (151 us on operands of
+// zeros, the same instructions), and the last of three rounds is 69% full.
 //
 // A stage holds the tokens (16-byte piece c of row r at position c ^ (r % 8)),
 // the sixteen value blocks (piece c of row r at c ^ (r / 2 % 4)) and their

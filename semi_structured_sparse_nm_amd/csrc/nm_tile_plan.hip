@@ -41,10 +41,10 @@ bool ffn_tile_override(const char* kind, int* shape, int* split) {
 }
 
 // Microseconds a slab takes with few workgroups running and with one on every
-// compute unit (their operands' traffic, and the power the matrix cores draw,
-// slow each other down), and a tile besides its slabs.  Fitted to products of
-// 64 to 2048 tokens by 411 to 11008 x 182 to 11008; the choice is within 7% of
-// the fastest shape and split there.  For example 2048 tokens, two 4:8 weights
+// compute unit (their operands' traffic, and for the forward products the power
+// the matrix cores draw, slow each other down), and a tile besides its slabs.
+// Fitted to products of 64 to 2048 tokens by 411 to 11008 x 182 to 11008; the
+// choice is within 7% of the fastest shape and split there.  For example 2048 tokens, two 4:8 weights
 // of 11008 x 4096, gated: 256 x 256 tiles 290 us, 128 x 256 306; 600 tokens, 1614
 // x 2364: 68, 44, 128 x 128 32 and 64 x 128 41; at 4 bits 26, 17, 12 and 18.
 namespace {
