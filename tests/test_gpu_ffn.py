@@ -1018,3 +1018,37 @@ def test_results_do_not_vary():
             first = out
         for a, b in zip(first, out):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,R,K", [(20, 200, 264), (200, 1000, 520)])
+def test_float32_products_in_a_graph(T, R, K):
+    """A step with float32 products (in two parts and in one) on a stream of its
+    own, then captured and replayed with eager work between."""
+    dt = "bf16"
+    pg, pu = weights(R, K, 2, 4, dt, "g")[0], weights(R, K, 2, 4, dt, "u")[0]
+    X, dH = normal((T, K), 1.0, dt, "X"), normal((T, R), 0.1, dt, "dH")
+    pre = torch.empty(2, T, R, device="cuda")
+    ws = torch.empty(nm.glu_backward_workspace_size(pg, pu, T), dtype=torch.uint8, device="cuda")
+
+    def step():
+        h = nm.glu(pg, pu, X, pre=pre)
+        return (h, *nm.glu_backward(pg, pu, X, pre, dH, workspace=ws))
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = step()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in range(4):
+        X.copy_(normal((T, K), 1.0, dt, "X", i))
+        dH.copy_(normal((T, R), 0.1, dt, "dH", i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), f"replay {i}"
