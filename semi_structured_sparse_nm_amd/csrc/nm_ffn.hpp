@@ -135,13 +135,12 @@ struct DenseArgs {
 };
 hipError_t launch_expand_dense(const Geometry& g, const DenseArgs& a, hipStream_t s);
 
-// The backward pass's operands (16-bit): from P = (G, U), in the weights' type
-// or binary32 (p32), and dH, dG = dH u
-// act'(g) and dU = dH act(g) as rows d [T][2 Rp] (gate at column 0, up at Rp,
-// zeros from R to Rp) and transposed dt [2][R][Tp]; both weights transposed,
-// wt [K][2 Rp]; their kept bits, mask[w] [R][Kp / 8]; X transposed, xt [K][Tp].
-// Rp, Tp, Kp: R, T, K rounded up to 64, zero filled.  Null outputs are left out.
-// parts = 2: what the rounding of dG and dU left, rounded too, follows them along
+// The backward pass's operands (16-bit): from G and U, in the weights' type or
+// binary32 (p32), and dH, dG = dH u act'(g) and dU = dH act(g) as rows d [T][2 Rp]
+// (gate at column 0, up at Rp, zeros from R to Rp) and transposed dt [2][R][Tp];
+// both weights transposed, wt [K][2 Rp]; their kept bits, mask[w] [R][Kp / 8]; X
+// transposed, xt [K][Tp].  Rp, Tp, Kp: R, T, K rounded up to 64, zero filled.  Null
+// outputs are left out.  parts = 2 (with p32): what the rounding of dG and dU left, rounded too, follows them along
 // the reductions, d [T][4 Rp] and dt [2][R][2 Tp], and the other operands come
 // twice, wt [K][4 Rp] and xt [K][2 Tp]: the same products add both.
 struct PrepareArgs {
@@ -213,6 +212,7 @@ __device__ __forceinline__ float silu_f32(float x) {
   sigmoid_parts(x, p, r);
   return (x * p) * (p * r);
 }
+
 // act(x) and act'(x) of the gated block (NM_ACT_GELU or NM_ACT_SILU)
 __device__ __forceinline__ float glu_act(int act, float x) { return act == NM_ACT_SILU ? silu_f32(x) : gelu_f32(x); }
 __device__ __forceinline__ void glu_act_slope(int act, float x, float& y, float& dy) {

@@ -332,10 +332,8 @@ hipError_t launch_glu_prepare(const PrepareArgs& a, int wdt, hipStream_t s) {
     wide ? launch(glu_prepare_kernel<WT, 512, P32, PARTS>, 512) : launch(glu_prepare_kernel<WT, 256, P32, PARTS>, 256);
   };
   auto pick_type = [&](auto wt) {
-    if (a.parts == 2)
-      a.p32 ? pick(wt, ic<1>(), ic<2>()) : pick(wt, ic<0>(), ic<2>());
-    else
-      a.p32 ? pick(wt, ic<1>(), ic<1>()) : pick(wt, ic<0>(), ic<1>());
+    if (!a.p32) return pick(wt, ic<0>(), ic<1>());
+    a.parts == 2 ? pick(wt, ic<1>(), ic<2>()) : pick(wt, ic<1>(), ic<1>());
   };
   wdt == NM_F16 ? pick_type(ic<NM_F16>()) : pick_type(ic<NM_BF16>());
   return hipGetLastError();
