@@ -140,9 +140,10 @@ hipError_t launch_expand_dense(const Geometry& g, const DenseArgs& a, hipStream_
 // (gate at column 0, up at Rp, zeros from R to Rp) and transposed dt [2][R][Tp];
 // both weights transposed, wt [K][2 Rp]; their kept bits, mask[w] [R][Kp / 8]; X
 // transposed, xt [K][Tp].  Rp, Tp, Kp: R, T, K rounded up to 64, zero filled.  Null
-// outputs are left out.  parts = 2 (with p32): what the rounding of dG and dU left, rounded too, follows them along
-// the reductions, d [T][4 Rp] and dt [2][R][2 Tp], and the other operands come
-// twice, wt [K][4 Rp] and xt [K][2 Tp]: the same products add both.
+// outputs are left out.  parts = 2 (with p32): what the rounding of dG and dU
+// left, rounded too, follows them along the reductions, d [T][4 Rp] and dt
+// [2][R][2 Tp], and the other operands come twice, wt [K][4 Rp] and xt [K][2 Tp]:
+// the same products add both.
 struct PrepareArgs {
   Geometry g;
   const uint8_t* values[2];
