@@ -518,6 +518,149 @@ nm_status nm_mx_glu(const nm_mx* gate, const nm_mx* up, const nm_mx* xq, const v
                     int32_t x_dtype, int64_t T, void* Ht, int64_t ldh, int32_t h_dtype, int32_t act,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit rows: each row (a token's activations, or an output channel's weights)
+ * as whole numbers with one binary32 scale.
+ *   scale   = amax / 127 rounded to binary32, at least 2^-126 (a row of zeros
+ *             has that too), amax the row's largest magnitude;
+ *   element = the exact quotient x / scale rounded half to even, in [-127, 127].
+ * A row that holds a NaN or an infinity gets a NaN scale and elements of 0: all
+ * of it reads back as NaN.  Layout: row r's elements at r * Kp bytes, Kp = K
+ * rounded up to 128, zero past K.  Quantised weights are pruned and packed by
+ * nm_pack (ldw = Kp, NM_I8), their scales are the products' w_scale.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int64_t rows, K;
+  uint32_t format_version;  /* NM_FORMAT_VERSION, written by nm_i8_quantize */
+  uint32_t reserved;        /* 0 */
+  void* codes;  size_t codes_bytes;    /* device, sizes from nm_i8_size */
+  void* scales; size_t scales_bytes;   /* float[rows] */
+} nm_i8;
+
+/* Sizes of the two buffers.  NM_EINVAL: null outputs, rows < 1, K < 1;
+ * NM_EUNSUPPORTED: K above 131071 (sums of products fit 32 bits up to there),
+ * rows above 2^40 / K. */
+nm_status nm_i8_size(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes);
+
+/*
+ * X [q->rows][ldx] of x_dtype (NM_F16, NM_BF16 or NM_F32) -> q's buffers.
+ * Every byte of both buffers is written.  NM_EINVAL: null pointers, ldx < K,
+ * buffer sizes not those of nm_i8_size; NM_EUNSUPPORTED: other types, X not
+ * aligned to its element, codes not 16-byte or scales not 4-byte aligned.
+ */
+nm_status nm_i8_quantize(const void* X, int64_t ldx, int32_t x_dtype, nm_i8* q, void* stream);
+
+/* The values q stands for, element x scale rounded to binary32 and then to
+ * y_dtype (NM_F16, NM_BF16, NM_F32), Y [rows][ldy].  Errors as nm_i8_quantize. */
+nm_status nm_i8_dequantize(const nm_i8* q, void* Y, int64_t ldy, int32_t y_dtype, void* stream);
+
+/*
+ * Y[t][r] = act(sum_k q[t][k] w[r][k] x scale[t] x w_scale[r] + bias[r]): an int8
+ * N:M packed weight with a binary32 scale for each output channel, activations
+ * with one for each token: either Xt [T][ldx] of x_dtype (NM_F16, NM_BF16,
+ * NM_F32), which the call quantises as nm_i8_quantize does, or xq with rows = T
+ * (then Xt, ldx and x_dtype are ignored).  The sum is an exact 32-bit integer,
+ * converted to binary32 and multiplied by the token's scale, then the
+ * channel's; Y [T][ldy] of y_dtype (NM_F16, NM_BF16, NM_F32) is rounded once.
+ * bias NULL or float[R]; act NM_ACT_NONE or NM_ACT_GELU.  Workspace:
+ * nm_i8_linear_workspace_size bytes (256-byte aligned; xq as the call gets it):
+ * quantised activations, and copies of weights that are neither 2:4 nor dense.
+ * Outputs and workspace overlap no other buffer of the call; calls that share
+ * a workspace must be ordered.
+ * NM_EINVAL: null pointers, T < 1, ldx < K, ldy < R, xq of another K or number
+ * of rows, descriptors with wrong sizes or versions, a small workspace;
+ * NM_EUNSUPPORTED: a weight that is not int8, other types, act not listed,
+ * misaligned pointers, K above 131071, T > 2^25, R > 2^22.
+ */
+nm_status nm_i8_linear_workspace_size(const nm_packed* w, const nm_i8* xq, int64_t T, size_t* bytes);
+nm_status nm_i8_linear(const nm_packed* w, const float* w_scale, const nm_i8* xq, const void* Xt, int64_t ldx,
+                       int32_t x_dtype, int64_t T, void* Yt, int64_t ldy, int32_t y_dtype, const float* bias,
+                       int32_t act, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products of rows grouped by expert: E packed weights of one shape, N:M and
+ * dtype, and rows sorted by expert, expert e's being rows offsets[e] ..
+ * offsets[e + 1] - 1 (E + 1 whole numbers in device memory, offsets_dtype
+ * NM_OFFSETS_I32 or NM_OFFSETS_I64).  The host never reads them, so a call can
+ * be captured into a graph and replayed with others.  Each offset is taken into
+ * [0, T] and as at least the one before it, so no offsets make a call read or
+ * write outside its buffers.  Any expert may have no rows.  Rows in front of the
+ * first expert's and behind the last one's belong to none: their outputs are
+ * left as they are, or set to zero where zero_rest is not 0.
+ * ---------------------------------------------------------------------- */
+typedef enum { NM_OFFSETS_I32 = 0, NM_OFFSETS_I64 = 1 } nm_offsets_dtype;
+
+typedef struct {
+  int64_t experts;          /* E, 1 to 1023 */
+  int64_t rows;             /* R of one expert */
+  int64_t K;
+  int32_t N, M;
+  int32_t dtype;            /* NM_I8, NM_F16 or NM_BF16 */
+  uint32_t format_version;  /* written by nm_experts_pack */
+  void* values;             /* expert e's packed values at e * (values_bytes / E), as nm_pack writes them */
+  size_t values_bytes;
+  void* meta;               /* and its positions; may be NULL when N == M */
+  size_t meta_bytes;
+} nm_experts;
+
+/* E times nm_pack_size's sizes; its errors, NM_EINVAL also for experts < 1,
+ * NM_EUNSUPPORTED for more than 1023. */
+nm_status nm_experts_size(int64_t experts, int64_t rows, int64_t K, int32_t N, int32_t M, int32_t dtype,
+                          size_t* values_bytes, size_t* meta_bytes);
+
+/* Prune and pack W [E][R][K] (expert e at W + e * lde elements, its rows ldw
+ * apart), one nm_pack an expert.  Errors as nm_pack, NM_EINVAL also for lde < 0. */
+nm_status nm_experts_pack(const void* W, int64_t lde, int64_t ldw, nm_experts* w, void* stream);
+
+/*
+ * Yt[s] = Xt[s] W_e^T for the rows s of every expert e: 16-bit weights, Xt [T]
+ * [ldx] and Yt [T][ldy] of their dtype, binary32 sums rounded once.  Workspace:
+ * nm_expert_linear_workspace_size bytes (256-byte aligned) for the rows Xt and
+ * ldx of the call (read are only the pointer's alignment and the stride), or,
+ * Xt NULL, for any rows: a padded copy of X and re-packed or dense copies of
+ * the weights, where the call takes them.  Activations are finite: whether an
+ * infinite or NaN one reaches an output through a pruned weight depends on the
+ * path the call takes (it never reaches another row).  Overlaps and sharing of
+ * workspaces as for nm_i8_linear.
+ * NM_EINVAL: null pointers, T < 1, ldx < K, ldy < R, descriptors with wrong
+ * sizes or versions, a small workspace; NM_EUNSUPPORTED: int8 weights,
+ * offsets_dtype not listed, misaligned pointers, rows of K so long that 256 of
+ * them pass 2^31 bytes, T > 2^25, R > 2^22, outputs past 2^31 tiles.
+ */
+nm_status nm_expert_linear_workspace_size(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T, size_t* bytes);
+nm_status nm_expert_linear(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T, const void* offsets,
+                           int32_t offsets_dtype, void* Yt, int64_t ldy, int32_t zero_rest, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients for a fixed mask, from dY = dL/dY [T][lddy]:
+ *     dX[s] = dY[s] W_e                               [T][lddx]
+ *     dW_e  = keep_e (.) sum over e's rows of dY[s]^T X[s]   [E][R][lddw], expert
+ *             stride R * lddw
+ * dW is written whole: exactly zero where a weight is not kept and for experts
+ * without rows.  dX or dW may be NULL (not computed), not both.  Operands are
+ * the 16-bit tensors as they are, sums binary32, every output rounded once; the
+ * result does not depend on launch order (no atomics).  Errors as
+ * nm_expert_linear; NM_EINVAL also for no output, lddx < K, lddw < K, lddy < R;
+ * NM_EUNSUPPORTED also where 64-row pieces of all experts' rows pass 2^31
+ * bytes for 256 columns, or the operands' tiles a launch (2^24).
+ */
+nm_status nm_expert_linear_backward_workspace_size(const nm_experts* w, int64_t T, size_t* bytes);
+nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T, const void* offsets,
+                                    int32_t offsets_dtype, const void* dY, int64_t lddy, void* dX, int64_t lddx,
+                                    int32_t zero_rest, void* dW, int64_t lddw, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * nm_i8_linear by expert: w_scale float[E][R], bias NULL or float[E][R].
+ * Arguments, arithmetic and errors as nm_i8_linear and nm_expert_linear.
+ */
+nm_status nm_i8_expert_linear_workspace_size(const nm_experts* w, const nm_i8* xq, int64_t T, size_t* bytes);
+nm_status nm_i8_expert_linear(const nm_experts* w, const float* w_scale, const nm_i8* xq, const void* Xt, int64_t ldx,
+                              int32_t x_dtype, int64_t T, const void* offsets, int32_t offsets_dtype, void* Yt,
+                              int64_t ldy, int32_t y_dtype, const float* bias, int32_t act, int32_t zero_rest,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

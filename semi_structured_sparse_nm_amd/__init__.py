@@ -18,6 +18,17 @@ library every call raises.
     Y = mx_linear(m, Xt)                                    # Xt: [T, K]  ->  Y: [T, R]
     H = mx_glu(mg, mu, Xt, act="silu")
 
+    # 8-bit rows: int8 packed weights with a scale for each channel, activations
+    # with one for each token
+    q = i8_quantize(W)                                      # q.values [R, K] int8, q.scales [R]
+    Y = i8_linear(pack(q.values, N, M), q.scales, Xt)       # Xt: [T, K]  ->  Y: [T, R]
+
+    # rows grouped by expert: E packed weights, expert e's rows offsets[e] .. offsets[e + 1]
+    x = pack_experts(W, N, M)                               # W: [E, R, K]
+    Y = expert_linear(x, Xt, offsets)                       # Xt: [T, K]  ->  Y: [T, R]
+    dX, dW = expert_linear_backward(x, Xt, offsets, dY)
+    Y = i8_expert_linear(x8, scales, Xt, offsets)           # x8: int8, scales [E, R]
+
 Operation: paper "Realizable N:M Sparse Transformer Inference via
 Search-Kernel Co-Design" (arXiv 2607.12505) -- Sec. 2.1 N:M constraint,
 Sec. 4.2 packed windows and micro-dense execution.
@@ -66,6 +77,19 @@ class NmMx(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("format_version", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("codes", ctypes.c_void_p), ("codes_bytes", ctypes.c_size_t),
                 ("scales", ctypes.c_void_p), ("scales_bytes", ctypes.c_size_t)]
+
+
+class NmI8(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("format_version", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("codes", ctypes.c_void_p), ("codes_bytes", ctypes.c_size_t),
+                ("scales", ctypes.c_void_p), ("scales_bytes", ctypes.c_size_t)]
+
+
+class NmExperts(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int32),
+                ("M", ctypes.c_int32), ("dtype", ctypes.c_int32), ("format_version", ctypes.c_uint32),
+                ("values", ctypes.c_void_p), ("values_bytes", ctypes.c_size_t), ("meta", ctypes.c_void_p),
+                ("meta_bytes", ctypes.c_size_t)]
 
 
 HYBRID_BUFFERS = ("values", "meta", "codes", "res_ptr", "res_ent")
@@ -131,6 +155,25 @@ def lib() -> ctypes.CDLL:
         L.nm_mx_workspace_size.argtypes = [MP, MP, I64, I32, ctypes.POINTER(SZ)]
         L.nm_mx_linear.argtypes = [MP, MP, P, I64, I32, I64, P, I64, I32, P, I32, P, SZ, P]
         L.nm_mx_glu.argtypes = [MP, MP, MP, P, I64, I32, I64, P, I64, I32, I32, P, SZ, P]
+        IP, EP = ctypes.POINTER(NmI8), ctypes.POINTER(NmExperts)
+        L.nm_i8_size.argtypes = [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
+        L.nm_i8_quantize.argtypes = [P, I64, I32, IP, P]
+        L.nm_i8_dequantize.argtypes = [IP, P, I64, I32, P]
+        L.nm_i8_linear_workspace_size.argtypes = [PP, IP, I64, ctypes.POINTER(SZ)]
+        L.nm_i8_linear.argtypes = [PP, P, IP, P, I64, I32, I64, P, I64, I32, P, I32, P, SZ, P]
+        L.nm_experts_size.argtypes = [I64, I64, I64, I32, I32, I32, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
+        L.nm_experts_pack.argtypes = [P, I64, I64, EP, P]
+        L.nm_expert_linear_workspace_size.argtypes = [EP, P, I64, I64, ctypes.POINTER(SZ)]
+        L.nm_expert_linear.argtypes = [EP, P, I64, I64, P, I32, P, I64, I32, P, SZ, P]
+        L.nm_expert_linear_backward_workspace_size.argtypes = [EP, I64, ctypes.POINTER(SZ)]
+        L.nm_expert_linear_backward.argtypes = [EP, P, I64, I64, P, I32, P, I64, P, I64, I32, P, I64, P, SZ, P]
+        L.nm_i8_expert_linear_workspace_size.argtypes = [EP, IP, I64, ctypes.POINTER(SZ)]
+        L.nm_i8_expert_linear.argtypes = [EP, P, IP, P, I64, I32, I64, P, I32, P, I64, I32, P, I32, I32, P, SZ, P]
+        for f in ("nm_i8_size", "nm_i8_quantize", "nm_i8_dequantize", "nm_i8_linear_workspace_size", "nm_i8_linear",
+                  "nm_experts_size", "nm_experts_pack", "nm_expert_linear_workspace_size", "nm_expert_linear",
+                  "nm_expert_linear_backward_workspace_size", "nm_expert_linear_backward",
+                  "nm_i8_expert_linear_workspace_size", "nm_i8_expert_linear"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("nm_pack_size", "nm_pack", "nm_spmm_workspace_size", "nm_spmm", "nm_hybrid_pack_size",
                   "nm_hybrid_pack", "nm_hybrid_spmm", "nm_glu_workspace_size", "nm_glu", "nm_glu_kept",
                   "nm_glu_backward_workspace_size", "nm_glu_backward", "nm_glu_backward_kept", "nm_mx_size", "nm_mx_quantize",
@@ -500,6 +543,9 @@ def _descriptor(p):
     if type(p) is Packed:
         v, m = p.values, p.meta
         key = (v.data_ptr(), v.numel(), p.rows, p.K, p.N, p.M, p.dtype, p.format_version)
+    elif type(p) is Experts:
+        v, m = p.values, p.meta
+        key = (v.data_ptr(), v.numel(), p.experts, p.rows, p.K, p.N, p.M, p.dtype, p.format_version)
     else:
         v, m = p.codes, p.scales
         key = (v.data_ptr(), v.numel(), p.rows, p.K, p.format_version)
@@ -865,4 +911,302 @@ def mx_glu(gate: Mx, up: Mx, X, act: str = "silu", out_dtype: torch.dtype | None
         "X, X scales, gate codes, gate scales, out, up codes, up scales", up.codes, up.scales)
     _call(dev, lib().nm_mx_glu, "nm_mx_glu", _descriptor(gate), _descriptor(up), xq, xp, ldx, xdt, T, out.data_ptr(),
           ldy, ydt, a, ws[1], ws[2])
+    return out
+
+
+# ---------------------------------------------------------------- 8-bit rows
+@dataclass
+class I8:
+    """rows x K values as 8-bit whole numbers with one float32 scale a row:
+    codes [rows, Kp] int8 (Kp = K rounded up to 128, zeros past K) and scales
+    [rows]."""
+    rows: int
+    K: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    format_version: int = FORMAT_VERSION
+
+    def desc(self) -> NmI8:
+        return NmI8(self.rows, self.K, self.format_version, 0, self.codes.data_ptr(), self.codes.numel(),
+                    self.scales.data_ptr(), self.scales.numel() * 4)
+
+    def __getstate__(self):
+        return _fields_of(self)
+
+    @property
+    def values(self) -> torch.Tensor:
+        """The [rows, K] int8 elements (a view): what pack() takes as a weight."""
+        return self.codes[:, :self.K]
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def i8_quantize(X: torch.Tensor) -> I8:
+    """nm_i8_quantize: X [rows, K] (float16, bfloat16 or float32) as 8-bit rows:
+    scale = amax / 127 of the row (float32, at least 2^-126), elements the exact
+    quotient rounded half to even.  For activations a row is a token, for
+    weights an output channel."""
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor")
+    xdt = _float_type("X", X.dtype)
+    rows, K = X.shape
+    ldx = _row_pitch("X", X, rows, K)
+    dev = _one_gpu("X", X)
+    q = I8(rows, K, X.new_empty((rows, (K + 127) // 128 * 128), dtype=torch.int8),
+           X.new_empty((rows,), dtype=torch.float32))
+    _call(dev, lib().nm_i8_quantize, "nm_i8_quantize", X.data_ptr(), ldx, xdt, _descriptor(q))
+    return q
+
+
+def i8_dequantize(q: I8, out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_i8_dequantize: the [rows, K] values q stands for."""
+    if out is None:
+        out = q.codes.new_empty((q.rows, q.K), dtype=out_dtype)
+    ydt = _float_type("out", out.dtype)
+    ld = _row_pitch("out", out, q.rows, q.K)
+    dev = _one_gpu("codes, scales, out", q.codes, q.scales, out)
+    _call(dev, lib().nm_i8_dequantize, "nm_i8_dequantize", _descriptor(q), out.data_ptr(), ld, ydt)
+    return out
+
+
+def _check_channels(name: str, t: torch.Tensor, shape: tuple) -> int:
+    """Address of a contiguous float32 tensor of one value an output channel."""
+    _check_dtype(name, t, torch.float32)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _i8_operands(w, w_scale, X, bias, out_dtype, out, act, shape, *others):
+    """Checks shared by i8_linear and i8_expert_linear: (device, T, xq, x
+    pointer, ldx, x dtype, out, ldy, y dtype, scale pointer, bias pointer)."""
+    if w.dtype != NM_I8:
+        raise TypeError(f"the 8-bit product takes int8 weights, not {w.torch_dtype}")
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    sp = _check_channels("w_scale", w_scale, shape)
+    bp = None if bias is None else _check_channels("bias", bias, shape)
+    if type(X) is I8:
+        if X.K != w.K:
+            raise ValueError(f"X has K={X.K}, the weight has K={w.K}")
+        T, xq, xp, ldx, xdt = X.rows, _descriptor(X), None, 0, 0
+        x0, xs, default = X.codes, X.scales, torch.bfloat16
+    else:
+        if X.dim() != 2:
+            raise ValueError("X must be a 2-D tensor or an I8")
+        xdt = _float_type("X", X.dtype)
+        T = X.shape[0]
+        ldx = _row_pitch("X", X, T, w.K)
+        xq, xp = None, X.data_ptr()
+        x0, xs, default = X, None, X.dtype
+    if out is None:
+        out = x0.new_empty((T, w.rows), dtype=default if out_dtype is None else out_dtype)
+    elif out_dtype is not None:
+        _check_dtype("out", out, out_dtype)
+    ydt = _float_type("out", out.dtype)
+    ldy = _row_pitch("out", out, T, w.rows)
+    dev = _one_gpu("X, X scales, weight, weight meta, w_scale, bias, out, offsets", x0, xs, w.values, w.meta, w_scale,
+                   bias, out, *others)
+    return dev, T, xq, xp, ldx, xdt, out, ldy, ydt, sp, bp
+
+
+def i8_linear_workspace_size(w: Packed, T: int) -> int:
+    """nm_i8_linear_workspace_size: bytes of workspace i8_linear() may need for
+    T tokens."""
+    n = ctypes.c_size_t()
+    _check(lib().nm_i8_linear_workspace_size(_descriptor(w), None, T, ctypes.byref(n)), "nm_i8_linear_workspace_size")
+    return n.value
+
+
+def i8_linear(w: Packed, w_scale: torch.Tensor, X, bias: torch.Tensor | None = None,
+              out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None, act: str = "none",
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_i8_linear: Y[T, R] = act((Xq @ (mask . W)^T) * X scales * w_scale + bias)
+    for an int8 packed weight with a float32 scale for each output channel
+    (w_scale [R]).  X: a [T, K] float16 / bfloat16 / float32 tensor, quantised by
+    the call with a scale for each token, or an I8; Y has X's dtype (an I8:
+    bfloat16) unless out_dtype says otherwise; act "none" or "gelu"."""
+    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, sp, bp = _i8_operands(w, w_scale, X, bias, out_dtype, out, act, (w.rows,))
+    L, d = lib(), _descriptor(w)
+    need = _sized(L.nm_i8_linear_workspace_size, "nm_i8_linear_workspace_size",
+                  ("i8", w.rows, w.K, w.N, w.M, T, xq is None, dev), d, xq, T)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call(dev, L.nm_i8_linear, "nm_i8_linear", d, sp, xq, xp, ldx, xdt, T, out.data_ptr(), ldy, ydt, bp, ACTS[act], wp,
+          wn)
+    return out
+
+
+# ---------------------------------------------------------------- rows grouped by expert
+@dataclass
+class Experts:
+    """Packed N:M weights of several experts, all [rows, K], in two uint8 device
+    buffers, one expert after another."""
+    experts: int
+    rows: int
+    K: int
+    N: int
+    M: int
+    dtype: int
+    values: torch.Tensor
+    meta: torch.Tensor | None
+    format_version: int = FORMAT_VERSION
+
+    def desc(self) -> NmExperts:
+        m = self.meta
+        return NmExperts(self.experts, self.rows, self.K, self.N, self.M, self.dtype, self.format_version,
+                         self.values.data_ptr(), self.values.numel(), None if m is None else m.data_ptr(),
+                         0 if m is None else m.numel())
+
+    def __getstate__(self):
+        return _fields_of(self)
+
+    @property
+    def torch_dtype(self):
+        return _NM_TO_TORCH[self.dtype]
+
+
+def pack_experts(W: torch.Tensor, N: int, M: int) -> Experts:
+    """nm_experts_pack: W [E, R, K] (int8, float16 or bfloat16), each expert's
+    weight pruned and packed as pack() does."""
+    if W.dim() != 3:
+        raise ValueError("W must be a 3-D tensor [experts, R, K]")
+    dt = _TORCH_TO_NM.get(W.dtype)
+    if dt not in (NM_I8, NM_F16, NM_BF16):
+        raise TypeError(f"unsupported weight dtype {W.dtype}")
+    E, R, K = W.shape
+    if E < 1:
+        raise ValueError("W holds no expert")
+    ldw = _row_pitch("W", W[0], R, K)
+    if E > 1 and W.stride(0) < 0:
+        raise ValueError("W must not run backwards")
+    dev = _one_gpu("W", W)
+    vb, mb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().nm_experts_size(E, R, K, N, M, dt, ctypes.byref(vb), ctypes.byref(mb)), "nm_experts_size")
+    x = Experts(E, R, K, N, M, dt, W.new_empty((vb.value,), dtype=torch.uint8),
+                W.new_empty((mb.value,), dtype=torch.uint8) if mb.value else None, 0)
+    d = x.desc()
+    _call(dev, lib().nm_experts_pack, "nm_experts_pack", W.data_ptr(), W.stride(0), ldw, ctypes.byref(d))
+    x.format_version = d.format_version
+    return x
+
+
+_OFFSETS = {torch.int32: 0, torch.int64: 1}
+
+
+def _check_offsets(w: Experts, offsets: torch.Tensor) -> int:
+    dt = _OFFSETS.get(offsets.dtype)
+    if dt is None:
+        raise TypeError(f"offsets must be int32 or int64, got {offsets.dtype}")
+    if offsets.shape != (w.experts + 1,) or offsets.stride(0) != 1:
+        raise ValueError(f"offsets must be a contiguous vector of length {w.experts + 1}, got {tuple(offsets.shape)}")
+    return dt
+
+
+def _expert_rows(w: Experts, X: torch.Tensor):
+    if w.dtype not in (NM_F16, NM_BF16):
+        raise TypeError(f"this product takes float16 / bfloat16 weights, not {w.torch_dtype}")
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor")
+    _check_dtype("X", X, w.torch_dtype)
+    return X.shape[0], _row_pitch("X", X, X.shape[0], w.K)
+
+
+def _expert_key(what: str, w: Experts, T: int, rows, dev: int) -> tuple:
+    return what, w.experts, w.rows, w.K, w.N, w.M, w.dtype, T, rows, dev
+
+
+def expert_linear_workspace_size(w: Experts, T: int) -> int:
+    """nm_expert_linear_workspace_size: bytes of workspace expert_linear() may
+    need for T rows of any stride and alignment."""
+    n = ctypes.c_size_t()
+    _check(lib().nm_expert_linear_workspace_size(_descriptor(w), None, 0, T, ctypes.byref(n)),
+           "nm_expert_linear_workspace_size")
+    return n.value
+
+
+def expert_linear(w: Experts, X: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_expert_linear: Y[s] = X[s] @ (mask . W_e)^T for the rows s of each expert
+    e, offsets[e] <= s < offsets[e + 1], float16 / bfloat16.  X [T, K] is sorted by
+    expert; offsets [E + 1] (int32 or int64) stays on the GPU.  Rows of no expert,
+    before offsets[0] and from offsets[E] on, are left as they are in `out` and
+    are zero in a new output.  Not part of autograd's graph."""
+    T, ldx = _expert_rows(w, X)
+    odt = _check_offsets(w, offsets)
+    fill = out is None
+    if fill:
+        out = X.new_empty((T, w.rows))
+    else:
+        _check_dtype("out", out, X.dtype)
+    ldy = _row_pitch("out", out, T, w.rows)
+    dev = _one_gpu("X, weight, weight meta, out, offsets", X, w.values, w.meta, out, offsets)
+    L, d, x = lib(), _descriptor(w), X.data_ptr()
+    need = _sized(L.nm_expert_linear_workspace_size, "nm_expert_linear_workspace_size",
+                  _expert_key("expert", w, T, (x % 16, ldx), dev), d, x, ldx, T)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call(dev, L.nm_expert_linear, "nm_expert_linear", d, x, ldx, T, offsets.data_ptr(), odt, out.data_ptr(), ldy, fill,
+          wp, wn)
+    return out
+
+
+def expert_linear_backward_workspace_size(w: Experts, T: int) -> int:
+    """nm_expert_linear_backward_workspace_size: bytes of workspace
+    expert_linear_backward() needs."""
+    n = ctypes.c_size_t()
+    _check(lib().nm_expert_linear_backward_workspace_size(_descriptor(w), T, ctypes.byref(n)),
+           "nm_expert_linear_backward_workspace_size")
+    return n.value
+
+
+def expert_linear_backward(w: Experts, X: torch.Tensor, offsets: torch.Tensor, dY: torch.Tensor, need_dx: bool = True,
+                           need_dw: bool = True, workspace: torch.Tensor | None = None):
+    """nm_expert_linear_backward: the gradients of expert_linear() for a fixed
+    mask, from dY [T, R]: (dX [T, K], dW [E, R, K]) in the weights' dtype; dW is
+    dense and zero where a weight is pruned and for experts without rows, dX is
+    zero in rows of no expert.  need_dx / need_dw = False leaves that part out
+    (None in its place).  Not part of autograd's graph."""
+    T, ldx = _expert_rows(w, X)
+    odt = _check_offsets(w, offsets)
+    if not need_dx and not need_dw:
+        raise ValueError("expert_linear_backward needs need_dx or need_dw")
+    E, R, K = w.experts, w.rows, w.K
+    lddy = _row_pitch("dY", dY, T, R)
+    _check_dtype("dY", dY, X.dtype)
+    dev = _one_gpu("X, weight, weight meta, dY, offsets", X, w.values, w.meta, dY, offsets)
+    L, d = lib(), _descriptor(w)
+    need = _sized(L.nm_expert_linear_backward_workspace_size, "nm_expert_linear_backward_workspace_size",
+                  _expert_key("expert_backward", w, T, None, dev), d, T)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    dX = X.new_empty((T, K)) if need_dx else None
+    dW = X.new_empty((E, R, K)) if need_dw else None
+    _call(dev, L.nm_expert_linear_backward, "nm_expert_linear_backward", d, X.data_ptr(), ldx, T, offsets.data_ptr(), odt,
+          dY.data_ptr(), lddy, dX.data_ptr() if need_dx else None, K, 1, dW.data_ptr() if need_dw else None, K, wp, wn)
+    return dX, dW
+
+
+def i8_expert_linear_workspace_size(w: Experts, T: int) -> int:
+    """nm_i8_expert_linear_workspace_size: bytes of workspace i8_expert_linear()
+    may need for T rows."""
+    n = ctypes.c_size_t()
+    _check(lib().nm_i8_expert_linear_workspace_size(_descriptor(w), None, T, ctypes.byref(n)),
+           "nm_i8_expert_linear_workspace_size")
+    return n.value
+
+
+def i8_expert_linear(w: Experts, w_scale: torch.Tensor, X, offsets: torch.Tensor, bias: torch.Tensor | None = None,
+                     out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None, act: str = "none",
+                     workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """nm_i8_expert_linear: i8_linear() by expert, w_scale and bias [E, R], rows
+    and offsets as in expert_linear()."""
+    odt = _check_offsets(w, offsets)
+    fill = out is None
+    dev, T, xq, xp, ldx, xdt, out, ldy, ydt, sp, bp = _i8_operands(
+        w, w_scale, X, bias, out_dtype, out, act, (w.experts, w.rows), offsets)
+    L, d = lib(), _descriptor(w)
+    need = _sized(L.nm_i8_expert_linear_workspace_size, "nm_i8_expert_linear_workspace_size",
+                  _expert_key("i8_expert", w, T, xq is None, dev), d, xq, T)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call(dev, L.nm_i8_expert_linear, "nm_i8_expert_linear", d, sp, xq, xp, ldx, xdt, T, offsets.data_ptr(), odt,
+          out.data_ptr(), ldy, ydt, bp, ACTS[act], fill, wp, wn)
     return out

@@ -32,7 +32,8 @@ inline int64_t mx_scales_bytes(int64_t rows, int64_t K) { return (rows + 31) / 3
 //   TILE_BACK    the gradients of the gated block in one launch: A B^T of the
 //                fields below (16-bit, or binary32 slices where split > 1), and
 //                A B^T of `w`, twice, where kept
-enum TileOp { TILE_LINEAR = 0, TILE_GLU = 1, TILE_BACK = 2 };
+//   TILE_ROWS, TILE_COLS  products of rows grouped by expert (nm_rows.hpp)
+enum TileOp { TILE_LINEAR = 0, TILE_GLU = 1, TILE_BACK = 2, TILE_ROWS = 3, TILE_COLS = 4 };
 
 struct TileGradArgs {
   const uint8_t* A[2];       // transposed dG, dU: [Mr] rows of ld bytes
@@ -71,7 +72,7 @@ struct TileArgs {
 };
 
 // Element types of the tile kernel's operands.
-enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2 };
+enum { TILE_F16 = 0, TILE_BF16 = 1, TILE_MX = 2, TILE_I8 = 3 };
 
 // Tile shape (0: 256 x 256, 1: 128 x 256, 2: 128 x 128, 3: 64 x 128) and slices
 // of the reduction for one product, by a model of its time.

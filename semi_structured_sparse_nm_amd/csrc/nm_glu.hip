@@ -2,77 +2,11 @@
 // expanded to dense rows or dense columns, the activation's backward step,
 // padded activation rows.  All of them are bound by HBM: every element is
 // read once and written once, in 16-byte pieces.
-#include "nm_ffn.hpp"
+#include "nm_expand_cols.hpp"
 
 namespace nm {
 
 namespace {
-
-// Eight dense columns c .. c + 7 (c % 8 == 0, c < nKB * 64) of packed row r
-// (16-bit weights): two groups of M = 4 or one of M = 8.  o: the eight values
-// as four dwords, zeros where pruned; returns the kept bits.
-__device__ __forceinline__ uint32_t expand8(const Geometry& g, const uint8_t* values, const uint8_t* meta, int64_t r,
-                                            int64_t c, uint32_t (&o)[4]) {
-  const int64_t blk = (r >> 4) * g.nKB + (c >> 6);
-  const int rr = (int)(r & 15);
-  const int cnt = g.N * (8 / g.M);                     // kept values of the eight columns
-  const int s0 = (int)(c & 63) / 8 * cnt;
-  const uint8_t* v = values + blk * g.vblk + ((int64_t)rr * g.C + s0) * 2;
-  if (g.N == g.M) {
-    const v4i x = *reinterpret_cast<const v4i*>(v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (uint32_t)x[i];
-    return 0xFF;
-  }
-  uint32_t e[4] = {0u, 0u, 0u, 0u};
-  if (cnt == 4) {
-    const v2i x = *reinterpret_cast<const v2i*>(v);
-    e[0] = (uint32_t)x[0];
-    e[1] = (uint32_t)x[1];
-  } else if (cnt % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (2 * i < cnt) e[i] = reinterpret_cast<const uint32_t*>(v)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < cnt) e[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(v)[i] << (16 * (i & 1));
-  }
-  const uint32_t* m = reinterpret_cast<const uint32_t*>(meta + blk * g.mblk + (int64_t)rr * g.MR);
-  const int bit = s0 * g.w, d = bit >> 5;
-  const uint64_t lo = m[d], hi = 4 * d + 4 < g.MR ? m[d + 1] : 0u;
-  const uint32_t pos = (uint32_t)((lo | hi << 32) >> (bit & 31));
-  uint64_t q0 = 0, q1 = 0;                             // columns 0..3, 4..7
-  uint32_t keep = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i < cnt) {
-      const uint64_t el = (e[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-      uint32_t p = (pos >> (i * g.w)) & ((1u << g.w) - 1u);
-      if (g.M == 4 && i >= g.N) p += 4;
-      keep |= 1u << p;
-      const uint64_t sh = el << (16 * (p & 3));
-      if (p < 4) q0 |= sh; else q1 |= sh;
-    }
-  }
-  o[0] = (uint32_t)q0; o[1] = (uint32_t)(q0 >> 32);
-  o[2] = (uint32_t)q1; o[3] = (uint32_t)(q1 >> 32);
-  return keep;
-}
-
-// Sixteen dense columns c .. c + 15 (c % 16 == 0): one 16-byte piece of the
-// packed row where four of eight are kept.
-__device__ __forceinline__ uint32_t expand16(const Geometry& g, const uint8_t* values, const uint8_t* meta, int64_t r,
-                                             int64_t c, uint32_t (&o)[8]) {
-  uint32_t h[4];
-  uint32_t keep = expand8(g, values, meta, r, c, h);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = h[i];
-  keep |= expand8(g, values, meta, r, c + 8, h) << 8;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[4 + i] = h[i];
-  return keep;
-}
 
 // blockIdx.y: the weight.  A wave covers one packed block (16 rows x 64
 // columns), lane 4 r + q its columns 16 q .. of row r.

@@ -1,0 +1,152 @@
+// Operands of the products of grouped rows: packed weights as dense blocks;
+// weights and rows transposed for the gradients.  All of them are bound by
+// HBM: every element is read once and written once, in 16-byte pieces.
+#include "nm_expand_cols.hpp"
+#include "nm_rows.hpp"
+
+namespace nm {
+
+namespace {
+
+// whether expert e may have rows (surely not where its offsets say so as they are)
+__device__ __forceinline__ bool may_have_rows(const RowGroups& o, int e) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return row_bound(o, e + 1) > row_bound(o, e);
+#else
+  return true;
+#endif
+}
+
+// A thread makes 16 bytes of a dense block: piece q % 8 of its row q / 8.
+template <int EB, int M>
+__global__ void __launch_bounds__(256) rows_dense_kernel(Geometry g, const uint8_t* values, const uint8_t* meta,
+                                                         RowGroups rows, uint8_t* dense) {
+  const int64_t per = g.nRB * g.nKB;
+  for (int64_t b = (int64_t)blockIdx.x * 2 + (threadIdx.x >> 7); b < per * rows.E; b += (int64_t)gridDim.x * 2) {
+    if (!may_have_rows(rows, (int)(b / per))) continue;
+    const int rr = (threadIdx.x & 127) >> 3, piece = threadIdx.x & 7;
+    v4i o;
+    if constexpr (EB == 1) {
+      o = expand16_i8<M>(g, values, meta, b, rr, piece);
+    } else {
+      // (blocks of all experts are one row of blocks to expand8)
+      Geometry one = g;
+      one.nKB = 1;
+      uint32_t h[4];
+      expand8(one, values, meta, b * 16 + rr, 8 * piece, h);
+      o = v4i{(int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+    }
+    *reinterpret_cast<v4i*>(dense + b * 2048 + rr * 128 + 16 * piece) = o;
+  }
+}
+
+// 128 rows x 64 columns of one expert's weight, expanded and transposed into
+// blocks, and the kept bits.  Pitch 130 halves: the four 16-column runs of a
+// packed row and its block's sixteen rows fall on different banks.
+__device__ __forceinline__ void prepare_weight(const RowsPrepareArgs& a, int64_t b, uint16_t* lds) {
+  uint16_t(*tile)[130] = reinterpret_cast<uint16_t(*)[130]>(lds);
+  const Geometry& g = a.g;
+  const int64_t rt = (g.R + 127) / 128, e = b / (rt * g.nKB);
+  if (!may_have_rows(a.rows, (int)e)) return;
+  b -= e * rt * g.nKB;
+  const int64_t kb = b % g.nKB, r0 = (b / g.nKB) * 128;
+  const uint8_t* values = a.values + e * (int64_t)g.values_bytes();
+  const uint8_t* meta = a.meta + e * (int64_t)g.meta_bytes();
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int rl = 16 * (it * 4 + (threadIdx.x >> 6)) + (lane >> 2), cl = (lane & 3) * 16;
+    const int64_t r = r0 + rl;
+    uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (r < g.R) {
+      const uint32_t keep = expand16(g, values, meta, r, kb * 64 + cl, o);
+      if (a.mask)
+        *reinterpret_cast<uint16_t*>(a.mask + (e * g.R + r) * (g.nKB * 8) + kb * 8 + cl / 8) = (uint16_t)keep;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) tile[cl + i][rl] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+  }
+  if (!a.wt) return;
+  __syncthreads();
+  const int64_t Rs = (g.R + 63) / 64;                   // blocks along R
+  uint16_t* wt = a.wt + e * ((g.K + 15) / 16 * Rs * 1024);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int q = it * 256 + threadIdx.x;
+    const int kl = q >> 4, rl = (q & 15) * 8;
+    const int64_t k = kb * 64 + kl, s = (r0 + rl) >> 6;
+    if (k < g.K && s < Rs) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[kl][rl]);
+      *reinterpret_cast<v4i*>(wt + ((k >> 4) * Rs + s) * 1024 + (k & 15) * 64 + (rl & 63)) =
+          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+    }
+  }
+}
+
+// 64 rows of one expert (zeros behind its last) x 64 columns of x, transposed.
+__device__ __forceinline__ void prepare_rows(const RowsPrepareArgs& a, const uint16_t* x, int64_t ldx, int64_t cols,
+                                             int slab, int64_t c0, uint16_t* xt, uint16_t* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  uint16_t(*tile)[66] = reinterpret_cast<uint16_t(*)[66]>(lds);
+  const RowUnit u = find_unit<64, true>(a.rows, slab);
+  if (u.e < 0) return;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int q = it * 256 + threadIdx.x;
+    const int tl = q >> 3, cl = (q & 7) * 8;
+    const int64_t t = u.row + tl, c = c0 + cl;
+    v4i o = {0, 0, 0, 0};
+    if (t < u.end && c < cols) o = load_piece(x + t * ldx, c, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[cl + i][tl] = (uint16_t)((uint32_t)o[i >> 1] >> (16 * (i & 1)));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int q = it * 256 + threadIdx.x;
+    const int cl = q >> 3, tl = (q & 7) * 8;
+    if (c0 + cl < cols) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[cl][tl]);
+      *reinterpret_cast<v4i*>(xt + (c0 + cl) * (64 * a.slabs) + 64 * (int64_t)slab + tl) =
+          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+    }
+  }
+#endif
+}
+
+// What the gradients' products read, in one launch; workgroups take, by index,
+// tiles of the weights, of X and of dY.  The tiles pass through LDS.
+__global__ void __launch_bounds__(256) rows_prepare_kernel(RowsPrepareArgs a, int64_t n_weight, int64_t n_x) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[64 * 130];
+  int64_t b = blockIdx.x;
+  if (b < n_weight) return prepare_weight(a, b, lds);
+  b -= n_weight;
+  if (b < n_x) return prepare_rows(a, a.X, a.ldx, a.g.K, (int)(b % a.slabs), b / a.slabs * 64, a.xt, lds);
+  b -= n_x;
+  prepare_rows(a, a.dY, a.lddy, a.g.R, (int)(b % a.slabs), b / a.slabs * 64, a.yt, lds);
+}
+
+}  // namespace
+
+hipError_t launch_rows_dense(const Geometry& g, const uint8_t* values, const uint8_t* meta, const RowGroups& rows,
+                             uint8_t* dense, hipStream_t s) {
+  const int64_t n = g.nRB * g.nKB * rows.E;
+  const dim3 grid(grid_1d(n * 128, 256)), block(256);
+  if (g.eb == 1 && g.M == 4)
+    hipLaunchKernelGGL((rows_dense_kernel<1, 4>), grid, block, 0, s, g, values, meta, rows, dense);
+  else if (g.eb == 1)
+    hipLaunchKernelGGL((rows_dense_kernel<1, 8>), grid, block, 0, s, g, values, meta, rows, dense);
+  else
+    hipLaunchKernelGGL((rows_dense_kernel<2, 4>), grid, block, 0, s, g, values, meta, rows, dense);
+  return hipGetLastError();
+}
+
+hipError_t launch_rows_prepare(const RowsPrepareArgs& a, hipStream_t s) {
+  const int64_t n_weight = a.wt || a.mask ? a.rows.E * ((a.g.R + 127) / 128) * a.g.nKB : 0;
+  const int64_t n_x = a.xt ? a.slabs * ((a.g.K + 63) / 64) : 0;
+  const int64_t n_y = a.yt ? a.slabs * ((a.g.R + 63) / 64) : 0;
+  hipLaunchKernelGGL(rows_prepare_kernel, dim3((unsigned)(n_weight + n_x + n_y)), dim3(256), 0, s, a, n_weight, n_x);
+  return hipGetLastError();
+}
+
+}  // namespace nm

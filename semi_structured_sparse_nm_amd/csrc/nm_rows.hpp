@@ -1,0 +1,205 @@
+// Shared definitions of the products of rows grouped by expert (16-bit and
+// 8-bit packed weights, one weight being one expert) and of the 8-bit row
+// format.  Internal; the public surface is include/nm_sparse.h.
+#pragma once
+
+#include "nm_ffn.hpp"
+
+namespace nm {
+
+// Most experts: each workgroup keeps a table of their rows in LDS.
+constexpr int kMaxExperts = 1023;
+
+// 8-bit rows: K elements and zeros up to a multiple of 128, one matrix
+// instruction's reduction of the sparse product.
+inline int64_t i8_kp(int64_t K) { return (K + 127) / 128 * 128; }
+
+// The rows of each expert: at[e] .. at[e + 1] - 1, `at` of E + 1 whole numbers
+// in device memory.  Read defensively, since the host does not see them: each
+// is taken into [0, T] and as at least the one before it, so whatever they
+// hold, experts' rows are disjoint and inside the call's.  Null: one expert,
+// all rows.
+struct RowGroups {
+  const void* at;
+  int wide;                  // 64-bit, else 32-bit
+  int E;
+  int64_t T;
+};
+
+// Y[s][r] = act(sum_k X[s][k] W_e[r][k] (x scale[s] x wscale[e][r]) + bias[e][r])
+struct RowsArgs {
+  Geometry g;                // of one expert's weight
+  int wdt;
+  const uint8_t* values;     // of expert 0; the others follow
+  const uint8_t* meta;
+  RowGroups rows;
+  const void* X;             // 16-bit values, or 8-bit elements
+  int64_t ldx;
+  const float* xscale;       // 8 bits: [T]
+  const float* wscale;       // 8 bits: [E][R]
+  const float* bias;         // 8 bits: [E][R] or nullptr
+  int act;
+  void* Y;
+  int64_t ldy;
+  int ydt;
+  bool zero_rest;            // rows of no expert: zeros, else left as they are
+};
+
+// Units of `u` rows that T rows of E experts make at most, each expert's
+// counted for itself.
+inline int64_t units_most(int64_t T, int64_t E, int64_t u) {
+  const int64_t some = T < E ? T : E;
+  return (T + some * (u - 1)) / u;
+}
+
+// few rows an expert: the packed weights streamed once per unit of 16 rows or more
+hipError_t launch_rows_decode(const RowsArgs& a, hipStream_t s);
+hipError_t launch_rows_decode_i8(const RowsArgs& a, hipStream_t s);
+hipError_t launch_rows_decode_f16(const RowsArgs& a, hipStream_t s);
+hipError_t launch_rows_decode_bf16(const RowsArgs& a, hipStream_t s);
+
+// Tile products of grouped rows.
+//   TILE_ROWS  C[s][n] = sum_k A[s][k] B_e[n][k] for expert e's rows s (8 bits:
+//              scaled, with bias and activation).  A [T] rows of lda bytes; B
+//              in blocks of 16 rows x 128 bytes (sparse: packed 2:4 blocks of
+//              64, with positions), nslab of them side by side, the blocks of
+//              an expert's ceil(Nr / 16) x nslab one after another, then the
+//              next expert's.
+//   TILE_COLS  C_e[m][n] = keep (.) sum over expert e's rows of A[m][t] B[n][t]:
+//              both operands with the rows along the reduction, expert e's from
+//              slab slab_at[e] of 64 on, each expert's padded with zeros to
+//              whole slabs, one at least.
+struct RowsTile : TileArgs {
+  RowGroups rows;
+  const uint8_t* meta;       // sparse TILE_ROWS
+  const float* xscale;       // 8 bits: [T], [E][Nr]; bias [E][Nr] or nullptr
+  const float* wscale;
+  bool zero_rest;            // TILE_ROWS: rows of no expert become zeros
+  int64_t es;                // TILE_COLS: elements between experts' outputs
+  const uint8_t* mask;       // and kept bits, [E][Mr][ldm]: bit k % 8 of byte k / 8
+  int64_t ldm;
+};
+// et: TILE_F16, TILE_BF16 (outputs of that type) or TILE_I8 (TILE_ROWS only)
+hipError_t launch_rows_tile(int et, TileOp op, int ydt, const RowsTile& a, hipStream_t s);
+// TILE_ROWS on 2:4 weights
+hipError_t launch_rows_tile24(int wdt, int ydt, const RowsTile& a, hipStream_t s);
+constexpr int kRowsTable = 1024;   // boundaries (E + 1) a workgroup's table holds
+
+// Packed weights -> the same blocks with every column (dense blocks of 16 rows
+// x 128 bytes), for experts that have rows.
+hipError_t launch_rows_dense(const Geometry& g, const uint8_t* values, const uint8_t* meta, const RowGroups& rows,
+                             uint8_t* dense, hipStream_t s);
+
+// Operands of the gradients (16-bit): each expert's weight transposed, in
+// blocks as above (wt: K rows, Rp = R rounded up to 64 columns) where it has
+// rows; its kept bits, mask [E][R][Kp / 8]; X and dY transposed, xt [K][ld] and
+// yt [R][ld], columns as ColsTileArgs has them.  Null outputs are left out.
+struct RowsPrepareArgs {
+  Geometry g;
+  RowGroups rows;
+  const uint8_t* values;
+  const uint8_t* meta;
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* dY;
+  int64_t lddy;
+  int64_t slabs;             // most slabs of rows; ld = 64 slabs
+  uint16_t* wt;
+  uint8_t* mask;
+  uint16_t* xt;
+  uint16_t* yt;
+};
+hipError_t launch_rows_prepare(const RowsPrepareArgs& a, hipStream_t s);
+
+// X [rows][ldx] of xdt -> elements [rows][i8_kp(K)] and scales [rows]; back
+hipError_t launch_i8_quantize(const void* X, int64_t ldx, int xdt, int64_t rows, int64_t K, int8_t* codes,
+                              float* scales, hipStream_t s);
+hipError_t launch_i8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t K, void* Y,
+                                int64_t ldy, int ydt, hipStream_t s);
+
+// ---------------------------------------------------------------- device
+#if defined(__HIP_DEVICE_COMPILE__)
+// at[i], taken into [0, T]
+__device__ __forceinline__ int row_bound(const RowGroups& o, int i) {
+  if (!o.at) return i ? (int)o.T : 0;
+  const int64_t v = o.wide ? static_cast<const int64_t*>(o.at)[i] : (int64_t)static_cast<const int32_t*>(o.at)[i];
+  return (int)min(max(v, (int64_t)0), o.T);
+}
+__device__ __forceinline__ int wave_scan_max(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d);
+    v = lane >= d ? max(v, u) : v;
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_scan_add(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d);
+    v = lane >= d ? v + u : v;
+  }
+  return v;
+}
+
+// Experts' first rows and first units (of U rows; with LEAST an expert without
+// rows has one), a wave's lanes 64 boundaries at a time: f(i, from, at, unit, n)
+// for the lane's boundary i: the expert in front of it has the rows from .. at -
+// 1 and the units unit - n .. unit - 1 (i = 0 and i > E: none).  f returns
+// whether to stop, the same in every lane.
+template <int U, bool LEAST, class F>
+__device__ __forceinline__ void row_boundaries(const RowGroups& o, F&& f) {
+  const int lane = threadIdx.x & 63;
+  int last = 0, units = 0;                              // of the boundaries before this chunk
+  for (int c = 0; c <= o.E; c += 64) {
+    const int i = c + lane;
+    int v = i <= o.E ? row_bound(o, i) : 0;
+    v = max(wave_scan_max(v, lane), last);
+    int p = __shfl_up(v, 1);
+    if (lane == 0) p = c ? last : v;
+    int n = (v - p + U - 1) / U;
+    if (LEAST && n == 0) n = 1;
+    if (i == 0 || i > o.E) n = 0;
+    const int u = wave_scan_add(n, lane) + units;
+    if (f(i, p, v, u, n)) return;
+    last = __shfl(v, 63);
+    units = __shfl(u, 63);
+  }
+}
+
+// Unit `unit` of the rows (called by whole waves): its expert, first row, and
+// the expert's first row and end; e < 0 where there are fewer units.
+struct RowUnit {
+  int e, row, begin, end;
+};
+template <int U, bool LEAST>
+__device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int unit) {
+  if (!o.at) return {(int64_t)unit * U < o.T ? 0 : -1, unit * U, 0, (int)o.T};
+  RowUnit r = {-1, 0, 0, 0};
+  row_boundaries<U, LEAST>(o, [&](int i, int from, int at, int u, int n) {
+    const uint64_t hit = __ballot(u > unit && u - n <= unit);
+    if (!hit) return false;
+    const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+    r.e = __builtin_amdgcn_readlane(i, l) - 1;
+    r.begin = __builtin_amdgcn_readlane(from, l);
+    r.end = __builtin_amdgcn_readlane(at, l);
+    r.row = r.begin + (unit - __builtin_amdgcn_readlane(u - n, l)) * U;
+    return true;
+  });
+  return r;
+}
+
+// The rows of no expert are those before `first` and from `last` on.
+__device__ __forceinline__ void rows_taken(const RowGroups& o, int& first, int& last) {
+  first = 0;
+  last = (int)o.T;
+  if (!o.at) return;
+  first = row_bound(o, 0);
+  last = first;
+  for (int i = threadIdx.x & 63; i <= o.E; i += 64) last = max(last, row_bound(o, i));
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) last = max(last, __shfl_xor(last, d));
+}
+#endif
+
+}  // namespace nm

@@ -1,0 +1,323 @@
+// Products of grouped rows, few rows an expert: each expert's packed weight is
+// streamed once from HBM for every unit of 16 NT of its rows.
+//
+//   Y[s][r] = act(sum_k X[s][k] W_e[r][k] (x scale[s] x wscale[e][r]) + bias[e][r])
+//
+// With so few rows the bound is the packed weights' bytes.  A workgroup owns
+// one 16-row block of one expert's weight and one unit of its rows (found from
+// the offsets by the workgroup itself: the host does not know them, and starts
+// as many as there could be); its NW waves take every NW-th block along K,
+// straight to registers, U blocks in flight per wave.  2:4 windows go to the
+// sparse matrix instruction as they are; other patterns are expanded in
+// registers for the dense one.  Activations come from the caches, 128 bytes of
+// eight rows a load, and change to the instruction's order in the wave's own
+// LDS; the waves' sums meet in LDS, added in wave order.  (The gated block's
+// streamed kernel with one weight; why each of this is so is measured there.)
+//
+// 8-bit elements: sums are exact in 32-bit integers, converted once, then
+// multiplied by the row's scale and the channel's in binary32 (two roundings,
+// far below the output's).
+#pragma once
+
+#include "nm_expand.hpp"
+#include "nm_glu_decode.hpp"
+#include "nm_rows.hpp"
+
+namespace nm {
+
+namespace {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int WT>
+using acc_of = typename std::conditional<WT == NM_I8, v4i, v4f>::type;
+
+// One lane's part of one packed block of 8-bit weights (128 dense columns, a
+// run of 32 a lane), as GluFrag is of 16-bit ones.  Groups of eight columns hold
+// at most two registers of kept values, so each of a group's two dense
+// registers is one byte permute of them, whatever N, by the table of selectors.
+template <int N, int M>
+struct I8Frag {
+  static constexpr bool SPARSE = N == 2 && M == 4;
+  static constexpr bool TABLE = M == 8 && N < 8;
+  static constexpr int W = N == M ? 0 : M == 4 ? 2 : 3;
+  static constexpr int VB = 32 * N / M, VD = VB / 4;   // bytes, dwords of the run's values
+  static constexpr int MBL = VB * W;                   // bits of its positions
+  static constexpr int MRB = (4 * MBL + 31) / 32 * 4;  // bytes of a block row's positions
+  static constexpr int MD = (MBL + 31) / 32;
+  uint32_t vd[VD];
+  uint32_t mb[MD ? MD : 1];
+  __device__ __forceinline__ void load(const uint8_t* values, const uint8_t* meta, int64_t blk, int li, int lg) {
+    const uint8_t* v = values + blk * (64 * VB) + li * (4 * VB) + lg * VB;
+#pragma unroll
+    for (int i = 0; i < VD; ++i) vd[i] = reinterpret_cast<const uint32_t*>(v)[i];
+    if constexpr (N != M) {
+      const uint8_t* m = meta + blk * (16 * MRB) + li * MRB;
+      if constexpr (MBL % 32 == 0) {
+#pragma unroll
+        for (int i = 0; i < MD; ++i) mb[i] = reinterpret_cast<const uint32_t*>(m + lg * (MBL / 8))[i];
+      } else {
+        // the dwords the run's positions lie in (one more than they fill, none
+        // behind the row's last), shifted to start at bit 0
+        const int d = lg * MBL >> 5, sh = lg * MBL & 31;
+        uint32_t w[MD + 1];
+#pragma unroll
+        for (int i = 0; i <= MD; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[min(d + i, MRB / 4 - 1)];
+#pragma unroll
+        for (int i = 0; i < MD; ++i) mb[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], sh);
+      }
+    }
+  }
+  // bits b .. b + 23 and more of the positions, b known when compiled
+  __device__ __forceinline__ uint32_t positions(int b) const {
+    const int d = b >> 5, sh = b & 31;
+    return d + 1 < MD ? __builtin_amdgcn_alignbit(mb[d + 1], mb[d], sh) : mb[d] >> sh;
+  }
+  // the run's bytes b .. b + 3 (zeros behind the run)
+  __device__ __forceinline__ uint32_t bytes(int b) const {
+    const int d = b >> 2, sh = b & 3;
+    return d >= VD ? 0u : __builtin_amdgcn_alignbyte(d + 1 < VD ? vd[d + 1] : 0u, vd[d], sh);
+  }
+  // group q (of the lane's four) of eight columns, expanded
+  __device__ __forceinline__ v2i group(int q, const v2i* table) const {
+    const uint32_t pos = positions(3 * N * q);
+    uint32_t set = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) set |= 1u << (pos >> (3 * j) & 7u);
+    const uint32_t lo = bytes(N * q), hi = N > 4 ? bytes(N * q + 4) : 0u;
+    const v2i sel = table[set];
+    return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
+  }
+  __device__ __forceinline__ v4i mul(v4i x0, v4i x1, v4i c, const v2i* table) const {
+    if constexpr (TABLE) {
+      const v2i a0 = group(0, table), a1 = group(1, table), a2 = group(2, table), a3 = group(3, table);
+      c = mfma_dense<NM_I8>(v4i{a0[0], a0[1], a1[0], a1[1]}, x0, c);
+      return mfma_dense<NM_I8>(v4i{a2[0], a2[1], a3[0], a3[1]}, x1, c);
+    } else if constexpr (SPARSE) {
+      const v4i a = {(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
+      return __builtin_amdgcn_smfmac_i32_16x16x128_i8(
+          a, v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]}, c, (int)mb[0], 0, 0);
+    } else {
+      const uint64_t pos = MD > 1 ? (uint64_t)mb[MD - 1] << 32 | mb[0] : mb[0];
+      c = mfma_dense<NM_I8>(expand_step<NM_I8, N, M, 0>(vd, pos), x0, c);
+      return mfma_dense<NM_I8>(expand_step<NM_I8, N, M, 1>(vd, pos), x1, c);
+    }
+  }
+  // the two 16-byte pieces (of a row's eight in the block) the product wants
+  __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
+};
+
+template <int WT, int N, int M>
+struct RowsFrag : GluFrag<WT, N, M> {
+  typedef v4i Entry;
+  static constexpr int SLAB = 64;                      // columns of a block
+  __device__ static int kpiece(int p, int lg) { return GluFrag<WT, N, M>::kpiece(p, lg) >> 3; }
+};
+template <int N, int M>
+struct RowsFrag<NM_I8, N, M> : I8Frag<N, M> {
+  typedef v2i Entry;
+  static constexpr int SLAB = 128;
+};
+#endif
+
+// SHORT: 16-bit rows whose K is no multiple of eight (groups of four only);
+// 8-bit rows are whole pieces.
+template <int WT, int N, int M, int NT, bool SHORT>
+__global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a, int units) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NW = kGluWaves;
+  constexpr int U = NT == 1 ? 6 : NT == 2 ? 4 : 2;
+  typedef RowsFrag<WT, N, M> Frag;
+  typedef acc_of<WT> Acc;
+  typedef typename Frag::Entry Entry;
+  constexpr int XB = WT == NM_I8 ? 1 : 2;              // bytes of an activation
+  // a wave's activations of one block, then its sums
+  __shared__ __attribute__((aligned(16))) v4i red[NW][2 * NT][64];
+  __shared__ __attribute__((aligned(16))) Entry table[Frag::TABLE ? 256 : 1];
+  if constexpr (Frag::TABLE) {
+    // column c of set s: the bytes of its k-th kept value where it is the
+    // set's k-th (from 0), else zeros (selector 12)
+    constexpr int ND = sizeof(Entry) / 4;
+    for (int q = threadIdx.x; q < 256 * ND; q += NW * 64) {
+      const int s = q / ND, c = 4 / XB * (q % ND);
+      uint32_t sel = 0;
+#pragma unroll
+      for (int e = 0; e < 4 / XB; ++e) {
+        const int k = __builtin_popcount(s & ((1 << (c + e)) - 1));
+        const bool in = (s >> (c + e) & 1) && k < 8 / XB;
+        const uint32_t b = XB == 2 ? (in ? (uint32_t)((2 * k + 1) << 8 | 2 * k) : 0x0C0Cu) : (in ? (uint32_t)k : 0x0Cu);
+        sel |= b << (8 * XB * e);
+      }
+      reinterpret_cast<uint32_t*>(table)[q] = sel;
+    }
+    __syncthreads();
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int li = lane & 15, lg = lane >> 4;
+  // workgroups 8 apart (neighbours on their XCD) take the units of one row block
+  const int b = blockIdx.x >> 3, q8 = __builtin_amdgcn_readfirstlane(b / units);
+  const int64_t rb = q8 * 8 + (blockIdx.x & 7);
+  const int unit = b - q8 * units;
+  if (rb >= a.g.nRB) return;
+  if (a.zero_rest && a.rows.at) {
+    int first, last;
+    rows_taken(a.rows, first, last);
+    const int rest = first + (int)a.rows.T - last;
+    const int64_t r = rb * 16 + li;
+    for (int i = unit + units * (threadIdx.x >> 4); i < rest; i += units * (NW * 4)) {
+      const int64_t t = i < first ? i : last + (i - first);
+      if (r < a.g.R) {
+        if (a.ydt == NM_F32) static_cast<float*>(a.Y)[t * a.ldy + r] = 0.f;
+        else static_cast<uint16_t*>(a.Y)[t * a.ldy + r] = 0;
+      }
+    }
+  }
+  const RowUnit ru = find_unit<16 * NT, false>(a.rows, unit);
+  if (ru.e < 0) return;
+  const int nKB = (int)a.g.nKB;
+  const int KX = (int)a.g.K;                           // columns of a row that may be read
+  const uint8_t* values = a.values + (int64_t)ru.e * (a.g.nRB * nKB * a.g.vblk);
+  const uint8_t* meta = a.meta + (int64_t)ru.e * (a.g.nRB * nKB * a.g.mblk);
+
+  // activations: load h of row tile j brings rows 8 h .. 8 h + 7 of it, lane l
+  // piece l % 8 (16 bytes) of row 8 h + l / 8; rows past the expert's last
+  // repeat it (their results are not stored).  A 16-bit row's last piece may
+  // hold fewer than eight columns: it is read as the row's last eight and
+  // shifted, so nothing past the row is read.
+  const int piece = lane & 7;
+  const int short_by = SHORT ? 8 - (KX & 7) : 0;
+  const uint8_t* xr[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xr[j][h] = static_cast<const uint8_t*>(a.X) +
+                 (int64_t)min(ru.row + 16 * j + 8 * h + (lane >> 3), ru.end - 1) * (a.ldx * XB) + 16 * piece;
+  uint8_t* const xs = reinterpret_cast<uint8_t*>(&red[wave][0][0]);
+  const int put = (lane >> 3) * 128 + 16 * (piece ^ (lane >> 3));
+  const int get0 = li * 128 + 16 * (Frag::kpiece(0, lg) ^ (li & 7));
+  const int get1 = li * 128 + 16 * (Frag::kpiece(1, lg) ^ (li & 7));
+  Acc acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = Acc{0, 0, 0, 0};
+
+  for (int b0 = wave; b0 < nKB; b0 += NW * U) {
+    Frag f[U];
+    v4i x[U][NT][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int kb = min(b0 + NW * i, nKB - 1);        // past the end: a block read again, not used
+      f[i].load(values, meta, rb * nKB + kb, li, lg);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = kb * Frag::SLAB + 16 / XB * piece;
+          x[i][j][h] = v4i{0, 0, 0, 0};
+          if (k < KX) x[i][j][h] = load16(xr[j][h] + kb * 128 - (SHORT && k + 8 > KX ? 2 * short_by : 0));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (b0 + NW * i < nKB) {
+        if (SHORT && b0 + NW * i == nKB - 1) {
+          const bool last = (b0 + NW * i) * Frag::SLAB + 8 * piece + 8 > KX;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[i][j][h] = last ? shift_out(x[i][j][h], short_by) : x[i][j][h];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) *reinterpret_cast<v4i*>(xs + 2048 * j + 1024 * h + put) = x[i][j][h];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const v4i x0 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get0);
+          const v4i x1 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get1);
+          acc[j] = f[i].mul(x0, x1, acc[j], table);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) red[wave][2 * j][lane] = __builtin_bit_cast(v4i, acc[j]);
+  __syncthreads();
+  for (int q = threadIdx.x; q < 256 * NT; q += NW * 64) {
+    const int row = q & 15, tok = q >> 4;              // row tok % 16 of tile tok / 16
+    const int ln = 16 * (row >> 2) + (tok & 15), v = row & 3, j = tok >> 4;
+    const int64_t r = rb * 16 + row, t = ru.row + tok;
+    if (r >= a.g.R || t >= ru.end) continue;
+    float y;
+    if constexpr (WT == NM_I8) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) sum += reinterpret_cast<const int*>(&red[w][2 * j][ln])[v];
+      y = (float)sum * a.xscale[t] * a.wscale[ru.e * a.g.R + r];
+      if (a.bias) y += a.bias[ru.e * a.g.R + r];
+      if (a.act == NM_ACT_GELU) y = gelu_f32(y);
+    } else {
+      y = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) y += reinterpret_cast<const float*>(&red[w][2 * j][ln])[v];
+    }
+    const int64_t o = t * a.ldy + r;
+    if constexpr (WT == NM_I8) {
+      if (a.ydt == NM_F32) static_cast<float*>(a.Y)[o] = y;
+      else if (a.ydt == NM_F16) static_cast<uint16_t*>(a.Y)[o] = (uint16_t)pack_16x2<NM_F16>(y, 0.f);
+      else static_cast<uint16_t*>(a.Y)[o] = (uint16_t)pack_16x2<NM_BF16>(y, 0.f);
+    } else {
+      static_cast<uint16_t*>(a.Y)[o] = (uint16_t)pack_16x2<WT>(y, 0.f);
+    }
+  }
+#endif
+}
+
+template <int WT, int N, int M, bool SHORT>
+hipError_t launch_rows_decode_rows(const RowsArgs& a, hipStream_t s) {
+  const int64_t T = a.rows.T, E = a.rows.E;
+  // tiles of 16 rows a workgroup takes: those an expert has as a mean
+  const int64_t mean = (T + std::min(T, E) - 1) / std::min(T, E);
+  const int nt = stream_tiles(a.g.nRB * std::min(T, E), mean);
+  const int64_t units = units_most(T, E, 16 * nt);
+  const dim3 grid((unsigned)((a.g.nRB + 7) / 8 * 8 * units)), block(kGluWaves * 64);
+  if (nt == 1)
+    hipLaunchKernelGGL((rows_decode_kernel<WT, N, M, 1, SHORT>), grid, block, 0, s, a, (int)units);
+  else if (nt == 2)
+    hipLaunchKernelGGL((rows_decode_kernel<WT, N, M, 2, SHORT>), grid, block, 0, s, a, (int)units);
+  else
+    hipLaunchKernelGGL((rows_decode_kernel<WT, N, M, 4, SHORT>), grid, block, 0, s, a, (int)units);
+  return hipGetLastError();
+}
+
+template <int WT, int N, int M>
+hipError_t launch_rows_decode_nm(const RowsArgs& a, hipStream_t s) {
+  if constexpr (M == 4 && WT != NM_I8)
+    if (a.g.K % 8) return launch_rows_decode_rows<WT, N, M, true>(a, s);
+  return launch_rows_decode_rows<WT, N, M, false>(a, s);
+}
+
+template <int WT>
+hipError_t launch_rows_decode_wt(const RowsArgs& a, hipStream_t s) {
+  switch (a.g.M * 16 + a.g.N) {
+    case 4 * 16 + 1: return launch_rows_decode_nm<WT, 1, 4>(a, s);
+    case 4 * 16 + 2: return launch_rows_decode_nm<WT, 2, 4>(a, s);
+    case 4 * 16 + 3: return launch_rows_decode_nm<WT, 3, 4>(a, s);
+    case 4 * 16 + 4: return launch_rows_decode_nm<WT, 4, 4>(a, s);
+    case 8 * 16 + 1: return launch_rows_decode_nm<WT, 1, 8>(a, s);
+    case 8 * 16 + 2: return launch_rows_decode_nm<WT, 2, 8>(a, s);
+    case 8 * 16 + 3: return launch_rows_decode_nm<WT, 3, 8>(a, s);
+    case 8 * 16 + 4: return launch_rows_decode_nm<WT, 4, 8>(a, s);
+    case 8 * 16 + 5: return launch_rows_decode_nm<WT, 5, 8>(a, s);
+    case 8 * 16 + 6: return launch_rows_decode_nm<WT, 6, 8>(a, s);
+    case 8 * 16 + 7: return launch_rows_decode_nm<WT, 7, 8>(a, s);
+    case 8 * 16 + 8: return launch_rows_decode_nm<WT, 8, 8>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+}  // namespace nm

@@ -37,6 +37,8 @@
 // gradients' items changed nothing at 2048 tokens.)
 #pragma once
 
+#include <algorithm>
+
 #include "nm_tile_common.hpp"
 
 namespace nm {
@@ -75,10 +77,16 @@ __device__ __forceinline__ v4f mfma_16(v4i a, v4i b, v4f c) {
 }
 #endif
 
+constexpr bool grouped_op(int op) { return op == TILE_ROWS || op == TILE_COLS; }
+template <int OP>
+using tile_args = typename std::conditional<grouped_op(OP), RowsTile, TileArgs>::type;
+
 template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
 __global__ void __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
-tile_kernel(TileArgs a, TileList list, TileList list2) {
+tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool EROWS = OP == TILE_ROWS, COLS = OP == TILE_COLS, GROUPED = grouped_op(OP);
+  typedef typename std::conditional<ET == TILE_I8, v4i, v4f>::type Acc;
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 tiles of a wave
   constexpr bool MX = ET == TILE_MX;
@@ -96,16 +104,23 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
   constexpr int RJ = 8 * NW;                            // rows one load of every wave covers
   static_assert(BM % RJ == 0 && BN % RJ == 0, "every load of one operand");
   static_assert(!GLU || HB % RJ == 0 || RJ % (2 * HB) == 0, "a wave's load has rows of one weight");
-  static_assert(NS * STAGE <= 160 * 1024, "LDS");
+  constexpr int TABLE = rows_table_bytes(GROUPED, kRowsTable);
+  static_assert(NS * STAGE + TABLE <= 160 * 1024, "LDS");
   static_assert(!MX || !GLU || HB % 32 == 0, "whole scale units per half");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE + TABLE];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
 
-  const TileWalk<BACK> walk(list, list2, a.w.lead);
+  const auto walk = [&]() {
+    if constexpr (GROUPED)
+      return RowsWalk<BM, COLS, kRowsTable>(a, list.mt, list.nt, reinterpret_cast<int*>(lds + NS * STAGE));
+    else
+      return TileWalk<BACK>(list, list2, a.w.lead);
+  }();
+  if constexpr (EROWS) zero_other_rows<OUT>(a, walk.row_at);
   if (walk.count <= 0) return;
 
   // ---- operand loads: load d fills LDS rows 8 d .. 8 d + 7, lane l row
@@ -127,8 +142,8 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
   };
   // pieces past the end of a row, in the last slab: an offset no resource holds
   // (TILE_BACK: rows of whole slabs)
-  const int cut_a = !BACK && (a.ka & 7) && piece >= (a.ka & 7) ? (int)0x80000000 : 0;
-  const int cut_b = !BACK && (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
+  const int cut_a = !BACK && !COLS && (a.ka & 7) && piece >= (a.ka & 7) ? (int)0x80000000 : 0;
+  const int cut_b = !BACK && !GROUPED && (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
 
   // the load cursor: work item, its resources, next slab
   int ck = 0, cs, ce, voff[NL];
@@ -136,22 +151,30 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
   // (always inlined: a call would keep the cursor, and what it refers to, in memory)
   auto cursor_item = [&](int k) __attribute__((always_inline)) {
     const TileItem it = walk.item(k);
-    const int64_t m0 = (int64_t)it.m * BM, n0 = (int64_t)it.n * BNO;
+    const int64_t m0 = EROWS ? (int64_t)it.row : (int64_t)it.m * BM, n0 = (int64_t)it.n * BNO;
     auto tile_rsrc = [&](const uint8_t* p, int64_t row0, int64_t ld) {
       const v4i r = make_rsrc(p + row0 * ld, 0x7fffffff);
       return v4i{scalar(r[0]), scalar(r[1]), r[2], r[3]};
     };
     const bool grad = BACK && it.batch;                 // a weight gradient
-    const int64_t Mr = grad ? a.w.Mr : a.Mr, Nr = grad ? a.w.Nr : a.Nr;
+    const int64_t Mr = EROWS ? (int64_t)it.end : grad ? a.w.Mr : a.Mr, Nr = grad ? a.w.Nr : a.Nr;
     const int64_t lda = grad ? a.w.ld : a.lda, ldb = grad ? a.w.ld : a.ldb;
     const int mlast = (int)min(Mr - m0, (int64_t)BM) - 1, nlast = (int)min(Nr - n0, (int64_t)BNO) - 1;
     static_for<0, NL>([&](auto jc) {
       constexpr int j = decltype(jc)::value;
-      voff[j] = j < NLA ? min(load_row(jc), mlast) * (int)lda + 16 * piece
-                        : min(load_row(jc), nlast) * (int)ldb + 16 * piece;
+      if constexpr (EROWS && j >= NLA) {                 // blocks of 16 rows
+        const int row = min(load_row(jc), nlast);
+        voff[j] = (row >> 4) * (a.nslab * 2048) + (row & 15) * 128 + 16 * piece;
+      } else {
+        voff[j] = j < NLA ? min(load_row(jc), mlast) * (int)lda + 16 * piece
+                          : min(load_row(jc), nlast) * (int)ldb + 16 * piece;
+      }
     });
     ra = tile_rsrc(grad ? (it.batch > 1 ? a.w.A[1] : a.w.A[0]) : a.A, m0, lda);
-    rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], n0, ldb);
+    if constexpr (EROWS)
+      rb0 = tile_rsrc(a.B[0], (int64_t)it.batch * ((a.Nr + 15) / 16) + n0 / 16, (int64_t)a.nslab * 2048);
+    else
+      rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], n0, ldb);
     if constexpr (GLU && !SPAN) rb1 = tile_rsrc(a.B[1], n0, ldb);
     if constexpr (MX) {
       // unit u of a stage: LDS rows 32 u ..; row groups past the end repeat the last one
@@ -180,7 +203,7 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
     constexpr int j = decltype(jc)::value;
     uint8_t* sp = lds + st * STAGE;
     if constexpr (j < NL) {
-      const int so = scalar(cs * 128);
+      const int so = scalar(cs * (EROWS && j >= NLA ? 2048 : 128));
       const uint32_t dst = lds_addr(sp + 1024 * (wave + NW * j));
       constexpr bool UP = GLU && !SPAN && ((RJ * j - BM) / HB & 1);
       lds_dma16(j < NLA ? ra : (UP ? rb1 : rb0), dst, voff[j] | (j < NLA ? ca : cb), so);
@@ -193,7 +216,8 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
   // part p of NP of the cursor slab's loads into stage st
   auto issue_part = [&](auto pc, auto npc, int st) {
     constexpr int P = decltype(pc)::value, NP = decltype(npc)::value;
-    const int ca = BACK || cs + 1 < a.nslab ? 0 : cut_a, cb = BACK || cs + 1 < a.nslab ? 0 : cut_b;
+    const int ca = BACK || COLS || cs + 1 < a.nslab ? 0 : cut_a;
+    const int cb = BACK || GROUPED || cs + 1 < a.nslab ? 0 : cut_b;
     static_for<NLT * P / NP, NLT * (P + 1) / NP>([&](auto jc) { issue_one(jc, st, ca, cb); });
   };
   // past the last work item the cursor stays on its last slab: the loads fill
@@ -207,12 +231,12 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
     }
   };
 
-  v4f acc[TN][TM];
+  Acc acc[TN][TM];
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < TM; ++j) acc[i][j] = Acc{0, 0, 0, 0};
   };
   clear();
 
@@ -253,6 +277,8 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
       const int j = i & 1 ? TM - 1 - q : q;
       if constexpr (MX)
         acc[i][j] = mfma_mx(f.b[i], f.a[j], acc[i][j], c.b[i / 2], 2 * (i & 1) + kk, c.a[j / 2], 2 * (j & 1) + kk);
+      else if constexpr (ET == TILE_I8)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[i], f.a[j], acc[i][j], 0, 0, 0);
       else
         acc[i][j] = mfma_16<ET>(f.b[i], f.a[j], acc[i][j]);
     }
@@ -310,7 +336,11 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
       c0 = c1;
       st = nx;
     }
-    tile_epilogue<OP, OUT, TM, TN>(a, it, (int64_t)it.m * BM + wm * TM * 16, (int64_t)it.n * BNO + wn * (BNO / WN), acc);
+    if constexpr (GROUPED)
+      rows_epilogue<OP, OUT, TM, TN>(a, it, (EROWS ? it.row : it.m * BM) + wm * TM * 16,
+                                     (int64_t)it.n * BNO + wn * (BNO / WN), acc);
+    else
+      tile_epilogue<OP, OUT, TM, TN>(a, it, (int64_t)it.m * BM + wm * TM * 16, (int64_t)it.n * BNO + wn * (BNO / WN), acc);
     clear();
   }
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));           // nothing lands in LDS after this
@@ -318,8 +348,19 @@ tile_kernel(TileArgs a, TileList list, TileList list2) {
 }
 
 template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
-hipError_t launch_tile_cfg(const TileArgs& a, hipStream_t s) {
+hipError_t launch_tile_cfg(const tile_args<OP>& a, hipStream_t s) {
   constexpr int BNO = OP == TILE_GLU ? BN / 2 : BN;
+  if constexpr (grouped_op(OP)) {
+    // as many tiles as there could be: the host does not know the experts' rows
+    TileList l{};
+    l.mt = (int)((a.Mr + BM - 1) / BM);
+    l.nt = (int)((a.Nr + BN - 1) / BN);
+    const int64_t most = (OP == TILE_COLS ? (int64_t)l.mt * a.rows.E : units_most(a.rows.T, a.rows.E, BM)) * l.nt;
+    const int grid = 8 * tile_slots((int)std::min<int64_t>((most + 7) / 8, 1 << 20));
+    hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s,
+                       a, l, l);
+    return hipGetLastError();
+  }
   const bool back = OP == TILE_BACK;
   const TileList list = tile_list(a.Mr, a.Nr, BM, BNO, a.split, a.sps, a.nslab, back && !a.C ? 0 : 1);
   const TileList list2 = tile_list(a.w.Mr, a.w.Nr, BM, BNO, 1, a.w.nslab, a.w.nslab, back && a.w.C[0] ? 2 : 0);
@@ -330,7 +371,7 @@ hipError_t launch_tile_cfg(const TileArgs& a, hipStream_t s) {
 }
 
 template <int ET, int OP, int OUT>
-hipError_t launch_tile_op(const TileArgs& a, hipStream_t s) {
+hipError_t launch_tile_op(const tile_args<OP>& a, hipStream_t s) {
   switch (a.shape) {
     // wave tiles of 128 tokens x 64 rows of B keep one operand for eight
     // products (22016 x 4096 x 2048, bf16: 290 us against 341 for 64 x 128);

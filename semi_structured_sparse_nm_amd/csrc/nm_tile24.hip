@@ -54,7 +54,7 @@ double glu_tile24_time(int64_t T, int64_t R, int64_t nslab, int cus, int* shape)
 // tokens in X's own rows (a.X, a.ldx: 16-byte pieces), both weights 2:4
 hipError_t launch_glu_tile24(const GluArgs& g, hipStream_t s) {
   Tile24Args p{};
-  TileArgs& a = p.t;
+  TileArgs& a = p;
   a.A = static_cast<const uint8_t*>(g.X);
   a.lda = g.ldx * 2;
   a.Mr = g.T;

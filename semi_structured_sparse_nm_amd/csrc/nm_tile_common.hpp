@@ -1,7 +1,9 @@
 // What the tile kernels share: the list of work items, the epilogue.
 #pragma once
 
-#include "nm_ffn.hpp"
+#include <type_traits>
+
+#include "nm_rows.hpp"
 
 namespace nm {
 
@@ -49,9 +51,101 @@ struct TileItem {
   int m, n;        // tile
   int batch, ks;   // product, slice of the reduction
   int s0, s1;      // its slabs
+  int row, end;    // grouped rows: the tile's first row, its expert's end
 };
 
+// Bytes of LDS a kernel of grouped rows keeps its table of boundaries in.
+constexpr int rows_table_bytes(bool grouped, int entries) { return grouped ? 8 * entries : 0; }
+
 #if defined(__HIP_DEVICE_COMPILE__)
+// The items of one workgroup of a product of grouped rows, from the table of
+// the experts' rows that it builds in LDS (`table`, 2 * TAB words): the row
+// tiles of BM rows of every expert times the column tiles, expert by expert
+// (an XCD's run of the list meets few experts' weights), dealt as TileWalk
+// does.  COLS: every expert's mt x nt tiles, its slabs of 64 rows the
+// reduction.
+template <int BM, bool COLS, int TAB>
+struct RowsWalk {
+  const int* row_at;
+  const int* unit_at;
+  int E, mt, nt, x, j, step, per, count, nslab;
+  __device__ __forceinline__ RowsWalk(const RowsTile& a, int mt_, int nt_, int* table) {
+    int* rows = table;
+    int* units = table + TAB;
+    if (threadIdx.x < 64) {
+      row_boundaries<COLS ? 64 : BM, COLS>(a.rows, [&](int i, int, int at, int u, int) {
+        if (i <= a.rows.E) {
+          rows[i] = at;
+          units[i] = u;
+        }
+        return false;
+      });
+    }
+    __syncthreads();
+    row_at = rows;
+    unit_at = units;
+    E = a.rows.E;
+    mt = mt_;
+    nt = nt_;
+    nslab = a.nslab;
+    x = blockIdx.x & 7;
+    j = blockIdx.x >> 3;
+    step = gridDim.x >> 3;
+    const int total = COLS ? E * mt * nt : scalar(unit_at[E]) * nt;
+    per = (total + 7) / 8;
+    const int n = min(per, total - x * per) - j;
+    count = n > 0 ? scalar((n + step - 1) / step) : 0;
+  }
+  __device__ __forceinline__ TileItem item(int k) const {
+    int L = x * per + j + k * step;
+    TileItem t;
+    int e, rows_m;
+    if constexpr (COLS) {
+      e = scalar(L / (mt * nt));
+      L -= e * mt * nt;
+      rows_m = mt;
+    } else {
+      // the last expert whose first unit is not behind the item's
+      const int unit = scalar(L / nt), lane = threadIdx.x & 63;
+      e = -1;
+      for (int c = 0; c <= E; c += 64)
+        e += __popcll(__ballot(c + lane <= E && unit_at[min(c + lane, E)] <= unit));
+      e = scalar(e);
+      const int first = scalar(unit_at[e]);
+      L -= first * nt;
+      rows_m = scalar(unit_at[e + 1]) - first;
+    }
+    const int gm = min(rows_m, 8);
+    const int grp = scalar(L / (gm * nt));
+    const int in = L - grp * gm * nt;
+    const int rows = min(gm, rows_m - grp * gm);
+    t.batch = e;
+    t.ks = 0;
+    t.n = scalar(in / rows);
+    t.m = grp * gm + in - t.n * rows;
+    t.end = scalar(row_at[e + 1]);
+    t.row = scalar(row_at[e]) + t.m * BM;
+    t.s0 = COLS ? scalar(unit_at[e]) : 0;
+    t.s1 = COLS ? scalar(unit_at[e + 1]) : nslab;
+    return t;
+  }
+};
+
+// zeros in the rows of C that belong to no expert, by all workgroups
+template <int OUT>
+__device__ __forceinline__ void zero_other_rows(const RowsTile& a, const int* row_at) {
+  if (!a.zero_rest) return;
+  const int first = scalar(row_at[0]), last = scalar(row_at[a.rows.E]);
+  const int rest = first + (int)a.rows.T - last;
+  for (int i = blockIdx.x; i < rest; i += gridDim.x) {
+    const int64_t o = (int64_t)(i < first ? i : last + (i - first)) * a.ldc;
+    for (int64_t n = threadIdx.x; n < a.Nr; n += blockDim.x) {
+      if constexpr (OUT == NM_F32) static_cast<float*>(a.C)[o + n] = 0.f;
+      else static_cast<uint16_t*>(a.C)[o + n] = 0;
+    }
+  }
+}
+
 // The items of one workgroup, of `step` on its XCD: every step-th of the XCD's
 // run.  TWO: of list l, then of l2 (their products count from 1).  Where l
 // leaves q workgroups one item more than the others, those others take `lead`
@@ -196,6 +290,60 @@ __device__ __forceinline__ void tile_rows(void* C, int64_t ldc, int64_t Mr, int6
       if (m < Mr) store_pair<OUT>(C, m * ldc, n0 + 16 * i, Nr, lq, y[0], y[1], whole);
     }
   }
+}
+
+// One wave's tiles of 8-bit products as rows of C: integer sums, converted once,
+// times the row's scale, times the channel's, each product rounded to binary32
+// (bias, activation and the rounding to the output's type follow).
+template <int OUT, int TM, int TN>
+__device__ __forceinline__ void tile_rows_i8(const RowsTile& a, const TileItem& it, int64_t m0, int64_t n0,
+                                             const v4i (&acc)[TN][TM]) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+  const bool whole = whole_pieces(a.C, a.ldc);
+  const float* wscale = a.wscale + (int64_t)it.batch * a.Nr;
+  const float* bias = a.bias ? a.bias + (int64_t)it.batch * a.Nr : nullptr;
+  float sx[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) sx[j] = a.xscale[min(m0 + 16 * j + li, (int64_t)it.end - 1)];
+#pragma unroll
+  for (int i = 0; i < TN; i += 2) {
+    float sw[2][4], b[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t n = n0 + 16 * (i + e) + 4 * lq + v;
+        sw[e][v] = n < a.Nr ? wscale[n] : 0.f;
+        b[e][v] = bias && n < a.Nr ? bias[n] : 0.f;
+      }
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t m = m0 + 16 * j + li;
+      float y[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          y[e][v] = (float)acc[i + e][j][v] * sx[j] * sw[e][v] + b[e][v];
+          y[e][v] = a.act == NM_ACT_GELU ? gelu_f32(y[e][v]) : y[e][v];
+        }
+      __builtin_amdgcn_sched_barrier(0);                // one output's temporaries at a time
+      if (m < it.end) store_pair<OUT>(a.C, m * a.ldc, n0 + 16 * i, a.Nr, lq, y[0], y[1], whole);
+    }
+  }
+}
+
+// Epilogue of one wave's tiles of grouped rows.
+template <int OP, int OUT, int TM, int TN, class Acc>
+__device__ __forceinline__ void rows_epilogue(const RowsTile& a, const TileItem& it, int64_t m0, int64_t n0,
+                                              const Acc (&acc)[TN][TM]) {
+  if constexpr (OP == TILE_COLS)
+    tile_rows<true, OUT, TM, TN>(static_cast<uint16_t*>(a.C) + it.batch * a.es, a.ldc, a.Mr, a.Nr, nullptr,
+                                 NM_ACT_NONE, a.mask + it.batch * a.Mr * a.ldm, a.ldm, m0, n0, acc);
+  else if constexpr (std::is_same<Acc, v4i>::value)
+    tile_rows_i8<OUT, TM, TN>(a, it, m0, n0, acc);
+  else
+    tile_rows<false, OUT, TM, TN>(a.C, a.ldc, it.end, a.Nr, nullptr, NM_ACT_NONE, nullptr, 0, m0, n0, acc);
 }
 
 // Epilogue of one wave's tiles.  TILE_GLU: tiles i < TN / 2 are gate, the
