@@ -62,8 +62,10 @@ constexpr int rows_table_bytes(bool grouped, int entries) { return grouped ? 8 *
 // the experts' rows that it builds in LDS (`table`, 2 * TAB words): the row
 // tiles of BM rows of every expert times the column tiles, expert by expert
 // (an XCD's run of the list meets few experts' weights), dealt as TileWalk
-// does.  COLS: every expert's mt x nt tiles, its slabs of 64 rows the
-// reduction.
+// does.  COLS: every expert's mt x nt tiles, its slabs of 64 rows the reduction.
+// They last as long as the expert has rows, so all XCDs take a part of every
+// expert's (eight experts of 4096 rows, 2048 x 4096: 163 us where each XCD had
+// an expert of its own, about 100 so).
 template <int BM, bool COLS, int TAB>
 struct RowsWalk {
   const int* row_at;
@@ -93,11 +95,12 @@ struct RowsWalk {
     step = gridDim.x >> 3;
     const int total = COLS ? E * mt * nt : scalar(unit_at[E]) * nt;
     per = (total + 7) / 8;
-    const int n = min(per, total - x * per) - j;
-    count = n > 0 ? scalar((n + step - 1) / step) : 0;
+    const int n = COLS ? total - x * step - j : min(per, total - x * per) - j;
+    const int every = COLS ? 8 * step : step;
+    count = n > 0 ? scalar((n + every - 1) / every) : 0;
   }
   __device__ __forceinline__ TileItem item(int k) const {
-    int L = x * per + j + k * step;
+    int L = COLS ? (8 * k + x) * step + j : x * per + j + k * step;
     TileItem t;
     int e, rows_m;
     if constexpr (COLS) {
