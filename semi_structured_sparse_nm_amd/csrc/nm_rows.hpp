@@ -36,6 +36,7 @@ struct RowsArgs {
   const void* X;             // 16-bit values, or 8-bit elements
   int64_t ldx;
   const float* xscale;       // 8 bits: [T]
+  int xdt;                   // NM_I8, or (streamed, rows_decode_quantizes) the type the rows are quantised from
   const float* wscale;       // 8 bits: [E][R]
   const float* bias;         // 8 bits: [E][R] or nullptr
   int act;
@@ -54,6 +55,15 @@ inline int64_t units_most(int64_t T, int64_t E, int64_t u) {
 
 // few rows an expert: the packed weights streamed once per unit of 16 rows or more
 hipError_t launch_rows_decode(const RowsArgs& a, hipStream_t s);
+// Whether the streamed 8-bit product quantises T rows of E experts itself: what
+// a workgroup keeps of them fits its LDS, and they are so few that quantising
+// them in every workgroup takes less than a launch.  (One row, 11008 x 4096: 13.3
+// us with a launch for it, 9.7 without; sixteen rows of one expert's 4096
+// columns would take each workgroup 5 us, the launch takes 4.)
+inline bool rows_decode_quantizes(int64_t T, int64_t E, int64_t K) {
+  const int64_t Kp = i8_kp(K), some = T < E ? T : E;
+  return T <= 16 && T * (Kp + 16) <= 48 * 1024 && (T + some - 1) / some * Kp <= 16 * 1024;
+}
 hipError_t launch_rows_decode_i8(const RowsArgs& a, hipStream_t s);
 hipError_t launch_rows_decode_f16(const RowsArgs& a, hipStream_t s);
 hipError_t launch_rows_decode_bf16(const RowsArgs& a, hipStream_t s);
@@ -125,21 +135,23 @@ __device__ __forceinline__ int row_bound(const RowGroups& o, int i) {
   const int64_t v = o.wide ? static_cast<const int64_t*>(o.at)[i] : (int64_t)static_cast<const int32_t*>(o.at)[i];
   return (int)min(max(v, (int64_t)0), o.T);
 }
-__device__ __forceinline__ int wave_scan_max(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    v = lane >= d ? max(v, u) : v;
-  }
-  return v;
+// Inclusive scans over a wave by the vector unit's own lane moves (inside rows of
+// 16 lanes, then a row's last lane to the next one, then lane 31 to the upper
+// half); values are not negative.  By LDS exchanges a scan takes about 700 cycles.
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F&& op) {
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
 }
-__device__ __forceinline__ int wave_scan_add(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    v = lane >= d ? v + u : v;
-  }
-  return v;
+__device__ __forceinline__ int wave_scan_max(int v) {
+  return wave_scan(v, [](int x, int y) { return max(x, y); });
+}
+__device__ __forceinline__ int wave_scan_add(int v) {
+  return wave_scan(v, [](int x, int y) { return x + y; });
 }
 
 // Experts' first rows and first units (of U rows; with LEAST an expert without
@@ -154,16 +166,16 @@ __device__ __forceinline__ void row_boundaries(const RowGroups& o, F&& f) {
   for (int c = 0; c <= o.E; c += 64) {
     const int i = c + lane;
     int v = i <= o.E ? row_bound(o, i) : 0;
-    v = max(wave_scan_max(v, lane), last);
-    int p = __shfl_up(v, 1);
+    v = max(wave_scan_max(v), last);
+    int p = __builtin_amdgcn_update_dpp(0, v, 0x138, 0xf, 0xf, false);   // the lane before
     if (lane == 0) p = c ? last : v;
     int n = (v - p + U - 1) / U;
     if (LEAST && n == 0) n = 1;
     if (i == 0 || i > o.E) n = 0;
-    const int u = wave_scan_add(n, lane) + units;
+    const int u = wave_scan_add(n) + units;
     if (f(i, p, v, u, n)) return;
-    last = __shfl(v, 63);
-    units = __shfl(u, 63);
+    last = __builtin_amdgcn_readlane(v, 63);
+    units = __builtin_amdgcn_readlane(u, 63);
   }
 }
 
@@ -197,8 +209,7 @@ __device__ __forceinline__ void rows_taken(const RowGroups& o, int& first, int& 
   first = row_bound(o, 0);
   last = first;
   for (int i = threadIdx.x & 63; i <= o.E; i += 64) last = max(last, row_bound(o, i));
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) last = max(last, __shfl_xor(last, d));
+  last = __builtin_amdgcn_readlane(wave_scan_max(last), 63);
 }
 #endif
 

@@ -197,12 +197,17 @@ hipError_t multiply(const Weights& w, RowsPath path, const nm::RowsArgs& a, int 
 }
 
 // ---------------------------------------------------------------- 8-bit products
+bool quantizes_inside(const Weights& w, RowsPath path, int64_t T) {
+  return path == ROWS_STREAM && nm::rows_decode_quantizes(T, w.E, w.g.K);
+}
+
 nm_status i8_workspace(const Weights& w, const nm_i8* xq, int64_t T, size_t* bytes) {
   if (!bytes) return NM_EINVAL;
   if (w.dtype != NM_I8) return NM_EUNSUPPORTED;
   const nm_status st = check_sizes(w, T);
   if (st != NM_OK) return st;
-  *bytes = (xq ? 0 : quantized_bytes(T, w.g.K)) + copies_bytes(w, rows_path(w, T));
+  const RowsPath path = rows_path(w, T);
+  *bytes = (xq || quantizes_inside(w, path, T) ? 0 : quantized_bytes(T, w.g.K)) + copies_bytes(w, path);
   return NM_OK;
 }
 
@@ -226,14 +231,23 @@ nm_status i8_product(const Weights& w, const float* w_scale, const nm_i8* xq, co
     if (!float_dtype(xdt) || !aligned(X, (size_t)nm::dtype_bytes(xdt))) return NM_EUNSUPPORTED;
   }
   const RowsPath path = rows_path(w, T);
-  const size_t quant = xq ? 0 : quantized_bytes(T, g.K), need = quant + copies_bytes(w, path);
+  const bool inside = !xq && quantizes_inside(w, path, T);
+  const size_t quant = xq || inside ? 0 : quantized_bytes(T, g.K), need = quant + copies_bytes(w, path);
   if (need && (!workspace || ws_bytes < need)) return NM_EINVAL;
   if (need && !aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
+  const int64_t Kp = nm::i8_kp(g.K);
   nm::RowsArgs a{};
-  if (xq) {
+  a.g = g;
+  a.xdt = NM_I8;
+  a.ldx = Kp;
+  if (inside) {
+    a.X = X;
+    a.ldx = ldx;
+    a.xdt = xdt;
+  } else if (xq) {
     a.X = xq->codes;
     a.xscale = static_cast<const float*>(xq->scales);
   } else {
@@ -243,14 +257,11 @@ nm_status i8_product(const Weights& w, const float* w_scale, const nm_i8* xq, co
     a.X = ws;
     a.xscale = scales;
   }
-  const int64_t Kp = nm::i8_kp(g.K);
-  a.g = g;
-  a.g.K = Kp;                                           // a row's zeros may be read
+  if (!inside) a.g.K = Kp;                              // a row's zeros may be read
   a.wdt = NM_I8;
   a.values = w.values;
   a.meta = w.meta;
   a.rows = rows;
-  a.ldx = Kp;
   a.wscale = w_scale;
   a.bias = bias;
   a.act = act;

@@ -177,14 +177,14 @@ def test_expert_backward_refusals():
 
 
 def test_i8_expert_refusals():
-    def f(w=None, s=P[1], xq=None, X=P[0], ldx=128, xdt=nm.NM_F16, T=5, o=P[2], odt=0, Y=P[3], ldy=40, ydt=nm.NM_F16,
+    def f(w=None, s=P[1], xq=None, X=P[0], ldx=128, xdt=nm.NM_F16, T=50, o=P[2], odt=0, Y=P[3], ldy=40, ydt=nm.NM_F16,
           bias=None, act=0, ws=P[4], wsb=1 << 28):
         w = w or _experts(dt=nm.NM_I8)
         return nm.lib().nm_i8_expert_linear(ctypes.byref(w), s, None if xq is None else ctypes.byref(xq), X, ldx, xdt, T,
                                             o, odt, Y, ldy, ydt, bias, act, 0, ws, wsb, None)
 
     for kw in (dict(s=None), dict(X=None), dict(o=None), dict(Y=None), dict(T=0), dict(ldx=127), dict(ldy=39),
-               dict(ws=None), dict(wsb=10), dict(xq=_i8(6, 128)), dict(xq=_i8(5, 129)),
+               dict(ws=None), dict(wsb=10), dict(xq=_i8(49, 128)), dict(xq=_i8(50, 129)),
                dict(w=_experts(dt=nm.NM_I8, format_version=3))):
         assert f(**kw) == EINVAL, kw
     for kw in (dict(w=_experts()), dict(odt=7), dict(o=P[2] + 2), dict(act=2), dict(xdt=nm.NM_I32), dict(ydt=nm.NM_I8),
@@ -193,7 +193,9 @@ def test_i8_expert_refusals():
     n = ctypes.c_size_t()
     w = _experts(dt=nm.NM_I8)
     g = nm.lib().nm_i8_expert_linear_workspace_size
-    assert g(ctypes.byref(w), None, 5, ctypes.byref(n)) == nm.NM_OK and n.value == 5 * 128 + 128 + 256
+    assert g(ctypes.byref(w), None, 50, ctypes.byref(n)) == nm.NM_OK and n.value == 50 * 128 + 256
+    # few rows: quantised inside the product
+    assert g(ctypes.byref(w), None, 5, ctypes.byref(n)) == nm.NM_OK and n.value == 0
     assert g(ctypes.byref(w), ctypes.byref(_i8(5, 128)), 5, ctypes.byref(n)) == nm.NM_OK and n.value == 0
     assert g(ctypes.byref(_experts()), None, 5, ctypes.byref(n)) == EUNSUP
 
