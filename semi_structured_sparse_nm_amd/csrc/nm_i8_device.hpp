@@ -1,11 +1,13 @@
 // Device parts of the 8-bit rows: shared by the quantiser and the product that
 // quantises its own rows.
 //
-// Nearest element: q = rint(x r), r the reciprocal unit's 1 / scale (1 ulp),
-// is off by at most one, and only where x lies within 2^-15 scale of a border.
-// d = x - q scale is exact in one fused multiply-add there (a multiple of the
-// scale's last place no larger than the scale), so comparing 2 |d| with the
-// scale finds the nearest, and the tie, without a division.
+// Nearest element: the sum of x r (r the reciprocal unit's 1 / scale, 1 ulp) and
+// 1.5 2^23, rounded once, holds in its last bits a whole number q that is off by
+// at most one, and only where x lies within 2^-15 scale of a border.  d = x - q
+// scale is exact in one fused multiply-add there (a multiple of the scale's last
+// place no larger than the scale), so comparing |d| with half the scale finds the
+// nearest without a division; on a tie an odd q is the wrong one, so for odd q the
+// half's predecessor is compared with.
 #pragma once
 
 #include "nm_rows.hpp"
@@ -74,25 +76,32 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   return fmaxf(amax / 127.0f, 0x1p-126f);
 }
 
-// x / s to the nearest whole number, half to even (r: 1 / s within 1 ulp)
-__device__ __forceinline__ float nearest(float x, float s, float r) {
-  const float q = __builtin_rintf(x * r);
-  const float d = __builtin_fmaf(-q, s, x);
-  const float a = 2.0f * __builtin_fabsf(d);
-  const bool odd = (int)q & 1;
-  return a > s || (a == s && odd) ? q + __builtin_copysignf(1.0f, d) : q;
+// x / s to the nearest whole number, half to even, in the low byte (r: 1 / s
+// within 1 ulp, h: the bits of s / 2)
+__device__ __forceinline__ uint32_t nearest_byte(float x, float s, float r, uint32_t h) {
+  const float m = 12582912.0f;                          // 1.5 2^23
+  const float u = __builtin_fmaf(x, r, m);
+  const float d = __builtin_fmaf(m - u, s, x);
+  const uint32_t b = __builtin_bit_cast(uint32_t, u);
+  const float half = __builtin_bit_cast(float, h - (b & 1u));
+  const int step = (__builtin_bit_cast(int, d) >> 31) | 1;
+  return b + (__builtin_fabsf(d) > half ? step : 0);
 }
 
 template <int DT>
 __device__ __forceinline__ v2i codes_of(const Eight<DT>& e, float s, float r) {
   v2i c;
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t h = __builtin_bit_cast(uint32_t, 0.5f * s);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float q[4];
+  for (int i = 0; i < 2; ++i) {
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = nearest(e.value(4 * h + i), s, r);
-    c[h] = (int)pack_rne_i8x4(q[0], q[1], q[2], q[3]);
+    for (int k = 0; k < 4; ++k) q[k] = nearest_byte(e.value(4 * i + k), s, r, h);
+    const uint32_t lo = __builtin_amdgcn_perm(q[1], q[0], 0x0C0C0400u);
+    c[i] = (int)__builtin_amdgcn_perm(__builtin_amdgcn_perm(q[3], q[2], 0x0C0C0400u), lo, 0x05040100u);
   }
+#endif
   return c;
 }
 

@@ -122,16 +122,36 @@ struct RowsFrag<NM_I8, N, M> : I8Frag<N, M> {
 };
 #endif
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// Zeros in `n` outputs from r0 on of every units-th of the rows that belong to
+// no expert.  (Behind the product: it waits for the offsets once more.)
+__device__ __forceinline__ void zero_rows_of_none(const RowsArgs& a, int64_t r0, int n, int unit, int units) {
+  if (!a.zero_rest) return;
+  int first, last;
+  rows_taken(a.rows, first, last);
+  const int rest = first + (int)a.rows.T - last;
+  const int64_t r1 = min(r0 + n, a.g.R);
+  for (int i = unit + units * (threadIdx.x >> 4); i < rest; i += units * (kGluWaves * 4)) {
+    const int64_t t = i < first ? i : last + (i - first);
+    for (int64_t r = r0 + (threadIdx.x & 15); r < r1; r += 16) {
+      if (a.ydt == NM_F32) static_cast<float*>(a.Y)[t * a.ldy + r] = 0.f;
+      else static_cast<uint16_t*>(a.Y)[t * a.ldy + r] = 0;
+    }
+  }
+}
+#endif
+
 // SHORT: 16-bit rows whose K is no multiple of eight (groups of four only);
 // 8-bit rows are whole pieces.  XQ: NM_I8, or the type of rows that the
 // workgroup quantises itself, first their maxima, then their elements into LDS,
-// while its first blocks are on their way.
-template <int WT, int N, int M, int NT, bool SHORT, int XQ>
+// while its first blocks are on their way.  GROUPED: rows with offsets; else one
+// expert has them all.
+template <int WT, int N, int M, int NT, bool SHORT, int XQ, bool GROUPED>
 __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a, int units, int ks) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = kGluWaves;
-  constexpr int U = NT == 4 ? 2 : 4;
   constexpr bool QX = XQ != NM_I8;
+  constexpr int U = QX ? 8 : NT == 4 ? 2 : 4;
   typedef RowsFrag<WT, N, M> Frag;
   typedef acc_of<WT> Acc;
   typedef typename Frag::Entry Entry;
@@ -170,21 +190,12 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
   const int64_t rb0 = (int64_t)(q8 * 8 + (blockIdx.x & 7)) * nblk;
   const int unit = b - q8 * units;
   if (rb0 >= a.g.nRB) return;
-  if (a.zero_rest && a.rows.at) {
-    int first, last;
-    rows_taken(a.rows, first, last);
-    const int rest = first + (int)a.rows.T - last;
-    const int64_t r0 = rb0 * 16, r1 = min(r0 + 16 * nblk, a.g.R);
-    for (int i = unit + units * (threadIdx.x >> 4); i < rest; i += units * (NW * 4)) {
-      const int64_t t = i < first ? i : last + (i - first);
-      for (int64_t r = r0 + li; r < r1; r += 16) {
-        if (a.ydt == NM_F32) static_cast<float*>(a.Y)[t * a.ldy + r] = 0.f;
-        else static_cast<uint16_t*>(a.Y)[t * a.ldy + r] = 0;
-      }
-    }
+  RowUnit ru = {0, unit * (16 * NT), 0, (int)a.rows.T};
+  if constexpr (GROUPED) ru = find_unit<16 * NT, false>(a.rows, unit);
+  if (ru.e < 0) {
+    if constexpr (GROUPED) zero_rows_of_none(a, rb0 * 16, 16 * nblk, unit, units);
+    return;
   }
-  const RowUnit ru = find_unit<16 * NT, false>(a.rows, unit);
-  if (ru.e < 0) return;
   const int nrows = min(ru.end - ru.row, 16 * NT);
   const int nKB = (int)a.g.nKB;
   const int KX = (int)a.g.K;                           // columns of a row that may be read
@@ -373,17 +384,20 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
     float y;
     if constexpr (WT == NM_I8) {
       int sum = 0;
+      // (all eight reads at once: of no more than ks waves)
 #pragma unroll
       for (int w = 0; w < NW; ++w)
-        if (w < ks) sum += reinterpret_cast<const int*>(&red[(blk << lks) + w][2 * j][ln])[v];
+        sum += reinterpret_cast<const int*>(&red[(blk << lks) + (w & (ks - 1))][2 * j][ln])[v] & (w < ks ? -1 : 0);
       y = (float)sum * xscale[tok] * sw;
       if (a.bias) y += bias;
       if (a.act == NM_ACT_GELU) y = gelu_f32(y);
     } else {
       y = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
-        if (w < ks) y += reinterpret_cast<const float*>(&red[(blk << lks) + w][2 * j][ln])[v];
+      for (int w = 0; w < NW; ++w) {
+        const float part = reinterpret_cast<const float*>(&red[(blk << lks) + (w & (ks - 1))][2 * j][ln])[v];
+        y += w < ks ? part : 0.f;
+      }
     }
     const int64_t o = t * a.ldy + r;
     if constexpr (WT == NM_I8) {
@@ -394,15 +408,16 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
       static_cast<uint16_t*>(a.Y)[o] = (uint16_t)pack_16x2<WT>(y, 0.f);
     }
   }
+  if constexpr (GROUPED) zero_rows_of_none(a, rb0 * 16, 16 * nblk, unit, units);
 #endif
 }
 
-// Waves of a workgroup along K: as many as find four blocks each, so that short
-// reductions have fewer and longer workgroups; but no fewer workgroups than
-// compute units.
+// Waves of a workgroup along K: as many as find eight blocks each (what a wave does
+// once, before and after them, is 300 vector and 350 scalar instructions), but no
+// fewer workgroups than compute units.
 inline int waves_along_k(const RowsArgs& a, int64_t units) {
   int ks = kGluWaves;
-  while (ks > 1 && a.g.nKB < 4 * ks && a.g.nRB * units * (ks / 2) / kGluWaves >= device_cu_count()) ks /= 2;
+  while (ks > 1 && a.g.nKB < 8 * ks && a.g.nRB * units * (ks / 2) / kGluWaves >= device_cu_count()) ks /= 2;
   return ks;
 }
 
@@ -419,15 +434,22 @@ hipError_t launch_rows_decode_rows(const RowsArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(kernel, grid, block, (unsigned)lds, s, a, (int)units, ks);
     return hipGetLastError();
   };
-  if constexpr (WT == NM_I8) {
-    const int64_t lds = T * (a.g.nKB * 128 + 16);
-    if (a.xdt == NM_F16) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_F16>, lds);
-    if (a.xdt == NM_BF16) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_BF16>, lds);
-    if (a.xdt == NM_F32) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_F32>, lds);
-  }
-  if (nt == 1) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_I8>, 0);
-  if (nt == 2) return go(rows_decode_kernel<WT, N, M, 2, SHORT, NM_I8>, 0);
-  return go(rows_decode_kernel<WT, N, M, 4, SHORT, NM_I8>, 0);
+  auto pick = [&](auto grouped) {
+    constexpr bool G = decltype(grouped)::value;
+    if constexpr (WT == NM_I8) {
+      const int64_t lds = T * (a.g.nKB * 128 + 16);
+      if (a.xdt == NM_F16) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_F16, G>, lds);
+      if (a.xdt == NM_BF16) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_BF16, G>, lds);
+      if (a.xdt == NM_F32) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_F32, G>, lds);
+    }
+    if (nt == 1) return go(rows_decode_kernel<WT, N, M, 1, SHORT, NM_I8, G>, 0);
+    if (nt == 2) return go(rows_decode_kernel<WT, N, M, 2, SHORT, NM_I8, G>, 0);
+    return go(rows_decode_kernel<WT, N, M, 4, SHORT, NM_I8, G>, 0);
+  };
+  // (only 8-bit products come without offsets)
+  if constexpr (WT == NM_I8)
+    if (!a.rows.at) return pick(ic<0>());
+  return pick(ic<1>());
 }
 
 template <int WT, int N, int M>
