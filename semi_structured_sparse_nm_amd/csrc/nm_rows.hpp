@@ -68,6 +68,13 @@ hipError_t launch_rows_decode_i8(const RowsArgs& a, hipStream_t s);
 hipError_t launch_rows_decode_f16(const RowsArgs& a, hipStream_t s);
 hipError_t launch_rows_decode_bf16(const RowsArgs& a, hipStream_t s);
 
+// more rows an expert: the packed weights streamed once per 64 or 128 rows, which
+// the workgroup's waves share (tm: 4 or 8 tiles of 16)
+hipError_t launch_rows_wide(const RowsArgs& a, int tm, hipStream_t s);
+hipError_t launch_rows_wide_i8(const RowsArgs& a, int tm, hipStream_t s);
+hipError_t launch_rows_wide_f16(const RowsArgs& a, int tm, hipStream_t s);
+hipError_t launch_rows_wide_bf16(const RowsArgs& a, int tm, hipStream_t s);
+
 // Tile products of grouped rows.
 //   TILE_ROWS  C[s][n] = sum_k A[s][k] B_e[n][k] for expert e's rows s (8 bits:
 //              scaled, with bias and activation).  A [T] rows of lda bytes; B
@@ -199,6 +206,18 @@ __device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int unit) {
     return true;
   });
   return r;
+}
+
+// Units of all rows (called by whole waves).
+template <int U, bool LEAST>
+__device__ __forceinline__ int count_units(const RowGroups& o) {
+  if (!o.at) return (int)((o.T + U - 1) / U);
+  int n = 0;
+  row_boundaries<U, LEAST>(o, [&](int, int, int, int u, int) {
+    n = __builtin_amdgcn_readlane(u, 63);
+    return false;
+  });
+  return n;
 }
 
 // The rows of no expert are those before `first` and from `last` on.

@@ -84,6 +84,7 @@ nm_status check_sizes(const Weights& w, int64_t T) {
 // How a call multiplies.
 enum RowsPath {
   ROWS_STREAM,   // few rows an expert: the packed weights streamed past each 16 to 64 of them
+  ROWS_WIDE,     // more: past each 64 or 128, shared by a workgroup's waves
   ROWS_SPARSE,   // 2:4: the sparse tile product
   ROWS_REPACK,   // 1:4, 1:8, 2:8: re-packed to 2:4 in the workspace, then the same
   ROWS_DENSE     // others: dense blocks (in the workspace where N < M), the dense tile product
@@ -97,9 +98,18 @@ RowsPath rows_path(const Weights& w, int64_t T) {
   const int64_t groups = std::min(T, w.E), mean = (T + groups - 1) / groups;
   if ((g.nRB + 7) / 8 * 8 * nm::units_most(T, w.E, 16) >= kMaxGrid / 2) return tiles;
   int v;
+  if (nm::ffn_tile_override("wide", &v, nullptr)) return ROWS_WIDE;
   if (nm::ffn_tile_override("stream", &v, nullptr)) return v ? ROWS_STREAM : tiles;
   if (nm::ffn_tile_override("tile", &v, nullptr) || nm::ffn_tile_override("tile24", &v, nullptr)) return tiles;
   return mean <= 32 ? ROWS_STREAM : tiles;
+}
+
+// ROWS_WIDE: 16-row tiles of a workgroup (4 or 8)
+int wide_tiles(const Weights& w, int64_t T) {
+  int v;
+  if (nm::ffn_tile_override("wide", &v, nullptr)) return v ? 8 : 4;
+  const int64_t groups = std::min(T, w.E);
+  return (T + groups - 1) / groups > 64 ? 8 : 4;
 }
 
 // Tile shapes (rows x outputs), with the microseconds a slab and, besides, a
@@ -139,10 +149,11 @@ int rows_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t ns
 int tile_type(int dt) { return dt == NM_I8 ? nm::TILE_I8 : dt == NM_F16 ? nm::TILE_F16 : nm::TILE_BF16; }
 
 // Whether a 16-bit path's kernel reads X's rows as they are.  Streamed: any rows
-// of at least one 16-byte piece; tiles: 16-byte pieces, none of which crosses
+// of at least one 16-byte piece, wide: of whole ones; tiles: 16-byte pieces, none of which crosses
 // the end of a row, and 32-bit offsets.
 bool rows_direct(RowsPath path, const void* X, int64_t ldx, int64_t K) {
   if (path == ROWS_STREAM) return K >= 8;
+  if (path == ROWS_WIDE) return K % 8 == 0;
   return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
 }
 size_t padded_bytes(int64_t T, int64_t K) { return up256((size_t)(T * up64(K) * 2)); }
@@ -161,6 +172,7 @@ size_t quantized_bytes(int64_t T, int64_t K) { return codes_bytes(T, K) + up256(
 hipError_t multiply(const Weights& w, RowsPath path, const nm::RowsArgs& a, int ka, uint8_t* ws, hipStream_t s) {
   const Geometry& g = w.g;
   if (path == ROWS_STREAM) return nm::launch_rows_decode(a, s);
+  if (path == ROWS_WIDE) return nm::launch_rows_wide(a, wide_tiles(w, a.rows.T), s);
   nm::RowsTile t{};
   t.rows = a.rows;
   t.A = static_cast<const uint8_t*>(a.X);

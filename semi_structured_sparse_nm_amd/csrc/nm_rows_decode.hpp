@@ -22,105 +22,12 @@
 
 #include <algorithm>
 
-#include "nm_expand.hpp"
-#include "nm_glu_decode.hpp"
 #include "nm_i8_device.hpp"
+#include "nm_rows_frag.hpp"
 
 namespace nm {
 
 namespace {
-
-#if defined(__HIP_DEVICE_COMPILE__)
-template <int WT>
-using acc_of = typename std::conditional<WT == NM_I8, v4i, v4f>::type;
-
-// One lane's part of one packed block of 8-bit weights (128 dense columns, a
-// run of 32 a lane), as GluFrag is of 16-bit ones.  Groups of eight columns hold
-// at most two registers of kept values, so each of a group's two dense
-// registers is one byte permute of them, whatever N, by the table of selectors.
-template <int N, int M>
-struct I8Frag {
-  static constexpr bool SPARSE = N == 2 && M == 4;
-  static constexpr bool TABLE = M == 8 && N < 8;
-  static constexpr int W = N == M ? 0 : M == 4 ? 2 : 3;
-  static constexpr int VB = 32 * N / M, VD = VB / 4;   // bytes, dwords of the run's values
-  static constexpr int MBL = VB * W;                   // bits of its positions
-  static constexpr int MRB = (4 * MBL + 31) / 32 * 4;  // bytes of a block row's positions
-  static constexpr int MD = (MBL + 31) / 32;
-  uint32_t vd[VD];
-  uint32_t mb[MD ? MD : 1];
-  __device__ __forceinline__ void load(const uint8_t* values, const uint8_t* meta, int64_t blk, int li, int lg) {
-    const uint8_t* v = values + blk * (64 * VB) + li * (4 * VB) + lg * VB;
-#pragma unroll
-    for (int i = 0; i < VD; ++i) vd[i] = reinterpret_cast<const uint32_t*>(v)[i];
-    if constexpr (N != M) {
-      const uint8_t* m = meta + blk * (16 * MRB) + li * MRB;
-      if constexpr (MBL % 32 == 0) {
-#pragma unroll
-        for (int i = 0; i < MD; ++i) mb[i] = reinterpret_cast<const uint32_t*>(m + lg * (MBL / 8))[i];
-      } else {
-        // the dwords the run's positions lie in (one more than they fill, none
-        // behind the row's last), shifted to start at bit 0
-        const int d = lg * MBL >> 5, sh = lg * MBL & 31;
-        uint32_t w[MD + 1];
-#pragma unroll
-        for (int i = 0; i <= MD; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[min(d + i, MRB / 4 - 1)];
-#pragma unroll
-        for (int i = 0; i < MD; ++i) mb[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], sh);
-      }
-    }
-  }
-  // bits b .. b + 23 and more of the positions, b known when compiled
-  __device__ __forceinline__ uint32_t positions(int b) const {
-    const int d = b >> 5, sh = b & 31;
-    return d + 1 < MD ? __builtin_amdgcn_alignbit(mb[d + 1], mb[d], sh) : mb[d] >> sh;
-  }
-  // the run's bytes b .. b + 3 (zeros behind the run)
-  __device__ __forceinline__ uint32_t bytes(int b) const {
-    const int d = b >> 2, sh = b & 3;
-    return d >= VD ? 0u : __builtin_amdgcn_alignbyte(d + 1 < VD ? vd[d + 1] : 0u, vd[d], sh);
-  }
-  // group q (of the lane's four) of eight columns, expanded
-  __device__ __forceinline__ v2i group(int q, const v2i* table) const {
-    const uint32_t pos = positions(3 * N * q);
-    uint32_t set = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) set |= 1u << (pos >> (3 * j) & 7u);
-    const uint32_t lo = bytes(N * q), hi = N > 4 ? bytes(N * q + 4) : 0u;
-    const v2i sel = table[set];
-    return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
-  }
-  __device__ __forceinline__ v4i mul(v4i x0, v4i x1, v4i c, const v2i* table) const {
-    if constexpr (TABLE) {
-      const v2i a0 = group(0, table), a1 = group(1, table), a2 = group(2, table), a3 = group(3, table);
-      c = mfma_dense<NM_I8>(v4i{a0[0], a0[1], a1[0], a1[1]}, x0, c);
-      return mfma_dense<NM_I8>(v4i{a2[0], a2[1], a3[0], a3[1]}, x1, c);
-    } else if constexpr (SPARSE) {
-      const v4i a = {(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
-      return __builtin_amdgcn_smfmac_i32_16x16x128_i8(
-          a, v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]}, c, (int)mb[0], 0, 0);
-    } else {
-      const uint64_t pos = MD > 1 ? (uint64_t)mb[MD - 1] << 32 | mb[0] : mb[0];
-      c = mfma_dense<NM_I8>(expand_step<NM_I8, N, M, 0>(vd, pos), x0, c);
-      return mfma_dense<NM_I8>(expand_step<NM_I8, N, M, 1>(vd, pos), x1, c);
-    }
-  }
-  // the two 16-byte pieces (of a row's eight in the block) the product wants
-  __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
-};
-
-template <int WT, int N, int M>
-struct RowsFrag : GluFrag<WT, N, M> {
-  typedef v4i Entry;
-  static constexpr int SLAB = 64;                      // columns of a block
-  __device__ static int kpiece(int p, int lg) { return GluFrag<WT, N, M>::kpiece(p, lg) >> 3; }
-};
-template <int N, int M>
-struct RowsFrag<NM_I8, N, M> : I8Frag<N, M> {
-  typedef v2i Entry;
-  static constexpr int SLAB = 128;
-};
-#endif
 
 #if defined(__HIP_DEVICE_COMPILE__)
 // Zeros in `n` outputs from r0 on of every units-th of the rows that belong to
@@ -162,24 +69,7 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
   __shared__ uint32_t top[QX ? 16 : 1][QX ? NW : 1];
   __shared__ float xscale[WT == NM_I8 ? 16 * NT : 1];
   extern __shared__ __attribute__((aligned(16))) uint8_t xq[];   // QX: rows of Kp + 16 bytes
-  if constexpr (Frag::TABLE) {
-    // column c of set s: the bytes of its k-th kept value where it is the
-    // set's k-th (from 0), else zeros (selector 12)
-    constexpr int ND = sizeof(Entry) / 4;
-    for (int q = threadIdx.x; q < 256 * ND; q += NW * 64) {
-      const int s = q / ND, c = 4 / XB * (q % ND);
-      uint32_t sel = 0;
-#pragma unroll
-      for (int e = 0; e < 4 / XB; ++e) {
-        const int k = __builtin_popcount(s & ((1 << (c + e)) - 1));
-        const bool in = (s >> (c + e) & 1) && k < 8 / XB;
-        const uint32_t b = XB == 2 ? (in ? (uint32_t)((2 * k + 1) << 8 | 2 * k) : 0x0C0Cu) : (in ? (uint32_t)k : 0x0Cu);
-        sel |= b << (8 * XB * e);
-      }
-      reinterpret_cast<uint32_t*>(table)[q] = sel;
-    }
-    __syncthreads();
-  }
+  fill_table<Frag, XB>(table);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lg = lane >> 4;
@@ -320,7 +210,9 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
         if (kb < nKB) {
           const v4i x0 = *reinterpret_cast<const v4i*>(xqr + kb * 128 + 16 * Frag::kpiece(0, lg));
           const v4i x1 = *reinterpret_cast<const v4i*>(xqr + kb * 128 + 16 * Frag::kpiece(1, lg));
-          acc[0] = f[i].mul(x0, x1, acc[0], table);
+          v4i a0, a1;
+          f[i].ready(a0, a1, table);
+          acc[0] = rows_mul<WT, Frag::SPARSE>(a0, a1, x0, x1, acc[0]);
         }
       }
     } else {
@@ -356,11 +248,13 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
 #pragma unroll
             for (int h = 0; h < 2; ++h) *reinterpret_cast<v4i*>(xs + 2048 * j + 1024 * h + put) = x[i][j][h];
           __builtin_amdgcn_wave_barrier();
+          v4i a0, a1;
+          f[i].ready(a0, a1, table);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             const v4i x0 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get0);
             const v4i x1 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get1);
-            acc[j] = f[i].mul(x0, x1, acc[j], table);
+            acc[j] = rows_mul<WT, Frag::SPARSE>(a0, a1, x0, x1, acc[j]);
           }
           __builtin_amdgcn_wave_barrier();
         }

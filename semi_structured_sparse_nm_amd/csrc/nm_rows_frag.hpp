@@ -1,0 +1,157 @@
+// One lane's part of a packed block as an operand of the matrix instructions,
+// for the products of grouped rows.
+#pragma once
+
+#include "nm_expand.hpp"
+#include "nm_glu_decode.hpp"
+#include "nm_rows.hpp"
+
+namespace nm {
+
+namespace {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int WT>
+using acc_of = typename std::conditional<WT == NM_I8, v4i, v4f>::type;
+
+// One lane's part of one packed block of 8-bit weights (128 dense columns, a
+// run of 32 a lane), as GluFrag is of 16-bit ones.  Groups of eight columns hold
+// at most two registers of kept values, so each of a group's two dense
+// registers is one byte permute of them, whatever N, by the table of selectors.
+template <int N, int M>
+struct I8Frag {
+  static constexpr bool SPARSE = N == 2 && M == 4;
+  static constexpr bool TABLE = M == 8 && N < 8;
+  static constexpr int W = N == M ? 0 : M == 4 ? 2 : 3;
+  static constexpr int VB = 32 * N / M, VD = VB / 4;   // bytes, dwords of the run's values
+  static constexpr int MBL = VB * W;                   // bits of its positions
+  static constexpr int MRB = (4 * MBL + 31) / 32 * 4;  // bytes of a block row's positions
+  static constexpr int MD = (MBL + 31) / 32;
+  uint32_t vd[VD];
+  uint32_t mb[MD ? MD : 1];
+  __device__ __forceinline__ void load(const uint8_t* values, const uint8_t* meta, int64_t blk, int li, int lg) {
+    const uint8_t* v = values + blk * (64 * VB) + li * (4 * VB) + lg * VB;
+#pragma unroll
+    for (int i = 0; i < VD; ++i) vd[i] = reinterpret_cast<const uint32_t*>(v)[i];
+    if constexpr (N != M) {
+      const uint8_t* m = meta + blk * (16 * MRB) + li * MRB;
+      if constexpr (MBL % 32 == 0) {
+#pragma unroll
+        for (int i = 0; i < MD; ++i) mb[i] = reinterpret_cast<const uint32_t*>(m + lg * (MBL / 8))[i];
+      } else {
+        // the dwords the run's positions lie in (one more than they fill, none
+        // behind the row's last), shifted to start at bit 0
+        const int d = lg * MBL >> 5, sh = lg * MBL & 31;
+        uint32_t w[MD + 1];
+#pragma unroll
+        for (int i = 0; i <= MD; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[min(d + i, MRB / 4 - 1)];
+#pragma unroll
+        for (int i = 0; i < MD; ++i) mb[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], sh);
+      }
+    }
+  }
+  // bits b .. b + 23 and more of the positions, b known when compiled
+  __device__ __forceinline__ uint32_t positions(int b) const {
+    const int d = b >> 5, sh = b & 31;
+    return d + 1 < MD ? __builtin_amdgcn_alignbit(mb[d + 1], mb[d], sh) : mb[d] >> sh;
+  }
+  // the run's bytes b .. b + 3 (zeros behind the run)
+  __device__ __forceinline__ uint32_t bytes(int b) const {
+    const int d = b >> 2, sh = b & 3;
+    return d >= VD ? 0u : __builtin_amdgcn_alignbyte(d + 1 < VD ? vd[d + 1] : 0u, vd[d], sh);
+  }
+  // group q (of the lane's four) of eight columns, expanded
+  __device__ __forceinline__ v2i group(int q, const v2i* table) const {
+    const uint32_t pos = positions(3 * N * q);
+    uint32_t set = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) set |= 1u << (pos >> (3 * j) & 7u);
+    const uint32_t lo = bytes(N * q), hi = N > 4 ? bytes(N * q + 4) : 0u;
+    const v2i sel = table[set];
+    return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
+  }
+  __device__ __forceinline__ void ready(v4i& a0, v4i& a1, const v2i* table) const {
+    if constexpr (TABLE) {
+      const v2i g0 = group(0, table), g1 = group(1, table), g2 = group(2, table), g3 = group(3, table);
+      a0 = v4i{g0[0], g0[1], g1[0], g1[1]};
+      a1 = v4i{g2[0], g2[1], g3[0], g3[1]};
+    } else if constexpr (SPARSE) {
+      a0 = v4i{(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
+      a1[0] = (int)mb[0];
+    } else {
+      const uint64_t pos = MD > 1 ? (uint64_t)mb[MD - 1] << 32 | mb[0] : mb[0];
+      a0 = expand_step<NM_I8, N, M, 0>(vd, pos);
+      a1 = expand_step<NM_I8, N, M, 1>(vd, pos);
+    }
+  }
+  // the two 16-byte pieces (of a row's eight in the block) the product wants
+  __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
+};
+
+// ready: the operands of the block's product, a0 and a1 the dense ones of its two
+// steps, or the packed values and (a1[0]) their positions; table: as filled by
+// fill_table.
+template <int WT, int N, int M>
+struct RowsFrag : GluFrag<WT, N, M> {
+  typedef GluFrag<WT, N, M> Base;
+  typedef v4i Entry;
+  static constexpr int SLAB = 64;                      // columns of a block
+  __device__ static int kpiece(int p, int lg) { return Base::kpiece(p, lg) >> 3; }
+  __device__ __forceinline__ void ready(v4i& a0, v4i& a1, const v4i* table) const {
+    if constexpr (Base::TABLE) {
+      a0 = Base::group(0, table);
+      a1 = Base::group(1, table);
+    } else if constexpr (Base::SPARSE) {
+      a0 = v4i{(int)this->vd[0], (int)this->vd[1], (int)this->vd[2], (int)this->vd[3]};
+      a1[0] = (int)this->mb;
+    } else {
+      a0 = expand_step<WT, N, M, 0>(this->vd, this->mb);
+      a1 = expand_step<WT, N, M, 1>(this->vd, this->mb);
+    }
+  }
+};
+template <int N, int M>
+struct RowsFrag<NM_I8, N, M> : I8Frag<N, M> {
+  typedef v2i Entry;
+  static constexpr int SLAB = 128;
+};
+
+// x0, x1: the lane's 32 bytes of activations, as the pieces kpiece names
+template <int WT, bool SPARSE>
+__device__ __forceinline__ acc_of<WT> rows_mul(v4i a0, v4i a1, v4i x0, v4i x1, acc_of<WT> c) {
+  if constexpr (SPARSE) {
+    const v8i x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+    if constexpr (WT == NM_I8) return __builtin_amdgcn_smfmac_i32_16x16x128_i8(a0, x, c, a1[0], 0, 0);
+    else return smfmac24<WT>(a0, x, c, a1[0]);
+  } else {
+    return mfma_dense<WT>(a1, x1, mfma_dense<WT>(a0, x0, c));
+  }
+}
+
+// The selectors of every set of kept columns, by all threads: column c of set s
+// takes the bytes of its k-th kept value where it is the set's k-th (from 0),
+// else zeros (selector 12).
+template <class Frag, int XB>
+__device__ __forceinline__ void fill_table(typename Frag::Entry* table) {
+  if constexpr (Frag::TABLE) {
+    constexpr int ND = sizeof(typename Frag::Entry) / 4;
+    for (int q = threadIdx.x; q < 256 * ND; q += blockDim.x) {
+      const int s = q / ND, c = 4 / XB * (q % ND);
+      uint32_t sel = 0;
+#pragma unroll
+      for (int e = 0; e < 4 / XB; ++e) {
+        const int k = __builtin_popcount(s & ((1 << (c + e)) - 1));
+        const bool in = (s >> (c + e) & 1) && k < 8 / XB;
+        const uint32_t b = XB == 2 ? (in ? (uint32_t)((2 * k + 1) << 8 | 2 * k) : 0x0C0Cu) : (in ? (uint32_t)k : 0x0Cu);
+        sel |= b << (8 * XB * e);
+      }
+      reinterpret_cast<uint32_t*>(table)[q] = sel;
+    }
+    __syncthreads();
+  }
+}
+#endif
+
+}  // namespace
+
+}  // namespace nm

@@ -299,15 +299,14 @@ __device__ __forceinline__ void tile_rows(void* C, int64_t ldc, int64_t Mr, int6
 // times the row's scale, times the channel's, each product rounded to binary32
 // (bias, activation and the rounding to the output's type follow).
 template <int OUT, int TM, int TN>
-__device__ __forceinline__ void tile_rows_i8(const RowsTile& a, const TileItem& it, int64_t m0, int64_t n0,
+__device__ __forceinline__ void tile_rows_i8(void* C, int64_t ldc, int64_t Mr, int64_t Nr, const float* xscale,
+                                             const float* wscale, const float* bias, int act, int64_t m0, int64_t n0,
                                              const v4i (&acc)[TN][TM]) {
   const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
-  const bool whole = whole_pieces(a.C, a.ldc);
-  const float* wscale = a.wscale + (int64_t)it.batch * a.Nr;
-  const float* bias = a.bias ? a.bias + (int64_t)it.batch * a.Nr : nullptr;
+  const bool whole = whole_pieces(C, ldc);
   float sx[TM];
 #pragma unroll
-  for (int j = 0; j < TM; ++j) sx[j] = a.xscale[min(m0 + 16 * j + li, (int64_t)it.end - 1)];
+  for (int j = 0; j < TM; ++j) sx[j] = xscale[min(m0 + 16 * j + li, Mr - 1)];
 #pragma unroll
   for (int i = 0; i < TN; i += 2) {
     float sw[2][4], b[2][4];
@@ -316,8 +315,8 @@ __device__ __forceinline__ void tile_rows_i8(const RowsTile& a, const TileItem& 
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int64_t n = n0 + 16 * (i + e) + 4 * lq + v;
-        sw[e][v] = n < a.Nr ? wscale[n] : 0.f;
-        b[e][v] = bias && n < a.Nr ? bias[n] : 0.f;
+        sw[e][v] = n < Nr ? wscale[n] : 0.f;
+        b[e][v] = bias && n < Nr ? bias[n] : 0.f;
       }
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
@@ -328,10 +327,10 @@ __device__ __forceinline__ void tile_rows_i8(const RowsTile& a, const TileItem& 
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           y[e][v] = (float)acc[i + e][j][v] * sx[j] * sw[e][v] + b[e][v];
-          y[e][v] = a.act == NM_ACT_GELU ? gelu_f32(y[e][v]) : y[e][v];
+          y[e][v] = act == NM_ACT_GELU ? gelu_f32(y[e][v]) : y[e][v];
         }
       __builtin_amdgcn_sched_barrier(0);                // one output's temporaries at a time
-      if (m < it.end) store_pair<OUT>(a.C, m * a.ldc, n0 + 16 * i, a.Nr, lq, y[0], y[1], whole);
+      if (m < Mr) store_pair<OUT>(C, m * ldc, n0 + 16 * i, Nr, lq, y[0], y[1], whole);
     }
   }
 }
@@ -344,7 +343,8 @@ __device__ __forceinline__ void rows_epilogue(const RowsTile& a, const TileItem&
     tile_rows<true, OUT, TM, TN>(static_cast<uint16_t*>(a.C) + it.batch * a.es, a.ldc, a.Mr, a.Nr, nullptr,
                                  NM_ACT_NONE, a.mask + it.batch * a.Mr * a.ldm, a.ldm, m0, n0, acc);
   else if constexpr (std::is_same<Acc, v4i>::value)
-    tile_rows_i8<OUT, TM, TN>(a, it, m0, n0, acc);
+    tile_rows_i8<OUT, TM, TN>(a.C, a.ldc, it.end, a.Nr, a.xscale, a.wscale + it.batch * a.Nr,
+                              a.bias ? a.bias + it.batch * a.Nr : nullptr, a.act, m0, n0, acc);
   else
     tile_rows<false, OUT, TM, TN>(a.C, a.ldc, it.end, a.Nr, nullptr, NM_ACT_NONE, nullptr, 0, m0, n0, acc);
 }

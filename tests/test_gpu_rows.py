@@ -14,9 +14,9 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 SPARSE = [(2, 4), (1, 4), (1, 8), (2, 8)]             # as 2:4 blocks in the tile product; others as dense ones
 PATTERNS = [(1, 4), (2, 4), (3, 4), (4, 4), (1, 8), (2, 8), (3, 8), (4, 8), (5, 8), (6, 8), (7, 8), (8, 8)]
-# every pattern streamed and in each shape of its tile product
+# every pattern streamed, wide and in each shape of its tile product
 PATHS = [(p, *nm_) for nm_ in PATTERNS
-         for p in ["stream:1"] + [f"{'tile24' if nm_ in SPARSE else 'tile'}:{i}" for i in range(4)]]
+         for p in ["stream:1", "wide:0", "wide:1"] + [f"{'tile24' if nm_ in SPARSE else 'tile'}:{i}" for i in range(4)]]
 
 
 @contextlib.contextmanager
