@@ -153,7 +153,7 @@ int tile_type(int dt) { return dt == NM_I8 ? nm::TILE_I8 : dt == NM_F16 ? nm::TI
 // the end of a row, and 32-bit offsets.
 bool rows_direct(RowsPath path, const void* X, int64_t ldx, int64_t K) {
   if (path == ROWS_STREAM) return K >= 8;
-  if (path == ROWS_WIDE) return K % 8 == 0;
+  if (path == ROWS_WIDE) return K % 8 == 0 && row_ok(ldx * 2);
   return aligned(X, 16) && ldx % 8 == 0 && K % 8 == 0 && row_ok(ldx * 2);
 }
 size_t padded_bytes(int64_t T, int64_t K) { return up256((size_t)(T * up64(K) * 2)); }

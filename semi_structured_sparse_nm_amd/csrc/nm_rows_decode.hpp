@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
   const int nrows = min(ru.end - ru.row, 16 * NT);
   const int nKB = (int)a.g.nKB;
   const int KX = (int)a.g.K;                           // columns of a row that may be read
-  const uint8_t* values = a.values + (int64_t)ru.e * (a.g.nRB * nKB * a.g.vblk);
-  const uint8_t* meta = a.meta + (int64_t)ru.e * (a.g.nRB * nKB * a.g.mblk);
-  // (row blocks past the last: that one again, its results are not stored)
-  const int64_t rb = min(rb0 + (wave >> lks), a.g.nRB - 1);
+  // the wave's row block (past the last: that one again, its results are not stored)
+  const int64_t blk0 = (ru.e * a.g.nRB + min(rb0 + (wave >> lks), a.g.nRB - 1)) * nKB;
+  const uint8_t* values = a.values + blk0 * Frag::VBLK;
+  const uint8_t* meta = a.meta + blk0 * Frag::MBLK;
   const int k0 = wave & (ks - 1);
 
   // What the end needs, asked for first (a wave's loads come back in order): the
@@ -135,7 +135,10 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int kb = b0 + ks * i;
-      if (i == 0 || kb < nKB) f[i].load(values, meta, rb * nKB + min(kb, nKB - 1), li, lg);
+      if (i == 0 || kb < nKB) {
+        const int at = __builtin_amdgcn_readfirstlane(min(kb, nKB - 1));
+        f[i].load(values + at * Frag::VBLK, meta + at * Frag::MBLK, li, lg);
+      }
     }
   };
   load_blocks(k0);
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
           const v4i x0 = *reinterpret_cast<const v4i*>(xqr + kb * 128 + 16 * Frag::kpiece(0, lg));
           const v4i x1 = *reinterpret_cast<const v4i*>(xqr + kb * 128 + 16 * Frag::kpiece(1, lg));
           v4i a0, a1;
-          f[i].ready(a0, a1, table);
+          f[i].ready(lg, a0, a1, table);
           acc[0] = rows_mul<WT, Frag::SPARSE>(a0, a1, x0, x1, acc[0]);
         }
       }
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
             for (int h = 0; h < 2; ++h) *reinterpret_cast<v4i*>(xs + 2048 * j + 1024 * h + put) = x[i][j][h];
           __builtin_amdgcn_wave_barrier();
           v4i a0, a1;
-          f[i].ready(a0, a1, table);
+          f[i].ready(lg, a0, a1, table);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             const v4i x0 = *reinterpret_cast<const v4i*>(xs + 2048 * j + get0);

@@ -15,7 +15,10 @@ template <int WT>
 using acc_of = typename std::conditional<WT == NM_I8, v4i, v4f>::type;
 
 // One lane's part of one packed block of 8-bit weights (128 dense columns, a
-// run of 32 a lane), as GluFrag is of 16-bit ones.  Groups of eight columns hold
+// run of 32 a lane): load brings it as it is stored, so that nothing waits for it
+// there; ready gives the operands of the block's product, a0 and a1 the dense ones
+// of its two steps, or (2:4) the packed values and, in a1[0], their positions, with
+// the table as fill_table leaves it.  Groups of eight columns hold
 // at most two registers of kept values, so each of a group's two dense
 // registers is one byte permute of them, whatever N, by the table of selectors.
 template <int N, int M>
@@ -27,31 +30,23 @@ struct I8Frag {
   static constexpr int MBL = VB * W;                   // bits of its positions
   static constexpr int MRB = (4 * MBL + 31) / 32 * 4;  // bytes of a block row's positions
   static constexpr int MD = (MBL + 31) / 32;
+  static constexpr int VBLK = 64 * VB, MBLK = 16 * MRB;   // bytes of a block
+  // dwords that the run's positions lie in, from any bit of the first
+  static constexpr int ML = MBL % 32 == 0 ? MD : MD + 1;
   uint32_t vd[VD];
-  uint32_t mb[MD ? MD : 1];
-  __device__ __forceinline__ void load(const uint8_t* values, const uint8_t* meta, int64_t blk, int li, int lg) {
-    const uint8_t* v = values + blk * (64 * VB) + li * (4 * VB) + lg * VB;
+  uint32_t mw[ML ? ML : 1];
+  // v, m: the block's values and positions (the same in all lanes)
+  __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m, int li, int lg) {
+    const uint32_t at = (uint32_t)(li * (4 * VB) + lg * VB);
 #pragma unroll
-    for (int i = 0; i < VD; ++i) vd[i] = reinterpret_cast<const uint32_t*>(v)[i];
-    if constexpr (N != M) {
-      const uint8_t* m = meta + blk * (16 * MRB) + li * MRB;
-      if constexpr (MBL % 32 == 0) {
+    for (int i = 0; i < VD; ++i) vd[i] = *reinterpret_cast<const uint32_t*>(v + at + 4 * i);
+    // (none behind the row's last)
 #pragma unroll
-        for (int i = 0; i < MD; ++i) mb[i] = reinterpret_cast<const uint32_t*>(m + lg * (MBL / 8))[i];
-      } else {
-        // the dwords the run's positions lie in (one more than they fill, none
-        // behind the row's last), shifted to start at bit 0
-        const int d = lg * MBL >> 5, sh = lg * MBL & 31;
-        uint32_t w[MD + 1];
-#pragma unroll
-        for (int i = 0; i <= MD; ++i) w[i] = reinterpret_cast<const uint32_t*>(m)[min(d + i, MRB / 4 - 1)];
-#pragma unroll
-        for (int i = 0; i < MD; ++i) mb[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], sh);
-      }
-    }
+    for (int i = 0; i < ML; ++i)
+      mw[i] = *reinterpret_cast<const uint32_t*>(m + (uint32_t)(li * MRB + 4 * min((lg * MBL >> 5) + i, MRB / 4 - 1)));
   }
-  // bits b .. b + 23 and more of the positions, b known when compiled
-  __device__ __forceinline__ uint32_t positions(int b) const {
+  // bits b .. b + 23 and more of the positions mb, b known when compiled
+  __device__ static __forceinline__ uint32_t positions(const uint32_t* mb, int b) {
     const int d = b >> 5, sh = b & 31;
     return d + 1 < MD ? __builtin_amdgcn_alignbit(mb[d + 1], mb[d], sh) : mb[d] >> sh;
   }
@@ -61,8 +56,8 @@ struct I8Frag {
     return d >= VD ? 0u : __builtin_amdgcn_alignbyte(d + 1 < VD ? vd[d + 1] : 0u, vd[d], sh);
   }
   // group q (of the lane's four) of eight columns, expanded
-  __device__ __forceinline__ v2i group(int q, const v2i* table) const {
-    const uint32_t pos = positions(3 * N * q);
+  __device__ __forceinline__ v2i group(const uint32_t* mb, int q, const v2i* table) const {
+    const uint32_t pos = positions(mb, 3 * N * q);
     uint32_t set = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) set |= 1u << (pos >> (3 * j) & 7u);
@@ -70,9 +65,13 @@ struct I8Frag {
     const v2i sel = table[set];
     return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
   }
-  __device__ __forceinline__ void ready(v4i& a0, v4i& a1, const v2i* table) const {
+  __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v2i* table) const {
+    // the positions from bit 0
+    uint32_t mb[MD ? MD : 1];
+#pragma unroll
+    for (int i = 0; i < MD; ++i) mb[i] = ML > MD ? __builtin_amdgcn_alignbit(mw[i + 1], mw[i], lg * MBL & 31) : mw[i];
     if constexpr (TABLE) {
-      const v2i g0 = group(0, table), g1 = group(1, table), g2 = group(2, table), g3 = group(3, table);
+      const v2i g0 = group(mb, 0, table), g1 = group(mb, 1, table), g2 = group(mb, 2, table), g3 = group(mb, 3, table);
       a0 = v4i{g0[0], g0[1], g1[0], g1[1]};
       a1 = v4i{g2[0], g2[1], g3[0], g3[1]};
     } else if constexpr (SPARSE) {
@@ -88,25 +87,76 @@ struct I8Frag {
   __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
 };
 
-// ready: the operands of the block's product, a0 and a1 the dense ones of its two
-// steps, or the packed values and (a1[0]) their positions; table: as filled by
-// fill_table.
+// The same of 16-bit weights (64 columns, a run of 16 a lane).  With 1 to 4 kept
+// of 8 a group's values are at most two registers, and the table serves as above;
+// other patterns' values are shifted to their places one by one.
 template <int WT, int N, int M>
-struct RowsFrag : GluFrag<WT, N, M> {
-  typedef GluFrag<WT, N, M> Base;
+struct RowsFrag {
+  typedef Run<WT, N, M> RunT;
   typedef v4i Entry;
+  static constexpr bool SPARSE = N == 2 && M == 4;
+  static constexpr bool TABLE = M == 8 && N <= 4;
   static constexpr int SLAB = 64;                      // columns of a block
-  __device__ static int kpiece(int p, int lg) { return Base::kpiece(p, lg) >> 3; }
-  __device__ __forceinline__ void ready(v4i& a0, v4i& a1, const v4i* table) const {
-    if constexpr (Base::TABLE) {
-      a0 = Base::group(0, table);
-      a1 = Base::group(1, table);
-    } else if constexpr (Base::SPARSE) {
-      a0 = v4i{(int)this->vd[0], (int)this->vd[1], (int)this->vd[2], (int)this->vd[3]};
-      a1[0] = (int)this->mb;
+  static constexpr int MBL = RunT::MBL, MRB = RunT::MRB;
+  static constexpr int VBLK = 16 * RunT::C_B, MBLK = 16 * MRB;
+  static constexpr int MD = (MBL + 31) / 32;
+  static constexpr int ML = MBL % 32 == 0 ? MD : MD + 1;
+  uint32_t vd[RunT::VD];
+  uint32_t mw[ML ? ML : 1];
+  __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m, int li, int lg) {
+    const uint32_t at = (uint32_t)(li * RunT::C_B + lg * RunT::VB);
+#pragma unroll
+    for (int i = 0; i < RunT::VD; ++i) vd[i] = *reinterpret_cast<const uint32_t*>(v + at + 4 * i);
+    if constexpr (SPARSE) {
+      mw[0] = *reinterpret_cast<const uint16_t*>(m + (uint32_t)(li * MRB + 2 * lg));
     } else {
-      a0 = expand_step<WT, N, M, 0>(this->vd, this->mb);
-      a1 = expand_step<WT, N, M, 1>(this->vd, this->mb);
+#pragma unroll
+      for (int i = 0; i < ML; ++i)
+        mw[i] = *reinterpret_cast<const uint32_t*>(m + (uint32_t)(li * MRB + 4 * min((lg * MBL >> 5) + i, MRB / 4 - 1)));
+    }
+  }
+  // the two 16-byte pieces (of a row's eight in the block) the product wants
+  __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
+  // group q (of the lane's two) of eight columns, expanded
+  __device__ __forceinline__ v4i group(uint64_t mb, int q, const v4i* table) const {
+    uint32_t set = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) set |= 1u << ((uint32_t)(mb >> (3 * (q * N + j))) & 7u);
+    // the group's kept values: halves q N .. + N - 1 of the run
+    uint32_t lo, hi = 0;
+    if constexpr (N == 4) {
+      lo = vd[2 * q];
+      hi = vd[2 * q + 1];
+    } else if constexpr (N == 3) {
+      lo = q ? (uint32_t)__builtin_amdgcn_alignbit(vd[2], vd[1], 16) : vd[0];
+      hi = q ? vd[2] >> 16 : vd[1];
+    } else if constexpr (N == 2) {
+      lo = vd[q];
+    } else {
+      lo = vd[0] >> (16 * q);
+    }
+    const v4i sel = table[set];
+    v4i o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[i]);
+    return o;
+  }
+  __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v4i* table) const {
+    if constexpr (SPARSE) {
+      a0 = v4i{(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
+      a1[0] = (int)mw[0];
+    } else {
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < MD; ++i) w[i] = ML > MD ? __builtin_amdgcn_alignbit(mw[i + 1], mw[i], lg * MBL & 31) : mw[i];
+      const uint64_t mb = (uint64_t)w[1] << 32 | w[0];
+      if constexpr (TABLE) {
+        a0 = group(mb, 0, table);
+        a1 = group(mb, 1, table);
+      } else {
+        a0 = expand_step<WT, N, M, 0>(vd, mb);
+        a1 = expand_step<WT, N, M, 1>(vd, mb);
+      }
     }
   }
 };

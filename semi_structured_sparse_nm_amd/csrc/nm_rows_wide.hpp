@@ -59,32 +59,33 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   const RowUnit ru = find_unit<BM, false>(a.rows, u);
   const int nKB = (int)a.g.nKB, last = nKB - 1;
   const int KX = (int)a.g.K;
-  const int64_t eb = (int64_t)ru.e * a.g.nRB * nKB;
-  const uint8_t* values = a.values + eb * a.g.vblk;
-  const uint8_t* meta = a.meta + eb * a.g.mblk;
-  // (row blocks past the last: that one again, its results are not stored)
-  int64_t rb[2];
+  // the wave's row blocks (past the last: that one again, its results are not stored)
+  const uint8_t* values[2];
+  const uint8_t* meta[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) rb[i] = min((int64_t)n * (kWideOut / 16) + 2 * wave + i, a.g.nRB - 1) * nKB;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t b = (ru.e * a.g.nRB + min((int64_t)n * (kWideOut / 16) + 2 * wave + i, a.g.nRB - 1)) * nKB;
+    values[i] = a.values + b * Frag::VBLK;
+    meta[i] = a.meta + b * Frag::MBLK;
+  }
 
   // rows: piece q % 8 (16 bytes) of row q / 8 (past the expert's last: that one)
   const int piece = threadIdx.x & 7, row0 = threadIdx.x >> 3;
-  const uint8_t* xr[NP];
+  const uint8_t* x0 = static_cast<const uint8_t*>(a.X) + (int64_t)ru.row * (a.ldx * XB);
+  const int rlast = ru.end - 1 - ru.row;
+  uint32_t xoff[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
-    xr[i] = static_cast<const uint8_t*>(a.X) + (int64_t)min(ru.row + row0 + NW * 8 * i, ru.end - 1) * (a.ldx * XB) +
-            16 * piece;
+  for (int i = 0; i < NP; ++i) xoff[i] = (uint32_t)min(row0 + NW * 8 * i, rlast) * (uint32_t)(a.ldx * XB);
   struct Rows {
     v4i x[NP];
   };
   auto load_rows = [&](Rows& r, int s) __attribute__((always_inline)) {
     s = min(s, last);
-    const bool in = s * Frag::SLAB + 16 / XB * piece < KX;
+    // (a piece past the row's end meets weights that are zero: the slab's first
+    // one, so that no branch splits the loads)
+    const uint32_t p = s * Frag::SLAB + 16 / XB * piece < KX ? 16 * piece : 0;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      r.x[i] = v4i{0, 0, 0, 0};
-      if (in) r.x[i] = load16(xr[i] + s * 128);
-    }
+    for (int i = 0; i < NP; ++i) r.x[i] = load16(x0 + s * 128 + (xoff[i] + p));
   };
   const int put = row0 * 128 + 16 * (piece ^ (row0 & 7));
   auto store_rows = [&](const Rows& r, int p) __attribute__((always_inline)) {
@@ -96,7 +97,8 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   };
   auto load_blocks = [&](Blocks& b, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) b.f[i].load(values, meta, rb[i] + min(s, last), li, lg);
+    for (int i = 0; i < 2; ++i)
+      b.f[i].load(values[i] + min(s, last) * Frag::VBLK, meta[i] + min(s, last) * Frag::MBLK, li, lg);
   };
   const int get0 = li * 128 + 16 * (Frag::kpiece(0, lg) ^ (li & 7));
   const int get1 = li * 128 + 16 * (Frag::kpiece(1, lg) ^ (li & 7));
@@ -114,8 +116,12 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
     load_rows(r1, s + 3);
     v4i a0[2], a1[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) b.f[i].ready(a0[i], a1[i], table);
+    for (int i = 0; i < 2; ++i) {
+      b.f[i].ready(lg, a0[i], a1[i], table);
+      __builtin_amdgcn_sched_barrier(0);                // one block's temporaries at a time
+    }
     load_blocks(b, s + 2);
+    __builtin_amdgcn_sched_barrier(0);                  // (the loads are not sunk behind the products)
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const v4i x0 = *reinterpret_cast<const v4i*>(rows[P] + 2048 * j + get0);
@@ -128,20 +134,26 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   };
   Rows r0, r1;
   Blocks b0, b1;
+  // (in the loop's order: its waits count the loads behind the awaited ones)
   load_rows(r0, 0);
-  load_blocks(b0, 0);
+  __builtin_amdgcn_sched_barrier(0);
   load_rows(r1, 1);
-  load_blocks(b1, 1);
+  load_blocks(b0, 0);
+  __builtin_amdgcn_sched_barrier(0);
   store_rows(r0, 0);
   load_rows(r0, 2);
+  __builtin_amdgcn_sched_barrier(0);
+  load_blocks(b1, 1);
+  __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt(waitcnt(63, 0));
   barrier_nofence();
-  for (int s = 0;;) {
+  // (one way out of the loop: with two the sums are copied at every step)
+  int s = 0;
+  for (; s + 1 < nKB; s += 2) {
     step(s, ic<0>(), r1, b0);
-    if (++s == nKB) break;
-    step(s, ic<1>(), r0, b1);
-    if (++s == nKB) break;
+    step(s + 1, ic<1>(), r0, b1);
   }
+  if (s < nKB) step(s, ic<0>(), r1, b0);
 
   const int64_t n0 = (int64_t)n * kWideOut + 32 * wave;
   if constexpr (WT == NM_I8) {
