@@ -186,23 +186,35 @@ __device__ __forceinline__ void row_boundaries(const RowGroups& o, F&& f) {
   }
 }
 
-// Unit `unit` of the rows (called by whole waves): its expert, first row, and
-// the expert's first row and end; e < 0 where there are fewer units.
+// Item L of the units of all experts times nt column tiles, expert by expert,
+// an expert's units first (called by whole waves): the expert, the unit's first
+// row, the expert's first row and end, the column tile; e < 0 where there are
+// fewer items.
 struct RowUnit {
-  int e, row, begin, end;
+  int e, row, begin, end, n;
 };
 template <int U, bool LEAST>
-__device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int unit) {
-  if (!o.at) return {(int64_t)unit * U < o.T ? 0 : -1, unit * U, 0, (int)o.T};
-  RowUnit r = {-1, 0, 0, 0};
+__device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int L, int nt = 1) {
+  RowUnit r = {-1, 0, 0, 0, 0};
+  if (!o.at) {
+    const int units = (int)((o.T + U - 1) / U);
+    r.n = __builtin_amdgcn_readfirstlane(L / units);
+    r.row = (L - r.n * units) * U;
+    r.end = (int)o.T;
+    r.e = r.n < nt ? 0 : -1;
+    return r;
+  }
   row_boundaries<U, LEAST>(o, [&](int i, int from, int at, int u, int n) {
-    const uint64_t hit = __ballot(u > unit && u - n <= unit);
+    const uint64_t hit = __ballot(u * nt > L && (u - n) * nt <= L);
     if (!hit) return false;
     const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+    const int units = __builtin_amdgcn_readlane(n, l);
+    const int in = L - __builtin_amdgcn_readlane(u - n, l) * nt;
     r.e = __builtin_amdgcn_readlane(i, l) - 1;
     r.begin = __builtin_amdgcn_readlane(from, l);
     r.end = __builtin_amdgcn_readlane(at, l);
-    r.row = r.begin + (unit - __builtin_amdgcn_readlane(u - n, l)) * U;
+    r.n = __builtin_amdgcn_readfirstlane(in / units);
+    r.row = r.begin + (in - r.n * units) * U;
     return true;
   });
   return r;

@@ -50,13 +50,13 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
       }
     }
   };
-  // XCD x takes a contiguous run of the units times column tiles, column tiles
-  // first: its workgroups meet few experts
+  // XCD x takes a contiguous run of the items, an expert's units of one column
+  // tile next to each other: they share its weights in the XCD's L2
   const int total = count_units<BM, false>(a.rows) * nt, per = (total + 7) / 8;
   const int j8 = blockIdx.x >> 3, L = (blockIdx.x & 7) * per + j8;
   if (j8 >= per || L >= total) return zero_rest();
-  const int u = __builtin_amdgcn_readfirstlane(L / nt), n = L - u * nt;
-  const RowUnit ru = find_unit<BM, false>(a.rows, u);
+  const RowUnit ru = find_unit<BM, false>(a.rows, L, nt);
+  const int n = ru.n;
   const int nKB = (int)a.g.nKB, last = nKB - 1;
   const int KX = (int)a.g.K;
   // the wave's row blocks (past the last: that one again, its results are not stored)
@@ -114,20 +114,25 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
     constexpr int P = decltype(pc)::value;
     store_rows(r1, P ^ 1);
     load_rows(r1, s + 3);
+    // (each row tile is read from LDS before the products of the one in front of it)
+    v4i x0[2], x1[2];
+    auto read_tile = [&](int j) __attribute__((always_inline)) {
+      x0[j & 1] = *reinterpret_cast<const v4i*>(rows[P] + 2048 * j + get0);
+      x1[j & 1] = *reinterpret_cast<const v4i*>(rows[P] + 2048 * j + get1);
+    };
+    read_tile(0);
     v4i a0[2], a1[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      b.f[i].ready(lg, a0[i], a1[i], table);
-      __builtin_amdgcn_sched_barrier(0);                // one block's temporaries at a time
-    }
+    for (int i = 0; i < 2; ++i) b.f[i].ready(lg, a0[i], a1[i], table);
     load_blocks(b, s + 2);
     __builtin_amdgcn_sched_barrier(0);                  // (the loads are not sunk behind the products)
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const v4i x0 = *reinterpret_cast<const v4i*>(rows[P] + 2048 * j + get0);
-      const v4i x1 = *reinterpret_cast<const v4i*>(rows[P] + 2048 * j + get1);
+      if (j + 1 < TM) read_tile(j + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[i][j] = rows_mul<WT, Frag::SPARSE>(a0[i], a1[i], x0, x1, acc[i][j]);
+      for (int i = 0; i < 2; ++i) acc[i][j] = rows_mul<WT, Frag::SPARSE>(a0[i], a1[i], x0[j & 1], x1[j & 1], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_waitcnt(waitcnt(63, 0));         // slab s + 1 is written, slab s read
     barrier_nofence();
