@@ -14,6 +14,40 @@ namespace {
 template <int WT>
 using acc_of = typename std::conditional<WT == NM_I8, v4i, v4f>::type;
 
+// One lane's positions in a packed block row of MRB bytes: MBL bits from bit lg
+// MBL on, brought by one load of ML dwords from the byte they begin in (a load of
+// its own for every dword would cost the vector memory path as much as 1 KB of
+// values), or, where that would leave the row, from the row's last ML dwords.
+template <int MBL, int MRB>
+struct Positions {
+  static constexpr int MD = (MBL + 31) / 32;           // dwords they fill
+  static constexpr int ML = (MBL + (MBL % 8 == 0 ? 0 : MBL % 4 == 0 ? 4 : 6) + 31) / 32;
+  static_assert(4 * ML <= MRB, "inside the row");
+  uint32_t w[ML];
+  struct __attribute__((packed, aligned(1))) Words {
+    uint32_t w[ML];
+  };
+  __device__ static __forceinline__ int first(int lg) { return min(lg * MBL >> 3, MRB - 4 * ML); }
+  // m: the block's positions (the same in all lanes)
+  __device__ __forceinline__ void load(const uint8_t* m, int li, int lg) {
+    const Words v = *reinterpret_cast<const Words*>(m + (uint32_t)(li * MRB + first(lg)));
+#pragma unroll
+    for (int i = 0; i < ML; ++i) w[i] = v.w[i];
+  }
+  // from bit 0 of b
+  __device__ __forceinline__ void align(int lg, uint32_t (&b)[MD]) const {
+    const int sh = lg * MBL - 8 * first(lg);           // below 32
+#pragma unroll
+    for (int i = 0; i < MD; ++i) b[i] = i + 1 < ML ? __builtin_amdgcn_alignbit(w[i + 1], w[i], sh) : w[i] >> sh;
+  }
+};
+template <int MRB>
+struct Positions<0, MRB> {
+  static constexpr int MD = 1;
+  __device__ __forceinline__ void load(const uint8_t*, int, int) {}
+  __device__ __forceinline__ void align(int, uint32_t (&)[1]) const {}
+};
+
 // One lane's part of one packed block of 8-bit weights (128 dense columns, a
 // run of 32 a lane): load brings it as it is stored, so that nothing waits for it
 // there; ready gives the operands of the block's product, a0 and a1 the dense ones
@@ -29,21 +63,17 @@ struct I8Frag {
   static constexpr int VB = 32 * N / M, VD = VB / 4;   // bytes, dwords of the run's values
   static constexpr int MBL = VB * W;                   // bits of its positions
   static constexpr int MRB = (4 * MBL + 31) / 32 * 4;  // bytes of a block row's positions
-  static constexpr int MD = (MBL + 31) / 32;
   static constexpr int VBLK = 64 * VB, MBLK = 16 * MRB;   // bytes of a block
-  // dwords that the run's positions lie in, from any bit of the first
-  static constexpr int ML = MBL % 32 == 0 ? MD : MD + 1;
+  typedef Positions<MBL, MRB> Pos;
+  static constexpr int MD = Pos::MD;
   uint32_t vd[VD];
-  uint32_t mw[ML ? ML : 1];
+  Pos pos;
   // v, m: the block's values and positions (the same in all lanes)
   __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m, int li, int lg) {
     const uint32_t at = (uint32_t)(li * (4 * VB) + lg * VB);
 #pragma unroll
     for (int i = 0; i < VD; ++i) vd[i] = *reinterpret_cast<const uint32_t*>(v + at + 4 * i);
-    // (none behind the row's last)
-#pragma unroll
-    for (int i = 0; i < ML; ++i)
-      mw[i] = *reinterpret_cast<const uint32_t*>(m + (uint32_t)(li * MRB + 4 * min((lg * MBL >> 5) + i, MRB / 4 - 1)));
+    pos.load(m, li, lg);
   }
   // bits b .. b + 23 and more of the positions mb, b known when compiled
   __device__ static __forceinline__ uint32_t positions(const uint32_t* mb, int b) {
@@ -66,10 +96,8 @@ struct I8Frag {
     return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
   }
   __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v2i* table) const {
-    // the positions from bit 0
-    uint32_t mb[MD ? MD : 1];
-#pragma unroll
-    for (int i = 0; i < MD; ++i) mb[i] = ML > MD ? __builtin_amdgcn_alignbit(mw[i + 1], mw[i], lg * MBL & 31) : mw[i];
+    uint32_t mb[MD];
+    pos.align(lg, mb);
     if constexpr (TABLE) {
       const v2i g0 = group(mb, 0, table), g1 = group(mb, 1, table), g2 = group(mb, 2, table), g3 = group(mb, 3, table);
       a0 = v4i{g0[0], g0[1], g1[0], g1[1]};
@@ -78,9 +106,9 @@ struct I8Frag {
       a0 = v4i{(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
       a1[0] = (int)mb[0];
     } else {
-      const uint64_t pos = MD > 1 ? (uint64_t)mb[MD - 1] << 32 | mb[0] : mb[0];
-      a0 = expand_step<NM_I8, N, M, 0>(vd, pos);
-      a1 = expand_step<NM_I8, N, M, 1>(vd, pos);
+      const uint64_t bits = MD > 1 ? (uint64_t)mb[MD - 1] << 32 | mb[0] : mb[0];
+      a0 = expand_step<NM_I8, N, M, 0>(vd, bits);
+      a1 = expand_step<NM_I8, N, M, 1>(vd, bits);
     }
   }
   // the two 16-byte pieces (of a row's eight in the block) the product wants
@@ -99,21 +127,17 @@ struct RowsFrag {
   static constexpr int SLAB = 64;                      // columns of a block
   static constexpr int MBL = RunT::MBL, MRB = RunT::MRB;
   static constexpr int VBLK = 16 * RunT::C_B, MBLK = 16 * MRB;
-  static constexpr int MD = (MBL + 31) / 32;
-  static constexpr int ML = MBL % 32 == 0 ? MD : MD + 1;
+  typedef Positions<SPARSE ? 0 : MBL, MRB> Pos;
+  static constexpr int MD = Pos::MD;
   uint32_t vd[RunT::VD];
-  uint32_t mw[ML ? ML : 1];
+  uint32_t idx;                                        // 2:4
+  Pos pos;                                             // others
   __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m, int li, int lg) {
     const uint32_t at = (uint32_t)(li * RunT::C_B + lg * RunT::VB);
 #pragma unroll
     for (int i = 0; i < RunT::VD; ++i) vd[i] = *reinterpret_cast<const uint32_t*>(v + at + 4 * i);
-    if constexpr (SPARSE) {
-      mw[0] = *reinterpret_cast<const uint16_t*>(m + (uint32_t)(li * MRB + 2 * lg));
-    } else {
-#pragma unroll
-      for (int i = 0; i < ML; ++i)
-        mw[i] = *reinterpret_cast<const uint32_t*>(m + (uint32_t)(li * MRB + 4 * min((lg * MBL >> 5) + i, MRB / 4 - 1)));
-    }
+    if constexpr (SPARSE) idx = *reinterpret_cast<const uint16_t*>(m + (uint32_t)(li * MRB + 2 * lg));
+    else pos.load(m, li, lg);
   }
   // the two 16-byte pieces (of a row's eight in the block) the product wants
   __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
@@ -144,12 +168,11 @@ struct RowsFrag {
   __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v4i* table) const {
     if constexpr (SPARSE) {
       a0 = v4i{(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
-      a1[0] = (int)mw[0];
+      a1[0] = (int)idx;
     } else {
-      uint32_t w[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < MD; ++i) w[i] = ML > MD ? __builtin_amdgcn_alignbit(mw[i + 1], mw[i], lg * MBL & 31) : mw[i];
-      const uint64_t mb = (uint64_t)w[1] << 32 | w[0];
+      uint32_t w[MD];
+      pos.align(lg, w);
+      const uint64_t mb = MD > 1 ? (uint64_t)w[MD - 1] << 32 | w[0] : w[0];
       if constexpr (TABLE) {
         a0 = group(mb, 0, table);
         a1 = group(mb, 1, table);
