@@ -48,17 +48,29 @@ struct Positions<0, MRB> {
   __device__ __forceinline__ void align(int, uint32_t (&)[1]) const {}
 };
 
+// The set of kept columns, a bit each, of eight columns whose positions begin at
+// bit 0 of pos: one group of 8, or two of 4.
+template <int N, int M>
+__device__ __forceinline__ uint32_t kept_set(uint32_t pos) {
+  constexpr int W = M == 4 ? 2 : 3;
+  uint32_t set = 0;
+#pragma unroll
+  for (int j = 0; j < 8 * N / M; ++j) set |= (j < N ? 1u : 16u) << (pos >> (W * j) & (M - 1));
+  return set;
+}
+
 // One lane's part of one packed block of 8-bit weights (128 dense columns, a
 // run of 32 a lane): load brings it as it is stored, so that nothing waits for it
 // there; ready gives the operands of the block's product, a0 and a1 the dense ones
 // of its two steps, or (2:4) the packed values and, in a1[0], their positions, with
-// the table as fill_table leaves it.  Groups of eight columns hold
-// at most two registers of kept values, so each of a group's two dense
-// registers is one byte permute of them, whatever N, by the table of selectors.
+// the table as fill_table leaves it.  Eight columns hold at most
+// two registers of kept values, so each of their two dense registers is one byte
+// permute of them, by the table of selectors.
 template <int N, int M>
 struct I8Frag {
   static constexpr bool SPARSE = N == 2 && M == 4;
-  static constexpr bool TABLE = M == 8 && N < 8;
+  static constexpr int KEPT = 8 * N / M;               // of eight columns
+  static constexpr bool TABLE = !SPARSE && N < M && (M == 8 || N == 3);
   static constexpr int W = N == M ? 0 : M == 4 ? 2 : 3;
   static constexpr int VB = 32 * N / M, VD = VB / 4;   // bytes, dwords of the run's values
   static constexpr int MBL = VB * W;                   // bits of its positions
@@ -85,14 +97,10 @@ struct I8Frag {
     const int d = b >> 2, sh = b & 3;
     return d >= VD ? 0u : __builtin_amdgcn_alignbyte(d + 1 < VD ? vd[d + 1] : 0u, vd[d], sh);
   }
-  // group q (of the lane's four) of eight columns, expanded
+  // columns 8 q .. + 7 of the lane's 32, expanded
   __device__ __forceinline__ v2i group(const uint32_t* mb, int q, const v2i* table) const {
-    const uint32_t pos = positions(mb, 3 * N * q);
-    uint32_t set = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) set |= 1u << (pos >> (3 * j) & 7u);
-    const uint32_t lo = bytes(N * q), hi = N > 4 ? bytes(N * q + 4) : 0u;
-    const v2i sel = table[set];
+    const v2i sel = table[kept_set<N, M>(positions(mb, KEPT * W * q))];
+    const uint32_t lo = bytes(KEPT * q), hi = KEPT > 4 ? bytes(KEPT * q + 4) : 0u;
     return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
   }
   __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v2i* table) const {
@@ -115,15 +123,19 @@ struct I8Frag {
   __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
 };
 
-// The same of 16-bit weights (64 columns, a run of 16 a lane).  With 1 to 4 kept
-// of 8 a group's values are at most two registers, and the table serves as above;
-// other patterns' values are shifted to their places one by one.
+// The same of 16-bit weights (64 columns, a run of 16 a lane).  Dense register i of
+// eight columns holds columns 2 i and 2 i + 1: with at most four values kept they
+// are among the same two registers for every i; with six or seven, column c's is
+// one of values c - 2 .. c, so that i's are in two neighbouring registers known
+// when compiled.  (Of 5:8 they may be in three: its values are shifted to their
+// places one by one, which takes about twice the instructions.)
 template <int WT, int N, int M>
 struct RowsFrag {
   typedef Run<WT, N, M> RunT;
   typedef v4i Entry;
   static constexpr bool SPARSE = N == 2 && M == 4;
-  static constexpr bool TABLE = M == 8 && N <= 4;
+  static constexpr int KEPT = 8 * N / M;               // of eight columns
+  static constexpr bool TABLE = !SPARSE && N < M && ((M == 8 && N != 5) || N == 3);
   static constexpr int SLAB = 64;                      // columns of a block
   static constexpr int MBL = RunT::MBL, MRB = RunT::MRB;
   static constexpr int VBLK = 16 * RunT::C_B, MBLK = 16 * MRB;
@@ -141,30 +153,28 @@ struct RowsFrag {
   }
   // the two 16-byte pieces (of a row's eight in the block) the product wants
   __device__ static int kpiece(int p, int lg) { return SPARSE ? 4 * p + lg : 2 * lg + p; }
-  // group q (of the lane's two) of eight columns, expanded
+  // columns 8 q .. + 7 of the lane's 16, expanded
   __device__ __forceinline__ v4i group(uint64_t mb, int q, const v4i* table) const {
-    uint32_t set = 0;
+    constexpr int W = M == 4 ? 2 : 3;
+    const v4i sel = table[kept_set<N, M>((uint32_t)(mb >> (KEPT * W * q)))];
+    // the kept values: halves KEPT q .. of the run
+    uint32_t e[4];
 #pragma unroll
-    for (int j = 0; j < N; ++j) set |= 1u << ((uint32_t)(mb >> (3 * (q * N + j))) & 7u);
-    // the group's kept values: halves q N .. + N - 1 of the run
-    uint32_t lo, hi = 0;
-    if constexpr (N == 4) {
-      lo = vd[2 * q];
-      hi = vd[2 * q + 1];
-    } else if constexpr (N == 3) {
-      lo = q ? (uint32_t)__builtin_amdgcn_alignbit(vd[2], vd[1], 16) : vd[0];
-      hi = q ? vd[2] >> 16 : vd[1];
-    } else if constexpr (N == 2) {
-      lo = vd[q];
-    } else {
-      lo = vd[0] >> (16 * q);
+    for (int i = 0; i < 4; ++i) {
+      const int h = KEPT * q + 2 * i, d = h >> 1;
+      const uint32_t lo = d < RunT::VD ? vd[d] : 0u, hi = d + 1 < RunT::VD ? vd[d + 1] : 0u;
+      e[i] = 2 * i >= KEPT ? 0u : h & 1 ? (uint32_t)__builtin_amdgcn_alignbit(hi, lo, 16) : lo;
     }
-    const v4i sel = table[set];
     v4i o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int b = first_source(i);
+      o[i] = (int)__builtin_amdgcn_perm(e[b + 1], e[b], (uint32_t)sel[i]);
+    }
     return o;
   }
+  // register of the kept values from which dense register i's two sources begin
+  __host__ __device__ static constexpr int first_source(int i) { return KEPT <= 4 || i < 1 ? 0 : i - 1; }
   __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v4i* table) const {
     if constexpr (SPARSE) {
       a0 = v4i{(int)vd[0], (int)vd[1], (int)vd[2], (int)vd[3]};
@@ -201,20 +211,22 @@ __device__ __forceinline__ acc_of<WT> rows_mul(v4i a0, v4i a1, v4i x0, v4i x1, a
   }
 }
 
-// The selectors of every set of kept columns, by all threads: column c of set s
-// takes the bytes of its k-th kept value where it is the set's k-th (from 0),
-// else zeros (selector 12).
+// The selectors of every set of kept columns, by all threads: a column's bytes are
+// those of the set's k-th kept value where it is the set's k-th (from 0), else
+// zeros (selector 12).
 template <class Frag, int XB>
 __device__ __forceinline__ void fill_table(typename Frag::Entry* table) {
   if constexpr (Frag::TABLE) {
-    constexpr int ND = sizeof(typename Frag::Entry) / 4;
+    constexpr int ND = 2 * XB;                          // dwords of eight columns
     for (int q = threadIdx.x; q < 256 * ND; q += blockDim.x) {
-      const int s = q / ND, c = 4 / XB * (q % ND);
+      const int s = q / ND, i = q % ND, c = 4 / XB * i;
+      int base = 0;                                     // the first source's first value
+      if constexpr (XB == 2) base = 2 * Frag::first_source(i);
       uint32_t sel = 0;
 #pragma unroll
       for (int e = 0; e < 4 / XB; ++e) {
-        const int k = __builtin_popcount(s & ((1 << (c + e)) - 1));
-        const bool in = (s >> (c + e) & 1) && k < 8 / XB;
+        const int k = __builtin_popcount(s & ((1 << (c + e)) - 1)) - base;
+        const bool in = (s >> (c + e) & 1) && k >= 0 && k < 8 / XB;
         const uint32_t b = XB == 2 ? (in ? (uint32_t)((2 * k + 1) << 8 | 2 * k) : 0x0C0Cu) : (in ? (uint32_t)k : 0x0Cu);
         sel |= b << (8 * XB * e);
       }

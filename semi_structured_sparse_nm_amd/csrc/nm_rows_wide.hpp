@@ -123,7 +123,12 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
     read_tile(0);
     v4i a0[2], a1[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) b.f[i].ready(lg, a0[i], a1[i], table);
+    for (int i = 0; i < 2; ++i) {
+      b.f[i].ready(lg, a0[i], a1[i], table);
+      // (6:8 and 7:8 of 8 bits: one block's temporaries at a time, or two workgroups
+      // do not fit a compute unit's registers)
+      if (WT == NM_I8 && Frag::TABLE && N > 5) __builtin_amdgcn_sched_barrier(0);
+    }
     load_blocks(b, s + 2);
     __builtin_amdgcn_sched_barrier(0);                  // (the loads are not sunk behind the products)
 #pragma unroll
