@@ -53,8 +53,28 @@ inline int64_t units_most(int64_t T, int64_t E, int64_t u) {
   return (T + some * (u - 1)) / u;
 }
 
+// How a product multiplies.
+enum RowsPath {
+  ROWS_STREAM,   // few rows an expert: the packed weights streamed past each 16 to 64 of them
+  ROWS_WIDE,     // more: past each 64 or 128, shared by a workgroup's waves
+  ROWS_SPARSE,   // 2:4: the sparse tile product
+  ROWS_REPACK,   // 1:4, 1:8, 2:8: re-packed to 2:4 in the workspace, then the same
+  ROWS_DENSE     // others: dense blocks (in the workspace where N < M), the dense tile product
+};
+struct RowsPlan {
+  RowsPath path;
+  int shape;                 // tile shape; ROWS_WIDE: 16-row tiles of a workgroup
+};
+// For T rows of E experts, by time models; g: one expert's weight.
+RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus);
+// The tile product's shape (and its time by the model, in microseconds)
+int rows_tile_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t nslab, int cus, double* time);
+int cols_tile_shape(int64_t T, int64_t E, int64_t R, int64_t K, int cus);
+
 // few rows an expert: the packed weights streamed once per unit of 16 rows or more
 hipError_t launch_rows_decode(const RowsArgs& a, hipStream_t s);
+// Its launch: 16-row tiles of a workgroup, waves along K, and workgroups.
+void rows_decode_plan(const Geometry& g, int64_t T, int64_t E, int* nt, int* ks, int64_t* workgroups);
 // Whether the streamed 8-bit product quantises T rows of E experts itself: what
 // a workgroup keeps of them fits its LDS, and they are so few that quantising
 // them in every workgroup takes less than a launch.  (One row, 11008 x 4096: 13.3

@@ -81,70 +81,15 @@ nm_status check_sizes(const Weights& w, int64_t T) {
 }
 
 // ---------------------------------------------------------------- paths
-// How a call multiplies.
-enum RowsPath {
-  ROWS_STREAM,   // few rows an expert: the packed weights streamed past each 16 to 64 of them
-  ROWS_WIDE,     // more: past each 64 or 128, shared by a workgroup's waves
-  ROWS_SPARSE,   // 2:4: the sparse tile product
-  ROWS_REPACK,   // 1:4, 1:8, 2:8: re-packed to 2:4 in the workspace, then the same
-  ROWS_DENSE     // others: dense blocks (in the workspace where N < M), the dense tile product
-};
+using nm::ROWS_DENSE;
+using nm::ROWS_REPACK;
+using nm::ROWS_STREAM;
+using nm::ROWS_WIDE;
+using nm::RowsPath;
+using nm::RowsPlan;
 
 Geometry geometry24(const Geometry& g) { return Geometry::make(g.R, g.K, 2, 4, g.eb); }
-
-RowsPath rows_path(const Weights& w, int64_t T) {
-  const Geometry& g = w.g;
-  const RowsPath tiles = g.N == 2 && g.M == 4 ? ROWS_SPARSE : nm::repack24_supported(g) ? ROWS_REPACK : ROWS_DENSE;
-  const int64_t groups = std::min(T, w.E), mean = (T + groups - 1) / groups;
-  if ((g.nRB + 7) / 8 * 8 * nm::units_most(T, w.E, 16) >= kMaxGrid / 2) return tiles;
-  int v;
-  if (nm::ffn_tile_override("wide", &v, nullptr)) return ROWS_WIDE;
-  if (nm::ffn_tile_override("stream", &v, nullptr)) return v ? ROWS_STREAM : tiles;
-  if (nm::ffn_tile_override("tile", &v, nullptr) || nm::ffn_tile_override("tile24", &v, nullptr)) return tiles;
-  return mean <= 32 ? ROWS_STREAM : tiles;
-}
-
-// ROWS_WIDE: 16-row tiles of a workgroup (4 or 8)
-int wide_tiles(const Weights& w, int64_t T) {
-  int v;
-  if (nm::ffn_tile_override("wide", &v, nullptr)) return v ? 8 : 4;
-  const int64_t groups = std::min(T, w.E);
-  return (T + groups - 1) / groups > 64 ? 8 : 4;
-}
-
-// Tile shapes (rows x outputs), with the microseconds a slab and, besides, a
-// tile takes.
-struct Shape {
-  int bm, bn;
-  double slab, tile;
-};
-constexpr Shape kDense[4] = {{256, 256, 1.5, 6.0}, {128, 256, 0.85, 5.0}, {128, 128, 0.60, 4.0}, {64, 128, 0.34, 3.5}};
-constexpr Shape kSparse[4] = {{256, 256, 1.0, 5.0}, {128, 256, 0.55, 5.0}, {128, 128, 0.40, 5.0}, {64, 128, 0.31, 5.0}};
-
-int rows_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t nslab, int cus) {
-  int only;
-  if (nm::ffn_tile_override(sparse ? "tile24" : "tile", &only, nullptr)) {
-    if (sparse && i8 && E >= nm::kRowsTable / 2 && only % 2 == 0) ++only;
-    return only;
-  }
-  int best = 3;
-  double least = 0;
-  for (int i = 0; i < 4; ++i) {
-    // (the 8-bit shapes whose table of boundaries is the smaller one)
-    if (sparse && i8 && E >= nm::kRowsTable / 2 && i % 2 == 0) continue;
-    const Shape& h = sparse ? kSparse[i] : kDense[i];
-    // an expert's last row tile is half full as a mean
-    const double rows = (double)T / h.bm + (E > 1 ? 0.5 * (double)std::min(T, E) : 0.0);
-    const double items = std::max(1.0, E > 1 ? rows : (double)((T + h.bm - 1) / h.bm)) * (double)((R + h.bn - 1) / h.bn);
-    const double rounds = std::max(1.0, E > 1 ? items / cus + 0.5 : (double)(int64_t)((items + cus - 1) / cus));
-    const double t = rounds * ((double)nslab * h.slab + h.tile);
-    if (least == 0 || t < least) {
-      least = t;
-      best = i;
-    }
-  }
-  return best;
-}
+RowsPlan plan_of(const Weights& w, int64_t T) { return nm::rows_plan(w.g, T, w.E, nm::device_cu_count()); }
 
 int tile_type(int dt) { return dt == NM_I8 ? nm::TILE_I8 : dt == NM_F16 ? nm::TILE_F16 : nm::TILE_BF16; }
 
@@ -169,10 +114,11 @@ size_t quantized_bytes(int64_t T, int64_t K) { return codes_bytes(T, K) + up256(
 
 // The product of rows already in the kernels' form (a.X, a.ldx; ka: valid
 // 16-byte pieces of a row); `ws`: copies_bytes of workspace.
-hipError_t multiply(const Weights& w, RowsPath path, const nm::RowsArgs& a, int ka, uint8_t* ws, hipStream_t s) {
+hipError_t multiply(const Weights& w, const RowsPlan& plan, const nm::RowsArgs& a, int ka, uint8_t* ws, hipStream_t s) {
   const Geometry& g = w.g;
+  const RowsPath path = plan.path;
   if (path == ROWS_STREAM) return nm::launch_rows_decode(a, s);
-  if (path == ROWS_WIDE) return nm::launch_rows_wide(a, wide_tiles(w, a.rows.T), s);
+  if (path == ROWS_WIDE) return nm::launch_rows_wide(a, plan.shape, s);
   nm::RowsTile t{};
   t.rows = a.rows;
   t.A = static_cast<const uint8_t*>(a.X);
@@ -190,7 +136,7 @@ hipError_t multiply(const Weights& w, RowsPath path, const nm::RowsArgs& a, int 
   t.bias = a.bias;
   t.act = a.act;
   t.zero_rest = a.zero_rest;
-  t.shape = rows_shape(path != ROWS_DENSE, g.eb == 1, a.rows.T, w.E, g.R, g.nKB, nm::device_cu_count());
+  t.shape = plan.shape;
   hipError_t e = hipSuccess;
   if (path == ROWS_REPACK) {
     // the blocks of all experts as one weight's
@@ -218,7 +164,7 @@ nm_status i8_workspace(const Weights& w, const nm_i8* xq, int64_t T, size_t* byt
   if (w.dtype != NM_I8) return NM_EUNSUPPORTED;
   const nm_status st = check_sizes(w, T);
   if (st != NM_OK) return st;
-  const RowsPath path = rows_path(w, T);
+  const RowsPath path = plan_of(w, T).path;
   *bytes = (xq || quantizes_inside(w, path, T) ? 0 : quantized_bytes(T, w.g.K)) + copies_bytes(w, path);
   return NM_OK;
 }
@@ -242,9 +188,9 @@ nm_status i8_product(const Weights& w, const float* w_scale, const nm_i8* xq, co
     if (!X || ldx < g.K) return NM_EINVAL;
     if (!float_dtype(xdt) || !aligned(X, (size_t)nm::dtype_bytes(xdt))) return NM_EUNSUPPORTED;
   }
-  const RowsPath path = rows_path(w, T);
-  const bool inside = !xq && quantizes_inside(w, path, T);
-  const size_t quant = xq || inside ? 0 : quantized_bytes(T, g.K), need = quant + copies_bytes(w, path);
+  const RowsPlan plan = plan_of(w, T);
+  const bool inside = !xq && quantizes_inside(w, plan.path, T);
+  const size_t quant = xq || inside ? 0 : quantized_bytes(T, g.K), need = quant + copies_bytes(w, plan.path);
   if (need && (!workspace || ws_bytes < need)) return NM_EINVAL;
   if (need && !aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -281,7 +227,7 @@ nm_status i8_product(const Weights& w, const float* w_scale, const nm_i8* xq, co
   a.ldy = ldy;
   a.ydt = ydt;
   a.zero_rest = zero_rest;
-  return multiply(w, path, a, (int)(Kp / 16), ws + quant, s) == hipSuccess ? NM_OK : NM_EHIP;
+  return multiply(w, plan, a, (int)(Kp / 16), ws + quant, s) == hipSuccess ? NM_OK : NM_EHIP;
 }
 
 nm_status check_offsets(const void* offsets, int32_t dtype) {
@@ -409,7 +355,7 @@ nm_status nm_expert_linear_workspace_size(const nm_experts* w, const void* Xt, i
   st = check_sizes(ww, T);
   if (st != NM_OK) return st;
   if (Xt && ldx < ww.g.K) return NM_EINVAL;
-  const RowsPath path = rows_path(ww, T);
+  const RowsPath path = plan_of(ww, T).path;
   // (NULL: the worst rows)
   *bytes = (rows_direct(path, Xt ? Xt : reinterpret_cast<const void*>(2), ldx, ww.g.K) ? 0 : padded_bytes(T, ww.g.K)) +
            copies_bytes(ww, path);
@@ -430,9 +376,9 @@ nm_status nm_expert_linear(const nm_experts* w, const void* Xt, int64_t ldx, int
   st = check_offsets(offsets, offsets_dtype);
   if (st != NM_OK) return st;
   if (!aligned(Xt, 2) || !aligned(Yt, 2)) return NM_EUNSUPPORTED;
-  const RowsPath path = rows_path(ww, T);
-  const bool direct = rows_direct(path, Xt, ldx, g.K);
-  const size_t pad = direct ? 0 : padded_bytes(T, g.K), need = pad + copies_bytes(ww, path);
+  const RowsPlan plan = plan_of(ww, T);
+  const bool direct = rows_direct(plan.path, Xt, ldx, g.K);
+  const size_t pad = direct ? 0 : padded_bytes(T, g.K), need = pad + copies_bytes(ww, plan.path);
   if (need && (!workspace || workspace_bytes < need)) return NM_EINVAL;
   if (need && !aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -455,7 +401,7 @@ nm_status nm_expert_linear(const nm_experts* w, const void* Xt, int64_t ldx, int
   a.ldy = ldy;
   a.ydt = ww.dtype;
   a.zero_rest = zero_rest != 0;
-  return multiply(ww, path, a, (int)(a.g.K / 8), ws + pad, s) == hipSuccess ? NM_OK : NM_EHIP;
+  return multiply(ww, plan, a, (int)(a.g.K / 8), ws + pad, s) == hipSuccess ? NM_OK : NM_EHIP;
 }
 
 nm_status nm_expert_linear_backward_workspace_size(const nm_experts* w, int64_t T, size_t* bytes) {
@@ -532,7 +478,7 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
     t.C = dX;
     t.ldc = lddx;
     t.zero_rest = zero_rest != 0;
-    t.shape = rows_shape(false, false, T, ww.E, g.K, t.nslab, cus);
+    t.shape = nm::rows_tile_shape(false, false, T, ww.E, g.K, t.nslab, cus, nullptr);
     if (nm::launch_rows_tile(tile_type(ww.dtype), nm::TILE_ROWS, ww.dtype, t, s) != hipSuccess) return NM_EHIP;
   }
   if (dW) {
@@ -549,7 +495,7 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
     t.es = g.R * lddw;
     t.mask = mask;
     t.ldm = g.nKB * 8;
-    t.shape = rows_shape(false, false, ww.E * g.R, 1, g.K, std::max<int64_t>(1, T / 64 / ww.E), cus);
+    t.shape = nm::cols_tile_shape(T, ww.E, g.R, g.K, cus);
     if (nm::launch_rows_tile(tile_type(ww.dtype), nm::TILE_COLS, ww.dtype, t, s) != hipSuccess) return NM_EHIP;
   }
   return NM_OK;

@@ -309,24 +309,14 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
 #endif
 }
 
-// Waves of a workgroup along K: as many as find eight blocks each (what a wave does
-// once, before and after them, is 300 vector and 350 scalar instructions), but no
-// fewer workgroups than compute units.
-inline int waves_along_k(const RowsArgs& a, int64_t units) {
-  int ks = kGluWaves;
-  while (ks > 1 && a.g.nKB < 8 * ks && a.g.nRB * units * (ks / 2) / kGluWaves >= device_cu_count()) ks /= 2;
-  return ks;
-}
-
 template <int WT, int N, int M, bool SHORT>
 hipError_t launch_rows_decode_rows(const RowsArgs& a, hipStream_t s) {
   const int64_t T = a.rows.T, E = a.rows.E;
-  // tiles of 16 rows a workgroup takes: those an expert has as a mean
-  const int64_t mean = (T + std::min(T, E) - 1) / std::min(T, E);
-  const int nt = stream_tiles(a.g.nRB * std::min(T, E), mean);
+  int nt, ks;
+  int64_t workgroups;
+  rows_decode_plan(a.g, T, E, &nt, &ks, &workgroups);
   const int64_t units = units_most(T, E, 16 * nt);
-  const int ks = waves_along_k(a, units), nblk = kGluWaves / ks;
-  const dim3 grid((unsigned)((a.g.nRB + 8 * nblk - 1) / (8 * nblk) * 8 * units)), block(kGluWaves * 64);
+  const dim3 grid((unsigned)workgroups), block(kGluWaves * 64);
   auto go = [&](auto kernel, int64_t lds) {
     hipLaunchKernelGGL(kernel, grid, block, (unsigned)lds, s, a, (int)units, ks);
     return hipGetLastError();

@@ -1,0 +1,186 @@
+// How a product of grouped rows multiplies: time models of its paths.
+//
+// Fitted to 1084 products of 17 to 2048 rows an expert, 1 to 64 experts, 300 to
+// 11008 outputs, K 512 to 11008, seven patterns, 8 and 16 bits, every path and tile
+// shape measured with weights that change between calls: the wide and tile models
+// are 5 to 10% off as a root mean square, the streamed one 30%; the choice costs 2%
+// against the fastest path as a mean over them, 10% in one of ten, 60% at most.
+// For example, streamed, wide (64 rows), wide (128), best tiles, in microseconds:
+// 8-bit 4:8, 48 rows, 11008 x 4096 25, 33, 41, 42; 256 rows 59, 34, 41, 49; 32 experts
+// of 1536 x 2048, 16-bit 4:8, 256 rows 42, 30, 37, 149, 4096 rows -, 49, 63, 175;
+// 16-bit 2:4, 4096 rows of 8 experts of 2048 x 4096 587, 102, 97, 69.
+#include <algorithm>
+
+#include "nm_rows.hpp"
+
+namespace nm {
+
+namespace {
+
+// What a pattern costs the paths that expand in registers: 2:4 as it is, dense,
+// up to four kept of eight columns and more (byte permutes by a table), and the
+// 16-bit 5:8 (value by value).
+enum Kind { SPARSE, DENSE, FEW, MANY, SHIFTED, KINDS };
+Kind kind_of(const Geometry& g) {
+  if (g.N == 2 && g.M == 4) return SPARSE;
+  if (g.N == g.M) return DENSE;
+  if (g.eb == 2 && g.N == 5) return SHIFTED;
+  return 8 * g.N / g.M <= 4 ? FEW : MANY;
+}
+
+// Microseconds: a workgroup besides its slabs, a slab, and (wide, 64 rows) what a
+// further workgroup on the compute unit costs of one alone.
+struct Wide {
+  double base, slab, more;
+};
+constexpr Wide kWide[2][2][KINDS] = {
+    // 8 bits (slabs of 128 columns): 64 rows, 128 rows
+    {{{4.81, 0.528, 0.938}, {5.89, 0.935, 0.962}, {4.93, 0.729, 0.852}, {5.54, 1.03, 0.853}, {}},
+     {{5.96, 0.613, 1.0}, {7.65, 0.969, 1.0}, {6.61, 0.967, 1.0}, {6.89, 1.21, 1.0}, {}}},
+    // 16 bits (64 columns)
+    {{{3.01, 0.455, 1.0}, {4.57, 0.938, 0.992}, {4.23, 0.577, 0.895}, {4.46, 0.707, 0.932}, {4.95, 1.24, 0.925}},
+     {{4.59, 0.556, 1.0}, {5.81, 0.993, 1.0}, {5.29, 0.825, 1.0}, {5.80, 0.952, 1.0}, {5.86, 1.44, 1.0}}}};
+
+// A workgroup besides its blocks, a wave's block, and that for each 16-row tile.
+struct Stream {
+  double base, block, tile;
+};
+constexpr Stream kStream[2][KINDS] = {
+    {{1.12, 0.153, 0.224}, {1.98, 0.237, 0.223}, {1.56, 0.172, 0.223}, {1.31, 0.471, 0.253}, {}},
+    {{0.20, 0.119, 0.267}, {0.34, 0.418, 0.235}, {0.56, 0.232, 0.231}, {1.07, 0.300, 0.213}, {0.59, 0.663, 0.143}}};
+
+// Tile shapes (rows x outputs): a tile besides its slabs, a slab with one tile on
+// every compute unit, and with few.
+struct Shape {
+  int bm, bn;
+};
+constexpr Shape kShapes[4] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}};
+struct Tile {
+  double base, busy, idle;
+};
+constexpr Tile kTiles[2][2][4] = {
+    // 8 bits: dense, 2:4
+    {{{8.01, 1.30, 1.01}, {5.46, 0.777, 0.546}, {3.46, 0.487, 0.337}, {2.82, 0.312, 0.241}},
+     {{8.77, 0.920, 0.643}, {6.43, 0.611, 0.429}, {4.22, 0.380, 0.291}, {3.31, 0.270, 0.241}}},
+    // 16 bits
+    {{{4.79, 1.62, 1.00}, {3.55, 0.908, 0.533}, {2.46, 0.523, 0.327}, {2.20, 0.330, 0.226}},
+     {{5.70, 0.910, 0.611}, {3.82, 0.606, 0.373}, {2.88, 0.367, 0.265}, {2.27, 0.281, 0.238}}}};
+
+constexpr double kRate = 4.4e6;              // bytes of weights a microsecond
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// units of u rows: of several experts each one's last is half full as a mean
+double units(int64_t T, int64_t E, int64_t u) {
+  return E == 1 ? (double)ceil_div(T, u) : (double)T / u + 0.5 * (double)std::min(T, E);
+}
+
+// rounds of n workgroups over the compute units: whole ones of one expert; of
+// several, whose sizes the host does not know, part of one more
+double rounds(double n, int64_t E, int cus, double more) {
+  const double r = n / cus;
+  return std::max(1.0, E == 1 ? (double)(int64_t)(r + 0.999999) : r + more);
+}
+
+double wide_time(const Geometry& g, int64_t T, int64_t E, int tm, double bytes, int cus) {
+  const Wide& w = kWide[g.eb - 1][tm == 8][kind_of(g)];
+  const double r = rounds(units(T, E, 16 * tm) * (double)ceil_div(g.R, 256), E, cus, 0.55);
+  return 3.0 + std::max((w.base + g.nKB * w.slab) * std::max(1.0, w.more * r), bytes / kRate);
+}
+
+double stream_time(const Geometry& g, int64_t T, int64_t E, double bytes, int cus) {
+  const Stream& w = kStream[g.eb - 1][kind_of(g)];
+  int nt, ks;
+  int64_t most;
+  rows_decode_plan(g, T, E, &nt, &ks, &most);
+  const double n = units(T, E, 16 * nt) * (double)ceil_div(g.nRB, 8 / ks), r = n / cus;
+  const double in_turn = std::max(1.0, E == 1 && r < 3 ? (double)(int64_t)(r + 0.999999) : r + 1.0);
+  return 4.7 + std::max(in_turn * (w.base + (double)ceil_div(g.nKB, ks) * (w.block + w.tile * nt)), bytes / kRate);
+}
+
+double tile_time(const Tile& c, const Shape& h, double row_units, int64_t R, int64_t nslab, int64_t E, int cus) {
+  const double n = row_units * (double)ceil_div(R, h.bn);
+  const double slab = c.idle + (c.busy - c.idle) * std::min(1.0, n / cus);
+  return 5.0 + rounds(n, E, cus, 0.45) * (c.base + nslab * slab);
+}
+
+}  // namespace
+
+int rows_tile_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t nslab, int cus, double* time) {
+  const bool small_table = sparse && i8 && E >= kRowsTable / 2;
+  int best = 3;
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    // (the 8-bit shapes whose table of boundaries is the smaller one)
+    if (small_table && i % 2 == 0) continue;
+    const double t = tile_time(kTiles[i8 ? 0 : 1][sparse][i], kShapes[i], units(T, E, kShapes[i].bm), R, nslab, E, cus);
+    if (least == 0 || t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  int only;
+  if (ffn_tile_override(sparse ? "tile24" : "tile", &only, nullptr)) best = small_table ? only | 1 : only;
+  if (time) *time = least;
+  return best;
+}
+
+int cols_tile_shape(int64_t T, int64_t E, int64_t R, int64_t K, int cus) {
+  int best = 0;
+  if (ffn_tile_override("tile", &best, nullptr)) return best;
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const Shape& h = kShapes[i];
+    const double n = (double)(E * ceil_div(R, h.bm)) * (double)ceil_div(K, h.bn);
+    const Tile& c = kTiles[1][0][i];
+    const double slab = c.idle + (c.busy - c.idle) * std::min(1.0, n / cus);
+    const double t = std::max(1.0, n / cus + 0.45) * (c.base + (double)T / 64.0 / E * slab);
+    if (i == 0 || t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  return best;
+}
+
+RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus) {
+  RowsPlan tiles{g.N == 2 && g.M == 4 ? ROWS_SPARSE : repack24_supported(g) ? ROWS_REPACK : ROWS_DENSE, 0};
+  double time;
+  tiles.shape = rows_tile_shape(tiles.path != ROWS_DENSE, g.eb == 1, T, E, g.R, g.nKB, cus, &time);
+  // a launch has fewer than 2^32 threads
+  int nt, ks;
+  int64_t most;
+  rows_decode_plan(g, T, E, &nt, &ks, &most);
+  const bool can_stream = most < (1 << 22);
+  auto can_wide = [&](int tm) { return units_most(T, E, 16 * tm) * ceil_div(g.R, 256) < (1 << 22); };
+  int v;
+  if (ffn_tile_override("wide", &v, nullptr) && can_wide(v ? 8 : 4)) return {ROWS_WIDE, v ? 8 : 4};
+  if (ffn_tile_override("stream", &v, nullptr)) return v && can_stream ? RowsPlan{ROWS_STREAM, 0} : tiles;
+  if (ffn_tile_override("tile", &v, nullptr) || ffn_tile_override("tile24", &v, nullptr)) return tiles;
+  const int64_t groups = std::min(T, E), mean = ceil_div(T, groups);
+  if (mean <= 16 && can_stream) return {ROWS_STREAM, 0};
+
+  const double dense = (double)E * (double)(g.nRB * g.nKB) * 2048.0;
+  const double bytes = (double)E * (double)(g.values_bytes() + g.meta_bytes());
+  if (tiles.path == ROWS_REPACK) time += (bytes + dense * (0.5 + 0.125 / g.eb)) / 4.7e6;
+  if (tiles.path == ROWS_DENSE && g.N != g.M) time += 2.0 + (bytes + dense) / 3.1e6;
+  RowsPlan best = tiles;
+  if (mean <= 1024 && can_stream) {
+    const double t = stream_time(g, T, E, bytes, cus);
+    if (t < time) {
+      time = t;
+      best = {ROWS_STREAM, 0};
+    }
+  }
+  for (const int tm : {4, 8}) {
+    if (!can_wide(tm)) continue;
+    const double t = wide_time(g, T, E, tm, bytes, cus);
+    if (t < time) {
+      time = t;
+      best = {ROWS_WIDE, tm};
+    }
+  }
+  return best;
+}
+
+}  // namespace nm

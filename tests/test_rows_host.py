@@ -71,25 +71,29 @@ def _lin(w=None, ws=P[1], xq=None, X=P[0], ldx=300, xdt=nm.NM_BF16, T=20, Y=P[2]
                                  ydt, bias, act, wsp, wsb, None)
 
 
-def test_i8_linear_refusals():
+def test_i8_linear_refusals(monkeypatch):
     assert nm.lib().nm_i8_linear(None, P[1], None, P[0], 300, nm.NM_F16, 5, P[2], 40, nm.NM_F16, None, 0, P[3], 1 << 28,
                                  None) == EINVAL
     w = dict(R=40, K=300)
     for kw in (dict(X=None), dict(Y=None), dict(ws=None), dict(T=0), dict(ldx=299), dict(ldy=39),
                dict(w=_desc(**w, format_version=0)), dict(w=_desc(**w, values_bytes=7)), dict(w=_desc(**w, meta=None)),
                dict(xq=_i8(21)), dict(xq=_i8(20, 301)), dict(xq=_i8(format_version=0)), dict(xq=_i8(codes=None)),
-               dict(wsp=None), dict(wsb=64),
-               # dense copies in the workspace
-               dict(w=_desc(**w, N=3), xq=_i8(200), T=200, wsp=None)):
+               dict(wsp=None), dict(wsb=64)):
         assert _lin(**kw) == EINVAL, kw
     for kw in (dict(xdt=nm.NM_I8), dict(ydt=nm.NM_I32), dict(act=2), dict(X=P[0] + 1), dict(Y=P[2] + 1),
                dict(bias=P[4] + 2), dict(ws=P[1] + 1), dict(wsp=P[3] + 32), dict(T=(1 << 25) + 1),
                dict(w=_desc(**w, dt=nm.NM_F16)), dict(w=_desc(R=16, K=131072), ldx=131072), dict(xq=_i8(codes=P[8] + 4)),
                dict(w=_desc(R=(1 << 22) + 16, K=8), ldx=8, ldy=1 << 23)):
         assert _lin(**kw) == EUNSUP, kw
+    # dense copies in the workspace
+    monkeypatch.setenv("NM_FFN_TILE", "tile:1")
+    dense = dict(w=_desc(**w, N=3), xq=_i8(200), T=200)
+    assert _lin(**dense, wsp=None) == EINVAL and _lin(**dense, wsb=18000) == EINVAL
+    assert _lin(**dense, wsp=P[3] + 16) == EUNSUP
 
 
-def test_i8_workspace():
+def test_i8_workspace(monkeypatch):
+    monkeypatch.setenv("NM_FFN_TILE", "tile:1")           # (streamed or wide products need no copies)
     n = ctypes.c_size_t()
     f = nm.lib().nm_i8_linear_workspace_size
     x = _i8(20)
@@ -103,6 +107,10 @@ def test_i8_workspace():
     assert f(ctypes.byref(w), None, 0, ctypes.byref(n)) == EINVAL and f(ctypes.byref(w), None, 5, None) == EINVAL
     assert f(None, None, 5, ctypes.byref(n)) == EINVAL
     assert f(ctypes.byref(_desc(R=40, K=300, dt=nm.NM_BF16)), None, 5, ctypes.byref(n)) == EUNSUP
+    for path in ("stream:1", "wide:0", "wide:1"):
+        monkeypatch.setenv("NM_FFN_TILE", path)
+        assert f(ctypes.byref(_desc(R=40, K=300, N=3)), ctypes.byref(_i8(500)), 500, ctypes.byref(n)) == nm.NM_OK
+        assert n.value == 0
 
 
 # ---------------------------------------------------------------- experts
@@ -133,22 +141,25 @@ def _el(w=None, X=P[0], ldx=128, T=5, o=P[1], odt=0, Y=P[2], ldy=40, fill=0, ws=
     return nm.lib().nm_expert_linear(ctypes.byref(w), X, ldx, T, o, odt, Y, ldy, fill, ws, wsb, None)
 
 
-def test_expert_linear_refusals():
-    dense = dict(T=1100, w=_experts(N=4, M=8))
+def test_expert_linear_refusals(monkeypatch):
     assert nm.lib().nm_expert_linear(None, P[0], 128, 5, P[1], 0, P[2], 40, 0, None, 0, None) == EINVAL
     for kw in (dict(X=None), dict(Y=None), dict(o=None), dict(T=0), dict(T=-1), dict(ldx=127), dict(ldy=39),
                dict(w=_experts(format_version=0)), dict(w=_experts(values_bytes=7)), dict(w=_experts(meta=None)),
-               dict(w=_experts(experts=0)), dict(**dense, ws=None), dict(**dense, wsb=1000),
-               dict(T=1100, X=P[0] + 2, ws=None), dict(w=_experts(K=4), ldx=4, wsb=0)):
+               dict(w=_experts(experts=0)), dict(w=_experts(K=4), ldx=4, wsb=0)):
         assert _el(**kw) == EINVAL, kw
     for kw in (dict(w=_experts(dt=nm.NM_I8)), dict(odt=2), dict(odt=-1), dict(X=P[0] + 1), dict(Y=P[2] + 1),
-               dict(o=P[1] + 2), dict(o=P[1] + 4, odt=1), dict(**dense, ws=P[3] + 16), dict(T=(1 << 25) + 1),
+               dict(o=P[1] + 2), dict(o=P[1] + 4, odt=1), dict(T=(1 << 25) + 1),
                dict(w=_experts(E=1023, experts=1024, values_bytes=1 << 30, meta_bytes=1 << 30))):
         assert _el(**kw) == EUNSUP, kw
     big = _experts(E=1, R=(1 << 22) + 16, K=8)
     assert _el(w=big, ldx=8, ldy=1 << 23) == EUNSUP
     # more tiles than 32 bits count
     assert _el(w=_experts(E=1, R=1 << 22, K=8), ldx=8, ldy=1 << 22, T=1 << 25) == EUNSUP
+    # copies of weights and of rows that the tiles do not read as they are
+    monkeypatch.setenv("NM_FFN_TILE", "tile:1")
+    dense = dict(T=1100, w=_experts(N=4, M=8))
+    assert _el(**dense, ws=None) == EINVAL and _el(**dense, wsb=1000) == EINVAL
+    assert _el(**dense, ws=P[3] + 16) == EUNSUP and _el(T=1100, X=P[0] + 2, ws=None) == EINVAL
 
 
 def _eb(w=None, X=P[0], ldx=128, T=5, o=P[1], odt=0, dY=P[2], lddy=40, dX=P[3], lddx=128, fill=0, dW=P[4], lddw=128,
