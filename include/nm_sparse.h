@@ -521,8 +521,9 @@ nm_status nm_mx_glu(const nm_mx* gate, const nm_mx* up, const nm_mx* xq, const v
 /* ------------------------------------------------------------------------
  * 8-bit rows: each row (a token's activations, or an output channel's weights)
  * as whole numbers with one binary32 scale.
- *   scale   = amax / 127 rounded to binary32, at least 2^-126 (a row of zeros
- *             has that too), amax the row's largest magnitude;
+ *   scale   = amax times 1/127 in binary32 (0x1.020408p-7, one rounded product: at
+ *             most one unit in the last place from amax / 127), at least 2^-126 (a
+ *             row of zeros has that too), amax the row's largest magnitude;
  *   element = the exact quotient x / scale rounded half to even, in [-127, 127].
  * A row that holds a NaN or an infinity gets a NaN scale and elements of 0: all
  * of it reads back as NaN.  Layout: row r's elements at r * Kp bytes, Kp = K

@@ -944,8 +944,8 @@ class I8:
 
 def i8_quantize(X: torch.Tensor) -> I8:
     """nm_i8_quantize: X [rows, K] (float16, bfloat16 or float32) as 8-bit rows:
-    scale = amax / 127 of the row (float32, at least 2^-126), elements the exact
-    quotient rounded half to even.  For activations a row is a token, for
+    scale = amax times 1/127 (float32, at least 2^-126), elements the exact quotient
+    by it rounded half to even.  For activations a row is a token, for
     weights an output channel."""
     if X.dim() != 2:
         raise ValueError("X must be a 2-D tensor")

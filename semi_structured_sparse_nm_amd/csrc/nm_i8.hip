@@ -1,6 +1,6 @@
 // 8-bit rows: quantiser and its inverse.
 //
-//   scale[t] = amax(row t) / 127, rounded to binary32, at least 2^-126
+//   scale[t] = amax(row t) x 1/127 in binary32, at least 2^-126
 //   element  = x / scale rounded half to even, of the exact quotient
 //
 // The quantiser reads each row once: a wave (rows of up to 2048 elements) or a

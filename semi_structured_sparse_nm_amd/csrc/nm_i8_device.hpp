@@ -67,13 +67,14 @@ struct Eight {
   }
 };
 
+constexpr float kInv127 = 0x1.020408p-7f;              // 1 / 127, rounded
 // the row's scale from its largest magnitude's bits; NaN where that is no number
 template <int DT>
 __device__ __forceinline__ float scale_of(uint32_t top) {
   constexpr uint32_t inf = DT == NM_F32 ? 0x7F800000u : DT == NM_BF16 ? 0x7F80u : 0x7C00u;
   if (top >= inf) return __builtin_bit_cast(float, 0x7FC00000u);
   const float amax = DT == NM_F32 ? __builtin_bit_cast(float, top) : from_16<DT == NM_F32 ? NM_BF16 : DT>(top);
-  return fmaxf(amax / 127.0f, 0x1p-126f);
+  return fmaxf(amax * kInv127, 0x1p-126f);
 }
 
 // x / s to the nearest whole number, half to even, in the low byte (r: 1 / s

@@ -15,13 +15,14 @@ from tests._ffn import act64, act_err, kept, sum_err
 
 def i8_64(x):
     """(elements, scales) of x's rows from the definition, int64 and float32:
-    the scale amax / 127 rounded to binary32, at least 2^-126; the nearest whole
-    number of the exact quotient, the even one on a tie (whole-number
-    arithmetic on the mantissas); rows that are not finite: NaN and zeros."""
+    the scale amax times binary32's 1 / 127, rounded to binary32, at least 2^-126;
+    the nearest whole number of the exact quotient, the even one on a tie; rows
+    that are not finite: NaN and zeros."""
     x = x.double()
     fin = torch.isfinite(x).all(dim=1)
     f = torch.where(fin[:, None], x, torch.zeros_like(x))
-    s = (f.abs().amax(dim=1) / 127.0).float().clamp(min=2.0 ** -126)
+    # (a product of two binary32 numbers is exact in binary64)
+    s = (f.abs().amax(dim=1) * float.fromhex("0x1.020408p-7")).float().clamp(min=2.0 ** -126)
     u = f / s.double()[:, None]
     # a binary32 value over another is no closer than 2^-25 to a half without
     # being one, far beyond binary64's error of the quotient
