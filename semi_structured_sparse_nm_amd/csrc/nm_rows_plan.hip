@@ -28,18 +28,18 @@ Kind kind_of(const Geometry& g) {
   return 8 * g.N / g.M <= 4 ? FEW : MANY;
 }
 
-// Microseconds: a workgroup besides its slabs, a slab, and (wide, 64 rows) what a
-// further workgroup on the compute unit costs of one alone.
+// Microseconds: a workgroup besides its slabs, a slab, and what a further workgroup
+// on the compute unit costs of one alone.
 struct Wide {
   double base, slab, more;
 };
 constexpr Wide kWide[2][2][KINDS] = {
     // 8 bits (slabs of 128 columns): 64 rows, 128 rows
     {{{4.81, 0.528, 0.938}, {5.89, 0.935, 0.962}, {4.93, 0.729, 0.852}, {5.54, 1.03, 0.853}, {}},
-     {{5.96, 0.613, 1.0}, {7.65, 0.969, 1.0}, {6.61, 0.967, 1.0}, {6.89, 1.21, 1.0}, {}}},
+     {{6.22, 0.611, 1.32}, {7.90, 0.964, 1.11}, {6.82, 0.968, 1.16}, {7.58, 1.19, 1.13}, {}}},
     // 16 bits (64 columns)
     {{{3.01, 0.455, 1.0}, {4.57, 0.938, 0.992}, {4.23, 0.577, 0.895}, {4.46, 0.707, 0.932}, {4.95, 1.24, 0.925}},
-     {{4.59, 0.556, 1.0}, {5.81, 0.993, 1.0}, {5.29, 0.825, 1.0}, {5.80, 0.952, 1.0}, {5.86, 1.44, 1.0}}}};
+     {{5.17, 0.541, 1.40}, {6.51, 0.969, 1.19}, {6.08, 0.817, 1.11}, {6.20, 0.939, 1.33}, {6.78, 1.43, 1.20}}}};
 
 // A workgroup besides its blocks, a wave's block, and that for each 16-row tile.
 struct Stream {
@@ -84,8 +84,10 @@ double rounds(double n, int64_t E, int cus, double more) {
 
 double wide_time(const Geometry& g, int64_t T, int64_t E, int tm, double bytes, int cus) {
   const Wide& w = kWide[g.eb - 1][tm == 8][kind_of(g)];
-  const double r = rounds(units(T, E, 16 * tm) * (double)ceil_div(g.R, 256), E, cus, 0.55);
-  return 3.0 + std::max((w.base + g.nKB * w.slab) * std::max(1.0, w.more * r), bytes / kRate);
+  const double n = units(T, E, 16 * tm) * (double)ceil_div(g.R, 256), r = rounds(n, E, cus, 0.55);
+  // (two workgroups of 64 rows share a compute unit, those of 128 follow each other)
+  const double in_turn = tm == 4 ? std::max(1.0, w.more * r) : n <= cus ? 1.0 : 1.0 + w.more * (r - 1.0);
+  return 3.0 + std::max((w.base + g.nKB * w.slab) * in_turn, bytes / kRate);
 }
 
 double stream_time(const Geometry& g, int64_t T, int64_t E, double bytes, int cus) {
