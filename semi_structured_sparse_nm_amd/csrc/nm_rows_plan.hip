@@ -3,8 +3,8 @@
 // Fitted to 1084 products of 17 to 2048 rows an expert, 1 to 64 experts, 300 to
 // 11008 outputs, K 512 to 11008, seven patterns, 8 and 16 bits, every path and tile
 // shape measured with weights that change between calls: the wide and tile models
-// are 5 to 10% off as a root mean square, the streamed one 30%; the choice costs 2%
-// against the fastest path as a mean over them, 10% in one of ten, 60% at most.
+// are 5 to 10% off as a root mean square, the streamed one 30%; the choice costs 1.9%
+// against the fastest path as a mean over them, 9% in one of ten, 52% at most.
 // For example, streamed, wide (64 rows), wide (128), best tiles, in microseconds:
 // 8-bit 4:8, 48 rows, 11008 x 4096 25, 33, 41, 42; 256 rows 59, 34, 41, 49; 32 experts
 // of 1536 x 2048, 16-bit 4:8, 256 rows 42, 30, 37, 149, 4096 rows -, 49, 63, 175;
@@ -146,7 +146,9 @@ int cols_tile_shape(int64_t T, int64_t E, int64_t R, int64_t K, int cus) {
 }
 
 RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus) {
-  RowsPlan tiles{g.N == 2 && g.M == 4 ? ROWS_SPARSE : repack24_supported(g) ? ROWS_REPACK : ROWS_DENSE, 0};
+  // (re-packing takes up to 64 threads a block in one launch)
+  const bool repack = repack24_supported(g) && E * g.nRB * g.nKB < (1ll << 26);
+  RowsPlan tiles{g.N == 2 && g.M == 4 ? ROWS_SPARSE : repack ? ROWS_REPACK : ROWS_DENSE, 0};
   double time;
   tiles.shape = rows_tile_shape(tiles.path != ROWS_DENSE, g.eb == 1, T, E, g.R, g.nKB, cus, &time);
   // a launch has fewer than 2^32 threads

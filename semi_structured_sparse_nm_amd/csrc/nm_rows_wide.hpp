@@ -81,16 +81,19 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   };
   auto load_rows = [&](Rows& r, int s) __attribute__((always_inline)) {
     s = min(s, last);
-    // (a piece past the row's end meets weights that are zero: the slab's first
-    // one, so that no branch splits the loads)
+    // (a piece past the row's end: the slab's first one, so that no branch splits
+    // the loads; store_rows makes it zeros)
     const uint32_t p = s * Frag::SLAB + 16 / XB * piece < KX ? 16 * piece : 0;
 #pragma unroll
     for (int i = 0; i < NP; ++i) r.x[i] = load16(x0 + s * 128 + (xoff[i] + p));
   };
   const int put = row0 * 128 + 16 * (piece ^ (row0 & 7));
-  auto store_rows = [&](const Rows& r, int p) __attribute__((always_inline)) {
+  // (8-bit rows are whole slabs)
+  auto store_rows = [&](const Rows& r, int s, int p) __attribute__((always_inline)) {
+    const bool in = WT == NM_I8 || s * Frag::SLAB + 16 / XB * piece < KX;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) *reinterpret_cast<v4i*>(rows[p] + put + NW * 1024 * i) = r.x[i];
+    for (int i = 0; i < NP; ++i)
+      *reinterpret_cast<v4i*>(rows[p] + put + NW * 1024 * i) = in ? r.x[i] : v4i{0, 0, 0, 0};
   };
   struct Blocks {
     Frag f[2];
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   // of s + 2, b the blocks of s
   auto step = [&](int s, auto pc, Rows& r1, Blocks& b) __attribute__((always_inline)) {
     constexpr int P = decltype(pc)::value;
-    store_rows(r1, P ^ 1);
+    store_rows(r1, s + 1, P ^ 1);
     load_rows(r1, s + 3);
     // (each row tile is read from LDS before the products of the one in front of it)
     v4i x0[2], x1[2];
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   load_rows(r1, 1);
   load_blocks(b0, 0);
   __builtin_amdgcn_sched_barrier(0);
-  store_rows(r0, 0);
+  store_rows(r0, 0, 0);
   load_rows(r0, 2);
   __builtin_amdgcn_sched_barrier(0);
   load_blocks(b1, 1);
