@@ -44,10 +44,12 @@ __global__ void __launch_bounds__(256) rows_dense_kernel(Geometry g, const uint8
 // blocks, and the kept bits.  Pitch 130 halves: the four 16-column runs of a
 // packed row and its block's sixteen rows fall on different banks.
 __device__ __forceinline__ void prepare_weight(const RowsPrepareArgs& a, int64_t b, uint16_t* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
   uint16_t(*tile)[130] = reinterpret_cast<uint16_t(*)[130]>(lds);
   const Geometry& g = a.g;
   const int64_t rt = (g.R + 127) / 128, e = b / (rt * g.nKB);
   if (!may_have_rows(a.rows, (int)e)) return;
+  uint16_t* kept = reinterpret_cast<uint16_t*>(a.mask + b * 1024);
   b -= e * rt * g.nKB;
   const int64_t kb = b % g.nKB, r0 = (b / g.nKB) * 128;
   const uint8_t* values = a.values + e * (int64_t)g.values_bytes();
@@ -59,9 +61,18 @@ __device__ __forceinline__ void prepare_weight(const RowsPrepareArgs& a, int64_t
     const int64_t r = r0 + rl;
     uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
     if (r < g.R) {
-      const uint32_t keep = expand16(g, values, meta, r, kb * 64 + cl, o);
-      if (a.mask)
-        *reinterpret_cast<uint16_t*>(a.mask + (e * g.R + r) * (g.nKB * 8) + kb * 8 + cl / 8) = (uint16_t)keep;
+      const int keep = (int)expand16(g, values, meta, r, kb * 64 + cl, o);
+      if (a.mask) {
+        // four lanes have a row's sixteen columns each: lane lq gathers bits 4 lq ..
+        const int lq = lane & 3;
+        const int k0 = __builtin_amdgcn_update_dpp(0, keep, 0x00, 0xf, 0xf, false);
+        const int k1 = __builtin_amdgcn_update_dpp(0, keep, 0x55, 0xf, 0xf, false);
+        const int k2 = __builtin_amdgcn_update_dpp(0, keep, 0xaa, 0xf, 0xf, false);
+        const int k3 = __builtin_amdgcn_update_dpp(0, keep, 0xff, 0xf, 0xf, false);
+        auto four = [&](int k) { return k >> (4 * lq) & 15; };
+        kept[(lq * 16 + (lane >> 2)) * 8 + rl / 16] =
+            (uint16_t)(four(k0) | four(k1) << 4 | four(k2) << 8 | four(k3) << 12);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) tile[cl + i][rl] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
@@ -81,6 +92,7 @@ __device__ __forceinline__ void prepare_weight(const RowsPrepareArgs& a, int64_t
           v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
     }
   }
+#endif
 }
 
 // 64 rows of one expert (zeros behind its last) x 64 columns of x, transposed.
@@ -107,7 +119,7 @@ __device__ __forceinline__ void prepare_rows(const RowsPrepareArgs& a, const uin
     const int cl = q >> 3, tl = (q & 7) * 8;
     if (c0 + cl < cols) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[cl][tl]);
-      *reinterpret_cast<v4i*>(xt + (c0 + cl) * (64 * a.slabs) + 64 * (int64_t)slab + tl) =
+      *reinterpret_cast<v4i*>(xt + (slab * cols + c0 + cl) * 64 + tl) =
           v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
     }
   }

@@ -103,9 +103,10 @@ hipError_t launch_rows_wide_bf16(const RowsArgs& a, int tm, hipStream_t s);
 //              an expert's ceil(Nr / 16) x nslab one after another, then the
 //              next expert's.
 //   TILE_COLS  C_e[m][n] = keep (.) sum over expert e's rows of A[m][t] B[n][t]:
-//              both operands with the rows along the reduction, expert e's from
-//              slab slab_at[e] of 64 on, each expert's padded with zeros to
-//              whole slabs, one at least.
+//              both operands with the rows along the reduction, in slabs of 64
+//              of them (Mr or Nr columns x 128 bytes, a slab's one after another: a
+//              tile's part of a slab is one piece of memory), each expert's rows
+//              padded with zeros to whole slabs, one at least.
 struct RowsTile : TileArgs {
   RowGroups rows;
   const uint8_t* meta;       // sparse TILE_ROWS
@@ -113,9 +114,13 @@ struct RowsTile : TileArgs {
   const float* wscale;
   bool zero_rest;            // TILE_ROWS: rows of no expert become zeros
   int64_t es;                // TILE_COLS: elements between experts' outputs
-  const uint8_t* mask;       // and kept bits, [E][Mr][ldm]: bit k % 8 of byte k / 8
-  int64_t ldm;
+  const uint8_t* mask;       // and kept bits, one block for 128 rows x 64 columns
+  int64_t ldm;               // blocks along a row
 };
+// Kept bits as the weight gradients' lanes need them, 1 KB a block of 128 rows x
+// 64 columns: 16 bytes of lane 16 lq + li, 16 bits a row tile j of them: bits 4 i + v
+// of row 16 j + li, columns 16 i + 4 lq + v.
+inline int64_t kept_blocks(int64_t R, int64_t nKB) { return (R + 127) / 128 * nKB; }
 // et: TILE_F16, TILE_BF16 (outputs of that type) or TILE_I8 (TILE_ROWS only)
 hipError_t launch_rows_tile(int et, TileOp op, int ydt, const RowsTile& a, hipStream_t s);
 // TILE_ROWS on 2:4 weights
@@ -129,8 +134,8 @@ hipError_t launch_rows_dense(const Geometry& g, const uint8_t* values, const uin
 
 // Operands of the gradients (16-bit): each expert's weight transposed, in
 // blocks as above (wt: K rows, Rp = R rounded up to 64 columns) where it has
-// rows; its kept bits, mask [E][R][Kp / 8]; X and dY transposed, xt [K][ld] and
-// yt [R][ld], columns as ColsTileArgs has them.  Null outputs are left out.
+// rows; its kept bits, mask [E][kept_blocks]; X and dY transposed, xt [slabs][K][64]
+// and yt [slabs][R][64], slabs as TILE_COLS has them.  Null outputs are left out.
 struct RowsPrepareArgs {
   Geometry g;
   RowGroups rows;
@@ -140,7 +145,7 @@ struct RowsPrepareArgs {
   int64_t ldx;
   const uint16_t* dY;
   int64_t lddy;
-  int64_t slabs;             // most slabs of rows; ld = 64 slabs
+  int64_t slabs;             // most slabs of rows
   uint16_t* wt;
   uint8_t* mask;
   uint16_t* xt;

@@ -248,7 +248,7 @@ struct BackwardPlan {
     Rp = up64(g.R);
     slabs = T / 64 + w.E;
     wt = dx ? up256((size_t)(w.E * ((g.K + 15) / 16) * (Rp / 64) * 2048)) : 0;
-    mask = dw ? up256((size_t)(w.E * g.R * g.nKB * 8)) : 0;
+    mask = dw ? (size_t)(w.E * nm::kept_blocks(g.R, g.nKB) * 1024) : 0;
     xt = dw ? up256((size_t)(g.K * slabs * 128)) : 0;
     yt = dw ? up256((size_t)(g.R * slabs * 128)) : 0;
     pad = dx && pad_dy ? padded_bytes(T, g.R) : 0;
@@ -487,14 +487,14 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
     t.rows = rows;
     t.A = yt;
     t.B[0] = xt;
-    t.lda = t.ldb = p.slabs * 128;
+    t.lda = t.ldb = 128;
     t.Mr = g.R;
     t.Nr = g.K;
     t.C = dW;
     t.ldc = lddw;
     t.es = g.R * lddw;
     t.mask = mask;
-    t.ldm = g.nKB * 8;
+    t.ldm = g.nKB;
     t.shape = nm::cols_tile_shape(T, ww.E, g.R, g.K, cus);
     if (nm::launch_rows_tile(tile_type(ww.dtype), nm::TILE_COLS, ww.dtype, t, s) != hipSuccess) return NM_EHIP;
   }

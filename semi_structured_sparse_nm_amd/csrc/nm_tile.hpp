@@ -152,6 +152,8 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   auto cursor_item = [&](int k) __attribute__((always_inline)) {
     const TileItem it = walk.item(k);
     const int64_t m0 = EROWS ? (int64_t)it.row : (int64_t)it.m * BM, n0 = (int64_t)it.n * BNO;
+    // (TILE_COLS: rows of the first slab, as if they were a matrix's)
+    const int64_t ma = COLS ? it.s0 * a.Mr + m0 : m0, nb = COLS ? it.s0 * a.Nr + n0 : n0;
     auto tile_rsrc = [&](const uint8_t* p, int64_t row0, int64_t ld) {
       const v4i r = make_rsrc(p + row0 * ld, 0x7fffffff);
       return v4i{scalar(r[0]), scalar(r[1]), r[2], r[3]};
@@ -170,11 +172,11 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
                           : min(load_row(jc), nlast) * (int)ldb + 16 * piece;
       }
     });
-    ra = tile_rsrc(grad ? (it.batch > 1 ? a.w.A[1] : a.w.A[0]) : a.A, m0, lda);
+    ra = tile_rsrc(grad ? (it.batch > 1 ? a.w.A[1] : a.w.A[0]) : a.A, ma, lda);
     if constexpr (EROWS)
       rb0 = tile_rsrc(a.B[0], (int64_t)it.batch * ((a.Nr + 15) / 16) + n0 / 16, (int64_t)a.nslab * 2048);
     else
-      rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], n0, ldb);
+      rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], nb, ldb);
     if constexpr (GLU && !SPAN) rb1 = tile_rsrc(a.B[1], n0, ldb);
     if constexpr (MX) {
       // unit u of a stage: LDS rows 32 u ..; row groups past the end repeat the last one
@@ -203,7 +205,7 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
     constexpr int j = decltype(jc)::value;
     uint8_t* sp = lds + st * STAGE;
     if constexpr (j < NL) {
-      const int so = scalar(cs * (EROWS && j >= NLA ? 2048 : 128));
+      const int so = COLS ? 0 : scalar(cs * (EROWS && j >= NLA ? 2048 : 128));
       const uint32_t dst = lds_addr(sp + 1024 * (wave + NW * j));
       constexpr bool UP = GLU && !SPAN && ((RJ * j - BM) / HB & 1);
       lds_dma16(j < NLA ? ra : (UP ? rb1 : rb0), dst, voff[j] | (j < NLA ? ca : cb), so);
@@ -225,6 +227,15 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   auto advance = [&]() __attribute__((always_inline)) {
     if (__builtin_expect(cs + 1 < ce, 1)) {
       ++cs;
+      if constexpr (COLS) {
+        auto next_slab = [](v4i& r, int64_t bytes) __attribute__((always_inline)) {
+          const uint64_t p = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + bytes;
+          r[0] = (int)p;
+          r[1] = (int)(p >> 32);
+        };
+        next_slab(ra, a.Mr * 128);
+        next_slab(rb0, a.Nr * 128);
+      }
     } else if (ck + 1 < walk.count) {
       asm volatile("" ::: "memory");                    // a branch, not selects around it
       cursor_item(++ck);
@@ -306,6 +317,14 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   int st = 0;
   for (int k = 0; k < walk.count; ++k) {
     const TileItem it = walk.item(k);
+    const int64_t m0 = (EROWS ? (int64_t)it.row : (int64_t)it.m * BM) + wm * TM * 16;
+    const int64_t n0 = (int64_t)it.n * BNO + wn * (BNO / WN);
+    v4i kept = {0, 0, 0, 0};
+    if constexpr (COLS) {
+      if (m0 < a.Mr && n0 < a.Nr)
+        kept = *reinterpret_cast<const v4i*>(
+            a.mask + ((it.batch * ((a.Mr + 127) / 128) + (m0 >> 7)) * a.ldm + (n0 >> 6)) * 1024 + 16 * lane);
+    }
     for (int s = it.s0; s < it.s1; ++s) {
       static_for<0, TN>([&](auto i) {
         constexpr int I = decltype(i)::value;
@@ -336,11 +355,13 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
       c0 = c1;
       st = nx;
     }
-    if constexpr (GROUPED)
-      rows_epilogue<OP, OUT, TM, TN>(a, it, (EROWS ? it.row : it.m * BM) + wm * TM * 16,
-                                     (int64_t)it.n * BNO + wn * (BNO / WN), acc);
-    else
-      tile_epilogue<OP, OUT, TM, TN>(a, it, (int64_t)it.m * BM + wm * TM * 16, (int64_t)it.n * BNO + wn * (BNO / WN), acc);
+    if constexpr (COLS) {
+      tile_cols<OUT>(a, it, m0, n0, kept, acc);
+    } else if constexpr (EROWS) {
+      rows_epilogue<OP, OUT, TM, TN>(a, it, m0, n0, acc);
+    } else {
+      tile_epilogue<OP, OUT, TM, TN>(a, it, m0, n0, acc);
+    }
     clear();
   }
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));           // nothing lands in LDS after this

@@ -208,22 +208,26 @@ struct TileWalk {
 // anywhere (past them 2048 x 4098 outputs at 4 bits, K 4096, take 39 us against 32).
 // y0, y1: the lane's four values of each tile; n: first column of the pair.
 template <int OUT>
+__device__ __forceinline__ v4i pair_of(const float* y0, const float* y1) {
+  uint32_t a0 = pack_16x2<OUT>(y0[0], y0[1]), a1 = pack_16x2<OUT>(y0[2], y0[3]);
+  uint32_t b0 = pack_16x2<OUT>(y1[0], y1[1]), b1 = pack_16x2<OUT>(y1[2], y1[3]);
+  // lane groups of a: 0 1 2 3, of b: 4 5 6 7 -> (0 1 | 4 5), (2 3 | 6 7) -> (0 2 4 6), (1 3 5 7)
+  auto swap = [](uint32_t& x, uint32_t& y) {
+    auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    auto q = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
+    x = q[0];
+    y = q[1];
+  };
+  swap(a0, b0);
+  swap(a1, b1);
+  return v4i{(int)a0, (int)a1, (int)b0, (int)b1};
+}
+template <int OUT>
 __device__ __forceinline__ void store_pair(void* C, int64_t row, int64_t n, int64_t N, int lq, const float* y0,
                                            const float* y1, bool whole) {
   if constexpr (OUT != NM_F32) {
     if (n + 32 <= N) {
-      uint32_t a0 = pack_16x2<OUT>(y0[0], y0[1]), a1 = pack_16x2<OUT>(y0[2], y0[3]);
-      uint32_t b0 = pack_16x2<OUT>(y1[0], y1[1]), b1 = pack_16x2<OUT>(y1[2], y1[3]);
-      // lane groups of a: 0 1 2 3, of b: 4 5 6 7 -> (0 1 | 4 5), (2 3 | 6 7) -> (0 2 4 6), (1 3 5 7)
-      auto swap = [](uint32_t& x, uint32_t& y) {
-        auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-        auto q = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
-        x = q[0];
-        y = q[1];
-      };
-      swap(a0, b0);
-      swap(a1, b1);
-      const v4i v = {(int)a0, (int)a1, (int)b0, (int)b1};
+      const v4i v = pair_of<OUT>(y0, y1);
       uint16_t* p = static_cast<uint16_t*>(C) + row + n + 8 * lq;
       if (whole) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(p));
       else *reinterpret_cast<v4i_any*>(p) = v;
@@ -335,14 +339,38 @@ __device__ __forceinline__ void tile_rows_i8(void* C, int64_t ldc, int64_t Mr, i
   }
 }
 
+// One wave's tiles of a weight gradient; kept: its bits (one 16-byte load a lane,
+// asked for before the item's products; read row by row in the epilogue they cost
+// 3 us a tile of 256 x 256).
+template <int OUT, int TM, int TN>
+__device__ __forceinline__ void tile_cols(const RowsTile& a, const TileItem& it, int64_t m0, int64_t n0, v4i kept,
+                                          const v4f (&acc)[TN][TM]) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lq = lane >> 4;
+  uint16_t* C = static_cast<uint16_t*>(a.C) + it.batch * a.es;
+  const bool whole = whole_pieces(a.C, a.ldc) && a.es % 8 == 0;
+  const int i0 = (int)(n0 >> 4) & 3, j0 = (int)(m0 >> 4) & 7;
+#pragma unroll
+  for (int i = 0; i < TN; i += 2)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int bits = (TM == 8 ? kept[j >> 1] : kept[(j0 + j) >> 1]) >> (16 * (j & 1) + 4 * (i0 + i));
+      const int64_t m = m0 + 16 * j + li;
+      float y[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          y[e][v] = bits >> (4 * e + v) & 1 ? acc[i + e][j][v] : 0.f;   // a select: NaN is masked too
+      __builtin_amdgcn_sched_barrier(0);                // one output's temporaries at a time
+      if (m < a.Mr) store_pair<OUT>(C, m * a.ldc, n0 + 16 * i, a.Nr, lq, y[0], y[1], whole);
+    }
+}
+
 // Epilogue of one wave's tiles of grouped rows.
 template <int OP, int OUT, int TM, int TN, class Acc>
 __device__ __forceinline__ void rows_epilogue(const RowsTile& a, const TileItem& it, int64_t m0, int64_t n0,
                                               const Acc (&acc)[TN][TM]) {
-  if constexpr (OP == TILE_COLS)
-    tile_rows<true, OUT, TM, TN>(static_cast<uint16_t*>(a.C) + it.batch * a.es, a.ldc, a.Mr, a.Nr, nullptr,
-                                 NM_ACT_NONE, a.mask + it.batch * a.Mr * a.ldm, a.ldm, m0, n0, acc);
-  else if constexpr (std::is_same<Acc, v4i>::value)
+  if constexpr (std::is_same<Acc, v4i>::value)
     tile_rows_i8<OUT, TM, TN>(a.C, a.ldc, it.end, a.Nr, a.xscale, a.wscale + it.batch * a.Nr,
                               a.bias ? a.bias + it.batch * a.Nr : nullptr, a.act, m0, n0, acc);
   else
