@@ -643,8 +643,7 @@ nm_status nm_expert_linear(const nm_experts* w, const void* Xt, int64_t ldx, int
  * the 16-bit tensors as they are, sums binary32, every output rounded once; the
  * result does not depend on launch order (no atomics).  Errors as
  * nm_expert_linear; NM_EINVAL also for no output, lddx < K, lddw < K, lddy < R;
- * NM_EUNSUPPORTED also where 64-row pieces of all experts' rows pass 2^31
- * bytes for 256 columns, or the operands' tiles a launch (2^24).
+ * NM_EUNSUPPORTED also where the weights' tiles of 128 x 64 pass a launch (2^24).
  */
 nm_status nm_expert_linear_backward_workspace_size(const nm_experts* w, int64_t T, size_t* bytes);
 nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T, const void* offsets,

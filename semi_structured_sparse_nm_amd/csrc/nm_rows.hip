@@ -1,6 +1,8 @@
-// Operands of the products of grouped rows: packed weights as dense blocks;
-// weights and rows transposed for the gradients.  All of them are bound by
+// Operands of the products of grouped rows: packed weights as dense blocks and
+// transposed, rows of whole slabs, for the gradients.  All of them are bound by
 // HBM: every element is read once and written once, in 16-byte pieces.
+#include <algorithm>
+
 #include "nm_expand_cols.hpp"
 #include "nm_rows.hpp"
 
@@ -95,47 +97,37 @@ __device__ __forceinline__ void prepare_weight(const RowsPrepareArgs& a, int64_t
 #endif
 }
 
-// 64 rows of one expert (zeros behind its last) x 64 columns of x, transposed.
-__device__ __forceinline__ void prepare_rows(const RowsPrepareArgs& a, const uint16_t* x, int64_t ldx, int64_t cols,
-                                             int slab, int64_t c0, uint16_t* xt, uint16_t* lds) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  uint16_t(*tile)[66] = reinterpret_cast<uint16_t(*)[66]>(lds);
-  const RowUnit u = find_unit<64, true>(a.rows, slab);
-  if (u.e < 0) return;
+constexpr int kPadPieces = 4 * 256;                     // of a workgroup in one step
+
+// x's rows as rows of whole slabs of 64 columns, by n workgroups, this one b.
+__device__ __forceinline__ void pad_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t cols, uint16_t* y,
+                                         int64_t b, int64_t n) {
+  const int64_t per = (cols + 63) / 64 * 8, total = T * per;
+  for (int64_t q0 = b * kPadPieces; q0 < total; q0 += n * kPadPieces) {
+    v4i o[4];
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int q = it * 256 + threadIdx.x;
-    const int tl = q >> 3, cl = (q & 7) * 8;
-    const int64_t t = u.row + tl, c = c0 + cl;
-    v4i o = {0, 0, 0, 0};
-    if (t < u.end && c < cols) o = load_piece(x + t * ldx, c, cols);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t q = q0 + 256 * i + threadIdx.x, t = q / per, c = (q - t * per) * 8;
+      o[i] = v4i{0, 0, 0, 0};
+      if (q < total && c < cols) o[i] = load_piece(x + t * ldx, c, cols);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile[cl + i][tl] = (uint16_t)((uint32_t)o[i >> 1] >> (16 * (i & 1)));
-  }
-  __syncthreads();
-#pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int q = it * 256 + threadIdx.x;
-    const int cl = q >> 3, tl = (q & 7) * 8;
-    if (c0 + cl < cols) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(&tile[cl][tl]);
-      *reinterpret_cast<v4i*>(xt + (slab * cols + c0 + cl) * 64 + tl) =
-          v4i{(int)p[0], (int)p[1], (int)p[2], (int)p[3]};
+    for (int i = 0; i < 4; ++i) {
+      const int64_t q = q0 + 256 * i + threadIdx.x;
+      if (q < total) *reinterpret_cast<v4i*>(y + q * 8) = o[i];
     }
   }
-#endif
 }
 
 // What the gradients' products read, in one launch; workgroups take, by index,
-// tiles of the weights, of X and of dY.  The tiles pass through LDS.
+// tiles of the weights (they pass through LDS), rows of X and of dY.
 __global__ void __launch_bounds__(256) rows_prepare_kernel(RowsPrepareArgs a, int64_t n_weight, int64_t n_x) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[64 * 130];
   int64_t b = blockIdx.x;
   if (b < n_weight) return prepare_weight(a, b, lds);
   b -= n_weight;
-  if (b < n_x) return prepare_rows(a, a.X, a.ldx, a.g.K, (int)(b % a.slabs), b / a.slabs * 64, a.xt, lds);
-  b -= n_x;
-  prepare_rows(a, a.dY, a.lddy, a.g.R, (int)(b % a.slabs), b / a.slabs * 64, a.yt, lds);
+  if (b < n_x) return pad_rows(a.X, a.ldx, a.rows.T, a.g.K, a.xp, b, n_x);
+  pad_rows(a.dY, a.lddy, a.rows.T, a.g.R, a.yp, b - n_x, (int64_t)gridDim.x - n_weight - n_x);
 }
 
 }  // namespace
@@ -155,8 +147,10 @@ hipError_t launch_rows_dense(const Geometry& g, const uint8_t* values, const uin
 
 hipError_t launch_rows_prepare(const RowsPrepareArgs& a, hipStream_t s) {
   const int64_t n_weight = a.wt || a.mask ? a.rows.E * ((a.g.R + 127) / 128) * a.g.nKB : 0;
-  const int64_t n_x = a.xt ? a.slabs * ((a.g.K + 63) / 64) : 0;
-  const int64_t n_y = a.yt ? a.slabs * ((a.g.R + 63) / 64) : 0;
+  auto pads = [&](int64_t cols) {
+    return std::min<int64_t>((a.rows.T * ((cols + 63) / 64) * 8 + kPadPieces - 1) / kPadPieces, 4096);
+  };
+  const int64_t n_x = a.xp ? pads(a.g.K) : 0, n_y = a.yp ? pads(a.g.R) : 0;
   hipLaunchKernelGGL(rows_prepare_kernel, dim3((unsigned)(n_weight + n_x + n_y)), dim3(256), 0, s, a, n_weight, n_x);
   return hipGetLastError();
 }

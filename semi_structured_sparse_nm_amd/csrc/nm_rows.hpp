@@ -102,11 +102,8 @@ hipError_t launch_rows_wide_bf16(const RowsArgs& a, int tm, hipStream_t s);
 //              64, with positions), nslab of them side by side, the blocks of
 //              an expert's ceil(Nr / 16) x nslab one after another, then the
 //              next expert's.
-//   TILE_COLS  C_e[m][n] = keep (.) sum over expert e's rows of A[m][t] B[n][t]:
-//              both operands with the rows along the reduction, in slabs of 64
-//              of them (Mr or Nr columns x 128 bytes, a slab's one after another: a
-//              tile's part of a slab is one piece of memory), each expert's rows
-//              padded with zeros to whole slabs, one at least.
+//   TILE_COLS  C_e[m][n] = keep (.) sum over expert e's rows t of A[t][m] B[t][n]:
+//              rows of lda and ldb bytes, of which ka and kb 16-byte pieces count.
 struct RowsTile : TileArgs {
   RowGroups rows;
   const uint8_t* meta;       // sparse TILE_ROWS
@@ -134,8 +131,8 @@ hipError_t launch_rows_dense(const Geometry& g, const uint8_t* values, const uin
 
 // Operands of the gradients (16-bit): each expert's weight transposed, in
 // blocks as above (wt: K rows, Rp = R rounded up to 64 columns) where it has
-// rows; its kept bits, mask [E][kept_blocks]; X and dY transposed, xt [slabs][K][64]
-// and yt [slabs][R][64], slabs as TILE_COLS has them.  Null outputs are left out.
+// rows; its kept bits, mask [E][kept_blocks]; X and dY in rows of whole slabs of
+// 64 columns, the last filled with zeros (xp, yp).  Null outputs are left out.
 struct RowsPrepareArgs {
   Geometry g;
   RowGroups rows;
@@ -145,11 +142,10 @@ struct RowsPrepareArgs {
   int64_t ldx;
   const uint16_t* dY;
   int64_t lddy;
-  int64_t slabs;             // most slabs of rows
   uint16_t* wt;
   uint8_t* mask;
-  uint16_t* xt;
-  uint16_t* yt;
+  uint16_t* xp;
+  uint16_t* yp;
 };
 hipError_t launch_rows_prepare(const RowsPrepareArgs& a, hipStream_t s);
 
@@ -186,12 +182,11 @@ __device__ __forceinline__ int wave_scan_add(int v) {
   return wave_scan(v, [](int x, int y) { return x + y; });
 }
 
-// Experts' first rows and first units (of U rows; with LEAST an expert without
-// rows has one), a wave's lanes 64 boundaries at a time: f(i, from, at, unit, n)
-// for the lane's boundary i: the expert in front of it has the rows from .. at -
-// 1 and the units unit - n .. unit - 1 (i = 0 and i > E: none).  f returns
-// whether to stop, the same in every lane.
-template <int U, bool LEAST, class F>
+// Experts' first rows and first units (of U rows), a wave's lanes 64 boundaries at
+// a time: f(i, from, at, unit, n) for the lane's boundary i: the expert in front of
+// it has the rows from .. at - 1 and the units unit - n .. unit - 1 (i = 0 and i > E:
+// none).  f returns whether to stop, the same in every lane.
+template <int U, class F>
 __device__ __forceinline__ void row_boundaries(const RowGroups& o, F&& f) {
   const int lane = threadIdx.x & 63;
   int last = 0, units = 0;                              // of the boundaries before this chunk
@@ -202,7 +197,6 @@ __device__ __forceinline__ void row_boundaries(const RowGroups& o, F&& f) {
     int p = __builtin_amdgcn_update_dpp(0, v, 0x138, 0xf, 0xf, false);   // the lane before
     if (lane == 0) p = c ? last : v;
     int n = (v - p + U - 1) / U;
-    if (LEAST && n == 0) n = 1;
     if (i == 0 || i > o.E) n = 0;
     const int u = wave_scan_add(n) + units;
     if (f(i, p, v, u, n)) return;
@@ -218,7 +212,7 @@ __device__ __forceinline__ void row_boundaries(const RowGroups& o, F&& f) {
 struct RowUnit {
   int e, row, begin, end, n;
 };
-template <int U, bool LEAST>
+template <int U>
 __device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int L, int nt = 1) {
   RowUnit r = {-1, 0, 0, 0, 0};
   if (!o.at) {
@@ -229,7 +223,7 @@ __device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int L, int nt =
     r.e = r.n < nt ? 0 : -1;
     return r;
   }
-  row_boundaries<U, LEAST>(o, [&](int i, int from, int at, int u, int n) {
+  row_boundaries<U>(o, [&](int i, int from, int at, int u, int n) {
     const uint64_t hit = __ballot(u * nt > L && (u - n) * nt <= L);
     if (!hit) return false;
     const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
@@ -246,11 +240,11 @@ __device__ __forceinline__ RowUnit find_unit(const RowGroups& o, int L, int nt =
 }
 
 // Units of all rows (called by whole waves).
-template <int U, bool LEAST>
+template <int U>
 __device__ __forceinline__ int count_units(const RowGroups& o) {
   if (!o.at) return (int)((o.T + U - 1) / U);
   int n = 0;
-  row_boundaries<U, LEAST>(o, [&](int, int, int, int u, int) {
+  row_boundaries<U>(o, [&](int, int, int, int u, int) {
     n = __builtin_amdgcn_readlane(u, 63);
     return false;
   });

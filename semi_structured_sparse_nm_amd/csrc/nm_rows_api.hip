@@ -241,18 +241,14 @@ RowGroups groups_of(const void* offsets, int32_t dtype, int64_t E, int64_t T) {
 
 // ---------------------------------------------------------------- gradients
 struct BackwardPlan {
-  int64_t Rp, slabs;
-  size_t wt, mask, xt, yt, pad, total;       // bytes of each part
-  BackwardPlan(const Weights& w, int64_t T, bool dx, bool dw, bool pad_dy) {
+  size_t wt, mask, xp, yp, total;            // bytes of each part
+  BackwardPlan(const Weights& w, int64_t T, bool dx, bool dw, bool pad_x, bool pad_y) {
     const Geometry& g = w.g;
-    Rp = up64(g.R);
-    slabs = T / 64 + w.E;
-    wt = dx ? up256((size_t)(w.E * ((g.K + 15) / 16) * (Rp / 64) * 2048)) : 0;
+    wt = dx ? up256((size_t)(w.E * ((g.K + 15) / 16) * (up64(g.R) / 64) * 2048)) : 0;
     mask = dw ? (size_t)(w.E * nm::kept_blocks(g.R, g.nKB) * 1024) : 0;
-    xt = dw ? up256((size_t)(g.K * slabs * 128)) : 0;
-    yt = dw ? up256((size_t)(g.R * slabs * 128)) : 0;
-    pad = dx && pad_dy ? padded_bytes(T, g.R) : 0;
-    total = wt + mask + xt + yt + pad;
+    xp = dw && pad_x ? padded_bytes(T, g.K) : 0;
+    yp = pad_y ? padded_bytes(T, g.R) : 0;
+    total = wt + mask + xp + yp;
   }
 };
 
@@ -261,9 +257,8 @@ nm_status check_backward(const Weights& w, int64_t T) {
   const nm_status st = check_sizes(w, T);
   if (st != NM_OK) return st;
   const Geometry& g = w.g;
-  const int64_t slabs = T / 64 + w.E;
-  if (!row_ok(slabs * 128) || !row_ok(up64(g.R) * 2)) return NM_EUNSUPPORTED;
-  if (w.E * ((g.R + 127) / 128) * g.nKB + slabs * (g.nKB + up64(g.R) / 64) >= kMaxGrid) return NM_EUNSUPPORTED;
+  if (!row_ok(up64(g.R) * 2)) return NM_EUNSUPPORTED;
+  if (w.E * nm::kept_blocks(g.R, g.nKB) + 2 * 4096 >= kMaxGrid) return NM_EUNSUPPORTED;
   return NM_OK;
 }
 
@@ -411,7 +406,7 @@ nm_status nm_expert_linear_backward_workspace_size(const nm_experts* w, int64_t 
   if (!bytes) return NM_EINVAL;
   st = check_backward(ww, T);
   if (st != NM_OK) return st;
-  *bytes = BackwardPlan(ww, T, true, true, true).total;
+  *bytes = BackwardPlan(ww, T, true, true, true, true).total;
   return NM_OK;
 }
 
@@ -430,16 +425,15 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
   st = check_offsets(offsets, offsets_dtype);
   if (st != NM_OK) return st;
   if (!aligned(Xt, 2) || !aligned(dY, 2) || !aligned(dX, 2) || !aligned(dW, 2)) return NM_EUNSUPPORTED;
-  const bool direct = rows_direct(ROWS_DENSE, dY, lddy, g.R);
-  const BackwardPlan p(ww, T, dX != nullptr, dW != nullptr, !direct);
+  const bool pad_x = dW && !rows_direct(ROWS_DENSE, Xt, ldx, g.K), pad_y = !rows_direct(ROWS_DENSE, dY, lddy, g.R);
+  const BackwardPlan p(ww, T, dX != nullptr, dW != nullptr, pad_x, pad_y);
   if (!workspace || workspace_bytes < p.total) return NM_EINVAL;
   if (!aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* wt = static_cast<uint8_t*>(workspace);
   uint8_t* mask = wt + p.wt;
-  uint8_t* xt = mask + p.mask;
-  uint8_t* yt = xt + p.xt;
-  uint8_t* pad = yt + p.yt;
+  uint8_t* xp = mask + p.mask;
+  uint8_t* yp = xp + p.xp;
   const RowGroups rows = groups_of(offsets, offsets_dtype, ww.E, T);
   const int cus = nm::device_cu_count();
 
@@ -452,29 +446,26 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
   q.ldx = ldx;
   q.dY = static_cast<const uint16_t*>(dY);
   q.lddy = lddy;
-  q.slabs = p.slabs;
   q.wt = dX ? reinterpret_cast<uint16_t*>(wt) : nullptr;
   q.mask = dW ? mask : nullptr;
-  q.xt = dW ? reinterpret_cast<uint16_t*>(xt) : nullptr;
-  q.yt = dW ? reinterpret_cast<uint16_t*>(yt) : nullptr;
+  q.xp = pad_x ? reinterpret_cast<uint16_t*>(xp) : nullptr;
+  q.yp = pad_y ? reinterpret_cast<uint16_t*>(yp) : nullptr;
   if (nm::launch_rows_prepare(q, s) != hipSuccess) return NM_EHIP;
+  const int64_t Rp = up64(g.R), Kp = up64(g.K);
+  const uint8_t* y = pad_y ? yp : static_cast<const uint8_t*>(dY);
+  const int64_t ldy = pad_y ? Rp * 2 : lddy * 2;
+  const int ky = (int)((pad_y ? Rp : g.R) / 8);
   if (dX) {
     // dX[s][k] = sum_r dY[s][r] W_e[r][k]
     nm::RowsTile t{};
     t.rows = rows;
-    t.A = static_cast<const uint8_t*>(dY);
-    t.lda = lddy * 2;
-    t.ka = (int)(g.R / 8);
-    if (!direct) {
-      if (nm::launch_pad_rows(dY, lddy, T, g.R, pad, p.Rp, s) != hipSuccess) return NM_EHIP;
-      t.A = pad;
-      t.lda = p.Rp * 2;
-      t.ka = (int)(p.Rp / 8);
-    }
+    t.A = y;
+    t.lda = ldy;
+    t.ka = ky;
     t.B[0] = wt;
     t.Mr = T;
     t.Nr = g.K;
-    t.nslab = (int)(p.Rp / 64);
+    t.nslab = (int)(Rp / 64);
     t.C = dX;
     t.ldc = lddx;
     t.zero_rest = zero_rest != 0;
@@ -482,12 +473,15 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
     if (nm::launch_rows_tile(tile_type(ww.dtype), nm::TILE_ROWS, ww.dtype, t, s) != hipSuccess) return NM_EHIP;
   }
   if (dW) {
-    // dW_e[r][k] = sum over e's rows of dY[s][r] X[s][k], both transposed
+    // dW_e[r][k] = sum over e's rows of dY[s][r] X[s][k]
     nm::RowsTile t{};
     t.rows = rows;
-    t.A = yt;
-    t.B[0] = xt;
-    t.lda = t.ldb = 128;
+    t.A = y;
+    t.lda = ldy;
+    t.ka = ky;
+    t.B[0] = pad_x ? xp : static_cast<const uint8_t*>(Xt);
+    t.ldb = pad_x ? Kp * 2 : ldx * 2;
+    t.kb = (int)((pad_x ? Kp : g.K) / 8);
     t.Mr = g.R;
     t.Nr = g.K;
     t.C = dW;

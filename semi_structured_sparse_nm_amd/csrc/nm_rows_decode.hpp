@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kGluWaves * 64) rows_decode_kernel(RowsArgs a,
   const int unit = b - q8 * units;
   if (rb0 >= a.g.nRB) return;
   RowUnit ru = {0, unit * (16 * NT), 0, (int)a.rows.T, 0};
-  if constexpr (GROUPED) ru = find_unit<16 * NT, false>(a.rows, unit);
+  if constexpr (GROUPED) ru = find_unit<16 * NT>(a.rows, unit);
   if (ru.e < 0) {
     if constexpr (GROUPED) zero_rows_of_none(a, rb0 * 16, 16 * nblk, unit, units);
     return;

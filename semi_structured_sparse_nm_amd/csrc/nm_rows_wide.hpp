@@ -52,10 +52,10 @@ __global__ void __launch_bounds__(kWideWaves * 64) rows_wide_kernel(RowsArgs a, 
   };
   // XCD x takes a contiguous run of the items, an expert's units of one column
   // tile next to each other: they share its weights in the XCD's L2
-  const int total = count_units<BM, false>(a.rows) * nt, per = (total + 7) / 8;
+  const int total = count_units<BM>(a.rows) * nt, per = (total + 7) / 8;
   const int j8 = blockIdx.x >> 3, L = (blockIdx.x & 7) * per + j8;
   if (j8 >= per || L >= total) return zero_rest();
-  const RowUnit ru = find_unit<BM, false>(a.rows, L, nt);
+  const RowUnit ru = find_unit<BM>(a.rows, L, nt);
   const int n = ru.n;
   const int nKB = (int)a.g.nKB, last = nKB - 1;
   const int KX = (int)a.g.K;

@@ -131,6 +131,13 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   constexpr bool SPAN = GLU && HB % RJ != 0;
   const bool wave_up = SPAN && (8 * wave / HB & 1);
   // row of the tile (A: of BM, B: of BNO outputs) that load j brings this lane
+  // TILE_COLS: an operand's slab is 64 rows of BM (BN) columns as they lie in memory,
+  // read transposed from LDS; load d of it fills 1 KB, 16-byte position p of row t
+  // with piece p ^ 2 swz(t).  A read's sixteen lanes take 32 bytes each of four rows
+  // (t & 3), the next sixteen those eight rows on: all on different banks.
+  auto swz = [](int t, auto width) {
+    return decltype(width)::value >= 128 ? (t & 3) | (t >> 3 & 1) << 2 : (t >> 1 & 1) | (t >> 3 & 1) << 1;
+  };
   auto load_row = [&](auto jc) {
     constexpr int j = decltype(jc)::value;
     int row = 8 * wave + (lane >> 3) + RJ * j;
@@ -146,14 +153,18 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   const int cut_b = !BACK && !GROUPED && (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
 
   // the load cursor: work item, its resources, next slab
-  int ck = 0, cs, ce, voff[NL];
+  int ck = 0, cs, ce, cleft, cend_a, cend_b, voff[NL];  // TILE_COLS: rows left, ends of a row in the resources
   v4i ra, rb0, rb1, rsc[MX ? (NU + NW - 1) / NW : 1];
   // (always inlined: a call would keep the cursor, and what it refers to, in memory)
+  // TILE_COLS: rows past the expert's last are past the resources' ends, zeros
+  auto limit_rows = [&]() __attribute__((always_inline)) {
+    const int n = min(cleft, 64);
+    ra[2] = scalar(n > 0 ? (n - 1) * (int)a.lda + cend_a : 0);
+    rb0[2] = scalar(n > 0 ? (n - 1) * (int)a.ldb + cend_b : 0);
+  };
   auto cursor_item = [&](int k) __attribute__((always_inline)) {
     const TileItem it = walk.item(k);
     const int64_t m0 = EROWS ? (int64_t)it.row : (int64_t)it.m * BM, n0 = (int64_t)it.n * BNO;
-    // (TILE_COLS: rows of the first slab, as if they were a matrix's)
-    const int64_t ma = COLS ? it.s0 * a.Mr + m0 : m0, nb = COLS ? it.s0 * a.Nr + n0 : n0;
     auto tile_rsrc = [&](const uint8_t* p, int64_t row0, int64_t ld) {
       const v4i r = make_rsrc(p + row0 * ld, 0x7fffffff);
       return v4i{scalar(r[0]), scalar(r[1]), r[2], r[3]};
@@ -164,7 +175,11 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
     const int mlast = (int)min(Mr - m0, (int64_t)BM) - 1, nlast = (int)min(Nr - n0, (int64_t)BNO) - 1;
     static_for<0, NL>([&](auto jc) {
       constexpr int j = decltype(jc)::value;
-      if constexpr (EROWS && j >= NLA) {                 // blocks of 16 rows
+      if constexpr (COLS) {
+        constexpr int W = j < NLA ? BM : BN, PC = W / 8;
+        const int d = wave + NW * (j < NLA ? j : j - NLA), t = d * (64 / PC) + lane / PC;
+        voff[j] = t * (int)(j < NLA ? lda : ldb) + 16 * (lane % PC ^ 2 * swz(t, ic<W>()));
+      } else if constexpr (EROWS && j >= NLA) {          // blocks of 16 rows
         const int row = min(load_row(jc), nlast);
         voff[j] = (row >> 4) * (a.nslab * 2048) + (row & 15) * 128 + 16 * piece;
       } else {
@@ -172,11 +187,11 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
                           : min(load_row(jc), nlast) * (int)ldb + 16 * piece;
       }
     });
-    ra = tile_rsrc(grad ? (it.batch > 1 ? a.w.A[1] : a.w.A[0]) : a.A, ma, lda);
+    ra = tile_rsrc(grad ? (it.batch > 1 ? a.w.A[1] : a.w.A[0]) : a.A, COLS ? 0 : m0, lda);
     if constexpr (EROWS)
       rb0 = tile_rsrc(a.B[0], (int64_t)it.batch * ((a.Nr + 15) / 16) + n0 / 16, (int64_t)a.nslab * 2048);
     else
-      rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], nb, ldb);
+      rb0 = tile_rsrc(grad ? a.w.B : wave_up ? a.B[1] : a.B[0], COLS ? 0 : n0, ldb);
     if constexpr (GLU && !SPAN) rb1 = tile_rsrc(a.B[1], n0, ldb);
     if constexpr (MX) {
       // unit u of a stage: LDS rows 32 u ..; row groups past the end repeat the last one
@@ -200,6 +215,19 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
     }
     cs = it.s0;
     ce = it.s1;
+    if constexpr (COLS) {
+      auto at = [&](v4i& r, const uint8_t* p) {
+        const v4i q = make_rsrc(p, 0);
+        r[0] = scalar(q[0]);
+        r[1] = scalar(q[1]);
+      };
+      at(ra, a.A + it.row * a.lda + m0 * 2);
+      at(rb0, a.B[0] + it.row * a.ldb + n0 * 2);
+      cleft = it.end - it.row;
+      cend_a = a.ka * 16 - (int)m0 * 2;
+      cend_b = a.kb * 16 - (int)n0 * 2;
+      limit_rows();
+    }
   };
   auto issue_one = [&](auto jc, int st, int ca, int cb) {
     constexpr int j = decltype(jc)::value;
@@ -233,8 +261,10 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
           r[0] = (int)p;
           r[1] = (int)(p >> 32);
         };
-        next_slab(ra, a.Mr * 128);
-        next_slab(rb0, a.Nr * 128);
+        next_slab(ra, a.lda * 64);
+        next_slab(rb0, a.ldb * 64);
+        cleft -= 64;
+        limit_rows();
       }
     } else if (ck + 1 < walk.count) {
       asm volatile("" ::: "memory");                    // a branch, not selects around it
@@ -254,13 +284,33 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   // fragment addresses: row li of a 16-row tile, piece 4 kk + lq
   const int arow = (wm * TM * 16 + li) * 128;
   const int brow = (BM + wn * TN * 16 + li) * 128;
-  const int pos0 = 16 * (lq ^ (li & 7)), pos1 = 16 * ((4 + lq) ^ (li & 7));
+  // (TILE_COLS: its rows' first half and second)
+  const int pos0 = COLS ? 0 : 16 * (lq ^ (li & 7)), pos1 = COLS ? 1 : 16 * ((4 + lq) ^ (li & 7));
+  // TILE_COLS: of column tile X rows 8 lq + 4 h .. + 3; lane li brings row li / 4's
+  // columns 4 (li % 4) .. and takes column li of all four
+  int acol[COLS ? TM : 1], bcol[COLS ? TN : 1];
+  if constexpr (COLS) {
+    const int t = 8 * lq + (li >> 2);
+#pragma unroll
+    for (int x = 0; x < TM; ++x) acol[x] = t * (2 * BM) + (wm * TM + x ^ swz(t, ic<BM>())) * 32 + 8 * (li & 3);
+#pragma unroll
+    for (int x = 0; x < TN; ++x)
+      bcol[x] = BM * 128 + t * (2 * BN) + (wn * TN + x ^ swz(t, ic<BN>())) * 32 + 8 * (li & 3);
+  }
   struct Frag {
     v4i a[TM], b[TN];
   };
   constexpr int NF = TM + TN;
   auto read_one = [&](Frag& f, auto xc, int st, int pos) {
     constexpr int X = decltype(xc)::value;
+    if constexpr (COLS) {
+      constexpr bool A = X < TM;
+      constexpr int pitch = 2 * (A ? BM : BN);
+      const uint8_t* sp = lds + st * STAGE + (A ? acol[A ? X : 0] : bcol[A ? 0 : X - TM]) + pos * (32 * pitch);
+      const v2i lo = lds_tr16(sp), hi = lds_tr16(sp + 4 * pitch);
+      (A ? f.a[A ? X : 0] : f.b[A ? 0 : X - TM]) = v4i{lo[0], lo[1], hi[0], hi[1]};
+      return;
+    }
     const uint8_t* sp = lds + st * STAGE + pos;
     if constexpr (X < TM)
       f.a[X] = *reinterpret_cast<const v4i*>(sp + arow + X * 2048);

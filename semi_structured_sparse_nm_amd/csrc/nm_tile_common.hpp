@@ -75,7 +75,7 @@ struct RowsWalk {
     int* rows = table;
     int* units = table + TAB;
     if (threadIdx.x < 64) {
-      row_boundaries<COLS ? 64 : BM, COLS>(a.rows, [&](int i, int, int at, int u, int) {
+      row_boundaries<BM>(a.rows, [&](int i, int, int at, int u, int) {
         if (i <= a.rows.E) {
           rows[i] = at;
           units[i] = u;
@@ -127,9 +127,9 @@ struct RowsWalk {
     t.n = scalar(in / rows);
     t.m = grp * gm + in - t.n * rows;
     t.end = scalar(row_at[e + 1]);
-    t.row = scalar(row_at[e]) + t.m * BM;
-    t.s0 = COLS ? scalar(unit_at[e]) : 0;
-    t.s1 = COLS ? scalar(unit_at[e + 1]) : nslab;
+    t.row = scalar(row_at[e]) + (COLS ? 0 : t.m * BM);
+    t.s0 = 0;
+    t.s1 = COLS ? max((t.end - t.row + 63) / 64, 1) : nslab;
     return t;
   }
 };

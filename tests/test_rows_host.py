@@ -175,7 +175,8 @@ def test_expert_backward_refusals():
                dict(w=_experts(format_version=0))):
         assert _eb(**kw) == EINVAL, kw
     for kw in (dict(w=_experts(dt=nm.NM_I8)), dict(odt=5), dict(X=P[0] + 1), dict(dY=P[2] + 1), dict(dX=P[3] + 1),
-               dict(dW=P[4] + 1), dict(ws=P[5] + 8), dict(o=P[1] + 1), dict(T=1 << 22)):
+               dict(dW=P[4] + 1), dict(ws=P[5] + 8), dict(o=P[1] + 1),
+               dict(T=(1 << 25) + 1)):
         assert _eb(**kw) == EUNSUP, kw
     wide = _experts(E=64, R=1 << 16, K=1 << 15)
     assert _eb(w=wide, ldx=1 << 15, lddy=1 << 16, lddx=1 << 15, lddw=1 << 15, wsb=1 << 62) == EUNSUP
