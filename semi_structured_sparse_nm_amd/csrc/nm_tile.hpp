@@ -22,8 +22,9 @@
 // 16-byte pieces past ka / kb read as zeros, so the reduction's tail adds
 // nothing.  Every slab has a piece inside ka and one inside kb, so no load has
 // all its lanes outside its operand: such a load would return ahead of older
-// ones, and a count of outstanding loads could pass too early.  TILE_GLU: half of a wave's B rows are gate
-// rows, the other half the up rows of the same outputs, so g and u of one
+// ones, and a count of outstanding loads could pass too early (TILE_COLS: while a
+// slab that ends inside is on its way, all loads are waited for).  TILE_GLU: half of
+// a wave's B rows are gate rows, the other half the up rows of the same outputs, so g and u of one
 // output meet in one lane and the activation and product need no exchange.
 // TILE_BACK: the input's and both weights' gradients are items of one launch.
 //
@@ -153,7 +154,8 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   const int cut_b = !BACK && !GROUPED && (a.kb & 7) && piece >= (a.kb & 7) ? (int)0x80000000 : 0;
 
   // the load cursor: work item, its resources, next slab
-  int ck = 0, cs, ce, cleft, cend_a, cend_b, voff[NL];  // TILE_COLS: rows left, ends of a row in the resources
+  // (TILE_COLS: rows left, ends of a row in the resources, slabs with short ones in flight)
+  int ck = 0, cs, ce, cleft, cend_a, cend_b, short_slabs = 0, voff[NL];
   v4i ra, rb0, rb1, rsc[MX ? (NU + NW - 1) / NW : 1];
   // (always inlined: a call would keep the cursor, and what it refers to, in memory)
   // TILE_COLS: rows past the expert's last are past the resources' ends, zeros
@@ -248,7 +250,16 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
     constexpr int P = decltype(pc)::value, NP = decltype(npc)::value;
     const int ca = BACK || COLS || cs + 1 < a.nslab ? 0 : cut_a;
     const int cb = BACK || GROUPED || cs + 1 < a.nslab ? 0 : cut_b;
+    if constexpr (COLS && P == 0) short_slabs = cleft < 64 ? NS : max(short_slabs - 1, 0);
     static_for<NLT * P / NP, NLT * (P + 1) / NP>([&](auto jc) { issue_one(jc, st, ca, cb); });
+  };
+  // the loads of the slab after the one multiplied are in
+  auto wait_loads = [&](auto lgkm) __attribute__((always_inline)) {
+    constexpr int AHEAD = NLT * (NS - 2);               // loads that may be outstanding then
+    static_assert(AHEAD < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt(waitcnt(AHEAD, decltype(lgkm)::value));
+    if constexpr (COLS && AHEAD > 0)
+      if (short_slabs) __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
   };
   // past the last work item the cursor stays on its last slab: the loads fill
   // a stage nobody reads
@@ -354,9 +365,7 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
     issue_part(ic<0>(), ic<1>(), decltype(k)::value);
     advance();
   });
-  constexpr int AHEAD = NLT * (NS - 2);                 // loads that may be outstanding once the next slab is in
-  static_assert(AHEAD < 64, "vmcnt");
-  __builtin_amdgcn_s_waitcnt(waitcnt(AHEAD, 15));
+  wait_loads(ic<15>());
   barrier_nofence();
   issue_part(ic<0>(), ic<1>(), NS - 1);
   advance();
@@ -383,7 +392,7 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
         mul_row(i, ic<0>(), f0, c0);
         __builtin_amdgcn_sched_barrier(0);
       });
-      __builtin_amdgcn_s_waitcnt(waitcnt(AHEAD, 0));
+      wait_loads(ic<0>());
       barrier_nofence();
       const int nx = st + 1 == NS ? 0 : st + 1;
       read_scales(c1, nx);
