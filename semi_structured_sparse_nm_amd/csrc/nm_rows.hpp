@@ -69,7 +69,9 @@ struct RowsPlan {
 RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus);
 // The tile product's shape (and its time by the model, in microseconds)
 int rows_tile_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t nslab, int cus, double* time);
-int cols_tile_shape(int64_t T, int64_t E, int64_t R, int64_t K, int cus);
+// that of the gradients (16 bits), and how many of the weights' tiles take the time
+// of one of the rows' (0: no rows')
+int grads_tile_shape(const Geometry& g, int64_t T, int64_t E, bool dx, bool dw, int cus, int* lead);
 
 // few rows an expert: the packed weights streamed once per unit of 16 rows or more
 hipError_t launch_rows_decode(const RowsArgs& a, hipStream_t s);
@@ -118,8 +120,10 @@ struct RowsTile : TileArgs {
 // 64 columns: 16 bytes of lane 16 lq + li, 16 bits a row tile j of them: bits 4 i + v
 // of row 16 j + li, columns 16 i + 4 lq + v.
 inline int64_t kept_blocks(int64_t R, int64_t nKB) { return (R + 127) / 128 * nKB; }
-// et: TILE_F16, TILE_BF16 (outputs of that type) or TILE_I8 (TILE_ROWS only)
-hipError_t launch_rows_tile(int et, TileOp op, int ydt, const RowsTile& a, hipStream_t s);
+// TILE_ROWS; et: TILE_F16, TILE_BF16 (outputs of that type) or TILE_I8
+hipError_t launch_rows_tile(int et, int ydt, const RowsTile& a, hipStream_t s);
+// TILE_ROWS (x) and TILE_COLS (w), one launch in tiles of `shape`; C null: not that one
+hipError_t launch_rows_grads(int et, const RowsTile& x, const RowsTile& w, int shape, hipStream_t s);
 // TILE_ROWS on 2:4 weights
 hipError_t launch_rows_tile24(int wdt, int ydt, const RowsTile& a, hipStream_t s);
 constexpr int kRowsTable = 1024;   // boundaries (E + 1) a workgroup's table holds

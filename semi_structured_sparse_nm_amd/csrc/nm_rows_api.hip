@@ -150,7 +150,7 @@ hipError_t multiply(const Weights& w, const RowsPlan& plan, const nm::RowsArgs& 
     t.B[0] = ws;
   }
   if (e != hipSuccess) return e;
-  return path == ROWS_DENSE ? nm::launch_rows_tile(tile_type(w.dtype), nm::TILE_ROWS, a.ydt, t, s)
+  return path == ROWS_DENSE ? nm::launch_rows_tile(tile_type(w.dtype), a.ydt, t, s)
                             : nm::launch_rows_tile24(w.dtype, a.ydt, t, s);
 }
 
@@ -435,7 +435,6 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
   uint8_t* xp = mask + p.mask;
   uint8_t* yp = xp + p.xp;
   const RowGroups rows = groups_of(offsets, offsets_dtype, ww.E, T);
-  const int cus = nm::device_cu_count();
 
   nm::RowsPrepareArgs q{};
   q.g = g;
@@ -452,47 +451,32 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
   q.yp = pad_y ? reinterpret_cast<uint16_t*>(yp) : nullptr;
   if (nm::launch_rows_prepare(q, s) != hipSuccess) return NM_EHIP;
   const int64_t Rp = up64(g.R), Kp = up64(g.K);
-  const uint8_t* y = pad_y ? yp : static_cast<const uint8_t*>(dY);
-  const int64_t ldy = pad_y ? Rp * 2 : lddy * 2;
-  const int ky = (int)((pad_y ? Rp : g.R) / 8);
-  if (dX) {
-    // dX[s][k] = sum_r dY[s][r] W_e[r][k]
-    nm::RowsTile t{};
-    t.rows = rows;
-    t.A = y;
-    t.lda = ldy;
-    t.ka = ky;
-    t.B[0] = wt;
-    t.Mr = T;
-    t.Nr = g.K;
-    t.nslab = (int)(Rp / 64);
-    t.C = dX;
-    t.ldc = lddx;
-    t.zero_rest = zero_rest != 0;
-    t.shape = nm::rows_tile_shape(false, false, T, ww.E, g.K, t.nslab, cus, nullptr);
-    if (nm::launch_rows_tile(tile_type(ww.dtype), nm::TILE_ROWS, ww.dtype, t, s) != hipSuccess) return NM_EHIP;
-  }
-  if (dW) {
-    // dW_e[r][k] = sum over e's rows of dY[s][r] X[s][k]
-    nm::RowsTile t{};
-    t.rows = rows;
-    t.A = y;
-    t.lda = ldy;
-    t.ka = ky;
-    t.B[0] = pad_x ? xp : static_cast<const uint8_t*>(Xt);
-    t.ldb = pad_x ? Kp * 2 : ldx * 2;
-    t.kb = (int)((pad_x ? Kp : g.K) / 8);
-    t.Mr = g.R;
-    t.Nr = g.K;
-    t.C = dW;
-    t.ldc = lddw;
-    t.es = g.R * lddw;
-    t.mask = mask;
-    t.ldm = g.nKB;
-    t.shape = nm::cols_tile_shape(T, ww.E, g.R, g.K, cus);
-    if (nm::launch_rows_tile(tile_type(ww.dtype), nm::TILE_COLS, ww.dtype, t, s) != hipSuccess) return NM_EHIP;
-  }
-  return NM_OK;
+  nm::RowsTile tx{}, tw{};
+  tx.rows = tw.rows = rows;
+  tx.A = tw.A = pad_y ? yp : static_cast<const uint8_t*>(dY);
+  tx.lda = tw.lda = pad_y ? Rp * 2 : lddy * 2;
+  tx.ka = tw.ka = (int)((pad_y ? Rp : g.R) / 8);
+  // dX[s][k] = sum_r dY[s][r] W_e[r][k]
+  tx.B[0] = wt;
+  tx.Mr = T;
+  tx.Nr = g.K;
+  tx.nslab = (int)(Rp / 64);
+  tx.C = dX;
+  tx.ldc = lddx;
+  tx.zero_rest = zero_rest != 0;
+  // dW_e[r][k] = sum over e's rows of dY[s][r] X[s][k]
+  tw.B[0] = pad_x ? xp : static_cast<const uint8_t*>(Xt);
+  tw.ldb = pad_x ? Kp * 2 : ldx * 2;
+  tw.kb = (int)((pad_x ? Kp : g.K) / 8);
+  tw.Mr = g.R;
+  tw.Nr = g.K;
+  tw.C = dW;
+  tw.ldc = lddw;
+  tw.es = g.R * lddw;
+  tw.mask = mask;
+  tw.ldm = g.nKB;
+  const int shape = nm::grads_tile_shape(g, T, ww.E, dX != nullptr, dW != nullptr, nm::device_cu_count(), &tw.w.lead);
+  return nm::launch_rows_grads(tile_type(ww.dtype), tx, tw, shape, s) == hipSuccess ? NM_OK : NM_EHIP;
 }
 
 nm_status nm_i8_expert_linear_workspace_size(const nm_experts* w, const nm_i8* xq, int64_t T, size_t* bytes) {

@@ -127,19 +127,25 @@ int rows_tile_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64
   return best;
 }
 
-int cols_tile_shape(int64_t T, int64_t E, int64_t R, int64_t K, int cus) {
-  int best = 0;
-  if (ffn_tile_override("tile", &best, nullptr)) return best;
+int grads_tile_shape(const Geometry& g, int64_t T, int64_t E, bool dx, bool dw, int cus, int* lead) {
+  int best = 0, only;
   double least = 0;
-  for (int i = 0; i < 4; ++i) {
+  const bool forced = ffn_tile_override("tile", &only, nullptr);
+  for (int i = forced ? only : 0; i < (forced ? only + 1 : 4); ++i) {
     const Shape& h = kShapes[i];
-    const double n = (double)(E * ceil_div(R, h.bm)) * (double)ceil_div(K, h.bn);
+    const double nx = dx ? units(T, E, h.bm) * (double)ceil_div(g.K, h.bn) : 0.0;
+    const double nw = dw ? (double)(E * ceil_div(g.R, h.bm)) * (double)ceil_div(g.K, h.bn) : 0.0;
     const Tile& c = kTiles[1][0][i];
-    const double slab = c.idle + (c.busy - c.idle) * std::min(1.0, n / cus);
-    const double t = std::max(1.0, n / cus + 0.45) * (c.base + (double)T / 64.0 / E * slab);
-    if (i == 0 || t < least) {
+    const double slab = c.idle + (c.busy - c.idle) * std::min(1.0, (nx + nw) / cus);
+    const double tx = dx ? c.base + (double)ceil_div(g.R, 64) * slab : 0.0;
+    const double tw = c.base + ((double)T / 64.0 / E + 0.5) * slab;
+    // all of it on every compute unit, and half of the longer kind's tile at the end
+    const double longer = std::max(tx, dw ? tw : 0.0);
+    const double t = std::max(longer, (nx * tx + nw * tw) / cus + 0.5 * longer);
+    if (least == 0 || t < least) {
       least = t;
       best = i;
+      *lead = (int)std::min(tx / tw + 0.5, 64.0);
     }
   }
   return best;

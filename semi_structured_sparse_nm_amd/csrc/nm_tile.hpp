@@ -24,9 +24,10 @@
 // all its lanes outside its operand: such a load would return ahead of older
 // ones, and a count of outstanding loads could pass too early (TILE_COLS: while a
 // slab that ends inside is on its way, all loads are waited for).  TILE_GLU: half of
-// a wave's B rows are gate rows, the other half the up rows of the same outputs, so g and u of one
-// output meet in one lane and the activation and product need no exchange.
-// TILE_BACK: the input's and both weights' gradients are items of one launch.
+// a wave's B rows are gate rows, the other half the up rows of the same outputs, so
+// g and u of one output meet in one lane and the activation and product need no
+// exchange.  TILE_BACK: the input's and both weights' gradients are items of one
+// launch; those of grouped rows are TILE_ROWS, then TILE_COLS items of one.
 //
 // bf16, 2048 tokens, two 11008 x 4096 weights: gated 285 us (1.3 PFLOP/s), both
 // gradients 675 (1.09); 4 bits, 1900 tokens, gated 96 (3.6).  By counters the
@@ -82,10 +83,19 @@ constexpr bool grouped_op(int op) { return op == TILE_ROWS || op == TILE_COLS; }
 template <int OP>
 using tile_args = typename std::conditional<grouped_op(OP), RowsTile, TileArgs>::type;
 
-template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
-__global__ void __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
-tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
+// Bytes of LDS.
+template <int ET, int OP, int BM, int BN, int NS>
+constexpr int tile_lds() {
+  return NS * ((BM + BN) * (ET == TILE_MX ? 136 : 128)) + rows_table_bytes(grouped_op(OP), kRowsTable);
+}
+
 #if defined(__HIP_DEVICE_COMPILE__)
+// The items of a workgroup; TILE_COLS: the XCD's workgroups from `first` on get
+// w.lead of them ahead of the rest.  Returns, TILE_ROWS, how many of the XCD's
+// workgroups have one more than the others.
+template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
+__device__ __forceinline__ int tile_items(const tile_args<OP>& a, const TileList& list, const TileList& list2,
+                                          uint8_t* lds, int first) {
   constexpr bool EROWS = OP == TILE_ROWS, COLS = OP == TILE_COLS, GROUPED = grouped_op(OP);
   typedef typename std::conditional<ET == TILE_I8, v4i, v4f>::type Acc;
   constexpr int NW = WM * WN;
@@ -105,10 +115,8 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
   constexpr int RJ = 8 * NW;                            // rows one load of every wave covers
   static_assert(BM % RJ == 0 && BN % RJ == 0, "every load of one operand");
   static_assert(!GLU || HB % RJ == 0 || RJ % (2 * HB) == 0, "a wave's load has rows of one weight");
-  constexpr int TABLE = rows_table_bytes(GROUPED, kRowsTable);
-  static_assert(NS * STAGE + TABLE <= 160 * 1024, "LDS");
+  static_assert(tile_lds<ET, OP, BM, BN, NS>() <= 160 * 1024, "LDS");
   static_assert(!MX || !GLU || HB % 32 == 0, "whole scale units per half");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE + TABLE];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -117,12 +125,14 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
 
   const auto walk = [&]() {
     if constexpr (GROUPED)
-      return RowsWalk<BM, COLS, kRowsTable>(a, list.mt, list.nt, reinterpret_cast<int*>(lds + NS * STAGE));
+      return RowsWalk<BM, COLS, kRowsTable>(a, list.mt, list.nt, reinterpret_cast<int*>(lds + NS * STAGE), first);
     else
       return TileWalk<BACK>(list, list2, a.w.lead);
   }();
   if constexpr (EROWS) zero_other_rows<OUT>(a, walk.row_at);
-  if (walk.count <= 0) return;
+  int more = 0;
+  if constexpr (EROWS) more = walk.more;
+  if (walk.count <= 0) return more;
 
   // ---- operand loads: load d fills LDS rows 8 d .. 8 d + 7, lane l row
   // 8 d + l / 8, position l % 8 = piece (l % 8) ^ (l / 8); wave w issues
@@ -424,30 +434,82 @@ tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
     clear();
   }
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));           // nothing lands in LDS after this
+  return more;
+}
 #endif
+
+template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
+__global__ void __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+tile_kernel(tile_args<OP> a, TileList list, TileList list2) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[tile_lds<ET, OP, BM, BN, NS>()];
+  tile_items<ET, OP, OUT, BM, BN, WM, WN, NS>(a, list, list2, lds, 0);
+#endif
+}
+
+// Gradients of grouped rows: the rows' (x), then the weights' (w), of which those
+// workgroups get more that had an item less of x's.  Either's C may be null.
+template <int ET, int OUT, int BM, int BN, int WM, int WN, int NS>
+__global__ void __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+tile_grads_kernel(RowsTile x, RowsTile w, TileList lx, TileList lw) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[tile_lds<ET, TILE_ROWS, BM, BN, NS>()];
+  int more = 0;
+  if (x.C) {
+    more = tile_items<ET, TILE_ROWS, OUT, BM, BN, WM, WN, NS>(x, lx, lx, lds, 0);
+    __syncthreads();
+  }
+  if (w.C) tile_items<ET, TILE_COLS, OUT, BM, BN, WM, WN, NS>(w, lw, lw, lds, more);
+#endif
+}
+
+// The list of a product of grouped rows: as many items as there could be (the host
+// does not know the experts' rows).
+template <int OP, int BM, int BN>
+TileList rows_list(const RowsTile& a) {
+  TileList l{};
+  if (!a.C) return l;
+  l.mt = (int)((a.Mr + BM - 1) / BM);
+  l.nt = (int)((a.Nr + BN - 1) / BN);
+  const int64_t most = (OP == TILE_COLS ? (int64_t)l.mt * a.rows.E : units_most(a.rows.T, a.rows.E, BM)) * l.nt;
+  l.per = (int)std::min<int64_t>((most + 7) / 8, 1 << 20);
+  return l;
 }
 
 template <int ET, int OP, int OUT, int BM, int BN, int WM, int WN, int NS>
 hipError_t launch_tile_cfg(const tile_args<OP>& a, hipStream_t s) {
   constexpr int BNO = OP == TILE_GLU ? BN / 2 : BN;
-  if constexpr (grouped_op(OP)) {
-    // as many tiles as there could be: the host does not know the experts' rows
-    TileList l{};
-    l.mt = (int)((a.Mr + BM - 1) / BM);
-    l.nt = (int)((a.Nr + BN - 1) / BN);
-    const int64_t most = (OP == TILE_COLS ? (int64_t)l.mt * a.rows.E : units_most(a.rows.T, a.rows.E, BM)) * l.nt;
-    const int grid = 8 * tile_slots((int)std::min<int64_t>((most + 7) / 8, 1 << 20));
+  if constexpr (OP == TILE_ROWS) {
+    const TileList l = rows_list<OP, BM, BN>(a);
+    hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3(8u * tile_slots(l.per)),
+                       dim3(WM * WN * 64), 0, s, a, l, l);
+    return hipGetLastError();
+  } else {
+    const bool back = OP == TILE_BACK;
+    const TileList list = tile_list(a.Mr, a.Nr, BM, BNO, a.split, a.sps, a.nslab, back && !a.C ? 0 : 1);
+    const TileList list2 = tile_list(a.w.Mr, a.w.Nr, BM, BNO, 1, a.w.nslab, a.w.nslab, back && a.w.C[0] ? 2 : 0);
+    const int grid = 8 * tile_slots(list.per + list2.per);
     hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s,
-                       a, l, l);
+                       a, list, list2);
     return hipGetLastError();
   }
-  const bool back = OP == TILE_BACK;
-  const TileList list = tile_list(a.Mr, a.Nr, BM, BNO, a.split, a.sps, a.nslab, back && !a.C ? 0 : 1);
-  const TileList list2 = tile_list(a.w.Mr, a.w.Nr, BM, BNO, 1, a.w.nslab, a.w.nslab, back && a.w.C[0] ? 2 : 0);
-  const int grid = 8 * tile_slots(list.per + list2.per);
-  hipLaunchKernelGGL((tile_kernel<ET, OP, OUT, BM, BN, WM, WN, NS>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s,
-                     a, list, list2);
+}
+
+template <int ET, int OUT, int BM, int BN, int WM, int WN, int NS>
+hipError_t launch_grads_cfg(const RowsTile& x, const RowsTile& w, hipStream_t s) {
+  const TileList lx = rows_list<TILE_ROWS, BM, BN>(x), lw = rows_list<TILE_COLS, BM, BN>(w);
+  hipLaunchKernelGGL((tile_grads_kernel<ET, OUT, BM, BN, WM, WN, NS>), dim3(8u * tile_slots(lx.per + lw.per)),
+                     dim3(WM * WN * 64), 0, s, x, w, lx, lw);
   return hipGetLastError();
+}
+template <int ET, int OUT>
+hipError_t launch_grads(const RowsTile& x, const RowsTile& w, int shape, hipStream_t s) {
+  switch (shape) {
+    case 0: return launch_grads_cfg<ET, OUT, 256, 256, 2, 4, 2>(x, w, s);
+    case 1: return launch_grads_cfg<ET, OUT, 128, 256, 2, 4, 3>(x, w, s);
+    case 2: return launch_grads_cfg<ET, OUT, 128, 128, 2, 4, 4>(x, w, s);
+    default: return launch_grads_cfg<ET, OUT, 64, 128, 2, 4, 6>(x, w, s);
+  }
 }
 
 template <int ET, int OP, int OUT>

@@ -70,8 +70,9 @@ template <int BM, bool COLS, int TAB>
 struct RowsWalk {
   const int* row_at;
   const int* unit_at;
-  int E, mt, nt, x, j, step, per, count, nslab;
-  __device__ __forceinline__ RowsWalk(const RowsTile& a, int mt_, int nt_, int* table) {
+  int E, mt, nt, x, j, step, per, count, more, nslab;
+  int q, lead, ahead;                                   // COLS, as in TileWalk
+  __device__ __forceinline__ RowsWalk(const RowsTile& a, int mt_, int nt_, int* table, int first = 0) {
     int* rows = table;
     int* units = table + TAB;
     if (threadIdx.x < 64) {
@@ -95,12 +96,30 @@ struct RowsWalk {
     step = gridDim.x >> 3;
     const int total = COLS ? E * mt * nt : scalar(unit_at[E]) * nt;
     per = (total + 7) / 8;
-    const int n = COLS ? total - x * step - j : min(per, total - x * per) - j;
-    const int every = COLS ? 8 * step : step;
-    count = n > 0 ? scalar((n + every - 1) / every) : 0;
+    auto rounds = [](int n, int every) { return n > 0 ? scalar((n + every - 1) / every) : 0; };
+    if constexpr (COLS) {
+      // the XCD's items: of 8 step each, step from x step on
+      const int chunks = scalar(total / step);
+      const int n = (chunks + 7 - x) / 8 * step + ((chunks & 7) == x ? total - chunks * step : 0);
+      q = first;
+      lead = a.w.lead;
+      ahead = lead * (step - q);
+      count = rounds(n - ahead - j, step);
+      if (j >= q) count += min(lead, rounds(n - (j - q), step - q));
+    } else {
+      const int n = min(per, total - x * per);
+      more = n > 0 ? scalar(n - n / step * step) : 0;
+      count = rounds(n - j, step);
+    }
   }
   __device__ __forceinline__ TileItem item(int k) const {
-    int L = COLS ? (8 * k + x) * step + j : x * per + j + k * step;
+    int L = x * per + j + k * step;
+    if constexpr (COLS) {
+      if (j < q) k += lead;
+      const int i = k < lead ? k * (step - q) + j - q : ahead + (k - lead) * step + j;
+      const int chunk = scalar(i / step);
+      L = (8 * chunk + x) * step + i - chunk * step;
+    }
     TileItem t;
     int e, rows_m;
     if constexpr (COLS) {
