@@ -64,11 +64,11 @@ enum RowsPath {
 struct RowsPlan {
   RowsPath path;
   int shape;                 // tile shape; ROWS_WIDE: 16-row tiles of a workgroup
+  int64_t cut = 0;           // tiles: outputs from here on, if any, in a launch of their own
+  int rest = 0;              // and in this shape
 };
 // For T rows of E experts, by time models; g: one expert's weight.
 RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus);
-// The tile product's shape (and its time by the model, in microseconds)
-int rows_tile_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t nslab, int cus, double* time);
 // that of the gradients (16 bits), and how many of the weights' tiles take the time
 // of one of the rows' (0: no rows')
 int grads_tile_shape(const Geometry& g, int64_t T, int64_t E, bool dx, bool dw, int cus, int* lead);

@@ -150,8 +150,24 @@ hipError_t multiply(const Weights& w, const RowsPlan& plan, const nm::RowsArgs& 
     t.B[0] = ws;
   }
   if (e != hipSuccess) return e;
-  return path == ROWS_DENSE ? nm::launch_rows_tile(tile_type(w.dtype), a.ydt, t, s)
-                            : nm::launch_rows_tile24(w.dtype, a.ydt, t, s);
+  auto launch = [&] {
+    return path == ROWS_DENSE ? nm::launch_rows_tile(tile_type(w.dtype), a.ydt, t, s)
+                              : nm::launch_rows_tile24(w.dtype, a.ydt, t, s);
+  };
+  if (!plan.cut) return launch();
+  t.Nr = plan.cut;
+  e = launch();
+  if (e != hipSuccess) return e;
+  const int64_t blocks = plan.cut / 16 * g.nKB;
+  const Geometry tg = path == ROWS_DENSE ? g : geometry24(g);
+  t.B[0] += blocks * (path == ROWS_DENSE ? 2048 : tg.vblk);
+  if (path != ROWS_DENSE) t.meta += blocks * tg.mblk;
+  t.C = static_cast<uint8_t*>(t.C) + plan.cut * nm::dtype_bytes(a.ydt);
+  if (t.wscale) t.wscale += plan.cut;
+  if (t.bias) t.bias += plan.cut;
+  t.Nr = g.R - plan.cut;
+  t.shape = plan.rest;
+  return launch();
 }
 
 // ---------------------------------------------------------------- 8-bit products

@@ -108,24 +108,42 @@ double tile_time(const Tile& c, const Shape& h, double row_units, int64_t R, int
 
 }  // namespace
 
-int rows_tile_shape(bool sparse, bool i8, int64_t T, int64_t E, int64_t R, int64_t nslab, int cus, double* time) {
-  const bool small_table = sparse && i8 && E >= kRowsTable / 2;
-  int best = 3;
-  double least = 0;
+namespace {
+
+// The tile product's shape, cut and rest, and its time by the model.
+RowsPlan tiles_plan(RowsPath path, const Geometry& g, int64_t T, int64_t E, int cus, double* time) {
+  const bool sparse = path != ROWS_DENSE, small_table = sparse && g.eb == 1 && E >= kRowsTable / 2;
+  const Tile* tiles = kTiles[g.eb - 1][sparse];
+  auto time_of = [&](int i, int64_t R) {
+    return tile_time(tiles[i], kShapes[i], units(T, E, kShapes[i].bm), R, g.nKB, E, cus);
+  };
+  RowsPlan best{path, 3};
+  *time = 0;
+  auto take = [&](double t, const RowsPlan& p) {
+    if (*time > 0 && t >= *time) return;
+    *time = t;
+    best = p;
+  };
+  int only = 0;
+  const bool forced = ffn_tile_override(sparse ? "tile24" : "tile", &only, nullptr);
   for (int i = 0; i < 4; ++i) {
     // (the 8-bit shapes whose table of boundaries is the smaller one)
     if (small_table && i % 2 == 0) continue;
-    const double t = tile_time(kTiles[i8 ? 0 : 1][sparse][i], kShapes[i], units(T, E, kShapes[i].bm), R, nslab, E, cus);
-    if (least == 0 || t < least) {
-      least = t;
-      best = i;
-    }
+    if (forced && i != (small_table ? only | 1 : only)) continue;
+    take(time_of(i, g.R), RowsPlan{path, i});
+    if (E > 1 || forced) continue;
+    // one weight: whole rounds in one shape, then the rest in smaller tiles (a second
+    // launch costs 3 us of the 5 that a first one does)
+    const int64_t mt = ceil_div(T, kShapes[i].bm), nt = ceil_div(g.R, kShapes[i].bn);
+    const int64_t cut = mt * nt / cus * cus / mt * kShapes[i].bn;
+    if (cut == 0 || cut >= g.R) continue;
+    const double t = time_of(i, cut);
+    for (int j = i + 1; j < 4; ++j) take(t + time_of(j, g.R - cut) - 2.0, RowsPlan{path, i, cut, j});
   }
-  int only;
-  if (ffn_tile_override(sparse ? "tile24" : "tile", &only, nullptr)) best = small_table ? only | 1 : only;
-  if (time) *time = least;
   return best;
 }
+
+}  // namespace
 
 int grads_tile_shape(const Geometry& g, int64_t T, int64_t E, bool dx, bool dw, int cus, int* lead) {
   int best = 0, only;
@@ -154,9 +172,9 @@ int grads_tile_shape(const Geometry& g, int64_t T, int64_t E, bool dx, bool dw, 
 RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus) {
   // (re-packing takes up to 64 threads a block in one launch)
   const bool repack = repack24_supported(g) && E * g.nRB * g.nKB < (1ll << 26);
-  RowsPlan tiles{g.N == 2 && g.M == 4 ? ROWS_SPARSE : repack ? ROWS_REPACK : ROWS_DENSE, 0};
   double time;
-  tiles.shape = rows_tile_shape(tiles.path != ROWS_DENSE, g.eb == 1, T, E, g.R, g.nKB, cus, &time);
+  const RowsPlan tiles =
+      tiles_plan(g.N == 2 && g.M == 4 ? ROWS_SPARSE : repack ? ROWS_REPACK : ROWS_DENSE, g, T, E, cus, &time);
   // a launch has fewer than 2^32 threads
   int nt, ks;
   int64_t most;

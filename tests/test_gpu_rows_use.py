@@ -323,3 +323,22 @@ def test_weights_past_32_bits(path):
         check(dX, want[0], b[0], "dX")
         check(dW[-1:], want[1], b[1], "dW")
         assert not dW[:-1].any()
+
+
+@pytest.mark.parametrize("T,R,K,N,M", [(2048, 11000, 640, 2, 4), (2000, 9001, 512, 1, 8), (1500, 14000, 384, 4, 4),
+                                       (3000, 7300, 768, 6, 8)])
+def test_long_prompts_in_two_shapes(T, R, K, N, M):
+    """More tiles than compute units: whole rounds of large ones, the last outputs in
+    smaller ones, each with its own scales and bias."""
+    p, sw, w = i8_weight(R, K, N, M, R)
+    X, bias = randn(T, K, seed=T, dt=torch.bfloat16), randn(R, seed=2)
+    wide = torch.full((T, R + 24), 3.0, dtype=torch.bfloat16, device=DEV)
+    nm.i8_linear(p, sw, X, bias=bias, act="gelu", out=wide[:, 8:8 + R])
+    q, sx = i8_64(X)
+    check(wide[:, 8:8 + R], *i8_product64(q, sx, w, sw, bias, "gelu"), "i8_linear")
+    assert (wide[:, :8] == 3).all() and (wide[:, 8 + R:] == 3).all()
+    W = randn(1, R, K, seed=1, dt=torch.float16, scale=0.1)
+    x, (we, _) = nm.pack_experts(W, N, M), pruned(W, N, M)
+    X = X.half()
+    o = torch.tensor([5, T - 7], dtype=torch.int32, device=DEV)
+    check(nm.expert_linear(x, X, o), *expert64(X, we, o), "expert_linear")
