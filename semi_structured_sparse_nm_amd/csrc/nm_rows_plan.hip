@@ -3,8 +3,8 @@
 // Fitted to 1084 products of 17 to 2048 rows an expert, 1 to 64 experts, 300 to
 // 11008 outputs, K 512 to 11008, seven patterns, 8 and 16 bits, every path and tile
 // shape measured with weights that change between calls: the wide and tile models
-// are 5 to 10% off as a root mean square, the streamed one 30%; the choice costs 1.9%
-// against the fastest path as a mean over them, 9% in one of ten, 52% at most.
+// are 4 to 10% off as a root mean square, the streamed one 30%; the choice costs 1.7%
+// against the fastest path as a mean over them, 8% in one of ten, 52% at most.
 // For example, streamed, wide (64 rows), wide (128), best tiles, in microseconds:
 // 8-bit 4:8, 48 rows, 11008 x 4096 25, 33, 41, 42; 256 rows 59, 34, 41, 49; 32 experts
 // of 1536 x 2048, 16-bit 4:8, 256 rows 42, 30, 37, 149, 4096 rows -, 49, 63, 175;
@@ -28,18 +28,21 @@ Kind kind_of(const Geometry& g) {
   return 8 * g.N / g.M <= 4 ? FEW : MANY;
 }
 
-// Microseconds: a workgroup besides its slabs, a slab, and what a further workgroup
-// on the compute unit costs of one alone.
+// Microseconds: a workgroup besides its slabs, a slab with one workgroup on every
+// compute unit, what a further workgroup on the compute unit costs of one alone, and
+// the part of a slab's time that stays with few workgroups.
 struct Wide {
-  double base, slab, more;
+  double base, slab, more, idle;
 };
 constexpr Wide kWide[2][2][KINDS] = {
     // 8 bits (slabs of 128 columns): 64 rows, 128 rows
-    {{{4.81, 0.528, 0.938}, {5.89, 0.935, 0.962}, {4.93, 0.729, 0.852}, {5.54, 1.03, 0.853}, {}},
-     {{6.22, 0.611, 1.32}, {7.90, 0.964, 1.11}, {6.82, 0.968, 1.16}, {7.58, 1.19, 1.13}, {}}},
+    {{{4.97, 0.632, 0.833, 0.779}, {6.07, 1.07, 0.868, 0.836}, {5.10, 0.805, 0.785, 0.865}, {5.67, 1.15, 0.776, 0.862}, {}},
+     {{6.10, 0.831, 0.963, 0.671}, {7.77, 1.15, 0.923, 0.811}, {6.75, 1.15, 0.951, 0.802}, {7.38, 1.41, 0.925, 0.807}, {}}},
     // 16 bits (64 columns)
-    {{{3.01, 0.455, 1.0}, {4.57, 0.938, 0.992}, {4.23, 0.577, 0.895}, {4.46, 0.707, 0.932}, {4.95, 1.24, 0.925}},
-     {{5.17, 0.541, 1.40}, {6.51, 0.969, 1.19}, {6.08, 0.817, 1.11}, {6.20, 0.939, 1.33}, {6.78, 1.43, 1.20}}}};
+    {{{3.41, 0.601, 0.785, 0.677}, {4.94, 1.03, 0.904, 0.867}, {4.35, 0.669, 0.790, 0.816}, {4.69, 0.823, 0.819, 0.818},
+      {5.01, 1.32, 0.873, 0.920}},
+     {{4.89, 0.741, 0.951, 0.680}, {6.32, 1.20, 0.888, 0.765}, {5.73, 0.997, 0.833, 0.778}, {6.02, 1.20, 0.974, 0.739},
+      {6.26, 1.64, 0.981, 0.843}}}};
 
 // A workgroup besides its blocks, a wave's block, and that for each 16-row tile.
 struct Stream {
@@ -87,7 +90,8 @@ double wide_time(const Geometry& g, int64_t T, int64_t E, int tm, double bytes, 
   const double n = units(T, E, 16 * tm) * (double)ceil_div(g.R, 256), r = rounds(n, E, cus, 0.55);
   // (two workgroups of 64 rows share a compute unit, those of 128 follow each other)
   const double in_turn = tm == 4 ? std::max(1.0, w.more * r) : n <= cus ? 1.0 : 1.0 + w.more * (r - 1.0);
-  return 3.0 + std::max((w.base + g.nKB * w.slab) * in_turn, bytes / kRate);
+  const double slab = w.slab * (w.idle + (1.0 - w.idle) * std::min(1.0, n / cus));
+  return 3.0 + std::max((w.base + g.nKB * slab) * in_turn, bytes / kRate);
 }
 
 double stream_time(const Geometry& g, int64_t T, int64_t E, double bytes, int cus) {
