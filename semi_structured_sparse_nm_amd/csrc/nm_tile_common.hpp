@@ -63,15 +63,15 @@ constexpr int rows_table_bytes(bool grouped, int entries) { return grouped ? 8 *
 // tiles of BM rows of every expert times the column tiles, expert by expert
 // (an XCD's run of the list meets few experts' weights), dealt as TileWalk
 // does.  COLS: every expert's mt x nt tiles, its slabs of 64 rows the reduction.
-// They last as long as the expert has rows, so all XCDs take a part of every
-// expert's (eight experts of 4096 rows, 2048 x 4096: 163 us where each XCD had
-// an expert of its own, about 100 so).
+// They last as long as the expert has rows, so every XCD takes an eighth of each
+// expert's, side by side (eight experts of 4096 rows, 2048 x 4096, both gradients: 163
+// us for the weights' alone where each XCD had an expert of its own, 177 for both so).
 template <int BM, bool COLS, int TAB>
 struct RowsWalk {
   const int* row_at;
   const int* unit_at;
   int E, mt, nt, x, j, step, per, count, more, nslab;
-  int q, lead, ahead;                                   // COLS, as in TileWalk
+  int q, lead, ahead, chunk;                            // COLS: as in TileWalk, and items of a chunk
   __device__ __forceinline__ RowsWalk(const RowsTile& a, int mt_, int nt_, int* table, int first = 0) {
     int* rows = table;
     int* units = table + TAB;
@@ -98,9 +98,10 @@ struct RowsWalk {
     per = (total + 7) / 8;
     auto rounds = [](int n, int every) { return n > 0 ? scalar((n + every - 1) / every) : 0; };
     if constexpr (COLS) {
-      // the XCD's items: of 8 step each, step from x step on
-      const int chunks = scalar(total / step);
-      const int n = (chunks + 7 - x) / 8 * step + ((chunks & 7) == x ? total - chunks * step : 0);
+      // the XCD's items: every eighth chunk
+      chunk = min(max(mt * nt / 8, 1), step);
+      const int chunks = scalar(total / chunk);
+      const int n = (chunks + 7 - x) / 8 * chunk + ((chunks & 7) == x ? total - chunks * chunk : 0);
       q = first;
       lead = a.w.lead;
       ahead = lead * (step - q);
@@ -117,8 +118,8 @@ struct RowsWalk {
     if constexpr (COLS) {
       if (j < q) k += lead;
       const int i = k < lead ? k * (step - q) + j - q : ahead + (k - lead) * step + j;
-      const int chunk = scalar(i / step);
-      L = (8 * chunk + x) * step + i - chunk * step;
+      const int c = scalar(i / chunk);
+      L = (8 * c + x) * chunk + i - c * chunk;
     }
     TileItem t;
     int e, rows_m;
