@@ -1180,8 +1180,9 @@ def expert_linear_backward(w: Experts, X: torch.Tensor, offsets: torch.Tensor, d
     ws, wp, wn = _workspace(workspace, need, dev)
     dX = X.new_empty((T, K)) if need_dx else None
     dW = X.new_empty((E, R, K)) if need_dw else None
-    _call(dev, L.nm_expert_linear_backward, "nm_expert_linear_backward", d, X.data_ptr(), ldx, T, offsets.data_ptr(), odt,
-          dY.data_ptr(), lddy, dX.data_ptr() if need_dx else None, K, 1, dW.data_ptr() if need_dw else None, K, wp, wn)
+    _call(dev, L.nm_expert_linear_backward, "nm_expert_linear_backward", d, X.data_ptr(), ldx, T, offsets.data_ptr(),
+          odt, dY.data_ptr(), lddy, dX.data_ptr() if need_dx else None, K, 1, dW.data_ptr() if need_dw else None, K, wp,
+          wn)
     return dX, dW
 
 

@@ -101,7 +101,8 @@ struct I8Frag {
   __device__ __forceinline__ v2i group(const uint32_t* mb, int q, const v2i* table) const {
     const v2i sel = table[kept_set<N, M>(positions(mb, KEPT * W * q))];
     const uint32_t lo = bytes(KEPT * q), hi = KEPT > 4 ? bytes(KEPT * q + 4) : 0u;
-    return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]), (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
+    return v2i{(int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[0]),
+               (int)__builtin_amdgcn_perm(hi, lo, (uint32_t)sel[1])};
   }
   __device__ __forceinline__ void ready(int lg, v4i& a0, v4i& a1, const v2i* table) const {
     uint32_t mb[MD];

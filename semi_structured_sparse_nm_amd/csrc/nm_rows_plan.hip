@@ -36,8 +36,10 @@ struct Wide {
 };
 constexpr Wide kWide[2][2][KINDS] = {
     // 8 bits (slabs of 128 columns): 64 rows, 128 rows
-    {{{4.97, 0.632, 0.833, 0.779}, {6.07, 1.07, 0.868, 0.836}, {5.10, 0.805, 0.785, 0.865}, {5.67, 1.15, 0.776, 0.862}, {}},
-     {{6.10, 0.831, 0.963, 0.671}, {7.77, 1.15, 0.923, 0.811}, {6.75, 1.15, 0.951, 0.802}, {7.38, 1.41, 0.925, 0.807}, {}}},
+    {{{4.97, 0.632, 0.833, 0.779}, {6.07, 1.07, 0.868, 0.836}, {5.10, 0.805, 0.785, 0.865}, {5.67, 1.15, 0.776, 0.862},
+      {}},
+     {{6.10, 0.831, 0.963, 0.671}, {7.77, 1.15, 0.923, 0.811}, {6.75, 1.15, 0.951, 0.802}, {7.38, 1.41, 0.925, 0.807},
+      {}}},
     // 16 bits (64 columns)
     {{{3.41, 0.601, 0.785, 0.677}, {4.94, 1.03, 0.904, 0.867}, {4.35, 0.669, 0.790, 0.816}, {4.69, 0.823, 0.819, 0.818},
       {5.01, 1.32, 0.873, 0.920}},

@@ -427,7 +427,7 @@ __device__ __forceinline__ int tile_items(const tile_args<OP>& a, const TileList
     if constexpr (COLS) {
       tile_cols<OUT>(a, it, m0, n0, kept, acc);
     } else if constexpr (EROWS) {
-      rows_epilogue<OP, OUT, TM, TN>(a, it, m0, n0, acc);
+      rows_epilogue<OUT, TM, TN>(a, it, m0, n0, acc);
     } else {
       tile_epilogue<OP, OUT, TM, TN>(a, it, m0, n0, acc);
     }

@@ -1,7 +1,7 @@
 // Products with 2:4 packed weights, more than a few tokens: the gated block, and
-// products of rows grouped by expert (16-bit and 8-bit).  The packed blocks go to the sparse matrix instruction (v_smfmac_f32_16x16x64) as they
-// are, so neither a dense copy of the weights nor the products with pruned
-// ones exist.
+// products of rows grouped by expert (16-bit and 8-bit).  The packed blocks go to
+// the sparse matrix instruction (v_smfmac_f32_16x16x64) as they are, so neither a
+// dense copy of the weights nor the products with pruned ones exist.
 //
 // The structure is the dense tile product's (nm_tile.hpp): persistent
 // workgroups, one stream of slabs through NS LDS stages, loads and fragment
@@ -44,8 +44,8 @@ typedef __bf16 v16bf_t __attribute__((ext_vector_type(16)));
 
 #if defined(__HIP_DEVICE_COMPILE__)
 template <int WT>
-__device__ __forceinline__ auto smfmac_tile(v4i a, v4i b0, v4i b1, typename std::conditional<WT == NM_I8, v4i, v4f>::type c,
-                                            int idx) {
+__device__ __forceinline__ auto smfmac_tile(v4i a, v4i b0, v4i b1,
+                                            typename std::conditional<WT == NM_I8, v4i, v4f>::type c, int idx) {
   const v8i b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
   if constexpr (WT == NM_I8)
     return __builtin_amdgcn_smfmac_i32_16x16x128_i8(a, b, c, idx, 0, 0);
@@ -63,8 +63,6 @@ struct Tile24Args : TileArgs { // A, lda, Mr, Nr, ka, nslab, outputs, act
   const uint8_t* meta[2];
 };
 
-// TM: 16-token tiles of a wave, H: its 16-output tiles; four waves along the
-// tokens, two along the outputs
 template <int OP>
 using tile24_args = typename std::conditional<OP == TILE_ROWS, RowsTile, Tile24Args>::type;
 
@@ -75,6 +73,8 @@ constexpr int rows24_table = NS * (64 * TM * 128 + 4 * H * (WT == NM_I8 ? 1280 :
                                  ? kRowsTable
                                  : kRowsTable / 2;
 
+// TM: 16-token tiles of a wave, H: its 16-output tiles; four waves along the
+// tokens, two along the outputs
 template <int WT, int OP, int OUT, int TM, int H, int NS>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 tile24_kernel(tile24_args<OP> p, TileList list) {
@@ -261,7 +261,7 @@ tile24_kernel(tile24_args<OP> p, TileList list) {
       st = nx;
     }
     if constexpr (EROWS)
-      rows_epilogue<TILE_ROWS, OUT, TM, TN>(p, it, it.row + wm * TM * 16, (int64_t)it.n * BNO + wn * TN * 16, acc);
+      rows_epilogue<OUT, TM, TN>(p, it, it.row + wm * TM * 16, (int64_t)it.n * BNO + wn * TN * 16, acc);
     else
       tile_epilogue<TILE_GLU, WT, TM, TN>(a, it, (int64_t)it.m * BM + wm * TM * 16, (int64_t)it.n * BNO + wn * H * 16,
                                           acc);
@@ -274,8 +274,8 @@ tile24_kernel(tile24_args<OP> p, TileList list) {
 template <int WT, int TM, int H, int NS>
 hipError_t launch_tile24_cfg(const Tile24Args& p, hipStream_t s) {
   const TileList list = tile_list(p.Mr, p.Nr, 64 * TM, 32 * H, 1, p.nslab, p.nslab, 1);
-  hipLaunchKernelGGL((tile24_kernel<WT, TILE_GLU, WT, TM, H, NS>), dim3((unsigned)(8 * tile_slots(list.per))), dim3(512),
-                     0, s, p, list);
+  hipLaunchKernelGGL((tile24_kernel<WT, TILE_GLU, WT, TM, H, NS>), dim3((unsigned)(8 * tile_slots(list.per))),
+                     dim3(512), 0, s, p, list);
   return hipGetLastError();
 }
 

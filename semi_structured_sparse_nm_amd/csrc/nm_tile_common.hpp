@@ -387,7 +387,7 @@ __device__ __forceinline__ void tile_cols(const RowsTile& a, const TileItem& it,
 }
 
 // Epilogue of one wave's tiles of grouped rows.
-template <int OP, int OUT, int TM, int TN, class Acc>
+template <int OUT, int TM, int TN, class Acc>
 __device__ __forceinline__ void rows_epilogue(const RowsTile& a, const TileItem& it, int64_t m0, int64_t n0,
                                               const Acc (&acc)[TN][TM]) {
   if constexpr (std::is_same<Acc, v4i>::value)

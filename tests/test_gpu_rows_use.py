@@ -98,7 +98,8 @@ def test_gradients_against_differences(N, M):
 
     def along(a, b):
         """(sum a b, what the rounding of a moves it by)"""
-        return float((a.double() * b.double()).sum()), float((half_step(a.dtype) * a.double().abs() * b.double().abs()).sum())
+        p = a.double() * b.double()
+        return float(p.sum()), float(half_step(a.dtype) * p.abs().sum())
 
     up, down = (nm.expert_linear(x, X + s * dX, o) for s in (1, -1))
     (a, ea), (b, eb), (c, ec) = along(up, dY), along(down, dY), along(gX, dX)
@@ -207,6 +208,30 @@ def test_other_stream():
     q, sx = i8_64(X0)
     check(Y, *i8_expert64(q, sx, w8, s8, None, "none", o), "i8_expert_linear")
     assert torch.equal(Z, q.float() * sx[:, None])
+
+
+@pytest.mark.parametrize("T", [20, 600])
+def test_two_streams_at_once(T):
+    """Calls on two streams, side by side on the same weights, rows and offsets."""
+    R, K, E = 200, 328, 5
+    W = randn(E, R, K, seed=1, dt=torch.bfloat16, scale=0.1)
+    x = nm.pack_experts(W, 5, 8)
+    x8, s8, w8 = i8_weight(R, K, 3, 4, 2, E=E)
+    X, dY, o = randn(T, K, dt=torch.bfloat16), randn(T, R, seed=1, dt=torch.bfloat16), counts(T, E, "ragged", 2)
+
+    def run():
+        return (nm.expert_linear(x, X, o), *nm.expert_linear_backward(x, X, o, dY), nm.i8_expert_linear(x8, s8, X, o),
+                nm.i8_dequantize(nm.i8_quantize(X)))
+
+    want = run()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
 
 
 # ---------------------------------------------------------------- copies, rows, lengths
