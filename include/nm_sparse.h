@@ -618,8 +618,8 @@ nm_status nm_experts_pack(const void* W, int64_t lde, int64_t ldw, nm_experts* w
  * [ldx] and Yt [T][ldy] of their dtype, binary32 sums rounded once.  Workspace:
  * nm_expert_linear_workspace_size bytes (256-byte aligned) for the rows Xt and
  * ldx of the call (read are only the pointer's alignment and the stride), or,
- * Xt NULL, for any rows: a padded copy of X and re-packed or dense copies of
- * the weights, where the call takes them.  Activations are finite: whether an
+ * Xt NULL, for rows of any address and stride (ldx is not read): a padded copy of
+ * X and re-packed or dense copies of the weights, where the call takes them.  Activations are finite: whether an
  * infinite or NaN one reaches an output through a pruned weight depends on the
  * path the call takes (it never reaches another row).  Overlaps and sharing of
  * workspaces as for nm_i8_linear.

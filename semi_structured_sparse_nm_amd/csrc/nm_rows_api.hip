@@ -14,7 +14,8 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 // rows the tile kernels address with 32-bit offsets: 256 of them within 2^31 bytes
-bool row_ok(int64_t row_bytes) { return row_bytes < (1ll << 23); }
+constexpr int64_t kMaxStride = 1ll << 23;
+bool row_ok(int64_t row_bytes) { return row_bytes < kMaxStride; }
 bool float_dtype(int32_t dt) { return dt == NM_F16 || dt == NM_BF16 || dt == NM_F32; }
 
 constexpr int64_t kMaxLen = 1ll << 25;      // rows
@@ -367,9 +368,10 @@ nm_status nm_expert_linear_workspace_size(const nm_experts* w, const void* Xt, i
   if (st != NM_OK) return st;
   if (Xt && ldx < ww.g.K) return NM_EINVAL;
   const RowsPath path = plan_of(ww, T).path;
-  // (NULL: the worst rows)
-  *bytes = (rows_direct(path, Xt ? Xt : reinterpret_cast<const void*>(2), ldx, ww.g.K) ? 0 : padded_bytes(T, ww.g.K)) +
-           copies_bytes(ww, path);
+  // NULL: the worst rows, at an odd address and farther apart than 32-bit offsets reach
+  const bool direct = Xt ? rows_direct(path, Xt, ldx, ww.g.K)
+                         : rows_direct(path, reinterpret_cast<const void*>(2), kMaxStride, ww.g.K);
+  *bytes = (direct ? 0 : padded_bytes(T, ww.g.K)) + copies_bytes(ww, path);
   return NM_OK;
 }
 

@@ -212,6 +212,28 @@ def test_i8_expert_refusals():
     assert g(ctypes.byref(_experts()), None, 5, ctypes.byref(n)) == EUNSUP
 
 
+def _el_size(w, X, ldx, T):
+    n = ctypes.c_size_t()
+    assert nm.lib().nm_expert_linear_workspace_size(ctypes.byref(w), X, ldx, T, ctypes.byref(n)) == nm.NM_OK
+    return n.value
+
+
+@pytest.mark.parametrize("path", [None, "stream:1", "wide:0", "wide:1", "tile:0", "tile:2", "tile24:1", "tile24:3"])
+@pytest.mark.parametrize("K,N,M", [(4, 2, 4), (8, 2, 4), (136, 4, 8), (132, 3, 4), (128, 1, 4), (2048, 4, 4)])
+def test_expert_linear_workspace_covers_any_rows(monkeypatch, path, K, N, M):
+    """What the query answers without rows is enough for rows of any address and stride."""
+    if path:
+        monkeypatch.setenv("NM_FFN_TILE", path)
+    for E, R, T in ((3, 40, 5), (32, 1536, 4096), (2, 300, 700)):
+        w = _experts(E=E, R=R, K=K, N=N, M=M)
+        any_rows = _el_size(w, None, 0, T)
+        for X in (P[0], P[0] + 2, P[0] + 8):
+            for ldx in (K, K + 1, K + 8, 1 << 14, (1 << 22) - 8, 1 << 22, (1 << 22) + 1, 1 << 30):
+                assert _el_size(w, X, ldx, T) <= any_rows, (E, R, T, X - P[0], ldx)
+        # the stride given beside no rows is not read
+        assert _el_size(w, None, 1 << 30, T) == any_rows
+
+
 # ---------------------------------------------------------------- binding
 def _packed_experts(E=2, R=16, K=64, N=2, M=4, dt=nm.NM_F16):
     v, m = nm.pack_size(R, K, N, M, dt)
