@@ -123,6 +123,30 @@ def test_i8_quantize_ties():
     assert torch.equal(nm.i8_quantize(x.half()).values, q.values)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_i8_quantize_beside_the_quotient(dt):
+    """How far the stored rows are from those of the rounded quotient amax / 127.  The
+    scale is amax c rounded, c = 1/127 cut to 24 bits, within 2^-28 of it: it and the
+    rounded quotient are off by at most (2^-28 + 2^-24) and 2^-24 of amax / 127, less
+    than one and a half steps apart, so neighbours at most.  x over either is then the
+    same within 127 (2^-23 + 2^-28 + 2^-46) < 2^-16 (2^-23 a step's most), so only elements
+    that close to a border may differ, by one.  Every element is within half a scale of
+    x, and 127 scales within 127 (2^-28 + 2^-24) < 2^-16 scales of amax."""
+    x = randn(2000, 1000, seed=7, dt=TORCH[dt])
+    x[::3] *= randn(667, 1, seed=8).exp().to(x.dtype)
+    q = nm.i8_quantize(x)
+    amax = x.double().abs().amax(dim=1)
+    s = (amax / 127).float()
+    assert ((q.scales.view(torch.int32) - s.view(torch.int32)).abs() <= 1).all()
+    u = x.double() / s.double()[:, None]
+    low = torch.floor(u)
+    border = (u - low - 0.5).abs() <= 2.0 ** -16
+    off = (q.values.double() - torch.round(u)).abs()
+    assert not off[~border].any() and (off <= 1).all()
+    scale = q.scales.double()[:, None]
+    assert ((q.values.double() * scale - x.double()).abs() <= (0.5 + 2.0 ** -16) * scale).all()
+
+
 # ---------------------------------------------------------------- 8-bit product
 def i8_weight(R, K, N, M, seed, E=None):
     """(packed, scales, pruned whole numbers)."""
