@@ -210,6 +210,50 @@ def test_i8_linear_long_sums():
         check(Y, *i8_product64(q, sx, w, sw, None, "none"), "long sums")
 
 
+# Rows that the streamed product quantises itself, longer than the 4096 columns that
+# its threads have a piece each of: two to four pieces a thread, whose maximum is carried
+# across them, and rows beyond the four pieces that a thread holds.
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T,K,N,M", [(1, 4100, 2, 4), (1, 8192, 4, 8), (1, 11008, 2, 4), (1, 11008, 4, 8), (1, 12292, 3, 4),
+                                     (1, 16384, 4, 8), (2, 8184, 5, 8), (3, 5376, 4, 8), (2, 4224, 4, 4)])
+def test_i8_linear_long_rows_quantised_inside(dt, T, K, N, M):
+    R = 90
+    p, sw, w = i8_weight(R, K, N, M, K)
+    assert nm.i8_linear_workspace_size(p, T) == 0         # (no launch of the quantiser)
+    X = randn(T, K, seed=T, dt=TORCH[dt])
+    # (each row's largest element in another piece of another thread)
+    for t in range(T):
+        X[t, (K - 1 - 700 * t) % K] = 9.0 + t
+    X = strided(X, 5)
+    Y = nm.i8_linear(p, sw, X, out_dtype=torch.float32)
+    q, sx = i8_64(X)
+    check(Y, *i8_product64(q, sx, w, sw, None, "none"), "i8_linear")
+    assert torch.equal(nm.i8_linear(p, sw, nm.i8_quantize(X), out_dtype=torch.float32), Y)
+    X[0, K - 1] = float("nan")                            # in the last piece
+    Y2 = nm.i8_linear(p, sw, X, out_dtype=torch.float32)
+    assert Y2[0].isnan().all() and torch.equal(Y2[1:], Y[1:])
+
+
+# The rows of one expert, up to 48 KB of LDS beside the kernel's own 19: launches with
+# more than 64 KB.
+@pytest.mark.parametrize("kind", ["one", "ragged", "even"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T,E,K,N,M", [(15, 32, 3200, 4, 8), (15, 32, 3136, 2, 4), (3, 3, 16200, 4, 8),
+                                       (2, 7, 16384, 3, 4), (16, 16, 2944, 6, 8)])
+def test_i8_expert_linear_rows_quantised_inside(T, E, K, N, M, dt, kind):
+    R = 40
+    x, sw, w = i8_weight(R, K, N, M, K, E=E)
+    assert nm.i8_expert_linear_workspace_size(x, T) == 0
+    X = randn(T, K, seed=T, dt=TORCH[dt])
+    for t in range(T):
+        X[t, (K - 1 - 900 * t) % K] = 9.0 + t
+    o = counts(T, E, kind, seed=K)
+    Y = nm.i8_expert_linear(x, sw, X, o, out_dtype=torch.float32)
+    q, sx = i8_64(X)
+    check(Y, *i8_expert64(q, sx, w, sw, None, "none", o), "i8_expert_linear")
+    assert torch.equal(nm.i8_expert_linear(x, sw, nm.i8_quantize(X), o, out_dtype=torch.float32), Y)
+
+
 def test_i8_linear_not_finite():
     p, sw, w = i8_weight(40, 256, 2, 4, 0)
     for T in (4, 90):
