@@ -641,11 +641,19 @@ nm_status nm_expert_linear(const nm_experts* w, const void* Xt, int64_t ldx, int
  * dW is written whole: exactly zero where a weight is not kept and for experts
  * without rows.  dX or dW may be NULL (not computed), not both.  Operands are
  * the 16-bit tensors as they are, sums binary32, every output rounded once; the
- * result does not depend on launch order (no atomics).  Errors as
+ * result does not depend on launch order (no atomics).  Workspace (256-byte
+ * aligned): nm_expert_linear_backward_workspace_size bytes for both outputs and
+ * rows of any address and stride, or what one call needs, ..._size_for: of Xt and
+ * dY only the alignment and the strides are read, dx and dw say which outputs it
+ * gets.  dX takes a dense transposed copy of the weights, dW 1 KB for 128 x 64 of
+ * them, and rows that are not 16-byte pieces a padded copy.  Errors as
  * nm_expert_linear; NM_EINVAL also for no output, lddx < K, lddw < K, lddy < R;
  * NM_EUNSUPPORTED also where the weights' tiles of 128 x 64 pass a launch (2^24).
  */
 nm_status nm_expert_linear_backward_workspace_size(const nm_experts* w, int64_t T, size_t* bytes);
+nm_status nm_expert_linear_backward_workspace_size_for(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T,
+                                                       const void* dY, int64_t lddy, int32_t dx, int32_t dw,
+                                                       size_t* bytes);
 nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T, const void* offsets,
                                     int32_t offsets_dtype, const void* dY, int64_t lddy, void* dX, int64_t lddx,
                                     int32_t zero_rest, void* dW, int64_t lddw, void* workspace, size_t workspace_bytes,

@@ -166,13 +166,14 @@ def lib() -> ctypes.CDLL:
         L.nm_expert_linear_workspace_size.argtypes = [EP, P, I64, I64, ctypes.POINTER(SZ)]
         L.nm_expert_linear.argtypes = [EP, P, I64, I64, P, I32, P, I64, I32, P, SZ, P]
         L.nm_expert_linear_backward_workspace_size.argtypes = [EP, I64, ctypes.POINTER(SZ)]
+        L.nm_expert_linear_backward_workspace_size_for.argtypes = [EP, P, I64, I64, P, I64, I32, I32, ctypes.POINTER(SZ)]
         L.nm_expert_linear_backward.argtypes = [EP, P, I64, I64, P, I32, P, I64, P, I64, I32, P, I64, P, SZ, P]
         L.nm_i8_expert_linear_workspace_size.argtypes = [EP, IP, I64, ctypes.POINTER(SZ)]
         L.nm_i8_expert_linear.argtypes = [EP, P, IP, P, I64, I32, I64, P, I32, P, I64, I32, P, I32, I32, P, SZ, P]
         for f in ("nm_i8_size", "nm_i8_quantize", "nm_i8_dequantize", "nm_i8_linear_workspace_size", "nm_i8_linear",
                   "nm_experts_size", "nm_experts_pack", "nm_expert_linear_workspace_size", "nm_expert_linear",
-                  "nm_expert_linear_backward_workspace_size", "nm_expert_linear_backward",
-                  "nm_i8_expert_linear_workspace_size", "nm_i8_expert_linear"):
+                  "nm_expert_linear_backward_workspace_size", "nm_expert_linear_backward_workspace_size_for",
+                  "nm_expert_linear_backward", "nm_i8_expert_linear_workspace_size", "nm_i8_expert_linear"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("nm_pack_size", "nm_pack", "nm_spmm_workspace_size", "nm_spmm", "nm_hybrid_pack_size",
                   "nm_hybrid_pack", "nm_hybrid_spmm", "nm_glu_workspace_size", "nm_glu", "nm_glu_kept",
@@ -1152,7 +1153,7 @@ def expert_linear(w: Experts, X: torch.Tensor, offsets: torch.Tensor, out: torch
 
 def expert_linear_backward_workspace_size(w: Experts, T: int) -> int:
     """nm_expert_linear_backward_workspace_size: bytes of workspace
-    expert_linear_backward() needs."""
+    expert_linear_backward() may need for T rows of any stride and alignment."""
     n = ctypes.c_size_t()
     _check(lib().nm_expert_linear_backward_workspace_size(_descriptor(w), T, ctypes.byref(n)),
            "nm_expert_linear_backward_workspace_size")
@@ -1174,15 +1175,15 @@ def expert_linear_backward(w: Experts, X: torch.Tensor, offsets: torch.Tensor, d
     lddy = _row_pitch("dY", dY, T, R)
     _check_dtype("dY", dY, X.dtype)
     dev = _one_gpu("X, weight, weight meta, dY, offsets", X, w.values, w.meta, dY, offsets)
-    L, d = lib(), _descriptor(w)
-    need = _sized(L.nm_expert_linear_backward_workspace_size, "nm_expert_linear_backward_workspace_size",
-                  _expert_key("expert_backward", w, T, None, dev), d, T)
+    L, d, x, y = lib(), _descriptor(w), X.data_ptr(), dY.data_ptr()
+    need = _sized(L.nm_expert_linear_backward_workspace_size_for, "nm_expert_linear_backward_workspace_size_for",
+                  _expert_key("expert_backward", w, T, (x % 16, ldx, y % 16, lddy, need_dx, need_dw), dev), d, x, ldx, T,
+                  y, lddy, need_dx, need_dw)
     ws, wp, wn = _workspace(workspace, need, dev)
     dX = X.new_empty((T, K)) if need_dx else None
     dW = X.new_empty((E, R, K)) if need_dw else None
-    _call(dev, L.nm_expert_linear_backward, "nm_expert_linear_backward", d, X.data_ptr(), ldx, T, offsets.data_ptr(),
-          odt, dY.data_ptr(), lddy, dX.data_ptr() if need_dx else None, K, 1, dW.data_ptr() if need_dw else None, K, wp,
-          wn)
+    _call(dev, L.nm_expert_linear_backward, "nm_expert_linear_backward", d, x, ldx, T, offsets.data_ptr(), odt, y, lddy,
+          dX.data_ptr() if need_dx else None, K, 1, dW.data_ptr() if need_dw else None, K, wp, wn)
     return dX, dW
 
 

@@ -269,6 +269,12 @@ struct BackwardPlan {
   }
 };
 
+// that of a call with these rows
+BackwardPlan backward_plan(const Weights& w, const void* X, int64_t ldx, int64_t T, const void* dY, int64_t lddy,
+                           bool dx, bool dw) {
+  return BackwardPlan(w, T, dx, dw, !rows_direct(ROWS_DENSE, X, ldx, w.g.K), !rows_direct(ROWS_DENSE, dY, lddy, w.g.R));
+}
+
 nm_status check_backward(const Weights& w, int64_t T) {
   if (w.dtype == NM_I8) return NM_EUNSUPPORTED;
   const nm_status st = check_sizes(w, T);
@@ -428,6 +434,19 @@ nm_status nm_expert_linear_backward_workspace_size(const nm_experts* w, int64_t 
   return NM_OK;
 }
 
+nm_status nm_expert_linear_backward_workspace_size_for(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T,
+                                                       const void* dY, int64_t lddy, int32_t dx, int32_t dw,
+                                                       size_t* bytes) {
+  Weights ww;
+  nm_status st = weights_of(w, &ww);
+  if (st != NM_OK) return st;
+  st = check_backward(ww, T);
+  if (st != NM_OK) return st;
+  if (!bytes || !Xt || !dY || ldx < ww.g.K || lddy < ww.g.R || (!dx && !dw)) return NM_EINVAL;
+  *bytes = backward_plan(ww, Xt, ldx, T, dY, lddy, dx != 0, dw != 0).total;
+  return NM_OK;
+}
+
 nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t ldx, int64_t T, const void* offsets,
                                     int32_t offsets_dtype, const void* dY, int64_t lddy, void* dX, int64_t lddx,
                                     int32_t zero_rest, void* dW, int64_t lddw, void* workspace, size_t workspace_bytes,
@@ -443,8 +462,8 @@ nm_status nm_expert_linear_backward(const nm_experts* w, const void* Xt, int64_t
   st = check_offsets(offsets, offsets_dtype);
   if (st != NM_OK) return st;
   if (!aligned(Xt, 2) || !aligned(dY, 2) || !aligned(dX, 2) || !aligned(dW, 2)) return NM_EUNSUPPORTED;
-  const bool pad_x = dW && !rows_direct(ROWS_DENSE, Xt, ldx, g.K), pad_y = !rows_direct(ROWS_DENSE, dY, lddy, g.R);
-  const BackwardPlan p(ww, T, dX != nullptr, dW != nullptr, pad_x, pad_y);
+  const BackwardPlan p = backward_plan(ww, Xt, ldx, T, dY, lddy, dX != nullptr, dW != nullptr);
+  const bool pad_x = p.xp != 0, pad_y = p.yp != 0;
   if (!workspace || workspace_bytes < p.total) return NM_EINVAL;
   if (!aligned(workspace, 256)) return NM_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -214,8 +214,9 @@ def test_i8_linear_long_sums():
 # its threads have a piece each of: two to four pieces a thread, whose maximum is carried
 # across them, and rows beyond the four pieces that a thread holds.
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("T,K,N,M", [(1, 4100, 2, 4), (1, 8192, 4, 8), (1, 11008, 2, 4), (1, 11008, 4, 8), (1, 12292, 3, 4),
-                                     (1, 16384, 4, 8), (2, 8184, 5, 8), (3, 5376, 4, 8), (2, 4224, 4, 4)])
+@pytest.mark.parametrize("T,K,N,M", [(1, 4100, 2, 4), (1, 8192, 4, 8), (1, 11008, 2, 4), (1, 11008, 4, 8),
+                                     (1, 12292, 3, 4), (1, 16384, 4, 8), (2, 8184, 5, 8), (3, 5376, 4, 8),
+                                     (2, 4224, 4, 4)])
 def test_i8_linear_long_rows_quantised_inside(dt, T, K, N, M):
     R = 90
     p, sw, w = i8_weight(R, K, N, M, K)

@@ -234,6 +234,24 @@ def test_two_streams_at_once(T):
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
 
 
+def test_backward_reserves_what_it_uses():
+    """The binding's own workspace: no dense weights without dX, no padded rows for whole
+    ones."""
+    T, R, K, E = 64, 256, 512, 8
+    x = nm.pack_experts(randn(E, R, K, seed=1, dt=torch.bfloat16, scale=0.1), 2, 4)
+    X, dY, o = randn(T, K, dt=torch.bfloat16), randn(T, R, seed=1, dt=torch.bfloat16), counts(T, E, "even")
+    dense, rows, mask = E * R * K * 2, T * (K + R) * 2, E * (R // 128) * (K // 64) * 1024
+    for dx, dw, most in ((True, True, dense + mask), (True, False, dense), (False, True, mask)):
+        nm.expert_linear_backward(x, X, o, dY, need_dx=dx, need_dw=dw)
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        out = nm.expert_linear_backward(x, X, o, dY, need_dx=dx, need_dw=dw)
+        peak = torch.cuda.max_memory_allocated() - before
+        assert peak == sum(g.numel() * 2 for g in out if g is not None) + most, (dx, dw)
+        del out
+    assert nm.expert_linear_backward_workspace_size(x, T) == dense + mask + rows
+
+
 # ---------------------------------------------------------------- copies, rows, lengths
 def test_copies_and_pickles():
     x8, s8, w8 = i8_weight(40, 136, 2, 4, 1, E=3)

@@ -234,6 +234,38 @@ def test_expert_linear_workspace_covers_any_rows(monkeypatch, path, K, N, M):
         assert _el_size(w, None, 1 << 30, T) == any_rows
 
 
+def test_backward_workspace_of_a_call():
+    """The query for one call is what that call asks for, byte by byte, and no more than
+    its parts: one byte less is refused, with all of them the misaligned workspace is."""
+    L, n = nm.lib(), ctypes.c_size_t()
+
+    def f(w, X=P[0], ldx=128, T=5, dY=P[2], lddy=40, dx=1, dw=1):
+        return L.nm_expert_linear_backward_workspace_size_for(ctypes.byref(w), X, ldx, T, dY, lddy, dx, dw,
+                                                              ctypes.byref(n))
+
+    for K, R in ((128, 40), (132, 40), (128, 41), (196, 333)):
+        w, T, Kp, Rp = _experts(K=K, R=R), 70, -(-K // 64) * 64, -(-R // 64) * 64
+        wt, mask = 3 * -(-K // 16) * 16 * Rp * 2, 3 * -(-R // 128) * (Kp // 64) * 1024
+        worst = ctypes.c_size_t()
+        assert L.nm_expert_linear_backward_workspace_size(ctypes.byref(w), T, ctypes.byref(worst)) == nm.NM_OK
+        for X, ldx in ((P[0], K), (P[0], K + 12), (P[0] + 2, K + 24), (P[0], 1 << 22)):
+            for dY, lddy in ((P[2], R), (P[2], R + 15), (P[2] + 8, R)):
+                px = (X - P[0]) % 16 or ldx % 8 or K % 8 or ldx >= 1 << 22
+                py = (dY - P[2]) % 16 or lddy % 8 or R % 8
+                for dx, dw in ((1, 1), (1, 0), (0, 1)):
+                    assert f(w, X, ldx, T, dY, lddy, dx, dw) == nm.NM_OK
+                    parts = [wt * dx, mask * dw, T * Kp * 2 * bool(dw and px), T * Rp * 2 * bool(py)]
+                    assert n.value == sum(-(-v // 256) * 256 for v in parts) <= worst.value
+                    call = dict(w=w, X=X, ldx=ldx, T=T, dY=dY, lddy=lddy, dX=P[3] if dx else None, lddx=K,
+                                dW=P[4] if dw else None, lddw=K, ws=P[5] + 8)
+                    assert _eb(**call, wsb=n.value - 1) == EINVAL and _eb(**call, wsb=n.value) == EUNSUP
+    w = _experts()
+    for kw in (dict(X=None), dict(dY=None), dict(ldx=127), dict(lddy=39), dict(T=0), dict(dx=0, dw=0)):
+        assert f(w, **kw) == EINVAL, kw
+    assert L.nm_expert_linear_backward_workspace_size_for(ctypes.byref(w), P[0], 128, 5, P[2], 40, 1, 1, None) == EINVAL
+    assert f(_experts(dt=nm.NM_I8)) == EUNSUP and f(_experts(format_version=0)) == EINVAL
+
+
 # ---------------------------------------------------------------- binding
 def _packed_experts(E=2, R=16, K=64, N=2, M=4, dt=nm.NM_F16):
     v, m = nm.pack_size(R, K, N, M, dt)
