@@ -48,7 +48,6 @@
   // TILE_GLU with the RJ rows of a load spanning both halves: a wave's rows are all gate or all up rows
   constexpr bool SPAN = GLU && HB % RJ != 0;
   const bool wave_up = SPAN && (8 * wave / HB & 1);
-  // row of the tile (A: of BM, B: of BNO outputs) that load j brings this lane
   // TILE_COLS: an operand's slab is 64 rows of BM (BN) columns as they lie in memory,
   // read transposed from LDS; load d of it fills 1 KB, 16-byte position p of row t
   // with piece p ^ 2 swz(t).  A read's sixteen lanes take 32 bytes each of four rows
@@ -56,6 +55,7 @@
   auto swz = [](int t, auto width) {
     return decltype(width)::value >= 128 ? (t & 3) | (t >> 3 & 1) << 2 : (t >> 1 & 1) | (t >> 3 & 1) << 1;
   };
+  // row of the tile (A: of BM, B: of BNO outputs) that load j brings this lane
   auto load_row = [&](auto jc) {
     constexpr int j = decltype(jc)::value;
     int row = 8 * wave + (lane >> 3) + RJ * j;
