@@ -64,8 +64,14 @@ constexpr int rows_table_bytes(bool grouped, int entries) { return grouped ? 8 *
 // (an XCD's run of the list meets few experts' weights), dealt as TileWalk
 // does.  COLS: every expert's mt x nt tiles, its slabs of 64 rows the reduction.
 // They last as long as the expert has rows, so every XCD takes an eighth of each
-// expert's, side by side (eight experts of 4096 rows, 2048 x 4096, both gradients: 163
-// us for the weights' alone where each XCD had an expert of its own, 177 for both so).
+// expert's, side by side.  bf16, eight experts of 2048 x 4096 with 4096 rows together,
+// a call for the weights' gradients alone, in us: rows even, by a router, or all of one
+// expert 128, 128, 356 where each XCD has an eighth of the list (an expert of its own),
+// 124, 110, 130 where the XCDs take runs of one tile a workgroup in turn, 125, 106, 116
+// so; four times the rows 298, 350, 1376; 291, 292, 428; 287, 292, 396.  With the rows'
+// gradients as well 205, 230, 393; 200, 205, 180; 200, 206, 168.  (32 experts of 1536 x
+// 2048, 4096 rows, both: 210, 245, 300; 202, 239, 150; 213, 251, 143: runs in turn are
+// 5% better there.)
 template <int BM, bool COLS, int TAB>
 struct RowsWalk {
   const int* row_at;
