@@ -2,9 +2,10 @@
 //
 // Fitted to 1084 products of 17 to 2048 rows an expert, 1 to 64 experts, 300 to
 // 11008 outputs, K 512 to 11008, seven patterns, 8 and 16 bits, every path and tile
-// shape measured with weights that change between calls: the wide and tile models
-// are 4 to 10% off as a root mean square, the streamed one 30%; the choice costs 1.7%
-// against the fastest path as a mean over them, 8% in one of ten, 52% at most.
+// shape measured with weights that change between calls
+// (profiles/rows_plan_products.csv): the wide and tile models are 4 to 10% off as a
+// root mean square, the streamed one 24 to 32%; the path taken costs 2.1% against the
+// fastest as a mean over them, 8% or more in one of ten, 51% at most.
 // For example, streamed, wide (64 rows), wide (128), best tiles, in microseconds:
 // 8-bit 4:8, 48 rows, 11008 x 4096 25, 33, 41, 42; 256 rows 59, 34, 41, 49; 32 experts
 // of 1536 x 2048, 16-bit 4:8, 256 rows 42, 30, 37, 149, 4096 rows -, 49, 63, 175;
@@ -192,6 +193,10 @@ RowsPlan rows_plan(const Geometry& g, int64_t T, int64_t E, int cus) {
   if (ffn_tile_override("stream", &v, nullptr)) return v && can_stream ? RowsPlan{ROWS_STREAM, 0} : tiles;
   if (ffn_tile_override("tile", &v, nullptr) || ffn_tile_override("tile24", &v, nullptr)) return tiles;
   const int64_t groups = std::min(T, E), mean = ceil_div(T, groups);
+  // (by the mean alone, the host knows no more: sixteen rows of each of 32 experts of 1536
+  // x 2048, 16-bit 2:4, 32 us evenly, 33 by a router, 25 all of one expert's, wide 24, 24
+  // and 20; of 8 experts of 2048 x 4096 23, 23 and 20, the fastest others 23, 23 and 22;
+  // four rows of each of the 32 25, 25 and 13, others 24, 24 and 14)
   if (mean <= 16 && can_stream) return {ROWS_STREAM, 0};
 
   const double dense = (double)E * (double)(g.nRB * g.nKB) * 2048.0;
