@@ -540,13 +540,17 @@ _forced_path = functools.partial(os.environ._data.get, os.environ.encodekey("NM_
 
 
 def _descriptor(p):
-    """byref of p's C descriptor, built again whenever a field changed."""
+    """byref of p's C descriptor, built again whenever a field changed (Experts and
+    I8: desc() checks the tensors, so another one counts as a change too)."""
     if type(p) is Packed:
         v, m = p.values, p.meta
         key = (v.data_ptr(), v.numel(), p.rows, p.K, p.N, p.M, p.dtype, p.format_version)
     elif type(p) is Experts:
         v, m = p.values, p.meta
-        key = (v.data_ptr(), v.numel(), p.experts, p.rows, p.K, p.N, p.M, p.dtype, p.format_version)
+        key = (v.data_ptr(), v.numel(), id(v), id(m), p.experts, p.rows, p.K, p.N, p.M, p.dtype, p.format_version)
+    elif type(p) is I8:
+        v, m = p.codes, p.scales
+        key = (v.data_ptr(), v.numel(), id(v), id(m), p.rows, p.K, p.format_version)
     else:
         v, m = p.codes, p.scales
         key = (v.data_ptr(), v.numel(), p.rows, p.K, p.format_version)
@@ -632,6 +636,13 @@ def _glu_act(act: str) -> int:
 def _check_dtype(name: str, t: torch.Tensor, want: torch.dtype) -> None:
     if t.dtype != want:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
+
+
+def _check_buffer(name: str, t: torch.Tensor, want: torch.dtype) -> None:
+    """A buffer the library gets by address and bytes alone."""
+    _check_dtype(name, t, want)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
 
 
 def _call(dev: int, f, what: str, *args) -> None:
@@ -928,6 +939,8 @@ class I8:
     format_version: int = FORMAT_VERSION
 
     def desc(self) -> NmI8:
+        _check_buffer("codes", self.codes, torch.int8)
+        _check_buffer("scales", self.scales, torch.float32)
         return NmI8(self.rows, self.K, self.format_version, 0, self.codes.data_ptr(), self.codes.numel(),
                     self.scales.data_ptr(), self.scales.numel() * 4)
 
@@ -1055,6 +1068,9 @@ class Experts:
 
     def desc(self) -> NmExperts:
         m = self.meta
+        _check_buffer("values", self.values, torch.uint8)
+        if m is not None:
+            _check_buffer("meta", m, torch.uint8)
         return NmExperts(self.experts, self.rows, self.K, self.N, self.M, self.dtype, self.format_version,
                          self.values.data_ptr(), self.values.numel(), None if m is None else m.data_ptr(),
                          0 if m is None else m.numel())

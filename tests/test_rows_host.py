@@ -360,3 +360,35 @@ def test_i8_definition():
 def test_offsets_as_read():
     assert experts_of(torch.tensor([-7, 5, 3, 80, 20, 10]), 60) == ([(0, 5), (5, 5), (5, 60), (60, 60), (60, 60)], [])
     assert experts_of(torch.tensor([2, 4, 4, 6]), 8) == ([(2, 4), (4, 4), (4, 6)], [0, 1, 6, 7])
+
+
+def test_binding_refuses_buffers_of_other_types_and_strides():
+    """What an I8 or Experts holds may be replaced by its user; the library gets addresses
+    only, so 16-bit scales would be read past their end and strided codes as others."""
+    p = nm.Packed(16, 64, 2, 4, nm.NM_I8, *(torch.empty(n, dtype=torch.uint8) for n in nm.pack_size(16, 64, 2, 4, nm.NM_I8)))
+    s, codes, scales = torch.ones(16), torch.zeros(3, 128, dtype=torch.int8), torch.ones(3)
+    for q, err, text in ((nm.I8(3, 64, codes, scales.half()), TypeError, "scales has dtype"),
+                         (nm.I8(3, 64, codes, torch.ones(6)[::2]), ValueError, "scales must be contiguous"),
+                         (nm.I8(3, 64, codes.to(torch.int16), scales), TypeError, "codes has dtype"),
+                         (nm.I8(3, 64, torch.zeros(6, 128, dtype=torch.int8)[::2], scales), ValueError, "codes must be")):
+        with pytest.raises(err, match=text):
+            nm.i8_linear(p, s, q)
+        with pytest.raises(err, match=text):
+            nm.i8_expert_linear(_packed_experts(dt=nm.NM_I8), torch.ones(2, 16), q, torch.zeros(3, dtype=torch.int32))
+    # replaced after a call that was fine, the same address and length
+    q = nm.I8(3, 64, torch.zeros(6, 128, dtype=torch.int8), scales)
+    all6, q.codes = q.codes, q.codes[:3]
+    with pytest.raises(ValueError, match="not on a GPU"):
+        nm.i8_linear(p, s, q)
+    q.codes = all6[::2]
+    with pytest.raises(ValueError, match="codes must be contiguous"):
+        nm.i8_linear(p, s, q)
+    X, o = torch.zeros(3, 64, dtype=torch.float16), torch.zeros(3, dtype=torch.int32)
+    for name in ("values", "meta"):
+        w = _packed_experts()
+        t = getattr(w, name)
+        for bad, err, text in ((t.to(torch.int16), TypeError, f"{name} has dtype"),
+                               (torch.empty(2 * t.numel(), dtype=torch.uint8)[::2], ValueError, f"{name} must be contig")):
+            setattr(w, name, bad)
+            with pytest.raises(err, match=text):
+                nm.expert_linear_workspace_size(w, 3)
