@@ -1185,6 +1185,7 @@ def expert_linear_backward(w: Experts, X: torch.Tensor, offsets: torch.Tensor, d
     (None in its place).  Not part of autograd's graph."""
     T, ldx = _expert_rows(w, X)
     odt = _check_offsets(w, offsets)
+    need_dx, need_dw = bool(need_dx), bool(need_dw)
     if not need_dx and not need_dw:
         raise ValueError("expert_linear_backward needs need_dx or need_dw")
     E, R, K = w.experts, w.rows, w.K

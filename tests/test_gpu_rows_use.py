@@ -252,6 +252,18 @@ def test_backward_reserves_what_it_uses():
     assert nm.expert_linear_backward_workspace_size(x, T) == dense + mask + rows
 
 
+def test_backward_takes_any_truth_value():
+    T, R, K, E = 30, 40, 64, 2
+    x = nm.pack_experts(randn(E, R, K, seed=1, dt=torch.float16, scale=0.1), 2, 4)
+    X, dY, o = randn(T, K, dt=torch.float16), randn(T, R, seed=1, dt=torch.float16), counts(T, E, "even")
+    dX, dW = nm.expert_linear_backward(x, X, o, dY)
+    for no in (None, 0, []):
+        a, b = nm.expert_linear_backward(x, X, o, dY, need_dx=1, need_dw=no)
+        assert torch.equal(a, dX) and b is None
+        a, b = nm.expert_linear_backward(x, X, o, dY, need_dx=no, need_dw="yes")
+        assert a is None and torch.equal(b, dW)
+
+
 # ---------------------------------------------------------------- copies, rows, lengths
 def test_copies_and_pickles():
     x8, s8, w8 = i8_weight(40, 136, 2, 4, 1, E=3)
